@@ -91,6 +91,8 @@ typedef enum {
 #define PD_DEVFLAG_BAD_PAGE 0x1u     /* a block-table entry outside [0, num_pages) */
 #define PD_DEVFLAG_BAD_SEQLEN 0x2u   /* a device seq_len outside the block table */
 #define PD_DEVFLAG_WAIT_TIMEOUT 0x4u /* a pipeline wait gave up after ~1 s */
+#define PD_DEVFLAG_NO_PAGES 0x8u     /* the free list is too short for a request's new tokens */
+#define PD_DEVFLAG_BAD_GROUP 0x10u   /* device group starts that do not cut the batch as planned */
 
 /* Element type of the KV cache (pd_layer_desc.kv_dtype). */
 #define PD_KV_BF16 0      /* bf16 K/V rows */
@@ -136,7 +138,8 @@ typedef struct {
                                 than its copies deliver, so its pipeline waits run out (~1 s) and
                                 report PD_DEVFLAG_WAIT_TIMEOUT without any fault */
   int32_t query_tokens;     /* T: query tokens per request (1 = decode; > 1 = paged_decode_plan_multi) */
-  int32_t partial;          /* 1: made by paged_decode_plan_partial (fp32 pieces always left for a merge) */
+  int32_t partial;          /* 1: made by paged_decode_plan_partial (fp32 pieces always left for a merge);
+                               2: the own part of a pd_shared_plan (likewise) */
   int32_t early_kv;         /* 0 (as planned). A caller may set 1 when no kernel that can still be
                                running as stage 1 starts writes block_tables, seq_lens, the FP8 scales
                                or a cached row other than each request's newest query_tokens positions.
@@ -432,6 +435,181 @@ pd_status paged_decode_qkv_norm_rope_write(const pd_layer_desc* layer, int32_t b
                                            const void* v_norm_weight, const float* cos_sin,
                                            const int32_t* block_tables, const int32_t* seq_lens, void* q_out,
                                            void* k_pool, void* v_pool, uint32_t* device_flags, void* stream);
+
+/* ---- Before the cache write: block tables and slot maps from lengths -----------
+ *
+ * A serving step starts from lengths: request b holds cached_lens[b] tokens in
+ * its pages and gets new_tokens[b] more (one in a decode step, a chunk of a
+ * prompt, none). This call hands out the pages the new tokens need, in request
+ * order from a list of free page ids, extends the block tables, and writes for
+ * every new token its position (the RoPE angle's) and its slot, the row
+ * page * page_size + position % page_size of the pool that the cache write
+ * takes. With old_b = ceil(cached_b / P) and need_b = ceil((cached_b + new_b) / P)
+ * - old_b, page k of request b's new ones is
+ *   free_pages[free_range[0] + sum_{i < b} need_i + k].
+ */
+
+/* Bytes of the workspace paged_decode_append_slots takes for `batch` requests. */
+size_t paged_decode_append_slots_workspace(int32_t batch);
+
+/*
+ *   batch         requests (>= 0)
+ *   page_size     P, tokens per page (> 0)
+ *   num_pages     pages in the pool (num_pages * P < 2^31)
+ *   max_pages     block-table row length (max_pages * P < 2^31)
+ *   max_tokens    entries of slot_map and positions (>= 0)
+ *   cached_lens   device int32 [batch]
+ *   new_tokens    device int32 [batch]
+ *   free_pages    device int32 [num_free]: ids of free pages
+ *   num_free      entries of free_pages (>= 0)
+ *   free_range    device int32 [2]: entries [free_range[0], free_range[1]) of
+ *                 free_pages are still free (a range outside [0, num_free] is
+ *                 cut to it)
+ *   block_tables  device int32 [batch, max_pages], in and out: the entries of
+ *                 the new pages are written, the others stay
+ *   seq_lens      device int32 [batch], out: cached + new (the decode call's
+ *                 lengths); may be cached_lens
+ *   token_starts  device int32 [batch + 1], out: request b's new tokens are
+ *                 entries [token_starts[b], token_starts[b + 1]) of slot_map
+ *   slot_map      device int32 [max_tokens], out: slots; -1 from the last new
+ *                 token on (padding, which the cache write skips)
+ *   positions     device int32 [max_tokens], out, or NULL: positions; -1 like slot_map
+ *   free_range_out device int32 [2], out: what is free afterwards; may be free_range
+ *   device_flags  device uint32 word, zeroed by the caller; bits are or-ed in
+ *   workspace     device buffer of paged_decode_append_slots_workspace(batch)
+ *                 bytes, 256-byte aligned, zeroed once after allocating it;
+ *                 calls that share one must not overlap on the GPU
+ *   stream        cudaStream_t as void*
+ * A request that cannot be served keeps its length and table, takes no page,
+ * and its tokens' slots (where they lie below max_tokens) are -1:
+ *   - cached < 0, new < 0, cached + new past max_pages * P, or tokens that end
+ *     past max_tokens: PD_DEVFLAG_BAD_SEQLEN (a negative or too large new
+ *     count takes no entries of slot_map);
+ *   - pages past the end of the free range: PD_DEVFLAG_NO_PAGES (requests
+ *     after it that need no page are still served).
+ * A page id outside [0, num_pages), from the free list or in the table, gives
+ * its tokens slot -1 and sets PD_DEVFLAG_BAD_PAGE. Whole-number results, the
+ * same on every run. Capturable; nothing is allocated.
+ * Returns PD_ERR_INVALID_ARG / PD_ERR_WORKSPACE_TOO_SMALL without launching,
+ * PD_ERR_CUDA if a launch fails.
+ */
+pd_status paged_decode_append_slots(int32_t batch, int32_t page_size, int32_t num_pages, int32_t max_pages,
+                                    int32_t max_tokens, const int32_t* cached_lens, const int32_t* new_tokens,
+                                    const int32_t* free_pages, int32_t num_free, const int32_t* free_range,
+                                    int32_t* block_tables, int32_t* seq_lens, int32_t* token_starts,
+                                    int32_t* slot_map, int32_t* positions, int32_t* free_range_out,
+                                    uint32_t* device_flags, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- The cache write of any number of tokens, by slot ---------------------------
+ *
+ * k / v rows of num_tokens tokens (a prompt's, a chunk's, a decode step's) into
+ * the pages their slots name: with s = slot_map[t], page = s / P,
+ *   k_pool[page, g, s % P, :] = k_in[t, g, :]   (and v likewise on a K != V layer)
+ * and over an e4m3 cache, whose scales the caller has set (calibrated, or of
+ * the pages' earlier rows),
+ *   k_pool[page, g, s % P, i] = e4m3(k_in[t, g, i] / k_scale[page, g]),
+ * the quotient in fp32, rounded to nearest even, clamped to +-448 (NaN stays NaN).
+ *   layer       the decode layer descriptor; head_dim 128, 256 or 512
+ *   num_tokens  >= 0
+ *   k_in, v_in  device bf16, token t's heads [Hkv, d] contiguous from element
+ *               t * k_stride (t * v_stride); strides in elements, multiples of
+ *               8, at least Hkv * d (a fused projection's rows are longer);
+ *               v_in unused when layer->kv_shared
+ *   slot_map    device int32 [num_tokens]; -1 skips the token; no slot twice
+ *   k_pool, v_pool, k_scale, v_scale: as for decode
+ *   device_flags device uint32 word, zeroed by the caller; PD_DEVFLAG_BAD_PAGE
+ *               is or-ed in for a slot below -1 or past the pool (its rows are
+ *               not written)
+ *   stream      cudaStream_t as void*
+ * Inputs and pools 16-byte aligned. Launched as a programmatic dependent that
+ * lets the launch behind it start once it has waited itself.
+ * Returns PD_ERR_INVALID_ARG / PD_ERR_UNSUPPORTED without launching,
+ * PD_ERR_CUDA if the launch fails.
+ */
+pd_status paged_decode_write_slots(const pd_layer_desc* layer, int32_t num_tokens, const void* k_in,
+                                   const void* v_in, int64_t k_stride, int64_t v_stride, const int32_t* slot_map,
+                                   void* k_pool, void* v_pool, uint32_t* device_flags, void* stream);
+pd_status paged_decode_write_slots_fp8(const pd_layer_desc* layer, int32_t num_tokens, const void* k_in,
+                                       const void* v_in, int64_t k_stride, int64_t v_stride,
+                                       const int32_t* slot_map, void* k_pool, void* v_pool, const float* k_scale,
+                                       const float* v_scale, uint32_t* device_flags, void* stream);
+
+/* ---- Decode of a batch whose requests share prefixes ----------------------------
+ *
+ * Groups of consecutive requests share a prefix (a system prompt, a document):
+ * group n is the requests [group_starts[n], group_starts[n + 1]), whose first
+ * prefix_lens[n] tokens lie in the pages of prefix_tables' row n, held once for
+ * all of them; block_tables and seq_lens hold each request's own tokens, which
+ * follow the prefix. Request b attends prefix and own tokens alike:
+ *   out[b, h] = softmax over [prefix | own] (scale q.K) . V,
+ * computed as the prefix part of all of a group's query rows at once (every
+ * prefix byte read once for the group instead of once a request), the own part
+ * as decode, and their merge by log-sum-exp. With T query tokens they are the
+ * last T own tokens, causal among themselves.
+ */
+typedef struct {
+  pd_plan own;              /* the own tokens' part */
+  int32_t num_groups;
+  int32_t max_prefix_pages; /* row length of prefix_tables */
+  int32_t row_tile;         /* query rows a CTA of the prefix pass serves */
+  int32_t tiles;            /* row tiles per KV head over all groups */
+  int32_t num_pieces;       /* pieces a prefix is cut into */
+  int32_t chunk_tokens;     /* prefix tokens per piece */
+  int32_t max_prefix_len;   /* longest prefix the plan was made for */
+  int32_t variant;          /* kernel instance of the prefix pass */
+  uint64_t workspace_bytes; /* bytes the caller must provide */
+  uint64_t lse_offset;      /* fp32 [batch, T, Hq, num_pieces] prefix log-sum-exps */
+  uint64_t o_offset;        /* fp32 [batch, T, Hq, num_pieces, d] prefix partials */
+  uint32_t magic;
+  uint32_t version;
+} pd_shared_plan;
+
+/*
+ * Plan of a shared-prefix decode (pure host function).
+ *   layer            a global layer (window 0; PD_ERR_UNSUPPORTED otherwise), any
+ *                    shape paged_decode_plan_multi serves with this query_tokens;
+ *                    max_pages_per_seq is block_tables' row length
+ *   batch, query_tokens, seq_lens_host, sm_count: as for paged_decode_plan_multi,
+ *                    lengths counting own tokens only
+ *   num_groups       >= 1 (0 only with batch 0)
+ *   group_starts_host [num_groups + 1]: 0 = s_0 <= s_1 <= ... <= s_n = batch
+ *   prefix_lens_host [num_groups]: whole pages, 0 .. max_prefix_pages * page_size
+ * The plan stays valid for calls with the same batch and at most as many row
+ * tiles (groups cut alike; any shorter lengths).
+ */
+pd_status paged_decode_plan_shared(const pd_layer_desc* layer, int32_t batch, int32_t query_tokens,
+                                   const int32_t* seq_lens_host, int32_t num_groups,
+                                   const int32_t* group_starts_host, const int32_t* prefix_lens_host,
+                                   int32_t max_prefix_pages, int32_t sm_count, pd_shared_plan* plan);
+
+/*
+ * One shared-prefix decode of a global layer, merge included.
+ *   q, out           bf16 [batch, Hq, d] ([batch, T, Hq, d] for T > 1)
+ *   k_pool, v_pool (and scales): as for decode
+ *   prefix_tables    device int32 [num_groups, max_prefix_pages]
+ *   prefix_lens      device int32 [num_groups]
+ *   group_starts     device int32 [num_groups + 1]
+ *   block_tables, seq_lens, scale: as for decode, over own tokens
+ *   workspace        at least plan->workspace_bytes, 256-byte aligned, zeroed once
+ * Device conditions go to the workspace's error word
+ * (paged_decode_check_device_error with &plan->own): the decode's own; a bad
+ * prefix page is masked like any other; a prefix length outside its table or
+ * not whole pages sets PD_DEVFLAG_BAD_SEQLEN and is cut; group starts that do
+ * not cut the batch, or need more row tiles than planned, set
+ * PD_DEVFLAG_BAD_GROUP and leave out unspecified (nothing is read or written
+ * out of range). Errors as for paged_decode_global / _global_fp8.
+ */
+pd_status paged_decode_global_shared(const pd_shared_plan* plan, const void* q, const void* k_pool,
+                                     const void* v_pool, const int32_t* prefix_tables, const int32_t* prefix_lens,
+                                     const int32_t* group_starts, const int32_t* block_tables,
+                                     const int32_t* seq_lens, float scale, void* workspace,
+                                     size_t workspace_bytes, void* out, void* stream);
+pd_status paged_decode_global_shared_fp8(const pd_shared_plan* plan, const void* q, const void* k_pool,
+                                         const void* v_pool, const float* k_scale, const float* v_scale,
+                                         const int32_t* prefix_tables, const int32_t* prefix_lens,
+                                         const int32_t* group_starts, const int32_t* block_tables,
+                                         const int32_t* seq_lens, float scale, void* workspace,
+                                         size_t workspace_bytes, void* out, void* stream);
 
 /* ---- Host-in/host-out decode loops ---------------------------------------------
  *

@@ -32,6 +32,8 @@ PD_KV_FP8_E4M3 = 1
 PD_DEVFLAG_BAD_PAGE = 0x1
 PD_DEVFLAG_BAD_SEQLEN = 0x2
 PD_DEVFLAG_WAIT_TIMEOUT = 0x4
+PD_DEVFLAG_NO_PAGES = 0x8
+PD_DEVFLAG_BAD_GROUP = 0x10
 
 EXPORTED = (
     "paged_decode_plan",
@@ -51,6 +53,13 @@ EXPORTED = (
     "paged_decode_rope_table",
     "paged_decode_qkv_norm_rope_write",
     "paged_decode_stage_copy",
+    "paged_decode_append_slots_workspace",
+    "paged_decode_append_slots",
+    "paged_decode_write_slots",
+    "paged_decode_write_slots_fp8",
+    "paged_decode_plan_shared",
+    "paged_decode_global_shared",
+    "paged_decode_global_shared_fp8",
 )
 
 
@@ -91,6 +100,25 @@ class Plan(ctypes.Structure):
         ("workspace_bytes", ctypes.c_uint64),
         ("lse_offset", ctypes.c_uint64),
         ("opart_offset", ctypes.c_uint64),
+        ("magic", ctypes.c_uint32),
+        ("version", ctypes.c_uint32),
+    ]
+
+
+class SharedPlan(ctypes.Structure):
+    _fields_ = [
+        ("own", Plan),
+        ("num_groups", ctypes.c_int32),
+        ("max_prefix_pages", ctypes.c_int32),
+        ("row_tile", ctypes.c_int32),
+        ("tiles", ctypes.c_int32),
+        ("num_pieces", ctypes.c_int32),
+        ("chunk_tokens", ctypes.c_int32),
+        ("max_prefix_len", ctypes.c_int32),
+        ("variant", ctypes.c_int32),
+        ("workspace_bytes", ctypes.c_uint64),
+        ("lse_offset", ctypes.c_uint64),
+        ("o_offset", ctypes.c_uint64),
         ("magic", ctypes.c_uint32),
         ("version", ctypes.c_uint32),
     ]
@@ -160,6 +188,22 @@ def load_library(path: Optional[str] = None):
         lib.paged_decode_rope_table.restype = ctypes.c_int
         lib.paged_decode_qkv_norm_rope_write.argtypes = [ctypes.POINTER(LayerDesc), i32, i32, i32, f32] + [vp] * 14
         lib.paged_decode_qkv_norm_rope_write.restype = ctypes.c_int
+        i64 = ctypes.c_int64
+        lib.paged_decode_append_slots_workspace.argtypes = [i32]
+        lib.paged_decode_append_slots_workspace.restype = u64
+        lib.paged_decode_append_slots.argtypes = [i32] * 5 + [vp] * 3 + [i32] + [vp] * 9 + [u64, vp]
+        lib.paged_decode_append_slots.restype = ctypes.c_int
+        lib.paged_decode_write_slots.argtypes = [ctypes.POINTER(LayerDesc), i32, vp, vp, i64, i64] + [vp] * 5
+        lib.paged_decode_write_slots.restype = ctypes.c_int
+        lib.paged_decode_write_slots_fp8.argtypes = [ctypes.POINTER(LayerDesc), i32, vp, vp, i64, i64] + [vp] * 7
+        lib.paged_decode_write_slots_fp8.restype = ctypes.c_int
+        lib.paged_decode_plan_shared.argtypes = [ctypes.POINTER(LayerDesc), i32, i32, vp, i32, vp, vp, i32, i32,
+                                                 ctypes.POINTER(SharedPlan)]
+        lib.paged_decode_plan_shared.restype = ctypes.c_int
+        lib.paged_decode_global_shared.argtypes = [ctypes.POINTER(SharedPlan)] + [vp] * 8 + [f32, vp, u64, vp, vp]
+        lib.paged_decode_global_shared.restype = ctypes.c_int
+        lib.paged_decode_global_shared_fp8.argtypes = [ctypes.POINTER(SharedPlan)] + [vp] * 10 + [f32, vp, u64, vp, vp]
+        lib.paged_decode_global_shared_fp8.restype = ctypes.c_int
         found = int(lib.paged_decode_abi_version())
         if found != ABI_VERSION:
             raise RuntimeError(f"{p} has ABI version {found}, this binding marshals version {ABI_VERSION}: rebuild it "
@@ -459,3 +503,221 @@ def paged_decode_combine(o_parts, lse_parts, out, stream=None) -> None:
     st = load_library().paged_decode_combine(int(R), int(rows), int(d), _ptr(o_parts), _ptr(lse_parts), _ptr(out),
                                              _stream_ptr(stream))
     _check(st, "paged_decode_combine")
+
+
+# ----------------------------------------------------------------------------
+# Block tables and slot maps, the cache write by slot, shared-prefix decode
+# ----------------------------------------------------------------------------
+
+def _want(t, name: str, dtype, shape=None) -> None:
+    """A tensor handed to the library is contiguous and of the type (and shape) its C argument has."""
+    if t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor, got {t.dtype}"
+                         + ("" if t.is_contiguous() else " (not contiguous)"))
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _same_device(first, **others) -> None:
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+
+
+def paged_decode_append_slots_workspace(batch: int) -> int:
+    """Bytes of the (zeroed) workspace paged_decode_append_slots takes."""
+    return int(load_library().paged_decode_append_slots_workspace(int(batch)))
+
+
+def paged_decode_append_slots(page_size: int, num_pages: int, cached_lens, new_tokens, free_pages, free_range,
+                              block_tables, seq_lens, token_starts, slot_map, positions, free_range_out, device_flags,
+                              workspace, stream=None) -> None:
+    """Hand out the pages the requests' new tokens need and write their slots:
+    block_tables [B, max_pages] is extended in place; seq_lens [B],
+    token_starts [B + 1], slot_map and positions (None: not wanted) [max_tokens]
+    and free_range_out [2] are written. All int32; seq_lens may be cached_lens
+    and free_range_out may be free_range."""
+    import torch
+    i32 = torch.int32
+    B = cached_lens.shape[0]
+    _want(cached_lens, "cached_lens", i32, (B,))
+    _want(new_tokens, "new_tokens", i32, (B,))
+    _want(free_pages, "free_pages", i32, (free_pages.numel(),))
+    _want(free_range, "free_range", i32, (2,))
+    _want(block_tables, "block_tables", i32, (B, block_tables.shape[-1]))
+    _want(seq_lens, "seq_lens", i32, (B,))
+    _want(token_starts, "token_starts", i32, (B + 1,))
+    _want(slot_map, "slot_map", i32, (slot_map.numel(),))
+    if positions is not None:
+        _want(positions, "positions", i32, tuple(slot_map.shape))
+    _want(free_range_out, "free_range_out", i32, (2,))
+    _same_device(cached_lens, new_tokens=new_tokens, free_pages=free_pages, free_range=free_range,
+                 block_tables=block_tables, seq_lens=seq_lens, token_starts=token_starts, slot_map=slot_map,
+                 positions=positions, free_range_out=free_range_out, device_flags=device_flags, workspace=workspace)
+    st = load_library().paged_decode_append_slots(
+        int(B), int(page_size), int(num_pages), int(block_tables.shape[-1]), int(slot_map.numel()),
+        _ptr(cached_lens), _ptr(new_tokens), _ptr(free_pages), int(free_pages.numel()), _ptr(free_range),
+        _ptr(block_tables), _ptr(seq_lens), _ptr(token_starts), _ptr(slot_map), _ptr(positions),
+        _ptr(free_range_out), _ptr(device_flags), _ptr(workspace), int(workspace.numel() * workspace.element_size()),
+        _stream_ptr(stream))
+    _check(st, "paged_decode_append_slots")
+
+
+def _token_rows(t, name: str, desc: LayerDesc, tokens: int) -> int:
+    """The token stride (elements) of k / v rows [tokens, Hkv, d] whose heads are contiguous."""
+    import torch
+    if t.dtype != torch.bfloat16 or tuple(t.shape) != (tokens, desc.num_kv_heads, desc.head_dim):
+        raise ValueError(f"{name}: expected bf16 {(tokens, desc.num_kv_heads, desc.head_dim)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    if (desc.head_dim > 1 and t.stride(2) != 1) or (desc.num_kv_heads > 1 and t.stride(1) != desc.head_dim):
+        raise ValueError(f"{name}: a token's heads must be contiguous, strides {t.stride()}")
+    return t.stride(0) if tokens > 1 else max(t.stride(0), desc.num_kv_heads * desc.head_dim)
+
+
+def _write_slots(fp8: bool, desc, k_in, v_in, slot_map, k_pool, v_pool, k_scale, v_scale, device_flags, stream):
+    import torch
+    n = slot_map.numel()
+    _want(slot_map, "slot_map", torch.int32)
+    pool_type = torch.uint8 if fp8 else torch.bfloat16
+    shape = (desc.num_pages, desc.num_kv_heads, desc.page_size, desc.head_dim)
+    _want(k_pool, "k_pool", pool_type, shape)
+    ks = _token_rows(k_in, "k_in", desc, n)
+    vs = 0
+    if not desc.kv_shared:
+        if v_in is None or v_pool is None:
+            raise ValueError("a K != V layer needs v_in and v_pool")
+        _want(v_pool, "v_pool", pool_type, shape)
+        vs = _token_rows(v_in, "v_in", desc, n)
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t is not None:
+            _want(t, name, torch.float32, shape[:2])
+    _same_device(k_in, v_in=v_in, slot_map=slot_map, k_pool=k_pool, v_pool=v_pool, k_scale=k_scale, v_scale=v_scale,
+                 device_flags=device_flags)
+    args = [ctypes.byref(desc), n, _ptr(k_in), _ptr(None if desc.kv_shared else v_in), ks, vs, _ptr(slot_map),
+            _ptr(k_pool), _ptr(v_pool)]
+    lib = load_library()
+    if fp8:
+        st = lib.paged_decode_write_slots_fp8(*args, _ptr(k_scale), _ptr(v_scale), _ptr(device_flags),
+                                              _stream_ptr(stream))
+    else:
+        st = lib.paged_decode_write_slots(*args, _ptr(device_flags), _stream_ptr(stream))
+    _check(st, "paged_decode_write_slots_fp8" if fp8 else "paged_decode_write_slots")
+
+
+def paged_decode_write_slots(desc: LayerDesc, k_in, v_in, slot_map, k_pool, v_pool, device_flags, stream=None) -> None:
+    """Write k_in / v_in [tokens, Hkv, d] (any token stride) into the pools' rows
+    slot_map names; -1 skips a token."""
+    _write_slots(False, desc, k_in, v_in, slot_map, k_pool, v_pool, None, None, device_flags, stream)
+
+
+def paged_decode_write_slots_fp8(desc: LayerDesc, k_in, v_in, slot_map, k_pool, v_pool, k_scale, v_scale,
+                                 device_flags, stream=None) -> None:
+    """The same into e4m3 pools (uint8), each row divided by its (page, head)'s scale."""
+    _write_slots(True, desc, k_in, v_in, slot_map, k_pool, v_pool, k_scale, v_scale, device_flags, stream)
+
+
+def paged_decode_plan_shared(desc: LayerDesc, query_tokens: int, seq_lens_host: Sequence[int],
+                             group_starts_host: Sequence[int], prefix_lens_host: Sequence[int], max_prefix_pages: int,
+                             sm_count: int) -> SharedPlan:
+    """Plan of a shared-prefix decode: group n is requests
+    [group_starts[n], group_starts[n + 1]), its prefix prefix_lens[n] tokens;
+    seq_lens count each request's own tokens."""
+    def arr(v):
+        return ctypes.cast((ctypes.c_int32 * max(1, len(v)))(*[int(x) for x in v]), ctypes.c_void_p)
+
+    if len(group_starts_host) != len(prefix_lens_host) + 1:
+        raise ValueError("group_starts has one entry more than prefix_lens")
+    plan = SharedPlan()
+    st = load_library().paged_decode_plan_shared(
+        ctypes.byref(desc), len(seq_lens_host), int(query_tokens), arr(seq_lens_host), len(prefix_lens_host),
+        arr(group_starts_host), arr(prefix_lens_host), int(max_prefix_pages), int(sm_count), ctypes.byref(plan))
+    _check(st, "paged_decode_plan_shared")
+    return plan
+
+
+def _workspace_bytes(workspace, given) -> int:
+    return int(workspace.numel() * workspace.element_size() if given is None else given)
+
+
+def paged_decode_global_shared(plan: SharedPlan, q, k_pool, v_pool, prefix_tables, prefix_lens, group_starts,
+                               block_tables, seq_lens, scale: float, workspace, out, stream=None,
+                               workspace_bytes: Optional[int] = None) -> None:
+    """Decode of a batch whose groups share prefixes, merge included."""
+    st = load_library().paged_decode_global_shared(
+        ctypes.byref(plan), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(prefix_tables), _ptr(prefix_lens),
+        _ptr(group_starts), _ptr(block_tables), _ptr(seq_lens), float(scale), _ptr(workspace),
+        _workspace_bytes(workspace, workspace_bytes), _ptr(out), _stream_ptr(stream))
+    _check(st, "paged_decode_global_shared")
+
+
+def paged_decode_global_shared_fp8(plan: SharedPlan, q, k_pool, v_pool, k_scale, v_scale, prefix_tables, prefix_lens,
+                                   group_starts, block_tables, seq_lens, scale: float, workspace, out, stream=None,
+                                   workspace_bytes: Optional[int] = None) -> None:
+    """The same over an e4m3 cache with per-(page, KV head) scales."""
+    st = load_library().paged_decode_global_shared_fp8(
+        ctypes.byref(plan), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(prefix_tables),
+        _ptr(prefix_lens), _ptr(group_starts), _ptr(block_tables), _ptr(seq_lens), float(scale), _ptr(workspace),
+        _workspace_bytes(workspace, workspace_bytes), _ptr(out), _stream_ptr(stream))
+    _check(st, "paged_decode_global_shared_fp8")
+
+
+class SharedPrefixStep:
+    """Plan + workspace of a shared-prefix decode of one layer, reusable across
+    steps whose groups are cut alike and whose lengths are no longer than the
+    planned ones."""
+
+    def __init__(self, num_q_heads, num_kv_heads, head_dim, page_size, num_pages, max_pages_per_seq, seq_lens_host,
+                 *, group_starts, prefix_lens, max_prefix_pages, kv_shared=False, kv_dtype=PD_KV_BF16,
+                 query_tokens=1, sm_count=None, device=None):
+        import torch
+        device = torch.device("cuda") if device is None else torch.device(device)
+        if sm_count is None:
+            sm_count = torch.cuda.get_device_properties(device).multi_processor_count
+        self.desc = layer_desc(num_q_heads, num_kv_heads, head_dim, page_size, num_pages, max_pages_per_seq, 0,
+                               kv_shared, kv_dtype)
+        self.fp8 = kv_dtype == PD_KV_FP8_E4M3
+        self.query_tokens = int(query_tokens)
+        self.plan = paged_decode_plan_shared(self.desc, self.query_tokens, list(seq_lens_host), list(group_starts),
+                                             list(prefix_lens), max_prefix_pages, sm_count)
+        # zeroed once: the first word is the device error flag
+        nbytes = int(self.plan.workspace_bytes)
+        self.workspace = torch.zeros((nbytes + 255) // 256 * 256, dtype=torch.uint8, device=device)
+
+    def __call__(self, q, k_pool, v_pool, prefix_tables, prefix_lens, group_starts, block_tables, seq_lens, scale, out,
+                 stream=None, k_scale=None, v_scale=None):
+        self._check_tensors(q, k_pool, v_pool, prefix_tables, prefix_lens, group_starts, block_tables, seq_lens, out,
+                            k_scale, v_scale)
+        if self.fp8:
+            paged_decode_global_shared_fp8(self.plan, q, k_pool, v_pool, k_scale, v_scale, prefix_tables, prefix_lens,
+                                           group_starts, block_tables, seq_lens, scale, self.workspace, out, stream)
+        else:
+            paged_decode_global_shared(self.plan, q, k_pool, v_pool, prefix_tables, prefix_lens, group_starts,
+                                       block_tables, seq_lens, scale, self.workspace, out, stream)
+        return out
+
+    def _check_tensors(self, q, k_pool, v_pool, prefix_tables, prefix_lens, group_starts, block_tables, seq_lens, out,
+                       k_scale, v_scale):
+        import torch
+        d, pl = self.desc, self.plan
+        B, T = pl.own.batch, self.query_tokens
+        heads = (d.num_q_heads, d.head_dim)
+        _want(q, "q", torch.bfloat16, ((B, T) if T > 1 or q.dim() == 4 else (B,)) + heads)
+        _want(out, "out", torch.bfloat16, tuple(q.shape))
+        pool = (d.num_pages, d.num_kv_heads, d.page_size, d.head_dim)
+        for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
+            if t is not None:
+                _want(t, name, torch.uint8 if self.fp8 else torch.bfloat16, pool)
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is not None:
+                _want(t, name, torch.float32, pool[:2])
+        _want(prefix_tables, "prefix_tables", torch.int32, (pl.num_groups, pl.max_prefix_pages))
+        _want(prefix_lens, "prefix_lens", torch.int32, (pl.num_groups,))
+        _want(group_starts, "group_starts", torch.int32, (pl.num_groups + 1,))
+        _want(block_tables, "block_tables", torch.int32, (B, d.max_pages_per_seq))
+        _want(seq_lens, "seq_lens", torch.int32, (B,))
+        _same_device(q, k_pool=k_pool, v_pool=v_pool, prefix_tables=prefix_tables, prefix_lens=prefix_lens,
+                     group_starts=group_starts, block_tables=block_tables, seq_lens=seq_lens, out=out,
+                     k_scale=k_scale, v_scale=v_scale)
+
+    def check(self, stream=None) -> int:
+        return paged_decode_check_device_error(self.plan.own, self.workspace, stream)

@@ -268,6 +268,18 @@ pd_status merge_workspace(const pd_plan* plan, const uint8_t* ws, void* out, flo
 
 }  // namespace
 
+namespace pd {
+
+pd_status launch_own_part(const pd_plan* plan, const void* q, const void* k_pool, const void* v_pool,
+                          const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                          const int32_t* seq_lens, float scale, void* workspace, size_t workspace_bytes, void* out,
+                          void* stream) {
+  return stage1(plan, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens, 0, scale, workspace,
+                workspace_bytes, out, stream);
+}
+
+}  // namespace pd
+
 extern "C" {
 
 pd_status paged_decode_global(const pd_plan* plan, const void* q, const void* k_pool, const void* v_pool,
@@ -321,7 +333,7 @@ pd_status paged_decode_global_partial(const pd_plan* plan, const void* q, const 
                                       const int32_t* block_tables, const int32_t* seq_lens, float scale,
                                       void* workspace, size_t workspace_bytes, float* o_out, float* lse_out,
                                       void* stream) {
-  if (!plan || !pd::plan_is_valid(plan) || !plan->partial) return PD_ERR_INVALID_ARG;
+  if (!plan || !pd::plan_is_valid(plan) || plan->partial != 1) return PD_ERR_INVALID_ARG;
   if (plan->batch > 0 && (!o_out || !lse_out || !aligned(o_out, 16) || !aligned(lse_out, 4)))
     return PD_ERR_INVALID_ARG;
   // stage 1 writes only the workspace for a partial plan; its `out` is not touched

@@ -10,6 +10,8 @@ namespace pd {
 constexpr uint32_t kErrBadPage = 0x1u;
 constexpr uint32_t kErrBadSeqLen = 0x2u;
 constexpr uint32_t kErrTimeout = 0x4u;
+constexpr uint32_t kErrNoPages = 0x8u;
+constexpr uint32_t kErrBadGroup = 0x10u;
 
 // Workspace: [error word, padded to 256 B][lse fp32 B*Hq*S][o_part fp32 B*Hq*S*D]
 constexpr uint64_t kWorkspaceHeader = 256;

@@ -528,6 +528,13 @@ pd_status plan_impl(const pd_layer_desc* layer, int32_t batch, int32_t query_tok
 
 namespace pd {
 
+// The own tokens' part of a shared-prefix decode: a plan that always leaves
+// fp32 pieces in the workspace (partial 2: any query_tokens and cache type).
+pd_status plan_own_part(const pd_layer_desc* layer, int32_t batch, int32_t query_tokens,
+                        const int32_t* seq_lens_host, int32_t sm_count, pd_plan* plan) {
+  return plan_impl(layer, batch, query_tokens, seq_lens_host, sm_count, 2, plan);
+}
+
 bool plan_is_valid(const pd_plan* plan) {
   if (!plan || plan->magic != kPlanMagic || plan->version != (uint32_t)kAbiVersion) return false;
   if (plan->variant < 0 || plan->variant >= kNumVariants) return false;
@@ -552,9 +559,9 @@ bool plan_is_valid(const pd_plan* plan) {
   if (plan->merge_mode < 0 || plan->merge_mode > 2) return false;
   if (plan->test_stall_bytes < 0 || plan->test_stall_bytes > (1 << 16) || plan->test_stall_bytes % 16 != 0)
     return false;
-  if (plan->partial != 0 && plan->partial != 1) return false;
+  if (plan->partial < 0 || plan->partial > 2) return false;
   if (plan->early_kv != 0 && plan->early_kv != 1) return false;
-  if (plan->partial ? (plan->merge_mode != 1 || plan->query_tokens != 1 || ly.window != 0)
+  if (plan->partial ? (plan->merge_mode != 1 || (plan->partial == 1 && plan->query_tokens != 1) || ly.window != 0)
                     : ((plan->num_splits == 1) != (plan->merge_mode == 0)))
     return false;
   if (plan->merge_mode == 2 && plan->num_splits > std::min(kMaxClusterSplits, v.max_cluster)) return false;

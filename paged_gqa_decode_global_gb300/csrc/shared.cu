@@ -1,0 +1,373 @@
+// Decode of a batch whose requests share prefixes (sm_103a): planner, prefix
+// pass, merge and entry points.
+//
+// Mathematics: softmax attention over [prefix | own] splits into parts whose
+// normalised outputs o_s and log-sum-exps l_s merge exactly,
+//   out = sum_s w_s o_s,  w_s = exp(l_s - M) / sum_s' exp(l_s' - M),  M = max_s l_s,
+// so the prefix part is computed for all query rows of a group at once (rows =
+// requests x query tokens x heads of a KV head's group), the own part by the
+// decode's stage 1, and one merge joins the pieces of both.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "pd_common.cuh"
+#include "shared.h"
+
+namespace pd {
+namespace {
+
+constexpr uint32_t kSharedMagic = 0x50445348u;  // "PDSH"
+constexpr int32_t kSharedVersion = 1;
+
+// Row tile z of the launch: its group, first row and row count (0: none).
+struct Tile {
+  int group, first, rows, start;
+};
+
+__device__ __forceinline__ Tile find_tile(const SharedParams& p, int z) {
+  Tile t{-1, 0, 0, 0};
+  const int per_req = p.query_tokens * p.group;
+  int at = 0;
+  for (int g = 0; g < p.num_groups; ++g) {
+    const int s = max(0, min(p.group_starts[g], p.batch)), e = max(s, min(p.group_starts[g + 1], p.batch));
+    const int rows = (e - s) * per_req, n = (rows + p.row_tile - 1) / p.row_tile;
+    if (z < at + n) {
+      t.group = g;
+      t.first = (z - at) * p.row_tile;
+      t.rows = min(p.row_tile, rows - t.first);
+      t.start = s;
+      return t;
+    }
+    at += n;
+  }
+  return t;
+}
+
+// Whether the device's group starts cut the batch, in no more row tiles than planned.
+__device__ __forceinline__ bool groups_ok(const SharedParams& p) {
+  const int per_req = p.query_tokens * p.group;
+  long long tiles = 0;
+  if (p.group_starts[0] != 0 || p.group_starts[p.num_groups] != p.batch) return false;
+  for (int g = 0; g < p.num_groups; ++g) {
+    const int s = p.group_starts[g], e = p.group_starts[g + 1];
+    if (e < s || e > p.batch) return false;
+    tiles += ((long long)(e - s) * per_req + p.row_tile - 1) / p.row_tile;
+  }
+  return tiles <= p.tiles;
+}
+
+__device__ __forceinline__ float load_value(const uint8_t* pool, size_t i, bool fp8) {
+  if (fp8) return float(reinterpret_cast<const __nv_fp8_e4m3*>(pool)[i]);
+  return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(pool)[i]);
+}
+
+// The plain prefix pass: a warp per query row, the lanes across the head dims.
+__global__ void __launch_bounds__(256) prefix_plain_kernel(const SharedParams p) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int piece = blockIdx.x, g = blockIdx.y, lane = threadIdx.x & 31;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0 && !groups_ok(p))
+    atomicOr(p.err, kErrBadGroup);
+  const Tile t = find_tile(p, blockIdx.z);
+  if (t.group < 0) return;
+  int L = p.prefix_lens[t.group];
+  const int cap = p.max_prefix_pages * p.page_size;
+  if (L < 0 || L > cap || L % p.page_size != 0) {
+    if (threadIdx.x == 0) atomicOr(p.err, kErrBadSeqLen);
+    L = max(0, min(L, cap)) / p.page_size * p.page_size;
+  }
+  const long long lo = (long long)piece * p.chunk_tokens;
+  const long long hi = piece == p.num_pieces - 1 ? L : min((long long)L, lo + p.chunk_tokens);
+  const bool fp8 = p.k_scale != nullptr;
+  const int n = p.head_dim / 32;
+  for (int r = threadIdx.x >> 5; r < t.rows; r += 8) {
+    const int i = t.first + r, per_req = p.query_tokens * p.group;
+    const size_t row = ((size_t)(t.start + i / per_req) * p.query_tokens + (i / p.group) % p.query_tokens) *
+                           p.num_q_heads + (size_t)g * p.group + i % p.group;
+    float q[16], o[16], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      o[k] = 0.f;
+      q[k] = k < n ? __uint_as_float((uint32_t)p.q[row * p.head_dim + k * 32 + lane] << 16) : 0.f;
+    }
+    for (long long tok = lo; tok < hi; ++tok) {
+      const int page = p.prefix_tables[(size_t)t.group * p.max_prefix_pages + tok / p.page_size];
+      if ((unsigned)page >= (unsigned)p.num_pages) {
+        if (lane == 0) atomicOr(p.err, kErrBadPage);
+        continue;
+      }
+      const size_t head = (size_t)page * p.num_kv_heads + g;
+      const size_t at = (head * p.page_size + tok % p.page_size) * p.head_dim;
+      float s = 0.f;
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        if (k < n) s = fmaf(q[k], load_value(p.k_pool, at + k * 32 + lane, fp8), s);
+#pragma unroll
+      for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(kFullMask, s, d);
+      s *= p.scale_log2 * (fp8 ? p.k_scale[head] : 1.f);
+      const float mn = fmaxf(m, s), a = exp2f(m - mn), e = exp2f(s - mn), v = e * (fp8 ? p.v_scale[head] : 1.f);
+      l = l * a + e;
+      m = mn;
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        if (k < n) o[k] = fmaf(v, load_value(p.v_pool, at + k * 32 + lane, fp8), o[k] * a);
+    }
+    const size_t part = row * p.num_pieces + piece;
+    if (lane == 0) p.lse_part[part] = l > 0.f || isnan(l) ? (m + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      if (k < n) p.o_part[part * p.head_dim + k * 32 + lane] = l > 0.f || isnan(l) ? o[k] / l : 0.f;
+  }
+}
+
+struct JoinParams {
+  const float* lse[2];  // own, prefix: [rows][pieces]
+  const float* o[2];
+  int pieces[2];
+  uint16_t* out;
+  int head_dim;
+};
+
+// One CTA per row: out = sum over both parts' pieces of w_s o_s.
+__global__ void __launch_bounds__(128) join_kernel(const JoinParams p) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const size_t row = blockIdx.x;
+  float M = -INFINITY;
+  for (int part = 0; part < 2; ++part)
+    for (int s = 0; s < p.pieces[part]; ++s) {
+      const float l = p.lse[part][row * p.pieces[part] + s];
+      M = (l > M || isnan(l)) ? l : M;
+    }
+  for (int d = threadIdx.x; d < p.head_dim; d += 128) {
+    float acc = 0.f, sum = 0.f;
+    if (M != -INFINITY)
+      for (int part = 0; part < 2; ++part)
+        for (int s = 0; s < p.pieces[part]; ++s) {
+          const size_t at = row * p.pieces[part] + s;
+          const float l = p.lse[part][at];
+          if (l == -INFINITY) continue;
+          const float w = expf(l - M);
+          sum += w;
+          acc = fmaf(w, p.o[part][at * p.head_dim + d], acc);
+        }
+    const __nv_bfloat16 v = __float2bfloat16_rn(M != -INFINITY ? acc / sum : 0.f);
+    p.out[row * p.head_dim + d] = *reinterpret_cast<const uint16_t*>(&v);
+  }
+}
+
+uint64_t align_up(uint64_t x, uint64_t a) { return (x + a - 1) / a * a; }
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// Query rows a CTA of the prefix pass serves.
+int row_tile_for(int head_dim, long long rows) {
+  const int most = head_dim == 512 ? 64 : 128;
+  int n = 16;
+  while (n < most && n < rows) n *= 2;
+  return n;
+}
+
+bool shared_plan_is_valid(const pd_shared_plan* plan) {
+  if (!plan || plan->magic != kSharedMagic || plan->version != (uint32_t)kSharedVersion) return false;
+  const pd_plan& own = plan->own;
+  if (!plan_is_valid(&own) || own.partial != 2) return false;
+  if (plan->num_groups < 0 || plan->max_prefix_pages < 1 || plan->tiles < 0 || plan->tiles > 65535) return false;
+  if (own.batch > 0 && plan->num_groups < 1) return false;
+  if (plan->row_tile != 16 && plan->row_tile != 32 && plan->row_tile != 64 && plan->row_tile != 128) return false;
+  if (plan->num_pieces < 1 || plan->num_pieces > 1024) return false;
+  if (plan->chunk_tokens < kPrefixTile || plan->chunk_tokens % kPrefixTile != 0) return false;
+  if ((long long)plan->max_prefix_pages * own.layer.page_size > 0x7fffffffLL) return false;
+  const uint64_t rows = (uint64_t)own.batch * own.query_tokens * own.layer.num_q_heads;
+  if (rows > 0x7fffffffull) return false;
+  uint64_t lse = 0, o = 0, end = 0;
+  if (plan->lse_offset < own.workspace_bytes || plan->lse_offset % 256 != 0 || plan->o_offset % 256 != 0) return false;
+  if (__builtin_mul_overflow(rows, (uint64_t)plan->num_pieces * 4ull, &lse) ||
+      __builtin_mul_overflow(lse, (uint64_t)own.layer.head_dim, &o) ||
+      __builtin_add_overflow(plan->lse_offset, lse, &end) || plan->o_offset < end ||
+      __builtin_add_overflow(plan->o_offset, o, &end) || plan->workspace_bytes < end)
+    return false;
+  return true;
+}
+
+pd_status plan_shared(const pd_layer_desc* layer, int32_t batch, int32_t query_tokens, const int32_t* seq_lens_host,
+                      int32_t num_groups, const int32_t* group_starts_host, const int32_t* prefix_lens_host,
+                      int32_t max_prefix_pages, int32_t sm_count, pd_shared_plan* plan) {
+  if (!layer || !plan || num_groups < 0 || max_prefix_pages < 1) return PD_ERR_INVALID_ARG;
+  if (layer->window != 0) return layer->window < 0 ? PD_ERR_INVALID_ARG : PD_ERR_UNSUPPORTED;
+  pd_shared_plan sp;
+  std::memset(&sp, 0, sizeof(sp));
+  const pd_status st = plan_own_part(layer, batch, query_tokens, seq_lens_host, sm_count, &sp.own);
+  if (st != PD_OK) return st;
+  const pd_layer_desc& ly = *layer;
+  const long long cap = (long long)max_prefix_pages * ly.page_size;
+  if (cap > 0x7fffffffLL || num_groups > 65535) return PD_ERR_INVALID_ARG;
+  if (batch > 0 && (num_groups < 1 || !group_starts_host || !prefix_lens_host)) return PD_ERR_INVALID_ARG;
+  const int per_req = query_tokens * (ly.num_q_heads / ly.num_kv_heads);
+  long long most_rows = 0;
+  int32_t longest = 0;
+  if (batch > 0) {
+    if (group_starts_host[0] != 0 || group_starts_host[num_groups] != batch) return PD_ERR_INVALID_ARG;
+    for (int n = 0; n < num_groups; ++n) {
+      const int32_t s = group_starts_host[n], e = group_starts_host[n + 1], len = prefix_lens_host[n];
+      if (e < s || e > batch) return PD_ERR_INVALID_ARG;
+      if (len < 0 || len > cap || len % ly.page_size != 0) return PD_ERR_INVALID_ARG;
+      most_rows = std::max(most_rows, (long long)(e - s) * per_req);
+      if (e > s) longest = std::max(longest, len);
+    }
+  }
+  sp.num_groups = num_groups;
+  sp.max_prefix_pages = max_prefix_pages;
+  sp.max_prefix_len = longest;
+  sp.row_tile = row_tile_for(ly.head_dim, most_rows);
+  long long tiles = 0;
+  for (int n = 0; batch > 0 && n < num_groups; ++n)
+    tiles += ((long long)(group_starts_host[n + 1] - group_starts_host[n]) * per_req + sp.row_tile - 1) / sp.row_tile;
+  if (tiles > 65535) return PD_ERR_UNSUPPORTED;
+  sp.tiles = (int32_t)tiles;
+  // one wave of CTAs, pieces of whole tiles
+  const long long units = std::max<long long>(1, tiles * ly.num_kv_heads);
+  const long long pieces = std::max<long long>(1, sm_count / units);
+  const long long want = align_up((uint64_t)std::max<long long>(1, (longest + pieces - 1) / pieces), kPrefixTile);
+  sp.chunk_tokens = (int32_t)want;
+  sp.num_pieces = (int32_t)std::max<long long>(1, (longest + want - 1) / want);
+  const uint64_t rows = (uint64_t)batch * query_tokens * ly.num_q_heads;
+  if (rows > 0x7fffffffull) return PD_ERR_UNSUPPORTED;
+  sp.lse_offset = align_up(sp.own.workspace_bytes, 256);
+  sp.o_offset = align_up(sp.lse_offset + rows * sp.num_pieces * 4ull, 256);
+  sp.workspace_bytes = sp.o_offset + rows * sp.num_pieces * (uint64_t)ly.head_dim * 4ull;
+  sp.magic = kSharedMagic;
+  sp.version = kSharedVersion;
+  *plan = sp;
+  return PD_OK;
+}
+
+template <class... Params, class... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, void* stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  return e;
+}
+
+pd_status decode_shared(const pd_shared_plan* plan, bool fp8, const void* q, const void* k_pool, const void* v_pool,
+                        const float* k_scale, const float* v_scale, const int32_t* prefix_tables,
+                        const int32_t* prefix_lens, const int32_t* group_starts, const int32_t* block_tables,
+                        const int32_t* seq_lens, float scale, void* workspace, size_t workspace_bytes, void* out,
+                        void* stream) {
+  if (!shared_plan_is_valid(plan)) return PD_ERR_INVALID_ARG;
+  const pd_plan& own = plan->own;
+  const pd_layer_desc& ly = own.layer;
+  if ((ly.kv_dtype == PD_KV_FP8_E4M3) != fp8 || !std::isfinite(scale)) return PD_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256)) return PD_ERR_INVALID_ARG;
+  if (workspace_bytes < plan->workspace_bytes) return PD_ERR_WORKSPACE_TOO_SMALL;
+  if (own.batch == 0) return PD_OK;
+  // everything before anything is queued: what stage 1 refuses too
+  if (!q || !k_pool || !block_tables || !seq_lens || !out || !prefix_tables || !prefix_lens || !group_starts)
+    return PD_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(out, 16) || !aligned(block_tables, 4) ||
+      !aligned(seq_lens, 4) || !aligned(prefix_tables, 4) || !aligned(prefix_lens, 4) || !aligned(group_starts, 4))
+    return PD_ERR_INVALID_ARG;
+  if (ly.kv_shared ? (v_pool && v_pool != k_pool) : (!v_pool || v_pool == k_pool || !aligned(v_pool, 16)))
+    return PD_ERR_INVALID_ARG;
+  if (fp8) {
+    if (!k_scale || !aligned(k_scale, 4)) return PD_ERR_INVALID_ARG;
+    if (ly.kv_shared ? (v_scale && v_scale != k_scale) : (!v_scale || !aligned(v_scale, 4))) return PD_ERR_INVALID_ARG;
+  }
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  SharedParams p = {};
+  p.q = static_cast<const uint16_t*>(q);
+  p.k_pool = static_cast<const uint8_t*>(k_pool);
+  p.v_pool = static_cast<const uint8_t*>(ly.kv_shared ? k_pool : v_pool);
+  p.k_scale = fp8 ? k_scale : nullptr;
+  p.v_scale = fp8 ? (ly.kv_shared ? k_scale : v_scale) : nullptr;
+  p.prefix_tables = prefix_tables;
+  p.prefix_lens = prefix_lens;
+  p.group_starts = group_starts;
+  p.lse_part = reinterpret_cast<float*>(ws + plan->lse_offset);
+  p.o_part = reinterpret_cast<float*>(ws + plan->o_offset);
+  p.err = reinterpret_cast<uint32_t*>(ws);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.batch = own.batch;
+  p.num_groups = plan->num_groups;
+  p.query_tokens = own.query_tokens;
+  p.num_q_heads = ly.num_q_heads;
+  p.num_kv_heads = ly.num_kv_heads;
+  p.group = ly.num_q_heads / ly.num_kv_heads;
+  p.head_dim = ly.head_dim;
+  p.page_size = ly.page_size;
+  p.num_pages = ly.num_pages;
+  p.max_prefix_pages = plan->max_prefix_pages;
+  p.row_tile = plan->row_tile;
+  p.tiles = plan->tiles;
+  p.num_pieces = plan->num_pieces;
+  p.chunk_tokens = plan->chunk_tokens;
+  if (launch_dependent(prefix_plain_kernel, dim3(plan->num_pieces, ly.num_kv_heads, plan->tiles), 256, stream, p) !=
+      cudaSuccess)
+    return PD_ERR_CUDA;
+  const pd_status st = launch_own_part(&own, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens, scale,
+                                       workspace, workspace_bytes, out, stream);
+  if (st != PD_OK) return st;
+  JoinParams j = {};
+  j.lse[0] = reinterpret_cast<const float*>(ws + own.lse_offset);
+  j.o[0] = reinterpret_cast<const float*>(ws + own.opart_offset);
+  j.pieces[0] = own.num_splits;
+  j.lse[1] = p.lse_part;
+  j.o[1] = p.o_part;
+  j.pieces[1] = plan->num_pieces;
+  j.out = static_cast<uint16_t*>(out);
+  j.head_dim = ly.head_dim;
+  const unsigned rows = (unsigned)own.batch * own.query_tokens * ly.num_q_heads;
+  if (launch_dependent(join_kernel, dim3(rows), 128, stream, j) != cudaSuccess) return PD_ERR_CUDA;
+  return PD_OK;
+}
+
+}  // namespace
+}  // namespace pd
+
+extern "C" {
+
+pd_status paged_decode_plan_shared(const pd_layer_desc* layer, int32_t batch, int32_t query_tokens,
+                                   const int32_t* seq_lens_host, int32_t num_groups,
+                                   const int32_t* group_starts_host, const int32_t* prefix_lens_host,
+                                   int32_t max_prefix_pages, int32_t sm_count, pd_shared_plan* plan) {
+  try {
+    return pd::plan_shared(layer, batch, query_tokens, seq_lens_host, num_groups, group_starts_host,
+                           prefix_lens_host, max_prefix_pages, sm_count, plan);
+  } catch (...) {  // the planner's host allocations
+    return PD_ERR_UNSUPPORTED;
+  }
+}
+
+pd_status paged_decode_global_shared(const pd_shared_plan* plan, const void* q, const void* k_pool,
+                                     const void* v_pool, const int32_t* prefix_tables, const int32_t* prefix_lens,
+                                     const int32_t* group_starts, const int32_t* block_tables,
+                                     const int32_t* seq_lens, float scale, void* workspace,
+                                     size_t workspace_bytes, void* out, void* stream) {
+  return pd::decode_shared(plan, false, q, k_pool, v_pool, nullptr, nullptr, prefix_tables, prefix_lens, group_starts,
+                           block_tables, seq_lens, scale, workspace, workspace_bytes, out, stream);
+}
+
+pd_status paged_decode_global_shared_fp8(const pd_shared_plan* plan, const void* q, const void* k_pool,
+                                         const void* v_pool, const float* k_scale, const float* v_scale,
+                                         const int32_t* prefix_tables, const int32_t* prefix_lens,
+                                         const int32_t* group_starts, const int32_t* block_tables,
+                                         const int32_t* seq_lens, float scale, void* workspace,
+                                         size_t workspace_bytes, void* out, void* stream) {
+  return pd::decode_shared(plan, true, q, k_pool, v_pool, k_scale, v_scale, prefix_tables, prefix_lens, group_starts,
+                           block_tables, seq_lens, scale, workspace, workspace_bytes, out, stream);
+}
+
+}  // extern "C"

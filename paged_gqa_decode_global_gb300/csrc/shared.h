@@ -1,0 +1,41 @@
+// Shared-prefix decode: what its planner, entry points and kernels share.
+#pragma once
+
+#include <cstdint>
+
+#include "paged_decode.h"
+#include "pd_kernels.h"
+
+namespace pd {
+
+constexpr int kPrefixTile = 128;  // prefix tokens of one tile of the prefix pass
+
+struct SharedParams {
+  const uint16_t* q;
+  const uint8_t* k_pool;
+  const uint8_t* v_pool;
+  const float* k_scale;  // FP8
+  const float* v_scale;
+  const int32_t* prefix_tables;
+  const int32_t* prefix_lens;
+  const int32_t* group_starts;
+  float* lse_part;  // [B*T*Hq][num_pieces]
+  float* o_part;    // [B*T*Hq][num_pieces][D]
+  uint32_t* err;
+  float scale_log2;
+  int32_t batch, num_groups, query_tokens, num_q_heads, num_kv_heads, group, head_dim;
+  int32_t page_size, num_pages, max_prefix_pages;
+  int32_t row_tile, tiles, num_pieces, chunk_tokens;
+};
+
+// plan.cu
+bool plan_is_valid(const pd_plan* plan);
+pd_status plan_own_part(const pd_layer_desc* layer, int32_t batch, int32_t query_tokens,
+                        const int32_t* seq_lens_host, int32_t sm_count, pd_plan* plan);
+// abi.cu: stage 1 of the own part into the workspace
+pd_status launch_own_part(const pd_plan* plan, const void* q, const void* k_pool, const void* v_pool,
+                          const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                          const int32_t* seq_lens, float scale, void* workspace, size_t workspace_bytes, void* out,
+                          void* stream);
+
+}  // namespace pd
