@@ -20,11 +20,12 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxContexts = 64;
 
-// Per CUDA context, one bit per variant whose dynamic shared-memory limit has
-// been raised there (a function attribute belongs to the context it was set in).
+// Per CUDA context, one bit per kernel instance whose dynamic shared-memory limit
+// has been raised there (a function attribute belongs to the context it was set
+// in): word 0 the stage-1 variants, word 1 the prefix pass's.
 struct SmemReady {
   unsigned long long ctx_id;
-  uint64_t bits;
+  uint64_t bits[2];
 };
 #define PD_VARIANT_ID_FITS_A_BIT(ID, ...) static_assert((ID) >= 0 && (ID) < 64, "one bit per variant id");
 PD_FOR_EACH_VARIANT(PD_VARIANT_ID_FITS_A_BIT)
@@ -109,7 +110,7 @@ pd_status encode_pool_maps(pd::Stage1Params& p, const void* k_pool, const void* 
   return PD_OK;
 }
 
-pd_status ensure_smem_attr(int variant, const void* fn, int smem_bytes) {
+pd_status ensure_smem_attr(int word, int variant, const void* fn, int smem_bytes) {
   const pd::CtxFns* f = pd::ctx_fns();
   const unsigned long long id = f ? pd::current_ctx_id(*f) : 0;
   const uint64_t bit = 1ull << variant;
@@ -118,7 +119,7 @@ pd_status ensure_smem_attr(int variant, const void* fn, int smem_bytes) {
   if (id != 0) {
     for (int i = 0; i < g_smem_contexts; ++i)
       if (g_smem_ready[i].ctx_id == id) e = &g_smem_ready[i];
-    if (e && (e->bits & bit)) return PD_OK;
+    if (e && (e->bits[word] & bit)) return PD_OK;
   }
   // the first launch of this instance in this context (or no context id to
   // key on: set it every time)
@@ -134,10 +135,10 @@ pd_status ensure_smem_attr(int variant, const void* fn, int smem_bytes) {
       if (g_smem_ready[i].ctx_id == now) e = &g_smem_ready[i];
     if (!e && g_smem_contexts < kMaxContexts) {
       e = &g_smem_ready[g_smem_contexts++];
-      *e = SmemReady{now, 0};
+      *e = SmemReady{now, {0, 0}};
     }
   }
-  if (e) e->bits |= bit;
+  if (e) e->bits[word] |= bit;
   return PD_OK;
 }
 
@@ -174,7 +175,7 @@ pd_status stage1(const pd_plan* plan, const void* q, const void* k_pool, const v
 
   const void* fn = pd::stage1_kernel_ptr(plan->variant);
   if (!fn) return PD_ERR_INVALID_ARG;
-  pd_status st = ensure_smem_attr(plan->variant, fn, plan->smem_bytes);
+  pd_status st = ensure_smem_attr(0, plan->variant, fn, plan->smem_bytes);
   if (st != PD_OK) return st;
 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -276,6 +277,26 @@ pd_status launch_own_part(const pd_plan* plan, const void* q, const void* k_pool
                           void* stream) {
   return stage1(plan, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens, 0, scale, workspace,
                 workspace_bytes, out, stream);
+}
+
+pd_status encode_row_map(CUtensorMap* map, const void* pool, const pd_layer_desc& ly, int rows) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return PD_ERR_CUDA;
+  const bool fp8 = ly.kv_dtype == PD_KV_FP8_E4M3;
+  const cuuint64_t elem = fp8 ? 1 : 2;
+  const cuuint64_t dims[2] = {(cuuint64_t)ly.head_dim, (cuuint64_t)ly.num_pages * ly.num_kv_heads * ly.page_size};
+  const cuuint64_t strides[1] = {(cuuint64_t)ly.head_dim * elem};
+  const cuuint32_t box[2] = {(cuuint32_t)(128 / elem), (cuuint32_t)rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                        const_cast<void*>(pool), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PD_OK : PD_ERR_CUDA;
+}
+
+pd_status ensure_prefix_smem(int variant, const void* fn, int smem_bytes) {
+  return ensure_smem_attr(1, variant, fn, smem_bytes);
 }
 
 }  // namespace pd

@@ -8,7 +8,6 @@
 // requests x query tokens x heads of a KV head's group), the own part by the
 // decode's stage 1, and one merge joins the pieces of both.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -23,107 +22,6 @@ namespace {
 
 constexpr uint32_t kSharedMagic = 0x50445348u;  // "PDSH"
 constexpr int32_t kSharedVersion = 1;
-
-// Row tile z of the launch: its group, first row and row count (0: none).
-struct Tile {
-  int group, first, rows, start;
-};
-
-__device__ __forceinline__ Tile find_tile(const SharedParams& p, int z) {
-  Tile t{-1, 0, 0, 0};
-  const int per_req = p.query_tokens * p.group;
-  int at = 0;
-  for (int g = 0; g < p.num_groups; ++g) {
-    const int s = max(0, min(p.group_starts[g], p.batch)), e = max(s, min(p.group_starts[g + 1], p.batch));
-    const int rows = (e - s) * per_req, n = (rows + p.row_tile - 1) / p.row_tile;
-    if (z < at + n) {
-      t.group = g;
-      t.first = (z - at) * p.row_tile;
-      t.rows = min(p.row_tile, rows - t.first);
-      t.start = s;
-      return t;
-    }
-    at += n;
-  }
-  return t;
-}
-
-// Whether the device's group starts cut the batch, in no more row tiles than planned.
-__device__ __forceinline__ bool groups_ok(const SharedParams& p) {
-  const int per_req = p.query_tokens * p.group;
-  long long tiles = 0;
-  if (p.group_starts[0] != 0 || p.group_starts[p.num_groups] != p.batch) return false;
-  for (int g = 0; g < p.num_groups; ++g) {
-    const int s = p.group_starts[g], e = p.group_starts[g + 1];
-    if (e < s || e > p.batch) return false;
-    tiles += ((long long)(e - s) * per_req + p.row_tile - 1) / p.row_tile;
-  }
-  return tiles <= p.tiles;
-}
-
-__device__ __forceinline__ float load_value(const uint8_t* pool, size_t i, bool fp8) {
-  if (fp8) return float(reinterpret_cast<const __nv_fp8_e4m3*>(pool)[i]);
-  return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(pool)[i]);
-}
-
-// The plain prefix pass: a warp per query row, the lanes across the head dims.
-__global__ void __launch_bounds__(256) prefix_plain_kernel(const SharedParams p) {
-  grid_dependency_wait();
-  grid_launch_dependents();
-  const int piece = blockIdx.x, g = blockIdx.y, lane = threadIdx.x & 31;
-  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0 && !groups_ok(p))
-    atomicOr(p.err, kErrBadGroup);
-  const Tile t = find_tile(p, blockIdx.z);
-  if (t.group < 0) return;
-  int L = p.prefix_lens[t.group];
-  const int cap = p.max_prefix_pages * p.page_size;
-  if (L < 0 || L > cap || L % p.page_size != 0) {
-    if (threadIdx.x == 0) atomicOr(p.err, kErrBadSeqLen);
-    L = max(0, min(L, cap)) / p.page_size * p.page_size;
-  }
-  const long long lo = (long long)piece * p.chunk_tokens;
-  const long long hi = piece == p.num_pieces - 1 ? L : min((long long)L, lo + p.chunk_tokens);
-  const bool fp8 = p.k_scale != nullptr;
-  const int n = p.head_dim / 32;
-  for (int r = threadIdx.x >> 5; r < t.rows; r += 8) {
-    const int i = t.first + r, per_req = p.query_tokens * p.group;
-    const size_t row = ((size_t)(t.start + i / per_req) * p.query_tokens + (i / p.group) % p.query_tokens) *
-                           p.num_q_heads + (size_t)g * p.group + i % p.group;
-    float q[16], o[16], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      o[k] = 0.f;
-      q[k] = k < n ? __uint_as_float((uint32_t)p.q[row * p.head_dim + k * 32 + lane] << 16) : 0.f;
-    }
-    for (long long tok = lo; tok < hi; ++tok) {
-      const int page = p.prefix_tables[(size_t)t.group * p.max_prefix_pages + tok / p.page_size];
-      if ((unsigned)page >= (unsigned)p.num_pages) {
-        if (lane == 0) atomicOr(p.err, kErrBadPage);
-        continue;
-      }
-      const size_t head = (size_t)page * p.num_kv_heads + g;
-      const size_t at = (head * p.page_size + tok % p.page_size) * p.head_dim;
-      float s = 0.f;
-#pragma unroll
-      for (int k = 0; k < 16; ++k)
-        if (k < n) s = fmaf(q[k], load_value(p.k_pool, at + k * 32 + lane, fp8), s);
-#pragma unroll
-      for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(kFullMask, s, d);
-      s *= p.scale_log2 * (fp8 ? p.k_scale[head] : 1.f);
-      const float mn = fmaxf(m, s), a = exp2f(m - mn), e = exp2f(s - mn), v = e * (fp8 ? p.v_scale[head] : 1.f);
-      l = l * a + e;
-      m = mn;
-#pragma unroll
-      for (int k = 0; k < 16; ++k)
-        if (k < n) o[k] = fmaf(v, load_value(p.v_pool, at + k * 32 + lane, fp8), o[k] * a);
-    }
-    const size_t part = row * p.num_pieces + piece;
-    if (lane == 0) p.lse_part[part] = l > 0.f || isnan(l) ? (m + log2f(l)) * 0.69314718055994530942f : -INFINITY;
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-      if (k < n) p.o_part[part * p.head_dim + k * 32 + lane] = l > 0.f || isnan(l) ? o[k] / l : 0.f;
-  }
-}
 
 struct JoinParams {
   const float* lse[2];  // own, prefix: [rows][pieces]
@@ -172,13 +70,25 @@ int row_tile_for(int head_dim, long long rows) {
   return n;
 }
 
+const PrefixInstance* find_prefix(int head_dim, int row_tile, bool fp8) {
+  for (int i = 0; i < kNumPrefixInstances; ++i) {
+    const PrefixInstance& v = kPrefixInstances[i];
+    if (v.head_dim == head_dim && v.row_tile == row_tile && v.fp8 == fp8) return &v;
+  }
+  return nullptr;
+}
+
 bool shared_plan_is_valid(const pd_shared_plan* plan) {
   if (!plan || plan->magic != kSharedMagic || plan->version != (uint32_t)kSharedVersion) return false;
   const pd_plan& own = plan->own;
   if (!plan_is_valid(&own) || own.partial != 2) return false;
   if (plan->num_groups < 0 || plan->max_prefix_pages < 1 || plan->tiles < 0 || plan->tiles > 65535) return false;
   if (own.batch > 0 && plan->num_groups < 1) return false;
-  if (plan->row_tile != 16 && plan->row_tile != 32 && plan->row_tile != 64 && plan->row_tile != 128) return false;
+  if (plan->variant < 0 || plan->variant >= kNumPrefixInstances) return false;
+  const PrefixInstance& v = kPrefixInstances[plan->variant];
+  if (v.head_dim != own.layer.head_dim || v.row_tile != plan->row_tile ||
+      v.fp8 != (own.layer.kv_dtype == PD_KV_FP8_E4M3))
+    return false;
   if (plan->num_pieces < 1 || plan->num_pieces > 1024) return false;
   if (plan->chunk_tokens < kPrefixTile || plan->chunk_tokens % kPrefixTile != 0) return false;
   if ((long long)plan->max_prefix_pages * own.layer.page_size > 0x7fffffffLL) return false;
@@ -224,6 +134,9 @@ pd_status plan_shared(const pd_layer_desc* layer, int32_t batch, int32_t query_t
   sp.max_prefix_pages = max_prefix_pages;
   sp.max_prefix_len = longest;
   sp.row_tile = row_tile_for(ly.head_dim, most_rows);
+  const PrefixInstance* v = find_prefix(ly.head_dim, sp.row_tile, ly.kv_dtype == PD_KV_FP8_E4M3);
+  if (!v) return PD_ERR_UNSUPPORTED;
+  sp.variant = v->id;
   long long tiles = 0;
   for (int n = 0; batch > 0 && n < num_groups; ++n)
     tiles += ((long long)(group_starts_host[n + 1] - group_starts_host[n]) * per_req + sp.row_tile - 1) / sp.row_tile;
@@ -246,18 +159,18 @@ pd_status plan_shared(const pd_layer_desc* layer, int32_t batch, int32_t query_t
   return PD_OK;
 }
 
-template <class... Params, class... Args>
-cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, void* stream, Args... args) {
+cudaError_t launch_dependent(const void* kernel, dim3 grid, int threads, int smem_bytes, void* stream, void** args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem_bytes;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, kernel, args);
   if (e != cudaSuccess) (void)cudaGetLastError();
   return e;
 }
@@ -289,8 +202,6 @@ pd_status decode_shared(const pd_shared_plan* plan, bool fp8, const void* q, con
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   SharedParams p = {};
   p.q = static_cast<const uint16_t*>(q);
-  p.k_pool = static_cast<const uint8_t*>(k_pool);
-  p.v_pool = static_cast<const uint8_t*>(ly.kv_shared ? k_pool : v_pool);
   p.k_scale = fp8 ? k_scale : nullptr;
   p.v_scale = fp8 ? (ly.kv_shared ? k_scale : v_scale) : nullptr;
   p.prefix_tables = prefix_tables;
@@ -314,11 +225,22 @@ pd_status decode_shared(const pd_shared_plan* plan, bool fp8, const void* q, con
   p.tiles = plan->tiles;
   p.num_pieces = plan->num_pieces;
   p.chunk_tokens = plan->chunk_tokens;
-  if (launch_dependent(prefix_plain_kernel, dim3(plan->num_pieces, ly.num_kv_heads, plan->tiles), 256, stream, p) !=
-      cudaSuccess)
+  p.box_rows = 16;
+  while (p.box_rows < kPrefixTile && ly.page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
+  p.keep_in_l2 = plan->tiles > 1 || ly.kv_shared;
+  p.stall_bytes = own.test_stall_bytes;
+  const PrefixInstance& v = kPrefixInstances[plan->variant];
+  const void* fn = prefix_kernel_ptr(plan->variant);
+  pd_status st = ensure_prefix_smem(plan->variant, fn, v.smem_bytes);
+  if (st == PD_OK) st = encode_row_map(&p.kmap, k_pool, ly, p.box_rows);
+  if (st == PD_OK) st = encode_row_map(&p.vmap, ly.kv_shared ? k_pool : v_pool, ly, p.box_rows);
+  if (st != PD_OK) return st;
+  void* args[] = {&p};
+  if (plan->tiles > 0 && launch_dependent(fn, dim3(plan->tiles, plan->num_pieces, ly.num_kv_heads), v.threads,
+                                          v.smem_bytes, stream, args) != cudaSuccess)
     return PD_ERR_CUDA;
-  const pd_status st = launch_own_part(&own, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens, scale,
-                                       workspace, workspace_bytes, out, stream);
+  st = launch_own_part(&own, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens, scale, workspace,
+                       workspace_bytes, out, stream);
   if (st != PD_OK) return st;
   JoinParams j = {};
   j.lse[0] = reinterpret_cast<const float*>(ws + own.lse_offset);
@@ -330,7 +252,9 @@ pd_status decode_shared(const pd_shared_plan* plan, bool fp8, const void* q, con
   j.out = static_cast<uint16_t*>(out);
   j.head_dim = ly.head_dim;
   const unsigned rows = (unsigned)own.batch * own.query_tokens * ly.num_q_heads;
-  if (launch_dependent(join_kernel, dim3(rows), 128, stream, j) != cudaSuccess) return PD_ERR_CUDA;
+  void* jargs[] = {&j};
+  if (launch_dependent(reinterpret_cast<const void*>(&join_kernel), dim3(rows), 128, 0, stream, jargs) != cudaSuccess)
+    return PD_ERR_CUDA;
   return PD_OK;
 }
 

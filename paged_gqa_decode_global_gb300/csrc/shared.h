@@ -11,9 +11,8 @@ namespace pd {
 constexpr int kPrefixTile = 128;  // prefix tokens of one tile of the prefix pass
 
 struct SharedParams {
+  CUtensorMap kmap, vmap;  // the pools as {D, rows}, boxes {128 bytes, box_rows}, 128-byte swizzle
   const uint16_t* q;
-  const uint8_t* k_pool;
-  const uint8_t* v_pool;
   const float* k_scale;  // FP8
   const float* v_scale;
   const int32_t* prefix_tables;
@@ -26,7 +25,20 @@ struct SharedParams {
   int32_t batch, num_groups, query_tokens, num_q_heads, num_kv_heads, group, head_dim;
   int32_t page_size, num_pages, max_prefix_pages;
   int32_t row_tile, tiles, num_pieces, chunk_tokens;
+  int32_t box_rows;     // tokens of one copy: the largest of 16, 32, 64, 128 that divides page_size
+  int32_t keep_in_l2;   // the prefix rows are read more than once (several row tiles, K=V)
+  int32_t stall_bytes;  // tests only: bytes expected per stage beyond what the copies deliver
 };
+
+// The prefix pass's kernel instances: head_dim, query rows a CTA serves, cache type.
+struct PrefixInstance {
+  int id, head_dim, row_tile;
+  bool fp8;
+  int threads, smem_bytes;
+};
+extern const PrefixInstance kPrefixInstances[];
+extern const int kNumPrefixInstances;
+const void* prefix_kernel_ptr(int variant);
 
 // plan.cu
 bool plan_is_valid(const pd_plan* plan);
@@ -37,5 +49,8 @@ pd_status launch_own_part(const pd_plan* plan, const void* q, const void* k_pool
                           const float* k_scale, const float* v_scale, const int32_t* block_tables,
                           const int32_t* seq_lens, float scale, void* workspace, size_t workspace_bytes, void* out,
                           void* stream);
+// abi.cu: a pool's tensor map with boxes of `rows` rows; the shared-memory limit of a prefix instance
+pd_status encode_row_map(CUtensorMap* map, const void* pool, const pd_layer_desc& ly, int rows);
+pd_status ensure_prefix_smem(int variant, const void* fn, int smem_bytes);
 
 }  // namespace pd
