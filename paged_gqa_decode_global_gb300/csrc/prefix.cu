@@ -56,7 +56,8 @@ struct PrefixCfg {
   static constexpr int Q_OFFSET = 0, P_OFFSET = Q_BYTES, RING_OFFSET = P_OFFSET + P_BYTES;
   static constexpr int RAW_OFFSET = RING_OFFSET + NST * kStage;
   static constexpr int REF_OFFSET = RAW_OFFSET + NRAW * kRaw;   // float ref[N]
-  static constexpr int BAR_OFFSET = REF_OFFSET + N * 4;
+  static constexpr int ROW_OFFSET = REF_OFFSET + N * 4;         // int row[N]: a tile row's row of q and out
+  static constexpr int BAR_OFFSET = ROW_OFFSET + N * 4;
   static constexpr int NBAR = 2 * NST + 2 * NRAW + 2 + 2 + 1 + 1 + 1 + 1;
   static constexpr int TMEM_OFFSET = BAR_OFFSET + NBAR * 8;
   static constexpr int SMEM_BYTES = TMEM_OFFSET + 16 + 1024;
@@ -125,10 +126,10 @@ __device__ __forceinline__ bool groups_ok(const SharedParams& p) {
 }
 
 // Row r of a tile: its row of q and out, [batch, T, Hq].
-__device__ __forceinline__ size_t row_of(const SharedParams& p, const Tile& t, int r, int g) {
+__device__ __forceinline__ int row_of(const SharedParams& p, const Tile& t, int r, int g) {
   const int i = t.first + r, per_req = p.query_tokens * p.group;
-  return ((size_t)(t.start + i / per_req) * p.query_tokens + (i / p.group) % p.query_tokens) * p.num_q_heads +
-         (size_t)g * p.group + i % p.group;
+  return ((t.start + i / per_req) * p.query_tokens + (i / p.group) % p.query_tokens) * p.num_q_heads + g * p.group +
+         i % p.group;
 }
 
 // Floats as signed integers of the same order, for an integer warp maximum.
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
   if (ntile == 0) {
     // nothing here: weight 0 (the join reads no row of such a piece)
     for (int r = tid; r < t.rows; r += C::THREADS)
-      p.lse_part[row_of(p, t, r, g) * p.num_pieces + piece] = -INFINITY;
+      p.lse_part[(size_t)row_of(p, t, r, g) * p.num_pieces + piece] = -INFINITY;
   } else if (warp == 5) {
     // ---- copies: stages in the order the products use them, K(0), K(1), V(0), K(2), V(1), ...
     const int box = p.box_rows, nbox = kTok / box;
@@ -291,67 +292,112 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     err = __reduce_or_sync(kFullMask, err);
     if (lane == 0 && err) atomicOr(p.err, err);
   } else if (warp == 4) {
-    // ---- matrix instructions: QK(0), then QK(i + 1) ahead of PV(i)
-    if (lane == 0) {
-      constexpr uint32_t kQk = mma_desc_bf16(128, N, false), kPv = mma_desc_bf16(128, N, true);
-      const uint32_t ring = smem_u32(smem + C::RING_OFFSET), qs = smem_u32(smem + C::Q_OFFSET);
-      const uint32_t ps = smem_u32(smem + C::P_OFFSET);
-      int it = 0;
-      bool ok = mbar_wait(q_full, 0);
-      auto qk = [&](int i) {
-        if (ok && i >= 2) ok = mbar_wait(&s_empty[i & 1], ((i >> 1) - 1) & 1);
-        for (int s = 0; s < KS && ok; ++s, ++it) {
-          const int st = it % NST;
-          ok = mbar_wait(&full[st], (it / NST) & 1);
-          if (!ok) return;
-          tmem_fence_after();
+    // ---- matrix instructions: QK(0), then QK(i + 1) ahead of PV(i). The warp
+    // walks the stages together and one elected lane issues: a lone thread
+    // computing descriptors took ~180 cycles an instruction.
+    constexpr uint32_t kQk = mma_desc_bf16(128, N, false), kPv = mma_desc_bf16(128, N, true);
+    // descriptors' bases; a step further is a constant added to the address field
+    const uint32_t base = smem_u32(smem);
+    const uint64_t k_desc = smem_desc(base + C::RING_OFFSET, 16, 1024), q_desc = smem_desc(base, 16, 1024);
+    const uint64_t v_desc = smem_desc(base + C::RING_OFFSET, kSlab, 1024);
+    const uint64_t p_desc = smem_desc(base + C::P_OFFSET, 16, 1024);
+    int st = 0;
+    uint32_t phase = 0;
+    bool ok = __all_sync(kFullMask, mbar_wait(q_full, 0));
+    auto next_stage = [&] {
+      if (++st == NST) {
+        st = 0;
+        phase ^= 1;
+      }
+    };
+    auto qk = [&](int i) {
+      if (ok && i >= 2) ok = __all_sync(kFullMask, mbar_wait(&s_empty[i & 1], ((i >> 1) - 1) & 1));
+      const uint32_t d = tmem + C::O_COLS + (i & 1) * N;
+#pragma unroll 1
+      for (int s = 0; s < KS && ok; ++s) {
+        ok = __all_sync(kFullMask, mbar_wait(&full[st], phase));
+        if (!ok) return;
+        tmem_fence_after();
+        if (elect_one()) {
+          const uint64_t a = k_desc + st * (kStage >> 4), b = q_desc + s * 2 * (N * 128 >> 4);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            mma_ss(tmem + C::O_COLS + (i & 1) * N,
-                   smem_desc(ring + st * kStage + (k >> 2) * kSlab + (k & 3) * 32, 16, 1024),
-                   smem_desc(qs + (s * 2 + (k >> 2)) * N * 128 + (k & 3) * 32, 16, 1024), kQk, (s | k) != 0);
+            mma_ss(d, a + (k >> 2) * (kSlab >> 4) + (k & 3) * 2, b + (k >> 2) * (N * 128 >> 4) + (k & 3) * 2, kQk,
+                   k != 0 || s != 0);
           mma_commit(&empty[st]);
+          if (s == KS - 1) mma_commit(&s_full[i & 1]);
         }
-        if (ok) mma_commit(&s_full[i & 1]);
-      };
-      qk(0);
-      for (int i = 0; i < ntile && ok; ++i) {
-        if (i + 1 < ntile) qk(i + 1);
-        if (ok) ok = mbar_wait(p_full, i & 1);
-        const int steps = (min(kTok, hi - lo - i * kTok)) / 16;
-        for (int s = 0; s < KS && ok; ++s, ++it) {
-          const int st = it % NST;
-          ok = mbar_wait(&full[st], (it / NST) & 1);
-          if (!ok) break;
-          tmem_fence_after();
-          for (int k = 0; k < steps; ++k)
-            mma_ss(tmem + s * N, smem_desc(ring + st * kStage + k * 2048, kSlab, 1024),
-                   smem_desc(ps + (k >> 2) * N * 128 + (k & 3) * 32, 16, 1024), kPv, (i | k) != 0);
-          mma_commit(&empty[st]);
-        }
-        if (ok) mma_commit(p_empty);
+        __syncwarp();
+        next_stage();
       }
-      if (!ok) {
-        // nothing may still be reading shared memory when the CTA exits
+    };
+    qk(0);
+#pragma unroll 1
+    for (int i = 0; i < ntile && ok; ++i) {
+      if (i + 1 < ntile) qk(i + 1);
+      if (ok) ok = __all_sync(kFullMask, mbar_wait(p_full, i & 1));
+      const int steps = (min(kTok, hi - lo - i * kTok)) / 16;
+#pragma unroll 1
+      for (int s = 0; s < KS && ok; ++s) {
+        ok = __all_sync(kFullMask, mbar_wait(&full[st], phase));
+        if (!ok) break;
+        tmem_fence_after();
+        if (elect_one()) {
+          const uint64_t a = v_desc + st * (kStage >> 4);
+          const uint32_t d = tmem + s * N;
+          if (steps == 8) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_ss(d, a + k * (2048 >> 4), p_desc + (k >> 2) * (N * 128 >> 4) + (k & 3) * 2, kPv, k != 0 || i != 0);
+          } else {
+#pragma unroll 1
+            for (int k = 0; k < steps; ++k)
+              mma_ss(d, a + k * (2048 >> 4), p_desc + (k >> 2) * (N * 128 >> 4) + (k & 3) * 2, kPv, k != 0 || i != 0);
+          }
+          mma_commit(&empty[st]);
+          if (s == KS - 1) mma_commit(p_empty);
+        }
+        __syncwarp();
+        next_stage();
+      }
+    }
+    if (!ok) {
+      // nothing may still be reading shared memory when the CTA exits
+      if (elect_one()) {
         mma_commit(drained);
         mbar_wait(drained, 0);
         atomicOr(p.err, kErrTimeout);
       }
+      __syncwarp();
     }
-    __syncwarp();
   } else if (warp < 4) {
     // ---- softmax: a thread per token lane
     float* ref = reinterpret_cast<float*>(smem + C::REF_OFFSET);
     float* swap = reinterpret_cast<float*>(smem + C::P_OFFSET);  // [4][N] warp maxima, then [N] factors
-    // the tile's query rows, swizzled as the K-major operand
-    for (int e = tid; e < N * (D / 8); e += 128) {
-      const int r = e / (D / 8), c = e % (D / 8);
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (r < t.rows) v = __ldg(reinterpret_cast<const uint4*>(p.q + row_of(p, t, r, g) * D) + c);
-      *reinterpret_cast<uint4*>(smem + C::Q_OFFSET + (c >> 3) * N * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+    int* rows = reinterpret_cast<int*>(smem + C::ROW_OFFSET);
+    if (tid < N) {
+      ref[tid] = -INFINITY;
+      rows[tid] = tid < t.rows ? row_of(p, t, tid, g) : -1;
     }
-    if (tid < N) ref[tid] = -INFINITY;
-    __syncwarp();
+    named_bar_sync(1, 128);
+    // the tile's query rows, swizzled as the K-major operand; all of a round's loads in flight at once
+    constexpr int kChunks = N * (D / 8), kRound = kChunks / 128 < 16 ? kChunks / 128 : 16;
+#pragma unroll 1
+    for (int e0 = tid; e0 < kChunks; e0 += 128 * kRound) {
+      uint4 v[kRound];
+#pragma unroll
+      for (int u = 0; u < kRound; ++u) {
+        const int e = e0 + u * 128, r = rows[e / (D / 8)];
+        v[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (r >= 0) v[u] = __ldg(reinterpret_cast<const uint4*>(p.q + (size_t)r * D) + e % (D / 8));
+      }
+#pragma unroll
+      for (int u = 0; u < kRound; ++u) {
+        const int e = e0 + u * 128, r = e / (D / 8), c = e % (D / 8);
+        *reinterpret_cast<uint4*>(smem + C::Q_OFFSET + (c >> 3) * N * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+            v[u];
+      }
+    }
     fence_proxy_async_smem();
     mbar_arrive(q_full);
     named_bar_sync(1, 128);
@@ -500,7 +546,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
         // no attended token: weight 0 and a zero row; NaN stays NaN
         inv[tid] = total == 0.f ? 0.f : 1.f / total;
         if (tid < t.rows)
-          p.lse_part[row_of(p, t, tid, g) * p.num_pieces + piece] =
+          p.lse_part[(size_t)rows[tid] * p.num_pieces + piece] =
               total == 0.f ? -INFINITY : ((ref[tid] == -INFINITY ? 0.f : ref[tid]) + log2f(total)) * 0.69314718055994530942f;
       }
       __syncwarp();
@@ -508,16 +554,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
 #pragma unroll 1
       for (int c0 = 0; c0 < N; c0 += 16) {
         if (c0 >= t.rows) break;
-#pragma unroll 1
-        for (int s = 0; s < KS; ++s) {
-          uint32_t x[16];
-          tmem_ld16(x, lanes + s * N + c0);
-          tmem_wait_ld();
+        uint32_t x[KS][16];
 #pragma unroll
-          for (int c = 0; c < 16; ++c)
-            if (c0 + c < t.rows)
-              p.o_part[(row_of(p, t, c0 + c, g) * p.num_pieces + piece) * D + s * 128 + tid] =
-                  __uint_as_float(x[c]) * inv[c0 + c];
+        for (int s = 0; s < KS; ++s) tmem_ld16(x[s], lanes + s * N + c0);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          if (c0 + c >= t.rows) break;
+          float* dst = p.o_part + ((size_t)rows[c0 + c] * p.num_pieces + piece) * D + tid;
+          const float f = inv[c0 + c];
+#pragma unroll
+          for (int s = 0; s < KS; ++s) dst[s * 128] = __uint_as_float(x[s][c]) * f;
         }
       }
     }

@@ -28,35 +28,104 @@ struct JoinParams {
   const float* o[2];
   int pieces[2];
   uint16_t* out;
-  int head_dim;
 };
 
-// One CTA per row: out = sum over both parts' pieces of w_s o_s.
-__global__ void __launch_bounds__(128) join_kernel(const JoinParams p) {
+constexpr int kJoinThreads = 128;
+constexpr int kJoinMaxPieces = 2048;  // both parts' caps
+constexpr int kJoinAhead = 8;         // pieces whose rows a thread has in flight
+
+// One CTA per row. The weights first (a thread per piece), then float4 column
+// `tid % (D / 4)` over the pieces tid / (D / 4), + 512 / D, ...; the piece
+// groups of a column are summed in shared memory. The first kJoinAhead rows of
+// each thread load together with the log-sum-exps.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p) {
+  constexpr int COLS = D / 4, GROUPS = kJoinThreads / COLS;
+  __shared__ float wt[kJoinMaxPieces], red[2][4];
+  __shared__ float4 part[GROUPS > 1 ? kJoinThreads : 1];
   grid_dependency_wait();
   grid_launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, col = tid % COLS, grp = tid / COLS;
   const size_t row = blockIdx.x;
-  float M = -INFINITY;
-  for (int part = 0; part < 2; ++part)
-    for (int s = 0; s < p.pieces[part]; ++s) {
-      const float l = p.lse[part][row * p.pieces[part] + s];
-      M = (l > M || isnan(l)) ? l : M;
-    }
-  for (int d = threadIdx.x; d < p.head_dim; d += 128) {
-    float acc = 0.f, sum = 0.f;
-    if (M != -INFINITY)
-      for (int part = 0; part < 2; ++part)
-        for (int s = 0; s < p.pieces[part]; ++s) {
-          const size_t at = row * p.pieces[part] + s;
-          const float l = p.lse[part][at];
-          if (l == -INFINITY) continue;
-          const float w = expf(l - M);
-          sum += w;
-          acc = fmaf(w, p.o[part][at * p.head_dim + d], acc);
-        }
-    const __nv_bfloat16 v = __float2bfloat16_rn(M != -INFINITY ? acc / sum : 0.f);
-    p.out[row * p.head_dim + d] = *reinterpret_cast<const uint16_t*>(&v);
+  const int s0 = p.pieces[0], total = s0 + p.pieces[1];
+  auto rows = [&](int s) {
+    return reinterpret_cast<const float4*>(s < s0 ? p.o[0] + (row * s0 + s) * D
+                                                  : p.o[1] + (row * p.pieces[1] + (s - s0)) * D) + col;
+  };
+  float4 ahead[kJoinAhead];
+#pragma unroll
+  for (int i = 0; i < kJoinAhead; ++i) {
+    const int s = grp + i * GROUPS;
+    ahead[i] = s < total ? __ldg(rows(s)) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
+  // NaN log-sum-exps stay NaN all the way
+  float M = -INFINITY;
+  for (int s = tid; s < total; s += kJoinThreads) {
+    const float l = s < s0 ? p.lse[0][row * s0 + s] : p.lse[1][row * p.pieces[1] + (s - s0)];
+    wt[s] = l;
+    M = (l > M || isnan(l)) ? l : M;
+  }
+#pragma unroll
+  for (int m = 16; m; m >>= 1) {
+    const float o = __shfl_xor_sync(kFullMask, M, m);
+    M = (o > M || isnan(o)) ? o : M;
+  }
+  if (lane == 0) red[0][warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 4; ++w) M = (red[0][w] > M || isnan(red[0][w])) ? red[0][w] : M;
+  float sum = 0.f;
+  for (int s = tid; s < total; s += kJoinThreads) {
+    // an empty piece weighs 0 (its row may never have been written)
+    const float w = wt[s] == -INFINITY ? 0.f : exp2f((wt[s] - M) * 1.4426950408889634f);
+    wt[s] = w;
+    sum += w;
+  }
+#pragma unroll
+  for (int m = 16; m; m >>= 1) sum += __shfl_xor_sync(kFullMask, sum, m);
+  if (lane == 0) red[1][warp] = sum;
+  __syncthreads();
+  sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](int s, const float4& v) {
+    const float w = wt[s];
+    if (w == 0.f) return;  // selected out, not multiplied
+    acc.x = fmaf(w, v.x, acc.x);
+    acc.y = fmaf(w, v.y, acc.y);
+    acc.z = fmaf(w, v.z, acc.z);
+    acc.w = fmaf(w, v.w, acc.w);
+  };
+#pragma unroll
+  for (int i = 0; i < kJoinAhead; ++i)
+    if (grp + i * GROUPS < total) add(grp + i * GROUPS, ahead[i]);
+  for (int base = grp + kJoinAhead * GROUPS; base < total; base += kJoinAhead * GROUPS) {
+#pragma unroll
+    for (int i = 0; i < kJoinAhead; ++i) {
+      const int s = base + i * GROUPS;
+      if (s < total) ahead[i] = __ldg(rows(s));
+    }
+#pragma unroll
+    for (int i = 0; i < kJoinAhead; ++i)
+      if (base + i * GROUPS < total) add(base + i * GROUPS, ahead[i]);
+  }
+  if constexpr (GROUPS > 1) {
+    part[tid] = acc;
+    __syncthreads();
+    if (grp != 0) return;
+#pragma unroll
+    for (int k = 1; k < GROUPS; ++k) {
+      const float4 v = part[k * COLS + col];
+      acc.x += v.x;
+      acc.y += v.y;
+      acc.z += v.z;
+      acc.w += v.w;
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no piece at all: a zero row
+  const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+  const __nv_bfloat162 b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  reinterpret_cast<uint2*>(p.out + row * D)[col] =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
 uint64_t align_up(uint64_t x, uint64_t a) { return (x + a - 1) / a * a; }
@@ -250,11 +319,12 @@ pd_status decode_shared(const pd_shared_plan* plan, bool fp8, const void* q, con
   j.o[1] = p.o_part;
   j.pieces[1] = plan->num_pieces;
   j.out = static_cast<uint16_t*>(out);
-  j.head_dim = ly.head_dim;
   const unsigned rows = (unsigned)own.batch * own.query_tokens * ly.num_q_heads;
   void* jargs[] = {&j};
-  if (launch_dependent(reinterpret_cast<const void*>(&join_kernel), dim3(rows), 128, 0, stream, jargs) != cudaSuccess)
-    return PD_ERR_CUDA;
+  const void* join = ly.head_dim == 512   ? reinterpret_cast<const void*>(&join_kernel<512>)
+                     : ly.head_dim == 256 ? reinterpret_cast<const void*>(&join_kernel<256>)
+                                          : reinterpret_cast<const void*>(&join_kernel<128>);
+  if (launch_dependent(join, dim3(rows), kJoinThreads, 0, stream, jargs) != cudaSuccess) return PD_ERR_CUDA;
   return PD_OK;
 }
 

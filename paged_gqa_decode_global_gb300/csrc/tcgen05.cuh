@@ -18,6 +18,18 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
          (uint64_t)((sbo >> 4) & 0x3fff) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
+// One lane of the (converged) warp; the matrix instructions and commits of a
+// warp go out under it, so that their operands stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      :
+      : "memory");
+  return r != 0;
+}
+
 // Instruction descriptor: bf16 x bf16 -> fp32, M x N; a_mn: A is MN-major (B is K-major).
 __host__ __device__ constexpr uint32_t mma_desc_bf16(int m, int n, bool a_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((uint32_t)(n >> 3) << 17) |
