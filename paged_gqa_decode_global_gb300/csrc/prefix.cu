@@ -17,15 +17,21 @@
 // rescale of O^T, a round trip through registers, becomes rare. Each row's
 // references depend on its own scores only.
 //
-// Roles: warps 0-3 softmax and epilogue (a thread per token lane), warp 4 the
-// matrix instructions (one lane), warp 5 the copies; FP8: warps 6-9 widen the
-// e4m3 stages to bf16 operands. K and V arrive as [64-dim slab][128 tokens][128
-// B] with the 128-byte swizzle: K-major for the first product, and the same
-// layout read M-major for the second, so nothing is transposed. A K=V layer
-// fetches the tile again for its second use (an L2 hit).
+// Roles: warps 0-7 softmax and epilogue (a thread per token lane, two
+// warpgroups with half the rows each: with one, its ~1700 instructions a tile
+// at one warp per scheduler took 5 us against 1.9 us of products), warp 8 the
+// matrix instructions, warp 9 the copies; FP8: warps 10-13 widen the e4m3
+// stages to f16 operands. K and V arrive as [64-dim slab][128 tokens][128 B]
+// with the 128-byte swizzle: K-major for the first product, and the same layout
+// read M-major for the second, so nothing is transposed; P is written N-major,
+// a token's row at a time. A K=V layer fetches the tile again for its second
+// use (an L2 hit).
 //
-// P is rounded to bf16 (the tensor core's operand): relative error 2^-9 a
-// probability; sums, references and accumulators stay in fp32.
+// Roundings: P to the operands' type. bf16 cache: bf16, 2^-9 a probability. FP8
+// cache: f16, into which e4m3 widens exactly; q rounds to f16 once (as in the
+// decode), and P carries the page's V scale over the piece's largest, so that it
+// stays below 2^8: 2^-12 a probability, 2^-25 absolute below 2^-14. Sums,
+// references and accumulators stay in fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -43,6 +49,8 @@ constexpr int kStage = 2 * kSlab;          // an operand stage: 128 dims
 constexpr int kRaw = kTok * 128;           // FP8: 128 dims of 128 tokens, e4m3
 constexpr int kBody = 224 * 1024;          // query rows, probabilities and rings
 constexpr float kSlack = 8.f;              // log2 of what a probability may exceed 1 by
+constexpr float kLow = 3e38f;              // negated reference of a row without a score yet
+constexpr int kNoTop = (int)0x807fffff;    // ordered(-inf)
 
 template <int D_, int N_, bool FP8_>
 struct PrefixCfg {
@@ -55,21 +63,25 @@ struct PrefixCfg {
   static constexpr int NRAW = FP8 ? ((ROOM - NST * kStage) / kRaw < 6 ? (ROOM - NST * kStage) / kRaw : 6) : 0;
   static constexpr int Q_OFFSET = 0, P_OFFSET = Q_BYTES, RING_OFFSET = P_OFFSET + P_BYTES;
   static constexpr int RAW_OFFSET = RING_OFFSET + NST * kStage;
-  static constexpr int REF_OFFSET = RAW_OFFSET + NRAW * kRaw;   // float ref[N]
-  static constexpr int ROW_OFFSET = REF_OFFSET + N * 4;         // int row[N]: a tile row's row of q and out
+  static constexpr int REF_OFFSET = RAW_OFFSET + NRAW * kRaw;   // float nref[N]: negated references
+  static constexpr int TOP_OFFSET = REF_OFFSET + N * 4;         // int top[N]: a tile's true maxima
+  static constexpr int ROW_OFFSET = TOP_OFFSET + N * 4;         // int row[N]: a tile row's row of q and out
   static constexpr int BAR_OFFSET = ROW_OFFSET + N * 4;
   static constexpr int NBAR = 2 * NST + 2 * NRAW + 2 + 2 + 1 + 1 + 1 + 1;
   static constexpr int TMEM_OFFSET = BAR_OFFSET + NBAR * 8;
   static constexpr int SMEM_BYTES = TMEM_OFFSET + 16 + 1024;
-  static constexpr int THREADS = FP8 ? 320 : 192;
+  static constexpr int THREADS = FP8 ? 448 : 320;
+  static constexpr int CW = N / 2;         // rows of a softmax warpgroup
+  static constexpr int LD = CW < 32 ? CW : 32;
+  // P: [N / 64 blocks][128 tokens][row of up to 64 query rows], swizzled over the row
+  static constexpr int P_ROW = N >= 64 ? 128 : N * 2;
   static constexpr int O_COLS = KS * N;
   static constexpr int TMEM_COLS = O_COLS + 2 * N <= 64 ? 64 : O_COLS + 2 * N <= 128 ? 128 :
                                    O_COLS + 2 * N <= 256 ? 256 : 512;
   static_assert(O_COLS + 2 * N <= 512, "tensor memory");
   static_assert(NST >= 3 && (!FP8 || NRAW >= 2), "rings");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
-  static_assert(kTok * (N + 1) * 4 <= NST * kStage, "the row sums are reduced in the ring");
-  static_assert(5 * N * 4 <= P_BYTES, "the references are exchanged in P's buffer");
+  static_assert(2 * (kTok * (CW + 1) + 128) * 4 <= NST * kStage, "the row sums are reduced in the ring");
 };
 
 struct Tile {
@@ -139,22 +151,28 @@ __device__ __forceinline__ int ordered(float x) {
 }
 __device__ __forceinline__ float unordered(int k) { return __int_as_float(k >= 0 ? k : k ^ 0x7fffffff); }
 
-// Four e4m3 codes -> four bf16, exactly. A code's exponent and mantissa bits put
-// at bits 4..10 of a bf16 read as the value over 2^120 (subnormal codes as bf16
-// subnormals), so one exact multiplication finishes; the NaN codes (0x7f, 0xff)
-// would read as 480 and are left to the caller.
+// Four e4m3 codes -> four f16, exactly (NaN included).
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t x = __byte_perm(w, 0u, 0x1404), y = __byte_perm(w, 0u, 0x3424);
-  const uint32_t a = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u), b = ((y >> 4) & 0x07f007f0u) | (y & 0x80008000u);
-  const uint32_t k = 0x7b807b80u;  // 2^120
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(k));
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(k));
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
-__device__ __forceinline__ bool has_nan4(uint32_t w) { return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0; }
-__device__ __forceinline__ uint32_t nan_fix(uint32_t v, uint32_t codes) {
-  if ((codes & 0x7fu) == 0x7fu) v |= 0x7fffu;
-  if ((codes & 0x7f00u) == 0x7f00u) v |= 0x7fff0000u;
-  return v;
+
+// Two fp32 as the operand type, the first in the low half.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if constexpr (F16)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Two bf16 -> two f16.
+__device__ __forceinline__ uint32_t to_f16x2(uint32_t w) {
+  return pack2<true>(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
 template <class C>
@@ -175,7 +193,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::TMEM_OFFSET);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
 
-  if (tid == 160) {
+  if (tid == 288) {
     prefetch_tensormap(&p.kmap);
     prefetch_tensormap(&p.vmap);
     for (int i = 0; i < NST; ++i) {
@@ -188,15 +206,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 128);
+      mbar_init(&s_empty[i], 256);
     }
-    mbar_init(p_full, 128);
+    mbar_init(p_full, 256);
     mbar_init(p_empty, 1);
-    mbar_init(q_full, 128);
+    mbar_init(q_full, 256);
     mbar_init(drained, 1);
     fence_barrier_init();
   }
-  if (warp == 4) tmem_alloc(tmem_at, C::TMEM_COLS);
+  if (warp == 8) tmem_alloc(tmem_at, C::TMEM_COLS);
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
@@ -228,7 +246,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     // nothing here: weight 0 (the join reads no row of such a piece)
     for (int r = tid; r < t.rows; r += C::THREADS)
       p.lse_part[(size_t)row_of(p, t, r, g) * p.num_pieces + piece] = -INFINITY;
-  } else if (warp == 5) {
+  } else if (warp == 9) {
     // ---- copies: stages in the order the products use them, K(0), K(1), V(0), K(2), V(1), ...
     const int box = p.box_rows, nbox = kTok / box;
     const uint64_t policy = p.keep_in_l2 ? 0 : l2_evict_first_policy();
@@ -291,16 +309,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     }
     err = __reduce_or_sync(kFullMask, err);
     if (lane == 0 && err) atomicOr(p.err, err);
-  } else if (warp == 4) {
+  } else if (warp == 8) {
     // ---- matrix instructions: QK(0), then QK(i + 1) ahead of PV(i). The warp
     // walks the stages together and one elected lane issues: a lone thread
     // computing descriptors took ~180 cycles an instruction.
-    constexpr uint32_t kQk = mma_desc_bf16(128, N, false), kPv = mma_desc_bf16(128, N, true);
+    constexpr uint32_t kQk = mma_desc_16bit(!C::FP8, 128, N, false, false);
+    constexpr uint32_t kPv = mma_desc_16bit(!C::FP8, 128, N, true, true);
     // descriptors' bases; a step further is a constant added to the address field
     const uint32_t base = smem_u32(smem);
     const uint64_t k_desc = smem_desc(base + C::RING_OFFSET, 16, 1024), q_desc = smem_desc(base, 16, 1024);
     const uint64_t v_desc = smem_desc(base + C::RING_OFFSET, kSlab, 1024);
-    const uint64_t p_desc = smem_desc(base + C::P_OFFSET, 16, 1024);
+    const uint64_t p_desc = smem_desc(base + C::P_OFFSET, kSlab, 8 * C::P_ROW, C::P_ROW);
     int st = 0;
     uint32_t phase = 0;
     bool ok = __all_sync(kFullMask, mbar_wait(q_full, 0));
@@ -348,11 +367,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
           if (steps == 8) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              mma_ss(d, a + k * (2048 >> 4), p_desc + (k >> 2) * (N * 128 >> 4) + (k & 3) * 2, kPv, k != 0 || i != 0);
+              mma_ss(d, a + k * (2048 >> 4), p_desc + k * (16 * C::P_ROW >> 4), kPv, k != 0 || i != 0);
           } else {
 #pragma unroll 1
             for (int k = 0; k < steps; ++k)
-              mma_ss(d, a + k * (2048 >> 4), p_desc + (k >> 2) * (N * 128 >> 4) + (k & 3) * 2, kPv, k != 0 || i != 0);
+              mma_ss(d, a + k * (2048 >> 4), p_desc + k * (16 * C::P_ROW >> 4), kPv, k != 0 || i != 0);
           }
           mma_commit(&empty[st]);
           if (s == KS - 1) mma_commit(p_empty);
@@ -370,47 +389,72 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       }
       __syncwarp();
     }
-  } else if (warp < 4) {
-    // ---- softmax: a thread per token lane
-    float* ref = reinterpret_cast<float*>(smem + C::REF_OFFSET);
-    float* swap = reinterpret_cast<float*>(smem + C::P_OFFSET);  // [4][N] warp maxima, then [N] factors
+  } else if (warp < 8) {
+    // ---- softmax: a thread per token lane, warpgroup wg the rows [wg CW, wg CW + CW)
+    constexpr int CW = C::CW, LD = C::LD;
+    const int wg = warp >> 2, lt = tid & 127, bar = 1 + wg;
+    float* nref = reinterpret_cast<float*>(smem + C::REF_OFFSET) + wg * CW;
+    int* top = reinterpret_cast<int*>(smem + C::TOP_OFFSET) + wg * CW;
     int* rows = reinterpret_cast<int*>(smem + C::ROW_OFFSET);
-    if (tid < N) {
-      ref[tid] = -INFINITY;
-      rows[tid] = tid < t.rows ? row_of(p, t, tid, g) : -1;
+    if (tid < N) rows[tid] = tid < t.rows ? row_of(p, t, tid, g) : -1;
+    if (lt < CW) {
+      nref[lt] = kLow;
+      top[lt] = kNoTop;
     }
-    named_bar_sync(1, 128);
+    __syncwarp();
+    named_bar_sync(3, 256);
     // the tile's query rows, swizzled as the K-major operand; all of a round's loads in flight at once
-    constexpr int kChunks = N * (D / 8), kRound = kChunks / 128 < 16 ? kChunks / 128 : 16;
+    constexpr int kChunks = N * (D / 8), kRound = kChunks / 256 < 16 ? kChunks / 256 : 16;
 #pragma unroll 1
-    for (int e0 = tid; e0 < kChunks; e0 += 128 * kRound) {
+    for (int e0 = tid; e0 < kChunks; e0 += 256 * kRound) {
       uint4 v[kRound];
 #pragma unroll
       for (int u = 0; u < kRound; ++u) {
-        const int e = e0 + u * 128, r = rows[e / (D / 8)];
+        const int e = e0 + u * 256, r = rows[e / (D / 8)];
         v[u] = make_uint4(0u, 0u, 0u, 0u);
         if (r >= 0) v[u] = __ldg(reinterpret_cast<const uint4*>(p.q + (size_t)r * D) + e % (D / 8));
       }
 #pragma unroll
       for (int u = 0; u < kRound; ++u) {
-        const int e = e0 + u * 128, r = e / (D / 8), c = e % (D / 8);
+        const int e = e0 + u * 256, r = e / (D / 8), c = e % (D / 8);
+        if constexpr (C::FP8)
+          v[u] = make_uint4(to_f16x2(v[u].x), to_f16x2(v[u].y), to_f16x2(v[u].z), to_f16x2(v[u].w));
         *reinterpret_cast<uint4*>(smem + C::Q_OFFSET + (c >> 3) * N * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
             v[u];
       }
     }
     fence_proxy_async_smem();
     mbar_arrive(q_full);
-    named_bar_sync(1, 128);
 
-    const uint32_t lanes = tmem + ((uint32_t)warp << 21);
-    float l[N];
+    float v_top = 1.f, v_inv = 1.f;  // FP8: the piece's largest V scale
+    if constexpr (C::FP8) {
+      float m = 0.f;
+      for (int tok = lo + lt * 16; tok < hi; tok += 128 * 16) {
+        const int page = __ldg(table + tok / p.page_size);
+        if ((unsigned)page < (unsigned)p.num_pages)
+          m = fmaxf(m, fabsf(__ldg(p.v_scale + (size_t)page * p.num_kv_heads + g)));
+      }
+      const int k = __reduce_max_sync(kFullMask, __float_as_int(m));
+      if (lane == 0) atomicMax(top, k);
+      __syncwarp();
+      named_bar_sync(bar, 128);
+      v_top = __int_as_float(top[0]);
+      v_inv = v_top > 0.f ? 1.f / v_top : 0.f;
+      named_bar_sync(bar, 128);
+      if (lt == 0) top[0] = kNoTop;
+      __syncwarp();
+    }
+
+    const uint32_t quarter = tmem + ((uint32_t)(warp & 3) << 21);
+    const uint32_t o_at = quarter + wg * CW;
+    float l[CW];
 #pragma unroll
-    for (int c = 0; c < N; ++c) l[c] = 0.f;
+    for (int c = 0; c < CW; ++c) l[c] = 0.f;
     uint32_t err = 0;
     bool ok = true;
     // this lane's token of tile i: whether it is attended, its scales
     auto token = [&](int i, bool& valid, float& ks, float& vs) {
-      const int tok = lo + i * kTok + tid;
+      const int tok = lo + i * kTok + lt;
       valid = false;
       ks = 1.f;
       vs = 1.f;
@@ -425,6 +469,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
         }
       }
     };
+    // P: this token's row; its 16-byte chunks swizzled over the row
+    constexpr int kChunkMask = C::P_ROW / 16 - 1, kSwShift = N >= 64 ? 0 : N == 32 ? 1 : 2;
+    uint8_t* p_row = smem + C::P_OFFSET + lt * C::P_ROW + (N == 128 ? wg * kSlab : 0);
+    const int p_sw = (lt >> kSwShift) & kChunkMask, p_chunk = N == 128 ? 0 : wg * (CW / 8);
     bool valid;
     float ks, vs;
     token(0, valid, ks, vs);
@@ -437,142 +485,163 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       ok = mbar_wait(&s_full[i & 1], (i >> 1) & 1) && ok;
       __syncwarp();
       tmem_fence_after();
-      const uint32_t sa = lanes + C::O_COLS + (i & 1) * N;
+      const uint32_t sa = quarter + C::O_COLS + (i & 1) * N + wg * CW;
       // does any score leave its row's range?
       float over = -INFINITY;
+      uint32_t x[LD];
 #pragma unroll
-      for (int c0 = 0; c0 < N; c0 += 16) {
-        uint32_t x[16];
-        tmem_ld16(x, sa + c0);
+      for (int c0 = 0; c0 < CW; c0 += LD) {
+        tmem_ld(x, sa + c0);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 16; c += 4) {
-          const float4 m = *reinterpret_cast<const float4*>(ref + c0 + c);
-          over = fmaxf(over, fmaxf(fmaxf(fmaf(__uint_as_float(x[c]), sc, -m.x), fmaf(__uint_as_float(x[c + 1]), sc, -m.y)),
-                                   fmaxf(fmaf(__uint_as_float(x[c + 2]), sc, -m.z), fmaf(__uint_as_float(x[c + 3]), sc, -m.w))));
-        }
+        for (int c = 0; c < LD; ++c) over = fmaxf(over, fmaf(__uint_as_float(x[c]), sc, nref[c0 + c]));
       }
-      if (named_bar_or(1, 128, !ok || i == 0 || (valid && over > kSlack))) {
+      if (named_bar_or(bar, 128, !ok || (valid && over > kSlack))) {
         // the rows that left theirs take the true maximum; P(i - 1) is spent
         if (i > 0) ok = mbar_wait(p_empty, (i - 1) & 1) && ok;
         __syncwarp();
-        if (named_bar_or(1, 128, !ok)) break;
+        if (named_bar_or(bar, 128, !ok)) break;
         tmem_fence_after();
 #pragma unroll 1
-        for (int c0 = 0; c0 < N; c0 += 16) {
-          uint32_t x[16];
-          tmem_ld16(x, sa + c0);
+        for (int c0 = 0; c0 < CW; c0 += LD) {
+          tmem_ld(x, sa + c0);
           tmem_wait_ld();
+          int mine = kNoTop;
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
+          for (int c = 0; c < LD; ++c) {
             const int m = __reduce_max_sync(kFullMask, ordered(valid ? __uint_as_float(x[c]) * sc : -INFINITY));
-            if (lane == c) swap[warp * N + c0 + c] = unordered(m);
+            if (lane == c) mine = m;
           }
-        }
-        named_bar_sync(1, 128);
-        if (tid < N) {
-          const float m = fmaxf(fmaxf(swap[tid], swap[N + tid]), fmaxf(swap[2 * N + tid], swap[3 * N + tid]));
-          const float was = ref[tid];
-          const bool move = m > was + kSlack || was == -INFINITY;
-          swap[4 * N + tid] = move && was != -INFINITY ? ex2(was - m) : 1.f;
-          if (move) ref[tid] = m;
+          if (lane < LD) atomicMax(top + c0 + lane, mine);
         }
         __syncwarp();
-        named_bar_sync(1, 128);
+        named_bar_sync(bar, 128);
+        // a row moves if its maximum left the range: factor of what it holds so far
+        auto moves = [&](int c) { return unordered(top[c]) + nref[c] > kSlack; };
+        auto factor = [&](int c) { return moves(c) ? ex2(-nref[c] - unordered(top[c])) : 1.f; };
 #pragma unroll
-        for (int c = 0; c < N; ++c) l[c] *= swap[4 * N + c];
+        for (int c = 0; c < CW; ++c) l[c] *= factor(c);
         if (i > 0) {
-#pragma unroll 1
-          for (int c0 = 0; c0 < C::O_COLS; c0 += 16) {
-            uint32_t x[16];
-            tmem_ld16(x, lanes + c0);
-            tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 16; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) * swap[4 * N + (c0 % N) + c]);
-            tmem_st16(lanes + c0, x);
+          for (int c0 = 0; c0 < CW; c0 += LD) {
+            float f[LD];
+#pragma unroll
+            for (int c = 0; c < LD; ++c) f[c] = factor(c0 + c);
+#pragma unroll 1
+            for (int s = 0; s < KS; ++s) {
+              tmem_ld(x, o_at + s * N + c0);
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < LD; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) * f[c]);
+              tmem_st(o_at + s * N + c0, x);
+            }
           }
           tmem_wait_st();
         }
-        named_bar_sync(1, 128);
+        named_bar_sync(bar, 128);
+        if (lt < CW) {
+          if (moves(lt)) nref[lt] = -unordered(top[lt]);
+          top[lt] = kNoTop;
+        }
+        __syncwarp();
+        named_bar_sync(bar, 128);
       } else if (i > 0) {
         ok = mbar_wait(p_empty, (i - 1) & 1);
         __syncwarp();
       }
-      // probabilities: [64-token slab][N rows][128 B], swizzled as the K-major operand
-      uint8_t* pd = smem + C::P_OFFSET + (tid >> 6) * N * 128 + (tid & 7) * 2;
-      const int chunk = (tid & 63) >> 3;
+      const bool all = __all_sync(kFullMask, valid);
+      const float pv = vs * v_inv;
 #pragma unroll
-      for (int c0 = 0; c0 < N; c0 += 16) {
-        uint32_t x[16];
-        tmem_ld16(x, sa + c0);
+      for (int c0 = 0; c0 < CW; c0 += LD) {
+        tmem_ld(x, sa + c0);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const float m = ref[c0 + c];
-          // a row without a finite score yet has reference -inf: its probabilities are 2^-inf
-          const float e = valid ? ex2(fmaf(__uint_as_float(x[c]), sc, m == -INFINITY ? 0.f : -m)) : 0.f;
-          l[c0 + c] += e;
-          const __nv_bfloat16 h = __float2bfloat16_rn(C::FP8 && valid ? e * vs : e);
-          *reinterpret_cast<__nv_bfloat16*>(pd + (c0 + c) * 128 + ((chunk ^ (c & 7)) << 4)) = h;
+        for (int c = 0; c < LD; c += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float e[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int cc = c + 2 * k + u;
+              e[u] = ex2(fmaf(__uint_as_float(x[cc]), sc, nref[c0 + cc]));
+              if (!all && !valid) e[u] = 0.f;
+              l[c0 + cc] += e[u];
+              if constexpr (C::FP8) e[u] = !all && !valid ? 0.f : e[u] * pv;
+            }
+            w[k] = pack2<C::FP8>(e[0], e[1]);
+          }
+          *reinterpret_cast<uint4*>(p_row + (((p_chunk + (c0 + c) / 8) ^ p_sw) << 4)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
       fence_proxy_async_smem();
       tmem_fence_before();
       mbar_arrive(p_full);
       mbar_arrive(&s_empty[i & 1]);
-      if (!valid && lo + i * kTok + tid < hi) err |= kErrBadPage;
+      if (!valid && lo + i * kTok + lt < hi) err |= kErrBadPage;
       valid = nvalid;
       ks = nks;
       vs = nvs;
     }
     ok = ok && mbar_wait(p_empty, (ntile - 1) & 1);
     __syncwarp();
-    if (named_bar_or(1, 128, !ok)) {
+    // (both warpgroups: the sums go where the other's last products read)
+    if (named_bar_or(3, 256, !ok)) {
       err |= kErrTimeout;
     } else {
       tmem_fence_after();
       // the rows' sums over the token lanes, in the ring (every product is done with it)
-      float* sum = reinterpret_cast<float*>(smem + C::RING_OFFSET);
+      float* sum = reinterpret_cast<float*>(smem + C::RING_OFFSET) + wg * (kTok * (CW + 1) + 128);
+      float* part = sum + kTok * (CW + 1);
 #pragma unroll
-      for (int c = 0; c < N; ++c) sum[tid * (N + 1) + c] = l[c];
-      named_bar_sync(1, 128);
-      float* inv = reinterpret_cast<float*>(smem + C::P_OFFSET);
-      if (tid < N) {
-        float a[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int k = 0; k < 128; k += 4)
+      for (int c = 0; c < CW; ++c) sum[lt * (CW + 1) + c] = l[c];
+      named_bar_sync(bar, 128);
+      const int col = lt % CW, first = lt / CW * CW;
+      float a[2] = {0.f, 0.f};
+#pragma unroll 4
+      for (int k = 0; k < CW; k += 2) {
+        a[0] += sum[(first + k) * (CW + 1) + col];
+        a[1] += sum[(first + k + 1) * (CW + 1) + col];
+      }
+      part[lt] = a[0] + a[1];
+      named_bar_sync(bar, 128);
+      if (lt < CW) {
+        float total = 0.f;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) a[u] += sum[(k + u) * (N + 1) + tid];
-        const float total = (a[0] + a[1]) + (a[2] + a[3]);
+        for (int k = 0; k < 128 / CW; ++k) total += part[k * CW + lt];
         // no attended token: weight 0 and a zero row; NaN stays NaN
-        inv[tid] = total == 0.f ? 0.f : 1.f / total;
-        if (tid < t.rows)
-          p.lse_part[(size_t)rows[tid] * p.num_pieces + piece] =
-              total == 0.f ? -INFINITY : ((ref[tid] == -INFINITY ? 0.f : ref[tid]) + log2f(total)) * 0.69314718055994530942f;
+        if (rows[wg * CW + lt] >= 0)
+          p.lse_part[(size_t)rows[wg * CW + lt] * p.num_pieces + piece] =
+              total == 0.f ? -INFINITY : (log2f(total) - nref[lt]) * 0.69314718055994530942f;
+        nref[lt] = total == 0.f ? 0.f : v_top / total;
       }
       __syncwarp();
-      named_bar_sync(1, 128);
+      named_bar_sync(bar, 128);
+      constexpr int OC = CW < 16 ? CW : 16;
 #pragma unroll 1
-      for (int c0 = 0; c0 < N; c0 += 16) {
-        if (c0 >= t.rows) break;
-        uint32_t x[KS][16];
+      for (int c0 = 0; c0 < CW; c0 += OC) {
+        if (wg * CW + c0 >= t.rows) break;
+        uint32_t y[KS][OC];
 #pragma unroll
-        for (int s = 0; s < KS; ++s) tmem_ld16(x[s], lanes + s * N + c0);
+        for (int s = 0; s < KS; ++s) tmem_ld(y[s], o_at + s * N + c0);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          if (c0 + c >= t.rows) break;
-          float* dst = p.o_part + ((size_t)rows[c0 + c] * p.num_pieces + piece) * D + tid;
-          const float f = inv[c0 + c];
+        for (int c = 0; c < OC; ++c) {
+          const int r = rows[wg * CW + c0 + c];
+          if (r < 0) break;
+          float* dst = p.o_part + ((size_t)r * p.num_pieces + piece) * D + lt;
+          const float f = nref[c0 + c];
 #pragma unroll
-          for (int s = 0; s < KS; ++s) dst[s * 128] = __uint_as_float(x[s][c]) * f;
+          for (int s = 0; s < KS; ++s) dst[s * 128] = __uint_as_float(y[s][c]) * f;
         }
       }
     }
     err = __reduce_or_sync(kFullMask, err);
     if (lane == 0 && err) atomicOr(p.err, err);
   } else if constexpr (C::FP8) {
-    // ---- FP8: e4m3 stages widened to bf16 operand stages, a thread per token row
-    const int row = tid - 192, sw = row & 7, total = 2 * KS * ntile;
+    // ---- FP8: e4m3 stages widened to f16 operand stages, a thread per token row
+    const int row = tid - 320, sw = row & 7, total = 2 * KS * ntile;
     bool ok = true;
     for (int it = 0; it < total; ++it) {
       const int st = it % NST, rs = it % C::NRAW;
@@ -592,10 +661,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
         widen4(w.y, a.z, a.w);
         widen4(w.z, b.x, b.y);
         widen4(w.w, b.z, b.w);
-        if (has_nan4(w.x) || has_nan4(w.y) || has_nan4(w.z) || has_nan4(w.w)) {
-          a.x = nan_fix(a.x, w.x), a.y = nan_fix(a.y, w.x >> 16), a.z = nan_fix(a.z, w.y), a.w = nan_fix(a.w, w.y >> 16);
-          b.x = nan_fix(b.x, w.z), b.y = nan_fix(b.y, w.z >> 16), b.z = nan_fix(b.z, w.w), b.w = nan_fix(b.w, w.w >> 16);
-        }
         uint8_t* to = dst + (c >> 2) * kSlab;
         const int cc = (c & 3) * 2;
         *reinterpret_cast<uint4*>(to + ((cc ^ sw) << 4)) = a;
@@ -611,7 +676,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
   }
   tmem_fence_before();
   __syncthreads();
-  if (warp == 4) tmem_dealloc(tmem, C::TMEM_COLS);
+  if (warp == 8) tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
 #define PD_FOR_EACH_PREFIX(X)                                                                          \
