@@ -279,16 +279,17 @@ pd_status launch_own_part(const pd_plan* plan, const void* q, const void* k_pool
                 workspace_bytes, out, stream);
 }
 
-pd_status encode_row_map(CUtensorMap* map, const void* pool, const pd_layer_desc& ly, int rows) {
+pd_status encode_group_map(CUtensorMap* map, const void* pool, const pd_layer_desc& ly, int rows, int slabs) {
   EncodeTiledFn fn = encode_tiled_fn();
   if (!fn) return PD_ERR_CUDA;
   const bool fp8 = ly.kv_dtype == PD_KV_FP8_E4M3;
-  const cuuint64_t elem = fp8 ? 1 : 2;
-  const cuuint64_t dims[2] = {(cuuint64_t)ly.head_dim, (cuuint64_t)ly.num_pages * ly.num_kv_heads * ly.page_size};
-  const cuuint64_t strides[1] = {(cuuint64_t)ly.head_dim * elem};
-  const cuuint32_t box[2] = {(cuuint32_t)(128 / elem), (cuuint32_t)rows};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = fn(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+  const cuuint64_t elem = fp8 ? 1 : 2, span = 128 / elem, row = (cuuint64_t)ly.head_dim * elem;
+  const cuuint64_t total = (cuuint64_t)ly.num_pages * ly.num_kv_heads * ly.page_size;
+  const cuuint64_t dims[4] = {span, 8, (cuuint64_t)ly.head_dim / span, total / 8};
+  const cuuint64_t strides[3] = {row, 128, 8 * row};
+  const cuuint32_t box[4] = {(cuuint32_t)span, 8, (cuuint32_t)slabs, (cuuint32_t)rows / 8};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
                         const_cast<void*>(pool), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);

@@ -21,9 +21,9 @@
 // warpgroups with half the rows each: with one, its ~1700 instructions a tile
 // at one warp per scheduler took 5 us against 1.9 us of products), warp 8 the
 // matrix instructions, warp 9 the copies; FP8: warps 10-13 widen the e4m3
-// stages to f16 operands. K and V arrive as [64-dim slab][128 tokens][128 B]
-// with the 128-byte swizzle: K-major for the first product, and the same layout
-// read M-major for the second, so nothing is transposed; P is written N-major,
+// stages to f16 operands. K and V arrive as [8-token group][64-dim slab][8][128 B]
+// atoms with the 128-byte swizzle: K-major for the first product, and the same
+// layout read M-major for the second, so nothing is transposed; P is written N-major,
 // a token's row at a time. A K=V layer fetches the tile again for its second
 // use (an L2 hit).
 //
@@ -44,9 +44,8 @@ namespace pd {
 namespace {
 
 constexpr int kTok = kPrefixTile;
-constexpr int kSlab = kTok * 128;          // bytes of a slab: 64 bf16 dims of 128 tokens
-constexpr int kStage = 2 * kSlab;          // an operand stage: 128 dims
-constexpr int kRaw = kTok * 128;           // FP8: 128 dims of 128 tokens, e4m3
+constexpr int kStage = kTok * 256;         // an operand stage: 128 dims of 128 tokens of K, or as many bytes of V
+constexpr int kRaw = kStage / 2;           // FP8: the same in e4m3
 constexpr int kBody = 224 * 1024;          // query rows, probabilities and rings
 constexpr float kSlack = 8.f;              // log2 of what a probability may exceed 1 by
 constexpr float kLow = 3e38f;              // negated reference of a row without a score yet
@@ -57,6 +56,7 @@ struct PrefixCfg {
   static constexpr int D = D_, N = N_;
   static constexpr bool FP8 = FP8_;
   static constexpr int KS = D / 128;       // stages of a tile's K (and of its V)
+  static constexpr int VT = kTok / KS;     // tokens of a V stage
   static constexpr int Q_BYTES = N * D * 2, P_BYTES = N * kTok * 2;
   static constexpr int ROOM = kBody - Q_BYTES - P_BYTES;
   static constexpr int NST = FP8 ? 3 : (ROOM / kStage < 6 ? ROOM / kStage : 6);
@@ -248,62 +248,85 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       p.lse_part[(size_t)row_of(p, t, r, g) * p.num_pieces + piece] = -INFINITY;
   } else if (warp == 9) {
     // ---- copies: stages in the order the products use them, K(0), K(1), V(0), K(2), V(1), ...
-    const int box = p.box_rows, nbox = kTok / box;
-    const uint64_t policy = p.keep_in_l2 ? 0 : l2_evict_first_policy();
-    const int j = lane % nbox, slab = lane / nbox;
-    constexpr int SLABS = C::FP8 ? 1 : 2;
+    // A K stage is 128 dims of the tile, a V stage all dims of VT tokens; both
+    // land as [8-row group][64-dim slab][8 rows][128 B], so that a 16-token page
+    // takes one copy of 4 KB (K) or 16 KB (V, d = 512): with a copy per page and
+    // slab (2 KB) the copies took 5.5 us a tile. Lane j holds the pool row of
+    // the tile's j-th K box and j-th V box.
+    const int k_boxes = kTok / p.k_box, v_boxes = C::VT / p.v_box;
+    const uint64_t policy = p.keep_in_l2 ? l2_evict_normal_policy() : l2_evict_first_policy();
     constexpr int NR = C::FP8 ? C::NRAW : NST;
     constexpr int BYTES = C::FP8 ? kRaw : kStage;
+    constexpr int K_SLABS = C::FP8 ? 1 : 2, ROW_BYTES = C::FP8 ? D : 2 * D;
     uint64_t* land = C::FP8 ? raw_full : full;
     uint64_t* freed = C::FP8 ? raw_empty : empty;
     uint8_t* ring = smem + (C::FP8 ? C::RAW_OFFSET : C::RING_OFFSET);
     uint32_t err = 0;
-    // the pool row of this lane's box of a tile (-1: past the piece); a page
-    // outside the pool is fetched past the pool's end, which reads zeros
-    auto row_at = [&](int tile) -> int {
-      const int tok = lo + tile * kTok + j * box;
-      if (tile >= ntile || tok >= hi || slab >= SLABS) return -1;
+    // the 8-row group of the pool where this lane's box of a tile starts (-1:
+    // past the piece); a page outside the pool is fetched past the pool's end,
+    // which reads zeros
+    auto group_at = [&](int tile, int box) -> int {
+      const int tok = lo + tile * kTok + lane * box;
+      if (tile >= ntile || tok >= hi || lane >= kTok / box) return -1;
       const int page = __ldg(table + tok / p.page_size);
       if ((unsigned)page >= (unsigned)p.num_pages) {
         err |= kErrBadPage;
-        return p.num_pages * p.num_kv_heads * p.page_size;
+        return p.num_pages * p.num_kv_heads * p.page_size / 8;
       }
-      return (page * p.num_kv_heads + g) * p.page_size + tok % p.page_size;
+      return ((page * p.num_kv_heads + g) * p.page_size + tok % p.page_size) / 8;
     };
-    int it = 0;
+    int st = 0, uses = 0;  // the next stage, and how many stages went out
+    uint32_t phase = 1;    // of the stage's release (the first round waits for nothing)
     bool ok = true;
-    auto load = [&](int row, const CUtensorMap* map) {
-      const int boxes = __popc(__ballot_sync(kFullMask, row >= 0));
-      for (int s = 0; s < KS && ok; ++s, ++it) {
-        const int st = it % NR;
-        if (it >= NR) ok = mbar_wait(&freed[st], ((it / NR) - 1) & 1);
-        ok = __all_sync(kFullMask, ok);
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&land[st], boxes * box * 128 + p.stall_bytes);
-        __syncwarp();
-        if (row >= 0) {
-          uint8_t* dst = ring + st * BYTES + slab * kSlab + j * box * 128;
-          const int dim = s * 128 + slab * 64;
-          if (p.keep_in_l2)
-            tma_load_2d_plain(dst, map, dim, row, &land[st]);
-          else
-            tma_load_2d(dst, map, dim, row, &land[st], policy);
-        }
+    auto begin = [&](int boxes, int box_bytes) {
+      ok = __all_sync(kFullMask, uses < NR || mbar_wait(&freed[st], phase));
+      if (ok && lane == 0) mbar_arrive_expect_tx(&land[st], boxes * box_bytes + p.stall_bytes);
+      __syncwarp();
+      return ok;
+    };
+    auto end = [&] {
+      ++uses;
+      if (++st == NR) {
+        st = 0;
+        phase ^= 1;
       }
     };
-    int row = row_at(0), next = row_at(1);
-    load(row, &p.kmap);
+    auto load_k = [&](int at) {
+      const int bytes = p.k_box * 128 * K_SLABS;
+      const int boxes = __popc(__ballot_sync(kFullMask, at >= 0));
+#pragma unroll 1
+      for (int s = 0; s < KS; ++s) {
+        if (!begin(boxes, bytes)) return;
+        if (at >= 0) tma_load_4d(ring + st * BYTES + lane * bytes, &p.kmap, 0, 0, s * K_SLABS, at, &land[st], policy);
+        end();
+      }
+    };
+    auto load_v = [&](int at) {
+      const int bytes = p.v_box * ROW_BYTES;
+#pragma unroll 1
+      for (int s = 0; s < KS; ++s) {
+        const bool mine = at >= 0 && lane / v_boxes == s;
+        if (!begin(__popc(__ballot_sync(kFullMask, mine)), bytes)) return;
+        if (mine)
+          tma_load_4d(ring + st * BYTES + lane % v_boxes * bytes, &p.vmap, 0, 0, 0, at, &land[st], policy);
+        end();
+      }
+    };
+    int k_next = group_at(0, p.k_box), v_at = group_at(0, p.v_box);
+    load_k(k_next);
+    k_next = group_at(1, p.k_box);
+#pragma unroll 1
     for (int i = 0; i < ntile && ok; ++i) {
-      const int after = row_at(i + 2);
-      if (i + 1 < ntile) load(next, &p.kmap);
-      if (ok) load(row, &p.vmap);
-      row = next;
-      next = after;
+      const int k_after = group_at(i + 2, p.k_box), v_next = group_at(i + 1, p.v_box);
+      if (i + 1 < ntile) load_k(k_next);
+      if (ok) load_v(v_at);
+      k_next = k_after;
+      v_at = v_next;
     }
     // no copy may still be landing when the CTA exits
     if (lane == 0) {
       const unsigned long long deadline = global_timer_ns() + kWaitTimeoutNs;
-      for (int k = max(0, it - NR); k < it; ++k)
+      for (int k = max(0, uses - NR); k < uses; ++k)
         if (!mbar_wait_until(&land[k % NR], (k / NR) & 1, deadline)) ok = false;
       if (!ok) err |= kErrTimeout;
     }
@@ -317,9 +340,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     constexpr uint32_t kPv = mma_desc_16bit(!C::FP8, 128, N, true, true);
     // descriptors' bases; a step further is a constant added to the address field
     const uint32_t base = smem_u32(smem);
-    const uint64_t k_desc = smem_desc(base + C::RING_OFFSET, 16, 1024), q_desc = smem_desc(base, 16, 1024);
-    const uint64_t v_desc = smem_desc(base + C::RING_OFFSET, kSlab, 1024);
-    const uint64_t p_desc = smem_desc(base + C::P_OFFSET, kSlab, 8 * C::P_ROW, C::P_ROW);
+    const uint64_t k_desc = smem_desc(base + C::RING_OFFSET, 16, 2048), q_desc = smem_desc(base, 16, 1024);
+    const uint64_t v_desc = smem_desc(base + C::RING_OFFSET, 1024, D * 16);
+    const uint64_t p_desc = smem_desc(base + C::P_OFFSET, kTok * 128, 8 * C::P_ROW, C::P_ROW);
     int st = 0;
     uint32_t phase = 0;
     bool ok = __all_sync(kFullMask, mbar_wait(q_full, 0));
@@ -341,7 +364,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
           const uint64_t a = k_desc + st * (kStage >> 4), b = q_desc + s * 2 * (N * 128 >> 4);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            mma_ss(d, a + (k >> 2) * (kSlab >> 4) + (k & 3) * 2, b + (k >> 2) * (N * 128 >> 4) + (k & 3) * 2, kQk,
+            mma_ss(d, a + (k >> 2) * (1024 >> 4) + (k & 3) * 2, b + (k >> 2) * (N * 128 >> 4) + (k & 3) * 2, kQk,
                    k != 0 || s != 0);
           mma_commit(&empty[st]);
           if (s == KS - 1) mma_commit(&s_full[i & 1]);
@@ -355,23 +378,29 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     for (int i = 0; i < ntile && ok; ++i) {
       if (i + 1 < ntile) qk(i + 1);
       if (ok) ok = __all_sync(kFullMask, mbar_wait(p_full, i & 1));
-      const int steps = (min(kTok, hi - lo - i * kTok)) / 16;
+      const int steps = min(kTok, hi - lo - i * kTok) / 16;
 #pragma unroll 1
       for (int s = 0; s < KS && ok; ++s) {
         ok = __all_sync(kFullMask, mbar_wait(&full[st], phase));
         if (!ok) break;
         tmem_fence_after();
         if (elect_one()) {
-          const uint64_t a = v_desc + st * (kStage >> 4);
-          const uint32_t d = tmem + s * N;
-          if (steps == 8) {
+          const uint64_t a = v_desc + st * (kStage >> 4), b = p_desc + s * (C::VT * C::P_ROW >> 4);
+          // 16 tokens at a time, all head dims
+          if ((s + 1) * (C::VT / 16) <= steps) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_ss(d, a + k * (2048 >> 4), p_desc + k * (16 * C::P_ROW >> 4), kPv, k != 0 || i != 0);
+            for (int k = 0; k < C::VT / 16; ++k)
+#pragma unroll
+              for (int m = 0; m < KS; ++m)
+                mma_ss(tmem + m * N, a + k * (D * 32 >> 4) + m * (2048 >> 4), b + k * (16 * C::P_ROW >> 4), kPv,
+                       k != 0 || s != 0 || i != 0);
           } else {
 #pragma unroll 1
-            for (int k = 0; k < steps; ++k)
-              mma_ss(d, a + k * (2048 >> 4), p_desc + k * (16 * C::P_ROW >> 4), kPv, k != 0 || i != 0);
+            for (int k = 0; s * (C::VT / 16) + k < steps; ++k)
+#pragma unroll 1
+              for (int m = 0; m < KS; ++m)
+                mma_ss(tmem + m * N, a + k * (D * 32 >> 4) + m * (2048 >> 4), b + k * (16 * C::P_ROW >> 4), kPv,
+                       k != 0 || s != 0 || i != 0);
           }
           mma_commit(&empty[st]);
           if (s == KS - 1) mma_commit(p_empty);
@@ -471,7 +500,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     };
     // P: this token's row; its 16-byte chunks swizzled over the row
     constexpr int kChunkMask = C::P_ROW / 16 - 1, kSwShift = N >= 64 ? 0 : N == 32 ? 1 : 2;
-    uint8_t* p_row = smem + C::P_OFFSET + lt * C::P_ROW + (N == 128 ? wg * kSlab : 0);
+    uint8_t* p_row = smem + C::P_OFFSET + lt * C::P_ROW + (N == 128 ? wg * (kTok * 128) : 0);
     const int p_sw = (lt >> kSwShift) & kChunkMask, p_chunk = N == 128 ? 0 : wg * (CW / 8);
     bool valid;
     float ks, vs;
@@ -652,7 +681,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
         break;
       }
       const uint8_t* src = smem + C::RAW_OFFSET + rs * kRaw + row * 128;
-      uint8_t* dst = smem + C::RING_OFFSET + st * kStage + row * 128;
+      uint8_t* dst = smem + C::RING_OFFSET + st * kStage + (row >> 3) * 2048 + (row & 7) * 128;
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         const uint4 w = *reinterpret_cast<const uint4*>(src + ((c ^ sw) << 4));
@@ -661,7 +690,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
         widen4(w.y, a.z, a.w);
         widen4(w.z, b.x, b.y);
         widen4(w.w, b.z, b.w);
-        uint8_t* to = dst + (c >> 2) * kSlab;
+        uint8_t* to = dst + (c >> 2) * 1024;
         const int cc = (c & 3) * 2;
         *reinterpret_cast<uint4*>(to + ((cc ^ sw) << 4)) = a;
         *reinterpret_cast<uint4*>(to + (((cc + 1) ^ sw) << 4)) = b;

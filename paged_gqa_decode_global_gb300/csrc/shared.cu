@@ -294,15 +294,19 @@ pd_status decode_shared(const pd_shared_plan* plan, bool fp8, const void* q, con
   p.tiles = plan->tiles;
   p.num_pieces = plan->num_pieces;
   p.chunk_tokens = plan->chunk_tokens;
-  p.box_rows = 16;
-  while (p.box_rows < kPrefixTile && ly.page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
+  // a stage of the pass holds 128 tokens x 128 dims of K, or all dims of v_tokens tokens of V
+  const int v_tokens = kPrefixTile * 128 / ly.head_dim;
+  p.k_box = 16;
+  while (p.k_box < kPrefixTile && ly.page_size % (2 * p.k_box) == 0) p.k_box *= 2;
+  p.v_box = std::min<int32_t>(p.k_box, v_tokens);
   p.keep_in_l2 = plan->tiles > 1 || ly.kv_shared;
   p.stall_bytes = own.test_stall_bytes;
   const PrefixInstance& v = kPrefixInstances[plan->variant];
   const void* fn = prefix_kernel_ptr(plan->variant);
   pd_status st = ensure_prefix_smem(plan->variant, fn, v.smem_bytes);
-  if (st == PD_OK) st = encode_row_map(&p.kmap, k_pool, ly, p.box_rows);
-  if (st == PD_OK) st = encode_row_map(&p.vmap, ly.kv_shared ? k_pool : v_pool, ly, p.box_rows);
+  const int slabs = ly.head_dim / (fp8 ? 128 : 64);
+  if (st == PD_OK) st = encode_group_map(&p.kmap, k_pool, ly, p.k_box, fp8 ? 1 : 2);
+  if (st == PD_OK) st = encode_group_map(&p.vmap, ly.kv_shared ? k_pool : v_pool, ly, p.v_box, slabs);
   if (st != PD_OK) return st;
   void* args[] = {&p};
   if (plan->tiles > 0 && launch_dependent(fn, dim3(plan->tiles, plan->num_pieces, ly.num_kv_heads), v.threads,

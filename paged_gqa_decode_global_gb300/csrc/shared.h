@@ -11,7 +11,9 @@ namespace pd {
 constexpr int kPrefixTile = 128;  // prefix tokens of one tile of the prefix pass
 
 struct SharedParams {
-  CUtensorMap kmap, vmap;  // the pools as {D, rows}, boxes {128 bytes, box_rows}, 128-byte swizzle
+  // the pools as {128 bytes, 8 rows, slabs, 8-row groups}, 128-byte swizzle: a
+  // box lands as [group][slab][8 rows][128 B]
+  CUtensorMap kmap, vmap;
   const uint16_t* q;
   const float* k_scale;  // FP8
   const float* v_scale;
@@ -25,7 +27,7 @@ struct SharedParams {
   int32_t batch, num_groups, query_tokens, num_q_heads, num_kv_heads, group, head_dim;
   int32_t page_size, num_pages, max_prefix_pages;
   int32_t row_tile, tiles, num_pieces, chunk_tokens;
-  int32_t box_rows;     // tokens of one copy: the largest of 16, 32, 64, 128 that divides page_size
+  int32_t k_box, v_box;  // tokens of one copy of K and of V (both divide page_size)
   int32_t keep_in_l2;   // the prefix rows are read more than once (several row tiles, K=V)
   int32_t stall_bytes;  // tests only: bytes expected per stage beyond what the copies deliver
 };
@@ -49,8 +51,9 @@ pd_status launch_own_part(const pd_plan* plan, const void* q, const void* k_pool
                           const float* k_scale, const float* v_scale, const int32_t* block_tables,
                           const int32_t* seq_lens, float scale, void* workspace, size_t workspace_bytes, void* out,
                           void* stream);
-// abi.cu: a pool's tensor map with boxes of `rows` rows; the shared-memory limit of a prefix instance
-pd_status encode_row_map(CUtensorMap* map, const void* pool, const pd_layer_desc& ly, int rows);
+// abi.cu: a pool's tensor map with boxes of `rows` rows by `slabs` 128-byte slabs; the shared-memory limit of a
+// prefix instance
+pd_status encode_group_map(CUtensorMap* map, const void* pool, const pd_layer_desc& ly, int rows, int slabs);
 pd_status ensure_prefix_smem(int variant, const void* fn, int smem_bytes);
 
 }  // namespace pd
