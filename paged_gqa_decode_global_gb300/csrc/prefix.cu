@@ -20,8 +20,8 @@
 // Roles: warps 0-7 softmax and epilogue (a thread per token lane, two
 // warpgroups with half the rows each: with one, its ~1700 instructions a tile
 // at one warp per scheduler took 5 us against 1.9 us of products), warp 8 the
-// matrix instructions, warp 9 the copies; FP8: warps 10-13 widen the e4m3
-// stages to f16 operands. K and V arrive as [8-token group][64-dim slab][8][128 B]
+// matrix instructions, warps 9-11 the copies (every third stage each: a lone
+// warp spends ~60 cycles a copy); FP8: warps 12-15 widen the e4m3 stages to f16 operands. K and V arrive as [8-token group][64-dim slab][8][128 B]
 // atoms with the 128-byte swizzle: K-major for the first product, and the same
 // layout read M-major for the second, so nothing is transposed; P is written N-major,
 // a token's row at a time. A K=V layer fetches the tile again for its second
@@ -47,6 +47,7 @@ constexpr int kTok = kPrefixTile;
 constexpr int kStage = kTok * 256;         // an operand stage: 128 dims of 128 tokens of K, or as many bytes of V
 constexpr int kRaw = kStage / 2;           // FP8: the same in e4m3
 constexpr int kBody = 224 * 1024;          // query rows, probabilities and rings
+constexpr int kCopyWarps = 3;              // warps 9..11 (12 or 16 warps keep 168 or 128 registers a thread)
 constexpr float kSlack = 8.f;              // log2 of what a probability may exceed 1 by
 constexpr float kLow = 3e38f;              // negated reference of a row without a score yet
 constexpr int kNoTop = (int)0x807fffff;    // ordered(-inf)
@@ -70,7 +71,7 @@ struct PrefixCfg {
   static constexpr int NBAR = 2 * NST + 2 * NRAW + 2 + 2 + 1 + 1 + 1 + 1;
   static constexpr int TMEM_OFFSET = BAR_OFFSET + NBAR * 8;
   static constexpr int SMEM_BYTES = TMEM_OFFSET + 16 + 1024;
-  static constexpr int THREADS = FP8 ? 448 : 320;
+  static constexpr int THREADS = 32 * (9 + kCopyWarps + (FP8 ? 4 : 0));
   static constexpr int CW = N / 2;         // rows of a softmax warpgroup
   static constexpr int LD = CW < 32 ? CW : 32;
   // P: [N / 64 blocks][128 tokens][row of up to 64 query rows], swizzled over the row
@@ -246,14 +247,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     // nothing here: weight 0 (the join reads no row of such a piece)
     for (int r = tid; r < t.rows; r += C::THREADS)
       p.lse_part[(size_t)row_of(p, t, r, g) * p.num_pieces + piece] = -INFINITY;
-  } else if (warp == 9) {
+  } else if (warp >= 9 && warp < 9 + kCopyWarps) {
     // ---- copies: stages in the order the products use them, K(0), K(1), V(0), K(2), V(1), ...
     // A K stage is 128 dims of the tile, a V stage all dims of VT tokens; both
     // land as [8-row group][64-dim slab][8 rows][128 B], so that a 16-token page
     // takes one copy of 4 KB (K) or 16 KB (V, d = 512): with a copy per page and
     // slab (2 KB) the copies took 5.5 us a tile. Lane j holds the pool row of
     // the tile's j-th K box and j-th V box.
-    const int k_boxes = kTok / p.k_box, v_boxes = C::VT / p.v_box;
+    const int v_boxes = C::VT / p.v_box;
     const uint64_t policy = p.keep_in_l2 ? l2_evict_normal_policy() : l2_evict_first_policy();
     constexpr int NR = C::FP8 ? C::NRAW : NST;
     constexpr int BYTES = C::FP8 ? kRaw : kStage;
@@ -275,16 +276,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       }
       return ((page * p.num_kv_heads + g) * p.page_size + tok % p.page_size) / 8;
     };
-    int st = 0, uses = 0;  // the next stage, and how many stages went out
+    int st = 0, uses = 0;  // the next stage, and how many stages were passed
+    int turn = warp - 9;   // stages until this warp's next
     uint32_t phase = 1;    // of the stage's release (the first round waits for nothing)
     bool ok = true;
+    // this warp's stage, free to be filled? (ok false: the wait ran out)
     auto begin = [&](int boxes, int box_bytes) {
+      if (turn != 0) return false;
       ok = __all_sync(kFullMask, uses < NR || mbar_wait(&freed[st], phase));
       if (ok && lane == 0) mbar_arrive_expect_tx(&land[st], boxes * box_bytes + p.stall_bytes);
       __syncwarp();
       return ok;
     };
     auto end = [&] {
+      turn = turn == 0 ? kCopyWarps - 1 : turn - 1;
       ++uses;
       if (++st == NR) {
         st = 0;
@@ -296,8 +301,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       const int boxes = __popc(__ballot_sync(kFullMask, at >= 0));
 #pragma unroll 1
       for (int s = 0; s < KS; ++s) {
-        if (!begin(boxes, bytes)) return;
-        if (at >= 0) tma_load_4d(ring + st * BYTES + lane * bytes, &p.kmap, 0, 0, s * K_SLABS, at, &land[st], policy);
+        if (begin(boxes, bytes) && at >= 0)
+          tma_load_4d(ring + st * BYTES + lane * bytes, &p.kmap, 0, 0, s * K_SLABS, at, &land[st], policy);
+        if (!ok) return;
         end();
       }
     };
@@ -306,9 +312,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
 #pragma unroll 1
       for (int s = 0; s < KS; ++s) {
         const bool mine = at >= 0 && lane / v_boxes == s;
-        if (!begin(__popc(__ballot_sync(kFullMask, mine)), bytes)) return;
-        if (mine)
+        if (begin(__popc(__ballot_sync(kFullMask, mine)), bytes) && mine)
           tma_load_4d(ring + st * BYTES + lane % v_boxes * bytes, &p.vmap, 0, 0, 0, at, &land[st], policy);
+        if (!ok) return;
         end();
       }
     };
@@ -327,7 +333,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     if (lane == 0) {
       const unsigned long long deadline = global_timer_ns() + kWaitTimeoutNs;
       for (int k = max(0, uses - NR); k < uses; ++k)
-        if (!mbar_wait_until(&land[k % NR], (k / NR) & 1, deadline)) ok = false;
+        if (k % kCopyWarps == warp - 9 && !mbar_wait_until(&land[k % NR], (k / NR) & 1, deadline)) ok = false;
       if (!ok) err |= kErrTimeout;
     }
     err = __reduce_or_sync(kFullMask, err);
@@ -670,7 +676,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     if (lane == 0 && err) atomicOr(p.err, err);
   } else if constexpr (C::FP8) {
     // ---- FP8: e4m3 stages widened to f16 operand stages, a thread per token row
-    const int row = tid - 320, sw = row & 7, total = 2 * KS * ntile;
+    const int row = tid - 32 * (9 + kCopyWarps), sw = row & 7, total = 2 * KS * ntile;
     bool ok = true;
     for (int it = 0; it < total; ++it) {
       const int st = it % NST, rs = it % C::NRAW;
