@@ -141,6 +141,8 @@ _lib = None
 def load_library(path: Optional[str] = None):
     """Load the CUDA library; raises if it has not been built."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -509,19 +511,26 @@ def paged_decode_combine(o_parts, lse_parts, out, stream=None) -> None:
 # Block tables and slot maps, the cache write by slot, shared-prefix decode
 # ----------------------------------------------------------------------------
 
-def _want(t, name: str, dtype, shape=None) -> None:
-    """A tensor handed to the library is contiguous and of the type (and shape) its C argument has."""
-    if t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor, got {t.dtype}"
-                         + ("" if t.is_contiguous() else " (not contiguous)"))
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+_torch_module = None
 
 
-def _same_device(first, **others) -> None:
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+def _refuse(name: str, t, dtype, shape) -> None:
+    raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {shape}, got {t.dtype} "
+                     f"{tuple(t.shape)}{'' if t.is_contiguous() else ' (not contiguous)'} on {t.device}")
+
+
+def _want(t, name: str, dtype, shape, device: int) -> None:
+    """A tensor handed to the library is contiguous, of the type and shape its C argument has, on the call's device."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        _refuse(name, t, dtype, shape)
 
 
 def paged_decode_append_slots_workspace(batch: int) -> int:
@@ -537,71 +546,68 @@ def paged_decode_append_slots(page_size: int, num_pages: int, cached_lens, new_t
     token_starts [B + 1], slot_map and positions (None: not wanted) [max_tokens]
     and free_range_out [2] are written. All int32; seq_lens may be cached_lens
     and free_range_out may be free_range."""
-    import torch
-    i32 = torch.int32
-    B = cached_lens.shape[0]
-    _want(cached_lens, "cached_lens", i32, (B,))
-    _want(new_tokens, "new_tokens", i32, (B,))
-    _want(free_pages, "free_pages", i32, (free_pages.numel(),))
-    _want(free_range, "free_range", i32, (2,))
-    _want(block_tables, "block_tables", i32, (B, block_tables.shape[-1]))
-    _want(seq_lens, "seq_lens", i32, (B,))
-    _want(token_starts, "token_starts", i32, (B + 1,))
-    _want(slot_map, "slot_map", i32, (slot_map.numel(),))
+    i32 = _torch().int32
+    dev, (B,), (n,), (free,) = cached_lens.get_device(), cached_lens.shape, slot_map.shape, free_pages.shape
+    width = block_tables.shape[-1]
+    _want(cached_lens, "cached_lens", i32, (B,), dev)
+    _want(new_tokens, "new_tokens", i32, (B,), dev)
+    _want(free_pages, "free_pages", i32, (free,), dev)
+    _want(free_range, "free_range", i32, (2,), dev)
+    _want(block_tables, "block_tables", i32, (B, width), dev)
+    _want(seq_lens, "seq_lens", i32, (B,), dev)
+    _want(token_starts, "token_starts", i32, (B + 1,), dev)
+    _want(slot_map, "slot_map", i32, (n,), dev)
     if positions is not None:
-        _want(positions, "positions", i32, tuple(slot_map.shape))
-    _want(free_range_out, "free_range_out", i32, (2,))
-    _same_device(cached_lens, new_tokens=new_tokens, free_pages=free_pages, free_range=free_range,
-                 block_tables=block_tables, seq_lens=seq_lens, token_starts=token_starts, slot_map=slot_map,
-                 positions=positions, free_range_out=free_range_out, device_flags=device_flags, workspace=workspace)
+        _want(positions, "positions", i32, (n,), dev)
+    _want(free_range_out, "free_range_out", i32, (2,), dev)
     st = load_library().paged_decode_append_slots(
-        int(B), int(page_size), int(num_pages), int(block_tables.shape[-1]), int(slot_map.numel()),
-        _ptr(cached_lens), _ptr(new_tokens), _ptr(free_pages), int(free_pages.numel()), _ptr(free_range),
-        _ptr(block_tables), _ptr(seq_lens), _ptr(token_starts), _ptr(slot_map), _ptr(positions),
-        _ptr(free_range_out), _ptr(device_flags), _ptr(workspace), int(workspace.numel() * workspace.element_size()),
-        _stream_ptr(stream))
-    _check(st, "paged_decode_append_slots")
+        B, page_size, num_pages, width, n, cached_lens.data_ptr(), new_tokens.data_ptr(), free_pages.data_ptr(), free,
+        free_range.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), token_starts.data_ptr(),
+        slot_map.data_ptr(), _ptr(positions), free_range_out.data_ptr(), device_flags.data_ptr(),
+        workspace.data_ptr(), workspace.nbytes, _stream_ptr(stream))
+    if st != PD_OK:
+        raise PagedDecodeError(st, "paged_decode_append_slots")
 
 
-def _token_rows(t, name: str, desc: LayerDesc, tokens: int) -> int:
+def _token_rows(t, name: str, dtype, shape, device: int) -> int:
     """The token stride (elements) of k / v rows [tokens, Hkv, d] whose heads are contiguous."""
-    import torch
-    if t.dtype != torch.bfloat16 or tuple(t.shape) != (tokens, desc.num_kv_heads, desc.head_dim):
-        raise ValueError(f"{name}: expected bf16 {(tokens, desc.num_kv_heads, desc.head_dim)}, "
-                         f"got {t.dtype} {tuple(t.shape)}")
-    if (desc.head_dim > 1 and t.stride(2) != 1) or (desc.num_kv_heads > 1 and t.stride(1) != desc.head_dim):
-        raise ValueError(f"{name}: a token's heads must be contiguous, strides {t.stride()}")
-    return t.stride(0) if tokens > 1 else max(t.stride(0), desc.num_kv_heads * desc.head_dim)
+    n, heads, d = shape
+    token, head, one = t.stride() if t.dim() == 3 else (0, 0, 0)
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or one != 1 or (heads > 1 and head != d):
+        raise ValueError(f"{name}: expected {dtype} {shape} with each token's heads contiguous, got {t.dtype} "
+                         f"{tuple(t.shape)}, strides {t.stride()} on {t.device}")
+    return token if n > 1 else max(token, heads * d)
 
 
 def _write_slots(fp8: bool, desc, k_in, v_in, slot_map, k_pool, v_pool, k_scale, v_scale, device_flags, stream):
-    import torch
-    n = slot_map.numel()
-    _want(slot_map, "slot_map", torch.int32)
+    torch = _torch()
+    (n,), dev, heads, d = slot_map.shape, slot_map.get_device(), desc.num_kv_heads, desc.head_dim
+    _want(slot_map, "slot_map", torch.int32, (n,), dev)
     pool_type = torch.uint8 if fp8 else torch.bfloat16
-    shape = (desc.num_pages, desc.num_kv_heads, desc.page_size, desc.head_dim)
-    _want(k_pool, "k_pool", pool_type, shape)
-    ks = _token_rows(k_in, "k_in", desc, n)
-    vs = 0
-    if not desc.kv_shared:
+    pool, rows = (desc.num_pages, heads, desc.page_size, d), (n, heads, d)
+    _want(k_pool, "k_pool", pool_type, pool, dev)
+    ks, vs = _token_rows(k_in, "k_in", torch.bfloat16, rows, dev), 0
+    if desc.kv_shared:
+        v_in = None
+    else:
         if v_in is None or v_pool is None:
             raise ValueError("a K != V layer needs v_in and v_pool")
-        _want(v_pool, "v_pool", pool_type, shape)
-        vs = _token_rows(v_in, "v_in", desc, n)
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if t is not None:
-            _want(t, name, torch.float32, shape[:2])
-    _same_device(k_in, v_in=v_in, slot_map=slot_map, k_pool=k_pool, v_pool=v_pool, k_scale=k_scale, v_scale=v_scale,
-                 device_flags=device_flags)
-    args = [ctypes.byref(desc), n, _ptr(k_in), _ptr(None if desc.kv_shared else v_in), ks, vs, _ptr(slot_map),
-            _ptr(k_pool), _ptr(v_pool)]
+        _want(v_pool, "v_pool", pool_type, pool, dev)
+        vs = _token_rows(v_in, "v_in", torch.bfloat16, rows, dev)
     lib = load_library()
     if fp8:
-        st = lib.paged_decode_write_slots_fp8(*args, _ptr(k_scale), _ptr(v_scale), _ptr(device_flags),
-                                              _stream_ptr(stream))
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is not None:
+                _want(t, name, torch.float32, pool[:2], dev)
+        st = lib.paged_decode_write_slots_fp8(ctypes.byref(desc), n, k_in.data_ptr(), _ptr(v_in), ks, vs,
+                                              slot_map.data_ptr(), k_pool.data_ptr(), _ptr(v_pool), _ptr(k_scale),
+                                              _ptr(v_scale), device_flags.data_ptr(), _stream_ptr(stream))
     else:
-        st = lib.paged_decode_write_slots(*args, _ptr(device_flags), _stream_ptr(stream))
-    _check(st, "paged_decode_write_slots_fp8" if fp8 else "paged_decode_write_slots")
+        st = lib.paged_decode_write_slots(ctypes.byref(desc), n, k_in.data_ptr(), _ptr(v_in), ks, vs,
+                                          slot_map.data_ptr(), k_pool.data_ptr(), _ptr(v_pool),
+                                          device_flags.data_ptr(), _stream_ptr(stream))
+    if st != PD_OK:
+        raise PagedDecodeError(st, "paged_decode_write_slots_fp8" if fp8 else "paged_decode_write_slots")
 
 
 def paged_decode_write_slots(desc: LayerDesc, k_in, v_in, slot_map, k_pool, v_pool, device_flags, stream=None) -> None:
@@ -682,6 +688,13 @@ class SharedPrefixStep:
         # zeroed once: the first word is the device error flag
         nbytes = int(self.plan.workspace_bytes)
         self.workspace = torch.zeros((nbytes + 255) // 256 * 256, dtype=torch.uint8, device=device)
+        # what each call's tensors have to look like
+        B, heads = self.plan.own.batch, (num_q_heads, head_dim)
+        T = self.query_tokens
+        self._q_shapes = ((B,) + heads if T == 1 else None, (B, T) + heads)
+        self._pool = (num_pages, num_kv_heads, page_size, head_dim)
+        self._prefix = (self.plan.num_groups, max_prefix_pages)
+        self._tables = (B, max_pages_per_seq)
 
     def __call__(self, q, k_pool, v_pool, prefix_tables, prefix_lens, group_starts, block_tables, seq_lens, scale, out,
                  stream=None, k_scale=None, v_scale=None):
@@ -697,27 +710,24 @@ class SharedPrefixStep:
 
     def _check_tensors(self, q, k_pool, v_pool, prefix_tables, prefix_lens, group_starts, block_tables, seq_lens, out,
                        k_scale, v_scale):
-        import torch
-        d, pl = self.desc, self.plan
-        B, T = pl.own.batch, self.query_tokens
-        heads = (d.num_q_heads, d.head_dim)
-        _want(q, "q", torch.bfloat16, ((B, T) if T > 1 or q.dim() == 4 else (B,)) + heads)
-        _want(out, "out", torch.bfloat16, tuple(q.shape))
-        pool = (d.num_pages, d.num_kv_heads, d.page_size, d.head_dim)
-        for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
-            if t is not None:
-                _want(t, name, torch.uint8 if self.fp8 else torch.bfloat16, pool)
-        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-            if t is not None:
-                _want(t, name, torch.float32, pool[:2])
-        _want(prefix_tables, "prefix_tables", torch.int32, (pl.num_groups, pl.max_prefix_pages))
-        _want(prefix_lens, "prefix_lens", torch.int32, (pl.num_groups,))
-        _want(group_starts, "group_starts", torch.int32, (pl.num_groups + 1,))
-        _want(block_tables, "block_tables", torch.int32, (B, d.max_pages_per_seq))
-        _want(seq_lens, "seq_lens", torch.int32, (B,))
-        _same_device(q, k_pool=k_pool, v_pool=v_pool, prefix_tables=prefix_tables, prefix_lens=prefix_lens,
-                     group_starts=group_starts, block_tables=block_tables, seq_lens=seq_lens, out=out,
-                     k_scale=k_scale, v_scale=v_scale)
+        torch = _torch()
+        i32, bf16, dev = torch.int32, torch.bfloat16, self.workspace.get_device()
+        pool_type = torch.uint8 if self.fp8 else bf16
+        shape = self._q_shapes[0] if q.dim() == 3 else self._q_shapes[1]
+        _want(q, "q", bf16, shape, dev)
+        _want(out, "out", bf16, shape, dev)
+        _want(k_pool, "k_pool", pool_type, self._pool, dev)
+        if v_pool is not None:
+            _want(v_pool, "v_pool", pool_type, self._pool, dev)
+        if self.fp8:
+            for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+                if t is not None:
+                    _want(t, name, torch.float32, self._pool[:2], dev)
+        _want(prefix_tables, "prefix_tables", i32, self._prefix, dev)
+        _want(prefix_lens, "prefix_lens", i32, self._prefix[:1], dev)
+        _want(group_starts, "group_starts", i32, (self._prefix[0] + 1,), dev)
+        _want(block_tables, "block_tables", i32, self._tables, dev)
+        _want(seq_lens, "seq_lens", i32, self._tables[:1], dev)
 
     def check(self, stream=None) -> int:
         return paged_decode_check_device_error(self.plan.own, self.workspace, stream)

@@ -9,9 +9,11 @@
 // entry p below ceil(c_b / P), else the free list's at first + p - ceil(c_b / P).
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "paged_decode.h"
+#include "pd_common.cuh"
 #include "pd_variants.h"
 
 namespace pd {
@@ -30,117 +32,220 @@ struct SlotParams {
   int32_t* positions;  // or null
   int32_t* free_range_out;
   uint32_t* flags;
-  int32_t* first_page;  // workspace [batch]: first free-list entry, or -1 for a request not served
-  int32_t* cached;      // workspace [batch]: cached_lens (which seq_lens may alias)
+  uint32_t* ticket;  // workspace: CTAs done reading (0 between calls)
+  bool wide;         // slot_map and positions take 16-byte stores
 };
 
-constexpr int kScanThreads = 1024;
+constexpr int kThreads = 1024;
 
-// Inclusive sum over the CTA's threads (warp shuffles, then the warps' sums).
-__device__ __forceinline__ long long cta_scan(long long x, long long* warp_sum) {
+// What a CTA knows of the 1024 requests of one round.
+struct Round {
+  int start[kThreads];   // first token (clamped to 31 bits)
+  int first[kThreads];   // first free-list entry, -1 for a request not served
+  int cached[kThreads];
+};
+
+struct Sums {
+  long long tokens, pages;
+};
+
+// Inclusive sums over the CTA's threads; `total` of all of them. One barrier:
+// every warp scans the 32 warps' sums itself. `scratch` must not be in use.
+__device__ __forceinline__ Sums cta_scan(Sums x, Sums* scratch, Sums& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const long long a = __shfl_up_sync(kFullMask, x.tokens, o), b = __shfl_up_sync(kFullMask, x.pages, o);
+    if (lane >= o) {
+      x.tokens += a;
+      x.pages += b;
+    }
   }
-  if (lane == 31) warp_sum[warp] = x;
+  if (lane == 31) scratch[warp] = x;
   __syncthreads();
-  long long before = 0;
-  for (int w = 0; w < warp; ++w) before += warp_sum[w];
-  __syncthreads();
-  return x + before;
+  Sums w = scratch[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long a = __shfl_up_sync(kFullMask, w.tokens, o), b = __shfl_up_sync(kFullMask, w.pages, o);
+    if (lane >= o) {
+      w.tokens += a;
+      w.pages += b;
+    }
+  }
+  total.tokens = __shfl_sync(kFullMask, w.tokens, 31);
+  total.pages = __shfl_sync(kFullMask, w.pages, 31);
+  const long long a = __shfl_sync(kFullMask, w.tokens, (warp + 31) & 31);
+  const long long b = __shfl_sync(kFullMask, w.pages, (warp + 31) & 31);
+  if (warp > 0) {
+    x.tokens += a;
+    x.pages += b;
+  }
+  return x;
 }
 
-__global__ void __launch_bounds__(kScanThreads) slots_scan_kernel(const SlotParams p) {
-  __shared__ long long warp_sum[32], total[2];
+// The slot and position of token t, which belongs to request b of the batch (entry r of the round).
+__device__ __forceinline__ void place(const SlotParams& p, const Round& rd, int r, int b, int t, int& slot, int& pos) {
+  slot = pos = -1;
+  const int first = rd.first[r];
+  if (first < 0) return;
+  const int c = rd.cached[r];
+  pos = c + t - rd.start[r];
+  const int held = (c + p.page_size - 1) / p.page_size, at = pos / p.page_size;
+  int32_t* entry = p.block_tables + (size_t)b * p.max_pages + at;
+  int page;
+  if (at < held) {
+    page = *entry;
+  } else {
+    // every new page begins with a new token, whose thread writes the table's entry
+    page = __ldg(p.free_pages + first + at - held);
+    if (pos == at * p.page_size) *entry = page;
+  }
+  if ((unsigned)page < (unsigned)p.num_pages) slot = page * p.page_size + (pos - at * p.page_size);
+  else atomicOr(p.flags, kErrBadPage);
+}
+
+// A CTA serves TPT * 1024 entries of slot_map, but scans the lengths of every
+// request up to its last token (at most a few rounds of 1024): with B requests
+// in L2 that costs less than a launch of its own for the sums. The lengths may
+// be updated in place, so they are written by the CTA that is last to have read
+// them (the only one, for a batch of few tokens).
+template <int TPT>
+__global__ void __launch_bounds__(kThreads) slots_kernel(const SlotParams p) {
+  __shared__ Round rd;
+  __shared__ Sums scratch[2][32];
+  __shared__ bool last;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int tid = threadIdx.x;
   const long long cap = (long long)p.max_pages * p.page_size;
   long long next = p.free_range[0], end = p.free_range[1];
   if (next < 0) next = 0;
   if (end > p.num_free) end = p.num_free;
   if (end < next) end = next;
-  const long long first_free = next;
-  long long tok_base = 0, page_base = next, taken = next;
-  uint32_t err = 0;
-  for (int b0 = 0; b0 < p.batch; b0 += kScanThreads) {
-    const int b = b0 + threadIdx.x;
-    long long c = 0, n = 0, need = 0;
-    bool ok = false;
-    if (b < p.batch) {
-      c = p.cached_lens[b];
-      n = p.new_tokens[b];
-      ok = c >= 0 && n >= 0 && c + n <= cap;
-      if (ok) need = (c + n + p.page_size - 1) / p.page_size - (c + p.page_size - 1) / p.page_size;
-      else if (n < 0 || n > cap) n = 0;
-    }
-    const long long tok_end = tok_base + cta_scan(n, warp_sum);
-    const long long page_end = page_base + cta_scan(need, warp_sum);
-    if (b < p.batch) {
-      if (!ok || tok_end > p.max_tokens) {
-        ok = false;
-        err |= kErrBadSeqLen;
-      } else if (need > 0 && page_end > end) {
-        ok = false;
-        err |= kErrNoPages;
-      }
-      p.first_page[b] = ok ? (int32_t)(page_end - need) : -1;
-      p.cached[b] = (int32_t)c;
-      p.seq_lens[b] = (int32_t)(ok ? c + n : c);
-      p.token_starts[b] = (int32_t)min(tok_end - n, 0x7fffffffLL);
-    }
-    const long long got = (b < p.batch && ok && need > 0) ? need : 0;
-    const long long sum = cta_scan(got, warp_sum);
-    if (threadIdx.x == kScanThreads - 1) {
-      total[0] = tok_end;
-      total[1] = page_end;
-      warp_sum[0] = sum;
-    }
-    __syncthreads();
-    tok_base = total[0];
-    page_base = total[1];
-    taken += warp_sum[0];
-    __syncthreads();
-  }
-  if (err) atomicOr(p.flags, err);
-  if (threadIdx.x == 0) {
-    p.token_starts[p.batch] = (int32_t)min(tok_base, 0x7fffffffLL);
-    p.free_range_out[0] = (int32_t)(p.batch > 0 ? taken : first_free);
-    p.free_range_out[1] = (int32_t)end;
-  }
-}
+  const bool only = gridDim.x == 1;
+  const long long t0 = (long long)blockIdx.x * (TPT * kThreads);
+  const long long t1 = min((long long)p.max_tokens, t0 + TPT * kThreads);
 
-// One thread per entry of slot_map; the thread of a new page's first token
-// (every new page begins with one) writes the page into the table.
-__global__ void __launch_bounds__(256) slots_fill_kernel(const SlotParams p) {
-  const int t = blockIdx.x * 256 + threadIdx.x;
-  if (t >= p.max_tokens) return;
-  int slot = -1, pos = -1;
-  if (p.batch > 0 && t < p.token_starts[p.batch]) {
-    int lo = 0, hi = p.batch;  // the last request that starts at or before t
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p.token_starts[mid] <= t) lo = mid;
-      else hi = mid;
-    }
-    const int first = p.first_page[lo];
-    if (first >= 0) {
-      const int c = p.cached[lo];
-      pos = c + t - p.token_starts[lo];
-      const int held = (c + p.page_size - 1) / p.page_size, at = pos / p.page_size;
-      int32_t* entry = p.block_tables + (size_t)lo * p.max_pages + at;
-      int page;
-      if (at < held) {
-        page = *entry;
-      } else {
-        page = p.free_pages[first + at - held];
-        if (pos == at * p.page_size) *entry = page;
+  // all requests in rounds of 1024: fill this CTA's entries, or (write) the results per request
+  auto walk = [&](bool fill, bool write) {
+    Sums base{0, next}, served{0, 0};
+    uint32_t err = 0;
+    int turn = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
+      const int b = b0 + tid;
+      long long c = 0, n = 0, need = 0;
+      bool ok = false;
+      if (b < p.batch) {
+        c = p.cached_lens[b];
+        n = p.new_tokens[b];
+        ok = c >= 0 && n >= 0 && c + n <= cap;
+        if (ok)
+          need = (unsigned)(c + n + p.page_size - 1) / (unsigned)p.page_size - (unsigned)(c + p.page_size - 1) / (unsigned)p.page_size;
+        else if (n < 0 || n > cap)
+          n = 0;
       }
-      if ((unsigned)page < (unsigned)p.num_pages) slot = page * p.page_size + (pos - at * p.page_size);
-      else atomicOr(p.flags, kErrBadPage);
+      Sums total;
+      const Sums in = cta_scan(Sums{n, need}, scratch[turn], total);
+      turn ^= 1;
+      const long long tok_end = base.tokens + in.tokens, page_end = base.pages + in.pages;
+      if (b < p.batch) {
+        if (!ok || tok_end > p.max_tokens) {
+          ok = false;
+          err |= kErrBadSeqLen;
+        } else if (need > 0 && page_end > end) {
+          ok = false;
+          err |= kErrNoPages;
+        }
+        if (ok && need > 0) served.pages = page_end;  // served requests that take pages come before all that cannot
+        if (write) {
+          p.seq_lens[b] = (int32_t)(ok ? c + n : c);
+          p.token_starts[b] = (int32_t)min(tok_end - n, 0x7fffffffLL);
+        }
+      }
+      if (fill) {
+        rd.start[tid] = (int)min(tok_end - n, 0x7fffffffLL);
+        rd.first[tid] = ok ? (int)(page_end - need) : -1;
+        rd.cached[tid] = (int)c;
+        __syncthreads();
+        const int in_round = min(kThreads, p.batch - b0);
+        const long long lo = max(t0, base.tokens), hi = min(t1, base.tokens + total.tokens);
+        const long long mine = t0 + (long long)tid * TPT;
+        if (mine < hi && mine + TPT > lo) {
+          // the last request of the round that starts at or before the first of this thread's tokens
+          int t = (int)max(mine, lo);
+          int a = 0, z = in_round;
+          while (z - a > 1) {
+            const int mid = (a + z) >> 1;
+            if (rd.start[mid] <= t) a = mid;
+            else z = mid;
+          }
+          int slot[TPT], pos[TPT];
+#pragma unroll
+          for (int k = 0; k < TPT; ++k) {
+            const long long tk = mine + k;
+            slot[k] = pos[k] = -1;
+            if (tk < lo || tk >= hi) continue;
+            while (a + 1 < in_round && rd.start[a + 1] <= (int)tk) ++a;
+            place(p, rd, a, b0 + a, (int)tk, slot[k], pos[k]);
+          }
+          if (TPT == 4 && p.wide && mine >= lo && mine + TPT <= hi) {
+            *reinterpret_cast<int4*>(p.slot_map + mine) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+            if (p.positions) *reinterpret_cast<int4*>(p.positions + mine) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < TPT; ++k) {
+              if (mine + k < lo || mine + k >= hi) continue;
+              p.slot_map[mine + k] = slot[k];
+              if (p.positions) p.positions[mine + k] = pos[k];
+            }
+          }
+        }
+        __syncthreads();
+      }
+      base.tokens += total.tokens;
+      base.pages += total.pages;
+      if (!write && base.tokens >= t1) break;
     }
+    if (fill)  // padding behind the last new token
+      for (long long t = max(t0, base.tokens) + tid; t < t1; t += kThreads) {
+        p.slot_map[t] = -1;
+        if (p.positions) p.positions[t] = -1;
+      }
+    if (write) {
+      if (err) atomicOr(p.flags, err);
+      // the end of the pages taken: the largest of the threads'
+      __syncthreads();
+      const Sums mine{0, max(served.pages, next)};
+      long long m = mine.pages;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) m = max(m, __shfl_xor_sync(kFullMask, m, o));
+      if ((tid & 31) == 0) scratch[0][tid >> 5].pages = m;
+      __syncthreads();
+      if (tid < 32) {
+        m = scratch[0][tid].pages;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = max(m, __shfl_xor_sync(kFullMask, m, o));
+        if (tid == 0) {
+          p.token_starts[p.batch] = (int32_t)min(base.tokens, 0x7fffffffLL);
+          p.free_range_out[0] = (int32_t)m;
+          p.free_range_out[1] = (int32_t)end;
+        }
+      }
+    }
+  };
+  if (only) {
+    walk(true, true);
+    return;
   }
-  p.slot_map[t] = slot;
-  if (p.positions) p.positions[t] = pos;
+  walk(true, false);
+  __syncthreads();
+  if (tid == 0) {
+    __threadfence();
+    last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
+    if (last) *p.ticket = 0;
+  }
+  __syncthreads();
+  if (last) walk(false, true);
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -151,8 +256,8 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 extern "C" {
 
 size_t paged_decode_append_slots_workspace(int32_t batch) {
-  const size_t n = batch > 0 ? (size_t)batch : 0;
-  return (256 + n * 8 + 255) / 256 * 256;
+  (void)batch;  // a counter, whatever the batch
+  return 256;
 }
 
 pd_status paged_decode_append_slots(int32_t batch, int32_t page_size, int32_t num_pages, int32_t max_pages,
@@ -193,12 +298,25 @@ pd_status paged_decode_append_slots(int32_t batch, int32_t page_size, int32_t nu
   p.positions = positions;
   p.free_range_out = free_range_out;
   p.flags = device_flags;
-  p.first_page = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + 256);
-  p.cached = p.first_page + batch;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  pd::slots_scan_kernel<<<1, pd::kScanThreads, 0, s>>>(p);
-  if (max_tokens > 0) pd::slots_fill_kernel<<<(max_tokens + 255) / 256, 256, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? PD_OK : PD_ERR_CUDA;
+  p.ticket = static_cast<uint32_t*>(workspace);
+  p.wide = pd::aligned(slot_map, 16) && pd::aligned(positions, 16);
+  // one entry a thread while a few CTAs hold them all (a decode step: one CTA,
+  // no counter), four (16-byte stores) from 16384 on
+  const int per_thread = max_tokens >= 16384 ? 4 : 1;
+  const long long per_cta = (long long)per_thread * pd::kThreads;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::max<long long>(1, (max_tokens + per_cta - 1) / per_cta));
+  cfg.blockDim = dim3(pd::kThreads);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = per_thread == 4 ? cudaLaunchKernelEx(&cfg, pd::slots_kernel<4>, p)
+                                        : cudaLaunchKernelEx(&cfg, pd::slots_kernel<1>, p);
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  return e == cudaSuccess ? PD_OK : PD_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -1,8 +1,10 @@
 // The cache write of any number of tokens by slot (sm_103a): k / v rows copied
 // into the pages their slots name, or quantised to e4m3 under the pages' scales.
 //
-// Bound: HBM, every row read and written once. One thread moves 16 bf16 values
-// (two 16-byte loads; two 16-byte stores, or one of e4m3 codes).
+// Bound: HBM, every row read and written once. A CTA takes a run of tokens of K
+// or of V: their rows' places in the pool are worked out once per token, then
+// every thread moves the same 16 bf16 (8 for a bf16 cache) of each token, eight
+// tokens' loads in flight.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -23,11 +25,13 @@ struct WriteParams {
   const float* scale[2];  // FP8
   const int32_t* slot_map;
   uint32_t* flags;
-  int num_tokens, heads, dim, page_size;
+  int num_tokens, heads, dim, page_size, run;
   long long num_slots;
 };
 
 constexpr int kWriteThreads = 256;
+constexpr int kMaxRun = 16;  // tokens of a CTA
+constexpr int kAhead = 8;    // tokens a thread has in flight
 
 // Two fp32 quotients -> two e4m3 codes (low byte the first), to nearest even, clamped to +-448.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
@@ -36,44 +40,78 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t e4m3x4(uint32_t a, uint32_t b, float s) {
+  return e4m3x2(__fdiv_rn(__uint_as_float(a << 16), s), __fdiv_rn(__uint_as_float(a & 0xffff0000u), s)) |
+         e4m3x2(__fdiv_rn(__uint_as_float(b << 16), s), __fdiv_rn(__uint_as_float(b & 0xffff0000u), s)) << 16;
+}
+
+// Rows are read once: keep them out of L1.
+__device__ __forceinline__ uint4 load_once(const uint16_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 template <bool FP8>
-__global__ void __launch_bounds__(kWriteThreads) write_slots_kernel(const WriteParams p) {
+__global__ void __launch_bounds__(kWriteThreads) write_slots_kernel(const __grid_constant__ WriteParams p) {
+  __shared__ long long place[kMaxRun];  // first element of the token's first head in the pool, -1: not written
+  __shared__ int page_of[kMaxRun];
+  constexpr int ELEMS = FP8 ? 16 : 8;  // of a thread and token
   grid_dependency_wait();
   grid_launch_dependents();
-  const int which = blockIdx.y;
-  const int per_row = p.dim / 16, per_token = p.heads * per_row;
-  const long long n = (long long)p.num_tokens * per_token;
-  for (long long e = blockIdx.x * (long long)kWriteThreads + threadIdx.x; e < n;
-       e += (long long)gridDim.x * kWriteThreads) {
-    const int t = (int)(e / per_token), c = (int)(e % per_token);
-    const int h = c / per_row, d = (c % per_row) * 16;
-    const int slot = p.slot_map[t];
-    if (slot < 0 || slot >= p.num_slots) {
-      if (slot != -1 && c == 0) atomicOr(p.flags, kErrBadPage);
-      continue;
+  const int tid = threadIdx.x;
+  const bool v = blockIdx.y != 0;
+  const int first = blockIdx.x * p.run, run = min(p.run, p.num_tokens - first);
+  if (tid < run) {
+    const int slot = __ldg(p.slot_map + first + tid);
+    place[tid] = -1;
+    if (slot >= 0 && slot < p.num_slots) {
+      const int page = slot / p.page_size;
+      page_of[tid] = page;
+      place[tid] = ((long long)page * p.heads * p.page_size + (slot - page * p.page_size)) * p.dim;
+    } else if (slot != -1) {
+      atomicOr(p.flags, kErrBadPage);
     }
-    const int page = slot / p.page_size, off = slot - page * p.page_size;
-    const uint4* src = reinterpret_cast<const uint4*>(p.in[which] + t * p.stride[which] + h * p.dim + d);
-    const uint4 a = src[0], b = src[1];
-    const size_t at = (((size_t)page * p.heads + h) * p.page_size + off) * p.dim + d;
-    if constexpr (FP8) {
-      const float s = p.scale[which][(size_t)page * p.heads + h];
-      float x[8], y[8];
-      unpack_bf16x8(a, x);
-      unpack_bf16x8(b, y);
-      uint32_t w[4];
+  }
+  __syncthreads();
+  const uint16_t* in = v ? p.in[1] : p.in[0];
+  const int64_t stride = v ? p.stride[1] : p.stride[0];
+  uint8_t* pool = v ? p.pool[1] : p.pool[0];
+  const float* scale = v ? p.scale[1] : p.scale[0];
+  // `lanes` threads share a token; narrow rows leave a CTA room for several at a time
+  const int per_row = p.dim / ELEMS, per_token = p.heads * per_row;
+  const int lanes = min(per_token, kWriteThreads), together = kWriteThreads / lanes;
+  const int sub = tid / lanes;
+  if (sub >= together) return;
+  for (int c = tid - sub * lanes; c < per_token; c += lanes) {
+    const int h = c / per_row;
+    const uint16_t* src = in + (int64_t)first * stride + c * ELEMS;
+    const long long to = (long long)h * (p.page_size - 1) * p.dim + (long long)c * ELEMS;  // h P d + (c mod row) ELEMS
+    for (int t0 = sub; t0 < run; t0 += together * kAhead) {
+      uint4 a[kAhead], b[kAhead];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        w[i] = e4m3x2(__fdiv_rn(x[4 * i], s), __fdiv_rn(x[4 * i + 1], s)) |
-               e4m3x2(__fdiv_rn(x[4 * i + 2], s), __fdiv_rn(x[4 * i + 3], s)) << 16;
-        w[2 + i] = e4m3x2(__fdiv_rn(y[4 * i], s), __fdiv_rn(y[4 * i + 1], s)) |
-                   e4m3x2(__fdiv_rn(y[4 * i + 2], s), __fdiv_rn(y[4 * i + 3], s)) << 16;
+      for (int k = 0; k < kAhead; ++k) {
+        const int t = t0 + k * together;
+        if (t < run && place[t] >= 0) {
+          a[k] = load_once(src + t * stride);
+          if constexpr (FP8) b[k] = load_once(src + t * stride + 8);
+        }
       }
-      *reinterpret_cast<uint4*>(p.pool[which] + at) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-      uint4* dst = reinterpret_cast<uint4*>(p.pool[which] + at * 2);
-      dst[0] = a;
-      dst[1] = b;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int t = t0 + k * together;
+        if (t >= run || place[t] < 0) continue;
+        const long long at = place[t] + to;
+        if constexpr (FP8) {
+          const float s = __ldg(scale + (size_t)page_of[t] * p.heads + h);
+          *reinterpret_cast<uint4*>(pool + at) = make_uint4(e4m3x4(a[k].x, a[k].y, s), e4m3x4(a[k].z, a[k].w, s),
+                                                            e4m3x4(b[k].x, b[k].y, s), e4m3x4(b[k].z, b[k].w, s));
+        } else {
+          *reinterpret_cast<uint4*>(pool + at * 2) = a[k];
+        }
+      }
     }
   }
 }
@@ -123,10 +161,12 @@ pd_status write_slots(const pd_layer_desc* layer, bool fp8, int32_t num_tokens, 
   p.dim = ly.head_dim;
   p.page_size = ly.page_size;
   p.num_slots = slots;
-  const long long n = (long long)num_tokens * (row / 16);
-  const long long want = (n + kWriteThreads - 1) / kWriteThreads;
+  // runs of up to 16 tokens, shorter while that leaves SMs without a CTA (a
+  // decode step's 64 tokens: a CTA each)
+  p.run = kMaxRun;
+  while (p.run > 1 && (long long)num_tokens < 304ll * p.run) p.run /= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(want < (1 << 20) ? want : (1 << 20)), kvs ? 1 : 2);
+  cfg.gridDim = dim3((unsigned)((num_tokens + p.run - 1) / p.run), kvs ? 1 : 2);
   cfg.blockDim = dim3(kWriteThreads);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
