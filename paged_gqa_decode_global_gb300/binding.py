@@ -222,6 +222,17 @@ def status_string(status: int) -> str:
         return f"status {status}"
 
 
+_torch_module = None
+
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
 def _ptr(t) -> Optional[int]:
     if t is None:
         return None
@@ -232,7 +243,10 @@ def _ptr(t) -> Optional[int]:
 
 def _stream_ptr(stream) -> Optional[int]:
     if stream is None:
-        import torch
+        torch = _torch()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the same without a Stream object
+        if raw is not None:
+            return raw(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -510,17 +524,6 @@ def paged_decode_combine(o_parts, lse_parts, out, stream=None) -> None:
 # ----------------------------------------------------------------------------
 # Block tables and slot maps, the cache write by slot, shared-prefix decode
 # ----------------------------------------------------------------------------
-
-_torch_module = None
-
-
-def _torch():
-    global _torch_module
-    if _torch_module is None:
-        import torch
-        _torch_module = torch
-    return _torch_module
-
 
 def _refuse(name: str, t, dtype, shape) -> None:
     raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {shape}, got {t.dtype} "

@@ -220,7 +220,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = *tmem_at;
-  grid_dependency_wait();
+  // launched behind the own part's stage 1, whose threads let this grid start
+  // only after their own wait: all that both read is in place, and nothing here
+  // depends on stage 1 itself, so this grid waits for it only as it ends (the
+  // join behind it relies on both)
   grid_launch_dependents();
 
   const int piece = blockIdx.y, g = blockIdx.z;
@@ -712,6 +715,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
   tmem_fence_before();
   __syncthreads();
   if (warp == 8) tmem_dealloc(tmem, C::TMEM_COLS);
+  grid_dependency_wait();
 }
 
 #define PD_FOR_EACH_PREFIX(X)                                                                          \

@@ -308,13 +308,14 @@ pd_status decode_shared(const pd_shared_plan* plan, bool fp8, const void* q, con
   if (st == PD_OK) st = encode_group_map(&p.kmap, k_pool, ly, p.k_box, fp8 ? 1 : 2);
   if (st == PD_OK) st = encode_group_map(&p.vmap, ly.kv_shared ? k_pool : v_pool, ly, p.v_box, slabs);
   if (st != PD_OK) return st;
+  // the own part first: the prefix pass starts on the SMs it leaves free
+  st = launch_own_part(&own, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens, scale, workspace,
+                       workspace_bytes, out, stream);
+  if (st != PD_OK) return st;
   void* args[] = {&p};
   if (plan->tiles > 0 && launch_dependent(fn, dim3(plan->tiles, plan->num_pieces, ly.num_kv_heads), v.threads,
                                           v.smem_bytes, stream, args) != cudaSuccess)
     return PD_ERR_CUDA;
-  st = launch_own_part(&own, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens, scale, workspace,
-                       workspace_bytes, out, stream);
-  if (st != PD_OK) return st;
   JoinParams j = {};
   j.lse[0] = reinterpret_cast<const float*>(ws + own.lse_offset);
   j.o[0] = reinterpret_cast<const float*>(ws + own.opart_offset);
