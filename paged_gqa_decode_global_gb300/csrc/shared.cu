@@ -173,6 +173,75 @@ bool shared_plan_is_valid(const pd_shared_plan* plan) {
   return true;
 }
 
+// What the cost model takes of the prefix pass, in microseconds on a 152-SM
+// GB300: a CTA's start and end, and a tile of 128 tokens (measured at head_dim
+// 512 with few CTAs, in proportion to head_dim); the tiles in flight share the
+// memory's rate, and the pieces' partial results are written and read once.
+constexpr double kFixedUs = 9.0, kTileUs = 3.4, kTileFp8Us = 5.0, kHbmBytesPerUs = 6.8e6, kPartialBytesPerUs = 5.0e6;
+
+double tile_us(const pd_layer_desc& ly) {
+  return (ly.kv_dtype == PD_KV_FP8_E4M3 ? kTileFp8Us : kTileUs) * ly.head_dim / 512.0;
+}
+
+// The prefix's pieces: of every count of pieces for the longest prefix, the one
+// whose launch is modelled to end first. More pieces fill the SMs and even out
+// prefixes of different lengths; each costs a CTA's fixed time and its partials.
+void plan_pieces(pd_shared_plan& sp, const int32_t* starts, const int32_t* lens, int per_req, int sm_count) {
+  const pd_layer_desc& ly = sp.own.layer;
+  const long long most = ((long long)sp.max_prefix_len + kPrefixTile - 1) / kPrefixTile;
+  sp.chunk_tokens = kPrefixTile;
+  sp.num_pieces = 1;
+  if (most <= 1) return;
+  const double cta_us = tile_us(ly);
+  const double tile_bytes = (double)kPrefixTile * ly.head_dim * (ly.kv_dtype == PD_KV_FP8_E4M3 ? 1 : 2) *
+                            (ly.kv_shared ? 1 : 2);
+  const double rows = (double)sp.own.batch * sp.own.query_tokens * ly.num_q_heads;
+  double best = 1e300;
+  for (long long pieces = 1; pieces <= std::min<long long>(most, 1024); ++pieces) {
+    const long long c = (most + pieces - 1) / pieces;
+    if ((most + c - 1) / c != pieces) continue;  // the same cut as fewer pieces
+    double ctas = 0, tiles = 0, distinct = 0;
+    for (int n = 0; n < sp.num_groups; ++n) {
+      const long long row_tiles = ((long long)(starts[n + 1] - starts[n]) * per_req + sp.row_tile - 1) / sp.row_tile;
+      const long long len = (lens[n] + kPrefixTile - 1) / kPrefixTile;
+      ctas += (double)row_tiles * ly.num_kv_heads * ((len + c - 1) / c);
+      tiles += (double)row_tiles * ly.num_kv_heads * len;
+      if (row_tiles > 0) distinct += (double)ly.num_kv_heads * len;
+    }
+    const double one = kFixedUs + c * cta_us;
+    const double all = (ctas * kFixedUs + tiles * cta_us) / sm_count;
+    // within one wave the longest CTA; beyond, the mean load and part of a last one
+    double us = ctas <= sm_count ? one : std::max(one, all + 0.4 * one);
+    us = std::max(us, kFixedUs + distinct * tile_bytes / kHbmBytesPerUs) +
+         2.0 * rows * pieces * ly.head_dim * 4.0 / kPartialBytesPerUs;
+    if (us < best) {
+      best = us;
+      sp.chunk_tokens = (int32_t)(c * kPrefixTile);
+      sp.num_pieces = (int32_t)pieces;
+    }
+  }
+}
+
+// Alone, the own part would be cut to fill the SMs; beside the prefix pass,
+// whose CTAs take every SM it leaves free, each further CTA only adds its fixed
+// time. So its pieces grow to what a prefix CTA takes.
+void shorten_own(pd_shared_plan& sp, const int32_t* lens) {
+  pd_plan& own = sp.own;
+  const pd_layer_desc& ly = own.layer;
+  int longest = 0;
+  for (int b = 0; b < own.batch; ++b) longest = std::max(longest, lens[b]);
+  if (own.num_splits <= 1 || longest <= 0 || sp.max_prefix_len == 0) return;
+  const double us = kFixedUs + sp.chunk_tokens / kPrefixTile * tile_us(ly);
+  const double per_us = 50.0 * 512 / ly.head_dim;  // tokens of a lone stage-1 CTA
+  const int chunk = std::max(own.chunk_tokens, (int)(us * per_us) / 64 * 64);
+  own.chunk_tokens = std::min(chunk, (longest + 63) / 64 * 64);
+  own.num_splits = (longest + own.chunk_tokens - 1) / own.chunk_tokens;
+  own.grid_x = own.num_splits;
+  const uint64_t rows = (uint64_t)own.batch * own.query_tokens * ly.num_q_heads;
+  own.opart_offset = align_up(own.lse_offset + rows * own.num_splits * 4ull, 256);
+  own.workspace_bytes = own.opart_offset + rows * own.num_splits * (uint64_t)ly.head_dim * 4ull;
+}
+
 pd_status plan_shared(const pd_layer_desc* layer, int32_t batch, int32_t query_tokens, const int32_t* seq_lens_host,
                       int32_t num_groups, const int32_t* group_starts_host, const int32_t* prefix_lens_host,
                       int32_t max_prefix_pages, int32_t sm_count, pd_shared_plan* plan) {
@@ -211,12 +280,8 @@ pd_status plan_shared(const pd_layer_desc* layer, int32_t batch, int32_t query_t
     tiles += ((long long)(group_starts_host[n + 1] - group_starts_host[n]) * per_req + sp.row_tile - 1) / sp.row_tile;
   if (tiles > 65535) return PD_ERR_UNSUPPORTED;
   sp.tiles = (int32_t)tiles;
-  // one wave of CTAs, pieces of whole tiles
-  const long long units = std::max<long long>(1, tiles * ly.num_kv_heads);
-  const long long pieces = std::max<long long>(1, sm_count / units);
-  const long long want = align_up((uint64_t)std::max<long long>(1, (longest + pieces - 1) / pieces), kPrefixTile);
-  sp.chunk_tokens = (int32_t)want;
-  sp.num_pieces = (int32_t)std::max<long long>(1, (longest + want - 1) / want);
+  plan_pieces(sp, group_starts_host, prefix_lens_host, per_req, sm_count);
+  shorten_own(sp, seq_lens_host);
   const uint64_t rows = (uint64_t)batch * query_tokens * ly.num_q_heads;
   if (rows > 0x7fffffffull) return PD_ERR_UNSUPPORTED;
   sp.lse_offset = align_up(sp.own.workspace_bytes, 256);

@@ -3,8 +3,8 @@
 //
 // Bound: HBM, every row read and written once. A CTA takes a run of tokens of K
 // or of V: their rows' places in the pool are worked out once per token, then
-// every thread moves the same 16 bf16 (8 for a bf16 cache) of each token, eight
-// tokens' loads in flight.
+// every thread moves the same 16 bf16 (8 for a bf16 cache) of each token, 128
+// bytes of loads in flight.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -31,7 +31,6 @@ struct WriteParams {
 
 constexpr int kWriteThreads = 256;
 constexpr int kMaxRun = 16;  // tokens of a CTA
-constexpr int kAhead = 8;    // tokens a thread has in flight
 
 // Two fp32 quotients -> two e4m3 codes (low byte the first), to nearest even, clamped to +-448.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
@@ -94,6 +93,7 @@ __global__ void __launch_bounds__(kWriteThreads) write_slots_kernel(const __grid
   __shared__ long long place[kMaxRun];  // first element of the token's first head in the pool, -1: not written
   __shared__ int page_of[kMaxRun];
   constexpr int ELEMS = FP8 ? 16 : 8;  // of a thread and token
+  constexpr int kAhead = FP8 ? 4 : 8;  // tokens a thread has in flight: 128 bytes of loads
   grid_dependency_wait();
   grid_launch_dependents();
   const int tid = threadIdx.x;
