@@ -3,35 +3,46 @@
 // tile.
 //
 // Mathematics, for one (piece of the prefix, KV head, tile of N query rows),
-// 128 tokens at a time, with the query rows on the N side of both products:
-//   S^T[128 x N]  = K[128 x d] . q^T          (tokens on the M side)
-//   P^T           = 2^(S^T scale log2 e - ref)  ref: each row's reference maximum
-//   O^T[d x N]   += V^T[d x 128] . P^T        (head dims on the M side, 128 at a time)
+// a tile of tokens at a time, with the query rows on the N side of both products:
+//   S^T[tokens x N] = K[tokens x d] . q^T          (tokens on the M side)
+//   P^T             = 2^(S^T scale log2 e - ref)   ref: each row's reference
+//   O^T[d x N]     += V^T[d x tokens] . P^T        (head dims on the M side, 128 at a time)
 // A query row is a column of both accumulators, so N = 16 rows cost what they
-// need and d = 512 leaves room: O^T takes (d / 128) N columns of tensor memory
-// (256 at N = 64), S^T two buffers of N. The sum of a row's probabilities is
-// kept per token lane in registers and reduced once at the end. The reference
-// of a row moves only when a score exceeds it by 2^8 (it then jumps to the true
-// maximum and the row's O^T and sum are rescaled): any reference within range
-// gives the same quotient, p <= 256 loses nothing in fp32 or bf16, and the
-// rescale of O^T, a round trip through registers, becomes rare. Each row's
-// references depend on its own scores only.
+// need and d = 512 leaves room in tensor memory. The sum of a row's
+// probabilities is kept per token lane in registers and reduced once at the end.
+//
+// References: any reference in range gives the same quotient, and fp32 sums and
+// bf16 operands lose nothing while scores stay below 2^60 over it (FP8's f16
+// operands: 2^12). So a row keeps the maximum of the tile that set its
+// reference until a score leaves that range. The tile's P is then not used:
+// the rows that left take the tile's true maximum, their sums and O^T are
+// rescaled, and P is written again. The matrix warp, which sees every P before
+// its product, gives the verdict, so the softmax warps need no barrier of their
+// own per tile. Each row's references depend on its own scores only.
+//
+// One CTA (CT = 1): tiles of 128 tokens, N <= 64 at d = 512 (O^T takes 4 N
+// columns of tensor memory, S^T two buffers of N), 128 below. There the matrix
+// instruction is bound by its A operand (M = 128, N = 64: 55 cycles against 64
+// at N = 128) and the SM by the bytes it takes in. A pair of CTAs (CT = 2, d =
+// 512, 128 rows): tiles of 256 tokens, each CTA the scores of its 128 tokens
+// and half of the head dims; every byte of K and V then serves twice the rows
+// per SM. The token lanes' probabilities of rows 64 wg .. + 63 go to the CTA of
+// rank wg, which holds that half of the B operand.
 //
 // Roles: warps 0-7 softmax and epilogue (a thread per token lane, two
-// warpgroups with half the rows each: with one, its ~1700 instructions a tile
-// at one warp per scheduler took 5 us against 1.9 us of products), warp 8 the
-// matrix instructions, warps 9-11 the copies (every third stage each: a lone
-// warp spends ~60 cycles a copy); FP8: warps 12-15 widen the e4m3 stages to f16 operands. K and V arrive as [8-token group][64-dim slab][8][128 B]
-// atoms with the 128-byte swizzle: K-major for the first product, and the same
-// layout read M-major for the second, so nothing is transposed; P is written N-major,
-// a token's row at a time. A K=V layer fetches the tile again for its second
-// use (an L2 hit).
+// warpgroups with half the rows each), warp 8 the matrix instructions, warps
+// 9-11 the copies (every third stage each: a lone warp spends ~60 cycles a
+// copy); FP8: warps 12-15 widen the e4m3 stages to f16 operands. K and V arrive
+// as [8-token group][64-dim slab][8][128 B] atoms with the 128-byte swizzle:
+// K-major for the first product, and the same layout read M-major for the
+// second, so nothing is transposed; P is written N-major, a token's row at a
+// time. A K=V layer fetches the tile again for its second use (an L2 hit).
 //
 // Roundings: P to the operands' type. bf16 cache: bf16, 2^-9 a probability. FP8
 // cache: f16, into which e4m3 widens exactly; q rounds to f16 once (as in the
-// decode), and P carries the page's V scale over the piece's largest, so that it
-// stays below 2^8: 2^-12 a probability, 2^-25 absolute below 2^-14. Sums,
-// references and accumulators stay in fp32.
+// decode), and P carries the page's V scale over the piece's largest: 2^-12 a
+// probability, 2^-25 absolute below 2^-14. Sums, references and accumulators
+// stay in fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -48,17 +59,22 @@ constexpr int kStage = kTok * 256;         // an operand stage: 128 dims of 128 
 constexpr int kRaw = kStage / 2;           // FP8: the same in e4m3
 constexpr int kBody = 224 * 1024;          // query rows, probabilities and rings
 constexpr int kCopyWarps = 3;              // warps 9..11 (12 or 16 warps keep 168 or 128 registers a thread)
-constexpr float kSlack = 8.f;              // log2 of what a probability may exceed 1 by
+constexpr int kSoftWarps = 8;
 constexpr float kLow = 3e38f;              // negated reference of a row without a score yet
 constexpr int kNoTop = (int)0x807fffff;    // ordered(-inf)
 
-template <int D_, int N_, bool FP8_>
+template <int D_, int N_, bool FP8_, int CT_>
 struct PrefixCfg {
-  static constexpr int D = D_, N = N_;
+  static constexpr int D = D_, N = N_, CT = CT_;
   static constexpr bool FP8 = FP8_;
-  static constexpr int KS = D / 128;       // stages of a tile's K (and of its V)
-  static constexpr int VT = kTok / KS;     // tokens of a V stage
-  static constexpr int Q_BYTES = N * D * 2, P_BYTES = N * kTok * 2;
+  static constexpr float SLACK = FP8 ? 12.f : 60.f;  // log2 of what a probability may exceed 1 by
+  static constexpr int TT = kTok * CT;     // tokens of a tile
+  static constexpr int KS = D / 128;       // stages of a tile's K (and of its V) in a CTA
+  static constexpr int VT = TT / KS;       // tokens of a V stage
+  static constexpr int MC = D / 128 / CT;  // 128-dim chunks of O^T in a CTA
+  static constexpr int V_ATOMS = D / 64 / CT;  // 64-dim slabs of V in a CTA
+  static constexpr int QN = N / CT;        // query rows whose operands a CTA holds
+  static constexpr int Q_BYTES = QN * D * 2, P_BYTES = QN * TT * 2;
   static constexpr int ROOM = kBody - Q_BYTES - P_BYTES;
   static constexpr int NST = FP8 ? 3 : (ROOM / kStage < 6 ? ROOM / kStage : 6);
   static constexpr int NRAW = FP8 ? ((ROOM - NST * kStage) / kRaw < 6 ? (ROOM - NST * kStage) / kRaw : 6) : 0;
@@ -68,21 +84,25 @@ struct PrefixCfg {
   static constexpr int TOP_OFFSET = REF_OFFSET + N * 4;         // int top[N]: a tile's true maxima
   static constexpr int ROW_OFFSET = TOP_OFFSET + N * 4;         // int row[N]: a tile row's row of q and out
   static constexpr int BAR_OFFSET = ROW_OFFSET + N * 4;
-  static constexpr int NBAR = 2 * NST + 2 * NRAW + 2 + 2 + 1 + 1 + 1 + 1;
-  static constexpr int TMEM_OFFSET = BAR_OFFSET + NBAR * 8;
+  static constexpr int NBAR = 2 * NST + 2 * NRAW + 2 + 1 + 1 + 1 + 1 + 1 + 2;
+  static constexpr int TMEM_OFFSET = BAR_OFFSET + NBAR * 8;     // tensor memory address, left, verdict
   static constexpr int SMEM_BYTES = TMEM_OFFSET + 16 + 1024;
-  static constexpr int THREADS = 32 * (9 + kCopyWarps + (FP8 ? 4 : 0));
+  static constexpr int THREADS = 32 * (kSoftWarps + 1 + kCopyWarps + (FP8 ? 4 : 0));
   static constexpr int CW = N / 2;         // rows of a softmax warpgroup
   static constexpr int LD = CW < 32 ? CW : 32;
-  // P: [N / 64 blocks][128 tokens][row of up to 64 query rows], swizzled over the row
-  static constexpr int P_ROW = N >= 64 ? 128 : N * 2;
-  static constexpr int O_COLS = KS * N;
+  // P: [QN / 64 blocks][TT tokens][row of up to 64 query rows], swizzled over the row
+  static constexpr int P_ROW = QN >= 64 ? 128 : QN * 2;
+  // after the last product, in the ring: the rows' sums (per warpgroup [128][CW + 1], [128]), then [2][N] totals
+  static constexpr int SUM_FLOATS = kTok * (CW + 1) + 128;
+  static constexpr int TOTAL_OFFSET = RING_OFFSET + 2 * SUM_FLOATS * 4;
+  static constexpr int O_COLS = MC * N;
   static constexpr int TMEM_COLS = O_COLS + 2 * N <= 64 ? 64 : O_COLS + 2 * N <= 128 ? 128 :
                                    O_COLS + 2 * N <= 256 ? 256 : 512;
+  static_assert(CT == 1 || (D == 512 && N == 128), "a pair serves 128 rows at head_dim 512");
   static_assert(O_COLS + 2 * N <= 512, "tensor memory");
   static_assert(NST >= 3 && (!FP8 || NRAW >= 2), "rings");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
-  static_assert(2 * (kTok * (CW + 1) + 128) * 4 <= NST * kStage, "the row sums are reduced in the ring");
+  static_assert(2 * SUM_FLOATS * 4 + 2 * N * 4 <= NST * kStage, "the row sums are reduced in the ring");
 };
 
 struct Tile {
@@ -176,48 +196,88 @@ __device__ __forceinline__ uint32_t to_f16x2(uint32_t w) {
   return pack2<true>(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
+// What a role calls the same for one CTA and for a pair.
+template <int CT>
+struct Sync {
+  static __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+    if constexpr (CT == 1) return mbar_wait(bar, parity);
+    return mbar_wait_cluster(bar, parity);
+  }
+  // an arrival at rank 0's barrier
+  static __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
+    if constexpr (CT == 1) mbar_arrive(bar);
+    else mbar_arrive_cluster(map_smem_rank(smem_u32(bar), 0));
+  }
+  // an arrival at every CTA's
+  static __device__ __forceinline__ void arrive_all(uint64_t* bar) {
+    if constexpr (CT == 1) {
+      mbar_arrive(bar);
+    } else {
+      mbar_arrive_cluster(map_smem_rank(smem_u32(bar), 0));
+      mbar_arrive_cluster(map_smem_rank(smem_u32(bar), 1));
+    }
+  }
+  static __device__ __forceinline__ void all_threads() {
+    if constexpr (CT == 1) __syncthreads();
+    else cluster_sync_all();
+  }
+};
+
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_constant__ SharedParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  constexpr int N = C::N, D = C::D, KS = C::KS, NST = C::NST;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFFSET);
+  constexpr int N = C::N, D = C::D, KS = C::KS, NST = C::NST, CT = C::CT, TT = C::TT, CW = C::CW, LD = C::LD;
+  using S = Sync<CT>;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFFSET);  // (pair: rank 0's, for both CTAs' stages)
   uint64_t* empty = full + NST;
   uint64_t* raw_full = empty + NST;
   uint64_t* raw_empty = raw_full + C::NRAW;
   uint64_t* s_full = raw_empty + C::NRAW;  // [2]
-  uint64_t* s_empty = s_full + 2;          // [2]
-  uint64_t* p_full = s_empty + 2;
+  uint64_t* p_full = s_full + 2;           // (rank 0's)
   uint64_t* p_empty = p_full + 1;
-  uint64_t* q_full = p_empty + 1;
+  uint64_t* q_full = p_empty + 1;          // (rank 0's)
   uint64_t* drained = q_full + 1;
+  uint64_t* judged = drained + 1;          // the matrix warp has looked at the P that arrived
+  uint64_t* swapped = judged + 1;          // [2], one per softmax warpgroup
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::TMEM_OFFSET);
+  volatile uint32_t* left = tmem_at + 1;     // rank 0's: some score of the P that just arrived left its row's range
+  volatile uint32_t* verdict = tmem_at + 2;  // the round (P arrivals so far) that has to be written again
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+  const int rank = CT == 1 ? 0 : (int)cluster_ctarank();
 
   if (tid == 288) {
     prefetch_tensormap(&p.kmap);
     prefetch_tensormap(&p.vmap);
     for (int i = 0; i < NST; ++i) {
-      mbar_init(&full[i], C::FP8 ? 4 : 1);
+      mbar_init(&full[i], CT * (C::FP8 ? 4 : 1));
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < C::NRAW; ++i) {
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], 4);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 256);
-    }
-    mbar_init(p_full, 256);
+    mbar_init(&s_full[0], 1);
+    mbar_init(&s_full[1], 1);
+    mbar_init(p_full, CT * kSoftWarps);
     mbar_init(p_empty, 1);
-    mbar_init(q_full, 256);
+    mbar_init(q_full, CT * kSoftWarps);
     mbar_init(drained, 1);
+    mbar_init(judged, 1);
+    mbar_init(&swapped[0], CT * 4);
+    mbar_init(&swapped[1], CT * 4);
+    *left = 0;
+    *verdict = 0;
     fence_barrier_init();
   }
-  if (warp == 8) tmem_alloc(tmem_at, C::TMEM_COLS);
+  if (tid < N) {
+    reinterpret_cast<float*>(smem + C::REF_OFFSET)[tid] = kLow;
+    reinterpret_cast<int*>(smem + C::TOP_OFFSET)[tid] = kNoTop;
+  }
+  __syncwarp();
+  if (warp == 8) tmem_alloc<CT>(tmem_at, C::TMEM_COLS);
   tmem_fence_before();
-  __syncthreads();
+  S::all_threads();
   tmem_fence_after();
   const uint32_t tmem = *tmem_at;
   // launched behind the own part's stage 1, whose threads let this grid start
@@ -229,7 +289,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
   const int piece = blockIdx.y, g = blockIdx.z;
   if (blockIdx.x == 0 && piece == 0 && g == 0 && warp == 0 && !groups_ok(p) && lane == 0)
     atomicOr(p.err, kErrBadGroup);
-  const Tile t = find_tile(p, blockIdx.x);
+  const Tile t = find_tile(p, blockIdx.x / CT);
   int L = 0;
   if (t.group >= 0) {
     L = __ldg(p.prefix_lens + t.group);
@@ -243,25 +303,46 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
   const long long want = (long long)piece * p.chunk_tokens;
   const int lo = (int)min(want, (long long)L);
   const int hi = piece == p.num_pieces - 1 ? L : (int)min((long long)L, want + p.chunk_tokens);
-  const int ntile = (hi - lo + kTok - 1) / kTok;
+  const int ntile = (hi - lo + TT - 1) / TT;
   const int32_t* table = p.prefix_tables + (size_t)max(t.group, 0) * p.max_prefix_pages;
+  int* rows = reinterpret_cast<int*>(smem + C::ROW_OFFSET);
 
   if (ntile == 0) {
     // nothing here: weight 0 (the join reads no row of such a piece)
-    for (int r = tid; r < t.rows; r += C::THREADS)
-      p.lse_part[(size_t)row_of(p, t, r, g) * p.num_pieces + piece] = -INFINITY;
-  } else if (warp >= 9 && warp < 9 + kCopyWarps) {
+    if (rank == 0)
+      for (int r = tid; r < t.rows; r += C::THREADS)
+        p.lse_part[(size_t)row_of(p, t, r, g) * p.num_pieces + piece] = -INFINITY;
+    S::all_threads();
+    if (warp == 8) tmem_dealloc<CT>(tmem, C::TMEM_COLS);
+    grid_dependency_wait();
+    return;
+  }
+
+  // softmax warps: what the epilogue takes from the loop
+  bool done = false;
+  float v_top = 1.f;  // FP8: the piece's largest V scale
+  const int wg = (warp >> 2) & 1, lt = tid & 127, bar = 1 + wg;
+  float* nref = reinterpret_cast<float*>(smem + C::REF_OFFSET) + wg * CW;
+  int* top = reinterpret_cast<int*>(smem + C::TOP_OFFSET) + wg * CW;
+  const uint32_t quarter = tmem + ((uint32_t)(warp & 3) << 21);
+  const uint32_t o_at = quarter + wg * CW;
+  float* totals = reinterpret_cast<float*>(smem + C::TOTAL_OFFSET);  // [2][N]
+
+  if (warp >= 9 && warp < 9 + kCopyWarps) {
     // ---- copies: stages in the order the products use them, K(0), K(1), V(0), K(2), V(1), ...
-    // A K stage is 128 dims of the tile, a V stage all dims of VT tokens; both
-    // land as [8-row group][64-dim slab][8 rows][128 B], so that a 16-token page
-    // takes one copy of 4 KB (K) or 16 KB (V, d = 512): with a copy per page and
-    // slab (2 KB) the copies took 5.5 us a tile. Lane j holds the pool row of
-    // the tile's j-th K box and j-th V box.
+    // A K stage is 128 dims of this CTA's tokens, a V stage this CTA's dims of
+    // VT tokens; a 16-token page takes one copy of 4 KB (K) or 16 KB (V, d =
+    // 512): with a copy per page and slab (2 KB) the copies took 5.5 us a tile.
+    // Lane j holds the pool row of the tile's j-th K box and j-th V box.
+    // W warps take every W-th stage. W <= NR: a warp that comes to a stage has
+    // seen the stage NR + W uses back released, so the release it waits for is
+    // the barrier's next; one further ahead, the parity would read as done.
     const int v_boxes = C::VT / p.v_box;
     const uint64_t policy = p.keep_in_l2 ? l2_evict_normal_policy() : l2_evict_first_policy();
     constexpr int NR = C::FP8 ? C::NRAW : NST;
+    constexpr int W = NR < kCopyWarps ? NR : kCopyWarps;
     constexpr int BYTES = C::FP8 ? kRaw : kStage;
-    constexpr int K_SLABS = C::FP8 ? 1 : 2, ROW_BYTES = C::FP8 ? D : 2 * D;
+    constexpr int K_SLABS = C::FP8 ? 1 : 2, V_SLABS = C::V_ATOMS / (C::FP8 ? 2 : 1);
     uint64_t* land = C::FP8 ? raw_full : full;
     uint64_t* freed = C::FP8 ? raw_empty : empty;
     uint8_t* ring = smem + (C::FP8 ? C::RAW_OFFSET : C::RING_OFFSET);
@@ -269,9 +350,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     // the 8-row group of the pool where this lane's box of a tile starts (-1:
     // past the piece); a page outside the pool is fetched past the pool's end,
     // which reads zeros
-    auto group_at = [&](int tile, int box) -> int {
-      const int tok = lo + tile * kTok + lane * box;
-      if (tile >= ntile || tok >= hi || lane >= kTok / box) return -1;
+    auto group_at = [&](int tile, int first, int tokens, int box) -> int {
+      const int tok = lo + tile * TT + first + lane * box;
+      if (tile >= ntile || tok >= hi || lane >= tokens / box) return -1;
       const int page = __ldg(table + tok / p.page_size);
       if ((unsigned)page >= (unsigned)p.num_pages) {
         err |= kErrBadPage;
@@ -279,20 +360,31 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       }
       return ((page * p.num_kv_heads + g) * p.page_size + tok % p.page_size) / 8;
     };
+    auto k_group = [&](int tile) { return group_at(tile, rank * kTok, kTok, p.k_box); };
+    auto v_group = [&](int tile) { return group_at(tile, 0, TT, p.v_box); };
     int st = 0, uses = 0;  // the next stage, and how many stages were passed
-    int turn = warp - 9;   // stages until this warp's next
+    int turn = warp - 9 < W ? warp - 9 : 1 << 30;  // stages until this warp's next
     uint32_t phase = 1;    // of the stage's release (the first round waits for nothing)
     bool ok = true;
     // this warp's stage, free to be filled? (ok false: the wait ran out)
     auto begin = [&](int boxes, int box_bytes) {
       if (turn != 0) return false;
       ok = __all_sync(kFullMask, uses < NR || mbar_wait(&freed[st], phase));
-      if (ok && lane == 0) mbar_arrive_expect_tx(&land[st], boxes * box_bytes + p.stall_bytes);
+      if (ok && lane == 0) {
+        const uint32_t bytes = boxes * box_bytes + p.stall_bytes;
+        if (CT == 1 || C::FP8) mbar_arrive_expect_tx(&land[st], bytes);
+        else mbar_arrive_expect_tx_cluster(map_smem_rank(smem_u32(&land[st]), 0), bytes);
+      }
       __syncwarp();
       return ok;
     };
+    auto copy = [&](int at_byte, const CUtensorMap* map, int slab, int group) {
+      uint8_t* dst = ring + st * BYTES + at_byte;
+      if (CT == 1 || C::FP8) tma_load_4d(dst, map, 0, 0, slab, group, &land[st], policy);
+      else tma_load_4d_pair(dst, map, 0, 0, slab, group, map_smem_rank(smem_u32(&land[st]), 0), policy);
+    };
     auto end = [&] {
-      turn = turn == 0 ? kCopyWarps - 1 : turn - 1;
+      turn = turn == 0 ? W - 1 : turn - 1;
       ++uses;
       if (++st == NR) {
         st = 0;
@@ -304,79 +396,82 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       const int boxes = __popc(__ballot_sync(kFullMask, at >= 0));
 #pragma unroll 1
       for (int s = 0; s < KS; ++s) {
-        if (begin(boxes, bytes) && at >= 0)
-          tma_load_4d(ring + st * BYTES + lane * bytes, &p.kmap, 0, 0, s * K_SLABS, at, &land[st], policy);
+        if (begin(boxes, bytes) && at >= 0) copy(lane * bytes, &p.kmap, s * K_SLABS, at);
         if (!ok) return;
         end();
       }
     };
     auto load_v = [&](int at) {
-      const int bytes = p.v_box * ROW_BYTES;
+      const int bytes = p.v_box * 128 * V_SLABS;
 #pragma unroll 1
       for (int s = 0; s < KS; ++s) {
         const bool mine = at >= 0 && lane / v_boxes == s;
         if (begin(__popc(__ballot_sync(kFullMask, mine)), bytes) && mine)
-          tma_load_4d(ring + st * BYTES + lane % v_boxes * bytes, &p.vmap, 0, 0, 0, at, &land[st], policy);
+          copy(lane % v_boxes * bytes, &p.vmap, rank * V_SLABS, at);
         if (!ok) return;
         end();
       }
     };
-    int k_next = group_at(0, p.k_box), v_at = group_at(0, p.v_box);
+    int k_next = k_group(0), v_at = v_group(0);
     load_k(k_next);
-    k_next = group_at(1, p.k_box);
+    k_next = k_group(1);
 #pragma unroll 1
     for (int i = 0; i < ntile && ok; ++i) {
-      const int k_after = group_at(i + 2, p.k_box), v_next = group_at(i + 1, p.v_box);
+      const int k_after = k_group(i + 2), v_next = v_group(i + 1);
       if (i + 1 < ntile) load_k(k_next);
       if (ok) load_v(v_at);
       k_next = k_after;
       v_at = v_next;
     }
-    // no copy may still be landing when the CTA exits
+    // no copy may still be landing when the CTA exits (a pair's land on rank
+    // 0's barriers: it waits for both, and the CTAs leave together)
     if (lane == 0) {
       const unsigned long long deadline = global_timer_ns() + kWaitTimeoutNs;
-      for (int k = max(0, uses - NR); k < uses; ++k)
-        if (k % kCopyWarps == warp - 9 && !mbar_wait_until(&land[k % NR], (k / NR) & 1, deadline)) ok = false;
+      if (CT == 1 || C::FP8 || rank == 0)
+        for (int k = max(0, uses - NR); k < uses; ++k)
+          if (k % W == warp - 9 && !mbar_wait_until(&land[k % NR], (k / NR) & 1, deadline)) ok = false;
       if (!ok) err |= kErrTimeout;
     }
     err = __reduce_or_sync(kFullMask, err);
     if (lane == 0 && err) atomicOr(p.err, err);
   } else if (warp == 8) {
-    // ---- matrix instructions: QK(0), then QK(i + 1) ahead of PV(i). The warp
-    // walks the stages together and one elected lane issues: a lone thread
-    // computing descriptors took ~180 cycles an instruction.
-    constexpr uint32_t kQk = mma_desc_16bit(!C::FP8, 128, N, false, false);
-    constexpr uint32_t kPv = mma_desc_16bit(!C::FP8, 128, N, true, true);
+    // ---- matrix instructions (rank 0 for both CTAs of a pair): QK(0), then
+    // QK(i + 1) ahead of PV(i). The warp walks the stages together and one
+    // elected lane issues: a lone thread computing descriptors took ~180 cycles
+    // an instruction.
+    constexpr uint32_t kQk = mma_desc_16bit(!C::FP8, TT, N, false, false);
+    constexpr uint32_t kPv = mma_desc_16bit(!C::FP8, TT, N, true, true);
+    if (rank == 0) {
     // descriptors' bases; a step further is a constant added to the address field
     const uint32_t base = smem_u32(smem);
     const uint64_t k_desc = smem_desc(base + C::RING_OFFSET, 16, 2048), q_desc = smem_desc(base, 16, 1024);
-    const uint64_t v_desc = smem_desc(base + C::RING_OFFSET, 1024, D * 16);
-    const uint64_t p_desc = smem_desc(base + C::P_OFFSET, kTok * 128, 8 * C::P_ROW, C::P_ROW);
+    const uint64_t v_desc = smem_desc(base + C::RING_OFFSET, 1024, C::V_ATOMS * 1024);
+    const uint64_t p_desc = smem_desc(base + C::P_OFFSET, TT * 128, 8 * C::P_ROW, C::P_ROW);
     int st = 0;
-    uint32_t phase = 0;
-    bool ok = __all_sync(kFullMask, mbar_wait(q_full, 0));
+    uint32_t phase = 0, rounds = 0;
+    bool ok = __all_sync(kFullMask, S::wait(q_full, 0));
     auto next_stage = [&] {
       if (++st == NST) {
         st = 0;
         phase ^= 1;
       }
     };
+    // the other S buffer is free once P of the tile before last was accepted
     auto qk = [&](int i) {
-      if (ok && i >= 2) ok = __all_sync(kFullMask, mbar_wait(&s_empty[i & 1], ((i >> 1) - 1) & 1));
       const uint32_t d = tmem + C::O_COLS + (i & 1) * N;
 #pragma unroll 1
       for (int s = 0; s < KS && ok; ++s) {
-        ok = __all_sync(kFullMask, mbar_wait(&full[st], phase));
+        ok = __all_sync(kFullMask, S::wait(&full[st], phase));
         if (!ok) return;
         tmem_fence_after();
         if (elect_one()) {
-          const uint64_t a = k_desc + st * (kStage >> 4), b = q_desc + s * 2 * (N * 128 >> 4);
+          const uint64_t a = k_desc + st * (kStage >> 4), b = q_desc + s * 2 * (C::QN * 128 >> 4);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            mma_ss(d, a + (k >> 2) * (1024 >> 4) + (k & 3) * 2, b + (k >> 2) * (N * 128 >> 4) + (k & 3) * 2, kQk,
-                   k != 0 || s != 0);
-          mma_commit(&empty[st]);
-          if (s == KS - 1) mma_commit(&s_full[i & 1]);
+            mma_ss<CT>(d, a + (k >> 2) * (1024 >> 4) + (k & 3) * 2, b + (k >> 2) * (C::QN * 128 >> 4) + (k & 3) * 2,
+                       kQk, k != 0 || s != 0);
+          mma_commit<CT>(&empty[st]);
+          if (s == KS - 1) mma_commit<CT>(&s_full[i & 1]);
         }
         __syncwarp();
         next_stage();
@@ -386,33 +481,50 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
 #pragma unroll 1
     for (int i = 0; i < ntile && ok; ++i) {
       if (i + 1 < ntile) qk(i + 1);
-      if (ok) ok = __all_sync(kFullMask, mbar_wait(p_full, i & 1));
-      const int steps = min(kTok, hi - lo - i * kTok) / 16;
+      bool refused = true;
+      while (ok && refused) {
+        ok = __all_sync(kFullMask, S::wait(p_full, rounds & 1));
+        ++rounds;
+        if (!ok) break;
+        refused = *left != 0;
+        __syncwarp();
+        if (lane == 0) {
+          if (refused) {
+            // P is written again, under references that hold
+            *left = 0;
+            *verdict = rounds;
+            if constexpr (CT == 2) st_dsmem_u32(map_smem_rank(smem_u32(tmem_at + 2), 1), rounds);
+          }
+          S::arrive_all(judged);
+        }
+        __syncwarp();
+      }
+      const int steps = min(TT, hi - lo - i * TT) / 16;
 #pragma unroll 1
       for (int s = 0; s < KS && ok; ++s) {
-        ok = __all_sync(kFullMask, mbar_wait(&full[st], phase));
+        ok = __all_sync(kFullMask, S::wait(&full[st], phase));
         if (!ok) break;
         tmem_fence_after();
         if (elect_one()) {
           const uint64_t a = v_desc + st * (kStage >> 4), b = p_desc + s * (C::VT * C::P_ROW >> 4);
-          // 16 tokens at a time, all head dims
+          // 16 tokens at a time, all of the CTA's head dims
+          auto step = [&](int k, int m) {
+            mma_ss<CT>(tmem + m * N, a + k * (C::V_ATOMS * 2048 >> 4) + m * (2048 >> 4),
+                       b + k * (16 * C::P_ROW >> 4), kPv, k != 0 || s != 0 || i != 0);
+          };
           if ((s + 1) * (C::VT / 16) <= steps) {
 #pragma unroll
             for (int k = 0; k < C::VT / 16; ++k)
 #pragma unroll
-              for (int m = 0; m < KS; ++m)
-                mma_ss(tmem + m * N, a + k * (D * 32 >> 4) + m * (2048 >> 4), b + k * (16 * C::P_ROW >> 4), kPv,
-                       k != 0 || s != 0 || i != 0);
+              for (int m = 0; m < C::MC; ++m) step(k, m);
           } else {
 #pragma unroll 1
             for (int k = 0; s * (C::VT / 16) + k < steps; ++k)
 #pragma unroll 1
-              for (int m = 0; m < KS; ++m)
-                mma_ss(tmem + m * N, a + k * (D * 32 >> 4) + m * (2048 >> 4), b + k * (16 * C::P_ROW >> 4), kPv,
-                       k != 0 || s != 0 || i != 0);
+              for (int m = 0; m < C::MC; ++m) step(k, m);
           }
-          mma_commit(&empty[st]);
-          if (s == KS - 1) mma_commit(p_empty);
+          mma_commit<CT>(&empty[st]);
+          if (s == KS - 1) mma_commit<CT>(p_empty);
         }
         __syncwarp();
         next_stage();
@@ -421,34 +533,26 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     if (!ok) {
       // nothing may still be reading shared memory when the CTA exits
       if (elect_one()) {
-        mma_commit(drained);
+        mma_commit<CT>(drained);
         mbar_wait(drained, 0);
         atomicOr(p.err, kErrTimeout);
       }
       __syncwarp();
     }
-  } else if (warp < 8) {
-    // ---- softmax: a thread per token lane, warpgroup wg the rows [wg CW, wg CW + CW)
-    constexpr int CW = C::CW, LD = C::LD;
-    const int wg = warp >> 2, lt = tid & 127, bar = 1 + wg;
-    float* nref = reinterpret_cast<float*>(smem + C::REF_OFFSET) + wg * CW;
-    int* top = reinterpret_cast<int*>(smem + C::TOP_OFFSET) + wg * CW;
-    int* rows = reinterpret_cast<int*>(smem + C::ROW_OFFSET);
-    if (tid < N) rows[tid] = tid < t.rows ? row_of(p, t, tid, g) : -1;
-    if (lt < CW) {
-      nref[lt] = kLow;
-      top[lt] = kNoTop;
     }
+  } else if (warp < kSoftWarps) {
+    // ---- softmax: a thread per token lane, warpgroup wg the rows [wg CW, wg CW + CW)
+    if (tid < N) rows[tid] = tid < t.rows ? row_of(p, t, tid, g) : -1;
     __syncwarp();
     named_bar_sync(3, 256);
-    // the tile's query rows, swizzled as the K-major operand; all of a round's loads in flight at once
-    constexpr int kChunks = N * (D / 8), kRound = kChunks / 256 < 16 ? kChunks / 256 : 16;
+    // this CTA's query rows, swizzled as the K-major operand; all of a round's loads in flight at once
+    constexpr int kChunks = C::QN * (D / 8), kRound = kChunks / 256 < 16 ? kChunks / 256 : 16;
 #pragma unroll 1
     for (int e0 = tid; e0 < kChunks; e0 += 256 * kRound) {
       uint4 v[kRound];
 #pragma unroll
       for (int u = 0; u < kRound; ++u) {
-        const int e = e0 + u * 256, r = rows[e / (D / 8)];
+        const int e = e0 + u * 256, r = rows[rank * C::QN + e / (D / 8)];
         v[u] = make_uint4(0u, 0u, 0u, 0u);
         if (r >= 0) v[u] = __ldg(reinterpret_cast<const uint4*>(p.q + (size_t)r * D) + e % (D / 8));
       }
@@ -457,14 +561,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
         const int e = e0 + u * 256, r = e / (D / 8), c = e % (D / 8);
         if constexpr (C::FP8)
           v[u] = make_uint4(to_f16x2(v[u].x), to_f16x2(v[u].y), to_f16x2(v[u].z), to_f16x2(v[u].w));
-        *reinterpret_cast<uint4*>(smem + C::Q_OFFSET + (c >> 3) * N * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-            v[u];
+        *reinterpret_cast<uint4*>(smem + C::Q_OFFSET + (c >> 3) * C::QN * 128 + r * 128 +
+                                  (((c & 7) ^ (r & 7)) << 4)) = v[u];
       }
     }
-    fence_proxy_async_smem();
-    mbar_arrive(q_full);
+    fence_proxy_async_all();
+    __syncwarp();
+    if (lane == 0) S::arrive_leader(q_full);
 
-    float v_top = 1.f, v_inv = 1.f;  // FP8: the piece's largest V scale
+    float v_inv = 1.f;
     if constexpr (C::FP8) {
       float m = 0.f;
       for (int tok = lo + lt * 16; tok < hi; tok += 128 * 16) {
@@ -473,213 +578,252 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
           m = fmaxf(m, fabsf(__ldg(p.v_scale + (size_t)page * p.num_kv_heads + g)));
       }
       const int k = __reduce_max_sync(kFullMask, __float_as_int(m));
-      if (lane == 0) atomicMax(top, k);
+      // (exchanged where the maxima of refused tiles go: the other CTA writes there only after this one's first P)
+      if (lane == 0) top[warp & 3] = k;
       __syncwarp();
       named_bar_sync(bar, 128);
-      v_top = __int_as_float(top[0]);
+      v_top = __int_as_float(max(max(top[0], top[1]), max(top[2], top[3])));
       v_inv = v_top > 0.f ? 1.f / v_top : 0.f;
       named_bar_sync(bar, 128);
-      if (lt == 0) top[0] = kNoTop;
+      if (lt < 4) top[lt] = kNoTop;
       __syncwarp();
     }
 
-    const uint32_t quarter = tmem + ((uint32_t)(warp & 3) << 21);
-    const uint32_t o_at = quarter + wg * CW;
     float l[CW];
 #pragma unroll
     for (int c = 0; c < CW; ++c) l[c] = 0.f;
-    uint32_t err = 0;
+    uint32_t err = 0, round = 0;
     bool ok = true;
-    // this lane's token of tile i: whether it is attended, its scales
-    auto token = [&](int i, bool& valid, float& ks, float& vs) {
-      const int tok = lo + i * kTok + lt;
-      valid = false;
-      ks = 1.f;
-      vs = 1.f;
+    // a lane's token of a tile: whether it is attended, its scales
+    struct Token {
+      bool valid;
+      float sc, pv;
+    };
+    auto token = [&](int i) -> Token {
+      const int tok = lo + i * TT + rank * kTok + lt;
+      Token k{false, p.scale_log2, v_inv};
       if (i < ntile && tok < hi) {
         const int page = __ldg(table + tok / p.page_size);
-        valid = (unsigned)page < (unsigned)p.num_pages;
+        k.valid = (unsigned)page < (unsigned)p.num_pages;
+        if (!k.valid) err |= kErrBadPage;
         if constexpr (C::FP8) {
-          if (valid) {
-            ks = __ldg(p.k_scale + (size_t)page * p.num_kv_heads + g);
-            vs = __ldg(p.v_scale + (size_t)page * p.num_kv_heads + g);
+          if (k.valid) {
+            k.sc *= __ldg(p.k_scale + (size_t)page * p.num_kv_heads + g);
+            k.pv *= __ldg(p.v_scale + (size_t)page * p.num_kv_heads + g);
           }
         }
+      }
+      return k;
+    };
+    // P: this token's row, in the CTA that holds these query rows; its 16-byte chunks swizzled over the row
+    constexpr int kChunkMask = C::P_ROW / 16 - 1, kSwShift = C::QN >= 64 ? 0 : C::QN == 32 ? 1 : 2;
+    const int p_tok = rank * kTok + lt;
+    const uint32_t p_row = smem_u32(smem + C::P_OFFSET) + p_tok * C::P_ROW +
+                           (CT == 1 && N == 128 ? wg * (TT * 128) : 0);
+    const uint32_t p_remote = CT == 2 ? map_smem_rank(p_row, wg) : p_row;
+    const int p_sw = (p_tok >> kSwShift) & kChunkMask, p_chunk = CT == 2 || N == 128 ? 0 : wg * (CW / 8);
+    // two rows' probabilities of this token, packed; sums kept when `add`
+    auto prob = [&](const uint32_t (&x)[LD], int c0, int c, const Token& k, bool all, bool add, float& over) {
+      float e[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float y = fmaf(__uint_as_float(x[c + u]), k.sc, nref[c0 + c + u]);
+        over = fmaxf(over, y);
+        e[u] = ex2(y);
+        if (!all && !k.valid) e[u] = 0.f;
+        if (add) l[c0 + c + u] += e[u];
+        if constexpr (C::FP8) e[u] = !all && !k.valid ? 0.f : e[u] * k.pv;
+      }
+      return pack2<C::FP8>(e[0], e[1]);
+    };
+    auto store = [&](const uint32_t (&w)[CW / 2]) {
+#pragma unroll
+      for (int c = 0; c < CW / 8; ++c) {
+        const uint32_t at = p_remote + (((p_chunk + c) ^ p_sw) << 4);
+        const uint4 v = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        if constexpr (CT == 2) st_dsmem_u32x4(at, v);
+        else sts128_addr(at, v);
       }
     };
-    // P: this token's row; its 16-byte chunks swizzled over the row
-    constexpr int kChunkMask = C::P_ROW / 16 - 1, kSwShift = N >= 64 ? 0 : N == 32 ? 1 : 2;
-    uint8_t* p_row = smem + C::P_OFFSET + lt * C::P_ROW + (N == 128 ? wg * (kTok * 128) : 0);
-    const int p_sw = (lt >> kSwShift) & kChunkMask, p_chunk = N == 128 ? 0 : wg * (CW / 8);
-    bool valid;
-    float ks, vs;
-    token(0, valid, ks, vs);
-#pragma unroll 1
-    for (int i = 0; i < ntile; ++i) {
-      bool nvalid;
-      float nks, nvs;
-      token(i + 1, nvalid, nks, nvs);
-      const float sc = p.scale_log2 * ks;
-      ok = mbar_wait(&s_full[i & 1], (i >> 1) & 1) && ok;
-      __syncwarp();
-      tmem_fence_after();
-      const uint32_t sa = quarter + C::O_COLS + (i & 1) * N + wg * CW;
-      // does any score leave its row's range?
-      float over = -INFINITY;
-      uint32_t x[LD];
-#pragma unroll
-      for (int c0 = 0; c0 < CW; c0 += LD) {
-        tmem_ld(x, sa + c0);
-        tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < LD; ++c) over = fmaxf(over, fmaf(__uint_as_float(x[c]), sc, nref[c0 + c]));
-      }
-      if (named_bar_or(bar, 128, !ok || (valid && over > kSlack))) {
-        // the rows that left theirs take the true maximum; P(i - 1) is spent
-        if (i > 0) ok = mbar_wait(p_empty, (i - 1) & 1) && ok;
-        __syncwarp();
-        if (named_bar_or(bar, 128, !ok)) break;
-        tmem_fence_after();
-#pragma unroll 1
-        for (int c0 = 0; c0 < CW; c0 += LD) {
-          tmem_ld(x, sa + c0);
-          tmem_wait_ld();
-          int mine = kNoTop;
-#pragma unroll
-          for (int c = 0; c < LD; ++c) {
-            const int m = __reduce_max_sync(kFullMask, ordered(valid ? __uint_as_float(x[c]) * sc : -INFINITY));
-            if (lane == c) mine = m;
-          }
-          if (lane < LD) atomicMax(top + c0 + lane, mine);
-        }
-        __syncwarp();
-        named_bar_sync(bar, 128);
-        // a row moves if its maximum left the range: factor of what it holds so far
-        auto moves = [&](int c) { return unordered(top[c]) + nref[c] > kSlack; };
-        auto factor = [&](int c) { return moves(c) ? ex2(-nref[c] - unordered(top[c])) : 1.f; };
-#pragma unroll
-        for (int c = 0; c < CW; ++c) l[c] *= factor(c);
-        if (i > 0) {
-#pragma unroll
-          for (int c0 = 0; c0 < CW; c0 += LD) {
-            float f[LD];
-#pragma unroll
-            for (int c = 0; c < LD; ++c) f[c] = factor(c0 + c);
-#pragma unroll 1
-            for (int s = 0; s < KS; ++s) {
-              tmem_ld(x, o_at + s * N + c0);
-              tmem_wait_ld();
-#pragma unroll
-              for (int c = 0; c < LD; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) * f[c]);
-              tmem_st(o_at + s * N + c0, x);
-            }
-          }
-          tmem_wait_st();
-        }
-        named_bar_sync(bar, 128);
-        if (lt < CW) {
-          if (moves(lt)) nref[lt] = -unordered(top[lt]);
-          top[lt] = kNoTop;
-        }
-        __syncwarp();
-        named_bar_sync(bar, 128);
-      } else if (i > 0) {
-        ok = mbar_wait(p_empty, (i - 1) & 1);
-        __syncwarp();
-      }
-      const bool all = __all_sync(kFullMask, valid);
-      const float pv = vs * v_inv;
-#pragma unroll
-      for (int c0 = 0; c0 < CW; c0 += LD) {
-        tmem_ld(x, sa + c0);
-        tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < LD; c += 8) {
-          uint32_t w[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float e[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int cc = c + 2 * k + u;
-              e[u] = ex2(fmaf(__uint_as_float(x[cc]), sc, nref[c0 + cc]));
-              if (!all && !valid) e[u] = 0.f;
-              l[c0 + cc] += e[u];
-              if constexpr (C::FP8) e[u] = !all && !valid ? 0.f : e[u] * pv;
-            }
-            w[k] = pack2<C::FP8>(e[0], e[1]);
-          }
-          *reinterpret_cast<uint4*>(p_row + (((p_chunk + (c0 + c) / 8) ^ p_sw) << 4)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
-      fence_proxy_async_smem();
+    // P of a tile is complete
+    auto publish = [&](bool leaves) {
+      fence_proxy_async_all();
       tmem_fence_before();
-      mbar_arrive(p_full);
-      mbar_arrive(&s_empty[i & 1]);
-      if (!valid && lo + i * kTok + lt < hi) err |= kErrBadPage;
-      valid = nvalid;
-      ks = nks;
-      vs = nvs;
-    }
-    ok = ok && mbar_wait(p_empty, (ntile - 1) & 1);
-    __syncwarp();
-    // (both warpgroups: the sums go where the other's last products read)
-    if (named_bar_or(3, 256, !ok)) {
-      err |= kErrTimeout;
-    } else {
-      tmem_fence_after();
-      // the rows' sums over the token lanes, in the ring (every product is done with it)
-      float* sum = reinterpret_cast<float*>(smem + C::RING_OFFSET) + wg * (kTok * (CW + 1) + 128);
-      float* part = sum + kTok * (CW + 1);
-#pragma unroll
-      for (int c = 0; c < CW; ++c) sum[lt * (CW + 1) + c] = l[c];
-      named_bar_sync(bar, 128);
-      const int col = lt % CW, first = lt / CW * CW;
-      float a[2] = {0.f, 0.f};
-#pragma unroll 4
-      for (int k = 0; k < CW; k += 2) {
-        a[0] += sum[(first + k) * (CW + 1) + col];
-        a[1] += sum[(first + k + 1) * (CW + 1) + col];
+      if (__any_sync(kFullMask, leaves) && lane == 0) {
+        if constexpr (CT == 2) st_dsmem_u32(map_smem_rank(smem_u32(tmem_at + 1), 0), 1);
+        else *left = 1;
       }
-      part[lt] = a[0] + a[1];
+      __syncwarp();
+      if (lane == 0) S::arrive_leader(p_full);
+      ++round;
+    };
+    // Tile i's P was refused: rows that left their range take the tile's true
+    // maximum over both CTAs' tokens, what they hold is rescaled, P written again.
+    uint32_t swaps = 0;
+    auto again = [&](int i, const Token& k) {
+      const uint32_t sa = quarter + C::O_COLS + (i & 1) * N + wg * CW;
+      uint32_t x[LD];
+#pragma unroll 1
+      for (int c0 = 0; c0 < CW; c0 += LD) {
+        tmem_ld(x, sa + c0);
+        tmem_wait_ld();
+        int mine = kNoTop;
+#pragma unroll
+        for (int c = 0; c < LD; ++c) {
+          const int m = __reduce_max_sync(kFullMask, ordered(k.valid ? __uint_as_float(x[c]) * k.sc : -INFINITY));
+          if (lane == c) mine = m;
+        }
+        if (lane < LD) {
+          atomicMax(top + c0 + lane, mine);
+          if constexpr (CT == 2) max_dsmem_s32(map_smem_rank(smem_u32(top + c0 + lane), rank ^ 1), mine);
+        }
+      }
+      __syncwarp();
+      if constexpr (CT == 2) {
+        if (lane == 0) S::arrive_all(&swapped[wg]);
+        ok = S::wait(&swapped[wg], swaps & 1) && ok;
+        ++swaps;
+        __syncwarp();
+      }
+      named_bar_sync(bar, 128);
+      auto moves = [&](int c) { return unordered(top[c]) + nref[c] > C::SLACK; };
+      // factor of what a row holds; 1 where it stays
+      auto factor = [&](int c) { return moves(c) ? ex2(-nref[c] - unordered(top[c])) : 1.f; };
+      // a lane's sum holds this tile's probabilities already, under the old
+      // reference; past 2^100 they may be infinite and all before them is
+      // negligible: the probability itself, under the new one
+#pragma unroll
+      for (int c0 = 0; c0 < CW; c0 += LD) {
+        tmem_ld(x, sa + c0);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < LD; ++c) {
+          const int cc = c0 + c;
+          const float s = __uint_as_float(x[c]) * k.sc;
+          const bool far = moves(cc) && k.valid && fmaf(__uint_as_float(x[c]), k.sc, nref[cc]) > 100.f;
+          l[cc] = far ? ex2(s - unordered(top[cc])) : l[cc] * factor(cc);
+        }
+      }
+      if (i > 0) {
+#pragma unroll
+        for (int c0 = 0; c0 < CW; c0 += LD) {
+          float f[LD];
+#pragma unroll
+          for (int c = 0; c < LD; ++c) f[c] = factor(c0 + c);
+#pragma unroll 1
+          for (int m = 0; m < C::MC; ++m) {
+            tmem_ld(x, o_at + m * N + c0);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < LD; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) * f[c]);
+            tmem_st(o_at + m * N + c0, x);
+          }
+        }
+        tmem_wait_st();
+      }
       named_bar_sync(bar, 128);
       if (lt < CW) {
-        float total = 0.f;
-#pragma unroll
-        for (int k = 0; k < 128 / CW; ++k) total += part[k * CW + lt];
-        // no attended token: weight 0 and a zero row; NaN stays NaN
-        if (rows[wg * CW + lt] >= 0)
-          p.lse_part[(size_t)rows[wg * CW + lt] * p.num_pieces + piece] =
-              total == 0.f ? -INFINITY : (log2f(total) - nref[lt]) * 0.69314718055994530942f;
-        nref[lt] = total == 0.f ? 0.f : v_top / total;
+        if (moves(lt)) nref[lt] = -unordered(top[lt]);
+        top[lt] = kNoTop;
       }
       __syncwarp();
       named_bar_sync(bar, 128);
-      constexpr int OC = CW < 16 ? CW : 16;
-#pragma unroll 1
-      for (int c0 = 0; c0 < CW; c0 += OC) {
-        if (wg * CW + c0 >= t.rows) break;
-        uint32_t y[KS][OC];
+      uint32_t w[CW / 2];
+      float over = -INFINITY;
 #pragma unroll
-        for (int s = 0; s < KS; ++s) tmem_ld(y[s], o_at + s * N + c0);
+      for (int c0 = 0; c0 < CW; c0 += LD) {
+        tmem_ld(x, sa + c0);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < OC; ++c) {
-          const int r = rows[wg * CW + c0 + c];
-          if (r < 0) break;
-          float* dst = p.o_part + ((size_t)r * p.num_pieces + piece) * D + lt;
-          const float f = nref[c0 + c];
-#pragma unroll
-          for (int s = 0; s < KS; ++s) dst[s * 128] = __uint_as_float(y[s][c]) * f;
-        }
+        for (int c = 0; c < LD; c += 2) w[(c0 + c) / 2] = prob(x, c0, c, k, false, false, over);
       }
+      store(w);
+      publish(false);
+    };
+    // Until tile i's P was accepted. A wait that ran out shows here, to the
+    // whole warpgroup at once: its warps leave together.
+    auto judge = [&](int i, const Token& k) {
+      while (true) {
+        ok = ok && S::wait(judged, (round - 1) & 1);
+        __syncwarp();
+        ok = !named_bar_or(bar, 128, !ok);
+        if (!ok || *verdict != round) return;
+        tmem_fence_after();
+        again(i, k);
+      }
+    };
+
+    Token now = token(0), before{};
+#pragma unroll 1
+    for (int i = 0; i < ntile; ++i) {
+      const Token after = token(i + 1);
+      ok = S::wait(&s_full[i & 1], (i >> 1) & 1) && ok;
+      __syncwarp();
+      tmem_fence_after();
+      if (i > 0) {
+        judge(i - 1, before);
+        if (!ok) break;
+      }
+      const uint32_t sa = quarter + C::O_COLS + (i & 1) * N + wg * CW;
+      const bool all = __all_sync(kFullMask, now.valid);
+      uint32_t w[CW / 2];
+      float over = -INFINITY;
+#pragma unroll
+      for (int c0 = 0; c0 < CW; c0 += LD) {
+        uint32_t x[LD];
+        tmem_ld(x, sa + c0);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < LD; c += 2) w[(c0 + c) / 2] = prob(x, c0, c, now, all, true, over);
+      }
+      if (i > 0) ok = S::wait(p_empty, (i - 1) & 1) && ok;
+      __syncwarp();
+      store(w);
+      publish(now.valid && over > C::SLACK);
+      before = now;
+      now = after;
+    }
+    if (ok) judge(ntile - 1, before);
+    ok = ok && S::wait(p_empty, (ntile - 1) & 1);
+    __syncwarp();
+    done = !named_bar_or(bar, 128, !ok);
+    if (!done) err |= kErrTimeout;
+    if (done) {
+      tmem_fence_after();
+      // the rows' sums over this CTA's token lanes, in the ring (every product is done with it)
+      float* sum = reinterpret_cast<float*>(smem + C::RING_OFFSET) + wg * C::SUM_FLOATS;
+#pragma unroll
+      for (int c = 0; c < CW; ++c) sum[lt * (CW + 1) + c] = l[c];
     }
     err = __reduce_or_sync(kFullMask, err);
     if (lane == 0 && err) atomicOr(p.err, err);
+    named_bar_sync(bar, 128);
+    {
+      const float* sum = reinterpret_cast<const float*>(smem + C::RING_OFFSET) + wg * C::SUM_FLOATS;
+      float* part = reinterpret_cast<float*>(smem + C::RING_OFFSET) + wg * C::SUM_FLOATS + kTok * (CW + 1);
+      const int col = lt % CW, first = lt / CW * CW;
+      float a[2] = {0.f, 0.f};
+      if (done) {
+#pragma unroll 4
+        for (int k = 0; k < CW; k += 2) {
+          a[0] += sum[(first + k) * (CW + 1) + col];
+          a[1] += sum[(first + k + 1) * (CW + 1) + col];
+        }
+        part[lt] = a[0] + a[1];
+      }
+      named_bar_sync(bar, 128);
+      if (done && lt < CW) {
+        float total = 0.f;
+#pragma unroll
+        for (int k = 0; k < 128 / CW; ++k) total += part[k * CW + lt];
+        totals[rank * N + wg * CW + lt] = total;
+        if constexpr (CT == 2)
+          st_dsmem_f32(map_smem_rank(smem_u32(totals + rank * N + wg * CW + lt), rank ^ 1), total);
+      }
+    }
   } else if constexpr (C::FP8) {
     // ---- FP8: e4m3 stages widened to f16 operand stages, a thread per token row
-    const int row = tid - 32 * (9 + kCopyWarps), sw = row & 7, total = 2 * KS * ntile;
+    const int row = tid - 32 * (kSoftWarps + 1 + kCopyWarps), sw = row & 7, total = 2 * KS * ntile;
     bool ok = true;
     for (int it = 0; it < total; ++it) {
       const int st = it % NST, rs = it % C::NRAW;
@@ -704,40 +848,78 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
         *reinterpret_cast<uint4*>(to + ((cc ^ sw) << 4)) = a;
         *reinterpret_cast<uint4*>(to + (((cc + 1) ^ sw) << 4)) = b;
       }
-      fence_proxy_async_smem();
+      fence_proxy_async_all();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&raw_empty[rs]);
-        mbar_arrive(&full[st]);
+        S::arrive_leader(&full[st]);
       }
     }
   }
-  tmem_fence_before();
+
+  // ---- epilogue: both CTAs' totals are in place
+  __syncwarp();
+  S::all_threads();
+  if (warp < kSoftWarps && done) {
+    tmem_fence_after();
+    if (lt < CW) {
+      const int c = wg * CW + lt;
+      const float total = CT == 1 ? totals[c] : totals[c] + totals[N + c];
+      // no attended token: weight 0 and a zero row; NaN stays NaN
+      if (rank == 0 && rows[c] >= 0)
+        p.lse_part[(size_t)rows[c] * p.num_pieces + piece] =
+            total == 0.f ? -INFINITY : (log2f(total) - nref[lt]) * 0.69314718055994530942f;
+      nref[lt] = total == 0.f ? 0.f : v_top / total;
+    }
+  }
   __syncthreads();
-  if (warp == 8) tmem_dealloc(tmem, C::TMEM_COLS);
+  if (warp < kSoftWarps && done) {
+    constexpr int OC = CW < 16 ? CW : 16;
+#pragma unroll 1
+    for (int c0 = 0; c0 < CW; c0 += OC) {
+      if (wg * CW + c0 >= t.rows) break;
+      uint32_t y[C::MC][OC];
+#pragma unroll
+      for (int m = 0; m < C::MC; ++m) tmem_ld(y[m], o_at + m * N + c0);
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < OC; ++c) {
+        const int r = rows[wg * CW + c0 + c];
+        if (r < 0) break;
+        float* dst = p.o_part + ((size_t)r * p.num_pieces + piece) * D + rank * (C::MC * 128) + lt;
+        const float f = nref[c0 + c];
+#pragma unroll
+        for (int m = 0; m < C::MC; ++m) dst[m * 128] = __uint_as_float(y[m][c]) * f;
+      }
+    }
+  }
+  __syncwarp();
+  tmem_fence_before();
+  S::all_threads();
+  if (warp == 8) tmem_dealloc<CT>(tmem, C::TMEM_COLS);
   grid_dependency_wait();
 }
 
 #define PD_FOR_EACH_PREFIX(X)                                                                          \
-  X(0, 512, 16, false) X(1, 512, 32, false) X(2, 512, 64, false) X(3, 256, 16, false)                  \
-  X(4, 256, 32, false) X(5, 256, 64, false) X(6, 256, 128, false) X(7, 128, 16, false)                 \
-  X(8, 128, 32, false) X(9, 128, 64, false) X(10, 128, 128, false) X(11, 512, 16, true)                \
-  X(12, 512, 32, true) X(13, 512, 64, true) X(14, 256, 16, true) X(15, 256, 32, true)                  \
-  X(16, 256, 64, true) X(17, 256, 128, true)
+  X(0, 512, 16, false, 1) X(1, 512, 32, false, 1) X(2, 512, 64, false, 1) X(3, 256, 16, false, 1)      \
+  X(4, 256, 32, false, 1) X(5, 256, 64, false, 1) X(6, 256, 128, false, 1) X(7, 128, 16, false, 1)     \
+  X(8, 128, 32, false, 1) X(9, 128, 64, false, 1) X(10, 128, 128, false, 1) X(11, 512, 16, true, 1)    \
+  X(12, 512, 32, true, 1) X(13, 512, 64, true, 1) X(14, 256, 16, true, 1) X(15, 256, 32, true, 1)      \
+  X(16, 256, 64, true, 1) X(17, 256, 128, true, 1) X(18, 512, 128, false, 2) X(19, 512, 128, true, 2)
 
 }  // namespace
 
-#define PD_PREFIX_ROW(ID, D, N, F)                                                                     \
-  PrefixInstance{ID, D, N, F, PrefixCfg<D, N, F>::THREADS, PrefixCfg<D, N, F>::SMEM_BYTES},
+#define PD_PREFIX_ROW(ID, D, N, F, CT) \
+  PrefixInstance{ID, D, N, F, CT, PrefixCfg<D, N, F, CT>::THREADS, PrefixCfg<D, N, F, CT>::SMEM_BYTES},
 const PrefixInstance kPrefixInstances[] = {PD_FOR_EACH_PREFIX(PD_PREFIX_ROW)};
 #undef PD_PREFIX_ROW
 const int kNumPrefixInstances = sizeof(kPrefixInstances) / sizeof(kPrefixInstances[0]);
 
 const void* prefix_kernel_ptr(int variant) {
   switch (variant) {
-#define PD_PREFIX_CASE(ID, D, N, F) \
-  case ID:                          \
-    return reinterpret_cast<const void*>(&prefix_kernel<PrefixCfg<D, N, F>>);
+#define PD_PREFIX_CASE(ID, D, N, F, CT) \
+  case ID:                              \
+    return reinterpret_cast<const void*>(&prefix_kernel<PrefixCfg<D, N, F, CT>>);
     PD_FOR_EACH_PREFIX(PD_PREFIX_CASE)
 #undef PD_PREFIX_CASE
     default:

@@ -131,9 +131,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p) 
 uint64_t align_up(uint64_t x, uint64_t a) { return (x + a - 1) / a * a; }
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// Query rows a CTA of the prefix pass serves.
-int row_tile_for(int head_dim, long long rows) {
-  const int most = head_dim == 512 ? 64 : 128;
+// Query rows a tile of the prefix pass serves: the smallest of 16, 32, 64 and
+// 128 that holds the largest group's (128 at head_dim 512: a pair of CTAs).
+int row_tile_for(long long rows) {
+  const int most = 128;
   int n = 16;
   while (n < most && n < rows) n *= 2;
   return n;
@@ -188,12 +189,14 @@ double tile_us(const pd_layer_desc& ly) {
 // prefixes of different lengths; each costs a CTA's fixed time and its partials.
 void plan_pieces(pd_shared_plan& sp, const int32_t* starts, const int32_t* lens, int per_req, int sm_count) {
   const pd_layer_desc& ly = sp.own.layer;
-  const long long most = ((long long)sp.max_prefix_len + kPrefixTile - 1) / kPrefixTile;
-  sp.chunk_tokens = kPrefixTile;
+  const int unit = kPrefixTile * kPrefixInstances[sp.variant].ctas;  // tokens of a tile
+  const int slots = sm_count / kPrefixInstances[sp.variant].ctas;
+  const long long most = ((long long)sp.max_prefix_len + unit - 1) / unit;
+  sp.chunk_tokens = unit;
   sp.num_pieces = 1;
   if (most <= 1) return;
   const double cta_us = tile_us(ly);
-  const double tile_bytes = (double)kPrefixTile * ly.head_dim * (ly.kv_dtype == PD_KV_FP8_E4M3 ? 1 : 2) *
+  const double tile_bytes = (double)unit * ly.head_dim * (ly.kv_dtype == PD_KV_FP8_E4M3 ? 1 : 2) *
                             (ly.kv_shared ? 1 : 2);
   const double rows = (double)sp.own.batch * sp.own.query_tokens * ly.num_q_heads;
   double best = 1e300;
@@ -203,20 +206,20 @@ void plan_pieces(pd_shared_plan& sp, const int32_t* starts, const int32_t* lens,
     double ctas = 0, tiles = 0, distinct = 0;
     for (int n = 0; n < sp.num_groups; ++n) {
       const long long row_tiles = ((long long)(starts[n + 1] - starts[n]) * per_req + sp.row_tile - 1) / sp.row_tile;
-      const long long len = (lens[n] + kPrefixTile - 1) / kPrefixTile;
+      const long long len = (lens[n] + unit - 1) / unit;
       ctas += (double)row_tiles * ly.num_kv_heads * ((len + c - 1) / c);
       tiles += (double)row_tiles * ly.num_kv_heads * len;
       if (row_tiles > 0) distinct += (double)ly.num_kv_heads * len;
     }
     const double one = kFixedUs + c * cta_us;
-    const double all = (ctas * kFixedUs + tiles * cta_us) / sm_count;
+    const double all = (ctas * kFixedUs + tiles * cta_us) / slots;
     // within one wave the longest CTA; beyond, the mean load and part of a last one
-    double us = ctas <= sm_count ? one : std::max(one, all + 0.4 * one);
+    double us = ctas <= slots ? one : std::max(one, all + 0.4 * one);
     us = std::max(us, kFixedUs + distinct * tile_bytes / kHbmBytesPerUs) +
          2.0 * rows * pieces * ly.head_dim * 4.0 / kPartialBytesPerUs;
     if (us < best) {
       best = us;
-      sp.chunk_tokens = (int32_t)(c * kPrefixTile);
+      sp.chunk_tokens = (int32_t)(c * unit);
       sp.num_pieces = (int32_t)pieces;
     }
   }
@@ -271,7 +274,7 @@ pd_status plan_shared(const pd_layer_desc* layer, int32_t batch, int32_t query_t
   sp.num_groups = num_groups;
   sp.max_prefix_pages = max_prefix_pages;
   sp.max_prefix_len = longest;
-  sp.row_tile = row_tile_for(ly.head_dim, most_rows);
+  sp.row_tile = row_tile_for(most_rows);
   const PrefixInstance* v = find_prefix(ly.head_dim, sp.row_tile, ly.kv_dtype == PD_KV_FP8_E4M3);
   if (!v) return PD_ERR_UNSUPPORTED;
   sp.variant = v->id;
@@ -293,17 +296,22 @@ pd_status plan_shared(const pd_layer_desc* layer, int32_t batch, int32_t query_t
   return PD_OK;
 }
 
-cudaError_t launch_dependent(const void* kernel, dim3 grid, int threads, int smem_bytes, void* stream, void** args) {
+cudaError_t launch_dependent(const void* kernel, dim3 grid, int threads, int smem_bytes, void* stream, void** args,
+                             int cluster = 1) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem_bytes;
   cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelExC(&cfg, kernel, args);
   if (e != cudaSuccess) (void)cudaGetLastError();
   return e;
@@ -359,17 +367,17 @@ pd_status decode_shared(const pd_shared_plan* plan, bool fp8, const void* q, con
   p.tiles = plan->tiles;
   p.num_pieces = plan->num_pieces;
   p.chunk_tokens = plan->chunk_tokens;
-  // a stage of the pass holds 128 tokens x 128 dims of K, or all dims of v_tokens tokens of V
-  const int v_tokens = kPrefixTile * 128 / ly.head_dim;
+  const PrefixInstance& v = kPrefixInstances[plan->variant];
+  // a stage of the pass holds 128 tokens x 128 dims of K, or a CTA's dims of v_tokens tokens of V
+  const int v_tokens = kPrefixTile * 128 * v.ctas / ly.head_dim;
   p.k_box = 16;
   while (p.k_box < kPrefixTile && ly.page_size % (2 * p.k_box) == 0) p.k_box *= 2;
   p.v_box = std::min<int32_t>(p.k_box, v_tokens);
   p.keep_in_l2 = plan->tiles > 1 || ly.kv_shared;
   p.stall_bytes = own.test_stall_bytes;
-  const PrefixInstance& v = kPrefixInstances[plan->variant];
   const void* fn = prefix_kernel_ptr(plan->variant);
   pd_status st = ensure_prefix_smem(plan->variant, fn, v.smem_bytes);
-  const int slabs = ly.head_dim / (fp8 ? 128 : 64);
+  const int slabs = ly.head_dim / (fp8 ? 128 : 64) / v.ctas;
   if (st == PD_OK) st = encode_group_map(&p.kmap, k_pool, ly, p.k_box, fp8 ? 1 : 2);
   if (st == PD_OK) st = encode_group_map(&p.vmap, ly.kv_shared ? k_pool : v_pool, ly, p.v_box, slabs);
   if (st != PD_OK) return st;
@@ -378,8 +386,8 @@ pd_status decode_shared(const pd_shared_plan* plan, bool fp8, const void* q, con
                        workspace_bytes, out, stream);
   if (st != PD_OK) return st;
   void* args[] = {&p};
-  if (plan->tiles > 0 && launch_dependent(fn, dim3(plan->tiles, plan->num_pieces, ly.num_kv_heads), v.threads,
-                                          v.smem_bytes, stream, args) != cudaSuccess)
+  if (plan->tiles > 0 && launch_dependent(fn, dim3(plan->tiles * v.ctas, plan->num_pieces, ly.num_kv_heads), v.threads,
+                                          v.smem_bytes, stream, args, v.ctas) != cudaSuccess)
     return PD_ERR_CUDA;
   JoinParams j = {};
   j.lse[0] = reinterpret_cast<const float*>(ws + own.lse_offset);

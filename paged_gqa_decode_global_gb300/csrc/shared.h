@@ -32,11 +32,12 @@ struct SharedParams {
   int32_t stall_bytes;  // tests only: bytes expected per stage beyond what the copies deliver
 };
 
-// The prefix pass's kernel instances: head_dim, query rows a CTA serves, cache type.
+// The prefix pass's kernel instances: head_dim, query rows of a row tile, cache
+// type, CTAs that serve a row tile together (a cluster of two, or one).
 struct PrefixInstance {
   int id, head_dim, row_tile;
   bool fp8;
-  int threads, smem_bytes;
+  int ctas, threads, smem_bytes;
 };
 extern const PrefixInstance kPrefixInstances[];
 extern const int kNumPrefixInstances;
