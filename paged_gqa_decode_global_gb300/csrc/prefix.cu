@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
                                   (((c & 7) ^ (r & 7)) << 4)) = v[u];
       }
     }
-    fence_proxy_async_all();
+    fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) S::arrive_leader(q_full);
 
@@ -647,7 +647,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     };
     // P of a tile is complete
     auto publish = [&](bool leaves) {
-      fence_proxy_async_all();
+      if constexpr (CT == 2) fence_proxy_async_pair();
+      else fence_proxy_async_smem();
       tmem_fence_before();
       if (__any_sync(kFullMask, leaves) && lane == 0) {
         if constexpr (CT == 2) st_dsmem_u32(map_smem_rank(smem_u32(tmem_at + 1), 0), 1);
@@ -848,7 +849,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
         *reinterpret_cast<uint4*>(to + ((cc ^ sw) << 4)) = a;
         *reinterpret_cast<uint4*>(to + (((cc + 1) ^ sw) << 4)) = b;
       }
-      fence_proxy_async_all();
+      fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&raw_empty[rs]);

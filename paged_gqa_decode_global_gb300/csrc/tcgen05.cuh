@@ -196,7 +196,11 @@ __device__ __forceinline__ void max_dsmem_s32(uint32_t addr, int v) {
   asm volatile("red.relaxed.cluster.shared::cluster.max.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// Order this thread's generic-proxy writes (of either CTA's shared memory) before async-proxy accesses.
-__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+// Order this thread's generic-proxy writes of either CTA's shared memory before
+// async-proxy accesses (the fence over all state spaces would also wait for the
+// global loads in flight: ~1500 cycles a tile).
+__device__ __forceinline__ void fence_proxy_async_pair() {
+  asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
+}
 
 }  // namespace pd
