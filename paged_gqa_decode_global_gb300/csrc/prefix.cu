@@ -84,9 +84,11 @@ struct PrefixCfg {
   static constexpr int TOP_OFFSET = REF_OFFSET + N * 4;         // int top[N]: a tile's true maxima
   static constexpr int ROW_OFFSET = TOP_OFFSET + N * 4;         // int row[N]: a tile row's row of q and out
   static constexpr int BAR_OFFSET = ROW_OFFSET + N * 4;
-  static constexpr int NBAR = 2 * NST + 2 * NRAW + 2 + 1 + 1 + 1 + 1 + 1 + 2;
-  static constexpr int TMEM_OFFSET = BAR_OFFSET + NBAR * 8;     // tensor memory address, left, verdict
-  static constexpr int SMEM_BYTES = TMEM_OFFSET + 16 + 1024;
+  static constexpr int NBAR = 2 * NST + 2 * NRAW + 10;
+  static constexpr int TMEM_OFFSET = BAR_OFFSET + NBAR * 8;     // tensor memory address, verdict, peer, -, left[8]
+  static constexpr int SMEM_BYTES = TMEM_OFFSET + 48 + 1024;
+  // pair: what a CTA's P takes from the other CTA a round: 128 tokens' rows, and its warps' flags
+  static constexpr int P_TX = kTok * QN * 2 + 16;
   static constexpr int THREADS = 32 * (kSoftWarps + 1 + kCopyWarps + (FP8 ? 4 : 0));
   static constexpr int CW = N / 2;         // rows of a softmax warpgroup
   static constexpr int LD = CW < 32 ? CW : 32;
@@ -199,23 +201,15 @@ __device__ __forceinline__ uint32_t to_f16x2(uint32_t w) {
 // What a role calls the same for one CTA and for a pair.
 template <int CT>
 struct Sync {
-  static __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
-    if constexpr (CT == 1) return mbar_wait(bar, parity);
-    return mbar_wait_cluster(bar, parity);
-  }
-  // an arrival at rank 0's barrier
+  // an arrival at rank 0's barrier, behind this CTA's own writes
   static __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
     if constexpr (CT == 1) mbar_arrive(bar);
-    else mbar_arrive_cluster(map_smem_rank(smem_u32(bar), 0));
+    else mbar_arrive_remote(map_smem_rank(smem_u32(bar), 0));
   }
-  // an arrival at every CTA's
-  static __device__ __forceinline__ void arrive_all(uint64_t* bar) {
-    if constexpr (CT == 1) {
-      mbar_arrive(bar);
-    } else {
-      mbar_arrive_cluster(map_smem_rank(smem_u32(bar), 0));
-      mbar_arrive_cluster(map_smem_rank(smem_u32(bar), 1));
-    }
+  // a wait behind which data of the other CTA is read
+  static __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+    if constexpr (CT == 1) return mbar_wait(bar, parity);
+    else return mbar_wait_cluster(bar, parity);
   }
   static __device__ __forceinline__ void all_threads() {
     if constexpr (CT == 1) __syncthreads();
@@ -234,15 +228,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
   uint64_t* raw_full = empty + NST;
   uint64_t* raw_empty = raw_full + C::NRAW;
   uint64_t* s_full = raw_empty + C::NRAW;  // [2]
-  uint64_t* p_full = s_full + 2;           // (rank 0's)
+  uint64_t* p_full = s_full + 2;           // (pair: each CTA's, for the P that it holds)
   uint64_t* p_empty = p_full + 1;
   uint64_t* q_full = p_empty + 1;          // (rank 0's)
   uint64_t* drained = q_full + 1;
   uint64_t* judged = drained + 1;          // the matrix warp has looked at the P that arrived
-  uint64_t* swapped = judged + 1;          // [2], one per softmax warpgroup
+  uint64_t* p_peer = judged + 1;           // pair: rank 1's P is complete
+  uint64_t* swapped = p_peer + 1;          // [2], one per softmax warpgroup
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::TMEM_OFFSET);
-  volatile uint32_t* left = tmem_at + 1;     // rank 0's: some score of the P that just arrived left its row's range
-  volatile uint32_t* verdict = tmem_at + 2;  // the round (P arrivals so far) that has to be written again
+  volatile uint32_t* verdict = tmem_at + 1;  // the round (P arrivals so far) that has to be written again
+  volatile uint32_t* peer = tmem_at + 2;     // pair, rank 0: whether a flag of rank 1 is set
+  // per softmax warp that writes into this CTA's P: a score left its row's range
+  volatile uint32_t* left = tmem_at + 4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
   const int rank = CT == 1 ? 0 : (int)cluster_ctarank();
 
@@ -259,16 +256,22 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     }
     mbar_init(&s_full[0], 1);
     mbar_init(&s_full[1], 1);
-    mbar_init(p_full, CT * kSoftWarps);
+    mbar_init(p_full, CT == 1 ? kSoftWarps : 4 + 1);
     mbar_init(p_empty, 1);
     mbar_init(q_full, CT * kSoftWarps);
     mbar_init(drained, 1);
     mbar_init(judged, 1);
+    mbar_init(p_peer, 1);
     mbar_init(&swapped[0], CT * 4);
     mbar_init(&swapped[1], CT * 4);
-    *left = 0;
     *verdict = 0;
     fence_barrier_init();
+    if constexpr (CT == 2) {
+      // the first round's bytes from the other CTA
+      mbar_arrive_expect_tx(p_full, C::P_TX);
+      if (rank == 0) mbar_arrive_expect_tx(p_peer, 4);
+      else mbar_arrive_expect_tx(judged, 4);
+    }
   }
   if (tid < N) {
     reinterpret_cast<float*>(smem + C::REF_OFFSET)[tid] = kLow;
@@ -373,7 +376,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       if (ok && lane == 0) {
         const uint32_t bytes = boxes * box_bytes + p.stall_bytes;
         if (CT == 1 || C::FP8) mbar_arrive_expect_tx(&land[st], bytes);
-        else mbar_arrive_expect_tx_cluster(map_smem_rank(smem_u32(&land[st]), 0), bytes);
+        else mbar_arrive_expect_tx_remote(map_smem_rank(smem_u32(&land[st]), 0), bytes);
       }
       __syncwarp();
       return ok;
@@ -449,7 +452,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     const uint64_t p_desc = smem_desc(base + C::P_OFFSET, TT * 128, 8 * C::P_ROW, C::P_ROW);
     int st = 0;
     uint32_t phase = 0, rounds = 0;
-    bool ok = __all_sync(kFullMask, S::wait(q_full, 0));
+    bool ok = __all_sync(kFullMask, mbar_wait(q_full, 0));
     auto next_stage = [&] {
       if (++st == NST) {
         st = 0;
@@ -461,7 +464,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       const uint32_t d = tmem + C::O_COLS + (i & 1) * N;
 #pragma unroll 1
       for (int s = 0; s < KS && ok; ++s) {
-        ok = __all_sync(kFullMask, S::wait(&full[st], phase));
+        ok = __all_sync(kFullMask, mbar_wait(&full[st], phase));
         if (!ok) return;
         tmem_fence_after();
         if (elect_one()) {
@@ -483,26 +486,31 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       if (i + 1 < ntile) qk(i + 1);
       bool refused = true;
       while (ok && refused) {
-        ok = __all_sync(kFullMask, S::wait(p_full, rounds & 1));
+        ok = __all_sync(kFullMask, S::wait(p_full, rounds & 1) && (CT == 1 || S::wait(p_peer, rounds & 1)));
         ++rounds;
         if (!ok) break;
-        refused = *left != 0;
+        refused = __any_sync(kFullMask, lane < 8 && left[lane & 7] != 0);
+        if constexpr (CT == 2) {
+          refused = refused || *peer != 0;
+          fence_proxy_async_smem();  // the rows from the other CTA
+        }
         __syncwarp();
         if (lane == 0) {
-          if (refused) {
-            // P is written again, under references that hold
-            *left = 0;
-            *verdict = rounds;
-            if constexpr (CT == 2) st_dsmem_u32(map_smem_rank(smem_u32(tmem_at + 2), 1), rounds);
+          // a refused P is written again, under references that hold
+          if (refused) *verdict = rounds;
+          if constexpr (CT == 2) {
+            mbar_arrive_expect_tx(p_full, C::P_TX);
+            mbar_arrive_expect_tx(p_peer, 4);
+            st_async_u32(map_smem_rank(smem_u32(tmem_at + 1), 1), refused ? rounds : 0, map_smem_rank(smem_u32(judged), 1));
           }
-          S::arrive_all(judged);
+          mbar_arrive(judged);
         }
         __syncwarp();
       }
       const int steps = min(TT, hi - lo - i * TT) / 16;
 #pragma unroll 1
       for (int s = 0; s < KS && ok; ++s) {
-        ok = __all_sync(kFullMask, S::wait(&full[st], phase));
+        ok = __all_sync(kFullMask, mbar_wait(&full[st], phase));
         if (!ok) break;
         tmem_fence_after();
         if (elect_one()) {
@@ -539,6 +547,28 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       }
       __syncwarp();
     }
+    } else {
+      // rank 1: tells rank 0 of each P that is complete here, and takes the verdict
+      uint32_t rounds = 0;
+      bool ok = true;
+      for (int accepted = 0; accepted < ntile;) {
+        ok = __all_sync(kFullMask, S::wait(p_full, rounds & 1));
+        if (!ok) break;
+        const bool any = __any_sync(kFullMask, lane < 8 && left[lane & 7] != 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_expect_tx(p_full, C::P_TX);
+          st_async_u32(map_smem_rank(smem_u32(tmem_at + 2), 0), any, map_smem_rank(smem_u32(p_peer), 0));
+        }
+        ok = __all_sync(kFullMask, S::wait(judged, rounds & 1));
+        if (!ok) break;
+        ++rounds;
+        if (*verdict != rounds) ++accepted;
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(judged, 4);
+      }
+      if (!ok && lane == 0) atomicOr(p.err, kErrTimeout);
     }
   } else if (warp < kSoftWarps) {
     // ---- softmax: a thread per token lane, warpgroup wg the rows [wg CW, wg CW + CW)
@@ -620,7 +650,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     const int p_tok = rank * kTok + lt;
     const uint32_t p_row = smem_u32(smem + C::P_OFFSET) + p_tok * C::P_ROW +
                            (CT == 1 && N == 128 ? wg * (TT * 128) : 0);
+    const bool here = CT == 1 || wg == rank;  // this CTA holds the rows' P
     const uint32_t p_remote = CT == 2 ? map_smem_rank(p_row, wg) : p_row;
+    const uint32_t p_bar = CT == 2 ? map_smem_rank(smem_u32(p_full), wg) : 0;
     const int p_sw = (p_tok >> kSwShift) & kChunkMask, p_chunk = CT == 2 || N == 128 ? 0 : wg * (CW / 8);
     // two rows' probabilities of this token, packed; sums kept when `add`
     auto prob = [&](const uint32_t (&x)[LD], int c0, int c, const Token& k, bool all, bool add, float& over) {
@@ -636,26 +668,56 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       }
       return pack2<C::FP8>(e[0], e[1]);
     };
-    auto store = [&](const uint32_t (&w)[CW / 2]) {
+    auto store = [&](uint32_t (&w)[CW / 2]) {
+      if constexpr (CT == 2) {
+        if (!here) {
+          // To the other CTA whole 128-byte rows at a time: eight lanes transpose
+          // their eight tokens' eight chunks, lane j then holds chunk j of each
+          // token (lone 16-byte pieces took 4300 cycles a tile).
 #pragma unroll
-      for (int c = 0; c < CW / 8; ++c) {
-        const uint32_t at = p_remote + (((p_chunk + c) ^ p_sw) << 4);
-        const uint4 v = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-        if constexpr (CT == 2) st_dsmem_u32x4(at, v);
-        else sts128_addr(at, v);
+          for (int s = 1; s < 8; s <<= 1) {
+            const bool up = (lane & s) != 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              if (k & s) continue;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                uint32_t& a = w[4 * k + q];
+                uint32_t& b = w[4 * (k | s) + q];
+                const uint32_t got = __shfl_xor_sync(kFullMask, up ? a : b, s);
+                if (up) a = got;
+                else b = got;
+              }
+            }
+          }
+          const int j = lane & 7;
+          const uint32_t at = p_remote - j * C::P_ROW;  // the first of the eight tokens' rows
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            st_async_u32x4(at + k * C::P_ROW + ((j ^ k) << 4),
+                           make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]), p_bar);
+          return;
+        }
       }
+#pragma unroll
+      for (int c = 0; c < CW / 8; ++c)
+        sts128_addr(p_row + (((p_chunk + c) ^ p_sw) << 4),
+                    make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]));
     };
     // P of a tile is complete
     auto publish = [&](bool leaves) {
-      if constexpr (CT == 2) fence_proxy_async_pair();
-      else fence_proxy_async_smem();
+      leaves = __any_sync(kFullMask, leaves);
+      if (here) fence_proxy_async_smem();
       tmem_fence_before();
-      if (__any_sync(kFullMask, leaves) && lane == 0) {
-        if constexpr (CT == 2) st_dsmem_u32(map_smem_rank(smem_u32(tmem_at + 1), 0), 1);
-        else *left = 1;
-      }
       __syncwarp();
-      if (lane == 0) S::arrive_leader(p_full);
+      if (lane == 0) {
+        if (here) {
+          left[CT == 1 ? warp : warp & 3] = leaves;
+          mbar_arrive(p_full);
+        } else {
+          st_async_u32(map_smem_rank(smem_u32(tmem_at + 8 + (warp & 3)), wg), leaves, p_bar);
+        }
+      }
       ++round;
     };
     // Tile i's P was refused: rows that left their range take the tile's true
@@ -681,8 +743,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       }
       __syncwarp();
       if constexpr (CT == 2) {
-        if (lane == 0) S::arrive_all(&swapped[wg]);
-        ok = S::wait(&swapped[wg], swaps & 1) && ok;
+        if (lane < 2) mbar_arrive_cluster(map_smem_rank(smem_u32(&swapped[wg]), lane));
+        ok = mbar_wait_cluster(&swapped[wg], swaps & 1) && ok;
         ++swaps;
         __syncwarp();
       }
@@ -758,7 +820,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
 #pragma unroll 1
     for (int i = 0; i < ntile; ++i) {
       const Token after = token(i + 1);
-      ok = S::wait(&s_full[i & 1], (i >> 1) & 1) && ok;
+      ok = mbar_wait(&s_full[i & 1], (i >> 1) & 1) && ok;
       __syncwarp();
       tmem_fence_after();
       if (i > 0) {
@@ -777,7 +839,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
 #pragma unroll
         for (int c = 0; c < LD; c += 2) w[(c0 + c) / 2] = prob(x, c0, c, now, all, true, over);
       }
-      if (i > 0) ok = S::wait(p_empty, (i - 1) & 1) && ok;
+      if (i > 0) ok = mbar_wait(p_empty, (i - 1) & 1) && ok;
       __syncwarp();
       store(w);
       publish(now.valid && over > C::SLACK);
@@ -785,7 +847,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       now = after;
     }
     if (ok) judge(ntile - 1, before);
-    ok = ok && S::wait(p_empty, (ntile - 1) & 1);
+    ok = ok && mbar_wait(p_empty, (ntile - 1) & 1);
     __syncwarp();
     done = !named_bar_or(bar, 128, !ok);
     if (!done) err |= kErrTimeout;

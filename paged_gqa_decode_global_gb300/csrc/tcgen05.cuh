@@ -143,14 +143,31 @@ __device__ __forceinline__ bool named_bar_or(int id, int nthreads, bool pred) {
   return r != 0;
 }
 
-// ---- a pair's barriers: arrivals from both CTAs, release / acquire at cluster scope
-// `addr`: a barrier's shared::cluster address (map_smem_rank), of either CTA.
+// ---- a pair's barriers. `addr`: a shared::cluster address (map_smem_rank) in either CTA.
+// An arrival that orders nothing but this CTA's own memory: no data of the
+// other CTA hangs on it.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_expect_tx_remote(uint32_t addr, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(addr), "r"(bytes) : "memory");
+}
+// A store into the other CTA that completes its bytes on a barrier of that CTA:
+// whoever sees the barrier's phase complete sees the data. (A release at cluster
+// scope instead, behind plain stores, took 3400 cycles.)
+__device__ __forceinline__ void st_async_u32(uint32_t addr, uint32_t v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr), "r"(v),
+               "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void st_async_u32x4(uint32_t addr, uint4 v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+               "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(bar)
+               : "memory");
+}
+// Release / acquire at cluster scope, for what happens once a piece.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t addr, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(addr), "r"(bytes)
-               : "memory");
 }
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t done;
@@ -185,22 +202,8 @@ __device__ __forceinline__ void tma_load_4d_pair(void* dst, const void* tmap, in
       : "memory");
 }
 
-__device__ __forceinline__ void st_dsmem_u32x4(uint32_t addr, uint4 v) {
-  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
-}
-__device__ __forceinline__ void st_dsmem_u32(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
 __device__ __forceinline__ void max_dsmem_s32(uint32_t addr, int v) {
   asm volatile("red.relaxed.cluster.shared::cluster.max.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-
-// Order this thread's generic-proxy writes of either CTA's shared memory before
-// async-proxy accesses (the fence over all state spaces would also wait for the
-// global loads in flight: ~1500 cycles a tile).
-__device__ __forceinline__ void fence_proxy_async_pair() {
-  asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
 }
 
 }  // namespace pd
