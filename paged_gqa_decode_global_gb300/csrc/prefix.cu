@@ -84,7 +84,7 @@ struct PrefixCfg {
   static constexpr int TOP_OFFSET = REF_OFFSET + N * 4;         // int top[N]: a tile's true maxima
   static constexpr int ROW_OFFSET = TOP_OFFSET + N * 4;         // int row[N]: a tile row's row of q and out
   static constexpr int BAR_OFFSET = ROW_OFFSET + N * 4;
-  static constexpr int NBAR = 2 * NST + 2 * NRAW + 10;
+  static constexpr int NBAR = 2 * NST + 2 * NRAW + 11;
   static constexpr int TMEM_OFFSET = BAR_OFFSET + NBAR * 8;     // tensor memory address, verdict, peer, -, left[8]
   static constexpr int SMEM_BYTES = TMEM_OFFSET + 48 + 1024;
   // pair: what a CTA's P takes from the other CTA a round: 128 tokens' rows, and its warps' flags
@@ -234,7 +234,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
   uint64_t* drained = q_full + 1;
   uint64_t* judged = drained + 1;          // the matrix warp has looked at the P that arrived
   uint64_t* p_peer = judged + 1;           // pair: rank 1's P is complete
-  uint64_t* swapped = p_peer + 1;          // [2], one per softmax warpgroup
+  uint64_t* ref_full = p_peer + 1;         // pair, rank 1: the first references are here
+  uint64_t* swapped = ref_full + 1;        // [2], one per softmax warpgroup
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::TMEM_OFFSET);
   volatile uint32_t* verdict = tmem_at + 1;  // the round (P arrivals so far) that has to be written again
   volatile uint32_t* peer = tmem_at + 2;     // pair, rank 0: whether a flag of rank 1 is set
@@ -262,6 +263,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     mbar_init(drained, 1);
     mbar_init(judged, 1);
     mbar_init(p_peer, 1);
+    mbar_init(ref_full, 1);
     mbar_init(&swapped[0], CT * 4);
     mbar_init(&swapped[1], CT * 4);
     *verdict = 0;
@@ -269,8 +271,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     if constexpr (CT == 2) {
       // the first round's bytes from the other CTA
       mbar_arrive_expect_tx(p_full, C::P_TX);
-      if (rank == 0) mbar_arrive_expect_tx(p_peer, 4);
-      else mbar_arrive_expect_tx(judged, 4);
+      if (rank == 0) {
+        mbar_arrive_expect_tx(p_peer, 4);
+      } else {
+        mbar_arrive_expect_tx(judged, 4);
+        mbar_arrive_expect_tx(ref_full, 4 * N);
+      }
     }
   }
   if (tid < N) {
@@ -803,6 +809,44 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       store(w);
       publish(false);
     };
+    // The first references: the largest of 32 of the first tile's scores (any
+    // within range do, and a refused tile costs ~15 us), by rank 0, whose warp
+    // w takes its own tokens' for a quarter of its group's rows (warp 0 for
+    // all, where the tile is short).
+    auto first_refs = [&](const Token& k) {
+      if (rank == 0) {
+        const bool whole = hi - lo >= kTok;
+        const int from = whole ? (warp & 3) * (CW / 4) : 0;
+        const int to = whole ? from + CW / 4 : (warp & 3) == 0 ? CW : 0;
+        uint32_t x[LD];
+#pragma unroll
+        for (int c0 = 0; c0 < CW; c0 += LD) {
+          tmem_ld(x, quarter + C::O_COLS + wg * CW + c0);
+          tmem_wait_ld();
+          int mine = kNoTop;
+#pragma unroll
+          for (int c = 0; c < LD; ++c) {
+            if (c0 + c < from || c0 + c >= to) continue;
+            const int m = __reduce_max_sync(kFullMask, ordered(k.valid ? __uint_as_float(x[c]) * k.sc : -INFINITY));
+            if (lane == c) mine = m;
+          }
+          const int c = c0 + lane;
+          if (lane < LD && c >= from && c < to) {
+            // (no score among them, or an infinite one: left to the first verdict)
+            const float r = fabsf(unordered(mine)) < kLow ? -unordered(mine) : kLow;
+            nref[c] = r;
+            if constexpr (CT == 2)
+              st_async_u32(map_smem_rank(smem_u32(nref + c), 1), __float_as_uint(r),
+                           map_smem_rank(smem_u32(ref_full), 1));
+          }
+        }
+        __syncwarp();
+        named_bar_sync(bar, 128);
+      } else {
+        ok = mbar_wait_cluster(ref_full, 0) && ok;
+        __syncwarp();
+      }
+    };
     // Until tile i's P was accepted. A wait that ran out shows here, to the
     // whole warpgroup at once: its warps leave together.
     auto judge = [&](int i, const Token& k) {
@@ -826,6 +870,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       if (i > 0) {
         judge(i - 1, before);
         if (!ok) break;
+      } else {
+        first_refs(now);
       }
       const uint32_t sa = quarter + C::O_COLS + (i & 1) * N + wg * CW;
       const bool all = __all_sync(kFullMask, now.valid);
