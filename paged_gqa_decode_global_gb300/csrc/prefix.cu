@@ -810,37 +810,35 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       publish(false);
     };
     // The first references: the largest of 32 of the first tile's scores (any
-    // within range do, and a refused tile costs ~15 us), by rank 0, whose warp
-    // w takes its own tokens' for a quarter of its group's rows (warp 0 for
-    // all, where the tile is short).
+    // within range do, and a refused tile costs ~15 us), by rank 0, whose warps
+    // take their own tokens' for every fourth block of 8 of their group's rows
+    // (the first warp for all, where the tile is short). Kept small: it runs
+    // once, out of a cold instruction cache.
     auto first_refs = [&](const Token& k) {
       if (rank == 0) {
         const bool whole = hi - lo >= kTok;
-        const int from = whole ? (warp & 3) * (CW / 4) : 0;
-        const int to = whole ? from + CW / 4 : (warp & 3) == 0 ? CW : 0;
-        uint32_t x[LD];
-#pragma unroll
-        for (int c0 = 0; c0 < CW; c0 += LD) {
+        const int w = warp & 3;
+#pragma unroll 1
+        for (int c0 = whole ? 8 * w : w == 0 ? 0 : CW; c0 < CW; c0 += whole ? 32 : 8) {
+          uint32_t x[8];
           tmem_ld(x, quarter + C::O_COLS + wg * CW + c0);
           tmem_wait_ld();
           int mine = kNoTop;
 #pragma unroll
-          for (int c = 0; c < LD; ++c) {
-            if (c0 + c < from || c0 + c >= to) continue;
+          for (int c = 0; c < 8; ++c) {
             const int m = __reduce_max_sync(kFullMask, ordered(k.valid ? __uint_as_float(x[c]) * k.sc : -INFINITY));
             if (lane == c) mine = m;
           }
-          const int c = c0 + lane;
-          if (lane < LD && c >= from && c < to) {
+          if (lane < 8) {
             // (no score among them, or an infinite one: left to the first verdict)
             const float r = fabsf(unordered(mine)) < kLow ? -unordered(mine) : kLow;
-            nref[c] = r;
+            nref[c0 + lane] = r;
             if constexpr (CT == 2)
-              st_async_u32(map_smem_rank(smem_u32(nref + c), 1), __float_as_uint(r),
+              st_async_u32(map_smem_rank(smem_u32(nref + c0 + lane), 1), __float_as_uint(r),
                            map_smem_rank(smem_u32(ref_full), 1));
           }
+          __syncwarp();
         }
-        __syncwarp();
         named_bar_sync(bar, 128);
       } else {
         ok = mbar_wait_cluster(ref_full, 0) && ok;
@@ -862,14 +860,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
 
     Token now = token(0), before{};
 #pragma unroll 1
-    for (int i = 0; i < ntile; ++i) {
+    for (int i = 0;; ++i) {
       const Token after = token(i + 1);
-      ok = mbar_wait(&s_full[i & 1], (i >> 1) & 1) && ok;
+      if (i < ntile) ok = mbar_wait(&s_full[i & 1], (i >> 1) & 1) && ok;
       __syncwarp();
       tmem_fence_after();
       if (i > 0) {
         judge(i - 1, before);
-        if (!ok) break;
+        if (!ok || i == ntile) break;
       } else {
         first_refs(now);
       }
@@ -892,7 +890,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       before = now;
       now = after;
     }
-    if (ok) judge(ntile - 1, before);
     ok = ok && mbar_wait(p_empty, (ntile - 1) & 1);
     __syncwarp();
     done = !named_bar_or(bar, 128, !ok);
