@@ -22,10 +22,11 @@ constexpr int kMaxContexts = 64;
 
 // Per CUDA context, one bit per kernel instance whose dynamic shared-memory limit
 // has been raised there (a function attribute belongs to the context it was set
-// in): word 0 the stage-1 variants, word 1 the prefix pass's.
+// in): word 0 the stage-1 variants, word 1 the prefix pass's, word 2 the stage-1
+// variants that run beside it.
 struct SmemReady {
   unsigned long long ctx_id;
-  uint64_t bits[2];
+  uint64_t bits[3];
 };
 #define PD_VARIANT_ID_FITS_A_BIT(ID, ...) static_assert((ID) >= 0 && (ID) < 64, "one bit per variant id");
 PD_FOR_EACH_VARIANT(PD_VARIANT_ID_FITS_A_BIT)
@@ -135,7 +136,7 @@ pd_status ensure_smem_attr(int word, int variant, const void* fn, int smem_bytes
       if (g_smem_ready[i].ctx_id == now) e = &g_smem_ready[i];
     if (!e && g_smem_contexts < kMaxContexts) {
       e = &g_smem_ready[g_smem_contexts++];
-      *e = SmemReady{now, {0, 0}};
+      *e = SmemReady{now, {0, 0, 0}};
     }
   }
   if (e) e->bits[word] |= bit;
@@ -144,7 +145,8 @@ pd_status ensure_smem_attr(int word, int variant, const void* fn, int smem_bytes
 
 pd_status stage1(const pd_plan* plan, const void* q, const void* k_pool, const void* v_pool, const float* k_scale,
                  const float* v_scale, const int32_t* block_tables, const int32_t* seq_lens, int32_t window,
-                 float scale, void* workspace, size_t workspace_bytes, void* out, void* stream) {
+                 float scale, void* workspace, size_t workspace_bytes, void* out, void* stream,
+                 bool beside = false) {
   if (!pd::plan_is_valid(plan)) return PD_ERR_INVALID_ARG;
   const pd_layer_desc& ly = plan->layer;
   const bool fp8 = ly.kv_dtype == PD_KV_FP8_E4M3;
@@ -173,9 +175,9 @@ pd_status stage1(const pd_plan* plan, const void* q, const void* k_pool, const v
     if (!v_pool || v_pool == k_pool || !aligned(v_pool, 16)) return PD_ERR_INVALID_ARG;
   }
 
-  const void* fn = pd::stage1_kernel_ptr(plan->variant);
+  const void* fn = beside ? pd::stage1_beside_kernel_ptr(plan->variant) : pd::stage1_kernel_ptr(plan->variant);
   if (!fn) return PD_ERR_INVALID_ARG;
-  pd_status st = ensure_smem_attr(0, plan->variant, fn, plan->smem_bytes);
+  pd_status st = ensure_smem_attr(beside ? 2 : 0, plan->variant, fn, plan->smem_bytes);
   if (st != PD_OK) return st;
 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -276,7 +278,7 @@ pd_status launch_own_part(const pd_plan* plan, const void* q, const void* k_pool
                           const int32_t* seq_lens, float scale, void* workspace, size_t workspace_bytes, void* out,
                           void* stream) {
   return stage1(plan, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens, 0, scale, workspace,
-                workspace_bytes, out, stream);
+                workspace_bytes, out, stream, true);
 }
 
 pd_status encode_group_map(CUtensorMap* map, const void* pool, const pd_layer_desc& ly, int rows, int slabs) {

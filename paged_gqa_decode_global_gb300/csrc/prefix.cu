@@ -108,20 +108,22 @@ struct PrefixCfg {
 };
 
 struct Tile {
-  int group, first, rows, start;
+  int group, first, rows, start, len;
 };
 
-// Row tile z of the launch: its group, first row and rows (group -1: none).
-// Every warp finds it by itself, 32 groups at a time.
+// Row tile z of the launch: its group, first row, rows and prefix length (group
+// -1: none). Every warp finds it by itself, 32 groups at a time.
 __device__ __forceinline__ Tile find_tile(const SharedParams& p, int z) {
   const int lane = threadIdx.x & 31, per_req = p.query_tokens * p.group;
   int at = 0;
   for (int g0 = 0; g0 < p.num_groups; g0 += 32) {
     const int g = g0 + lane;
-    int s = 0, rows = 0;
+    int s = 0, rows = 0, len = 0;
     if (g < p.num_groups) {
-      s = max(0, min(__ldg(p.group_starts + g), p.batch));
-      rows = (max(s, min(__ldg(p.group_starts + g + 1), p.batch)) - s) * per_req;
+      const int a = __ldg(p.group_starts + g), b = __ldg(p.group_starts + g + 1);
+      len = __ldg(p.prefix_lens + g);
+      s = max(0, min(a, p.batch));
+      rows = (max(s, min(b, p.batch)) - s) * per_req;
     }
     const int n = (rows + p.row_tile - 1) / p.row_tile;
     int end = n;
@@ -139,11 +141,12 @@ __device__ __forceinline__ Tile find_tile(const SharedParams& p, int z) {
       t.first = (z - __shfl_sync(kFullMask, end - n, src)) * p.row_tile;
       t.rows = min(p.row_tile, __shfl_sync(kFullMask, rows, src) - t.first);
       t.start = __shfl_sync(kFullMask, s, src);
+      t.len = __shfl_sync(kFullMask, len, src);
       return t;
     }
     at = __shfl_sync(kFullMask, end, 31);
   }
-  return Tile{-1, 0, 0, 0};
+  return Tile{-1, 0, 0, 0, 0};
 }
 
 // Whether the device's group starts cut the batch, in no more row tiles than planned (one warp).
@@ -285,23 +288,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
   }
   __syncwarp();
   if (warp == 8) tmem_alloc<CT>(tmem_at, C::TMEM_COLS);
+  // behind whatever wrote what this grid reads; the own part's stage 1 behind
+  // this grid may start once every thread here has waited
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int piece = blockIdx.y, g = blockIdx.z;
+  const Tile t = find_tile(p, blockIdx.x / CT);
   tmem_fence_before();
   S::all_threads();
   tmem_fence_after();
   const uint32_t tmem = *tmem_at;
-  // launched behind the own part's stage 1, whose threads let this grid start
-  // only after their own wait: all that both read is in place, and nothing here
-  // depends on stage 1 itself, so this grid waits for it only as it ends (the
-  // join behind it relies on both)
-  grid_launch_dependents();
-
-  const int piece = blockIdx.y, g = blockIdx.z;
   if (blockIdx.x == 0 && piece == 0 && g == 0 && warp == 0 && !groups_ok(p) && lane == 0)
     atomicOr(p.err, kErrBadGroup);
-  const Tile t = find_tile(p, blockIdx.x / CT);
-  int L = 0;
+  int L = t.len;
   if (t.group >= 0) {
-    L = __ldg(p.prefix_lens + t.group);
     const int cap = p.max_prefix_pages * p.page_size;
     if (L < 0 || L > cap || L % p.page_size != 0) {
       if (tid == 0) atomicOr(p.err, kErrBadSeqLen);
@@ -323,7 +323,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
         p.lse_part[(size_t)row_of(p, t, r, g) * p.num_pieces + piece] = -INFINITY;
     S::all_threads();
     if (warp == 8) tmem_dealloc<CT>(tmem, C::TMEM_COLS);
-    grid_dependency_wait();
     return;
   }
 
@@ -421,9 +420,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
         end();
       }
     };
-    int k_next = k_group(0), v_at = v_group(0);
-    load_k(k_next);
-    k_next = k_group(1);
+    load_k(k_group(0));
+    int k_next = k_group(1), v_at = v_group(0);
 #pragma unroll 1
     for (int i = 0; i < ntile && ok; ++i) {
       const int k_after = k_group(i + 2), v_next = v_group(i + 1);
@@ -1003,7 +1001,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
   tmem_fence_before();
   S::all_threads();
   if (warp == 8) tmem_dealloc<CT>(tmem, C::TMEM_COLS);
-  grid_dependency_wait();
 }
 
 #define PD_FOR_EACH_PREFIX(X)                                                                          \

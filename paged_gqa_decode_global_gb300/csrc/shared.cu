@@ -34,18 +34,19 @@ constexpr int kJoinThreads = 128;
 constexpr int kJoinMaxPieces = 2048;  // both parts' caps
 constexpr int kJoinAhead = 8;         // pieces whose rows a thread has in flight
 
-// One CTA per row. The weights first (a thread per piece), then float4 column
-// `tid % (D / 4)` over the pieces tid / (D / 4), + 512 / D, ...; the piece
-// groups of a column are summed in shared memory. The first kJoinAhead rows of
-// each thread load together with the log-sum-exps.
-template <int D>
+// A CTA per row and COLS float4 columns of it. The weights first (a thread per
+// piece), then column `tid % COLS` over the pieces tid / COLS, + 128 / COLS, ...;
+// the piece groups of a column are summed in shared memory. The first
+// kJoinAhead rows of each thread load together with the log-sum-exps.
+template <int D, int COLS>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p) {
-  constexpr int COLS = D / 4, GROUPS = kJoinThreads / COLS;
+  constexpr int GROUPS = kJoinThreads / COLS;
   __shared__ float wt[kJoinMaxPieces], red[2][4];
   __shared__ float4 part[GROUPS > 1 ? kJoinThreads : 1];
   grid_dependency_wait();
   grid_launch_dependents();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, col = tid % COLS, grp = tid / COLS;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, at = tid % COLS, grp = tid / COLS;
+  const int col = blockIdx.y * COLS + at;
   const size_t row = blockIdx.x;
   const int s0 = p.pieces[0], total = s0 + p.pieces[1];
   auto rows = [&](int s) {
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p) 
     if (grp != 0) return;
 #pragma unroll
     for (int k = 1; k < GROUPS; ++k) {
-      const float4 v = part[k * COLS + col];
+      const float4 v = part[k * COLS + at];
       acc.x += v.x;
       acc.y += v.y;
       acc.z += v.z;
@@ -175,13 +176,13 @@ bool shared_plan_is_valid(const pd_shared_plan* plan) {
 }
 
 // What the cost model takes of the prefix pass, in microseconds on a 152-SM
-// GB300: a CTA's start and end, and a tile of 128 tokens (measured at head_dim
-// 512 with few CTAs, in proportion to head_dim); the tiles in flight share the
-// memory's rate, and the pieces' partial results are written and read once.
-constexpr double kFixedUs = 9.0, kTileUs = 3.4, kTileFp8Us = 5.0, kHbmBytesPerUs = 6.8e6, kPartialBytesPerUs = 5.0e6;
+// GB300: a CTA's start and end, and a tile (128 tokens; a pair's 256), measured
+// at head_dim 512 and in proportion to head_dim below; the tiles in flight share
+// the memory's rate, and the pieces' partial results are written and read once.
+constexpr double kFixedUs = 9.0, kHbmBytesPerUs = 6.8e6, kPartialBytesPerUs = 5.0e6;
 
-double tile_us(const pd_layer_desc& ly) {
-  return (ly.kv_dtype == PD_KV_FP8_E4M3 ? kTileFp8Us : kTileUs) * ly.head_dim / 512.0;
+double tile_us(const PrefixInstance& v) {
+  return (v.ctas == 2 ? (v.fp8 ? 6.5 : 3.7) : (v.fp8 ? 4.5 : 3.3)) * v.head_dim / 512.0;
 }
 
 // The prefix's pieces: of every count of pieces for the longest prefix, the one
@@ -195,7 +196,7 @@ void plan_pieces(pd_shared_plan& sp, const int32_t* starts, const int32_t* lens,
   sp.chunk_tokens = unit;
   sp.num_pieces = 1;
   if (most <= 1) return;
-  const double cta_us = tile_us(ly);
+  const double cta_us = tile_us(kPrefixInstances[sp.variant]);
   const double tile_bytes = (double)unit * ly.head_dim * (ly.kv_dtype == PD_KV_FP8_E4M3 ? 1 : 2) *
                             (ly.kv_shared ? 1 : 2);
   const double rows = (double)sp.own.batch * sp.own.query_tokens * ly.num_q_heads;
@@ -225,17 +226,25 @@ void plan_pieces(pd_shared_plan& sp, const int32_t* starts, const int32_t* lens,
   }
 }
 
-// Alone, the own part would be cut to fill the SMs; beside the prefix pass,
-// whose CTAs take every SM it leaves free, each further CTA only adds its fixed
-// time. So its pieces grow to what a prefix CTA takes.
-void shorten_own(pd_shared_plan& sp, const int32_t* lens) {
+// Alone, the own part is cut to fill the SMs. Where the prefix pass leaves SMs
+// free for long enough to take the whole own part beside it, each further piece
+// only adds its fixed time: its pieces then grow to what a prefix CTA takes.
+void shorten_own(pd_shared_plan& sp, const int32_t* starts, const int32_t* prefix, const int32_t* lens, int per_req,
+                 int sm_count) {
   pd_plan& own = sp.own;
   const pd_layer_desc& ly = own.layer;
   int longest = 0;
   for (int b = 0; b < own.batch; ++b) longest = std::max(longest, lens[b]);
   if (own.num_splits <= 1 || longest <= 0 || sp.max_prefix_len == 0) return;
-  const double us = kFixedUs + sp.chunk_tokens / kPrefixTile * tile_us(ly);
+  const PrefixInstance& v = kPrefixInstances[sp.variant];
+  const double us = kFixedUs + sp.chunk_tokens / (kPrefixTile * v.ctas) * tile_us(v);
   const double per_us = 50.0 * 512 / ly.head_dim;  // tokens of a lone stage-1 CTA
+  double prefix_ctas = 0, own_us = 0;
+  for (int n = 0; n < sp.num_groups; ++n)
+    prefix_ctas += (double)(((long long)(starts[n + 1] - starts[n]) * per_req + sp.row_tile - 1) / sp.row_tile) *
+                   ((prefix[n] + sp.chunk_tokens - 1) / sp.chunk_tokens) * ly.num_kv_heads * v.ctas;
+  for (int b = 0; b < own.batch; ++b) own_us += (5.0 + lens[b] / per_us) * own.grid_y;
+  if ((sm_count - prefix_ctas) * us < own_us) return;
   const int chunk = std::max(own.chunk_tokens, (int)(us * per_us) / 64 * 64);
   own.chunk_tokens = std::min(chunk, (longest + 63) / 64 * 64);
   own.num_splits = (longest + own.chunk_tokens - 1) / own.chunk_tokens;
@@ -284,7 +293,7 @@ pd_status plan_shared(const pd_layer_desc* layer, int32_t batch, int32_t query_t
   if (tiles > 65535) return PD_ERR_UNSUPPORTED;
   sp.tiles = (int32_t)tiles;
   plan_pieces(sp, group_starts_host, prefix_lens_host, per_req, sm_count);
-  shorten_own(sp, seq_lens_host);
+  shorten_own(sp, group_starts_host, prefix_lens_host, seq_lens_host, per_req, sm_count);
   const uint64_t rows = (uint64_t)batch * query_tokens * ly.num_q_heads;
   if (rows > 0x7fffffffull) return PD_ERR_UNSUPPORTED;
   sp.lse_offset = align_up(sp.own.workspace_bytes, 256);
@@ -381,14 +390,14 @@ pd_status decode_shared(const pd_shared_plan* plan, bool fp8, const void* q, con
   if (st == PD_OK) st = encode_group_map(&p.kmap, k_pool, ly, p.k_box, fp8 ? 1 : 2);
   if (st == PD_OK) st = encode_group_map(&p.vmap, ly.kv_shared ? k_pool : v_pool, ly, p.v_box, slabs);
   if (st != PD_OK) return st;
-  // the own part first: the prefix pass starts on the SMs it leaves free
-  st = launch_own_part(&own, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens, scale, workspace,
-                       workspace_bytes, out, stream);
-  if (st != PD_OK) return st;
   void* args[] = {&p};
   if (plan->tiles > 0 && launch_dependent(fn, dim3(plan->tiles * v.ctas, plan->num_pieces, ly.num_kv_heads), v.threads,
                                           v.smem_bytes, stream, args, v.ctas) != cudaSuccess)
     return PD_ERR_CUDA;
+  // the own part's CTAs take the SMs that the prefix pass leaves free
+  st = launch_own_part(&own, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens, scale, workspace,
+                       workspace_bytes, out, stream);
+  if (st != PD_OK) return st;
   JoinParams j = {};
   j.lse[0] = reinterpret_cast<const float*>(ws + own.lse_offset);
   j.o[0] = reinterpret_cast<const float*>(ws + own.opart_offset);
@@ -399,10 +408,18 @@ pd_status decode_shared(const pd_shared_plan* plan, bool fp8, const void* q, con
   j.out = static_cast<uint16_t*>(out);
   const unsigned rows = (unsigned)own.batch * own.query_tokens * ly.num_q_heads;
   void* jargs[] = {&j};
-  const void* join = ly.head_dim == 512   ? reinterpret_cast<const void*>(&join_kernel<512>)
-                     : ly.head_dim == 256 ? reinterpret_cast<const void*>(&join_kernel<256>)
-                                          : reinterpret_cast<const void*>(&join_kernel<128>);
-  if (launch_dependent(join, dim3(rows), kJoinThreads, 0, stream, jargs) != cudaSuccess) return PD_ERR_CUDA;
+  // few rows of many pieces: a CTA per 128 dims, its threads on four pieces at a
+  // time (256 rows of 25 pieces: 13.4 -> 6 us); otherwise whole rows a CTA
+  const bool wide = rows >= 2048 || j.pieces[0] + j.pieces[1] <= 2 * kJoinAhead;
+  const void* join = nullptr;
+  if (ly.head_dim == 512)
+    join = wide ? reinterpret_cast<const void*>(&join_kernel<512, 128>) : reinterpret_cast<const void*>(&join_kernel<512, 32>);
+  else if (ly.head_dim == 256)
+    join = wide ? reinterpret_cast<const void*>(&join_kernel<256, 64>) : reinterpret_cast<const void*>(&join_kernel<256, 32>);
+  else
+    join = reinterpret_cast<const void*>(&join_kernel<128, 32>);
+  if (launch_dependent(join, dim3(rows, wide ? 1 : ly.head_dim / 128), kJoinThreads, 0, stream, jargs) != cudaSuccess)
+    return PD_ERR_CUDA;
   return PD_OK;
 }
 

@@ -47,7 +47,7 @@ const void* prefix_kernel_ptr(int variant);
 bool plan_is_valid(const pd_plan* plan);
 pd_status plan_own_part(const pd_layer_desc* layer, int32_t batch, int32_t query_tokens,
                         const int32_t* seq_lens_host, int32_t sm_count, pd_plan* plan);
-// abi.cu: stage 1 of the own part into the workspace
+// abi.cu: stage 1 of the own part into the workspace, beside the prefix pass launched in front of it
 pd_status launch_own_part(const pd_plan* plan, const void* q, const void* k_pool, const void* v_pool,
                           const float* k_scale, const float* v_scale, const int32_t* block_tables,
                           const int32_t* seq_lens, float scale, void* workspace, size_t workspace_bytes, void* out,

@@ -194,7 +194,11 @@ constexpr int kMergeNothing = 0;   // not waited at the cluster barrier; the CTA
 constexpr int kMergePushed = 1;    // waited there, and the CTA's result went out (rank 0: stayed local)
 constexpr int kMergeToWait = 2;    // not waited; the CTA's result went out (the producer warp)
 
-template <class C>
+// BESIDE: the instances of the own part of a shared-prefix decode, launched
+// behind a grid that lets this one start only after its own wait and whose
+// results this one does not read: nobody waits here, and the last CTA waits as
+// it ends (in the kernel below), so that this grid completes after that one.
+template <class C, bool BESIDE>
 __device__ __forceinline__ int stage1_cta(const Stage1Params& p, uint8_t* smem) {
   uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + C::BAR_OFFSET);
   uint64_t* empty_bar = full_bar + C::NST;
@@ -213,7 +217,7 @@ __device__ __forceinline__ int stage1_cta(const Stage1Params& p, uint8_t* smem) 
   // first copy that has to wait for a free stage, and before it leaves. It
   // writes nothing to global memory before that wait: a bad page id it meets
   // is recorded in a register and reaches the error word afterwards.
-  const bool early = p.early_kv != 0 && threadIdx.x >= C::NW * 32;
+  const bool early = !BESIDE && p.early_kv != 0 && threadIdx.x >= C::NW * 32;
   if (threadIdx.x == C::NW * 32) {
     prefetch_tensormap(&p.kmap);
     if (!C::KVS) prefetch_tensormap(&p.vmap);
@@ -224,7 +228,7 @@ __device__ __forceinline__ int stage1_cta(const Stage1Params& p, uint8_t* smem) 
     }
     fence_barrier_init();
   }
-  if (!early) grid_dependency_wait();
+  if (!BESIDE && !early) grid_dependency_wait();
 
   const ColMap<C> cm(p);
   const int split = blockIdx.x;
@@ -1172,29 +1176,46 @@ __device__ __forceinline__ void cluster_merge(const Stage1Params& p, uint8_t* sm
   }
 }
 
-template <class C>
+template <class C, bool BESIDE>
 __global__ void __launch_bounds__(C::THREADS, 1) stage1_kernel(const __grid_constant__ Stage1Params p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // the swizzle pattern repeats every 1024 bytes of shared address: start there
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   if (C::DED_SLOTS > 0 && p.cluster_merge == 2) cluster_arrive_relaxed();  // this CTA has started
-  const int state = stage1_cta<C>(p, smem);
-  if (p.cluster_merge) cluster_merge<C>(p, smem, state);
+  const int state = stage1_cta<C, BESIDE>(p, smem);
+  if constexpr (BESIDE) {
+    // (its pieces are always left in the workspace)
+    if (blockIdx.x + 1 == gridDim.x && blockIdx.y + 1 == gridDim.y && blockIdx.z + 1 == gridDim.z)
+      grid_dependency_wait();
+  } else {
+    if (p.cluster_merge) cluster_merge<C>(p, smem, state);
+  }
 }
 
 // ---- instantiation and dispatch -------------------------------------------------
 
-#define PD_STAGE1_INSTANCE(ID, D, G, KVS, KV8, NW, SPW, MQ, NSUB, TW)                       \
-  template __global__ void stage1_kernel<Stage1Cfg<D, G, KVS, KV8, NW, SPW, MQ, NSUB, TW>>( \
+// (stage1_beside.cu compiles this file a second time, for the BESIDE instances)
+#ifdef PD_STAGE1_BESIDE
+constexpr bool kBeside = true;
+#else
+constexpr bool kBeside = false;
+#endif
+
+#define PD_STAGE1_INSTANCE(ID, D, G, KVS, KV8, NW, SPW, MQ, NSUB, TW)                                \
+  template __global__ void stage1_kernel<Stage1Cfg<D, G, KVS, KV8, NW, SPW, MQ, NSUB, TW>, kBeside>( \
       const __grid_constant__ Stage1Params);
 PD_FOR_EACH_VARIANT(PD_STAGE1_INSTANCE)
 #undef PD_STAGE1_INSTANCE
 
+#ifdef PD_STAGE1_BESIDE
+const void* stage1_beside_kernel_ptr(int variant) {
+#else
 const void* stage1_kernel_ptr(int variant) {
+#endif
   switch (variant) {
 #define PD_STAGE1_CASE(ID, D, G, KVS, KV8, NW, SPW, MQ, NSUB, TW) \
   case ID:                                                        \
-    return reinterpret_cast<const void*>(&stage1_kernel<Stage1Cfg<D, G, KVS, KV8, NW, SPW, MQ, NSUB, TW>>);
+    return reinterpret_cast<const void*>(&stage1_kernel<Stage1Cfg<D, G, KVS, KV8, NW, SPW, MQ, NSUB, TW>, kBeside>);
     PD_FOR_EACH_VARIANT(PD_STAGE1_CASE)
 #undef PD_STAGE1_CASE
     default:
