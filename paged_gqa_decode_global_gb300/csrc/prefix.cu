@@ -105,6 +105,7 @@ struct PrefixCfg {
   static_assert(NST >= 3 && (!FP8 || NRAW >= 2), "rings");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
   static_assert(2 * SUM_FLOATS * 4 + 2 * N * 4 <= NST * kStage, "the row sums are reduced in the ring");
+  static_assert(N * MC * 128 * 4 <= NST * kStage + NRAW * kRaw, "the partial rows leave through the rings");
 };
 
 struct Tile {
@@ -977,24 +978,32 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     }
   }
   __syncthreads();
-  if (warp < kSoftWarps && done) {
-    constexpr int OC = CW < 16 ? CW : 16;
+  if (warp < kSoftWarps && done && wg * CW < t.rows) {
+    // The partial rows go through shared memory (the rings, idle by now), a row
+    // of this CTA's dims contiguous, and out as one bulk copy each: stored from
+    // the registers, 128 bytes a warp, 128 rows took 4 us.
+    constexpr int OC = CW < 16 ? CW : 16, ROW = C::MC * 128;
+    float* stage = reinterpret_cast<float*>(smem + C::RING_OFFSET) + wg * CW * ROW;
+    const int n = min(CW, t.rows - wg * CW);
 #pragma unroll 1
-    for (int c0 = 0; c0 < CW; c0 += OC) {
-      if (wg * CW + c0 >= t.rows) break;
+    for (int c0 = 0; c0 < n; c0 += OC) {
       uint32_t y[C::MC][OC];
 #pragma unroll
       for (int m = 0; m < C::MC; ++m) tmem_ld(y[m], o_at + m * N + c0);
       tmem_wait_ld();
 #pragma unroll
       for (int c = 0; c < OC; ++c) {
-        const int r = rows[wg * CW + c0 + c];
-        if (r < 0) break;
-        float* dst = p.o_part + ((size_t)r * p.num_pieces + piece) * D + rank * (C::MC * 128) + lt;
         const float f = nref[c0 + c];
 #pragma unroll
-        for (int m = 0; m < C::MC; ++m) dst[m * 128] = __uint_as_float(y[m][c]) * f;
+        for (int m = 0; m < C::MC; ++m) stage[(c0 + c) * ROW + m * 128 + lt] = __uint_as_float(y[m][c]) * f;
       }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    named_bar_sync(bar, 128);
+    if (lt < n) {
+      bulk_s2g(p.o_part + ((size_t)rows[wg * CW + lt] * p.num_pieces + piece) * D + rank * ROW, stage + lt * ROW, ROW * 4);
+      wait_bulk_stores();
     }
   }
   __syncwarp();

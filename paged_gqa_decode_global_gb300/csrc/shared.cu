@@ -180,15 +180,25 @@ bool shared_plan_is_valid(const pd_shared_plan* plan) {
 // at head_dim 512 and in proportion to head_dim below; the tiles in flight share
 // the memory's rate, and the pieces' partial results are written and read once.
 constexpr double kFixedUs = 9.0, kHbmBytesPerUs = 6.8e6, kPartialBytesPerUs = 5.0e6;
+constexpr double kOwnFixedUs = 5.0;  // a stage-1 CTA of the own part
 
 double tile_us(const PrefixInstance& v) {
-  return (v.ctas == 2 ? (v.fp8 ? 6.5 : 3.7) : (v.fp8 ? 4.5 : 3.3)) * v.head_dim / 512.0;
+  return (v.ctas == 2 ? (v.fp8 ? 7.0 : 3.8) : (v.fp8 ? 4.5 : 3.4)) * v.head_dim / 512.0;
+}
+
+// SM time of the own part in one piece a request, in microseconds.
+double own_sm_us(const pd_plan& own, const int32_t* lens) {
+  const double per_us = 50.0 * 512 / own.layer.head_dim;  // tokens of a lone stage-1 CTA
+  double us = 0;
+  for (int b = 0; b < own.batch; ++b) us += (kOwnFixedUs + lens[b] / per_us) * own.grid_y;
+  return us;
 }
 
 // The prefix's pieces: of every count of pieces for the longest prefix, the one
 // whose launch is modelled to end first. More pieces fill the SMs and even out
 // prefixes of different lengths; each costs a CTA's fixed time and its partials.
-void plan_pieces(pd_shared_plan& sp, const int32_t* starts, const int32_t* lens, int per_req, int sm_count) {
+void plan_pieces(pd_shared_plan& sp, const int32_t* starts, const int32_t* lens, int per_req, int sm_count,
+                 double own_us) {
   const pd_layer_desc& ly = sp.own.layer;
   const int unit = kPrefixTile * kPrefixInstances[sp.variant].ctas;  // tokens of a tile
   const int slots = sm_count / kPrefixInstances[sp.variant].ctas;
@@ -213,9 +223,11 @@ void plan_pieces(pd_shared_plan& sp, const int32_t* starts, const int32_t* lens,
       if (row_tiles > 0) distinct += (double)ly.num_kv_heads * len;
     }
     const double one = kFixedUs + c * cta_us;
-    const double all = (ctas * kFixedUs + tiles * cta_us) / slots;
-    // within one wave the longest CTA; beyond, the mean load and part of a last one
-    double us = ctas <= slots ? one : std::max(one, all + 0.4 * one);
+    // within one wave the longest CTA; beyond, the mean load and part of a last
+    // one; and what the own part finds free
+    const double load = (ctas * kFixedUs + tiles * cta_us) / slots;
+    double us = ctas <= slots ? one : std::max(one, load + 0.4 * one);
+    us = std::max(us, load + own_us / sm_count + kOwnFixedUs);
     us = std::max(us, kFixedUs + distinct * tile_bytes / kHbmBytesPerUs) +
          2.0 * rows * pieces * ly.head_dim * 4.0 / kPartialBytesPerUs;
     if (us < best) {
@@ -230,7 +242,7 @@ void plan_pieces(pd_shared_plan& sp, const int32_t* starts, const int32_t* lens,
 // free for long enough to take the whole own part beside it, each further piece
 // only adds its fixed time: its pieces then grow to what a prefix CTA takes.
 void shorten_own(pd_shared_plan& sp, const int32_t* starts, const int32_t* prefix, const int32_t* lens, int per_req,
-                 int sm_count) {
+                 int sm_count, double own_us) {
   pd_plan& own = sp.own;
   const pd_layer_desc& ly = own.layer;
   int longest = 0;
@@ -239,11 +251,10 @@ void shorten_own(pd_shared_plan& sp, const int32_t* starts, const int32_t* prefi
   const PrefixInstance& v = kPrefixInstances[sp.variant];
   const double us = kFixedUs + sp.chunk_tokens / (kPrefixTile * v.ctas) * tile_us(v);
   const double per_us = 50.0 * 512 / ly.head_dim;  // tokens of a lone stage-1 CTA
-  double prefix_ctas = 0, own_us = 0;
+  double prefix_ctas = 0;
   for (int n = 0; n < sp.num_groups; ++n)
     prefix_ctas += (double)(((long long)(starts[n + 1] - starts[n]) * per_req + sp.row_tile - 1) / sp.row_tile) *
                    ((prefix[n] + sp.chunk_tokens - 1) / sp.chunk_tokens) * ly.num_kv_heads * v.ctas;
-  for (int b = 0; b < own.batch; ++b) own_us += (5.0 + lens[b] / per_us) * own.grid_y;
   if ((sm_count - prefix_ctas) * us < own_us) return;
   const int chunk = std::max(own.chunk_tokens, (int)(us * per_us) / 64 * 64);
   own.chunk_tokens = std::min(chunk, (longest + 63) / 64 * 64);
@@ -292,8 +303,9 @@ pd_status plan_shared(const pd_layer_desc* layer, int32_t batch, int32_t query_t
     tiles += ((long long)(group_starts_host[n + 1] - group_starts_host[n]) * per_req + sp.row_tile - 1) / sp.row_tile;
   if (tiles > 65535) return PD_ERR_UNSUPPORTED;
   sp.tiles = (int32_t)tiles;
-  plan_pieces(sp, group_starts_host, prefix_lens_host, per_req, sm_count);
-  shorten_own(sp, group_starts_host, prefix_lens_host, seq_lens_host, per_req, sm_count);
+  const double own_us = own_sm_us(sp.own, seq_lens_host);
+  plan_pieces(sp, group_starts_host, prefix_lens_host, per_req, sm_count, own_us);
+  shorten_own(sp, group_starts_host, prefix_lens_host, seq_lens_host, per_req, sm_count, own_us);
   const uint64_t rows = (uint64_t)batch * query_tokens * ly.num_q_heads;
   if (rows > 0x7fffffffull) return PD_ERR_UNSUPPORTED;
   sp.lse_offset = align_up(sp.own.workspace_bytes, 256);
