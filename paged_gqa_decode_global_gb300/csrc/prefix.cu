@@ -85,7 +85,7 @@ struct PrefixCfg {
   static constexpr int ROW_OFFSET = TOP_OFFSET + N * 4;         // int row[N]: a tile row's row of q and out
   static constexpr int BAR_OFFSET = ROW_OFFSET + N * 4;
   static constexpr int NBAR = 2 * NST + 2 * NRAW + 11;
-  static constexpr int TMEM_OFFSET = BAR_OFFSET + NBAR * 8;     // tensor memory address, verdict, peer, -, left[8]
+  static constexpr int TMEM_OFFSET = (BAR_OFFSET + NBAR * 8 + 15) / 16 * 16;  // tensor memory address, verdict, peer, -, left[8]
   static constexpr int SMEM_BYTES = TMEM_OFFSET + 48 + 1024;
   // pair: what a CTA's P takes from the other CTA a round: 128 tokens' rows, and its warps' flags
   static constexpr int P_TX = kTok * QN * 2 + 16;
@@ -444,137 +444,137 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     if (lane == 0 && err) atomicOr(p.err, err);
   } else if (warp == 8) {
     // ---- matrix instructions (rank 0 for both CTAs of a pair): QK(0), then
-    // QK(i + 1) ahead of PV(i). The warp walks the stages together and one
-    // elected lane issues: a lone thread computing descriptors took ~180 cycles
-    // an instruction.
+    // QK(i + 1) ahead of PV(i). One elected lane walks the stages, two at a time:
+    // the tensor core holds little of what is issued ahead, so each look at a
+    // barrier leaves it idle (a stage of 8 instructions: 48 cycles each without,
+    // 59 with one lane's look, 70 where the warp votes).
     constexpr uint32_t kQk = mma_desc_16bit(!C::FP8, TT, N, false, false);
     constexpr uint32_t kPv = mma_desc_16bit(!C::FP8, TT, N, true, true);
-    if (rank == 0) {
-    // descriptors' bases; a step further is a constant added to the address field
-    const uint32_t base = smem_u32(smem);
-    const uint64_t k_desc = smem_desc(base + C::RING_OFFSET, 16, 2048), q_desc = smem_desc(base, 16, 1024);
-    const uint64_t v_desc = smem_desc(base + C::RING_OFFSET, 1024, C::V_ATOMS * 1024);
-    const uint64_t p_desc = smem_desc(base + C::P_OFFSET, TT * 128, 8 * C::P_ROW, C::P_ROW);
-    int st = 0;
-    uint32_t phase = 0, rounds = 0;
-    bool ok = __all_sync(kFullMask, mbar_wait(q_full, 0));
-    auto next_stage = [&] {
-      if (++st == NST) {
-        st = 0;
-        phase ^= 1;
-      }
-    };
-    // the other S buffer is free once P of the tile before last was accepted
-    auto qk = [&](int i) {
-      const uint32_t d = tmem + C::O_COLS + (i & 1) * N;
+    if (rank == 0 && elect_one()) {
+      // descriptors' bases; a step further is a constant added to the address field
+      const uint32_t base = smem_u32(smem);
+      const uint64_t k_desc = smem_desc(base + C::RING_OFFSET, 16, 2048), q_desc = smem_desc(base, 16, 1024);
+      const uint64_t v_desc = smem_desc(base + C::RING_OFFSET, 1024, C::V_ATOMS * 1024);
+      const uint64_t p_desc = smem_desc(base + C::P_OFFSET, TT * 128, 8 * C::P_ROW, C::P_ROW);
+      int st = 0;
+      uint32_t phase = 0, rounds = 0;
+      constexpr int TWO = KS >= 2 ? 2 : 1;  // stages waited for together
+      bool ok = mbar_wait_cluster(q_full, 0);
+      auto next_stage = [&] {
+        if (++st == NST) {
+          st = 0;
+          phase ^= 1;
+        }
+      };
+      auto landed = [&] {
+        if constexpr (TWO == 1) return mbar_wait(&full[st], phase);
+        const int st2 = st + 1 == NST ? 0 : st + 1;
+        return mbar_wait2(&full[st], phase, &full[st2], st2 == 0 ? phase ^ 1 : phase);
+      };
+      // the other S buffer is free once P of the tile before last was accepted
+      auto qk = [&](int i) {
+        const uint32_t d = tmem + C::O_COLS + (i & 1) * N;
 #pragma unroll 1
-      for (int s = 0; s < KS && ok; ++s) {
-        ok = __all_sync(kFullMask, mbar_wait(&full[st], phase));
-        if (!ok) return;
-        tmem_fence_after();
-        if (elect_one()) {
-          const uint64_t a = k_desc + st * (kStage >> 4), b = q_desc + s * 2 * (C::QN * 128 >> 4);
+        for (int s = 0; s < KS && ok; s += TWO) {
+          ok = landed();
+          if (!ok) return;
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_ss<CT>(d, a + (k >> 2) * (1024 >> 4) + (k & 3) * 2, b + (k >> 2) * (C::QN * 128 >> 4) + (k & 3) * 2,
-                       kQk, k != 0 || s != 0);
-          mma_commit<CT>(&empty[st]);
-          if (s == KS - 1) mma_commit<CT>(&s_full[i & 1]);
+          for (int u = 0; u < TWO; ++u) {
+            const uint64_t a = k_desc + st * (kStage >> 4), b = q_desc + (s + u) * 2 * (C::QN * 128 >> 4);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_ss<CT>(d, a + (k >> 2) * (1024 >> 4) + (k & 3) * 2, b + (k >> 2) * (C::QN * 128 >> 4) + (k & 3) * 2,
+                         kQk, k != 0 || u != 0 || s != 0);
+            mma_commit<CT>(&empty[st]);
+            next_stage();
+          }
         }
-        __syncwarp();
-        next_stage();
-      }
-    };
-    qk(0);
+        mma_commit<CT>(&s_full[i & 1]);
+      };
+      qk(0);
 #pragma unroll 1
-    for (int i = 0; i < ntile && ok; ++i) {
-      if (i + 1 < ntile) qk(i + 1);
-      bool refused = true;
-      while (ok && refused) {
-        ok = __all_sync(kFullMask, S::wait(p_full, rounds & 1) && (CT == 1 || S::wait(p_peer, rounds & 1)));
-        ++rounds;
-        if (!ok) break;
-        refused = __any_sync(kFullMask, lane < 8 && left[lane & 7] != 0);
-        if constexpr (CT == 2) {
-          refused = refused || *peer != 0;
-          fence_proxy_async_smem();  // the rows from the other CTA
-        }
-        __syncwarp();
-        if (lane == 0) {
+      for (int i = 0; i < ntile && ok; ++i) {
+        if (i + 1 < ntile) qk(i + 1);
+        bool refused = true;
+        while (ok && refused) {
+          ok = S::wait(p_full, rounds & 1) && (CT == 1 || S::wait(p_peer, rounds & 1));
+          ++rounds;
+          if (!ok) break;
+          const uint4 fa = lds128(tmem_at + 4), fb = lds128(tmem_at + 8);
+          refused = (fa.x | fa.y | fa.z | fa.w | fb.x | fb.y | fb.z | fb.w) != 0;
           // a refused P is written again, under references that hold
-          if (refused) *verdict = rounds;
           if constexpr (CT == 2) {
+            refused = refused || *peer != 0;
+            fence_proxy_async_smem();  // the rows from the other CTA
+            if (refused) *verdict = rounds;
             mbar_arrive_expect_tx(p_full, C::P_TX);
             mbar_arrive_expect_tx(p_peer, 4);
-            st_async_u32(map_smem_rank(smem_u32(tmem_at + 1), 1), refused ? rounds : 0, map_smem_rank(smem_u32(judged), 1));
+            st_async_u32(map_smem_rank(smem_u32(tmem_at + 1), 1), refused ? rounds : 0,
+                         map_smem_rank(smem_u32(judged), 1));
+          } else {
+            if (refused) *verdict = rounds;
           }
           mbar_arrive(judged);
         }
-        __syncwarp();
-      }
-      const int steps = min(TT, hi - lo - i * TT) / 16;
-#pragma unroll 1
-      for (int s = 0; s < KS && ok; ++s) {
-        ok = __all_sync(kFullMask, mbar_wait(&full[st], phase));
-        if (!ok) break;
         tmem_fence_after();
-        if (elect_one()) {
-          const uint64_t a = v_desc + st * (kStage >> 4), b = p_desc + s * (C::VT * C::P_ROW >> 4);
+        const int steps = min(TT, hi - lo - i * TT) / 16;
+#pragma unroll 1
+        for (int s = 0; s < KS && ok; s += TWO) {
+          ok = landed();
+          if (!ok) break;
           // 16 tokens at a time, all of the CTA's head dims
-          auto step = [&](int k, int m) {
+          auto step = [&](uint64_t a, uint64_t b, int k, int m, bool first) {
             mma_ss<CT>(tmem + m * N, a + k * (C::V_ATOMS * 2048 >> 4) + m * (2048 >> 4),
-                       b + k * (16 * C::P_ROW >> 4), kPv, k != 0 || s != 0 || i != 0);
+                       b + k * (16 * C::P_ROW >> 4), kPv, !first || k != 0);
           };
-          if ((s + 1) * (C::VT / 16) <= steps) {
 #pragma unroll
-            for (int k = 0; k < C::VT / 16; ++k)
+          for (int u = 0; u < TWO; ++u) {
+            const uint64_t a = v_desc + st * (kStage >> 4), b = p_desc + (s + u) * (C::VT * C::P_ROW >> 4);
+            const bool first = i == 0 && s + u == 0;
+            if ((s + u + 1) * (C::VT / 16) <= steps) {
 #pragma unroll
-              for (int m = 0; m < C::MC; ++m) step(k, m);
-          } else {
+              for (int k = 0; k < C::VT / 16; ++k)
+#pragma unroll
+                for (int m = 0; m < C::MC; ++m) step(a, b, k, m, first);
+            } else {
 #pragma unroll 1
-            for (int k = 0; s * (C::VT / 16) + k < steps; ++k)
+              for (int k = 0; (s + u) * (C::VT / 16) + k < steps; ++k)
 #pragma unroll 1
-              for (int m = 0; m < C::MC; ++m) step(k, m);
+                for (int m = 0; m < C::MC; ++m) step(a, b, k, m, first);
+            }
+            mma_commit<CT>(&empty[st]);
+            next_stage();
           }
-          mma_commit<CT>(&empty[st]);
-          if (s == KS - 1) mma_commit<CT>(p_empty);
         }
-        __syncwarp();
-        next_stage();
+        if (ok) mma_commit<CT>(p_empty);
       }
-    }
-    if (!ok) {
-      // nothing may still be reading shared memory when the CTA exits
-      if (elect_one()) {
+      if (!ok) {
+        // nothing may still be reading shared memory when the CTA exits
         mma_commit<CT>(drained);
         mbar_wait(drained, 0);
         atomicOr(p.err, kErrTimeout);
       }
-      __syncwarp();
-    }
-    } else {
-      // rank 1: tells rank 0 of each P that is complete here, and takes the verdict
+    } else if (rank == 1 && elect_one()) {
+      // tells rank 0 of each P that is complete here, and takes the verdict
       uint32_t rounds = 0;
       bool ok = true;
       for (int accepted = 0; accepted < ntile;) {
-        ok = __all_sync(kFullMask, S::wait(p_full, rounds & 1));
+        ok = S::wait(p_full, rounds & 1);
         if (!ok) break;
-        const bool any = __any_sync(kFullMask, lane < 8 && left[lane & 7] != 0);
+        const uint4 fa = lds128(tmem_at + 4), fb = lds128(tmem_at + 8);
         fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_expect_tx(p_full, C::P_TX);
-          st_async_u32(map_smem_rank(smem_u32(tmem_at + 2), 0), any, map_smem_rank(smem_u32(p_peer), 0));
-        }
-        ok = __all_sync(kFullMask, S::wait(judged, rounds & 1));
+        mbar_arrive_expect_tx(p_full, C::P_TX);
+        st_async_u32(map_smem_rank(smem_u32(tmem_at + 2), 0), fa.x | fa.y | fa.z | fa.w | fb.x | fb.y | fb.z | fb.w,
+                     map_smem_rank(smem_u32(p_peer), 0));
+        ok = S::wait(judged, rounds & 1);
         if (!ok) break;
         ++rounds;
         if (*verdict != rounds) ++accepted;
-        __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(judged, 4);
+        mbar_arrive_expect_tx(judged, 4);
       }
-      if (!ok && lane == 0) atomicOr(p.err, kErrTimeout);
+      if (!ok) atomicOr(p.err, kErrTimeout);
     }
+    __syncwarp();
   } else if (warp < kSoftWarps) {
     // ---- softmax: a thread per token lane, warpgroup wg the rows [wg CW, wg CW + CW)
     if (tid < N) rows[tid] = tid < t.rows ? row_of(p, t, tid, g) : -1;

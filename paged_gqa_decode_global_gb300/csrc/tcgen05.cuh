@@ -131,6 +131,21 @@ __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[32]) 
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ uint32_t mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done;
+}
+// Two barriers at once: one latency where both are done.
+__device__ __forceinline__ bool mbar_wait2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb) {
+  const uint32_t x = mbar_test(a, pa), y = mbar_test(b, pb);
+  return (x & y) != 0 || (mbar_wait(a, pa) && mbar_wait(b, pb));
+}
+
 // Bulk copy shared -> global (16-byte aligned, a multiple of 16 bytes) in the
 // calling thread's bulk group; wait_bulk_stores: all of them done.
 __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
