@@ -76,8 +76,10 @@ struct PrefixCfg {
   static constexpr int QN = N / CT;        // query rows whose operands a CTA holds
   static constexpr int Q_BYTES = QN * D * 2, P_BYTES = QN * TT * 2;
   static constexpr int ROOM = kBody - Q_BYTES - P_BYTES;
-  static constexpr int NST = FP8 ? 3 : (ROOM / kStage < 6 ? ROOM / kStage : 6);
-  static constexpr int NRAW = FP8 ? ((ROOM - NST * kStage) / kRaw < 6 ? (ROOM - NST * kStage) / kRaw : 6) : 0;
+  // FP8: two operand stages (one filled while the other is used), the rest for
+  // copies in flight: with three, and so 2 raw stages a pair, copies bound it
+  static constexpr int NST = FP8 ? 2 : (ROOM / kStage < 6 ? ROOM / kStage : 6);
+  static constexpr int NRAW = FP8 ? ((ROOM - NST * kStage) / kRaw < 8 ? (ROOM - NST * kStage) / kRaw : 8) : 0;
   static constexpr int Q_OFFSET = 0, P_OFFSET = Q_BYTES, RING_OFFSET = P_OFFSET + P_BYTES;
   static constexpr int RAW_OFFSET = RING_OFFSET + NST * kStage;
   static constexpr int REF_OFFSET = RAW_OFFSET + NRAW * kRaw;   // float nref[N]: negated references
@@ -102,9 +104,9 @@ struct PrefixCfg {
                                    O_COLS + 2 * N <= 256 ? 256 : 512;
   static_assert(CT == 1 || (D == 512 && N == 128), "a pair serves 128 rows at head_dim 512");
   static_assert(O_COLS + 2 * N <= 512, "tensor memory");
-  static_assert(NST >= 3 && (!FP8 || NRAW >= 2), "rings");
+  static_assert(NST >= 2 && (!FP8 || NRAW >= 3), "rings");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
-  static_assert(2 * SUM_FLOATS * 4 + 2 * N * 4 <= NST * kStage, "the row sums are reduced in the ring");
+  static_assert(2 * SUM_FLOATS * 4 + 2 * N * 4 <= NST * kStage + NRAW * kRaw, "the row sums are reduced in the rings");
   static_assert(N * MC * 128 * 4 <= NST * kStage + NRAW * kRaw, "the partial rows leave through the rings");
 };
 
@@ -458,7 +460,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       const uint64_t p_desc = smem_desc(base + C::P_OFFSET, TT * 128, 8 * C::P_ROW, C::P_ROW);
       int st = 0;
       uint32_t phase = 0, rounds = 0;
-      constexpr int TWO = KS >= 2 ? 2 : 1;  // stages waited for together
+      constexpr int TWO = KS >= 2 && !C::FP8 ? 2 : 1;  // stages waited for together
       bool ok = mbar_wait_cluster(q_full, 0);
       auto next_stage = [&] {
         if (++st == NST) {
