@@ -32,7 +32,8 @@
 // Roles: warps 0-7 softmax and epilogue (a thread per token lane, two
 // warpgroups with half the rows each), warp 8 the matrix instructions, warps
 // 9-11 the copies (every third stage each: a lone warp spends ~60 cycles a
-// copy); FP8: warps 12-15 widen the e4m3 stages to f16 operands. K and V arrive
+// copy); FP8: warps 12-15 (up to 32 rows: 12-19) widen the e4m3 stages to f16
+// operands. K and V arrive
 // as [8-token group][64-dim slab][8][128 B] atoms with the 128-byte swizzle:
 // K-major for the first product, and the same layout read M-major for the
 // second, so nothing is transposed; P is written N-major, a token's row at a
@@ -79,7 +80,11 @@ struct PrefixCfg {
   // FP8: two operand stages (one filled while the other is used), the rest for
   // copies in flight: with three, and so 2 raw stages a pair, copies bound it
   static constexpr int NST = FP8 ? 2 : (ROOM / kStage < 6 ? ROOM / kStage : 6);
-  static constexpr int NRAW = FP8 ? ((ROOM - NST * kStage) / kRaw < 8 ? (ROOM - NST * kStage) / kRaw : 8) : 0;
+  static constexpr int NRAW_FIT = (ROOM - NST * kStage) / kRaw < 8 ? (ROOM - NST * kStage) / kRaw : 8;
+  // teams of four widening warps, each with every other stage (of an even
+  // ring); the rows of a large tile leave registers for one
+  static constexpr int TEAMS = N <= 32 ? 2 : 1;
+  static constexpr int NRAW = FP8 ? NRAW_FIT / TEAMS * TEAMS : 0;
   static constexpr int Q_OFFSET = 0, P_OFFSET = Q_BYTES, RING_OFFSET = P_OFFSET + P_BYTES;
   static constexpr int RAW_OFFSET = RING_OFFSET + NST * kStage;
   static constexpr int REF_OFFSET = RAW_OFFSET + NRAW * kRaw;   // float nref[N]: negated references
@@ -91,7 +96,7 @@ struct PrefixCfg {
   static constexpr int SMEM_BYTES = TMEM_OFFSET + 48 + 1024;
   // pair: what a CTA's P takes from the other CTA a round: 128 tokens' rows, and its warps' flags
   static constexpr int P_TX = kTok * QN * 2 + 16;
-  static constexpr int THREADS = 32 * (kSoftWarps + 1 + kCopyWarps + (FP8 ? 4 : 0));
+  static constexpr int THREADS = 32 * (kSoftWarps + 1 + kCopyWarps + (FP8 ? 4 * TEAMS : 0));
   static constexpr int CW = N / 2;         // rows of a softmax warpgroup
   static constexpr int LD = CW < 32 ? CW : 32;
   // P: [QN / 64 blocks][TT tokens][row of up to 64 query rows], swizzled over the row
@@ -930,9 +935,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     }
   } else if constexpr (C::FP8) {
     // ---- FP8: e4m3 stages widened to f16 operand stages, a thread per token row
-    const int row = tid - 32 * (kSoftWarps + 1 + kCopyWarps), sw = row & 7, total = 2 * KS * ntile;
+    const int team = (warp - (kSoftWarps + 1 + kCopyWarps)) / 4;
+    const int row = (tid - 32 * (kSoftWarps + 1 + kCopyWarps)) & 127, sw = row & 7, total = 2 * KS * ntile;
+    static_assert(NST % C::TEAMS == 0 && C::NRAW % C::TEAMS == 0, "a stage always has the same team");
     bool ok = true;
-    for (int it = 0; it < total; ++it) {
+    for (int it = team; it < total; it += C::TEAMS) {
       const int st = it % NST, rs = it % C::NRAW;
       ok = mbar_wait(&raw_full[rs], (it / C::NRAW) & 1);
       if (ok && it >= NST) ok = mbar_wait(&empty[st], ((it / NST) - 1) & 1);
