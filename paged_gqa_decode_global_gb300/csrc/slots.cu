@@ -34,6 +34,7 @@ struct SlotParams {
   uint32_t* flags;
   uint32_t* ticket;  // workspace: CTAs done reading (0 between calls)
   bool wide;         // slot_map and positions take 16-byte stores
+  bool in_place;     // an output is one of the inputs
 };
 
 constexpr int kThreads = 1024;
@@ -106,9 +107,11 @@ __device__ __forceinline__ void place(const SlotParams& p, const Round& rd, int 
 
 // A CTA serves TPT * 1024 entries of slot_map, but scans the lengths of every
 // request up to its last token (at most a few rounds of 1024): with B requests
-// in L2 that costs less than a launch of its own for the sums. The lengths may
-// be updated in place, so they are written by the CTA that is last to have read
-// them (the only one, for a batch of few tokens).
+// in L2 that costs less than a launch of its own for the sums (12.5 us as two
+// launches). Bound: the chain of dependent loads, ~4 us for a decode step of
+// 256 requests. The first CTA writes the results per request; where they
+// update the inputs in place and other CTAs read those too, the CTA that is
+// last to have read them does, in a second walk (~3 us).
 template <int TPT>
 __global__ void __launch_bounds__(kThreads) slots_kernel(const SlotParams p) {
   __shared__ Round rd;
@@ -233,8 +236,8 @@ __global__ void __launch_bounds__(kThreads) slots_kernel(const SlotParams p) {
       }
     }
   };
-  if (only) {
-    walk(true, true);
+  if (only || !p.in_place) {
+    walk(true, blockIdx.x == 0);
     return;
   }
   walk(true, false);
@@ -300,9 +303,9 @@ pd_status paged_decode_append_slots(int32_t batch, int32_t page_size, int32_t nu
   p.flags = device_flags;
   p.ticket = static_cast<uint32_t*>(workspace);
   p.wide = pd::aligned(slot_map, 16) && pd::aligned(positions, 16);
-  // one entry a thread while a few CTAs hold them all (a decode step: one CTA,
-  // no counter), four (16-byte stores) from 16384 on
-  const int per_thread = max_tokens >= 16384 ? 4 : 1;
+  p.in_place = seq_lens == cached_lens || free_range_out == free_range;
+  // one entry a thread for a decode step (one CTA), four (16-byte stores) above
+  const int per_thread = max_tokens > pd::kThreads ? 4 : 1;
   const long long per_cta = (long long)per_thread * pd::kThreads;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)std::max<long long>(1, (max_tokens + per_cta - 1) / per_cta));
