@@ -368,3 +368,66 @@ def test_random_shapes(seed):
     Case(Hq, Hkv, d, [rng.randint(T, 150) for _ in range(B)], starts,
          [P * rng.randint(0, 2000 // P) for _ in range(N)], T=T, P=P, kvs=rng.random() < 0.4,
          fp8=d > 128 and rng.random() < 0.4, seed=seed, q_std=rng.choice((0.5, 1.0, 3.0))).check()
+
+
+@pytest.mark.parametrize("kvs", [False, True])
+@pytest.mark.parametrize("code", [1, 7, 8, 0x78, 0x7e, 0x81, 0xfe])
+def test_fp8_codes(code, kvs):
+    """Subnormal, smallest normal and largest e4m3 codes, both signs: V of one
+    code everywhere gives that code's value times its scale."""
+    c = Case(16, 4, 512, [9, 30], [0, 2], [272], fp8=True, kvs=kvs, seed=1, garbage=False)
+    (c.kp if kvs else c.vp).fill_(code)
+    scale = c.ks if kvs else c.vs
+    scale.copy_(torch.full_like(scale, 0.013))
+    c.check()
+
+
+def test_fp8_scales_of_very_different_pages():
+    """Page scales over six orders of magnitude, K's and V's each its own."""
+    c = Case(16, 4, 512, [40, 3], [0, 2], [1600], fp8=True, seed=1)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    c.vs *= 10.0 ** (torch.rand(c.vs.shape, generator=g, device="cuda") * 6 - 3)
+    c.ks *= torch.rand(c.ks.shape, generator=g, device="cuda") * 1.5 + 0.25
+    c.check()
+
+
+@pytest.mark.parametrize("batch,fp8", [(3, False), (40, False), (40, True)])
+@pytest.mark.parametrize("jump", [20.0, 200.0, 3000.0])
+def test_scores_that_jump_far_past_the_first_tile(batch, fp8, jump):
+    """One later token's score is far above all before it: past the references'
+    range, and past what an exponential can hold."""
+    c = Case(16, 4, 512, [7] * batch, [0, batch], [1200], fp8=fp8, seed=9, q_std=1.0, garbage=False)
+    at = 900
+    page = c.ptab[0][at // 16]
+    q = c.q.view(batch, 4, 4, 512)
+    c.q.copy_(q[:, :, :1].expand_as(q).reshape(c.q.shape))  # one direction per KV head and request
+    c.q[1:] = c.q[:1]
+    direction = c.q.view(batch, 4, 4, 512)[0, :, 0].float()
+    value = direction / direction.norm(dim=1, keepdim=True) * (jump * 22.6 / direction.norm(dim=1, keepdim=True))
+    if fp8:
+        big = value.abs().amax(1)
+        c.ks[page] = torch.maximum(c.ks[page], big / 448)
+        rows = c.kp[page].view(torch.float8_e4m3fn).float() * 0
+        rows[:, at % 16] = value / c.ks[page][:, None]
+        c.kp[page] = rows.to(torch.float8_e4m3fn).view(torch.uint8)
+    else:
+        c.kp[page, :, at % 16] = value.to(torch.bfloat16)
+    c.check()
+
+
+def test_infinite_scores():
+    """An infinite cached key gives its softmax's NaN to the rows that see it, and to no other KV head's."""
+    c = Case(16, 4, 512, [9, 30], [0, 2], [640], seed=3)
+    a = c.check()
+    c.kp[c.ptab[0][10], 2, 5] = float("inf")
+    out, _ = c.run()
+    assert out[:, 8:12].isnan().all()
+    keep = [h for h in range(16) if not 8 <= h < 12]
+    assert torch.equal(out[:, keep], a[:, keep])
+
+
+def test_negative_and_zero_scale():
+    for scale in (-0.05, 0.0):
+        c = Case(16, 4, 512, [9, 30], [0, 2], [640], seed=3)
+        c.scale = scale
+        c.check()
