@@ -183,7 +183,7 @@ constexpr double kFixedUs = 9.0, kHbmBytesPerUs = 6.8e6, kPartialBytesPerUs = 5.
 constexpr double kOwnFixedUs = 5.0;  // a stage-1 CTA of the own part
 
 double tile_us(const PrefixInstance& v) {
-  return (v.ctas == 2 ? (v.fp8 ? 7.0 : 3.8) : (v.fp8 ? 4.5 : 3.4)) * v.head_dim / 512.0;
+  return (v.ctas == 2 ? (v.fp8 ? 6.0 : 4.0) : (v.fp8 ? 4.5 : 3.4)) * v.head_dim / 512.0;
 }
 
 // SM time of the own part in one piece a request, in microseconds.
