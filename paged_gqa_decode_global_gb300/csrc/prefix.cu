@@ -17,7 +17,7 @@
 // reference until a score leaves that range. The tile's P is then not used:
 // the rows that left take the tile's true maximum, their sums and O^T are
 // rescaled, and P is written again. The matrix warp, which sees every P before
-// its product, gives the verdict, so the softmax warps need no barrier of their
+// its product, says which, so the softmax warps need no barrier of their
 // own per tile. Each row's references depend on its own scores only.
 //
 // One CTA (CT = 1): tiles of 128 tokens, N <= 64 at d = 512 (O^T takes 4 N
@@ -32,12 +32,21 @@
 // Roles: warps 0-7 softmax and epilogue (a thread per token lane, two
 // warpgroups with half the rows each), warp 8 the matrix instructions, warps
 // 9-11 the copies (every third stage each: a lone warp spends ~60 cycles a
-// copy); FP8: warps 12-15 (up to 32 rows: 12-19) widen the e4m3 stages to f16
+// copy; a stage shared out over the three was slower, 3.4 -> 3.6 us a tile of 64
+// rows); FP8: warps 12-15 (up to 32 rows: 12-19) widen the e4m3 stages to f16
 // operands. K and V arrive
 // as [8-token group][64-dim slab][8][128 B] atoms with the 128-byte swizzle:
 // K-major for the first product, and the same layout read M-major for the
 // second, so nothing is transposed; P is written N-major, a token's row at a
 // time. A K=V layer fetches the tile again for its second use (an L2 hit).
+//
+// What bounds it, at head_dim 512 (one GB300): a pair's tile of 256 tokens takes
+// 4.0-4.2 us, 2.1 us of it the products, the rest the copies' latency over a
+// ring of one tile (131 KB of 224: the query rows take 64 KB, P 32 KB); one CTA's
+// tile of 128 tokens 2.6 us with 16 rows and 3.4 us with 64, the copies of a page
+// at a time; FP8 4.6 us with 64 rows (single), 5.5 us (pair): the widening's
+// passes through shared memory. 1024 rows a KV head over 16384 tokens (137 GFLOP):
+// 145 us; 64 rows over 32768 (268 MB): 50 us.
 //
 // Roundings: P to the operands' type. bf16 cache: bf16, 2^-9 a probability. FP8
 // cache: f16, into which e4m3 widens exactly; q rounds to f16 once (as in the
@@ -59,7 +68,7 @@ constexpr int kTok = kPrefixTile;
 constexpr int kStage = kTok * 256;         // an operand stage: 128 dims of 128 tokens of K, or as many bytes of V
 constexpr int kRaw = kStage / 2;           // FP8: the same in e4m3
 constexpr int kBody = 224 * 1024;          // query rows, probabilities and rings
-constexpr int kCopyWarps = 3;              // warps 9..11 (12 or 16 warps keep 168 or 128 registers a thread)
+constexpr int kCopyWarps = 3;              // warps 9..11 (12, 16 or 20 warps leave 168, 128 or 96 registers a thread)
 constexpr int kSoftWarps = 8;
 constexpr float kLow = 3e38f;              // negated reference of a row without a score yet
 constexpr int kNoTop = (int)0x807fffff;    // ordered(-inf)
@@ -92,7 +101,7 @@ struct PrefixCfg {
   static constexpr int ROW_OFFSET = TOP_OFFSET + N * 4;         // int row[N]: a tile row's row of q and out
   static constexpr int BAR_OFFSET = ROW_OFFSET + N * 4;
   static constexpr int NBAR = 2 * NST + 2 * NRAW + 11;
-  static constexpr int TMEM_OFFSET = (BAR_OFFSET + NBAR * 8 + 15) / 16 * 16;  // tensor memory address, verdict, peer, -, left[8]
+  static constexpr int TMEM_OFFSET = (BAR_OFFSET + NBAR * 8 + 15) / 16 * 16;  // tensor memory address, redo, peer, -, left[8]
   static constexpr int SMEM_BYTES = TMEM_OFFSET + 48 + 1024;
   // pair: what a CTA's P takes from the other CTA a round: 128 tokens' rows, and its warps' flags
   static constexpr int P_TX = kTok * QN * 2 + 16;
@@ -243,12 +252,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
   uint64_t* p_empty = p_full + 1;
   uint64_t* q_full = p_empty + 1;          // (rank 0's)
   uint64_t* drained = q_full + 1;
-  uint64_t* judged = drained + 1;          // the matrix warp has looked at the P that arrived
-  uint64_t* p_peer = judged + 1;           // pair: rank 1's P is complete
+  uint64_t* looked = drained + 1;          // the matrix warp has looked at the P that arrived
+  uint64_t* p_peer = looked + 1;           // pair: rank 1's P is complete
   uint64_t* ref_full = p_peer + 1;         // pair, rank 1: the first references are here
   uint64_t* swapped = ref_full + 1;        // [2], one per softmax warpgroup
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::TMEM_OFFSET);
-  volatile uint32_t* verdict = tmem_at + 1;  // the round (P arrivals so far) that has to be written again
+  volatile uint32_t* redo = tmem_at + 1;  // the round (P arrivals so far) that has to be written again
   volatile uint32_t* peer = tmem_at + 2;     // pair, rank 0: whether a flag of rank 1 is set
   // per softmax warp that writes into this CTA's P: a score left its row's range
   volatile uint32_t* left = tmem_at + 4;
@@ -272,12 +281,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     mbar_init(p_empty, 1);
     mbar_init(q_full, CT * kSoftWarps);
     mbar_init(drained, 1);
-    mbar_init(judged, 1);
+    mbar_init(looked, 1);
     mbar_init(p_peer, 1);
     mbar_init(ref_full, 1);
     mbar_init(&swapped[0], CT * 4);
     mbar_init(&swapped[1], CT * 4);
-    *verdict = 0;
+    *redo = 0;
     fence_barrier_init();
     if constexpr (CT == 2) {
       // the first round's bytes from the other CTA
@@ -285,7 +294,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       if (rank == 0) {
         mbar_arrive_expect_tx(p_peer, 4);
       } else {
-        mbar_arrive_expect_tx(judged, 4);
+        mbar_arrive_expect_tx(looked, 4);
         mbar_arrive_expect_tx(ref_full, 4 * N);
       }
     }
@@ -513,15 +522,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
           if constexpr (CT == 2) {
             refused = refused || *peer != 0;
             fence_proxy_async_smem();  // the rows from the other CTA
-            if (refused) *verdict = rounds;
+            if (refused) *redo = rounds;
             mbar_arrive_expect_tx(p_full, C::P_TX);
             mbar_arrive_expect_tx(p_peer, 4);
             st_async_u32(map_smem_rank(smem_u32(tmem_at + 1), 1), refused ? rounds : 0,
-                         map_smem_rank(smem_u32(judged), 1));
+                         map_smem_rank(smem_u32(looked), 1));
           } else {
-            if (refused) *verdict = rounds;
+            if (refused) *redo = rounds;
           }
-          mbar_arrive(judged);
+          mbar_arrive(looked);
         }
         tmem_fence_after();
         const int steps = min(TT, hi - lo - i * TT) / 16;
@@ -562,7 +571,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
         atomicOr(p.err, kErrTimeout);
       }
     } else if (rank == 1 && elect_one()) {
-      // tells rank 0 of each P that is complete here, and takes the verdict
+      // tells rank 0 of each P that is complete here, and takes its answer
       uint32_t rounds = 0;
       bool ok = true;
       for (int accepted = 0; accepted < ntile;) {
@@ -573,11 +582,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
         mbar_arrive_expect_tx(p_full, C::P_TX);
         st_async_u32(map_smem_rank(smem_u32(tmem_at + 2), 0), fa.x | fa.y | fa.z | fa.w | fb.x | fb.y | fb.z | fb.w,
                      map_smem_rank(smem_u32(p_peer), 0));
-        ok = S::wait(judged, rounds & 1);
+        ok = S::wait(looked, rounds & 1);
         if (!ok) break;
         ++rounds;
-        if (*verdict != rounds) ++accepted;
-        mbar_arrive_expect_tx(judged, 4);
+        if (*redo != rounds) ++accepted;
+        mbar_arrive_expect_tx(looked, 4);
       }
       if (!ok) atomicOr(p.err, kErrTimeout);
     }
@@ -836,7 +845,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
             if (lane == c) mine = m;
           }
           if (lane < 8) {
-            // (no score among them, or an infinite one: left to the first verdict)
+            // (no score among them, or an infinite one: left to the first look)
             const float r = fabsf(unordered(mine)) < kLow ? -unordered(mine) : kLow;
             nref[c0 + lane] = r;
             if constexpr (CT == 2)
@@ -853,12 +862,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     };
     // Until tile i's P was accepted. A wait that ran out shows here, to the
     // whole warpgroup at once: its warps leave together.
-    auto judge = [&](int i, const Token& k) {
+    auto settle = [&](int i, const Token& k) {
       while (true) {
-        ok = ok && S::wait(judged, (round - 1) & 1);
+        ok = ok && S::wait(looked, (round - 1) & 1);
         __syncwarp();
         ok = !named_bar_or(bar, 128, !ok);
-        if (!ok || *verdict != round) return;
+        if (!ok || *redo != round) return;
         tmem_fence_after();
         again(i, k);
       }
@@ -872,7 +881,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       __syncwarp();
       tmem_fence_after();
       if (i > 0) {
-        judge(i - 1, before);
+        settle(i - 1, before);
         if (!ok || i == ntile) break;
       } else {
         first_refs(now);
