@@ -175,9 +175,12 @@ pd_status stage1(const pd_plan* plan, const void* q, const void* k_pool, const v
     if (!v_pool || v_pool == k_pool || !aligned(v_pool, 16)) return PD_ERR_INVALID_ARG;
   }
 
-  const void* fn = beside ? pd::stage1_beside_kernel_ptr(plan->variant) : pd::stage1_kernel_ptr(plan->variant);
+  const pd::BesideLaunch how = beside ? pd::stage1_beside(plan->variant)
+                                      : pd::BesideLaunch{pd::stage1_kernel_ptr(plan->variant), plan->threads_per_cta,
+                                                         plan->smem_bytes};
+  const void* fn = how.kernel;
   if (!fn) return PD_ERR_INVALID_ARG;
-  pd_status st = ensure_smem_attr(beside ? 2 : 0, plan->variant, fn, plan->smem_bytes);
+  pd_status st = ensure_smem_attr(beside ? 2 : 0, plan->variant, fn, how.smem_bytes);
   if (st != PD_OK) return st;
 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -219,8 +222,8 @@ pd_status stage1(const pd_plan* plan, const void* q, const void* k_pool, const v
   void* args[] = {&p};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(plan->grid_x, plan->grid_y, plan->grid_z);
-  cfg.blockDim = dim3(plan->threads_per_cta);
-  cfg.dynamicSmemBytes = plan->smem_bytes;
+  cfg.blockDim = dim3(how.threads);
+  cfg.dynamicSmemBytes = how.smem_bytes;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[2];
   int na = 0;

@@ -62,8 +62,13 @@ struct MergeParams {
 
 // Address of the stage-1 kernel of a variant (nullptr if unknown).
 const void* stage1_kernel_ptr(int variant);
-// The same for a launch beside the prefix pass of a shared-prefix decode.
-const void* stage1_beside_kernel_ptr(int variant);
+// The same for a launch beside the prefix pass of a shared-prefix decode, with
+// its own threads and shared memory (kernel null: no such variant).
+struct BesideLaunch {
+  const void* kernel;
+  int threads, smem_bytes;
+};
+BesideLaunch stage1_beside(int variant);
 
 // Launch the merge for rows = B * Hq; returns the CUDA error code.
 int launch_merge(const MergeParams& p, int rows, void* stream);

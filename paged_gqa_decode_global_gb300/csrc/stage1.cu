@@ -1195,32 +1195,26 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_kernel(const __grid_cons
 // ---- instantiation and dispatch -------------------------------------------------
 
 // (stage1_beside.cu compiles this file a second time, for the BESIDE instances)
-#ifdef PD_STAGE1_BESIDE
-constexpr bool kBeside = true;
-#else
-constexpr bool kBeside = false;
-#endif
+#ifndef PD_STAGE1_BESIDE
 
-#define PD_STAGE1_INSTANCE(ID, D, G, KVS, KV8, NW, SPW, MQ, NSUB, TW)                                \
-  template __global__ void stage1_kernel<Stage1Cfg<D, G, KVS, KV8, NW, SPW, MQ, NSUB, TW>, kBeside>( \
+#define PD_STAGE1_INSTANCE(ID, D, G, KVS, KV8, NW, SPW, MQ, NSUB, TW)                              \
+  template __global__ void stage1_kernel<Stage1Cfg<D, G, KVS, KV8, NW, SPW, MQ, NSUB, TW>, false>( \
       const __grid_constant__ Stage1Params);
 PD_FOR_EACH_VARIANT(PD_STAGE1_INSTANCE)
 #undef PD_STAGE1_INSTANCE
 
-#ifdef PD_STAGE1_BESIDE
-const void* stage1_beside_kernel_ptr(int variant) {
-#else
 const void* stage1_kernel_ptr(int variant) {
-#endif
   switch (variant) {
 #define PD_STAGE1_CASE(ID, D, G, KVS, KV8, NW, SPW, MQ, NSUB, TW) \
   case ID:                                                        \
-    return reinterpret_cast<const void*>(&stage1_kernel<Stage1Cfg<D, G, KVS, KV8, NW, SPW, MQ, NSUB, TW>, kBeside>);
+    return reinterpret_cast<const void*>(&stage1_kernel<Stage1Cfg<D, G, KVS, KV8, NW, SPW, MQ, NSUB, TW>, false>);
     PD_FOR_EACH_VARIANT(PD_STAGE1_CASE)
 #undef PD_STAGE1_CASE
     default:
       return nullptr;
   }
 }
+
+#endif
 
 }  // namespace pd
