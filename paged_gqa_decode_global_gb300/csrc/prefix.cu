@@ -372,21 +372,26 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     uint64_t* freed = C::FP8 ? raw_empty : empty;
     uint8_t* ring = smem + (C::FP8 ? C::RAW_OFFSET : C::RING_OFFSET);
     uint32_t err = 0;
-    // the 8-row group of the pool where this lane's box of a tile starts (-1:
-    // past the piece); a page outside the pool is fetched past the pool's end,
-    // which reads zeros
-    auto group_at = [&](int tile, int first, int tokens, int box) -> int {
+    // The page of this lane's box of a tile, and the 8-row group of the pool
+    // where the box starts (-1: none, or past the piece); a page outside the pool
+    // is fetched past the pool's end, which reads zeros. Page ids are loaded a
+    // tile before anything looks at them: looked at where they were loaded, each
+    // warp stood ~4000 cycles a tile waiting for them.
+    auto token_of = [&](int tile, int first, int tokens, int box) -> int {
       const int tok = lo + tile * TT + first + lane * box;
-      if (tile >= ntile || tok >= hi || lane >= tokens / box) return -1;
-      const int page = __ldg(table + tok / p.page_size);
+      return tile >= ntile || tok >= hi || lane >= tokens / box ? -1 : tok;
+    };
+    auto page_at = [&](int tok) -> int { return tok < 0 ? 0 : __ldg(table + tok / p.page_size); };
+    auto group_at = [&](int tok, int page) -> int {
+      if (tok < 0) return -1;
       if ((unsigned)page >= (unsigned)p.num_pages) {
         err |= kErrBadPage;
         return p.num_pages * p.num_kv_heads * p.page_size / 8;
       }
       return ((page * p.num_kv_heads + g) * p.page_size + tok % p.page_size) / 8;
     };
-    auto k_group = [&](int tile) { return group_at(tile, rank * kTok, kTok, p.k_box); };
-    auto v_group = [&](int tile) { return group_at(tile, 0, TT, p.v_box); };
+    auto k_token = [&](int tile) { return token_of(tile, rank * kTok, kTok, p.k_box); };
+    auto v_token = [&](int tile) { return token_of(tile, 0, TT, p.v_box); };
     int st = 0, uses = 0;  // the next stage, and how many stages were passed
     int turn = warp - 9 < W ? warp - 9 : 1 << 30;  // stages until this warp's next
     uint32_t phase = 1;    // of the stage's release (the first round waits for nothing)
@@ -437,15 +442,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
         end();
       }
     };
-    load_k(k_group(0));
-    int k_next = k_group(1), v_at = v_group(0);
+    int k_page = page_at(k_token(1)), v_page = page_at(v_token(0));
+    load_k(group_at(k_token(0), page_at(k_token(0))));
 #pragma unroll 1
     for (int i = 0; i < ntile && ok; ++i) {
-      const int k_after = k_group(i + 2), v_next = v_group(i + 1);
-      if (i + 1 < ntile) load_k(k_next);
-      if (ok) load_v(v_at);
-      k_next = k_after;
-      v_at = v_next;
+      const int k_after = page_at(k_token(i + 2)), v_after = page_at(v_token(i + 1));
+      if (i + 1 < ntile) load_k(group_at(k_token(i + 1), k_page));
+      if (ok) load_v(group_at(v_token(i), v_page));
+      k_page = k_after;
+      v_page = v_after;
     }
     // no copy may still be landing when the CTA exits (a pair's land on rank
     // 0's barriers: it waits for both, and the CTAs leave together)
@@ -645,24 +650,34 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     for (int c = 0; c < CW; ++c) l[c] = 0.f;
     uint32_t err = 0, round = 0;
     bool ok = true;
-    // a lane's token of a tile: whether it is attended, its scales
+    // A lane's token of a tile: whether it is attended, its scales. The page id
+    // is loaded a tile before it is looked at, and FP8's scales a tile before use.
     struct Token {
       bool valid;
       float sc, pv;
     };
-    auto token = [&](int i) -> Token {
+    auto page_at = [&](int i) -> int {
       const int tok = lo + i * TT + rank * kTok + lt;
-      Token k{false, p.scale_log2, v_inv};
-      if (i < ntile && tok < hi) {
-        const int page = __ldg(table + tok / p.page_size);
+      return i < ntile && tok < hi ? __ldg(table + tok / p.page_size) : 0;
+    };
+    auto token = [&](int i, int page) -> Token {
+      Token k{false, C::FP8 ? 0.f : p.scale_log2, C::FP8 ? 0.f : v_inv};
+      if (i < ntile && lo + i * TT + rank * kTok + lt < hi) {
         k.valid = (unsigned)page < (unsigned)p.num_pages;
         if (!k.valid) err |= kErrBadPage;
         if constexpr (C::FP8) {
           if (k.valid) {
-            k.sc *= __ldg(p.k_scale + (size_t)page * p.num_kv_heads + g);
-            k.pv *= __ldg(p.v_scale + (size_t)page * p.num_kv_heads + g);
+            k.sc = __ldg(p.k_scale + (size_t)page * p.num_kv_heads + g);
+            k.pv = __ldg(p.v_scale + (size_t)page * p.num_kv_heads + g);
           }
         }
+      }
+      return k;
+    };
+    auto scaled = [&](Token k) -> Token {
+      if constexpr (C::FP8) {
+        k.sc *= p.scale_log2;
+        k.pv *= v_inv;
       }
       return k;
     };
@@ -873,10 +888,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       }
     };
 
-    Token now = token(0), before{};
+    Token now = scaled(token(0, page_at(0))), before{};
+    int page = page_at(1);
 #pragma unroll 1
     for (int i = 0;; ++i) {
-      const Token after = token(i + 1);
+      const Token after = token(i + 1, page);
+      page = page_at(i + 2);
       if (i < ntile) ok = mbar_wait(&s_full[i & 1], (i >> 1) & 1) && ok;
       __syncwarp();
       tmem_fence_after();
@@ -903,7 +920,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       store(w);
       publish(now.valid && over > C::SLACK);
       before = now;
-      now = after;
+      now = scaled(after);
     }
     ok = ok && mbar_wait(p_empty, (ntile - 1) & 1);
     __syncwarp();
