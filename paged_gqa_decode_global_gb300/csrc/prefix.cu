@@ -194,6 +194,30 @@ __device__ __forceinline__ int ordered(float x) {
 }
 __device__ __forceinline__ float unordered(int k) { return __int_as_float(k >= 0 ? k : k ^ 0x7fffffff); }
 
+// A lane's tokens, one every TT of the piece: the entry of the page table and
+// the place in that page, without a division a tile. left: tokens still to come.
+template <int TT>
+struct Walk {
+  int index, offset, left, step_index, step_offset, page_size;
+  // (unsigned: a first token may lie past 2^31, and past `end`)
+  __device__ __forceinline__ Walk(const SharedParams& p, unsigned token, unsigned end)
+      : index(token / (unsigned)p.page_size),
+        offset(token % (unsigned)p.page_size),
+        left(token < end ? (end - token + TT - 1) / TT : 0),
+        step_index(TT / p.page_size),
+        step_offset(TT % p.page_size),
+        page_size(p.page_size) {}
+  __device__ __forceinline__ void next() {
+    --left;
+    index += step_index;
+    offset += step_offset;
+    if (offset >= page_size) {
+      offset -= page_size;
+      ++index;
+    }
+  }
+};
+
 // Four e4m3 codes -> four f16, exactly (NaN included).
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
@@ -362,7 +386,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     // W warps take every W-th stage. W <= NR: a warp that comes to a stage has
     // seen the stage NR + W uses back released, so the release it waits for is
     // the barrier's next; one further ahead, the parity would read as done.
-    const int v_boxes = C::VT / p.v_box;
+    // A warp's turn at a stage is on the path of the ring: everything that can be
+    // is worked out before the loop or a tile ahead. (Page positions by division,
+    // box numbers too, and page ids looked at where they were loaded: ~4000
+    // cycles a tile of 7700.)
     const uint64_t policy = p.keep_in_l2 ? l2_evict_normal_policy() : l2_evict_first_policy();
     constexpr int NR = C::FP8 ? C::NRAW : NST;
     constexpr int W = NR < kCopyWarps ? NR : kCopyWarps;
@@ -372,34 +399,40 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     uint64_t* freed = C::FP8 ? raw_empty : empty;
     uint8_t* ring = smem + (C::FP8 ? C::RAW_OFFSET : C::RING_OFFSET);
     uint32_t err = 0;
-    // The page of this lane's box of a tile, and the 8-row group of the pool
-    // where the box starts (-1: none, or past the piece); a page outside the pool
-    // is fetched past the pool's end, which reads zeros. Page ids are loaded a
-    // tile before anything looks at them: looked at where they were loaded, each
-    // warp stood ~4000 cycles a tile waiting for them.
-    auto token_of = [&](int tile, int first, int tokens, int box) -> int {
-      const int tok = lo + tile * TT + first + lane * box;
-      return tile >= ntile || tok >= hi || lane >= tokens / box ? -1 : tok;
+    const int k_bytes = p.k_box * 128 * K_SLABS, v_bytes = p.v_box * 128 * V_SLABS;
+    const int v_boxes = C::VT / p.v_box;  // of a stage
+    const int k_at = lane * k_bytes, v_at = lane % v_boxes * v_bytes, v_stage = lane / v_boxes;
+    // this lane's boxes: a tile further every time one is asked for
+    Walk<TT> k_walk(p, (unsigned)lo + rank * kTok + lane * p.k_box, lane < kTok / p.k_box ? hi : 0);
+    Walk<TT> v_walk(p, (unsigned)lo + lane * p.v_box, lane < TT / p.v_box ? hi : 0);
+    struct Box {
+      int page, offset;  // offset -1: no box
     };
-    auto page_at = [&](int tok) -> int { return tok < 0 ? 0 : __ldg(table + tok / p.page_size); };
-    auto group_at = [&](int tok, int page) -> int {
-      if (tok < 0) return -1;
-      if ((unsigned)page >= (unsigned)p.num_pages) {
+    auto next_box = [&](Walk<TT>& at) -> Box {
+      Box b{0, -1};
+      if (at.left > 0) b = {__ldg(table + at.index), at.offset};
+      at.next();
+      return b;
+    };
+    // the 8-row group of the pool where a box starts (-1: none); a page outside
+    // the pool is fetched past the pool's end, which reads zeros
+    const int page_groups = p.num_kv_heads * (p.page_size / 8), head_group = g * (p.page_size / 8);
+    auto group_of = [&](const Box& b) -> int {
+      if (b.offset < 0) return -1;
+      if ((unsigned)b.page >= (unsigned)p.num_pages) {
         err |= kErrBadPage;
-        return p.num_pages * p.num_kv_heads * p.page_size / 8;
+        return p.num_pages * page_groups;
       }
-      return ((page * p.num_kv_heads + g) * p.page_size + tok % p.page_size) / 8;
+      return b.page * page_groups + head_group + b.offset / 8;
     };
-    auto k_token = [&](int tile) { return token_of(tile, rank * kTok, kTok, p.k_box); };
-    auto v_token = [&](int tile) { return token_of(tile, 0, TT, p.v_box); };
-    int st = 0, uses = 0;  // the next stage, and how many stages were passed
-    int turn = warp - 9 < W ? warp - 9 : 1 << 30;  // stages until this warp's next
-    uint32_t phase = 1;    // of the stage's release (the first round waits for nothing)
+    // this warp's next stage: its number, place and (from the next block on) its
+    // place among the stages of a tile's K or V; phase: of the stage's release
+    // (the first round waits for nothing)
+    int use = warp - 9, st = use, turn = use < W ? use : 1 << 30;
+    uint32_t phase = 1;
     bool ok = true;
-    // this warp's stage, free to be filled? (ok false: the wait ran out)
     auto begin = [&](int boxes, int box_bytes) {
-      if (turn != 0) return false;
-      ok = __all_sync(kFullMask, uses < NR || mbar_wait(&freed[st], phase));
+      ok = __all_sync(kFullMask, use < NR || mbar_wait(&freed[st], phase));
       if (ok && lane == 0) {
         const uint32_t bytes = boxes * box_bytes + p.stall_bytes;
         if (CT == 1 || C::FP8) mbar_arrive_expect_tx(&land[st], bytes);
@@ -414,50 +447,51 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       else tma_load_4d_pair(dst, map, 0, 0, slab, group, map_smem_rank(smem_u32(&land[st]), 0), policy);
     };
     auto end = [&] {
-      turn = turn == 0 ? W - 1 : turn - 1;
-      ++uses;
-      if (++st == NR) {
-        st = 0;
+      turn += W;
+      use += W;
+      st += W;
+      if (st >= NR) {
+        st -= NR;
         phase ^= 1;
       }
     };
     auto load_k = [&](int at) {
-      const int bytes = p.k_box * 128 * K_SLABS;
       const int boxes = __popc(__ballot_sync(kFullMask, at >= 0));
 #pragma unroll 1
-      for (int s = 0; s < KS; ++s) {
-        if (begin(boxes, bytes) && at >= 0) copy(lane * bytes, &p.kmap, s * K_SLABS, at);
-        if (!ok) return;
+      while (turn < KS) {
+        if (!begin(boxes, k_bytes)) return;
+        if (at >= 0) copy(k_at, &p.kmap, turn * K_SLABS, at);
         end();
       }
+      turn -= KS;
     };
     auto load_v = [&](int at) {
-      const int bytes = p.v_box * 128 * V_SLABS;
 #pragma unroll 1
-      for (int s = 0; s < KS; ++s) {
-        const bool mine = at >= 0 && lane / v_boxes == s;
-        if (begin(__popc(__ballot_sync(kFullMask, mine)), bytes) && mine)
-          copy(lane % v_boxes * bytes, &p.vmap, rank * V_SLABS, at);
-        if (!ok) return;
+      while (turn < KS) {
+        const bool mine = at >= 0 && v_stage == turn;
+        if (!begin(__popc(__ballot_sync(kFullMask, mine)), v_bytes)) return;
+        if (mine) copy(v_at, &p.vmap, rank * V_SLABS, at);
         end();
       }
+      turn -= KS;
     };
-    int k_page = page_at(k_token(1)), v_page = page_at(v_token(0));
-    load_k(group_at(k_token(0), page_at(k_token(0))));
+    const Box k_first = next_box(k_walk);
+    Box k_box = next_box(k_walk), v_box = next_box(v_walk);
+    load_k(group_of(k_first));
 #pragma unroll 1
     for (int i = 0; i < ntile && ok; ++i) {
-      const int k_after = page_at(k_token(i + 2)), v_after = page_at(v_token(i + 1));
-      if (i + 1 < ntile) load_k(group_at(k_token(i + 1), k_page));
-      if (ok) load_v(group_at(v_token(i), v_page));
-      k_page = k_after;
-      v_page = v_after;
+      const Box k_after = next_box(k_walk), v_after = next_box(v_walk);
+      if (i + 1 < ntile) load_k(group_of(k_box));
+      if (ok) load_v(group_of(v_box));
+      k_box = k_after;
+      v_box = v_after;
     }
     // no copy may still be landing when the CTA exits (a pair's land on rank
     // 0's barriers: it waits for both, and the CTAs leave together)
     if (lane == 0) {
       const unsigned long long deadline = global_timer_ns() + kWaitTimeoutNs;
       if (CT == 1 || C::FP8 || rank == 0)
-        for (int k = max(0, uses - NR); k < uses; ++k)
+        for (int n = ok ? 2 * KS * ntile : use, k = max(0, n - NR); k < n; ++k)
           if (k % W == warp - 9 && !mbar_wait_until(&land[k % NR], (k / NR) & 1, deadline)) ok = false;
       if (!ok) err |= kErrTimeout;
     }
@@ -656,13 +690,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       bool valid;
       float sc, pv;
     };
-    auto page_at = [&](int i) -> int {
-      const int tok = lo + i * TT + rank * kTok + lt;
-      return i < ntile && tok < hi ? __ldg(table + tok / p.page_size) : 0;
+    Walk<TT> walk(p, (unsigned)lo + rank * kTok + lt, hi);
+    const int lane_tiles = walk.left;  // tiles that have a token of this lane
+    auto next_page = [&]() -> int {
+      const int page = walk.left > 0 ? __ldg(table + walk.index) : 0;
+      walk.next();
+      return page;
     };
     auto token = [&](int i, int page) -> Token {
       Token k{false, C::FP8 ? 0.f : p.scale_log2, C::FP8 ? 0.f : v_inv};
-      if (i < ntile && lo + i * TT + rank * kTok + lt < hi) {
+      if (i < lane_tiles) {
         k.valid = (unsigned)page < (unsigned)p.num_pages;
         if (!k.valid) err |= kErrBadPage;
         if constexpr (C::FP8) {
@@ -888,12 +925,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       }
     };
 
-    Token now = scaled(token(0, page_at(0))), before{};
-    int page = page_at(1);
+    Token now = scaled(token(0, next_page())), before{};
+    int page = next_page();
 #pragma unroll 1
     for (int i = 0;; ++i) {
       const Token after = token(i + 1, page);
-      page = page_at(i + 2);
+      page = next_page();
       if (i < ntile) ok = mbar_wait(&s_full[i & 1], (i >> 1) & 1) && ok;
       __syncwarp();
       tmem_fence_after();
