@@ -31,9 +31,8 @@
 //
 // Roles: warps 0-7 softmax and epilogue (a thread per token lane, two
 // warpgroups with half the rows each), warp 8 the matrix instructions, warps
-// 9-11 the copies (every third stage each: a lone warp spends ~60 cycles a
-// copy; a stage shared out over the three was slower, 3.4 -> 3.6 us a tile of 64
-// rows); FP8: warps 12-15 (up to 32 rows: 12-19) widen the e4m3 stages to f16
+// 9-11 the copies (a third of every stage's each: a lane's copies go out ~70
+// cycles apart); FP8: warps 12-15 (up to 32 rows: 12-19) widen the e4m3 stages to f16
 // operands. K and V arrive
 // as [8-token group][64-dim slab][8][128 B] atoms with the 128-byte swizzle:
 // K-major for the first product, and the same layout read M-major for the
@@ -292,11 +291,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     prefetch_tensormap(&p.kmap);
     prefetch_tensormap(&p.vmap);
     for (int i = 0; i < NST; ++i) {
-      mbar_init(&full[i], CT * (C::FP8 ? 4 : 1));
+      mbar_init(&full[i], CT * (C::FP8 ? 4 : kCopyWarps));
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < C::NRAW; ++i) {
-      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_full[i], kCopyWarps);
       mbar_init(&raw_empty[i], 4);
     }
     mbar_init(&s_full[0], 1);
@@ -382,17 +381,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     // A K stage is 128 dims of this CTA's tokens, a V stage this CTA's dims of
     // VT tokens; a 16-token page takes one copy of 4 KB (K) or 16 KB (V, d =
     // 512): with a copy per page and slab (2 KB) the copies took 5.5 us a tile.
-    // Lane j holds the pool row of the tile's j-th K box and j-th V box.
-    // W warps take every W-th stage. W <= NR: a warp that comes to a stage has
-    // seen the stage NR + W uses back released, so the release it waits for is
-    // the barrier's next; one further ahead, the parity would read as done.
-    // A warp's turn at a stage is on the path of the ring: everything that can be
-    // is worked out before the loop or a tile ahead. (Page positions by division,
+    // Box j of a tile is lane j / 3's of copy warp j mod 3.
+    // Filling a stage is on the path of the ring: everything that can be is worked
+    // out before the loop or a tile ahead. (Page positions by division,
     // box numbers too, and page ids looked at where they were loaded: ~4000
     // cycles a tile of 7700.)
     const uint64_t policy = p.keep_in_l2 ? l2_evict_normal_policy() : l2_evict_first_policy();
     constexpr int NR = C::FP8 ? C::NRAW : NST;
-    constexpr int W = NR < kCopyWarps ? NR : kCopyWarps;
+    const int w = warp - 9, box = lane * kCopyWarps + w;
     constexpr int BYTES = C::FP8 ? kRaw : kStage;
     constexpr int K_SLABS = C::FP8 ? 1 : 2, V_SLABS = C::V_ATOMS / (C::FP8 ? 2 : 1);
     uint64_t* land = C::FP8 ? raw_full : full;
@@ -401,10 +397,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     uint32_t err = 0;
     const int k_bytes = p.k_box * 128 * K_SLABS, v_bytes = p.v_box * 128 * V_SLABS;
     const int v_boxes = C::VT / p.v_box;  // of a stage
-    const int k_at = lane * k_bytes, v_at = lane % v_boxes * v_bytes, v_stage = lane / v_boxes;
+    const int k_at = box * k_bytes, v_at = box % v_boxes * v_bytes, v_stage = box / v_boxes;
     // this lane's boxes: a tile further every time one is asked for
-    Walk<TT> k_walk(p, (unsigned)lo + rank * kTok + lane * p.k_box, lane < kTok / p.k_box ? hi : 0);
-    Walk<TT> v_walk(p, (unsigned)lo + lane * p.v_box, lane < TT / p.v_box ? hi : 0);
+    Walk<TT> k_walk(p, (unsigned)lo + rank * kTok + box * p.k_box, box < kTok / p.k_box ? hi : 0);
+    Walk<TT> v_walk(p, (unsigned)lo + box * p.v_box, box < TT / p.v_box ? hi : 0);
     struct Box {
       int page, offset;  // offset -1: no box
     };
@@ -425,16 +421,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       }
       return b.page * page_groups + head_group + b.offset / 8;
     };
-    // this warp's next stage: its number, place and (from the next block on) its
-    // place among the stages of a tile's K or V; phase: of the stage's release
-    // (the first round waits for nothing)
-    int use = warp - 9, st = use, turn = use < W ? use : 1 << 30;
+    // the next stage's number and place, and the phase of its release (the first
+    // round waits for nothing)
+    int use = 0, st = 0;
     uint32_t phase = 1;
     bool ok = true;
     auto begin = [&](int boxes, int box_bytes) {
       ok = __all_sync(kFullMask, use < NR || mbar_wait(&freed[st], phase));
       if (ok && lane == 0) {
-        const uint32_t bytes = boxes * box_bytes + p.stall_bytes;
+        const uint32_t bytes = boxes * box_bytes + (w == 0 ? p.stall_bytes : 0);
         if (CT == 1 || C::FP8) mbar_arrive_expect_tx(&land[st], bytes);
         else mbar_arrive_expect_tx_remote(map_smem_rank(smem_u32(&land[st]), 0), bytes);
       }
@@ -447,33 +442,29 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       else tma_load_4d_pair(dst, map, 0, 0, slab, group, map_smem_rank(smem_u32(&land[st]), 0), policy);
     };
     auto end = [&] {
-      turn += W;
-      use += W;
-      st += W;
-      if (st >= NR) {
-        st -= NR;
+      ++use;
+      if (++st == NR) {
+        st = 0;
         phase ^= 1;
       }
     };
     auto load_k = [&](int at) {
       const int boxes = __popc(__ballot_sync(kFullMask, at >= 0));
 #pragma unroll 1
-      while (turn < KS) {
+      for (int s = 0; s < KS; ++s) {
         if (!begin(boxes, k_bytes)) return;
-        if (at >= 0) copy(k_at, &p.kmap, turn * K_SLABS, at);
+        if (at >= 0) copy(k_at, &p.kmap, s * K_SLABS, at);
         end();
       }
-      turn -= KS;
     };
     auto load_v = [&](int at) {
 #pragma unroll 1
-      while (turn < KS) {
-        const bool mine = at >= 0 && v_stage == turn;
+      for (int s = 0; s < KS; ++s) {
+        const bool mine = at >= 0 && v_stage == s;
         if (!begin(__popc(__ballot_sync(kFullMask, mine)), v_bytes)) return;
         if (mine) copy(v_at, &p.vmap, rank * V_SLABS, at);
         end();
       }
-      turn -= KS;
     };
     const Box k_first = next_box(k_walk);
     Box k_box = next_box(k_walk), v_box = next_box(v_walk);
@@ -490,9 +481,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     // 0's barriers: it waits for both, and the CTAs leave together)
     if (lane == 0) {
       const unsigned long long deadline = global_timer_ns() + kWaitTimeoutNs;
-      if (CT == 1 || C::FP8 || rank == 0)
+      if (w == 0 && (CT == 1 || C::FP8 || rank == 0))
         for (int n = ok ? 2 * KS * ntile : use, k = max(0, n - NR); k < n; ++k)
-          if (k % W == warp - 9 && !mbar_wait_until(&land[k % NR], (k / NR) & 1, deadline)) ok = false;
+          if (!mbar_wait_until(&land[k % NR], (k / NR) & 1, deadline)) ok = false;
       if (!ok) err |= kErrTimeout;
     }
     err = __reduce_or_sync(kFullMask, err);
