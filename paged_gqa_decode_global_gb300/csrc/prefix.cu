@@ -504,7 +504,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       const uint64_t p_desc = smem_desc(base + C::P_OFFSET, TT * 128, 8 * C::P_ROW, C::P_ROW);
       int st = 0;
       uint32_t phase = 0, rounds = 0;
-      constexpr int TWO = KS >= 2 && !C::FP8 ? 2 : 1;  // stages waited for together
       bool ok = mbar_wait_cluster(q_full, 0);
       auto next_stage = [&] {
         if (++st == NST) {
@@ -512,28 +511,32 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
           phase ^= 1;
         }
       };
+      // the next stage is there; a look at its barrier is one at the next's, too
+      uint32_t ahead = 0;
       auto landed = [&] {
-        if constexpr (TWO == 1) return mbar_wait(&full[st], phase);
+        if (ahead != 0) {
+          ahead = 0;
+          return true;
+        }
         const int st2 = st + 1 == NST ? 0 : st + 1;
-        return mbar_wait2(&full[st], phase, &full[st2], st2 == 0 ? phase ^ 1 : phase);
+        const uint32_t x = mbar_test(&full[st], phase), y = mbar_test(&full[st2], st2 == 0 ? phase ^ 1 : phase);
+        ahead = x & y;
+        return x != 0 || mbar_wait(&full[st], phase);
       };
       // the other S buffer is free once P of the tile before last was accepted
       auto qk = [&](int i) {
         const uint32_t d = tmem + C::O_COLS + (i & 1) * N;
 #pragma unroll 1
-        for (int s = 0; s < KS && ok; s += TWO) {
+        for (int s = 0; s < KS && ok; ++s) {
           ok = landed();
           if (!ok) return;
+          const uint64_t a = k_desc + st * (kStage >> 4), b = q_desc + s * 2 * (C::QN * 128 >> 4);
 #pragma unroll
-          for (int u = 0; u < TWO; ++u) {
-            const uint64_t a = k_desc + st * (kStage >> 4), b = q_desc + (s + u) * 2 * (C::QN * 128 >> 4);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_ss<CT>(d, a + (k >> 2) * (1024 >> 4) + (k & 3) * 2, b + (k >> 2) * (C::QN * 128 >> 4) + (k & 3) * 2,
-                         kQk, k != 0 || u != 0 || s != 0);
-            mma_commit<CT>(&empty[st]);
-            next_stage();
-          }
+          for (int k = 0; k < 8; ++k)
+            mma_ss<CT>(d, a + (k >> 2) * (1024 >> 4) + (k & 3) * 2, b + (k >> 2) * (C::QN * 128 >> 4) + (k & 3) * 2,
+                       kQk, k != 0 || s != 0);
+          mma_commit<CT>(&empty[st]);
+          next_stage();
         }
         mma_commit<CT>(&s_full[i & 1]);
       };
@@ -565,32 +568,29 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
         tmem_fence_after();
         const int steps = min(TT, hi - lo - i * TT) / 16;
 #pragma unroll 1
-        for (int s = 0; s < KS && ok; s += TWO) {
+        for (int s = 0; s < KS && ok; ++s) {
           ok = landed();
           if (!ok) break;
           // 16 tokens at a time, all of the CTA's head dims
-          auto step = [&](uint64_t a, uint64_t b, int k, int m, bool first) {
+          const uint64_t a = v_desc + st * (kStage >> 4), b = p_desc + s * (C::VT * C::P_ROW >> 4);
+          const bool first = i == 0 && s == 0;
+          auto step = [&](int k, int m) {
             mma_ss<CT>(tmem + m * N, a + k * (C::V_ATOMS * 2048 >> 4) + m * (2048 >> 4),
                        b + k * (16 * C::P_ROW >> 4), kPv, !first || k != 0);
           };
+          if ((s + 1) * (C::VT / 16) <= steps) {
 #pragma unroll
-          for (int u = 0; u < TWO; ++u) {
-            const uint64_t a = v_desc + st * (kStage >> 4), b = p_desc + (s + u) * (C::VT * C::P_ROW >> 4);
-            const bool first = i == 0 && s + u == 0;
-            if ((s + u + 1) * (C::VT / 16) <= steps) {
+            for (int k = 0; k < C::VT / 16; ++k)
 #pragma unroll
-              for (int k = 0; k < C::VT / 16; ++k)
-#pragma unroll
-                for (int m = 0; m < C::MC; ++m) step(a, b, k, m, first);
-            } else {
+              for (int m = 0; m < C::MC; ++m) step(k, m);
+          } else {
 #pragma unroll 1
-              for (int k = 0; (s + u) * (C::VT / 16) + k < steps; ++k)
+            for (int k = 0; s * (C::VT / 16) + k < steps; ++k)
 #pragma unroll 1
-                for (int m = 0; m < C::MC; ++m) step(a, b, k, m, first);
-            }
-            mma_commit<CT>(&empty[st]);
-            next_stage();
+              for (int m = 0; m < C::MC; ++m) step(k, m);
           }
+          mma_commit<CT>(&empty[st]);
+          next_stage();
         }
         if (ok) mma_commit<CT>(p_empty);
       }
