@@ -99,7 +99,7 @@ struct PrefixCfg {
   static constexpr int TOP_OFFSET = REF_OFFSET + N * 4;         // int top[N]: a tile's true maxima
   static constexpr int ROW_OFFSET = TOP_OFFSET + N * 4;         // int row[N]: a tile row's row of q and out
   static constexpr int BAR_OFFSET = ROW_OFFSET + N * 4;
-  static constexpr int NBAR = 2 * NST + 2 * NRAW + 11;
+  static constexpr int NBAR = 2 * NST + 2 * NRAW + 12;
   static constexpr int TMEM_OFFSET = (BAR_OFFSET + NBAR * 8 + 15) / 16 * 16;  // tensor memory address, redo, peer, -, left[8]
   static constexpr int SMEM_BYTES = TMEM_OFFSET + 48 + 1024;
   // pair: what a CTA's P takes from the other CTA a round: 128 tokens' rows, and its warps' flags
@@ -109,7 +109,8 @@ struct PrefixCfg {
   static constexpr int LD = CW < 32 ? CW : 32;
   // P: [QN / 64 blocks][TT tokens][row of up to 64 query rows], swizzled over the row
   static constexpr int P_ROW = QN >= 64 ? 128 : QN * 2;
-  // after the last product, in the ring: the rows' sums (per warpgroup [128][CW + 1], [128]), then [2][N] totals
+  // after the last product, in the ring: the rows' sums (per warpgroup [128][CW + 1], [128]), then a
+  // pair's sums of the other CTA's tokens [N]
   static constexpr int SUM_FLOATS = kTok * (CW + 1) + 128;
   static constexpr int TOTAL_OFFSET = RING_OFFSET + 2 * SUM_FLOATS * 4;
   static constexpr int O_COLS = MC * N;
@@ -119,7 +120,7 @@ struct PrefixCfg {
   static_assert(O_COLS + 2 * N <= 512, "tensor memory");
   static_assert(NST >= 2 && (!FP8 || NRAW >= 3), "rings");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
-  static_assert(2 * SUM_FLOATS * 4 + 2 * N * 4 <= NST * kStage + NRAW * kRaw, "the row sums are reduced in the rings");
+  static_assert(2 * SUM_FLOATS * 4 + N * 4 <= NST * kStage + NRAW * kRaw, "the row sums are reduced in the rings");
   static_assert(N * MC * 128 * 4 <= NST * kStage + NRAW * kRaw, "the partial rows leave through the rings");
 };
 
@@ -129,6 +130,7 @@ struct Tile {
 
 // Row tile z of the launch: its group, first row, rows and prefix length (group
 // -1: none). Every warp finds it by itself, 32 groups at a time.
+template <int N>
 __device__ __forceinline__ Tile find_tile(const SharedParams& p, int z) {
   const int lane = threadIdx.x & 31, per_req = p.query_tokens * p.group;
   int at = 0;
@@ -141,7 +143,7 @@ __device__ __forceinline__ Tile find_tile(const SharedParams& p, int z) {
       s = max(0, min(a, p.batch));
       rows = (max(s, min(b, p.batch)) - s) * per_req;
     }
-    const int n = (rows + p.row_tile - 1) / p.row_tile;
+    const int n = (rows + N - 1) / N;
     int end = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -154,8 +156,8 @@ __device__ __forceinline__ Tile find_tile(const SharedParams& p, int z) {
       const int src = __ffs(in) - 1;
       Tile t;
       t.group = g0 + src;
-      t.first = (z - __shfl_sync(kFullMask, end - n, src)) * p.row_tile;
-      t.rows = min(p.row_tile, __shfl_sync(kFullMask, rows, src) - t.first);
+      t.first = (z - __shfl_sync(kFullMask, end - n, src)) * N;
+      t.rows = min(N, __shfl_sync(kFullMask, rows, src) - t.first);
       t.start = __shfl_sync(kFullMask, s, src);
       t.len = __shfl_sync(kFullMask, len, src);
       return t;
@@ -199,13 +201,17 @@ template <int TT>
 struct Walk {
   int index, offset, left, step_index, step_offset, page_size;
   // (unsigned: a first token may lie past 2^31, and past `end`)
-  __device__ __forceinline__ Walk(const SharedParams& p, unsigned token, unsigned end)
-      : index(token / (unsigned)p.page_size),
-        offset(token % (unsigned)p.page_size),
+  __device__ __forceinline__ Walk(const Walk& step, unsigned token, unsigned end)
+      : index(token / (unsigned)step.page_size),
+        offset(token - index * step.page_size),
         left(token < end ? (end - token + TT - 1) / TT : 0),
-        step_index(TT / p.page_size),
-        step_offset(TT % p.page_size),
-        page_size(p.page_size) {}
+        step_index(step.step_index),
+        step_offset(step.step_offset),
+        page_size(step.page_size) {}
+  // the steps alone
+  __device__ __forceinline__ explicit Walk(int page) : step_index(TT / page), page_size(page) {
+    step_offset = TT - step_index * page;
+  }
   __device__ __forceinline__ void next() {
     --left;
     index += step_index;
@@ -254,6 +260,14 @@ struct Sync {
     if constexpr (CT == 1) return mbar_wait(bar, parity);
     else return mbar_wait_cluster(bar, parity);
   }
+  // all threads' barrier, and its two halves
+  static __device__ __forceinline__ void arrive() {
+    if constexpr (CT == 2) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  }
+  static __device__ __forceinline__ void wait_all() {
+    if constexpr (CT == 1) __syncthreads();
+    else cluster_wait();
+  }
   static __device__ __forceinline__ void all_threads() {
     if constexpr (CT == 1) __syncthreads();
     else cluster_sync_all();
@@ -278,7 +292,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
   uint64_t* looked = drained + 1;          // the matrix warp has looked at the P that arrived
   uint64_t* p_peer = looked + 1;           // pair: rank 1's P is complete
   uint64_t* ref_full = p_peer + 1;         // pair, rank 1: the first references are here
-  uint64_t* swapped = ref_full + 1;        // [2], one per softmax warpgroup
+  uint64_t* sums_full = ref_full + 1;      // pair: the other CTA's sums are here
+  uint64_t* swapped = sums_full + 1;       // [2], one per softmax warpgroup
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::TMEM_OFFSET);
   volatile uint32_t* redo = tmem_at + 1;  // the round (P arrivals so far) that has to be written again
   volatile uint32_t* peer = tmem_at + 2;     // pair, rank 0: whether a flag of rank 1 is set
@@ -307,6 +322,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     mbar_init(looked, 1);
     mbar_init(p_peer, 1);
     mbar_init(ref_full, 1);
+    mbar_init(sums_full, 1);
     mbar_init(&swapped[0], CT * 4);
     mbar_init(&swapped[1], CT * 4);
     *redo = 0;
@@ -314,6 +330,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     if constexpr (CT == 2) {
       // the first round's bytes from the other CTA
       mbar_arrive_expect_tx(p_full, C::P_TX);
+      mbar_arrive_expect_tx(sums_full, 4 * N);
       if (rank == 0) {
         mbar_arrive_expect_tx(p_peer, 4);
       } else {
@@ -328,14 +345,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
   }
   __syncwarp();
   if (warp == 8) tmem_alloc<CT>(tmem_at, C::TMEM_COLS);
+  tmem_fence_before();
+  S::arrive();
+  const Walk<TT> step(p.page_size);
   // behind whatever wrote what this grid reads; the own part's stage 1 behind
   // this grid may start once every thread here has waited
   grid_dependency_wait();
   grid_launch_dependents();
   const int piece = blockIdx.y, g = blockIdx.z;
-  const Tile t = find_tile(p, blockIdx.x / CT);
-  tmem_fence_before();
-  S::all_threads();
+  const Tile t = find_tile<N>(p, blockIdx.x / CT);
+  S::wait_all();
   tmem_fence_after();
   const uint32_t tmem = *tmem_at;
   if (blockIdx.x == 0 && piece == 0 && g == 0 && warp == 0 && !groups_ok(p) && lane == 0)
@@ -343,16 +362,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
   int L = t.len;
   if (t.group >= 0) {
     const int cap = p.max_prefix_pages * p.page_size;
-    if (L < 0 || L > cap || L % p.page_size != 0) {
+    const int cut = max(0, min(L, cap)) / p.page_size * p.page_size;
+    if (L != cut) {
       if (tid == 0) atomicOr(p.err, kErrBadSeqLen);
-      L = max(0, min(L, cap)) / p.page_size * p.page_size;
+      L = cut;
     }
   }
   // this piece's tokens [lo, hi); the last piece takes whatever remains
   const long long want = (long long)piece * p.chunk_tokens;
   const int lo = (int)min(want, (long long)L);
   const int hi = piece == p.num_pieces - 1 ? L : (int)min((long long)L, want + p.chunk_tokens);
-  const int ntile = (hi - lo + TT - 1) / TT;
+  const int ntile = (unsigned)(hi - lo + TT - 1) / TT;
   const int32_t* table = p.prefix_tables + (size_t)max(t.group, 0) * p.max_prefix_pages;
   int* rows = reinterpret_cast<int*>(smem + C::ROW_OFFSET);
 
@@ -366,15 +386,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     return;
   }
 
-  // softmax warps: what the epilogue takes from the loop
-  bool done = false;
-  float v_top = 1.f;  // FP8: the piece's largest V scale
   const int wg = (warp >> 2) & 1, lt = tid & 127, bar = 1 + wg;
   float* nref = reinterpret_cast<float*>(smem + C::REF_OFFSET) + wg * CW;
   int* top = reinterpret_cast<int*>(smem + C::TOP_OFFSET) + wg * CW;
   const uint32_t quarter = tmem + ((uint32_t)(warp & 3) << 21);
   const uint32_t o_at = quarter + wg * CW;
-  float* totals = reinterpret_cast<float*>(smem + C::TOTAL_OFFSET);  // [2][N]
 
   if (warp >= 9 && warp < 9 + kCopyWarps) {
     // ---- copies: stages in the order the products use them, K(0), K(1), V(0), K(2), V(1), ...
@@ -399,8 +415,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     const int v_boxes = C::VT / p.v_box;  // of a stage
     const int k_at = box * k_bytes, v_at = box % v_boxes * v_bytes, v_stage = box / v_boxes;
     // this lane's boxes: a tile further every time one is asked for
-    Walk<TT> k_walk(p, (unsigned)lo + rank * kTok + box * p.k_box, box < kTok / p.k_box ? hi : 0);
-    Walk<TT> v_walk(p, (unsigned)lo + box * p.v_box, box < TT / p.v_box ? hi : 0);
+    Walk<TT> k_walk(step, (unsigned)lo + rank * kTok + box * p.k_box, box < kTok / p.k_box ? hi : 0);
+    Walk<TT> v_walk(step, (unsigned)lo + box * p.v_box, box < TT / p.v_box ? hi : 0);
     struct Box {
       int page, offset;  // offset -1: no box
     };
@@ -650,7 +666,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     __syncwarp();
     if (lane == 0) S::arrive_leader(q_full);
 
-    float v_inv = 1.f;
+    float v_inv = 1.f, v_top = 1.f;  // FP8: the piece's largest V scale
     if constexpr (C::FP8) {
       float m = 0.f;
       for (int tok = lo + lt * 16; tok < hi; tok += 128 * 16) {
@@ -681,7 +697,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       bool valid;
       float sc, pv;
     };
-    Walk<TT> walk(p, (unsigned)lo + rank * kTok + lt, hi);
+    Walk<TT> walk(step, (unsigned)lo + rank * kTok + lt, hi);
     const int lane_tiles = walk.left;  // tiles that have a token of this lane
     auto next_page = [&]() -> int {
       const int page = walk.left > 0 ? __ldg(table + walk.index) : 0;
@@ -952,41 +968,79 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     }
     ok = ok && mbar_wait(p_empty, (ntile - 1) & 1);
     __syncwarp();
-    done = !named_bar_or(bar, 128, !ok);
+    // ---- epilogue: the last product is done, in both CTAs of a pair
+    const bool done = !named_bar_or(bar, 128, !ok);
     if (!done) err |= kErrTimeout;
+    // the rows' sums over this CTA's token lanes, in the ring
+    float* sum = reinterpret_cast<float*>(smem + C::RING_OFFSET) + wg * C::SUM_FLOATS;
+    float* part = sum + kTok * (CW + 1);
     if (done) {
       tmem_fence_after();
-      // the rows' sums over this CTA's token lanes, in the ring (every product is done with it)
-      float* sum = reinterpret_cast<float*>(smem + C::RING_OFFSET) + wg * C::SUM_FLOATS;
 #pragma unroll
       for (int c = 0; c < CW; ++c) sum[lt * (CW + 1) + c] = l[c];
     }
-    err = __reduce_or_sync(kFullMask, err);
-    if (lane == 0 && err) atomicOr(p.err, err);
     named_bar_sync(bar, 128);
-    {
-      const float* sum = reinterpret_cast<const float*>(smem + C::RING_OFFSET) + wg * C::SUM_FLOATS;
-      float* part = reinterpret_cast<float*>(smem + C::RING_OFFSET) + wg * C::SUM_FLOATS + kTok * (CW + 1);
+    if (done) {
       const int col = lt % CW, first = lt / CW * CW;
       float a[2] = {0.f, 0.f};
-      if (done) {
 #pragma unroll 4
-        for (int k = 0; k < CW; k += 2) {
-          a[0] += sum[(first + k) * (CW + 1) + col];
-          a[1] += sum[(first + k + 1) * (CW + 1) + col];
-        }
-        part[lt] = a[0] + a[1];
+      for (int k = 0; k < CW; k += 2) {
+        a[0] += sum[(first + k) * (CW + 1) + col];
+        a[1] += sum[(first + k + 1) * (CW + 1) + col];
       }
-      named_bar_sync(bar, 128);
-      if (done && lt < CW) {
-        float total = 0.f;
-#pragma unroll
-        for (int k = 0; k < 128 / CW; ++k) total += part[k * CW + lt];
-        totals[rank * N + wg * CW + lt] = total;
-        if constexpr (CT == 2)
-          st_dsmem_f32(map_smem_rank(smem_u32(totals + rank * N + wg * CW + lt), rank ^ 1), total);
-      }
+      part[lt] = a[0] + a[1];
     }
+    named_bar_sync(bar, 128);
+    if (done && lt < CW) {
+      float total = 0.f;
+#pragma unroll
+      for (int k = 0; k < 128 / CW; ++k) total += part[k * CW + lt];
+      const int c = wg * CW + lt;
+      if constexpr (CT == 2) {
+        // (a cluster barrier of all threads here took ~1300 cycles)
+        const float* other = reinterpret_cast<const float*>(smem + C::TOTAL_OFFSET) + c;
+        st_async_u32(map_smem_rank(smem_u32(other), rank ^ 1), __float_as_uint(total),
+                     map_smem_rank(smem_u32(sums_full), rank ^ 1));
+        if (!mbar_wait_cluster(sums_full, 0)) err |= kErrTimeout;
+        total += *other;
+      }
+      // no attended token: weight 0 and a zero row; NaN stays NaN
+      if (rank == 0 && rows[c] >= 0)
+        p.lse_part[(size_t)rows[c] * p.num_pieces + piece] =
+            total == 0.f ? -INFINITY : (log2f(total) - nref[lt]) * 0.69314718055994530942f;
+      nref[lt] = total == 0.f ? 0.f : v_top / total;
+    }
+    __syncwarp();
+    named_bar_sync(3, 256);
+    // The partial rows go through shared memory (the rings, idle by now), a row
+    // of this CTA's dims contiguous, and out as one bulk copy each, sixteen by one
+    // warp while the others go on: stored from the registers, 128 bytes a warp,
+    // 128 rows took 4 us.
+    constexpr int OC = CW < 16 ? CW : 16, ROW = C::MC * 128;
+    float* stage = reinterpret_cast<float*>(smem + C::RING_OFFSET) + wg * CW * ROW;
+    const int n = done ? min(CW, t.rows - wg * CW) : 0;
+#pragma unroll 1
+    for (int c0 = 0; c0 < n; c0 += OC) {
+      uint32_t y[C::MC][OC];
+#pragma unroll
+      for (int m = 0; m < C::MC; ++m) tmem_ld(y[m], o_at + m * N + c0);
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < OC; ++c) {
+        const float f = nref[c0 + c];
+#pragma unroll
+        for (int m = 0; m < C::MC; ++m) stage[(c0 + c) * ROW + m * 128 + lt] = __uint_as_float(y[m][c]) * f;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      named_bar_sync(bar, 128);
+      const int c = c0 + lane;
+      if ((warp & 3) == (c0 / OC & 3) && lane < OC && c < n)
+        bulk_s2g(p.o_part + ((size_t)rows[wg * CW + c] * p.num_pieces + piece) * D + rank * ROW, stage + c * ROW, ROW * 4);
+    }
+    wait_bulk_stores();
+    err = __reduce_or_sync(kFullMask, err);
+    if (lane == 0 && err) atomicOr(p.err, err);
   } else if constexpr (C::FP8) {
     // ---- FP8: e4m3 stages widened to f16 operand stages, a thread per token row
     const int team = (warp - (kSoftWarps + 1 + kCopyWarps)) / 4;
@@ -1025,50 +1079,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     }
   }
 
-  // ---- epilogue: both CTAs' totals are in place
-  __syncwarp();
-  S::all_threads();
-  if (warp < kSoftWarps && done) {
-    tmem_fence_after();
-    if (lt < CW) {
-      const int c = wg * CW + lt;
-      const float total = CT == 1 ? totals[c] : totals[c] + totals[N + c];
-      // no attended token: weight 0 and a zero row; NaN stays NaN
-      if (rank == 0 && rows[c] >= 0)
-        p.lse_part[(size_t)rows[c] * p.num_pieces + piece] =
-            total == 0.f ? -INFINITY : (log2f(total) - nref[lt]) * 0.69314718055994530942f;
-      nref[lt] = total == 0.f ? 0.f : v_top / total;
-    }
-  }
-  __syncthreads();
-  if (warp < kSoftWarps && done && wg * CW < t.rows) {
-    // The partial rows go through shared memory (the rings, idle by now), a row
-    // of this CTA's dims contiguous, and out as one bulk copy each: stored from
-    // the registers, 128 bytes a warp, 128 rows took 4 us.
-    constexpr int OC = CW < 16 ? CW : 16, ROW = C::MC * 128;
-    float* stage = reinterpret_cast<float*>(smem + C::RING_OFFSET) + wg * CW * ROW;
-    const int n = min(CW, t.rows - wg * CW);
-#pragma unroll 1
-    for (int c0 = 0; c0 < n; c0 += OC) {
-      uint32_t y[C::MC][OC];
-#pragma unroll
-      for (int m = 0; m < C::MC; ++m) tmem_ld(y[m], o_at + m * N + c0);
-      tmem_wait_ld();
-#pragma unroll
-      for (int c = 0; c < OC; ++c) {
-        const float f = nref[c0 + c];
-#pragma unroll
-        for (int m = 0; m < C::MC; ++m) stage[(c0 + c) * ROW + m * 128 + lt] = __uint_as_float(y[m][c]) * f;
-      }
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-    named_bar_sync(bar, 128);
-    if (lt < n) {
-      bulk_s2g(p.o_part + ((size_t)rows[wg * CW + lt] * p.num_pieces + piece) * D + rank * ROW, stage + lt * ROW, ROW * 4);
-      wait_bulk_stores();
-    }
-  }
   __syncwarp();
   tmem_fence_before();
   S::all_threads();

@@ -147,13 +147,14 @@ __device__ __forceinline__ bool mbar_wait2(uint64_t* a, uint32_t pa, uint64_t* b
 }
 
 // Bulk copy shared -> global (16-byte aligned, a multiple of 16 bytes) in the
-// calling thread's bulk group; wait_bulk_stores: all of them done.
+// calling thread's bulk group; wait_bulk_stores: all of them have read their
+// source (the grid's completion orders what they write).
 __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
                : "memory");
 }
 __device__ __forceinline__ void wait_bulk_stores() {
-  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 // Named barrier that also ORs a predicate over its threads.
