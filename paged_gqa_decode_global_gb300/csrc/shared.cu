@@ -179,19 +179,20 @@ bool shared_plan_is_valid(const pd_shared_plan* plan) {
 // GB300: a CTA's start and end, and a tile (128 tokens; a pair's 256), measured
 // at head_dim 512 and in proportion to head_dim below; the tiles in flight share
 // the memory's rate, and the pieces' partial results are written and read once.
-constexpr double kFixedUs = 9.0, kHbmBytesPerUs = 6.8e6, kPartialBytesPerUs = 5.0e6;
+constexpr double kFixedUs = 7.0, kHbmBytesPerUs = 6.8e6, kPartialBytesPerUs = 5.0e6;
 constexpr double kOwnFixedUs = 5.0;  // a stage-1 CTA of the own part
 
 double tile_us(const PrefixInstance& v) {
-  return (v.ctas == 2 ? (v.fp8 ? 6.0 : 4.0) : (v.fp8 ? 4.5 : 3.4)) * v.head_dim / 512.0;
+  return (v.ctas == 2 ? (v.fp8 ? 5.5 : 3.6) : (v.fp8 ? 4.6 : 2.9)) * v.head_dim / 512.0;
 }
 
-// SM time of the own part in one piece a request, in microseconds.
+// SM time of the own part in one piece a request, in microseconds (two of its
+// CTAs share an SM).
 double own_sm_us(const pd_plan& own, const int32_t* lens) {
   const double per_us = 50.0 * 512 / own.layer.head_dim;  // tokens of a lone stage-1 CTA
   double us = 0;
   for (int b = 0; b < own.batch; ++b) us += (kOwnFixedUs + lens[b] / per_us) * own.grid_y;
-  return us;
+  return us / 2;
 }
 
 // The prefix's pieces: of every count of pieces for the longest prefix, the one
@@ -228,7 +229,9 @@ void plan_pieces(pd_shared_plan& sp, const int32_t* starts, const int32_t* lens,
     const double load = (ctas * kFixedUs + tiles * cta_us) / slots;
     double us = ctas <= slots ? one : std::max(one, load + 0.4 * one);
     us = std::max(us, load + own_us / sm_count + kOwnFixedUs);
-    us = std::max(us, kFixedUs + distinct * tile_bytes / kHbmBytesPerUs) +
+    // (near the memory's rate a tile takes longer: a smooth maximum)
+    const double alone = us - kFixedUs, hbm = distinct * tile_bytes / kHbmBytesPerUs;
+    us = kFixedUs + std::pow(std::pow(alone, 4) + std::pow(hbm, 4), 0.25) +
          2.0 * rows * pieces * ly.head_dim * 4.0 / kPartialBytesPerUs;
     if (us < best) {
       best = us;
