@@ -489,7 +489,9 @@ size_t paged_decode_append_slots_workspace(int32_t batch);
  *     after it that need no page are still served).
  * A page id outside [0, num_pages), from the free list or in the table, gives
  * its tokens slot -1 and sets PD_DEVFLAG_BAD_PAGE. Whole-number results, the
- * same on every run. Capturable; nothing is allocated.
+ * same on every run. Capturable; nothing is allocated. Launched as a
+ * programmatic dependent that lets the launch behind it start once it has
+ * waited itself.
  * Returns PD_ERR_INVALID_ARG / PD_ERR_WORKSPACE_TOO_SMALL without launching,
  * PD_ERR_CUDA if a launch fails.
  */

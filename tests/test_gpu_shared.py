@@ -356,6 +356,13 @@ def test_long_prefix_past_32_bit_offsets():
     c.check()
 
 
+@pytest.mark.parametrize("Hq,Hkv,d,T", [(16, 4, 512, 1), (16, 4, 512, 4), (32, 2, 512, 1), (16, 8, 256, 5)])
+@pytest.mark.parametrize("fp8,kvs", [(False, False), (False, True), (True, False), (True, True)])
+def test_long_own_parts(Hq, Hkv, d, T, fp8, kvs):
+    # own tokens in several pieces, and two column tiles in a CTA (no sum is longer than a piece's)
+    Case(Hq, Hkv, d, [4200, 37, 1500], [0, 3], [64], T=T, fp8=fp8, kvs=kvs, seed=T).check()
+
+
 @pytest.mark.parametrize("seed", range(24))
 def test_random_shapes(seed):
     rng = random.Random(seed)
