@@ -61,14 +61,14 @@ FALLBACK_HBM_GBS = 6800.0
 # entry whose sources or plan differ from the run's is not used (the captures
 # and their commands are summarised under profiles/).
 NCU_TRAFFIC = {
-    "390644f8bf77bb67": {
-        "w4a": (1073983488 + 2760704, (9, 3648, 1)),
-        "w2": (67294976 + 501504, (4, 256, 2)),
-        "w3": (68276992 + 407808, (2, 544, 2)),
-        "w4a-fp8": (537289728 + 2464768, (9, 3648, 1)),
-        "w5global": (1596576512 + 4325632, (19, 5456, 1)),
-        "w5global-fp8": (798929920 + 4875776, (19, 5456, 1)),
-        "w5sliding": (68173312 + 504320, (2, 544, 2)),
+    "0da2d7215439a3d3": {
+        "w4a": (1073949440 + 3192064, (9, 3648, 1)),
+        "w2": (67294464 + 532480, (4, 256, 2)),
+        "w3": (68277504 + 377344, (2, 544, 2)),
+        "w4a-fp8": (537290240 + 2778880, (9, 3648, 1)),
+        "w5global": (1596575488 + 4344832, (19, 5456, 1)),
+        "w5global-fp8": (798928384 + 4827648, (19, 5456, 1)),
+        "w5sliding": (68174080 + 527872, (2, 544, 2)),
     },
 }
 

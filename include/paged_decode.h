@@ -550,7 +550,7 @@ pd_status paged_decode_write_slots_fp8(const pd_layer_desc* layer, int32_t num_t
  * last T own tokens, causal among themselves.
  */
 typedef struct {
-  pd_plan own;              /* the own tokens' part */
+  pd_plan own;              /* the own tokens' part (launched with fewer threads and less shared memory than it names) */
   int32_t num_groups;
   int32_t max_prefix_pages; /* row length of prefix_tables */
   int32_t row_tile;         /* query rows a CTA of the prefix pass serves */

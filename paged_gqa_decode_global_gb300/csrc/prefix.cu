@@ -39,13 +39,13 @@
 // second, so nothing is transposed; P is written N-major, a token's row at a
 // time. A K=V layer fetches the tile again for its second use (an L2 hit).
 //
-// What bounds it, at head_dim 512 (one GB300): a pair's tile of 256 tokens takes
-// 4.0-4.2 us, 2.1 us of it the products, the rest the copies' latency over a
-// ring of one tile (131 KB of 224: the query rows take 64 KB, P 32 KB); one CTA's
-// tile of 128 tokens 2.6 us with 16 rows and 3.4 us with 64, the copies of a page
-// at a time; FP8 4.6 us with 64 rows (single), 5.5 us (pair): the widening's
-// passes through shared memory. 1024 rows a KV head over 16384 tokens (137 GFLOP):
-// 145 us; 64 rows over 32768 (268 MB): 50 us.
+// What bounds it, at head_dim 512 (one GB300, the whole call over the tiles of
+// its longest CTA): a pair's tile of 256 tokens takes 3.4 us with few pairs and
+// 3.9 with 64, 2.15 us of it the products and most of the rest the copies'
+// latency over a ring of half a tile's bytes (128 of 224 KB: the query rows take
+// 64, P 32); one CTA's tile of 128 tokens 2.8 us with 64 rows, 2.3 with 16, and
+// 4 with 116 CTAs, which together take 6.1 TB/s; FP8 5.4 us (pair), 4.6 (64
+// rows), 3.5 (16): the widening's passes through shared memory.
 //
 // Roundings: P to the operands' type. bf16 cache: bf16, 2^-9 a probability. FP8
 // cache: f16, into which e4m3 widens exactly; q rounds to f16 once (as in the
