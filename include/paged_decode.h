@@ -613,6 +613,50 @@ pd_status paged_decode_global_shared_fp8(const pd_shared_plan* plan, const void*
                                          const int32_t* seq_lens, float scale, void* workspace,
                                          size_t workspace_bytes, void* out, void* stream);
 
+/* ---- The same calls with their arguments in a structure -------------------------
+ *
+ * For callers whose foreign calls cost by the argument (ctypes: ~2 us for twenty):
+ * member by member the arguments of the calls named above, which do the work.
+ * fp8 != 0: the _fp8 call (the scales are not looked at otherwise).
+ */
+typedef struct {
+  int32_t batch, page_size, num_pages, max_pages, max_tokens, num_free;
+  const int32_t *cached_lens, *new_tokens, *free_pages, *free_range;
+  int32_t *block_tables, *seq_lens, *token_starts, *slot_map, *positions, *free_range_out;
+  uint32_t* device_flags;
+  void* workspace;
+  uint64_t workspace_bytes;
+  void* stream;
+} pd_append_slots_args;
+
+typedef struct {
+  const pd_layer_desc* layer;
+  int32_t num_tokens, fp8;
+  const void *k_in, *v_in;
+  int64_t k_stride, v_stride;
+  const int32_t* slot_map;
+  void *k_pool, *v_pool;
+  const float *k_scale, *v_scale;
+  uint32_t* device_flags;
+  void* stream;
+} pd_write_slots_args;
+
+typedef struct {
+  const pd_shared_plan* plan;
+  const void *q, *k_pool, *v_pool;
+  const float *k_scale, *v_scale;
+  const int32_t *prefix_tables, *prefix_lens, *group_starts, *block_tables, *seq_lens;
+  float scale;
+  int32_t fp8;
+  void* workspace;
+  uint64_t workspace_bytes;
+  void *out, *stream;
+} pd_global_shared_args;
+
+pd_status paged_decode_append_slots_args(const pd_append_slots_args* args);
+pd_status paged_decode_write_slots_args(const pd_write_slots_args* args);
+pd_status paged_decode_global_shared_args(const pd_global_shared_args* args);
+
 /* ---- Host-in/host-out decode loops ---------------------------------------------
  *
  * Not an operation of the decode method: plumbing for a caller whose inputs

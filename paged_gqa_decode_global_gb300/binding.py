@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 import threading
 from typing import Optional, Sequence
 
@@ -60,6 +61,9 @@ EXPORTED = (
     "paged_decode_plan_shared",
     "paged_decode_global_shared",
     "paged_decode_global_shared_fp8",
+    "paged_decode_append_slots_args",
+    "paged_decode_write_slots_args",
+    "paged_decode_global_shared_args",
 )
 
 
@@ -206,6 +210,9 @@ def load_library(path: Optional[str] = None):
         lib.paged_decode_global_shared.restype = ctypes.c_int
         lib.paged_decode_global_shared_fp8.argtypes = [ctypes.POINTER(SharedPlan)] + [vp] * 10 + [f32, vp, u64, vp, vp]
         lib.paged_decode_global_shared_fp8.restype = ctypes.c_int
+        for fn in (lib.paged_decode_append_slots_args, lib.paged_decode_write_slots_args,
+                   lib.paged_decode_global_shared_args):
+            fn.argtypes, fn.restype = [ctypes.c_char_p], ctypes.c_int
         found = int(lib.paged_decode_abi_version())
         if found != ABI_VERSION:
             raise RuntimeError(f"{p} has ABI version {found}, this binding marshals version {ABI_VERSION}: rebuild it "
@@ -525,6 +532,13 @@ def paged_decode_combine(o_parts, lse_parts, out, stream=None) -> None:
 # Block tables and slot maps, the cache write by slot, shared-prefix decode
 # ----------------------------------------------------------------------------
 
+# pd_append_slots_args, pd_write_slots_args and pd_global_shared_args: one
+# argument for ctypes to convert instead of up to twenty (~2 us)
+_SLOTS_ARGS = struct.Struct("6i12PQP").pack
+_WRITE_ARGS = struct.Struct("P2i2P2q7P").pack
+_SHARED_ARGS = struct.Struct("P10PfiPQ2P").pack
+
+
 def _refuse(name: str, t, dtype, shape) -> None:
     raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {shape}, got {t.dtype} "
                      f"{tuple(t.shape)}{'' if t.is_contiguous() else ' (not contiguous)'} on {t.device}")
@@ -563,11 +577,11 @@ def paged_decode_append_slots(page_size: int, num_pages: int, cached_lens, new_t
     if positions is not None:
         _want(positions, "positions", i32, (n,), dev)
     _want(free_range_out, "free_range_out", i32, (2,), dev)
-    st = load_library().paged_decode_append_slots(
-        B, page_size, num_pages, width, n, cached_lens.data_ptr(), new_tokens.data_ptr(), free_pages.data_ptr(), free,
+    st = load_library().paged_decode_append_slots_args(_SLOTS_ARGS(
+        B, page_size, num_pages, width, n, free, cached_lens.data_ptr(), new_tokens.data_ptr(), free_pages.data_ptr(),
         free_range.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), token_starts.data_ptr(),
-        slot_map.data_ptr(), _ptr(positions), free_range_out.data_ptr(), device_flags.data_ptr(),
-        workspace.data_ptr(), workspace.nbytes, _stream_ptr(stream))
+        slot_map.data_ptr(), _ptr(positions) or 0, free_range_out.data_ptr(), device_flags.data_ptr(),
+        workspace.data_ptr(), workspace.nbytes, _stream_ptr(stream) or 0))
     if st != PD_OK:
         raise PagedDecodeError(st, "paged_decode_append_slots")
 
@@ -597,18 +611,14 @@ def _write_slots(fp8: bool, desc, k_in, v_in, slot_map, k_pool, v_pool, k_scale,
             raise ValueError("a K != V layer needs v_in and v_pool")
         _want(v_pool, "v_pool", pool_type, pool, dev)
         vs = _token_rows(v_in, "v_in", torch.bfloat16, rows, dev)
-    lib = load_library()
     if fp8:
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
             if t is not None:
                 _want(t, name, torch.float32, pool[:2], dev)
-        st = lib.paged_decode_write_slots_fp8(ctypes.byref(desc), n, k_in.data_ptr(), _ptr(v_in), ks, vs,
-                                              slot_map.data_ptr(), k_pool.data_ptr(), _ptr(v_pool), _ptr(k_scale),
-                                              _ptr(v_scale), device_flags.data_ptr(), _stream_ptr(stream))
-    else:
-        st = lib.paged_decode_write_slots(ctypes.byref(desc), n, k_in.data_ptr(), _ptr(v_in), ks, vs,
-                                          slot_map.data_ptr(), k_pool.data_ptr(), _ptr(v_pool),
-                                          device_flags.data_ptr(), _stream_ptr(stream))
+    st = load_library().paged_decode_write_slots_args(_WRITE_ARGS(
+        ctypes.addressof(desc), n, fp8, k_in.data_ptr(), _ptr(v_in) or 0, ks, vs, slot_map.data_ptr(),
+        k_pool.data_ptr(), _ptr(v_pool) or 0, _ptr(k_scale) or 0, _ptr(v_scale) or 0, device_flags.data_ptr(),
+        _stream_ptr(stream) or 0))
     if st != PD_OK:
         raise PagedDecodeError(st, "paged_decode_write_slots_fp8" if fp8 else "paged_decode_write_slots")
 
@@ -644,18 +654,23 @@ def paged_decode_plan_shared(desc: LayerDesc, query_tokens: int, seq_lens_host: 
     return plan
 
 
-def _workspace_bytes(workspace, given) -> int:
-    return int(workspace.numel() * workspace.element_size() if given is None else given)
+def _shared_status(fp8: bool, plan, k_scale, v_scale, scale, workspace, workspace_bytes, stream, q, k_pool, v_pool,
+                   *rest) -> int:
+    """The call on addresses (rest: the prefix tables' to the lengths', then out's); 0 for what is not there."""
+    *tables, out = rest
+    return load_library().paged_decode_global_shared_args(_SHARED_ARGS(
+        ctypes.addressof(plan), q, k_pool, v_pool, _ptr(k_scale) or 0, _ptr(v_scale) or 0, *tables, scale, fp8,
+        workspace.data_ptr(), workspace.nbytes if workspace_bytes is None else int(workspace_bytes), out,
+        _stream_ptr(stream) or 0))
 
 
 def paged_decode_global_shared(plan: SharedPlan, q, k_pool, v_pool, prefix_tables, prefix_lens, group_starts,
                                block_tables, seq_lens, scale: float, workspace, out, stream=None,
                                workspace_bytes: Optional[int] = None) -> None:
     """Decode of a batch whose groups share prefixes, merge included."""
-    st = load_library().paged_decode_global_shared(
-        ctypes.byref(plan), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(prefix_tables), _ptr(prefix_lens),
-        _ptr(group_starts), _ptr(block_tables), _ptr(seq_lens), float(scale), _ptr(workspace),
-        _workspace_bytes(workspace, workspace_bytes), _ptr(out), _stream_ptr(stream))
+    st = _shared_status(False, plan, None, None, scale, workspace, workspace_bytes, stream,
+                        *(_ptr(t) or 0 for t in (q, k_pool, v_pool, prefix_tables, prefix_lens, group_starts,
+                                                 block_tables, seq_lens, out)))
     _check(st, "paged_decode_global_shared")
 
 
@@ -663,10 +678,9 @@ def paged_decode_global_shared_fp8(plan: SharedPlan, q, k_pool, v_pool, k_scale,
                                    group_starts, block_tables, seq_lens, scale: float, workspace, out, stream=None,
                                    workspace_bytes: Optional[int] = None) -> None:
     """The same over an e4m3 cache with per-(page, KV head) scales."""
-    st = load_library().paged_decode_global_shared_fp8(
-        ctypes.byref(plan), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(prefix_tables),
-        _ptr(prefix_lens), _ptr(group_starts), _ptr(block_tables), _ptr(seq_lens), float(scale), _ptr(workspace),
-        _workspace_bytes(workspace, workspace_bytes), _ptr(out), _stream_ptr(stream))
+    st = _shared_status(True, plan, k_scale, v_scale, scale, workspace, workspace_bytes, stream,
+                        *(_ptr(t) or 0 for t in (q, k_pool, v_pool, prefix_tables, prefix_lens, group_starts,
+                                                 block_tables, seq_lens, out)))
     _check(st, "paged_decode_global_shared_fp8")
 
 
@@ -703,12 +717,12 @@ class SharedPrefixStep:
                  stream=None, k_scale=None, v_scale=None):
         self._check_tensors(q, k_pool, v_pool, prefix_tables, prefix_lens, group_starts, block_tables, seq_lens, out,
                             k_scale, v_scale)
-        if self.fp8:
-            paged_decode_global_shared_fp8(self.plan, q, k_pool, v_pool, k_scale, v_scale, prefix_tables, prefix_lens,
-                                           group_starts, block_tables, seq_lens, scale, self.workspace, out, stream)
-        else:
-            paged_decode_global_shared(self.plan, q, k_pool, v_pool, prefix_tables, prefix_lens, group_starts,
-                                       block_tables, seq_lens, scale, self.workspace, out, stream)
+        st = _shared_status(self.fp8, self.plan, k_scale, v_scale, scale, self.workspace, None, stream, q.data_ptr(),
+                            k_pool.data_ptr(), 0 if v_pool is None else v_pool.data_ptr(), prefix_tables.data_ptr(),
+                            prefix_lens.data_ptr(), group_starts.data_ptr(), block_tables.data_ptr(),
+                            seq_lens.data_ptr(), out.data_ptr())
+        if st != PD_OK:
+            raise PagedDecodeError(st, "paged_decode_global_shared_fp8" if self.fp8 else "paged_decode_global_shared")
         return out
 
     def _check_tensors(self, q, k_pool, v_pool, prefix_tables, prefix_lens, group_starts, block_tables, seq_lens, out,

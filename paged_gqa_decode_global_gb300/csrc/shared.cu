@@ -474,4 +474,11 @@ pd_status paged_decode_global_shared_fp8(const pd_shared_plan* plan, const void*
                            block_tables, seq_lens, scale, workspace, workspace_bytes, out, stream);
 }
 
+pd_status paged_decode_global_shared_args(const pd_global_shared_args* a) {
+  if (!a) return PD_ERR_INVALID_ARG;
+  return pd::decode_shared(a->plan, a->fp8 != 0, a->q, a->k_pool, a->v_pool, a->fp8 ? a->k_scale : nullptr,
+                           a->fp8 ? a->v_scale : nullptr, a->prefix_tables, a->prefix_lens, a->group_starts,
+                           a->block_tables, a->seq_lens, a->scale, a->workspace, a->workspace_bytes, a->out, a->stream);
+}
+
 }  // extern "C"

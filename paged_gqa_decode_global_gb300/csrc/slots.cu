@@ -322,4 +322,12 @@ pd_status paged_decode_append_slots(int32_t batch, int32_t page_size, int32_t nu
   return e == cudaSuccess ? PD_OK : PD_ERR_CUDA;
 }
 
+pd_status paged_decode_append_slots_args(const pd_append_slots_args* a) {
+  if (!a) return PD_ERR_INVALID_ARG;
+  return paged_decode_append_slots(a->batch, a->page_size, a->num_pages, a->max_pages, a->max_tokens, a->cached_lens,
+                                   a->new_tokens, a->free_pages, a->num_free, a->free_range, a->block_tables,
+                                   a->seq_lens, a->token_starts, a->slot_map, a->positions, a->free_range_out,
+                                   a->device_flags, a->workspace, a->workspace_bytes, a->stream);
+}
+
 }  // extern "C"

@@ -234,4 +234,11 @@ pd_status paged_decode_write_slots_fp8(const pd_layer_desc* layer, int32_t num_t
                          v_scale, device_flags, stream);
 }
 
+pd_status paged_decode_write_slots_args(const pd_write_slots_args* a) {
+  if (!a) return PD_ERR_INVALID_ARG;
+  return pd::write_slots(a->layer, a->fp8 != 0, a->num_tokens, a->k_in, a->v_in, a->k_stride, a->v_stride, a->slot_map,
+                         a->k_pool, a->v_pool, a->fp8 ? a->k_scale : nullptr, a->fp8 ? a->v_scale : nullptr,
+                         a->device_flags, a->stream);
+}
+
 }  // extern "C"

@@ -219,3 +219,13 @@ def test_binding_checks_tensors(lib):
                     (4, i(8, 4).t())):
         with pytest.raises(ValueError):
             b.paged_decode_append_slots(16, 64, *(args[:at] + [bad] + args[at + 1:]), stream=0)
+
+
+def test_calls_by_structure(lib):
+    # the structures are laid out as the binding packs them, and a missing one is refused
+    calls = (lib.paged_decode_append_slots_args, lib.paged_decode_write_slots_args, lib.paged_decode_global_shared_args)
+    packed = (b._SLOTS_ARGS(*[0] * 20), b._WRITE_ARGS(*[0] * 14), b._SHARED_ARGS(*[0] * 17))
+    assert [len(x) for x in packed] == [136, 104, 128]
+    for call, zeros in zip(calls, packed):
+        assert call(None) != b.PD_OK
+        assert call(zeros) != b.PD_OK  # page size 0, no layer, no plan
