@@ -44,8 +44,8 @@
 // 3.9 with 64, 2.15 us of it the products and most of the rest the copies'
 // latency over a ring of half a tile's bytes (128 of 224 KB: the query rows take
 // 64, P 32); one CTA's tile of 128 tokens 2.8 us with 64 rows, 2.3 with 16, and
-// 4 with 116 CTAs, which together take 6.1 TB/s; FP8 5.4 us (pair), 4.6 (64
-// rows), 3.5 (16): the widening's passes through shared memory.
+// 4 with 116 CTAs, which together take 6.1 TB/s; FP8 5.6 us (pair), 3.8 (64
+// rows), 3.25 (16): the widening's passes through shared memory.
 //
 // Roundings: P to the operands' type. bf16 cache: bf16, 2^-9 a probability. FP8
 // cache: f16, into which e4m3 widens exactly; q rounds to f16 once (as in the
@@ -1049,17 +1049,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     bool ok = true;
     for (int it = team; it < total; it += C::TEAMS) {
       const int st = it % NST, rs = it % C::NRAW;
+      // One CTA: the stage into registers, and released before the operand stage
+      // is waited for (64 rows 4.6 -> 3.8 us a tile, 16 rows 3.5 -> 3.25; a pair
+      // 5.4 -> 5.7). Not where its wait ran out (the copies into it are not
+      // done), and not before the fence: without it, copies overtook the reads.
       ok = mbar_wait(&raw_full[rs], (it / C::NRAW) & 1);
-      if (ok && it >= NST) ok = mbar_wait(&empty[st], ((it / NST) - 1) & 1);
-      if (__any_sync(kFullMask, !ok)) {
-        if (lane == 0) atomicOr(p.err, kErrTimeout);
-        break;
-      }
+      if (CT == 2 && ok && it >= NST) ok = mbar_wait(&empty[st], ((it / NST) - 1) & 1);
+      if (__any_sync(kFullMask, !ok)) break;
       const uint8_t* src = smem + C::RAW_OFFSET + rs * kRaw + row * 128;
       uint8_t* dst = smem + C::RING_OFFSET + st * kStage + (row >> 3) * 2048 + (row & 7) * 128;
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const uint4 w = *reinterpret_cast<const uint4*>(src + ((c ^ sw) << 4));
+      auto get = [&](int c) { return *reinterpret_cast<const uint4*>(src + ((c ^ sw) << 4)); };
+      auto put = [&](int c, const uint4& w) {
         uint4 a, b;
         widen4(w.x, a.x, a.y);
         widen4(w.y, a.z, a.w);
@@ -1069,14 +1069,30 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
         const int cc = (c & 3) * 2;
         *reinterpret_cast<uint4*>(to + ((cc ^ sw) << 4)) = a;
         *reinterpret_cast<uint4*>(to + (((cc + 1) ^ sw) << 4)) = b;
+      };
+      if constexpr (CT == 1) {
+        uint4 w[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) w[c] = get(c);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&raw_empty[rs]);
+        if (it >= NST) ok = mbar_wait(&empty[st], ((it / NST) - 1) & 1);
+        if (__any_sync(kFullMask, !ok)) break;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) put(c, w[c]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) put(c, get(c));
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&raw_empty[rs]);
+        if (CT == 2) mbar_arrive(&raw_empty[rs]);
         S::arrive_leader(&full[st]);
       }
     }
+    if (__any_sync(kFullMask, !ok) && lane == 0) atomicOr(p.err, kErrTimeout);
   }
 
   __syncwarp();

@@ -183,7 +183,7 @@ constexpr double kFixedUs = 7.0, kHbmBytesPerUs = 6.8e6, kPartialBytesPerUs = 5.
 constexpr double kOwnFixedUs = 5.0;  // a stage-1 CTA of the own part
 
 double tile_us(const PrefixInstance& v) {
-  return (v.ctas == 2 ? (v.fp8 ? 5.5 : 3.6) : (v.fp8 ? 4.6 : 2.9)) * v.head_dim / 512.0;
+  return (v.ctas == 2 ? (v.fp8 ? 5.5 : 3.6) : (v.fp8 ? 3.8 : 2.9)) * v.head_dim / 512.0;
 }
 
 // SM time of the own part in one piece a request, in microseconds (two of its

@@ -230,6 +230,20 @@ def test_same_bits_on_every_run_and_in_any_company():
     assert torch.equal(a[keep].view(torch.int16), o[keep].view(torch.int16))
 
 
+@pytest.mark.parametrize("batch", [2, 7, 15, 40])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_many_runs_give_the_same_bits(batch, fp8):
+    # calls in a row, each overlapping the ends of the others: what one stage of a ring
+    # took from the wrong copy would show as a run that differs
+    c = Case(16, 4, 512, [20] * batch, [0, batch], [8000], fp8=fp8, seed=batch)
+    ref, step = c.run()
+    outs = [torch.empty_like(ref) for _ in range(200)]
+    for o in outs:
+        c.run(step, o)
+    assert step.check() == 0
+    assert all(torch.equal(o.view(torch.int16), ref.view(torch.int16)) for o in outs)
+
+
 def test_agrees_with_plain_decode():
     """One table per request over the same pages: decode's result, within both tolerances."""
     c = Case(16, 4, 512, [17, 64, 1], [0, 3], [608], seed=2, garbage=False)
