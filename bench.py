@@ -74,7 +74,7 @@ NCU_TRAFFIC = {
 
 # the same for the fused QKV norm + RoPE + cache-write kernel (--op prepare)
 PREP_NCU_TRAFFIC = {
-    "bddd86ff645abd50": {"w2": 221184},
+    "88e0b76282d7ad37": {"w2": 221184},
 }
 
 STAGE1_SOURCES = ("stage1.cu", "pd_common.cuh", "pd_variants.h", "pd_kernels.h")
