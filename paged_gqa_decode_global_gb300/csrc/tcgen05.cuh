@@ -131,6 +131,7 @@ __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[32]) 
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Whether the phase of `parity` is complete, without waiting.
 __device__ __forceinline__ uint32_t mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
@@ -139,11 +140,6 @@ __device__ __forceinline__ uint32_t mbar_test(uint64_t* bar, uint32_t parity) {
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return done;
-}
-// Two barriers at once: one latency where both are done.
-__device__ __forceinline__ bool mbar_wait2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb) {
-  const uint32_t x = mbar_test(a, pa), y = mbar_test(b, pb);
-  return (x & y) != 0 || (mbar_wait(a, pa) && mbar_wait(b, pb));
 }
 
 // Bulk copy shared -> global (16-byte aligned, a multiple of 16 bytes) in the
