@@ -6,7 +6,8 @@
 // leaves: what counts is the CTAs an SM gets through, and a lone one spends most
 // of its ~7 us waiting (its length, page ids, query rows, first blocks, merge).
 // So these instances have three consumer warps and a ring of at most 96 KB, and
-// two of them share an SM.
+// two of them share an SM (1024 CTAs of ~100 tokens beside 64 pairs of the prefix
+// pass: the whole call 161 -> 145 us).
 #define PD_STAGE1_BESIDE 1
 #include <type_traits>
 
