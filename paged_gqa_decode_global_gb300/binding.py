@@ -577,6 +577,8 @@ def paged_decode_append_slots(page_size: int, num_pages: int, cached_lens, new_t
     if positions is not None:
         _want(positions, "positions", i32, (n,), dev)
     _want(free_range_out, "free_range_out", i32, (2,), dev)
+    if dev < 0 or device_flags.get_device() != dev or workspace.get_device() != dev:
+        raise ValueError("every tensor, device_flags and workspace among them, has to be on the call's GPU")
     st = load_library().paged_decode_append_slots_args(_SLOTS_ARGS(
         B, page_size, num_pages, width, n, free, cached_lens.data_ptr(), new_tokens.data_ptr(), free_pages.data_ptr(),
         free_range.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), token_starts.data_ptr(),
@@ -615,6 +617,8 @@ def _write_slots(fp8: bool, desc, k_in, v_in, slot_map, k_pool, v_pool, k_scale,
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
             if t is not None:
                 _want(t, name, torch.float32, pool[:2], dev)
+    if dev < 0 or device_flags.get_device() != dev:
+        raise ValueError("every tensor, device_flags among them, has to be on the call's GPU")
     st = load_library().paged_decode_write_slots_args(_WRITE_ARGS(
         ctypes.addressof(desc), n, fp8, k_in.data_ptr(), _ptr(v_in) or 0, ks, vs, slot_map.data_ptr(),
         k_pool.data_ptr(), _ptr(v_pool) or 0, _ptr(k_scale) or 0, _ptr(v_scale) or 0, device_flags.data_ptr(),
@@ -694,6 +698,8 @@ class SharedPrefixStep:
                  query_tokens=1, sm_count=None, device=None):
         import torch
         device = torch.device("cuda") if device is None else torch.device(device)
+        if device.type != "cuda":
+            raise ValueError(f"a decode runs on a GPU, not on {device}")
         if sm_count is None:
             sm_count = torch.cuda.get_device_properties(device).multi_processor_count
         self.desc = layer_desc(num_q_heads, num_kv_heads, head_dim, page_size, num_pages, max_pages_per_seq, 0,

@@ -229,3 +229,14 @@ def test_calls_by_structure(lib):
     for call, zeros in zip(calls, packed):
         assert call(None) != b.PD_OK
         assert call(zeros) != b.PD_OK  # page size 0, no layer, no plan
+
+
+def test_tensors_on_the_host_are_refused(lib):
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    with pytest.raises(ValueError, match="GPU"):
+        b.paged_decode_append_slots(16, 64, i(4), i(4), i(9), i(2), i(4, 8), i(4), i(5), i(32), None, i(2), i(1),
+                                    torch.zeros(512, dtype=torch.uint8), stream=0)
+    k = torch.zeros(3, 4, 512, dtype=torch.bfloat16)
+    pool = torch.zeros(4, 4, 16, 512, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="GPU"):
+        b.paged_decode_write_slots(_desc(num_pages=4), k, k, i(3), pool, pool.clone(), i(1), 0)
