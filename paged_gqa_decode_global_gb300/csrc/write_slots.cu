@@ -40,8 +40,8 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 }
 
 // x / s rounded to nearest, for s with its correctly rounded reciprocal r, all
-// normal and far from the ends of the range: the quotient q = x r corrected by
-// its exact remainder, q + (x - q s) r, is the correctly rounded one (P. W.
+// normal and far from the ends of the range (e4m3x16 sees to that): the quotient
+// q = x r corrected by its exact remainder, q + (x - q s) r, is the correctly rounded one (P. W.
 // Markstein, Computation of elementary functions on the IBM RISC System/6000
 // processor, IBM J. Res. Dev. 34, 1990). Three operations, for two elements at
 // once; with the general division 74 million elements took 70 us, one element
@@ -81,16 +81,18 @@ __device__ __noinline__ uint32_t e4m3x4_any(uint32_t a, uint32_t b, float s) {
          e4m3x2(__fdiv_rn(__uint_as_float(b << 16), s), __fdiv_rn(__uint_as_float(b & 0xffff0000u), s)) << 16;
 }
 
-// The larger magnitudes of two pairs of bf16, as integers (infinity and NaN: 0x7f80 and more).
+// The larger magnitudes of two pairs of bf16, as integers (their order is the magnitudes', infinity and NaN last).
 __device__ __forceinline__ uint32_t larger2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7fff7fffu); }
 
 __device__ __forceinline__ uint4 e4m3x16(const uint4& a, const uint4& b, float s) {
   // scales within 2^+-60 keep every quotient that matters (2^-11 to 2^9) and its
-  // remainder normal; a smaller quotient rounds to zero, a larger one saturates
+  // remainder normal, and a smaller quotient rounds to zero; values below 2^67
+  // (bf16 0x6100) keep the others below 2^127, which saturate. (A quotient past
+  // the fp32 range would have an infinite remainder and end as NaN.)
   const float size = fabsf(s);
   const uint32_t m = larger2(larger2(larger2(larger2(a.x & 0x7fff7fffu, a.y), larger2(a.z & 0x7fff7fffu, a.w)), b.x),
                              larger2(larger2(b.y & 0x7fff7fffu, b.z), b.w));
-  const bool odd = !(size > 0x1p-60f && size < 0x1p60f) || (m & 0xffffu) >= 0x7f80u || m >= 0x7f800000u;
+  const bool odd = !(size > 0x1p-60f && size < 0x1p60f) || (m & 0xffffu) >= 0x6100u || m >= 0x61000000u;
   if (odd)
     return make_uint4(e4m3x4_any(a.x, a.y, s), e4m3x4_any(a.z, a.w, s), e4m3x4_any(b.x, b.y, s),
                       e4m3x4_any(b.z, b.w, s));
