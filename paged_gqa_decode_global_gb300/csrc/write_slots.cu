@@ -45,9 +45,11 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 // Markstein, Computation of elementary functions on the IBM RISC System/6000
 // processor, IBM J. Res. Dev. 34, 1990). Three operations, for two elements at
 // once; with the general division 74 million elements took 70 us, one element
-// at a time 41.2 (38.3 now).
+// at a time 41.2 (38.3 now). It is the negated quotient that is computed, x (-r)
+// and so on: where x is a zero the remainder is +0, and added to a quotient of -0
+// it would lose its sign; added to the negated one it loses none.
 struct Scale2 {
-  uint64_t r, minus_s;  // the same in both halves
+  uint64_t minus_r, s;  // the same in both halves
 };
 __device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
   uint64_t r;
@@ -56,23 +58,23 @@ __device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
 }
 __device__ __forceinline__ Scale2 scale2(float s) {
   const float r = __frcp_rn(s);
-  return {f32x2(r, r), f32x2(-s, -s)};
+  return {f32x2(-r, -r), f32x2(s, s)};
 }
 
-// Two bf16 -> their quotients' codes.
-__device__ __forceinline__ uint32_t e4m3x2(uint32_t w, const Scale2& k) {
+// Two bf16 -> their negated quotients' codes.
+__device__ __forceinline__ uint32_t minus_e4m3x2(uint32_t w, const Scale2& k) {
   const uint64_t x = f32x2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   uint64_t q, e;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x), "l"(k.r));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e) : "l"(q), "l"(k.minus_s), "l"(x));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(e), "l"(k.r), "l"(q));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x), "l"(k.minus_r));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e) : "l"(q), "l"(k.s), "l"(x));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(e), "l"(k.minus_r), "l"(q));
   float lo, hi;
   asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(q));
   return e4m3x2(lo, hi);
 }
 
 __device__ __forceinline__ uint32_t e4m3x4(uint32_t a, uint32_t b, const Scale2& k) {
-  return e4m3x2(a, k) | e4m3x2(b, k) << 16;
+  return (minus_e4m3x2(a, k) | minus_e4m3x2(b, k) << 16) ^ 0x80808080u;
 }
 
 // Any scale and any values: the division itself.
@@ -85,14 +87,14 @@ __device__ __noinline__ uint32_t e4m3x4_any(uint32_t a, uint32_t b, float s) {
 __device__ __forceinline__ uint32_t larger2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7fff7fffu); }
 
 __device__ __forceinline__ uint4 e4m3x16(const uint4& a, const uint4& b, float s) {
-  // scales within 2^+-60 keep every quotient that matters (2^-11 to 2^9) and its
+  // scales from 2^-60 to 2^60 keep every quotient that matters (2^-11 to 2^9) and its
   // remainder normal, and a smaller quotient rounds to zero; values below 2^67
   // (bf16 0x6100) keep the others below 2^127, which saturate. (A quotient past
-  // the fp32 range would have an infinite remainder and end as NaN.)
-  const float size = fabsf(s);
+  // the fp32 range would have an infinite remainder and end as NaN.) Negative
+  // scales, under which zeros would lose their sign, take the division too.
   const uint32_t m = larger2(larger2(larger2(larger2(a.x & 0x7fff7fffu, a.y), larger2(a.z & 0x7fff7fffu, a.w)), b.x),
                              larger2(larger2(b.y & 0x7fff7fffu, b.z), b.w));
-  const bool odd = !(size > 0x1p-60f && size < 0x1p60f) || (m & 0xffffu) >= 0x6100u || m >= 0x61000000u;
+  const bool odd = !(s > 0x1p-60f && s < 0x1p60f) || (m & 0xffffu) >= 0x6100u || m >= 0x61000000u;
   if (odd)
     return make_uint4(e4m3x4_any(a.x, a.y, s), e4m3x4_any(a.z, a.w, s), e4m3x4_any(b.x, b.y, s),
                       e4m3x4_any(b.z, b.w, s));

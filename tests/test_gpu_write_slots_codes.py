@@ -82,3 +82,14 @@ def test_infinities_and_nan_beside_ordinary_values():
     bits[::16] = torch.tensor([0x7f80, 0xff80, 0x7fc0, 0xffc1, 0x7f81], dtype=torch.int32).repeat(25)
     x = _rows(bits)
     assert not _differ(_write(x, SCALES), x, True)
+
+
+def test_zeros_keep_their_quotients_sign():
+    """A zero's code has the sign of its quotient, whichever way its neighbours send it."""
+    bits = _finite()[:4000]
+    bits[::3] = torch.tensor([0x0000, 0x8000], dtype=torch.int32)[torch.arange(1334) % 2]
+    bits = torch.cat([bits, torch.tensor([0x0000, 0x8000] * 64, dtype=torch.int32)])
+    ordinary = bits & 0x7fff
+    bits[2000:4000] = torch.where(ordinary[2000:4000] >= 0x6000, 0x8000, bits[2000:4000])  # no value near the ends
+    x = _rows(bits)
+    assert not _differ(_write(x, SCALES), x, False)
