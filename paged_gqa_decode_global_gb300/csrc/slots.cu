@@ -91,7 +91,8 @@ __device__ __forceinline__ void place(const SlotParams& p, const Round& rd, int 
   if (first < 0) return;
   const int c = rd.cached[r];
   pos = c + t - rd.start[r];
-  const int held = (c + p.page_size - 1) / p.page_size, at = pos / p.page_size;
+  // (unsigned: a length and a page size of nearly 2^31 each are allowed)
+  const int held = ((unsigned)c + (unsigned)p.page_size - 1) / (unsigned)p.page_size, at = pos / p.page_size;
   int32_t* entry = p.block_tables + (size_t)b * p.max_pages + at;
   int page;
   if (at < held) {

@@ -1,0 +1,25 @@
+"""Slot maps at the ends of 31 bits."""
+import pytest
+import torch
+
+from paged_gqa_decode_global_gb300 import binding as b
+
+pytestmark = pytest.mark.gpu
+
+
+def _i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("P,cached", [(2 ** 31 - 1, 5), (2 ** 31 - 1, 2 ** 31 - 4), (2 ** 30 + 1, 2 ** 30 - 2)])
+def test_pages_of_nearly_31_bits(P, cached):
+    """The pages a request holds, where length + page size passes 31 bits: its tokens' page is its own first one."""
+    table, lens, starts = _i32([[0]]), _i32([0]), _i32([0, 0])
+    slots, pos, rng, flags = _i32([-7] * 4), _i32([-7] * 4), _i32([0, 0]), _i32([0])
+    ws = torch.zeros(b.paged_decode_append_slots_workspace(1), dtype=torch.uint8, device="cuda")
+    b.paged_decode_append_slots(P, 1, _i32([cached]), _i32([3]), _i32([0] * 8), _i32([0, 8]), table, lens, starts, slots,
+                                pos, rng, flags, ws)
+    want = [cached, cached + 1, cached + 2, -1]
+    assert int(flags) == 0 and lens.tolist() == [cached + 3]
+    assert slots.tolist() == want and pos.tolist() == want
+    assert rng.tolist() == [0, 8] and table.tolist() == [[0]]
