@@ -42,7 +42,7 @@ constexpr int kThreads = 1024;
 // What a CTA knows of the 1024 requests of one round.
 struct Round {
   int start[kThreads];   // first token (clamped to 31 bits)
-  int first[kThreads];   // first free-list entry, -1 for a request not served
+  int first[kThreads];   // first free-list entry (0 if it needs none), -1 for a request not served
   int cached[kThreads];
 };
 
@@ -168,7 +168,8 @@ __global__ void __launch_bounds__(kThreads) slots_kernel(const SlotParams p) {
       }
       if (fill) {
         rd.start[tid] = (int)min(tok_end - n, 0x7fffffffLL);
-        rd.first[tid] = ok ? (int)(page_end - need) : -1;
+        // (behind requests that found no page the count may pass 31 bits, where only those without need are served)
+        rd.first[tid] = !ok ? -1 : need > 0 ? (int)(page_end - need) : 0;
         rd.cached[tid] = (int)c;
         __syncthreads();
         const int in_round = min(kThreads, p.batch - b0);
