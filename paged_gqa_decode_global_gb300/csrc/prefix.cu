@@ -19,6 +19,12 @@
 // rescaled, and P is written again. The matrix warp, which sees every P before
 // its product, says which, so the softmax warps need no barrier of their
 // own per tile. Each row's references depend on its own scores only.
+// FP8: an operand is a probability times its page's V scale (over the piece's
+// largest), and that product is what has to stay in f16's range, so references
+// and range go by a token's score plus the log2 of its scale: a row whose
+// weight lies on pages of small scales keeps f16's precision there. (With the
+// scores alone, a peak on a page of 10^-6 of the largest scale sat at f16's
+// smallest steps, 3% each, and one of 10^-8 vanished.)
 //
 // One CTA (CT = 1): tiles of 128 tokens, N <= 64 at d = 512 (O^T takes 4 N
 // columns of tensor memory, S^T two buffers of N), 128 below. There the matrix
@@ -50,8 +56,9 @@
 // Roundings: P to the operands' type. bf16 cache: bf16, 2^-9 a probability. FP8
 // cache: f16, into which e4m3 widens exactly; q rounds to f16 once (as in the
 // decode), and P carries the page's V scale over the piece's largest: 2^-12 a
-// probability, 2^-25 absolute below 2^-14. Sums, references and accumulators
-// stay in fp32.
+// probability, and below 2^-14 of the row's largest product of probability and
+// V scale 2^-25 of that (scales below 2^-32 of the piece's largest count as
+// 2^-32 there). Sums, references and accumulators stay in fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -71,6 +78,7 @@ constexpr int kCopyWarps = 3;              // warps 9..11 (12, 16 or 20 warps le
 constexpr int kSoftWarps = 8;
 constexpr float kLow = 3e38f;              // negated reference of a row without a score yet
 constexpr int kNoTop = (int)0x807fffff;    // ordered(-inf)
+constexpr float kLeastScale = -32.f;       // log2: a probability may then exceed 1 by 2^44, and sums hold that
 
 template <int D_, int N_, bool FP8_, int CT_>
 struct PrefixCfg {
@@ -725,6 +733,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       }
       return k;
     };
+    // What a row's reference goes by: the token's score, FP8 with its V scale's log2 (worked out where it is needed:
+    // a register the less).
+    auto weight = [&](const Token& k) { return C::FP8 ? fminf(fmaxf(__log2f(fabsf(k.pv)), kLeastScale), 0.f) : 0.f; };
+    auto level = [&](uint32_t x, const Token& k) -> int {
+      const float s = __uint_as_float(x) * k.sc;
+      return ordered(!k.valid ? -INFINITY : C::FP8 ? s + weight(k) : s);
+    };
     // P: this token's row, in the CTA that holds these query rows; its 16-byte chunks swizzled over the row
     constexpr int kChunkMask = C::P_ROW / 16 - 1, kSwShift = C::QN >= 64 ? 0 : C::QN == 32 ? 1 : 2;
     const int p_tok = rank * kTok + lt;
@@ -801,7 +816,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       ++round;
     };
     // Tile i's P was refused: rows that left their range take the tile's true
-    // maximum over both CTAs' tokens, what they hold is rescaled, P written again.
+    // maximum (of scores, FP8 with the V scales) over both CTAs' tokens, what they hold is rescaled, P written again.
     uint32_t swaps = 0;
     auto again = [&](int i, const Token& k) {
       const uint32_t sa = quarter + C::O_COLS + (i & 1) * N + wg * CW;
@@ -813,7 +828,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
         int mine = kNoTop;
 #pragma unroll
         for (int c = 0; c < LD; ++c) {
-          const int m = __reduce_max_sync(kFullMask, ordered(k.valid ? __uint_as_float(x[c]) * k.sc : -INFINITY));
+          const int m = __reduce_max_sync(kFullMask, level(x[c], k));
           if (lane == c) mine = m;
         }
         if (lane < LD) {
@@ -900,7 +915,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
           int mine = kNoTop;
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            const int m = __reduce_max_sync(kFullMask, ordered(k.valid ? __uint_as_float(x[c]) * k.sc : -INFINITY));
+            const int m = __reduce_max_sync(kFullMask, level(x[c], k));
             if (lane == c) mine = m;
           }
           if (lane < 8) {
@@ -962,7 +977,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       if (i > 0) ok = mbar_wait(p_empty, (i - 1) & 1) && ok;
       __syncwarp();
       store(w);
-      publish(now.valid && over > C::SLACK);
+      publish(now.valid && over > C::SLACK - weight(now));
       before = now;
       now = scaled(after);
     }
