@@ -688,7 +688,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       __syncwarp();
       named_bar_sync(bar, 128);
       v_top = __int_as_float(max(max(top[0], top[1]), max(top[2], top[3])));
-      v_inv = v_top > 0.f ? 1.f / v_top : 0.f;
+      // (a subnormal one's reciprocal would be infinite: the smallest normal number serves below it, and for zero)
+      v_top = fmaxf(v_top, 0x1p-126f);
+      v_inv = 1.f / v_top;
       named_bar_sync(bar, 128);
       if (lt < 4) top[lt] = kNoTop;
       __syncwarp();

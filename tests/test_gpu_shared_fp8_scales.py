@@ -113,3 +113,15 @@ def test_scales_that_fall_along_the_prefix(batch):
     c.kp[pages] = (x / c.ks[pages][:, :, None])[:, :, None].expand(-1, -1, 16, -1).to(torch.float8_e4m3fn).view(
         torch.uint8)
     _check(c)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -120, 2.0 ** -130, 0.0])
+def test_scales_near_the_end_of_fp32(scale):
+    """Subnormal V scales give small finite rows. Flat scores: the rows' common factor, scale over 1200, then keeps
+    2^-10 in fp32's subnormal numbers; the output's step there is 2^-133."""
+    c = Case(16, 4, 512, [0] * 5, [0, 5], [1200], fp8=True, seed=5, q_std=0.0, garbage=False)
+    c.vs.fill_(scale)
+    out, step = c.run()
+    assert step.check() == 0
+    e, tol = _expect(c)
+    assert ((out.double() - e).abs() <= tol + 2.0 ** -10 * e.abs() + 2.0 ** -134).all()
