@@ -677,8 +677,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
     float v_inv = 1.f, v_top = 1.f;  // FP8: the piece's largest V scale
     if constexpr (C::FP8) {
       float m = 0.f;
-      for (int tok = lo + lt * 16; tok < hi; tok += 128 * 16) {
-        const int page = __ldg(table + tok / p.page_size);
+      // (unsigned: the step behind the last token may pass 31 bits)
+      for (unsigned tok = (unsigned)lo + lt * 16; tok < (unsigned)hi; tok += 128 * 16) {
+        const int page = __ldg(table + tok / (unsigned)p.page_size);
         if ((unsigned)page < (unsigned)p.num_pages)
           m = fmaxf(m, fabsf(__ldg(p.v_scale + (size_t)page * p.num_kv_heads + g)));
       }

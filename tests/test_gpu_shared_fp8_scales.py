@@ -125,3 +125,21 @@ def test_scales_near_the_end_of_fp32(scale):
     assert step.check() == 0
     e, tol = _expect(c)
     assert ((out.double() - e).abs() <= tol + 2.0 ** -10 * e.abs() + 2.0 ** -134).all()
+
+
+def test_the_longest_prefix():
+    """2^31 - 256 tokens (every page the same few): the last steps of its loops pass 31 bits. Flat scores over one V
+    code: the code's value. A piece's sums, below 2^24 and multiples of 24 below 2^25, are exact in fp32."""
+    P, pages = 256, 2 ** 23 - 1
+    kp = torch.zeros(4, 1, P, 256, dtype=torch.uint8, device="cuda")
+    vp = torch.full_like(kp, 0x3c)  # 1.5
+    scale = torch.ones(4, 1, device="cuda")
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    q = torch.ones(1, 1, 256, dtype=torch.bfloat16, device="cuda")
+    step = b.SharedPrefixStep(1, 1, 256, P, 4, 1, [0], group_starts=[0, 1], prefix_lens=[pages * P],
+                              max_prefix_pages=pages, kv_dtype=b.PD_KV_FP8_E4M3)
+    tables = (torch.arange(pages, device="cuda") % 4).to(torch.int32).view(1, pages)
+    out = step(q, kp, vp, tables, i32(pages * P), i32(0, 1), i32(-1).view(1, 1), i32(0), 1.0, torch.empty_like(q),
+               k_scale=scale, v_scale=scale)
+    assert step.check() == 0
+    assert (out == 1.5).all()
