@@ -550,6 +550,25 @@ def _want(t, name: str, dtype, shape, device: int) -> None:
         _refuse(name, t, dtype, shape)
 
 
+def _launch_stream(stream, device: int) -> int:
+    """The raw stream of a call whose tensors are all on GPU `device`: it launches on the current device, which has to
+    be that one."""
+    torch = _torch()
+    if device < 0:
+        raise ValueError("every tensor, device_flags and workspace among them, has to be on the call's GPU")
+    current = torch.cuda.current_device()
+    if device != current:
+        raise ValueError(f"the call's tensors are on cuda:{device}, but it would launch on the current device, "
+                         f"cuda:{current}: call it under torch.cuda.device({device})")
+    if stream is None:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the same without a Stream object
+        if raw is not None:
+            return raw(device)
+    elif getattr(stream, "device_index", device) != device:
+        raise ValueError(f"the call's tensors are on cuda:{device}, its stream is cuda:{stream.device_index}'s")
+    return _stream_ptr(stream) or 0
+
+
 def paged_decode_append_slots_workspace(batch: int) -> int:
     """Bytes of the (zeroed) workspace paged_decode_append_slots takes."""
     return int(load_library().paged_decode_append_slots_workspace(int(batch)))
@@ -577,13 +596,14 @@ def paged_decode_append_slots(page_size: int, num_pages: int, cached_lens, new_t
     if positions is not None:
         _want(positions, "positions", i32, (n,), dev)
     _want(free_range_out, "free_range_out", i32, (2,), dev)
-    if dev < 0 or device_flags.get_device() != dev or workspace.get_device() != dev:
+    if device_flags.get_device() != dev or workspace.get_device() != dev:
         raise ValueError("every tensor, device_flags and workspace among them, has to be on the call's GPU")
+    raw = _launch_stream(stream, dev)
     st = load_library().paged_decode_append_slots_args(_SLOTS_ARGS(
         B, page_size, num_pages, width, n, free, cached_lens.data_ptr(), new_tokens.data_ptr(), free_pages.data_ptr(),
         free_range.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), token_starts.data_ptr(),
         slot_map.data_ptr(), _ptr(positions) or 0, free_range_out.data_ptr(), device_flags.data_ptr(),
-        workspace.data_ptr(), workspace.nbytes, _stream_ptr(stream) or 0))
+        workspace.data_ptr(), workspace.nbytes, raw))
     if st != PD_OK:
         raise PagedDecodeError(st, "paged_decode_append_slots")
 
@@ -617,12 +637,13 @@ def _write_slots(fp8: bool, desc, k_in, v_in, slot_map, k_pool, v_pool, k_scale,
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
             if t is not None:
                 _want(t, name, torch.float32, pool[:2], dev)
-    if dev < 0 or device_flags.get_device() != dev:
+    if device_flags.get_device() != dev:
         raise ValueError("every tensor, device_flags among them, has to be on the call's GPU")
+    raw = _launch_stream(stream, dev)
     st = load_library().paged_decode_write_slots_args(_WRITE_ARGS(
         ctypes.addressof(desc), n, fp8, k_in.data_ptr(), _ptr(v_in) or 0, ks, vs, slot_map.data_ptr(),
         k_pool.data_ptr(), _ptr(v_pool) or 0, _ptr(k_scale) or 0, _ptr(v_scale) or 0, device_flags.data_ptr(),
-        _stream_ptr(stream) or 0))
+        raw))
     if st != PD_OK:
         raise PagedDecodeError(st, "paged_decode_write_slots_fp8" if fp8 else "paged_decode_write_slots")
 
@@ -723,7 +744,8 @@ class SharedPrefixStep:
                  stream=None, k_scale=None, v_scale=None):
         self._check_tensors(q, k_pool, v_pool, prefix_tables, prefix_lens, group_starts, block_tables, seq_lens, out,
                             k_scale, v_scale)
-        st = _shared_status(self.fp8, self.plan, k_scale, v_scale, scale, self.workspace, None, stream, q.data_ptr(),
+        raw = _launch_stream(stream, self.workspace.get_device())
+        st = _shared_status(self.fp8, self.plan, k_scale, v_scale, scale, self.workspace, None, raw, q.data_ptr(),
                             k_pool.data_ptr(), 0 if v_pool is None else v_pool.data_ptr(), prefix_tables.data_ptr(),
                             prefix_lens.data_ptr(), group_starts.data_ptr(), block_tables.data_ptr(),
                             seq_lens.data_ptr(), out.data_ptr())

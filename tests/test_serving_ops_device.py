@@ -1,0 +1,119 @@
+"""The slot, cache-write and shared-prefix calls launch on the current device:
+tensors of another one are refused before the library is called (no GPU: stand-ins
+for tensors, the current device and the library)."""
+
+import pytest
+import torch
+
+from paged_gqa_decode_global_gb300 import binding as b
+
+
+class OnGpu:
+    """What the binding asks of a tensor, of one on GPU `device`."""
+
+    def __init__(self, *shape, dtype=torch.int32, device=1):
+        self.shape, self.dtype, self._device = torch.Size(shape), dtype, device
+        self.device = torch.device("cuda", device)
+        n = 1
+        for x in shape:
+            n *= x
+        self.nbytes = n * torch.empty(0, dtype=dtype).element_size()
+
+    def get_device(self):
+        return self._device
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 1 << 20
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self):
+        out, n = [], 1
+        for x in reversed(self.shape):
+            out.append(n)
+            n *= x
+        return tuple(reversed(out))
+
+    def numel(self):
+        return self.nbytes // torch.empty(0, dtype=self.dtype).element_size()
+
+
+class Library:
+    """Counts the calls that reach it."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        return lambda *a: self.calls.append(name) or b.PD_OK
+
+
+BF16, U8 = torch.bfloat16, torch.uint8
+
+
+def _append(at, stream):
+    i = lambda *s: OnGpu(*s, device=at)  # noqa: E731
+    b.paged_decode_append_slots(16, 64, i(4), i(4), i(9), i(2), i(4, 8), i(4), i(5), i(32), i(32), i(2), i(1),
+                                OnGpu(256, dtype=U8, device=at), stream)
+
+
+def _write(at, stream):
+    desc = b.layer_desc(16, 4, 512, 16, 4, 8)
+    k, pool = OnGpu(3, 4, 512, dtype=BF16, device=at), OnGpu(4, 4, 16, 512, dtype=BF16, device=at)
+    b.paged_decode_write_slots(desc, k, k, OnGpu(3, device=at), pool, pool, OnGpu(1, device=at), stream)
+
+
+def _write_fp8(at, stream):
+    desc = b.layer_desc(16, 4, 512, 16, 4, 8, 0, True, b.PD_KV_FP8_E4M3)
+    pool, scale = OnGpu(4, 4, 16, 512, dtype=U8, device=at), OnGpu(4, 4, dtype=torch.float32, device=at)
+    b.paged_decode_write_slots_fp8(desc, OnGpu(3, 4, 512, dtype=BF16, device=at), None, OnGpu(3, device=at), pool, None,
+                                   scale, None, OnGpu(1, device=at), stream)
+
+
+def _shared(at, stream):
+    step = object.__new__(b.SharedPrefixStep)
+    step.fp8, step.query_tokens, step.plan = False, 1, b.SharedPlan()
+    step.workspace = OnGpu(4096, dtype=U8, device=at)
+    step._q_shapes, step._pool, step._prefix, step._tables = ((2, 16, 512), (2, 1, 16, 512)), (4, 4, 16, 512), (1, 3), (2, 8)
+    q, pool = OnGpu(2, 16, 512, dtype=BF16, device=at), OnGpu(4, 4, 16, 512, dtype=BF16, device=at)
+    i = lambda *s: OnGpu(*s, device=at)  # noqa: E731
+    step(q, pool, pool, i(1, 3), i(1), i(2), i(2, 8), i(2), 0.05, q, stream)
+
+
+CALLS = [_append, _write, _write_fp8, _shared]
+
+
+@pytest.fixture()
+def library(monkeypatch):
+    lib = Library()
+    monkeypatch.setattr(b, "load_library", lambda *a: lib)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0, raising=False)
+    return lib
+
+
+@pytest.mark.parametrize("call", CALLS)
+@pytest.mark.parametrize("stream", [None, 0, 1 << 12])
+def test_tensors_of_another_device_than_the_current_one_are_refused(library, call, stream):
+    with pytest.raises(ValueError, match="cuda:1"):
+        call(1, stream)
+    assert not library.calls
+    call(0, stream)
+    assert len(library.calls) == 1
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_a_stream_of_another_device_is_refused(library, call):
+    class Stream:
+        cuda_stream, device_index = 1 << 12, 1
+
+    with pytest.raises(ValueError, match="cuda:1"):
+        call(0, Stream())
+    assert not library.calls
+    Stream.device_index = 0
+    call(0, Stream())
+    assert len(library.calls) == 1
