@@ -550,6 +550,14 @@ def _want(t, name: str, dtype, shape, device: int) -> None:
         _refuse(name, t, dtype, shape)
 
 
+def _want_bytes(t, name: str, nbytes: int, device: int) -> None:
+    """At least nbytes of contiguous memory of any type on the call's device: what the kernel writes there."""
+    if t.nbytes < nbytes or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{name}: expected a contiguous tensor of at least {nbytes} bytes on the GPU of the call's other "
+                         f"tensors, got {t.dtype} {tuple(t.shape)}{'' if t.is_contiguous() else ' (not contiguous)'} on "
+                         f"{t.device}")
+
+
 def _launch_stream(stream, device: int) -> int:
     """The raw stream of a call whose tensors are all on GPU `device`: it launches on the current device, which has to
     be that one."""
@@ -596,8 +604,8 @@ def paged_decode_append_slots(page_size: int, num_pages: int, cached_lens, new_t
     if positions is not None:
         _want(positions, "positions", i32, (n,), dev)
     _want(free_range_out, "free_range_out", i32, (2,), dev)
-    if device_flags.get_device() != dev or workspace.get_device() != dev:
-        raise ValueError("every tensor, device_flags and workspace among them, has to be on the call's GPU")
+    _want_bytes(device_flags, "device_flags", 4, dev)
+    _want_bytes(workspace, "workspace", 0, dev)
     raw = _launch_stream(stream, dev)
     st = load_library().paged_decode_append_slots_args(_SLOTS_ARGS(
         B, page_size, num_pages, width, n, free, cached_lens.data_ptr(), new_tokens.data_ptr(), free_pages.data_ptr(),
@@ -637,8 +645,7 @@ def _write_slots(fp8: bool, desc, k_in, v_in, slot_map, k_pool, v_pool, k_scale,
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
             if t is not None:
                 _want(t, name, torch.float32, pool[:2], dev)
-    if device_flags.get_device() != dev:
-        raise ValueError("every tensor, device_flags among them, has to be on the call's GPU")
+    _want_bytes(device_flags, "device_flags", 4, dev)
     raw = _launch_stream(stream, dev)
     st = load_library().paged_decode_write_slots_args(_WRITE_ARGS(
         ctypes.addressof(desc), n, fp8, k_in.data_ptr(), _ptr(v_in) or 0, ks, vs, slot_map.data_ptr(),

@@ -11,8 +11,8 @@ from paged_gqa_decode_global_gb300 import binding as b
 class OnGpu:
     """What the binding asks of a tensor, of one on GPU `device`."""
 
-    def __init__(self, *shape, dtype=torch.int32, device=1):
-        self.shape, self.dtype, self._device = torch.Size(shape), dtype, device
+    def __init__(self, *shape, dtype=torch.int32, device=1, contiguous=True):
+        self.shape, self.dtype, self._device, self._contiguous = torch.Size(shape), dtype, device, contiguous
         self.device = torch.device("cuda", device)
         n = 1
         for x in shape:
@@ -23,7 +23,7 @@ class OnGpu:
         return self._device
 
     def is_contiguous(self):
-        return True
+        return self._contiguous
 
     def data_ptr(self):
         return 1 << 20
@@ -55,16 +55,18 @@ class Library:
 BF16, U8 = torch.bfloat16, torch.uint8
 
 
-def _append(at, stream):
+def _append(at, stream, flags=None, workspace=None):
     i = lambda *s: OnGpu(*s, device=at)  # noqa: E731
-    b.paged_decode_append_slots(16, 64, i(4), i(4), i(9), i(2), i(4, 8), i(4), i(5), i(32), i(32), i(2), i(1),
-                                OnGpu(256, dtype=U8, device=at), stream)
+    b.paged_decode_append_slots(16, 64, i(4), i(4), i(9), i(2), i(4, 8), i(4), i(5), i(32), i(32), i(2),
+                                i(1) if flags is None else flags,
+                                OnGpu(256, dtype=U8, device=at) if workspace is None else workspace, stream)
 
 
-def _write(at, stream):
+def _write(at, stream, flags=None):
     desc = b.layer_desc(16, 4, 512, 16, 4, 8)
     k, pool = OnGpu(3, 4, 512, dtype=BF16, device=at), OnGpu(4, 4, 16, 512, dtype=BF16, device=at)
-    b.paged_decode_write_slots(desc, k, k, OnGpu(3, device=at), pool, pool, OnGpu(1, device=at), stream)
+    b.paged_decode_write_slots(desc, k, k, OnGpu(3, device=at), pool, pool,
+                               OnGpu(1, device=at) if flags is None else flags, stream)
 
 
 def _write_fp8(at, stream):
@@ -117,3 +119,22 @@ def test_a_stream_of_another_device_is_refused(library, call):
     Stream.device_index = 0
     call(0, Stream())
     assert len(library.calls) == 1
+
+
+@pytest.mark.parametrize("call", [_append, _write])
+@pytest.mark.parametrize("flags", [OnGpu(1, dtype=U8, device=0), OnGpu(0, device=0), OnGpu(3, dtype=U8, device=0),
+                                   OnGpu(4, dtype=U8, device=0, contiguous=False), OnGpu(1, device=1)])
+def test_flags_that_hold_no_word_are_refused(library, call, flags):
+    with pytest.raises(ValueError, match="device_flags"):
+        call(0, 0, flags=flags)
+    assert not library.calls
+    for good in (OnGpu(1, device=0), OnGpu(1, dtype=torch.uint32, device=0), OnGpu(16, dtype=U8, device=0)):
+        call(0, 0, flags=good)
+    assert len(library.calls) == 3
+
+
+@pytest.mark.parametrize("workspace", [OnGpu(256, dtype=U8, device=0, contiguous=False), OnGpu(256, dtype=U8, device=1)])
+def test_workspaces_that_are_not_one_piece_of_the_calls_gpu_are_refused(library, workspace):
+    with pytest.raises(ValueError, match="workspace"):
+        _append(0, 0, workspace=workspace)
+    assert not library.calls
