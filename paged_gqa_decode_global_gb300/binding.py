@@ -550,12 +550,15 @@ def _want(t, name: str, dtype, shape, device: int) -> None:
         _refuse(name, t, dtype, shape)
 
 
-def _want_bytes(t, name: str, nbytes: int, device: int) -> None:
-    """At least nbytes of contiguous memory of any type on the call's device: what the kernel writes there."""
-    if t.nbytes < nbytes or not t.is_contiguous() or t.get_device() != device:
-        raise ValueError(f"{name}: expected a contiguous tensor of at least {nbytes} bytes on the GPU of the call's other "
-                         f"tensors, got {t.dtype} {tuple(t.shape)}{'' if t.is_contiguous() else ' (not contiguous)'} on "
-                         f"{t.device}")
+def _refuse_bytes(name: str, t, nbytes: int) -> None:
+    raise ValueError(f"{name}: expected a contiguous tensor of at least {nbytes} bytes on the GPU of the call's other "
+                     f"tensors, got {t.dtype} {tuple(t.shape)}{'' if t.is_contiguous() else ' (not contiguous)'} on "
+                     f"{t.device}")
+
+
+def _is_word(t, device: int) -> bool:
+    """Whether a flag word fits a tensor, of any type, on the call's device."""
+    return t.nbytes >= 4 and t.is_contiguous() and t.get_device() == device
 
 
 def _launch_stream(stream, device: int) -> int:
@@ -604,8 +607,10 @@ def paged_decode_append_slots(page_size: int, num_pages: int, cached_lens, new_t
     if positions is not None:
         _want(positions, "positions", i32, (n,), dev)
     _want(free_range_out, "free_range_out", i32, (2,), dev)
-    _want_bytes(device_flags, "device_flags", 4, dev)
-    _want_bytes(workspace, "workspace", 0, dev)
+    if not _is_word(device_flags, dev):
+        _refuse_bytes("device_flags", device_flags, 4)
+    if not workspace.is_contiguous() or workspace.get_device() != dev:
+        _refuse_bytes("workspace", workspace, 4)
     raw = _launch_stream(stream, dev)
     st = load_library().paged_decode_append_slots_args(_SLOTS_ARGS(
         B, page_size, num_pages, width, n, free, cached_lens.data_ptr(), new_tokens.data_ptr(), free_pages.data_ptr(),
@@ -645,7 +650,8 @@ def _write_slots(fp8: bool, desc, k_in, v_in, slot_map, k_pool, v_pool, k_scale,
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
             if t is not None:
                 _want(t, name, torch.float32, pool[:2], dev)
-    _want_bytes(device_flags, "device_flags", 4, dev)
+    if not _is_word(device_flags, dev):
+        _refuse_bytes("device_flags", device_flags, 4)
     raw = _launch_stream(stream, dev)
     st = load_library().paged_decode_write_slots_args(_WRITE_ARGS(
         ctypes.addressof(desc), n, fp8, k_in.data_ptr(), _ptr(v_in) or 0, ks, vs, slot_map.data_ptr(),
@@ -686,6 +692,59 @@ def paged_decode_plan_shared(desc: LayerDesc, query_tokens: int, seq_lens_host: 
     return plan
 
 
+class _SharedShapes:
+    """What the tensors of a shared-prefix decode have to look like, by its plan."""
+
+    def __init__(self, plan: SharedPlan):
+        ly, B, T = plan.own.layer, plan.own.batch, plan.own.query_tokens
+        self.fp8 = ly.kv_dtype == PD_KV_FP8_E4M3
+        self.q = (B, T, ly.num_q_heads, ly.head_dim)
+        self.q_one = (B, ly.num_q_heads, ly.head_dim) if T == 1 else self.q
+        self.pool = (ly.num_pages, ly.num_kv_heads, ly.page_size, ly.head_dim)
+        self.prefix = (plan.num_groups, plan.max_prefix_pages)
+        self.tables = (B, ly.max_pages_per_seq)
+
+    def check(self, want, device, q, k_pool, v_pool, k_scale, v_scale, prefix_tables, prefix_lens, group_starts,
+              block_tables, seq_lens, out) -> None:
+        torch = _torch()
+        i32, bf16 = torch.int32, torch.bfloat16
+        pool_type = torch.uint8 if self.fp8 else bf16
+        shape = self.q if len(getattr(q, "shape", ())) == 4 else self.q_one
+        want(q, "q", bf16, shape, device)
+        want(out, "out", bf16, shape, device)
+        want(k_pool, "k_pool", pool_type, self.pool, device)
+        if v_pool is not None:
+            want(v_pool, "v_pool", pool_type, self.pool, device)
+        if self.fp8:
+            for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+                if t is not None:
+                    want(t, name, torch.float32, self.pool[:2], device)
+        want(prefix_tables, "prefix_tables", i32, self.prefix, device)
+        want(prefix_lens, "prefix_lens", i32, self.prefix[:1], device)
+        want(group_starts, "group_starts", i32, (self.prefix[0] + 1,), device)
+        want(block_tables, "block_tables", i32, self.tables, device)
+        want(seq_lens, "seq_lens", i32, self.tables[:1], device)
+
+
+def _want_or_address(t, name: str, dtype, shape, device: int) -> None:
+    """As _want; a raw address is the caller's word, and the library refuses what is missing."""
+    if t is not None and not isinstance(t, int):
+        _want(t, name, dtype, shape, device)
+
+
+def _global_shared(fp8: bool, plan, q, k_pool, v_pool, k_scale, v_scale, prefix_tables, prefix_lens, group_starts,
+                   block_tables, seq_lens, scale, workspace, out, stream, workspace_bytes) -> None:
+    dev, nbytes = workspace.get_device(), workspace.nbytes if workspace_bytes is None else int(workspace_bytes)
+    if workspace.nbytes < nbytes or not workspace.is_contiguous():
+        _refuse_bytes("workspace", workspace, nbytes)
+    _SharedShapes(plan).check(_want_or_address, dev, q, k_pool, v_pool, k_scale, v_scale, prefix_tables, prefix_lens,
+                              group_starts, block_tables, seq_lens, out)
+    st = _shared_status(fp8, plan, k_scale, v_scale, scale, workspace, nbytes, _launch_stream(stream, dev),
+                        *(_ptr(t) or 0 for t in (q, k_pool, v_pool, prefix_tables, prefix_lens, group_starts,
+                                                 block_tables, seq_lens, out)))
+    _check(st, "paged_decode_global_shared_fp8" if fp8 else "paged_decode_global_shared")
+
+
 def _shared_status(fp8: bool, plan, k_scale, v_scale, scale, workspace, workspace_bytes, stream, q, k_pool, v_pool,
                    *rest) -> int:
     """The call on addresses (rest: the prefix tables' to the lengths', then out's); 0 for what is not there."""
@@ -699,21 +758,18 @@ def _shared_status(fp8: bool, plan, k_scale, v_scale, scale, workspace, workspac
 def paged_decode_global_shared(plan: SharedPlan, q, k_pool, v_pool, prefix_tables, prefix_lens, group_starts,
                                block_tables, seq_lens, scale: float, workspace, out, stream=None,
                                workspace_bytes: Optional[int] = None) -> None:
-    """Decode of a batch whose groups share prefixes, merge included."""
-    st = _shared_status(False, plan, None, None, scale, workspace, workspace_bytes, stream,
-                        *(_ptr(t) or 0 for t in (q, k_pool, v_pool, prefix_tables, prefix_lens, group_starts,
-                                                 block_tables, seq_lens, out)))
-    _check(st, "paged_decode_global_shared")
+    """Decode of a batch whose groups share prefixes, merge included. Tensors are checked against the plan; addresses
+    (int) are taken as they are."""
+    _global_shared(False, plan, q, k_pool, v_pool, None, None, prefix_tables, prefix_lens, group_starts, block_tables,
+                   seq_lens, scale, workspace, out, stream, workspace_bytes)
 
 
 def paged_decode_global_shared_fp8(plan: SharedPlan, q, k_pool, v_pool, k_scale, v_scale, prefix_tables, prefix_lens,
                                    group_starts, block_tables, seq_lens, scale: float, workspace, out, stream=None,
                                    workspace_bytes: Optional[int] = None) -> None:
     """The same over an e4m3 cache with per-(page, KV head) scales."""
-    st = _shared_status(True, plan, k_scale, v_scale, scale, workspace, workspace_bytes, stream,
-                        *(_ptr(t) or 0 for t in (q, k_pool, v_pool, prefix_tables, prefix_lens, group_starts,
-                                                 block_tables, seq_lens, out)))
-    _check(st, "paged_decode_global_shared_fp8")
+    _global_shared(True, plan, q, k_pool, v_pool, k_scale, v_scale, prefix_tables, prefix_lens, group_starts,
+                   block_tables, seq_lens, scale, workspace, out, stream, workspace_bytes)
 
 
 class SharedPrefixStep:
@@ -739,19 +795,14 @@ class SharedPrefixStep:
         # zeroed once: the first word is the device error flag
         nbytes = int(self.plan.workspace_bytes)
         self.workspace = torch.zeros((nbytes + 255) // 256 * 256, dtype=torch.uint8, device=device)
-        # what each call's tensors have to look like
-        B, heads = self.plan.own.batch, (num_q_heads, head_dim)
-        T = self.query_tokens
-        self._q_shapes = ((B,) + heads if T == 1 else None, (B, T) + heads)
-        self._pool = (num_pages, num_kv_heads, page_size, head_dim)
-        self._prefix = (self.plan.num_groups, max_prefix_pages)
-        self._tables = (B, max_pages_per_seq)
+        self._shapes = _SharedShapes(self.plan)
 
     def __call__(self, q, k_pool, v_pool, prefix_tables, prefix_lens, group_starts, block_tables, seq_lens, scale, out,
                  stream=None, k_scale=None, v_scale=None):
-        self._check_tensors(q, k_pool, v_pool, prefix_tables, prefix_lens, group_starts, block_tables, seq_lens, out,
-                            k_scale, v_scale)
-        raw = _launch_stream(stream, self.workspace.get_device())
+        dev = self.workspace.get_device()
+        self._shapes.check(_want, dev, q, k_pool, v_pool, k_scale, v_scale, prefix_tables, prefix_lens, group_starts,
+                           block_tables, seq_lens, out)
+        raw = _launch_stream(stream, dev)
         st = _shared_status(self.fp8, self.plan, k_scale, v_scale, scale, self.workspace, None, raw, q.data_ptr(),
                             k_pool.data_ptr(), 0 if v_pool is None else v_pool.data_ptr(), prefix_tables.data_ptr(),
                             prefix_lens.data_ptr(), group_starts.data_ptr(), block_tables.data_ptr(),
@@ -759,27 +810,6 @@ class SharedPrefixStep:
         if st != PD_OK:
             raise PagedDecodeError(st, "paged_decode_global_shared_fp8" if self.fp8 else "paged_decode_global_shared")
         return out
-
-    def _check_tensors(self, q, k_pool, v_pool, prefix_tables, prefix_lens, group_starts, block_tables, seq_lens, out,
-                       k_scale, v_scale):
-        torch = _torch()
-        i32, bf16, dev = torch.int32, torch.bfloat16, self.workspace.get_device()
-        pool_type = torch.uint8 if self.fp8 else bf16
-        shape = self._q_shapes[0] if q.dim() == 3 else self._q_shapes[1]
-        _want(q, "q", bf16, shape, dev)
-        _want(out, "out", bf16, shape, dev)
-        _want(k_pool, "k_pool", pool_type, self._pool, dev)
-        if v_pool is not None:
-            _want(v_pool, "v_pool", pool_type, self._pool, dev)
-        if self.fp8:
-            for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-                if t is not None:
-                    _want(t, name, torch.float32, self._pool[:2], dev)
-        _want(prefix_tables, "prefix_tables", i32, self._prefix, dev)
-        _want(prefix_lens, "prefix_lens", i32, self._prefix[:1], dev)
-        _want(group_starts, "group_starts", i32, (self._prefix[0] + 1,), dev)
-        _want(block_tables, "block_tables", i32, self._tables, dev)
-        _want(seq_lens, "seq_lens", i32, self._tables[:1], dev)
 
     def check(self, stream=None) -> int:
         return paged_decode_check_device_error(self.plan.own, self.workspace, stream)

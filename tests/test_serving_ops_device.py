@@ -76,17 +76,40 @@ def _write_fp8(at, stream):
                                    scale, None, OnGpu(1, device=at), stream)
 
 
-def _shared(at, stream):
-    step = object.__new__(b.SharedPrefixStep)
-    step.fp8, step.query_tokens, step.plan = False, 1, b.SharedPlan()
-    step.workspace = OnGpu(4096, dtype=U8, device=at)
-    step._q_shapes, step._pool, step._prefix, step._tables = ((2, 16, 512), (2, 1, 16, 512)), (4, 4, 16, 512), (1, 3), (2, 8)
-    q, pool = OnGpu(2, 16, 512, dtype=BF16, device=at), OnGpu(4, 4, 16, 512, dtype=BF16, device=at)
+def _shared_plan(fp8=False):
+    plan = b.SharedPlan()
+    plan.own.layer = b.layer_desc(16, 4, 512, 16, 4, 8, 0, False, b.PD_KV_FP8_E4M3 if fp8 else b.PD_KV_BF16)
+    plan.own.batch, plan.own.query_tokens, plan.num_groups, plan.max_prefix_pages = 2, 1, 1, 3
+    return plan
+
+
+def _shared_tensors(at, fp8=False):
     i = lambda *s: OnGpu(*s, device=at)  # noqa: E731
-    step(q, pool, pool, i(1, 3), i(1), i(2), i(2, 8), i(2), 0.05, q, stream)
+    pool = OnGpu(4, 4, 16, 512, dtype=U8 if fp8 else BF16, device=at)
+    t = dict(q=OnGpu(2, 16, 512, dtype=BF16, device=at), k_pool=pool, v_pool=pool)
+    if fp8:
+        t["k_scale"] = t["v_scale"] = OnGpu(4, 4, dtype=torch.float32, device=at)
+    return dict(t, prefix_tables=i(1, 3), prefix_lens=i(1), group_starts=i(2), block_tables=i(2, 8), seq_lens=i(2),
+                workspace=OnGpu(4096, dtype=U8, device=at), out=OnGpu(2, 16, 512, dtype=BF16, device=at))
 
 
-CALLS = [_append, _write, _write_fp8, _shared]
+def _shared(at, stream):
+    step, t = object.__new__(b.SharedPrefixStep), _shared_tensors(at)
+    step.fp8, step.query_tokens, step.plan, step.workspace = False, 1, _shared_plan(), t.pop("workspace")
+    step._shapes = b._SharedShapes(step.plan)
+    step(scale=0.05, stream=stream, **t)
+
+
+def _shared_call(at, stream, fp8=False, **kw):
+    call = b.paged_decode_global_shared_fp8 if fp8 else b.paged_decode_global_shared
+    call(_shared_plan(fp8), scale=0.05, stream=stream, **dict(_shared_tensors(at, fp8), **kw))
+
+
+def _shared_call_fp8(at, stream):
+    _shared_call(at, stream, True)
+
+
+CALLS = [_append, _write, _write_fp8, _shared, _shared_call, _shared_call_fp8]
 
 
 @pytest.fixture()
@@ -138,3 +161,35 @@ def test_workspaces_that_are_not_one_piece_of_the_calls_gpu_are_refused(library,
     with pytest.raises(ValueError, match="workspace"):
         _append(0, 0, workspace=workspace)
     assert not library.calls
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("name,bad", [
+    ("q", OnGpu(2, 16, 256, dtype=BF16, device=0)), ("q", OnGpu(2, 16, 512, dtype=torch.float16, device=0)),
+    ("q", OnGpu(3, 16, 512, dtype=BF16, device=0)), ("out", OnGpu(1, 16, 512, dtype=BF16, device=0)),
+    ("out", OnGpu(2, 16, 512, dtype=torch.float32, device=0)),
+    ("out", OnGpu(2, 16, 512, dtype=BF16, device=0, contiguous=False)),
+    ("k_pool", OnGpu(3, 4, 16, 512, dtype=BF16, device=0)), ("k_pool", OnGpu(3, 4, 16, 512, dtype=U8, device=0)),
+    ("v_pool", OnGpu(4, 4, 16, 512, dtype=torch.float32, device=0)),
+    ("prefix_tables", OnGpu(1, 2, device=0)), ("prefix_tables", OnGpu(1, 3, dtype=torch.int64, device=0)),
+    ("prefix_lens", OnGpu(2, device=0)), ("group_starts", OnGpu(1, device=0)), ("block_tables", OnGpu(2, 4, device=0)),
+    ("seq_lens", OnGpu(1, device=0)), ("seq_lens", OnGpu(2, device=1)), ("workspace", OnGpu(64, dtype=U8, device=0)),
+    ("k_scale", OnGpu(4, 3, dtype=torch.float32, device=0)), ("v_scale", OnGpu(4, 4, dtype=BF16, device=0))])
+def test_shared_calls_check_their_tensors(library, fp8, name, bad):
+    if name.endswith("_scale") and not fp8:
+        return
+    with pytest.raises(ValueError, match=name):
+        _shared_call(0, 0, fp8, **{name: bad}, workspace_bytes=4096)
+    assert not library.calls
+    _shared_call(0, 0, fp8, workspace_bytes=4096)
+    assert len(library.calls) == 1
+
+
+def test_shared_calls_take_addresses_and_leave_missing_tensors_to_the_library(library):
+    t = {n: 1 << 20 for n in _shared_tensors(0) if n != "workspace"}
+    _shared_call(0, 0, **t)
+    _shared_call(0, 0, v_pool=None)
+    assert len(library.calls) == 2
+    t["q"] = None
+    _shared_call(0, 0, **t)
+    assert len(library.calls) == 3
