@@ -628,7 +628,7 @@ def _token_rows(t, name: str, dtype, shape, device: int) -> int:
     if t.dtype is not dtype or t.shape != shape or t.get_device() != device or one != 1 or (heads > 1 and head != d):
         raise ValueError(f"{name}: expected {dtype} {shape} with each token's heads contiguous, got {t.dtype} "
                          f"{tuple(t.shape)}, strides {t.stride()} on {t.device}")
-    return token if n > 1 else max(token, heads * d)
+    return token if n > 1 else heads * d  # (one token's stride may be anything)
 
 
 def _write_slots(fp8: bool, desc, k_in, v_in, slot_map, k_pool, v_pool, k_scale, v_scale, device_flags, stream):

@@ -2,6 +2,8 @@
 tensors of another one are refused before the library is called (no GPU: stand-ins
 for tensors, the current device and the library)."""
 
+import struct
+
 import pytest
 import torch
 
@@ -11,9 +13,9 @@ from paged_gqa_decode_global_gb300 import binding as b
 class OnGpu:
     """What the binding asks of a tensor, of one on GPU `device`."""
 
-    def __init__(self, *shape, dtype=torch.int32, device=1, contiguous=True):
+    def __init__(self, *shape, dtype=torch.int32, device=1, contiguous=True, token_stride=None):
         self.shape, self.dtype, self._device, self._contiguous = torch.Size(shape), dtype, device, contiguous
-        self.device = torch.device("cuda", device)
+        self.device, self._token_stride = torch.device("cuda", device), token_stride
         n = 1
         for x in shape:
             n *= x
@@ -36,6 +38,8 @@ class OnGpu:
         for x in reversed(self.shape):
             out.append(n)
             n *= x
+        if self._token_stride is not None:
+            out[-1] = self._token_stride
         return tuple(reversed(out))
 
     def numel(self):
@@ -49,7 +53,7 @@ class Library:
         self.calls = []
 
     def __getattr__(self, name):
-        return lambda *a: self.calls.append(name) or b.PD_OK
+        return lambda *a: self.calls.append((name,) + a) or b.PD_OK
 
 
 BF16, U8 = torch.bfloat16, torch.uint8
@@ -193,3 +197,19 @@ def test_shared_calls_take_addresses_and_leave_missing_tensors_to_the_library(li
     t["q"] = None
     _shared_call(0, 0, **t)
     assert len(library.calls) == 3
+
+
+def test_one_tokens_stride_may_be_anything(library):
+    """A row of a tensor whose rows are no multiple of 8 elements apart is a whole row; two of them are not aligned."""
+    desc, pool = b.layer_desc(16, 4, 512, 16, 4, 8), OnGpu(4, 4, 16, 512, dtype=BF16, device=0)
+    strides = struct.Struct("P2i2P2q7P")
+
+    def call(n, stride):
+        k = OnGpu(n, 4, 512, dtype=BF16, device=0, token_stride=stride)
+        b.paged_decode_write_slots(desc, k, k, OnGpu(n, device=0), pool, pool, OnGpu(1, device=0), 0)
+        return strides.unpack(library.calls[-1][1])[5:7]
+
+    for stride in (2052, 1, 0, 1 << 40):
+        assert call(1, stride) == (2048, 2048)
+    assert call(2, 2056) == (2056, 2056)
+    assert call(2, 2052) == (2052, 2052)  # the library's to refuse
