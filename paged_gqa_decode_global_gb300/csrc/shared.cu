@@ -154,7 +154,8 @@ bool shared_plan_is_valid(const pd_shared_plan* plan) {
   const pd_plan& own = plan->own;
   if (!plan_is_valid(&own) || own.partial != 2) return false;
   if (plan->num_groups < 0 || plan->max_prefix_pages < 1 || plan->tiles < 0 || plan->tiles > 65535) return false;
-  if (own.batch > 0 && plan->num_groups < 1) return false;
+  // (the own part is ordered behind the prefix pass: without row tiles there would be none to wait for)
+  if (own.batch > 0 && (plan->num_groups < 1 || plan->tiles < 1)) return false;
   if (plan->variant < 0 || plan->variant >= kNumPrefixInstances) return false;
   const PrefixInstance& v = kPrefixInstances[plan->variant];
   if (v.head_dim != own.layer.head_dim || v.row_tile != plan->row_tile ||
@@ -406,8 +407,8 @@ pd_status decode_shared(const pd_shared_plan* plan, bool fp8, const void* q, con
   if (st == PD_OK) st = encode_group_map(&p.vmap, ly.kv_shared ? k_pool : v_pool, ly, p.v_box, slabs);
   if (st != PD_OK) return st;
   void* args[] = {&p};
-  if (plan->tiles > 0 && launch_dependent(fn, dim3(plan->tiles * v.ctas, plan->num_pieces, ly.num_kv_heads), v.threads,
-                                          v.smem_bytes, stream, args, v.ctas) != cudaSuccess)
+  if (launch_dependent(fn, dim3(plan->tiles * v.ctas, plan->num_pieces, ly.num_kv_heads), v.threads, v.smem_bytes,
+                       stream, args, v.ctas) != cudaSuccess)
     return PD_ERR_CUDA;
   // the own part's CTAs take the SMs that the prefix pass leaves free
   st = launch_own_part(&own, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens, scale, workspace,
