@@ -442,9 +442,13 @@ pd_status paged_decode_qkv_norm_rope_write(const pd_layer_desc* layer, int32_t b
  * its pages and gets new_tokens[b] more (one in a decode step, a chunk of a
  * prompt, none). This call hands out the pages the new tokens need, in request
  * order from a list of free page ids, extends the block tables, and writes for
- * every new token its position (the RoPE angle's) and its slot, the row
+ * every new token its position among its request's tokens and its slot, the row
  * page * page_size + position % page_size of the pool that the cache write
- * takes. With old_b = ceil(cached_b / P) and need_b = ceil((cached_b + new_b) / P)
+ * takes. The position is the RoPE angle's where cached_lens count all of a
+ * request's tokens. Under a shared prefix they count its own tokens only
+ * (paged_decode_global_shared wants them so): add the prefix's length to the
+ * positions before rotating. paged_decode_qkv_norm_rope_write, which rotates by
+ * seq_lens - 1, knows no prefix and does not serve such requests. With old_b = ceil(cached_b / P) and need_b = ceil((cached_b + new_b) / P)
  * - old_b, page k of request b's new ones is
  *   free_pages[free_range[0] + sum_{i < b} need_i + k].
  */
@@ -548,6 +552,16 @@ pd_status paged_decode_write_slots_fp8(const pd_layer_desc* layer, int32_t num_t
  * prefix byte read once for the group instead of once a request), the own part
  * as decode, and their merge by log-sum-exp. With T query tokens they are the
  * last T own tokens, causal among themselves.
+ *
+ * Ranges: over a bf16 cache the prefix part holds sums of probabilities of up to
+ * 2^60 (a row's reference is not its running maximum) times V in fp32, so V's
+ * magnitudes belong below 2^60. Over an e4m3 cache a probability times its
+ * page's V scale is rounded to f16: in the prefix part relative to the row's
+ * largest such product in its piece, whatever the scales (below 2^-32 of the
+ * piece's largest they count as that), in the own part, as in decode, as it is,
+ * with f16's smallest step of 2^-24. There a score more than 2^12 above its
+ * row's reference has a tile of the prefix done twice: results are the same,
+ * batches of peaked rows take longer.
  */
 typedef struct {
   pd_plan own;              /* the own tokens' part (launched with fewer threads and less shared memory than it names) */

@@ -47,11 +47,15 @@
 //
 // What bounds it, at head_dim 512 (one GB300, the whole call over the tiles of
 // its longest CTA): a pair's tile of 256 tokens takes 3.4 us with few pairs and
-// 3.9 with 64, 2.15 us of it the products and most of the rest the copies'
-// latency over a ring of half a tile's bytes (128 of 224 KB: the query rows take
-// 64, P 32); one CTA's tile of 128 tokens 2.8 us with 64 rows, 2.3 with 16, and
+// 3.9 with 64, 2.15 us of it the products and most of the rest, by elimination,
+// the copies' latency over a ring of half a tile's bytes (128 of 224 KB: the query
+// rows take 64, P 32; L2's slices deliver 24% of their peak over a launch of 64
+// requests and 16384 tokens); one CTA's tile of 128 tokens 2.8 us with 64 rows, 2.3 with 16, and
 // 4 with 116 CTAs, which together take 6.1 TB/s; FP8 5.6 us (pair), 3.8 (64
-// rows), 3.25 (16): the widening's passes through shared memory.
+// rows), 3.25 (16): the widening's passes through shared memory. What a refused
+// tile costs shows with e4m3's range: 32 requests over 32768 tokens 71 us with
+// scores of deviation 1.5 (nats), 130 with 3, 183 with 4, 181 with 12 (16
+// requests 52, 65, 87, 93; bf16, 32 requests: 71, 73, 73, 87).
 //
 // Roundings: P to the operands' type. bf16 cache: bf16, 2^-9 a probability. FP8
 // cache: f16, into which e4m3 widens exactly; q rounds to f16 once (as in the

@@ -178,8 +178,10 @@ bool shared_plan_is_valid(const pd_shared_plan* plan) {
 
 // What the cost model takes of the prefix pass, in microseconds on a 152-SM
 // GB300: a CTA's start and end, and a tile (128 tokens; a pair's 256), measured
-// at head_dim 512 and in proportion to head_dim below; the tiles in flight share
-// the memory's rate, and the pieces' partial results are written and read once.
+// at head_dim 512 (one figure for 16 to 64 rows, which take 2.3 to 2.8 in bf16
+// and 3.25 to 3.8 in e4m3) and taken in proportion to head_dim below, where it
+// was not measured; the tiles in flight share the memory's rate, and the pieces'
+// partial results are written and read once.
 constexpr double kFixedUs = 7.0, kHbmBytesPerUs = 6.8e6, kPartialBytesPerUs = 5.0e6;
 constexpr double kOwnFixedUs = 5.0;  // a stage-1 CTA of the own part
 

@@ -28,7 +28,7 @@ struct SharedParams {
   int32_t page_size, num_pages, max_prefix_pages;
   int32_t row_tile, tiles, num_pieces, chunk_tokens;
   int32_t k_box, v_box;  // tokens of one copy of K and of V (both divide page_size)
-  int32_t keep_in_l2;   // the prefix rows are read more than once (several row tiles, K=V)
+  int32_t keep_in_l2;   // the prefix rows may be read more than once (several row tiles or groups, K=V)
   int32_t stall_bytes;  // tests only: bytes expected per stage beyond what the copies deliver
 };
 

@@ -45,7 +45,7 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 // Markstein, Computation of elementary functions on the IBM RISC System/6000
 // processor, IBM J. Res. Dev. 34, 1990). Three operations, for two elements at
 // once; with the general division 74 million elements took 70 us, one element
-// at a time 41.2 (38.3 now). It is the negated quotient that is computed, x (-r)
+// at a time 41.2 (38.4 now). It is the negated quotient that is computed, x (-r)
 // and so on: where x is a zero the remainder is +0, and added to a quotient of -0
 // it would lose its sign; added to the negated one it loses none.
 struct Scale2 {

@@ -9,7 +9,9 @@ step attends [prompt | own tokens] with the prompt read once for all of them:
     SharedPrefixStep  the attention of the batch
 
 The lengths, tables and free list live on the GPU and are updated in place, so
-a step makes no round trip to the host. Random rows stand for a model's.
+a step makes no round trip to the host. Random rows stand for a model's, rotated
+already: PageTables.positions count a request's own tokens, so a model rotates
+its rows by the prompt's length plus those.
 
     python -m paged_gqa_decode_global_gb300.serving_step [steps]
 """
