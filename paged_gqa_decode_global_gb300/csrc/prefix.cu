@@ -856,7 +856,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
       auto factor = [&](int c) { return moves(c) ? ex2(-nref[c] - unordered(top[c])) : 1.f; };
       // a lane's sum holds this tile's probabilities already, under the old
       // reference; past 2^100 they may be infinite and all before them is
-      // negligible: the probability itself, under the new one
+      // negligible: the probability itself, under the new one (a NaN is none of that)
 #pragma unroll
       for (int c0 = 0; c0 < CW; c0 += LD) {
         tmem_ld(x, sa + c0);
@@ -866,7 +866,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefix_kernel(const __grid_cons
           const int cc = c0 + c;
           const float s = __uint_as_float(x[c]) * k.sc;
           const bool far = moves(cc) && k.valid && fmaf(__uint_as_float(x[c]), k.sc, nref[cc]) > 100.f;
-          l[cc] = far ? ex2(s - unordered(top[cc])) : l[cc] * factor(cc);
+          l[cc] = far && !isnan(l[cc]) ? ex2(s - unordered(top[cc])) : l[cc] * factor(cc);
         }
       }
       if (i > 0) {
