@@ -97,6 +97,7 @@ typedef enum {
 /* Element type of the KV cache (pd_layer_desc.kv_dtype). */
 #define PD_KV_BF16 0      /* bf16 K/V rows */
 #define PD_KV_FP8_E4M3 1  /* OCP e4m3 bytes; the value is byte * scale[page, KV head] */
+#define PD_KV_FP4_E2M1 2  /* OCP e2m1 codes, two a byte, with an e4m3 scale per 16 dims (see "A cache in 4 bits") */
 
 /* One attention layer's shape. */
 typedef struct {
@@ -108,7 +109,7 @@ typedef struct {
   int32_t max_pages_per_seq;  /* block-table row length */
   int32_t window;             /* 0 = global layer; > 0 = sliding window of this many tokens */
   int32_t kv_shared;          /* 1 = one pool is both K and V (K=V storage) */
-  int32_t kv_dtype;           /* PD_KV_BF16 or PD_KV_FP8_E4M3 */
+  int32_t kv_dtype;           /* PD_KV_BF16, PD_KV_FP8_E4M3 or PD_KV_FP4_E2M1 */
 } pd_layer_desc;
 
 /* Launch plan: a plain value filled by paged_decode_plan, copyable, reusable for
@@ -627,6 +628,88 @@ pd_status paged_decode_global_shared_fp8(const pd_shared_plan* plan, const void*
                                          const int32_t* seq_lens, float scale, void* workspace,
                                          size_t workspace_bytes, void* out, void* stream);
 
+/* ---- A cache in 4 bits ------------------------------------------------------------
+ *
+ * PD_KV_FP4_E2M1: a row of head_dim elements is head_dim / 2 bytes of e2m1 codes
+ * (element 2i in the low four bits of byte i) and head_dim / 16 e4m3 scales, one
+ * for every 16 consecutive elements:
+ *   value = e2m1(code) * e4m3(scale) * 2^exp,
+ * 4.5 bits an element. exp is a whole number in [-64, 64] for the layer's K and
+ * one for its V (the same on a K=V layer): the smallest with
+ * max |x| <= 6 * 448 * 2^exp keeps every value in range and all scales as far
+ * from e4m3's smallest as they can be.
+ *   k_pool, v_pool   uint8 [num_pages, num_kv_heads, page_size, head_dim / 2]
+ *   k_scale, v_scale uint8 [num_pages, num_kv_heads, page_size, head_dim / 16]
+ * all 16-byte aligned; head_dim 256 or 512.
+ *
+ * Quantising 16 elements x: scale = e4m3(max |x| / (6 * 2^exp)), code =
+ * e2m1(x / (scale * 2^exp)), both to nearest even and clamped to the largest;
+ * a block whose scale rounds to zero is held as zeros. A NaN makes its block's
+ * scale, and so the block, NaN; an infinity is clamped.
+ */
+
+/*
+ * The cache write by slot, quantised as it is written: as
+ * paged_decode_write_slots into a 4-bit cache, each row under scales of its own
+ * (nothing to calibrate but the layer's exponents). Returns as that does;
+ * PD_ERR_INVALID_ARG for exponents out of range.
+ */
+pd_status paged_decode_write_slots_fp4(const pd_layer_desc* layer, int32_t num_tokens, const void* k_in,
+                                       const void* v_in, int64_t k_stride, int64_t v_stride,
+                                       const int32_t* slot_map, void* k_pool, void* v_pool, void* k_scale,
+                                       void* v_scale, int32_t k_exp, int32_t v_exp, uint32_t* device_flags,
+                                       void* stream);
+
+/*
+ * The way back: the rows of any number of cached tokens, by slot, as bf16 (a
+ * prompt's next chunk attends them with a prefill kernel; a cache is checked or
+ * moved):
+ *   k_out[t, g, :] = the cached values of k_pool[page, g, s % P, :],  s = slot_map[t], page = s / P
+ * from a bf16 cache as they are, from an e4m3 cache the product with the page's
+ * scale in fp32 rounded to bf16, from a 4-bit cache exactly (six significant bits).
+ *   layer       head_dim 128, 256 or 512 (4 bits: 256 or 512)
+ *   slot_map    device int32 [num_tokens]; -1 skips a token (its output row
+ *               stays as it was); the same slot any number of times
+ *   k_out, v_out device bf16, token t's heads [Hkv, d] contiguous from element
+ *               t * k_stride (t * v_stride); strides as for the write; v_out
+ *               unused when layer->kv_shared
+ *   pools, scales, exponents: as for decode
+ *   device_flags PD_DEVFLAG_BAD_PAGE is or-ed in for a slot below -1 or past the
+ *               pool (its output row stays as it was)
+ * Launched as a programmatic dependent that lets the launch behind it start
+ * once it has waited itself. Returns as paged_decode_write_slots does.
+ */
+pd_status paged_decode_read_slots(const pd_layer_desc* layer, int32_t num_tokens, const int32_t* slot_map,
+                                  const void* k_pool, const void* v_pool, void* k_out, void* v_out, int64_t k_stride,
+                                  int64_t v_stride, uint32_t* device_flags, void* stream);
+pd_status paged_decode_read_slots_fp8(const pd_layer_desc* layer, int32_t num_tokens, const int32_t* slot_map,
+                                      const void* k_pool, const void* v_pool, const float* k_scale,
+                                      const float* v_scale, void* k_out, void* v_out, int64_t k_stride,
+                                      int64_t v_stride, uint32_t* device_flags, void* stream);
+pd_status paged_decode_read_slots_fp4(const pd_layer_desc* layer, int32_t num_tokens, const int32_t* slot_map,
+                                      const void* k_pool, const void* v_pool, const void* k_scale,
+                                      const void* v_scale, int32_t k_exp, int32_t v_exp, void* k_out, void* v_out,
+                                      int64_t k_stride, int64_t v_stride, uint32_t* device_flags, void* stream);
+
+/*
+ * Stage 1 over a 4-bit cache: as paged_decode_global / paged_decode_window
+ * (plans from paged_decode_plan or paged_decode_plan_multi on a layer with
+ * kv_dtype PD_KV_FP4_E2M1; paged_decode_merge follows). v_pool and v_scale of a
+ * K=V layer are NULL or k_pool and k_scale. A query element enters the score
+ * product as a sum of 4-bit terms that leaves out at most 2^-14 of the largest
+ * of its 16; a query row with a NaN or an infinity gives a NaN row.
+ * Probabilities are rounded to f16 relative to the largest so far of the tokens
+ * one quarter of the kernel serves (below 2^-39 of it they vanish).
+ */
+pd_status paged_decode_global_fp4(const pd_plan* plan, const void* q, const void* k_pool, const void* v_pool,
+                                  const void* k_scale, const void* v_scale, int32_t k_exp, int32_t v_exp,
+                                  const int32_t* block_tables, const int32_t* seq_lens, float scale, void* workspace,
+                                  size_t workspace_bytes, void* out, void* stream);
+pd_status paged_decode_window_fp4(const pd_plan* plan, const void* q, const void* k_pool, const void* v_pool,
+                                  const void* k_scale, const void* v_scale, int32_t k_exp, int32_t v_exp,
+                                  const int32_t* block_tables, const int32_t* seq_lens, int32_t window, float scale,
+                                  void* workspace, size_t workspace_bytes, void* out, void* stream);
+
 /* ---- The same calls with their arguments in a structure -------------------------
  *
  * For callers whose foreign calls cost by the argument (ctypes: ~2 us for twenty):
@@ -667,9 +750,24 @@ typedef struct {
   void *out, *stream;
 } pd_global_shared_args;
 
+/* Rows by slot: paged_decode_write_slots_fp4 (k_rows, v_rows are its inputs) and
+ * the reads (they are the outputs; which read goes by layer->kv_dtype). */
+typedef struct {
+  const pd_layer_desc* layer;
+  int32_t num_tokens, k_exp, v_exp, reserved; /* reserved 0 */
+  void *k_rows, *v_rows;
+  int64_t k_stride, v_stride;
+  const int32_t* slot_map;
+  void *k_pool, *v_pool, *k_scale, *v_scale;
+  uint32_t* device_flags;
+  void* stream;
+} pd_slot_rows_args;
+
 pd_status paged_decode_append_slots_args(const pd_append_slots_args* args);
 pd_status paged_decode_write_slots_args(const pd_write_slots_args* args);
 pd_status paged_decode_global_shared_args(const pd_global_shared_args* args);
+pd_status paged_decode_write_slots_fp4_args(const pd_slot_rows_args* args);
+pd_status paged_decode_read_slots_args(const pd_slot_rows_args* args);
 
 /* ---- Host-in/host-out decode loops ---------------------------------------------
  *

@@ -29,6 +29,7 @@ ABI_VERSION = 5
 
 PD_KV_BF16 = 0
 PD_KV_FP8_E4M3 = 1
+PD_KV_FP4_E2M1 = 2
 
 PD_DEVFLAG_BAD_PAGE = 0x1
 PD_DEVFLAG_BAD_SEQLEN = 0x2
@@ -64,6 +65,14 @@ EXPORTED = (
     "paged_decode_append_slots_args",
     "paged_decode_write_slots_args",
     "paged_decode_global_shared_args",
+    "paged_decode_global_fp4",
+    "paged_decode_window_fp4",
+    "paged_decode_write_slots_fp4",
+    "paged_decode_read_slots",
+    "paged_decode_read_slots_fp8",
+    "paged_decode_read_slots_fp4",
+    "paged_decode_write_slots_fp4_args",
+    "paged_decode_read_slots_args",
 )
 
 
@@ -210,8 +219,24 @@ def load_library(path: Optional[str] = None):
         lib.paged_decode_global_shared.restype = ctypes.c_int
         lib.paged_decode_global_shared_fp8.argtypes = [ctypes.POINTER(SharedPlan)] + [vp] * 10 + [f32, vp, u64, vp, vp]
         lib.paged_decode_global_shared_fp8.restype = ctypes.c_int
+        lib.paged_decode_global_fp4.argtypes = [ctypes.POINTER(Plan)] + [vp] * 5 + [i32] * 2 + [vp] * 2 + [
+            f32, vp, u64, vp, vp]
+        lib.paged_decode_global_fp4.restype = ctypes.c_int
+        lib.paged_decode_window_fp4.argtypes = [ctypes.POINTER(Plan)] + [vp] * 5 + [i32] * 2 + [vp] * 2 + [
+            i32, f32, vp, u64, vp, vp]
+        lib.paged_decode_window_fp4.restype = ctypes.c_int
+        rows = [ctypes.POINTER(LayerDesc), i32]
+        lib.paged_decode_write_slots_fp4.argtypes = rows + [vp] * 2 + [i64] * 2 + [vp] * 5 + [i32] * 2 + [vp] * 2
+        lib.paged_decode_write_slots_fp4.restype = ctypes.c_int
+        lib.paged_decode_read_slots.argtypes = rows + [vp] * 5 + [i64] * 2 + [vp] * 2
+        lib.paged_decode_read_slots.restype = ctypes.c_int
+        lib.paged_decode_read_slots_fp8.argtypes = rows + [vp] * 7 + [i64] * 2 + [vp] * 2
+        lib.paged_decode_read_slots_fp8.restype = ctypes.c_int
+        lib.paged_decode_read_slots_fp4.argtypes = rows + [vp] * 5 + [i32] * 2 + [vp] * 2 + [i64] * 2 + [vp] * 2
+        lib.paged_decode_read_slots_fp4.restype = ctypes.c_int
         for fn in (lib.paged_decode_append_slots_args, lib.paged_decode_write_slots_args,
-                   lib.paged_decode_global_shared_args):
+                   lib.paged_decode_global_shared_args, lib.paged_decode_write_slots_fp4_args,
+                   lib.paged_decode_read_slots_args):
             fn.argtypes, fn.restype = [ctypes.c_char_p], ctypes.c_int
         found = int(lib.paged_decode_abi_version())
         if found != ABI_VERSION:
@@ -337,6 +362,68 @@ def paged_decode_window_fp8(plan: Plan, q, k_pool, v_pool, k_scale, v_scale, blo
     _check(st, "paged_decode_window_fp8")
 
 
+def paged_decode_global_fp4(plan: Plan, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens, scale: float,
+                            workspace, out, stream=None, workspace_bytes: Optional[int] = None, *, k_exp: int = 0,
+                            v_exp: int = 0) -> None:
+    """Stage 1 over a 4-bit cache: k_pool / v_pool uint8 codes [pages, Hkv, P, d / 2], k_scale / v_scale uint8 (e4m3)
+    [pages, Hkv, P, d / 16], values times 2^k_exp and 2^v_exp (fp4_exponent). On a K=V layer v_exp is k_exp."""
+    _decode_fp4(plan, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens, None, scale, workspace, out, stream,
+                workspace_bytes, k_exp, v_exp)
+
+
+def paged_decode_window_fp4(plan: Plan, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens, window: int,
+                            scale: float, workspace, out, stream=None, workspace_bytes: Optional[int] = None, *,
+                            k_exp: int = 0, v_exp: int = 0) -> None:
+    """The same on a sliding-window layer."""
+    _decode_fp4(plan, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens, int(window), scale, workspace, out,
+                stream, workspace_bytes, k_exp, v_exp)
+
+
+def _decode_fp4(plan, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens, window, scale, workspace, out,
+                stream, workspace_bytes, k_exp, v_exp) -> None:
+    lib, ly = load_library(), plan.layer
+    dev, nbytes = workspace.get_device(), workspace.nbytes if workspace_bytes is None else int(workspace_bytes)
+    if workspace.nbytes < nbytes or not workspace.is_contiguous():
+        _refuse_bytes("workspace", workspace, nbytes)
+    torch = _torch()
+    B, T, Hq, d = plan.batch, plan.query_tokens, ly.num_q_heads, ly.head_dim
+    shape = (B, T, Hq, d) if T > 1 or (hasattr(q, "dim") and q.dim() == 4) else (B, Hq, d)
+    pool, scales = _fp4_shapes(ly)
+    _want_or_address(q, "q", torch.bfloat16, shape, dev)
+    _want_or_address(out, "out", torch.bfloat16, shape, dev)
+    _want_or_address(k_pool, "k_pool", torch.uint8, pool, dev)
+    _want_or_address(v_pool, "v_pool", torch.uint8, pool, dev)
+    _want_or_address(k_scale, "k_scale", torch.uint8, scales, dev)
+    _want_or_address(v_scale, "v_scale", torch.uint8, scales, dev)
+    _want_or_address(block_tables, "block_tables", torch.int32, (B, ly.max_pages_per_seq), dev)
+    _want_or_address(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    raw = _launch_stream(stream, dev)
+    head = (ctypes.byref(plan), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), k_exp, v_exp,
+            _ptr(block_tables), _ptr(seq_lens))
+    tail = (scale, workspace.data_ptr(), nbytes, _ptr(out), raw)
+    if window is None:
+        st = lib.paged_decode_global_fp4(*head, *tail)
+    else:
+        st = lib.paged_decode_window_fp4(*head, window, *tail)
+    if st != PD_OK:
+        raise PagedDecodeError(st, "paged_decode_global_fp4" if window is None else "paged_decode_window_fp4")
+
+
+def _fp4_shapes(ly) -> tuple:
+    """A layer's 4-bit pool and its block scales."""
+    rows = (ly.num_pages, ly.num_kv_heads, ly.page_size)
+    return rows + (ly.head_dim // 2,), rows + (ly.head_dim // 16,)
+
+
+def fp4_exponent(largest: float) -> int:
+    """The layer exponent for values of magnitudes up to `largest`: the smallest e in [-64, 64] with
+    largest <= 6 * 448 * 2^e."""
+    if not largest > 0.0:
+        return 0
+    m, e = math.frexp(largest / (6.0 * 448.0))
+    return max(-64, min(64, e - 1 if m == 0.5 else e))
+
+
 def paged_decode_merge(plan: Plan, workspace, out, stream=None, workspace_bytes: Optional[int] = None) -> None:
     lib = load_library()
     wb = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
@@ -391,6 +478,7 @@ class LayerStep:
         self.desc = layer_desc(num_q_heads, num_kv_heads, head_dim, page_size, num_pages, max_pages_per_seq,
                                window, kv_shared, kv_dtype)
         self.fp8 = kv_dtype == PD_KV_FP8_E4M3
+        self.fp4 = kv_dtype == PD_KV_FP4_E2M1
         self.query_tokens = int(query_tokens)
         if self.query_tokens > 1:
             self.plan = paged_decode_plan_multi(self.desc, self.query_tokens, list(seq_lens_host), sm_count)
@@ -414,8 +502,13 @@ class LayerStep:
                    query_tokens=query_tokens, early_kv=early_kv)
 
     def __call__(self, q, k_pool, v_pool, block_tables, seq_lens, scale, out, stream=None, k_scale=None,
-                 v_scale=None):
-        if self.fp8:
+                 v_scale=None, k_exp=0, v_exp=0):
+        if self.fp4:
+            _decode_fp4(self.plan, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens, self.window or None,
+                        scale, self.workspace, out, stream, None, k_exp, v_exp)
+            if self.plan.merge_mode != 1:  # merged already
+                return out
+        elif self.fp8:
             if self.window > 0:
                 paged_decode_window_fp8(self.plan, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens,
                                         self.window, scale, self.workspace, out, stream)
@@ -671,6 +764,79 @@ def paged_decode_write_slots_fp8(desc: LayerDesc, k_in, v_in, slot_map, k_pool, 
                                  device_flags, stream=None) -> None:
     """The same into e4m3 pools (uint8), each row divided by its (page, head)'s scale."""
     _write_slots(True, desc, k_in, v_in, slot_map, k_pool, v_pool, k_scale, v_scale, device_flags, stream)
+
+
+# pd_slot_rows_args
+_ROWS_ARGS = struct.Struct("P4i2P2q7P").pack
+
+
+def _slot_rows(what: str, kv: int, desc, k_rows, v_rows, slot_map, k_pool, v_pool, k_scale, v_scale, k_exp, v_exp,
+               device_flags, stream) -> None:
+    """paged_decode_write_slots_fp4 (rows in) and the reads (rows out)."""
+    torch = _torch()
+    (n,), dev, heads, d = slot_map.shape, slot_map.get_device(), desc.num_kv_heads, desc.head_dim
+    if desc.kv_dtype != kv:
+        raise ValueError(f"{what}: the layer's kv_dtype is {desc.kv_dtype}, not {kv}")
+    bf16, u8, shared = torch.bfloat16, torch.uint8, desc.kv_shared
+    _want(slot_map, "slot_map", torch.int32, (n,), dev)
+    pool, rows = (desc.num_pages, heads, desc.page_size, d), (n, heads, d)
+    if kv == PD_KV_FP4_E2M1:
+        pool, scales = _fp4_shapes(desc)
+        kinds = (u8, u8)
+    else:
+        scales, kinds = pool[:2], (u8, torch.float32) if kv == PD_KV_FP8_E4M3 else (bf16, None)
+    stride = [0, 0]
+    sides = (("k", k_rows, k_pool, k_scale),) if shared else (
+        ("k", k_rows, k_pool, k_scale), ("v", v_rows, v_pool, v_scale))
+    for i, (x, r, p, s) in enumerate(sides):
+        if r is None or p is None or (s is None and kinds[1] is not None):
+            raise ValueError(f"{what}: {x}'s rows, pool and (a quantised cache's) scales are wanted")
+        _want(p, x + "_pool", kinds[0], pool, dev)
+        if kinds[1] is not None:
+            _want(s, x + "_scale", kinds[1], scales, dev)
+        stride[i] = _token_rows(r, x + " rows", bf16, rows, dev)
+    if shared:
+        v_rows, v_pool, v_scale = None, None, None
+    if not _is_word(device_flags, dev):
+        _refuse_bytes("device_flags", device_flags, 4)
+    raw = _launch_stream(stream, dev)
+    args = _ROWS_ARGS(
+        ctypes.addressof(desc), n, k_exp, v_exp, 0, k_rows.data_ptr(), _ptr(v_rows) or 0, *stride, slot_map.data_ptr(),
+        k_pool.data_ptr(), _ptr(v_pool) or 0, _ptr(k_scale) or 0, _ptr(v_scale) or 0, device_flags.data_ptr(), raw)
+    lib = load_library()
+    write = what == "paged_decode_write_slots_fp4"
+    st = lib.paged_decode_write_slots_fp4_args(args) if write else lib.paged_decode_read_slots_args(args)
+    if st != PD_OK:
+        raise PagedDecodeError(st, what)
+
+
+def paged_decode_write_slots_fp4(desc: LayerDesc, k_in, v_in, slot_map, k_pool, v_pool, k_scale, v_scale,
+                                 device_flags, stream=None, *, k_exp: int = 0, v_exp: int = 0) -> None:
+    """Quantise k_in / v_in [tokens, Hkv, d] (any token stride) into the rows of a 4-bit cache that slot_map names
+    (codes and block scales); -1 skips a token. On a K=V layer v_exp is k_exp."""
+    _slot_rows("paged_decode_write_slots_fp4", PD_KV_FP4_E2M1, desc, k_in, v_in, slot_map, k_pool, v_pool, k_scale,
+               v_scale, k_exp, v_exp, device_flags, stream)
+
+
+def paged_decode_read_slots(desc: LayerDesc, slot_map, k_pool, v_pool, k_out, v_out, device_flags, stream=None) -> None:
+    """The cached rows that slot_map names into k_out / v_out bf16 [tokens, Hkv, d] (any token stride); -1 leaves a
+    row as it is."""
+    _slot_rows("paged_decode_read_slots", PD_KV_BF16, desc, k_out, v_out, slot_map, k_pool, v_pool, None, None, 0, 0,
+               device_flags, stream)
+
+
+def paged_decode_read_slots_fp8(desc: LayerDesc, slot_map, k_pool, v_pool, k_scale, v_scale, k_out, v_out,
+                                device_flags, stream=None) -> None:
+    """The same from e4m3 pools (uint8) with per-(page, KV head) scales."""
+    _slot_rows("paged_decode_read_slots_fp8", PD_KV_FP8_E4M3, desc, k_out, v_out, slot_map, k_pool, v_pool, k_scale,
+               v_scale, 0, 0, device_flags, stream)
+
+
+def paged_decode_read_slots_fp4(desc: LayerDesc, slot_map, k_pool, v_pool, k_scale, v_scale, k_out, v_out,
+                                device_flags, stream=None, *, k_exp: int = 0, v_exp: int = 0) -> None:
+    """The same from a 4-bit cache."""
+    _slot_rows("paged_decode_read_slots_fp4", PD_KV_FP4_E2M1, desc, k_out, v_out, slot_map, k_pool, v_pool, k_scale,
+               v_scale, k_exp, v_exp, device_flags, stream)
 
 
 def paged_decode_plan_shared(desc: LayerDesc, query_tokens: int, seq_lens_host: Sequence[int],

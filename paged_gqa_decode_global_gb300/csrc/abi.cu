@@ -23,10 +23,10 @@ constexpr int kMaxContexts = 64;
 // Per CUDA context, one bit per kernel instance whose dynamic shared-memory limit
 // has been raised there (a function attribute belongs to the context it was set
 // in): word 0 the stage-1 variants, word 1 the prefix pass's, word 2 the stage-1
-// variants that run beside it.
+// variants that run beside it, word 3 the 4-bit variants.
 struct SmemReady {
   unsigned long long ctx_id;
-  uint64_t bits[3];
+  uint64_t bits[4];
 };
 #define PD_VARIANT_ID_FITS_A_BIT(ID, ...) static_assert((ID) >= 0 && (ID) < 64, "one bit per variant id");
 PD_FOR_EACH_VARIANT(PD_VARIANT_ID_FITS_A_BIT)
@@ -136,7 +136,7 @@ pd_status ensure_smem_attr(int word, int variant, const void* fn, int smem_bytes
       if (g_smem_ready[i].ctx_id == now) e = &g_smem_ready[i];
     if (!e && g_smem_contexts < kMaxContexts) {
       e = &g_smem_ready[g_smem_contexts++];
-      *e = SmemReady{now, {0, 0, 0}};
+      *e = SmemReady{now, {0, 0, 0, 0}};
     }
   }
   if (e) e->bits[word] |= bit;
@@ -303,6 +303,27 @@ pd_status encode_group_map(CUtensorMap* map, const void* pool, const pd_layer_de
 
 pd_status ensure_prefix_smem(int variant, const void* fn, int smem_bytes) {
   return ensure_smem_attr(1, variant, fn, smem_bytes);
+}
+
+pd_status ensure_fp4_smem(int variant, const void* fn, int smem_bytes) {
+  return ensure_smem_attr(3, variant, fn, smem_bytes);
+}
+
+// A pool of 4-bit codes [num_pages, Hkv, P, D / 2] in boxes of 16 rows that land as
+// [8-row group][128-byte slab][8 rows][128 B], 128-byte swizzled.
+pd_status encode_code_map(CUtensorMap* map, const void* pool, const pd_layer_desc& ly) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return PD_ERR_CUDA;
+  const cuuint64_t row = (cuuint64_t)ly.head_dim / 2;
+  const cuuint64_t total = (cuuint64_t)ly.num_pages * ly.num_kv_heads * ly.page_size;
+  const cuuint64_t dims[4] = {128, 8, row / 128, total / 8};
+  const cuuint64_t strides[3] = {row, 128, 8 * row};
+  const cuuint32_t box[4] = {128, 8, (cuuint32_t)(row / 128), 2};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(pool), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PD_OK : PD_ERR_CUDA;
 }
 
 }  // namespace pd

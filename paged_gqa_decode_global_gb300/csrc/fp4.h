@@ -1,0 +1,87 @@
+// Decode over a 4-bit (e2m1 codes, e4m3 block scales) cache: instances and
+// launch geometry, shared by the host planner and the kernel.
+#pragma once
+
+#include <cstdint>
+
+#include "pd_kernels.h"
+
+namespace pd {
+
+constexpr int kFp4Block = 16;    // dims under one scale
+constexpr int kFp4Tile = 128;    // tokens of a tile: the matrix instruction's rows
+constexpr int kFp4Terms = 6;     // e2m1 terms a query element is written as
+constexpr int kFp4FirstId = 60;  // variant ids follow stage 1's
+constexpr int kFp4MaxCluster = 8;
+
+// D   head_dim; KVS K=V shared pool; CC columns (query rows) of a CTA
+template <int D_, bool KVS_, int CC_>
+struct Fp4Cfg {
+  static constexpr int D = D_, CC = CC_;
+  static constexpr bool KVS = KVS_;
+  static constexpr int SL = D / 256;       // 128-byte slabs of a row's codes
+  static constexpr int KSTEPS = D / 64;    // 64-dim steps of the matrix instruction
+  static constexpr int N = (CC * kFp4Terms + 15) / 16 * 16;  // its columns
+  static constexpr int ROW_SF = D / kFp4Block;               // scale bytes of a row
+  // one tile of K or V: codes [8-row group][slab][8 rows][128 B, swizzled], then scales [128][D / 16]
+  static constexpr int CODE_BYTES = kFp4Tile * D / 2;
+  static constexpr int SF_BYTES = kFp4Tile * ROW_SF;
+  static constexpr int ITEM_BYTES = CODE_BYTES + SF_BYTES;
+  // K != V: a ring for K (a tile is done with once its scores are computed)
+  // and a longer one for V
+  static constexpr int NK = KVS ? (D == 512 ? 5 : 10) : (D == 512 ? 2 : 4);
+  static constexpr int NV = KVS ? 0 : (D == 512 ? 3 : 6);
+  static constexpr int RING_BYTES = (NK + NV) * ITEM_BYTES;
+  // after the last tile, over the ring: the PV warps' sums, float [8][CC][288]
+  // (4 floats of padding every 32 dims), the CTA's result and its log-sum-exps
+  static constexpr int COMB_ROW = 288;
+  static constexpr int OUT_OFFSET = 8 * CC * COMB_ROW * 4;  // float [CC][D]
+  static_assert(OUT_OFFSET + CC * D * 4 <= RING_BYTES, "the end's buffers lie over the ring");
+  static constexpr int Q_OFFSET = RING_BYTES;                     // query terms' codes, like a tile's
+  static constexpr int QSF_OFFSET = Q_OFFSET + N * D / 2;         // their scales [N][D / 16]
+  static constexpr int P_ROW = 80;                                // bytes: 32 tokens in f16, spread over the banks
+  static constexpr int P_OFFSET = QSF_OFFSET + N * ROW_SF;        // [4 quarters][2][CC] rows
+  static constexpr int ALPHA_OFFSET = P_OFFSET + 8 * CC * P_ROW;  // float [4][2][8]
+  static constexpr int COL_OFFSET = ALPHA_OFFSET + 4 * 2 * 8 * 4; // float [CC]: score scale of a column
+  static constexpr int ML_OFFSET = COL_OFFSET + CC * 4;           // float2 [4][CC]
+  static constexpr int COEF_OFFSET = ML_OFFSET + 4 * CC * 8;      // float [4][CC], lse [CC]
+  static constexpr int VALID_OFFSET = COEF_OFFSET + 5 * CC * 4;   // u32 [NK + NV]
+  static constexpr int BAR_OFFSET = (VALID_OFFSET + (NK + NV) * 4 + 7) / 8 * 8;
+  static constexpr int NUM_BARS = 2 * (NK + NV) + 6 + 16;
+  static constexpr int SMEM_BYTES = BAR_OFFSET + NUM_BARS * 8 + 16 + 1024;  // (+ 1 KiB to start on a 1024-byte boundary)
+  static constexpr int WARPS = 14;  // 4 softmax, 8 PV, 1 copies, 1 matrix instructions
+  static constexpr int THREADS = 32 * WARPS;
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+  static_assert(Q_OFFSET % 1024 == 0 && QSF_OFFSET % 16 == 0 && P_OFFSET % 16 == 0 && ML_OFFSET % 8 == 0, "alignment");
+};
+
+// X(id, head_dim, K=V, columns)
+#define PD_FOR_EACH_FP4(X)  \
+  X(60, 512, false, 4)      \
+  X(61, 512, false, 8)      \
+  X(62, 512, true, 4)       \
+  X(63, 512, true, 8)       \
+  X(64, 256, false, 4)      \
+  X(65, 256, false, 8)      \
+  X(66, 256, true, 4)       \
+  X(67, 256, true, 8)
+
+// What a launch needs beyond Stage1Params' common part.
+struct Fp4Params {
+  CUtensorMap kmap, vmap;  // codes as {128 B, 8 rows, slabs, 8-row groups}
+  const uint16_t* q;       // bf16 [B, T, Hq, D]
+  const uint8_t *k_sf, *v_sf;  // e4m3 [num_pages, Hkv, P, D / 16]
+  const int32_t *block_tables, *seq_lens;
+  void* out;
+  float *lse_part, *o_part;
+  uint32_t* err;
+  float scale_log2;  // softmax scale * log2(e) * 2^k_exp
+  float v_mul;       // 2^v_exp
+  int32_t direct_out, cluster_merge, stall_bytes, early_kv;
+  int32_t window, num_pages, max_pages, page_size, num_q_heads, num_kv_heads, num_splits, chunk_tokens;
+  int32_t query_tokens, group, col_tiles;
+};
+
+const void* fp4_kernel_ptr(int variant);
+
+}  // namespace pd

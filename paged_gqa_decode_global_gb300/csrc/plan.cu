@@ -13,6 +13,7 @@
 #include <queue>
 #include <vector>
 
+#include "fp4.h"
 #include "paged_decode.h"
 #include "pd_kernels.h"
 
@@ -34,8 +35,13 @@ namespace pd {
               Stage1Cfg<D, G, KVS, KV8, NW, SPW, MQ, NSUB, TW>::DED_SLOTS,                                 \
               NSUB,                                                                                       \
               TW},
-const VariantInfo kVariants[] = {PD_FOR_EACH_VARIANT(PD_VARIANT_ROW)};
+// The 4-bit instances (kv_fp8 2, `group` their columns) follow by id.
+#define PD_FP4_ROW(ID, D, KVS, CC)                                                                   \
+  VariantInfo{ID, D, CC, KVS ? 1 : 0, 2, 8, 0, 16, Fp4Cfg<D, KVS, CC>::THREADS,                      \
+              Fp4Cfg<D, KVS, CC>::SMEM_BYTES, kFp4MaxCluster, 1, 0, kFp4Tile / 16, 1},
+const VariantInfo kVariants[] = {PD_FOR_EACH_VARIANT(PD_VARIANT_ROW) PD_FOR_EACH_FP4(PD_FP4_ROW)};
 #undef PD_VARIANT_ROW
+#undef PD_FP4_ROW
 const int kNumVariants = sizeof(kVariants) / sizeof(kVariants[0]);
 
 }  // namespace pd
@@ -78,11 +84,24 @@ const pd::VariantInfo* find_variant(int head_dim, int group, int kv_shared, int 
   return nullptr;
 }
 
+// The instance of a 4-bit cache for T x group query rows a KV head: four columns
+// a CTA where that holds them all, else eight.
+const pd::VariantInfo* find_fp4(int head_dim, int kv_shared, int rows) {
+  const pd::VariantInfo* best = nullptr;
+  for (int i = 0; i < pd::kNumVariants; ++i) {
+    const pd::VariantInfo& v = pd::kVariants[i];
+    if (v.kv_fp8 != PD_KV_FP4_E2M1 || v.head_dim != head_dim || v.kv_shared != kv_shared) continue;
+    if (!best || (best->group < rows ? v.group > best->group : v.group >= rows && v.group < best->group)) best = &v;
+  }
+  return best;
+}
+
 // 8-column tiles of a column-tiled plan: its T x group (token, head) pairs, 8 at a time.
 int col_tiles(int query_tokens, int group) { return (query_tokens * group + 7) / 8; }
 
 // CTAs per (KV head, piece) of a plan on instance v.
 int col_groups(const pd::VariantInfo& v, int query_tokens, int group) {
+  if (v.kv_fp8 == PD_KV_FP4_E2M1) return (query_tokens * group + v.group - 1) / v.group;
   return v.multi ? (col_tiles(query_tokens, group) + v.tiles - 1) / v.tiles : 1;
 }
 
@@ -130,6 +149,7 @@ int cluster_slots(int splits, int sm_count) {
 // in one tile), and for bf16 CTAs of two tiles.
 double cta_tokens_per_us(const pd::VariantInfo& v) {
   const bool kvs = v.kv_shared != 0;
+  if (v.kv_fp8 == PD_KV_FP4_E2M1) return v.head_dim == 512 ? (kvs ? 120.0 : 90.0) : (kvs ? 220.0 : 170.0);
   if (v.tiles == 2) {
     if (v.head_dim == 512) return kvs ? 48.5 : 47.2;
     return 67.0;  // d256 (K=V not measured: the K != V figure)
@@ -312,7 +332,10 @@ pd_status plan_impl(const pd_layer_desc* layer, int32_t batch, int32_t query_tok
   if (ly.head_dim <= 0 || ly.page_size <= 0 || ly.page_size % 16 != 0) return PD_ERR_INVALID_ARG;
   if (ly.num_pages <= 0 || ly.max_pages_per_seq <= 0 || ly.window < 0) return PD_ERR_INVALID_ARG;
   if (ly.kv_shared != 0 && ly.kv_shared != 1) return PD_ERR_INVALID_ARG;
-  if (ly.kv_dtype != PD_KV_BF16 && ly.kv_dtype != PD_KV_FP8_E4M3) return PD_ERR_INVALID_ARG;
+  if (ly.kv_dtype != PD_KV_BF16 && ly.kv_dtype != PD_KV_FP8_E4M3 && ly.kv_dtype != PD_KV_FP4_E2M1)
+    return PD_ERR_INVALID_ARG;
+  const bool fp4 = ly.kv_dtype == PD_KV_FP4_E2M1;
+  if (fp4 && partial) return PD_ERR_UNSUPPORTED;  // neither a shared prefix's own part nor a shard's
   if (batch < 0 || batch > 65535 || ly.num_kv_heads > 65535 || sm_count <= 0) return PD_ERR_INVALID_ARG;
   if (batch > 0 && !seq_lens_host) return PD_ERR_INVALID_ARG;
   const long long cap = (long long)ly.max_pages_per_seq * ly.page_size;
@@ -325,7 +348,7 @@ pd_status plan_impl(const pd_layer_desc* layer, int32_t batch, int32_t query_tok
     max_len = std::max(max_len, seq_lens_host[b]);
   }
   const int group = ly.num_q_heads / ly.num_kv_heads;
-  const bool multi = tiled(T, group);
+  const bool multi = !fp4 && tiled(T, group);
   const bool fp8 = ly.kv_dtype == PD_KV_FP8_E4M3;
   // Two tiles per CTA read each block once for both; separate CTAs read it
   // once each, the second read an L2 hit when the context is short. Measured
@@ -346,7 +369,9 @@ pd_status plan_impl(const pd_layer_desc* layer, int32_t batch, int32_t query_tok
   // us, windows of 1024 -1.6%); longer spans keep the seventh warp's
   // arithmetic (1 GiB: 84.1 us against 86.0 with six).
   const int want_nw = (fp8 && !ly.kv_shared && !multi && longest_span < 4096) ? 6 : 0;
-  const pd::VariantInfo* v = find_variant(ly.head_dim, group, ly.kv_shared, fp8, multi, want_tiles, want_nw);
+  const pd::VariantInfo* v = fp4 ? (group <= kMaxGroup ? find_fp4(ly.head_dim, ly.kv_shared, T * group) : nullptr)
+                                 : find_variant(ly.head_dim, group, ly.kv_shared, fp8, multi, want_tiles, want_nw);
+  if (!v && fp4) return PD_ERR_UNSUPPORTED;
   if (!v && want_nw > 0) v = find_variant(ly.head_dim, group, ly.kv_shared, fp8, multi, want_tiles);
   if (!v && want_tiles > 1) v = find_variant(ly.head_dim, group, ly.kv_shared, fp8, multi, 1);
   if (!v) return PD_ERR_UNSUPPORTED;
@@ -372,7 +397,7 @@ pd_status plan_impl(const pd_layer_desc* layer, int32_t batch, int32_t query_tok
 
   CostModel cm;
   const double kv_bytes_per_token =
-      (double)ly.head_dim * (ly.kv_dtype == PD_KV_FP8_E4M3 ? 1.0 : 2.0) * (ly.kv_shared ? 1.0 : 2.0);
+      (double)ly.head_dim * (fp4 ? 0.5 + 1.0 / 16 : fp8 ? 1.0 : 2.0) * (ly.kv_shared ? 1.0 : 2.0);
   // ~7.3 TB/s of HBM on a 152-SM GB300, in proportion for other SM counts
   cm.hbm_tok_per_us = 7.3e12 / 1e6 / kv_bytes_per_token * sm_count / 152.0;
   cm.cap_tok_per_us = cta_tokens_per_us(*v);
@@ -542,7 +567,10 @@ bool plan_is_valid(const pd_plan* plan) {
   const pd_layer_desc& ly = plan->layer;
   if (ly.num_kv_heads <= 0 || ly.num_q_heads % ly.num_kv_heads != 0) return false;
   const int group = ly.num_q_heads / ly.num_kv_heads;
-  if (v.multi) {
+  if (v.kv_fp8 == PD_KV_FP4_E2M1) {
+    if (group > kMaxGroup || plan->query_tokens < 1 || plan->query_tokens > kMaxQueryTokens) return false;
+    if (plan->partial || plan->grid_y != ly.num_kv_heads * col_groups(v, plan->query_tokens, group)) return false;
+  } else if (v.multi) {
     if (group > kMaxGroup || plan->query_tokens < 1 || plan->query_tokens > kMaxQueryTokens) return false;
     if (!tiled(plan->query_tokens, group)) return false;
     if (plan->grid_y != ly.num_kv_heads * col_groups(v, plan->query_tokens, group)) return false;
@@ -550,7 +578,7 @@ bool plan_is_valid(const pd_plan* plan) {
     if (group != v.group || plan->query_tokens != 1 || plan->grid_y != ly.num_kv_heads) return false;
   }
   if (ly.head_dim != v.head_dim || ly.kv_shared != v.kv_shared) return false;
-  if ((ly.kv_dtype == PD_KV_FP8_E4M3) != (v.kv_fp8 == 1)) return false;
+  if (ly.kv_dtype != v.kv_fp8) return false;
   if (plan->num_splits < 1 || plan->num_splits > kMaxSplits || plan->chunk_tokens < 16 || plan->chunk_tokens % 16 != 0)
     return false;
   if (plan->batch < 0 || plan->grid_x != plan->num_splits || plan->grid_z != plan->batch) return false;
