@@ -124,81 +124,100 @@ __device__ __forceinline__ uint32_t code_offset(int row, int byte) {
   return (row >> 3) * (C::SL * 1024) + sl * 1024 + (row & 7) * 128 + ((c ^ (row & 7)) << 4) + (byte & 15);
 }
 
-// The query rows of the CTA's columns as terms in shared memory, by `threads`
-// threads: four of them a block of 16 dims.
+// The query rows of the CTA's columns as terms in shared memory, by 8 warps:
+// one takes 256 dims of a row, a lane 8 of them, two lanes a block of 16.
 template <class C>
-__device__ __forceinline__ void write_query_terms(const Fp4Params& p, const Columns<C>& cm, uint8_t* smem, int tid,
-                                                  int threads) {
-  constexpr int PER_ROW = C::D / 4;  // threads of a row
-  for (int e0 = 0; e0 < C::CC * PER_ROW; e0 += threads) {
-    const int e = e0 + tid;
-    const int col = e / PER_ROW, part = e % PER_ROW;
-    const bool on = e < C::CC * PER_ROW && cm.valid(col);
-    uint2 w = make_uint2(0u, 0u);
-    if (on) w = __ldg(reinterpret_cast<const uint2*>(p.q + cm.row(col) * C::D) + part);
-    float x[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                  __uint_as_float(w.y & 0xffff0000u)};
+__device__ __forceinline__ void write_query_terms(const Fp4Params& p, const Columns<C>& cm, uint8_t* smem, int warp,
+                                                  int lane) {
+  constexpr int ITEMS = C::CC * C::SL, EACH = (ITEMS + 7) / 8;
+  uint4 w[EACH];
+  uint32_t big[EACH];
+#pragma unroll
+  for (int k = 0; k < EACH; ++k) {
+    const int item = warp + 8 * k, col = item / C::SL, part = item % C::SL;
+    uint4 o = make_uint4(0u, 0u, 0u, 0u);
+    w[k] = o;
+    if (item < ITEMS && cm.valid(col)) {
+      const uint4* row = reinterpret_cast<const uint4*>(p.q + cm.row(col) * C::D) + lane;
+      w[k] = __ldg(row + part * 32);
+      if (C::SL == 2) o = __ldg(row + (part ^ 1) * 32);  // (for the row's largest)
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (uint32_t v : {w[k].x, w[k].y, w[k].z, w[k].w, o.x, o.y, o.z, o.w}) m = __vmaxu2(m, v & 0x7fff7fffu);
+    big[k] = max(m << 16, m & 0xffff0000u);
+  }
+#pragma unroll
+  for (int k = 0; k < EACH; ++k) {
+    const int item = warp + 8 * k, col = item / C::SL, part = item % C::SL;
+    if (item >= ITEMS) break;
     // the row's largest magnitude, as whole numbers (infinity and NaN are the largest)
-    uint32_t big = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) big = max(big, __float_as_uint(x[i]) & 0x7fffffffu);
-    big = __reduce_max_sync(kFullMask, big);
-    uint32_t* row_big = reinterpret_cast<uint32_t*>(smem + C::COL_OFFSET);
-    if ((tid & 31) == 0 && on) atomicMax(row_big + col, big);
-    named_bar_sync(2, threads);
-    if (e < C::CC * PER_ROW) big = row_big[col];
-    const bool odd = big >= 0x7f800000u;  // a NaN or an infinity: the row's scores are NaN
+    const uint32_t top = __reduce_max_sync(kFullMask, big[k]);
+    const bool odd = top >= 0x7f800000u;  // a NaN or an infinity: the row's scores are NaN
     // brings the largest to [2^10, 2^11) (a row that is below 2^-116 altogether: as near as a factor of 2^126 does)
-    const int shift = min(126, 137 - (int)(big >> 23));
+    const int shift = min(126, 137 - (int)(top >> 23));
     const float up = __int_as_float((127 + shift) << 23);
+    const uint32_t v[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+    float x[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = odd ? 0.f : x[i] * up;
-    uint32_t store[kFp4Terms];
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = odd ? 0.f : __uint_as_float(v[i] << 16) * up;
+      x[2 * i + 1] = odd ? 0.f : __uint_as_float(v[i] & 0xffff0000u) * up;
+    }
 #pragma unroll
     for (int t = 0; t < kFp4Terms; ++t) {
-      float a = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+      float a = fmaxf(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))),
+                      fmaxf(fmaxf(fabsf(x[4]), fabsf(x[5])), fmaxf(fabsf(x[6]), fabsf(x[7]))));
       a = fmaxf(a, __shfl_xor_sync(kFullMask, a, 1));
-      a = fmaxf(a, __shfl_xor_sync(kFullMask, a, 2));
       uint16_t s8;
       asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s8) : "f"(0.f), "f"(a * (1.f / 6.f)));
       uint32_t s16;
       asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s16) : "h"(s8));
       const float s = __half2float(__ushort_as_half((unsigned short)(s16 & 0xffffu)));
-      const float r = s > 0.f ? __frcp_rn(s) : 0.f;
-      uint16_t codes;
-      asm("{\n\t.reg .b8 a, b;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-          "mov.b16 %0, {a, b};\n\t}"
-          : "=h"(codes)
-          : "f"(x[0] * r), "f"(x[1] * r), "f"(x[2] * r), "f"(x[3] * r));
-      uint32_t v[4];
-      e2m1x8_to_f16x8(codes, v);
-      const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&v[0]));
-      const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&v[1]));
-      x[0] = fmaf(-lo.x, s, x[0]);
-      x[1] = fmaf(-lo.y, s, x[1]);
-      x[2] = fmaf(-hi.x, s, x[2]);
-      x[3] = fmaf(-hi.y, s, x[3]);
-      store[t] = codes | (uint32_t)(odd ? 0x7f : (s8 & 0xff)) << 16;
-    }
-    named_bar_sync(2, threads);  // every thread has the row's largest
-    if (e < C::CC * PER_ROW) {
+      float r;  // (what a term leaves over, the next one takes: its rounding need not be exact)
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+      r = s > 0.f ? r : 0.f;
+      uint32_t codes;
+      asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+          "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+          "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+          "mov.b32 %0, {a, b, c, d};\n\t}"
+          : "=r"(codes)
+          : "f"(x[0] * r), "f"(x[1] * r), "f"(x[2] * r), "f"(x[3] * r), "f"(x[4] * r), "f"(x[5] * r), "f"(x[6] * r),
+            "f"(x[7] * r));
+      if (t + 1 < kFp4Terms) {
+        uint32_t f[4];
+        e2m1x8_to_f16x8(codes, f);
 #pragma unroll
-      for (int t = 0; t < kFp4Terms; ++t) {
-        const int n = t * C::CC + col;
-        *reinterpret_cast<uint16_t*>(smem + C::Q_OFFSET + code_offset<C>(n, part * 2)) = (uint16_t)store[t];
-        if ((part & 3) == 0) smem[C::QSF_OFFSET + n * C::ROW_SF + part / 4] = (uint8_t)(store[t] >> 16);
+        for (int i = 0; i < 4; ++i) {
+          const float2 two = __half22float2(*reinterpret_cast<const __half2*>(&f[i]));
+          x[2 * i] = fmaf(-two.x, s, x[2 * i]);
+          x[2 * i + 1] = fmaf(-two.y, s, x[2 * i + 1]);
+        }
       }
-      if (part == 0)
-        reinterpret_cast<float*>(smem + C::COL_OFFSET)[col] =
-            p.scale_log2 * __int_as_float((127 - shift) << 23);
+      const int n = t * C::CC + col;
+      *reinterpret_cast<uint32_t*>(smem + C::Q_OFFSET + code_offset<C>(n, part * 128 + lane * 4)) = codes;
+      if ((lane & 1) == 0)
+        smem[C::QSF_OFFSET + n * C::ROW_SF + part * 16 + lane / 2] = odd ? (uint8_t)0x7f : (uint8_t)s8;
     }
+    if (part == 0 && lane == 0)
+      reinterpret_cast<float*>(smem + C::COL_OFFSET)[col] = p.scale_log2 * __int_as_float((127 - shift) << 23);
   }
   // rows beyond the terms: zeros
   constexpr int USED = C::CC * kFp4Terms;
-  for (int i = tid; i < (C::N - USED) * C::ROW_SF; i += threads) smem[C::QSF_OFFSET + USED * C::ROW_SF + i] = 0;
-  for (int i = tid; i < (C::N - USED) * (C::D / 32); i += threads)
+  for (int i = warp * 32 + lane; i < (C::N - USED) * C::ROW_SF; i += 256) smem[C::QSF_OFFSET + USED * C::ROW_SF + i] = 0;
+  for (int i = warp * 32 + lane; i < (C::N - USED) * (C::D / 32); i += 256)
     *reinterpret_cast<uint4*>(smem + C::Q_OFFSET + code_offset<C>(USED + i / (C::D / 32), (i % (C::D / 32)) * 16)) =
         make_uint4(0u, 0u, 0u, 0u);
+}
+
+// 16 bytes global -> shared, counted by cp_async_arrive.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+// An arrival on `bar` (one that its count holds) once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // Two e4m3 scales, NaN as zero.
@@ -297,7 +316,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
     if (!C::KVS) prefetch_tensormap(&p.vmap);
 #pragma unroll 1
     for (int s = 0; s < C::NK + C::NV; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 33);  // the codes' byte count, and every copying lane's scales
       // K: the score product's end; V: the 8 PV warps; K = V: both
       mbar_init(&empty[s], C::KVS ? 9 : (s < C::NK ? 1 : 8));
     }
@@ -318,7 +337,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
     __syncwarp();
     named_bar_arrive(4, C::THREADS);
   }
-  if (tid < C::CC) reinterpret_cast<uint32_t*>(smem + C::COL_OFFSET)[tid] = 0u;
   // tensor memory: scores [2] at columns 0 and 64, K scales [2] at 128 and 160, query scales at 192
   if (warp == kMmaWarp) tmem_alloc<1>(tmem_at, 256);
   if (!early) grid_dependency_wait();
@@ -359,7 +377,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
   const uint32_t t_s = tmem, t_sfa = tmem + 128, t_sfb = tmem + 192;
 
   if (tiles > 0 && warp == kCopyWarp) {
-    // ---- copies: lane l takes the 16 tokens l % 8 of a tile; lanes 0-7 K's codes, 8-15 K's scales, 16-31 V's
+    // ---- copies: lane l takes the codes of the 16 tokens l % 8 of a tile (lanes 0-7 K's, 8-15 V's); the scales of
+    // each 16 tokens are 16 bytes a lane, by cp.async: as bulk copies they were
+    // half of all, and the copy engine's rate (~110 cycles a copy) bound the kernel
     const uint64_t policy = l2_evict_first_policy();
     const int blk = lane & 7, kind = lane >> 3;
     bool waited = !early, stop = false;
@@ -399,19 +419,25 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
         if (lane == 0) {
           valid[st] = bits;
           if (bits)
-            mbar_arrive_expect_tx(&full[st], __popc(bits) * (16 * C::D / 2 + 16 * C::ROW_SF) + (v ? 0 : p.stall_bytes));
+            mbar_arrive_expect_tx(&full[st], __popc(bits) * (16 * C::D / 2) + (v ? 0 : p.stall_bytes));
           else
             mbar_arrive(&full[st]);
         }
         __syncwarp();
         uint8_t* item = smem + st * C::ITEM_BYTES;
-        if (ok && (C::KVS ? kind < 2 : (kind >> 1) == v)) {
-          if (kind & 1)
-            bulk_g2s(item + C::CODE_BYTES + blk * 16 * C::ROW_SF, (v ? p.v_sf : p.k_sf) + (size_t)row0 * C::ROW_SF,
-                     16 * C::ROW_SF, &full[st], policy);
-          else
-            tma_load_4d(item + blk * 16 * (C::D / 2), v ? &p.vmap : &p.kmap, 0, 0, 0, row0 / 8, &full[st], policy);
+        if (ok && kind == v)
+          tma_load_4d(item + blk * 16 * (C::D / 2), v ? &p.vmap : &p.kmap, 0, 0, 0, row0 / 8, &full[st], policy);
+        constexpr int LANES = C::ROW_SF;  // 16-byte pieces of 16 tokens' scales
+        const uint8_t* sf = v ? p.v_sf : p.k_sf;
+#pragma unroll
+        for (int k = 0; k < 8; k += 32 / LANES) {
+          const int at = k + lane / LANES;  // the 16 tokens this lane copies a piece of
+          const int row = __shfl_sync(kFullMask, row0, at);
+          if ((bits >> at) & 1u)
+            cp_async16(item + C::CODE_BYTES + at * 16 * C::ROW_SF + (lane % LANES) * 16,
+                       sf + (size_t)row * C::ROW_SF + (lane % LANES) * 16);
         }
+        cp_async_arrive(&full[st]);
         done = C::KVS ? i + 1 : 2 * i + v + 1;
       }
       page = next;
@@ -437,9 +463,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
   }
 
   if (tiles > 0 && warp != kCopyWarp) {
-    // the query's terms, by the softmax and PV warps
-    if (warp < kCopyWarp) {
-      write_query_terms<C>(p, cm, smem, tid, kCopyWarp * 32);
+    // the query's terms, by the PV warps
+    if (warp >= 4 && warp < kCopyWarp) {
+      write_query_terms<C>(p, cm, smem, warp - 4, lane);
       fence_proxy_async_smem();
     }
     named_bar_sync(1, (C::WARPS - 1) * 32);
@@ -612,7 +638,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
       const int qd = (warp - 4) >> 1, part = (warp - 4) & 1;
       const int qh = lane >> 2, r = lane & 3;
       // positions [all_lo, all_hi) are attended by every column
-      const int all_hi = first_hi;
+      const int all_hi = cm.T > 1 ? first_hi : hi;
       const int all_lo = p.window > 0 ? L - cm.T + j_last + 1 - p.window : 0;
       float acc[16][4];
 #pragma unroll
@@ -643,8 +669,25 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
             acc[m][3] *= a1;
           }
         }
+        constexpr int BLOCKS = C::SL == 2 ? 2 : 1;  // 16-token blocks of this warp
+        const int first = C::SL == 2 ? 0 : part, slab = C::SL == 2 ? part : 0;
+        const int ta = t0 + first * 16;
+        const uint32_t want = BLOCKS == 2 ? 3u : 1u;
+        if (((here >> (qd * 2 + first)) & want) == want && ta >= tlo && ta + BLOCKS * 16 <= thi && ta >= all_lo &&
+            ta + BLOCKS * 16 <= all_hi) {
+          // every token is attended by every column
+#pragma unroll
+          for (int k = first; k < first + BLOCKS; ++k) {
+            uint32_t b0 = 0, b1 = 0;
+            if (C::CC == 8 || qh < C::CC) {
+              b0 = *reinterpret_cast<const uint32_t*>(pb + k * 32);
+              b1 = *reinterpret_cast<const uint32_t*>(pb + k * 32 + 16);
+            }
+            pv_block<C>(acc, tile, qd * 32 + k * 16, slab, b0, b1, 15u, false, lane);
+          }
+        } else {
 #pragma unroll 1
-        for (int k = C::SL == 2 ? 0 : part; k < (C::SL == 2 ? 2 : part + 1); ++k) {
+        for (int k = first; k < first + BLOCKS; ++k) {
           const int tk = t0 + k * 16, row0 = qd * 32 + k * 16;
           if (!((here >> (row0 >> 4)) & 1u) || tk >= thi || tk + 16 <= tlo) continue;
           uint32_t b0 = 0, b1 = 0;
@@ -654,16 +697,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
           }
           uint32_t ok = 15u;
           if (tk < tlo || tk + 16 > thi) {
-            const int ta = tk + 2 * r;
-            ok = (uint32_t)(ta >= tlo && ta < thi) | (uint32_t)(ta + 1 >= tlo && ta + 1 < thi) << 1 |
-                 (uint32_t)(ta + 8 >= tlo && ta + 8 < thi) << 2 | (uint32_t)(ta + 9 >= tlo && ta + 9 < thi) << 3;
+            const int tr = tk + 2 * r;
+            ok = (uint32_t)(tr >= tlo && tr < thi) | (uint32_t)(tr + 1 >= tlo && tr + 1 < thi) << 1 |
+                 (uint32_t)(tr + 8 >= tlo && tr + 8 < thi) << 2 | (uint32_t)(tr + 9 >= tlo && tr + 9 < thi) << 3;
           }
           // Tokens that some columns attend and others do not (several query
           // tokens): a NaN there belongs to the former alone, but 0 * NaN is NaN,
           // so it is taken out of the product and put into their sums.
           const bool mixed = p.query_tokens > 1 && (tk + 16 > all_hi || tk < all_lo);
           if (mixed) {
-            const uint8_t* sf = tile + C::CODE_BYTES + row0 * C::ROW_SF + (C::SL == 2 ? part : 0) * 16 + 2 * qh;
+            const uint8_t* sf = tile + C::CODE_BYTES + row0 * C::ROW_SF + slab * 16 + 2 * qh;
 #pragma unroll 1
             for (int j = 0; j < 16; ++j) {
               const uint32_t two = *reinterpret_cast<const uint16_t*>(sf + j * C::ROW_SF);
@@ -683,7 +726,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
               }
             }
           }
-          pv_block<C>(acc, tile, row0, C::SL == 2 ? part : 0, b0, b1, ok, mixed, lane);
+          pv_block<C>(acc, tile, row0, slab, b0, b1, ok, mixed, lane);
+        }
         }
         __syncwarp();
         if (lane == 0) {
