@@ -32,27 +32,30 @@ struct Fp4Cfg {
   static constexpr int NK = KVS ? (D == 512 ? 5 : 10) : (D == 512 ? 2 : 4);
   static constexpr int NV = KVS ? 0 : (D == 512 ? 3 : 6);
   static constexpr int RING_BYTES = (NK + NV) * ITEM_BYTES;
-  // after the last tile, over the ring: the PV warps' sums, float [8][CC][288]
-  // (4 floats of padding every 32 dims), the CTA's result and its log-sum-exps
-  static constexpr int COMB_ROW = 288;
-  static constexpr int OUT_OFFSET = 8 * CC * COMB_ROW * 4;  // float [CC][D]
-  static_assert(OUT_OFFSET + CC * D * 4 <= RING_BYTES, "the end's buffers lie over the ring");
+  static constexpr int CHUNKS = D / 128;   // of 128 dims: V is widened and summed a chunk at a time
+  static constexpr int S_BUFS = N <= 32 ? 2 : 1;  // score buffers in tensor memory
+  static_assert(CC * D * 4 <= RING_BYTES, "the CTA's result, float [CC][D], lies over the ring at the end");
   static constexpr int Q_OFFSET = RING_BYTES;                     // query terms' codes, like a tile's
-  static constexpr int QSF_OFFSET = Q_OFFSET + N * D / 2;         // their scales [N][D / 16]
-  static constexpr int P_ROW = 80;                                // bytes: 32 tokens in f16, spread over the banks
-  static constexpr int P_OFFSET = QSF_OFFSET + N * ROW_SF;        // [4 quarters][2][CC] rows
-  static constexpr int ALPHA_OFFSET = P_OFFSET + 8 * CC * P_ROW;  // float [4][2][8]
-  static constexpr int COL_OFFSET = ALPHA_OFFSET + 4 * 2 * 8 * 4; // float [CC]: score scale of a column
-  static constexpr int ML_OFFSET = COL_OFFSET + CC * 4;           // float2 [4][CC]
-  static constexpr int COEF_OFFSET = ML_OFFSET + 4 * CC * 8;      // float [4][CC], lse [CC]
-  static constexpr int VALID_OFFSET = COEF_OFFSET + 5 * CC * 4;   // u32 [NK + NV]
+  static constexpr int P_OFFSET = Q_OFFSET + N * D / 2;           // 2 x P, tf32: [32 tokens][16 columns][128 B, swizzled]
+  static constexpr int P_BYTES = 16 * kFp4Tile * 4;
+  static constexpr int EYE_OFFSET = P_OFFSET + 2 * P_BYTES;       // the unit matrix in e2m1: 128 rows of 64 B, swizzled
+  static constexpr int EYE_BYTES = 128 * 64;
+  static constexpr int QSF_OFFSET = EYE_OFFSET + EYE_BYTES;       // query terms' scales [N][D / 16]
+  static constexpr int COL_OFFSET = QSF_OFFSET + N * ROW_SF;      // float [CC]: score scale of a column
+  static constexpr int POISON_OFFSET = COL_OFFSET + CC * 4;       // u32 [CC]: 16-dim blocks that are NaN
+  static constexpr int RED_OFFSET = POISON_OFFSET + CC * 4;       // float [4][CC]: the softmax warps' maxima, then sums
+  static constexpr int LSE_OFFSET = RED_OFFSET + 4 * CC * 4;      // float [CC]
+  static constexpr int COEF_OFFSET = LSE_OFFSET + CC * 4;         // float [CC]
+  static constexpr int FAILED_OFFSET = COEF_OFFSET + CC * 4;      // u32: a softmax warp's wait ran out
+  static constexpr int VALID_OFFSET = FAILED_OFFSET + 4;          // u32 [NK + NV]: the 16-token blocks that a slot's tile holds
   static constexpr int BAR_OFFSET = (VALID_OFFSET + (NK + NV) * 4 + 7) / 8 * 8;
-  static constexpr int NUM_BARS = 2 * (NK + NV) + 6 + 16;
+  static constexpr int NUM_BARS = 2 * (NK + NV) + 15;
   static constexpr int SMEM_BYTES = BAR_OFFSET + NUM_BARS * 8 + 16 + 1024;  // (+ 1 KiB to start on a 1024-byte boundary)
-  static constexpr int WARPS = 14;  // 4 softmax, 8 PV, 1 copies, 1 matrix instructions
+  static constexpr int WARPS = 14;
   static constexpr int THREADS = 32 * WARPS;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
-  static_assert(Q_OFFSET % 1024 == 0 && QSF_OFFSET % 16 == 0 && P_OFFSET % 16 == 0 && ML_OFFSET % 8 == 0, "alignment");
+  static_assert(Q_OFFSET % 1024 == 0 && P_OFFSET % 1024 == 0 && EYE_OFFSET % 1024 == 0 && QSF_OFFSET % 16 == 0,
+                "alignment");
 };
 
 // X(id, head_dim, K=V, columns)

@@ -3,27 +3,33 @@
 // block scales once and serves up to CC query rows ("columns") of that KV head.
 //
 // Mathematics: a cached element is e2m1(code) * e4m3(scale of its 16 dims) *
-// 2^exp. Scores S = K q^T are a product of two block-scaled 4-bit operands: the
-// query row is written as kFp4Terms e2m1 terms, each with its own scale per 16
-// dims, the next term taking what the one before left over. A term leaves at
-// most 0.177 of its block's largest, so six leave 2^-14.9 of it (the row is
-// first brought to [2^10, 2^11) by a power of two, so that the last terms'
-// scales still are e4m3 numbers). K then needs no widening at all: the tensor
-// core takes codes and scales as they lie in the cache (tcgen05.mma
-// kind::mxf4nvf4, 128 tokens x CC * terms columns x 64 dims).
-// V's scales lie along the head dims, across the sum over tokens that P V is,
-// so V is widened: codes to f16 pairs of two tokens, times the pair of their
-// scales (exact: 2 and 4 significant bits), and multiplied by mma.sync.
+// 2^exp. All three products of a tile of 128 tokens run on tcgen05, and no
+// cached element passes through the CUDA cores:
+//   S = K q^T    kind::mxf4nvf4 on codes and scales as they lie in the cache. The
+//                query row is written as kFp4Terms e2m1 terms, each with its own
+//                scale per 16 dims, the next taking what the one before left
+//                over. A term leaves at most 0.177 of its block's largest, so six
+//                leave 2^-14.9 of it (the row is first brought to [2^10, 2^11) by
+//                a power of two, so that the last terms' scales still are e4m3
+//                numbers); the terms' scores are summed afterwards;
+//   V^T = I V^T  the same kind with a unit matrix: V widened, scaled and turned,
+//                128 dims at a time, exactly (one term a sum) and as fp32 in
+//                tensor memory, where it is a tf32 operand as it is (two and four
+//                significant bits make at most six);
+//   O^T += V^T P^T  kind::tf32 with V^T out of tensor memory and P from shared
+//                memory.
+// Widening V for mma.sync instead (codes to f16, times their scales) took 200
+// instructions a warp for 16 tokens of 256 dims, 1500 cycles a tile and
+// sub-partition at best and 3500 in place; these products take about 1800 a tile
+// of 512 dims in all, beside everything else.
 //
-// Roles (one CTA an SM): warp 12 copies tiles of 128 tokens (TMA: codes;
-// bulk copies: scales) into the rings; warp 13 issues the score products;
-// warps 0-3 write the tile's K scales to tensor memory, read the scores of
-// their quarter of the tile (a lane a token), keep its running maximum and sum
-// (each quarter its own, joined at the end) and leave P in shared memory as
-// f16; warps 4-11 accumulate P V, two warps a quarter (d 512: a half of the
-// dims each; d 256: 16 of the 32 tokens each).
-// P is held as 2^15 times the probability relative to the running maximum, so
-// that f16 keeps tokens down to 2^-39 of the largest.
+// Softmax without a running rescale: a column's reference is the maximum of the
+// first tile that holds a token it attends, and stays until a score exceeds it
+// by 2^60 (tf32 has fp32's exponents), which rescales the sums.
+//
+// Roles (one CTA an SM): warps 0-3 softmax (a lane a token); 4-7 write the
+// tiles' scales to tensor memory; 8, 9 copy codes (TMA), 10 scales (cp.async);
+// 11, 12, 13 issue the three products. Warps 0-7 read the sums at the end.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -37,7 +43,11 @@
 namespace pd {
 namespace {
 
-constexpr float kPShift = 15.f;
+constexpr float kRefRange = 60.f;  // log2 of how far a score may exceed its column's reference
+// tensor memory columns: scores [S_BUFS][N], scales of V, of the unit matrix, V^T [2][128], sums [CHUNKS][16],
+// scales of K, of the query
+constexpr uint32_t kTmemS = 0, kTmemSfv = 64, kTmemSfi = 96, kTmemVt = 128, kTmemO = 384, kTmemSfk = 448,
+                   kTmemSfq = 480, kTmemCols = 512;
 
 // D[tmem] (+)= A . B over 64 dims, both e2m1 with an e4m3 scale per 16 dims.
 __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
@@ -49,6 +59,15 @@ __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint
       : "memory");
 }
 
+// D[tmem] (+)= A[tmem] . B over 8 tokens, tf32.
+__device__ __forceinline__ void mma_tf32(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+
 // Four bytes of two e2m1 codes -> four f16 pairs (low code in the low half), exact.
 __device__ __forceinline__ void e2m1x8_to_f16x8(uint32_t w, uint32_t (&o)[4]) {
   asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
@@ -57,32 +76,6 @@ __device__ __forceinline__ void e2m1x8_to_f16x8(uint32_t w, uint32_t (&o)[4]) {
       : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
       : "r"(w));
 }
-
-// Four e4m3 bytes -> two f16 pairs, exact.
-__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-}
-
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// The low nibbles of x beside those of y: bytes (x's low code, y's low code).
-__device__ __forceinline__ uint32_t pair_codes(uint32_t x, uint32_t y) { return (x & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u); }
 
 // A float's bits in an order of whole numbers.
 __device__ __forceinline__ int ordered(float x) {
@@ -220,64 +213,8 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Two e4m3 scales, NaN as zero.
-__device__ __forceinline__ uint32_t without_nan(uint32_t s) {
-  if ((s & 0x7fu) == 0x7fu) s &= 0xff00u;
-  if ((s & 0x7f00u) == 0x7f00u) s &= 0xffu;
-  return s;
-}
-
-// Sum over tokens of 16 tokens x 256 dims: rows row0 .. row0 + 15 of a tile of V, its slab `sl`.
-// b0, b1: P of tokens 2 (lane % 4) + {0, 1} and + {8, 9}, column lane / 4.
-// ok: a bit for each of this lane's four tokens (2r, 2r + 1, 2r + 8, 2r + 9) whose row counts; drop: NaN scales are taken
-// as zeros.
-template <class C>
-__device__ __forceinline__ void pv_block(float (&acc)[16][4], const uint8_t* tile, int row0, int sl, uint32_t b0,
-                                         uint32_t b1, uint32_t ok, bool drop, int lane) {
-  const int qh = lane >> 2, r = lane & 3;
-  const uint8_t* g0 = tile + (row0 >> 3) * (C::SL * 1024) + sl * 1024;
-  const uint8_t* g1 = g0 + C::SL * 1024;
-  const int ra = 2 * r, rb = ra + 1;
-  const uint4 xa = *reinterpret_cast<const uint4*>(g0 + ra * 128 + ((qh ^ ra) << 4));
-  const uint4 xb = *reinterpret_cast<const uint4*>(g0 + rb * 128 + ((qh ^ rb) << 4));
-  const uint4 xc = *reinterpret_cast<const uint4*>(g1 + ra * 128 + ((qh ^ ra) << 4));
-  const uint4 xd = *reinterpret_cast<const uint4*>(g1 + rb * 128 + ((qh ^ rb) << 4));
-  // scales of blocks 2 qh, 2 qh + 1 of the slab; a row that does not count has scale 0
-  const uint8_t* sf = tile + C::CODE_BYTES + (row0 + ra) * C::ROW_SF + sl * 16 + 2 * qh;
-  uint32_t sa = *reinterpret_cast<const uint16_t*>(sf), sb = *reinterpret_cast<const uint16_t*>(sf + C::ROW_SF);
-  uint32_t sc = *reinterpret_cast<const uint16_t*>(sf + 8 * C::ROW_SF);
-  uint32_t sd = *reinterpret_cast<const uint16_t*>(sf + 9 * C::ROW_SF);
-  if (ok != 15u) {
-    sa = (ok & 1u) ? sa : 0u;
-    sb = (ok & 2u) ? sb : 0u;
-    sc = (ok & 4u) ? sc : 0u;
-    sd = (ok & 8u) ? sd : 0u;
-  }
-  if (drop) {
-    sa = without_nan(sa);
-    sb = without_nan(sb);
-    sc = without_nan(sc);
-    sd = without_nan(sd);
-  }
-  uint32_t s01[2], s23[2];  // (token, next token) of either block
-  e4m3x4_to_f16x4(__byte_perm(sa, sb, 0x5140), s01[0], s01[1]);
-  e4m3x4_to_f16x4(__byte_perm(sc, sd, 0x5140), s23[0], s23[1]);
-  const uint32_t wa[4] = {xa.x, xa.y, xa.z, xa.w}, wb[4] = {xb.x, xb.y, xb.z, xb.w};
-  const uint32_t wc[4] = {xc.x, xc.y, xc.z, xc.w}, wd[4] = {xd.x, xd.y, xd.z, xd.w};
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    // word w: dims 8 w + 0 .. 7 of the lane's 32; even dims in the low nibbles
-    uint32_t e01[4], o01[4], e23[4], o23[4];
-    e2m1x8_to_f16x8(pair_codes(wa[w], wb[w] << 4), e01);
-    e2m1x8_to_f16x8(pair_codes(wa[w] >> 4, wb[w]), o01);
-    e2m1x8_to_f16x8(pair_codes(wc[w], wd[w] << 4), e23);
-    e2m1x8_to_f16x8(pair_codes(wc[w] >> 4, wd[w]), o23);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      mma_f16(acc[w * 4 + i], mul_f16x2(e01[i], s01[w >> 1]), mul_f16x2(o01[i], s01[w >> 1]),
-              mul_f16x2(e23[i], s23[w >> 1]), mul_f16x2(o23[i], s23[w >> 1]), b0, b1);
-  }
-}
+// Four e4m3 scales: 0x80 in the bytes that are NaN.
+__device__ __forceinline__ uint32_t nan_scales(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
 __device__ __forceinline__ float ld_dsmem_f32(uint32_t addr) {
   float v;
@@ -297,48 +234,55 @@ template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_constant__ Fp4Params p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BAR_OFFSET);
-  uint64_t* full = bars;                       // [NK + NV]: K's ring, then V's
-  uint64_t* empty = full + C::NK + C::NV;      // [NK + NV]
-  uint64_t* sf_ready = empty + C::NK + C::NV;  // [2] K scales in tensor memory
-  uint64_t* s_full = sf_ready + 2;             // [2] scores computed
-  uint64_t* s_empty = s_full + 2;              // [2] scores read
-  uint64_t* p_full = s_empty + 2;              // [4][2]
-  uint64_t* p_empty = p_full + 8;              // [4][2]
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(bars + C::NUM_BARS);
+  constexpr int SB = C::S_BUFS, CH = C::CHUNKS, RINGS = C::NK + C::NV;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFFSET);  // [RINGS]: K's ring, then V's
+  uint64_t* empty = full + RINGS;                                      // [RINGS]
+  uint64_t* sfk_ready = empty + RINGS;                                 // K's scales in tensor memory
+  uint64_t* sfv_ready = sfk_ready + 1;                                 // V's
+  uint64_t* s_full = sfv_ready + 1;                                    // [2] scores computed
+  uint64_t* s_empty = s_full + 2;                                      // [2] scores read
+  uint64_t* vt_full = s_empty + 2;                                     // [2] a chunk of V^T there
+  uint64_t* vt_empty = vt_full + 2;                                    // [2] and used
+  uint64_t* dq_done = vt_empty + 2;                                    // a tile's V^T all there
+  uint64_t* p_full = dq_done + 1;                                      // [2]
+  uint64_t* p_empty = p_full + 2;                                      // [2]: the tile is in the sums
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(full + C::NUM_BARS);
   uint32_t* valid = reinterpret_cast<uint32_t*>(smem + C::VALID_OFFSET);
-  constexpr int kCopyWarp = 12, kMmaWarp = 13;
+  volatile uint32_t* failed_at = reinterpret_cast<uint32_t*>(smem + C::FAILED_OFFSET);
+  uint32_t* poison = reinterpret_cast<uint32_t*>(smem + C::POISON_OFFSET);
+  constexpr int kSfWarp = 4, kCodeWarp = 8, kScaleWarp = 10, kQkWarp = 11, kDqWarp = 12, kPvWarp = 13;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const bool early = p.early_kv != 0 && warp == kCopyWarp;
+  const bool copies = warp >= kCodeWarp && warp <= kScaleWarp;
+  const bool early = p.early_kv != 0 && copies;
 
-  if (tid == kCopyWarp * 32) {
+  if (tid == kCodeWarp * 32) {
     prefetch_tensormap(&p.kmap);
     if (!C::KVS) prefetch_tensormap(&p.vmap);
 #pragma unroll 1
-    for (int s = 0; s < C::NK + C::NV; ++s) {
-      mbar_init(&full[s], 33);  // the codes' byte count, and every copying lane's scales
-      // K: the score product's end; V: the 8 PV warps; K = V: both
-      mbar_init(&empty[s], C::KVS ? 9 : (s < C::NK ? 1 : 8));
+    for (int s = 0; s < RINGS; ++s) {
+      // the codes' byte count (K = V: two warps') and every lane's scales
+      mbar_init(&full[s], (C::KVS ? 2 : 1) + 32);
+      mbar_init(&empty[s], C::KVS ? 2 : 1);  // the products that read the slot
     }
+    mbar_init(sfk_ready, 4);
+    mbar_init(sfv_ready, 4);
+    mbar_init(dq_done, 1);
 #pragma unroll 1
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&sf_ready[s], 4);
       mbar_init(&s_full[s], 1);
       mbar_init(&s_empty[s], 4);
-    }
-#pragma unroll 1
-    for (int s = 0; s < 8; ++s) {
-      mbar_init(&p_full[s], 1);
-      mbar_init(&p_empty[s], 2);
+      mbar_init(&vt_full[s], 1);
+      mbar_init(&vt_empty[s], 1);
+      mbar_init(&p_full[s], 4);
+      mbar_init(&p_empty[s], 1);
     }
     fence_barrier_init();
   }
-  if (warp == kCopyWarp) {
-    __syncwarp();
+  if (warp == kPvWarp) tmem_alloc<1>(tmem_at, kTmemCols);
+  if (copies) {
+    named_bar_sync(5, 3 * 32);
     named_bar_arrive(4, C::THREADS);
   }
-  // tensor memory: scores [2] at columns 0 and 64, K scales [2] at 128 and 160, query scales at 192
-  if (warp == kMmaWarp) tmem_alloc<1>(tmem_at, 256);
   if (!early) grid_dependency_wait();
 
   const Columns<C> cm(p);
@@ -363,117 +307,275 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
   const int thi = (int)(piece_hi < hi ? piece_hi : hi);
   const int t_base = (tlo / 16) * 16;
   const int tiles = thi > tlo ? (thi - t_base + kFp4Tile - 1) / kFp4Tile : 0;
-
-  float* my_lse = reinterpret_cast<float*>(smem + C::COEF_OFFSET) + 4 * C::CC;  // [CC]
-  float* my_out = reinterpret_cast<float*>(smem + C::OUT_OFFSET);                // [CC][D]
   if (!early) grid_launch_dependents();
+
+  float* red = reinterpret_cast<float*>(smem + C::RED_OFFSET);     // [4][CC]
+  float* my_lse = reinterpret_cast<float*>(smem + C::LSE_OFFSET);  // [CC]
+  float* coef = reinterpret_cast<float*>(smem + C::COEF_OFFSET);   // [CC]
+  float* my_out = reinterpret_cast<float*>(smem);                  // [CC][D], over the ring
   uint32_t tmem = 0;
-  if (warp != kCopyWarp) {
+  if (!copies) {
     // the barriers and tensor memory are there (the copies do not wait for the other warps)
     named_bar_sync(4, C::THREADS);
     tmem_fence_after();
     tmem = *tmem_at;
   }
-  const uint32_t t_s = tmem, t_sfa = tmem + 128, t_sfb = tmem + 192;
+  const uint32_t quarter = (uint32_t)(warp & 3) << 21;  // this warp's lanes of tensor memory
 
-  if (tiles > 0 && warp == kCopyWarp) {
-    // ---- copies: lane l takes the codes of the 16 tokens l % 8 of a tile (lanes 0-7 K's, 8-15 V's); the scales of
-    // each 16 tokens are 16 bytes a lane, by cp.async: as bulk copies they were
-    // half of all, and the copy engine's rate (~110 cycles a copy) bound the kernel
-    const uint64_t policy = l2_evict_first_policy();
-    const int blk = lane & 7, kind = lane >> 3;
-    bool waited = !early, stop = false;
+  if (copies) {
+    bool waited = !early;
     uint32_t err_bits = 0;
-    // rows from here on may still be written by the kernel in front
-    const int fresh_from = L - p.query_tokens;
-    auto page_of = [&](int i) {
-      const int t = t_base + i * kFp4Tile + blk * 16;
-      return t < thi ? __ldg(table + t / p.page_size) : -1;
-    };
-    int page = page_of(0);
-    int done = 0;  // items whose copies went out
+    if (tiles > 0) {
+      // ---- copies. Rows four tiles at a time: lane l the 16 tokens 16 l .. of
+      // them, its page id fetched four tiles ahead (one tile ahead, its latency
+      // bound the kernel: 4 x 32768 tokens 77 -> 62 us).
+      const uint64_t policy = l2_evict_first_policy();
+      const int mine = warp - kCodeWarp;  // 0: K's codes, 1: V's (K = V: the lower and the upper half), 2: scales
+      const int fresh_from = L - p.query_tokens;  // rows from here on may still be written by the kernel in front
+      auto page_of = [&](int i) {
+        const int t = t_base + i * kFp4Tile + lane * 16;
+        return t < thi ? __ldg(table + t / p.page_size) : -1;
+      };
+      int page = page_of(0), rows = -1;
+      bool stop = false;
+      int done = 0;  // tiles whose copies went out
 #pragma unroll 1
-    for (int i = 0; i < tiles && !stop; ++i) {
-      const int next = i + 1 < tiles ? page_of(i + 1) : -1;
-      const int t = t_base + i * kFp4Tile + blk * 16;
-      const bool there = t < thi, ok = there && (unsigned)page < (unsigned)p.num_pages;
-      if (there && !ok) err_bits |= kErrBadPage;
-      const uint32_t bits = __ballot_sync(kFullMask, ok) & 0xffu;
-      if (!waited && (i >= C::NK || (!C::KVS && i >= C::NV) || t_base + (i + 1) * kFp4Tile > fresh_from)) {
-        grid_dependency_wait();
-        grid_launch_dependents();
-        waited = true;
-      }
-      const int row0 = ok ? (page * p.num_kv_heads + g) * p.page_size + t % p.page_size : 0;
+      for (int i = 0; i < tiles && !stop; ++i) {
+        if ((i & 3) == 0) {
+          const int t = t_base + i * kFp4Tile + lane * 16;
+          const bool here = (unsigned)page < (unsigned)p.num_pages;
+          if (t < thi && !here) err_bits |= kErrBadPage;
+          rows = t < thi && here ? (page * p.num_kv_heads + g) * p.page_size + t % p.page_size : -1;
+          page = page_of(i + 4);
+        }
+        const int row0 = __shfl_sync(kFullMask, rows, (i & 3) * 8 + (lane & 7));
+        const uint32_t bits = __ballot_sync(kFullMask, row0 >= 0) & 0xffu;
+        if (!waited && (i >= C::NK || (!C::KVS && i >= C::NV) || t_base + (i + 1) * kFp4Tile > fresh_from)) {
+          grid_dependency_wait();
+          grid_launch_dependents();
+          waited = true;
+        }
 #pragma unroll
-      for (int v = 0; v < (C::KVS ? 1 : 2); ++v) {
-        const int n = v ? C::NV : C::NK, st = (v ? C::NK : 0) + i % n, round = i / n;
-        if (round > 0) {
-          const bool freed = mbar_wait(&empty[st], (round - 1) & 1);
-          if (__any_sync(kFullMask, !freed)) {
-            err_bits |= kErrTimeout;
-            stop = true;
-            break;
+        for (int v = 0; v < (C::KVS ? 1 : 2); ++v) {
+          if (!C::KVS && mine != 2 && mine != v) continue;
+          const int n = v ? C::NV : C::NK, st = (v ? C::NK : 0) + i % n, round = i / n;
+          if (round > 0) {
+            const bool freed = mbar_wait(&empty[st], (round - 1) & 1);
+            if (__any_sync(kFullMask, !freed)) {
+              err_bits |= kErrTimeout;
+              stop = true;
+              break;
+            }
+          }
+          uint8_t* item = smem + st * C::ITEM_BYTES;
+          if (mine < 2) {
+            const uint32_t part = C::KVS ? (mine ? bits & 0xf0u : bits & 0x0fu) : bits;
+            if (lane == 0) {
+              if (!C::KVS || mine == 0) valid[st] = bits;
+              if (part)
+                mbar_arrive_expect_tx(&full[st], __popc(part) * (16 * C::D / 2) + (mine == 0 ? p.stall_bytes : 0));
+              else
+                mbar_arrive(&full[st]);
+            }
+            __syncwarp();
+            if (lane < 8 && ((part >> lane) & 1u))
+              tma_load_4d(item + lane * 16 * (C::D / 2), v ? &p.vmap : &p.kmap, 0, 0, 0, row0 / 8, &full[st], policy);
+          } else {
+            // 16 bytes a lane (as bulk copies these would be half of all copies)
+            constexpr int LANES = C::ROW_SF;  // 16-byte pieces of 16 tokens' scales
+            const uint8_t* sf = v ? p.v_sf : p.k_sf;
+#pragma unroll
+            for (int k = 0; k < 8; k += 32 / LANES) {
+              const int at = k + lane / LANES;  // the 16 tokens this lane copies a piece of
+              const int row = __shfl_sync(kFullMask, row0, at);
+              if ((bits >> at) & 1u)
+                cp_async16(item + C::CODE_BYTES + at * 16 * C::ROW_SF + (lane % LANES) * 16,
+                           sf + (size_t)row * C::ROW_SF + (lane % LANES) * 16);
+            }
+            cp_async_arrive(&full[st]);
           }
         }
-        if (lane == 0) {
-          valid[st] = bits;
-          if (bits)
-            mbar_arrive_expect_tx(&full[st], __popc(bits) * (16 * C::D / 2) + (v ? 0 : p.stall_bytes));
-          else
-            mbar_arrive(&full[st]);
-        }
-        __syncwarp();
-        uint8_t* item = smem + st * C::ITEM_BYTES;
-        if (ok && kind == v)
-          tma_load_4d(item + blk * 16 * (C::D / 2), v ? &p.vmap : &p.kmap, 0, 0, 0, row0 / 8, &full[st], policy);
-        constexpr int LANES = C::ROW_SF;  // 16-byte pieces of 16 tokens' scales
-        const uint8_t* sf = v ? p.v_sf : p.k_sf;
-#pragma unroll
-        for (int k = 0; k < 8; k += 32 / LANES) {
-          const int at = k + lane / LANES;  // the 16 tokens this lane copies a piece of
-          const int row = __shfl_sync(kFullMask, row0, at);
-          if ((bits >> at) & 1u)
-            cp_async16(item + C::CODE_BYTES + at * 16 * C::ROW_SF + (lane % LANES) * 16,
-                       sf + (size_t)row * C::ROW_SF + (lane % LANES) * 16);
-        }
-        cp_async_arrive(&full[st]);
-        done = C::KVS ? i + 1 : 2 * i + v + 1;
+        if (!stop) done = i + 1;
       }
-      page = next;
+      // no copy may still be landing when the shared memory is used for something else
+      const unsigned long long deadline = global_timer_ns() + kWaitTimeoutNs;
+      for (int s = lane; s < RINGS; s += 32) {
+        const int n = s < C::NK ? C::NK : C::NV, at = s < C::NK ? s : s - C::NK;
+        if (at >= done || (!C::KVS && mine != 2 && (s >= C::NK) != (mine == 1))) continue;
+        const int last = at + n * ((done - 1 - at) / n);
+        if (!mbar_wait_until(&full[s], (last / n) & 1, deadline)) err_bits |= kErrTimeout;
+      }
     }
     if (!waited) {
       grid_dependency_wait();
       grid_launch_dependents();
     }
-    // no copy may still be landing when the shared memory is used for something else
-    const unsigned long long deadline = global_timer_ns() + kWaitTimeoutNs;
-    const int k_items = C::KVS ? done : (done + 1) / 2, v_items = C::KVS ? 0 : done / 2;
-    for (int s = lane; s < C::NK + C::NV; s += 32) {
-      const int n = s < C::NK ? C::NK : C::NV, at = s < C::NK ? s : s - C::NK, items = s < C::NK ? k_items : v_items;
-      if (at >= items) continue;
-      const int last = at + n * ((items - 1 - at) / n);
-      if (!mbar_wait_until(&full[s], (last / n) & 1, deadline)) err_bits |= kErrTimeout;
-    }
     err_bits = __reduce_or_sync(kFullMask, err_bits);
     if (lane == 0 && err_bits) atomicOr(p.err, err_bits);
-  } else if (early) {
-    grid_dependency_wait();
-    grid_launch_dependents();
-  }
-
-  if (tiles > 0 && warp != kCopyWarp) {
-    // the query's terms, by the PV warps
-    if (warp >= 4 && warp < kCopyWarp) {
-      write_query_terms<C>(p, cm, smem, warp - 4, lane);
+  } else if (tiles > 0) {
+    bool good = true;
+    if (warp < 8) {
+      // the query's terms, the unit matrix and P's unused rows
+      write_query_terms<C>(p, cm, smem, warp, lane);
+      for (int i = tid; i < C::EYE_BYTES / 16; i += 256) {
+        // 16 bytes of row m: dims 32 c ..; its one lies at dim m (e2m1 1.0 is 2)
+        const int m = i >> 2, c = (i & 3) ^ ((m >> 1) & 3);
+        const uint32_t one = (m >> 5) == c ? 2u << (4 * (m & 7)) : 0u;
+        const int word = (m >> 3) & 3;
+        *reinterpret_cast<uint4*>(smem + C::EYE_OFFSET + (m >> 3) * 512 + (m & 7) * 64 + (i & 3) * 16) =
+            make_uint4(word == 0 ? one : 0u, word == 1 ? one : 0u, word == 2 ? one : 0u, word == 3 ? one : 0u);
+      }
+      for (int i = tid; i < 2 * C::P_BYTES / 16; i += 256) {
+        const int row = ((i >> 6) & 1) * 8 + ((i >> 3) & 7);  // [slab][2 groups][8 rows][128 B]
+        if (row >= C::CC) *reinterpret_cast<uint4*>(smem + C::P_OFFSET + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (tid < C::CC) poison[tid] = 0u;
+      if (tid == 0) *failed_at = 0u;
       fence_proxy_async_smem();
     }
-    named_bar_sync(1, (C::WARPS - 1) * 32);
-    if (warp < 4) {
-      // ---- softmax warps: rows 32 warp .. + 31 of every tile
-      const uint32_t quarter = (uint32_t)warp << 21;  // this warp's lanes of tensor memory
+    named_bar_sync(1, 11 * 32);  // warps 0-7 and the products'
+
+    if (warp < kSfWarp) {
+      // ---- softmax: rows 32 warp .. + 31 of every tile
+      float col_mul[C::CC], ref[C::CC], sum[C::CC];
+      int col_hi[C::CC], col_lo[C::CC];
+#pragma unroll
+      for (int c = 0; c < C::CC; ++c) {
+        col_mul[c] = reinterpret_cast<const float*>(smem + C::COL_OFFSET)[c];
+        col_hi[c] = cm.valid(c) ? min(thi, L - cm.T + cm.token(c) + 1) : 0;
+        col_lo[c] = max(tlo, (p.window > 0 && cm.valid(c)) ? L - cm.T + cm.token(c) + 1 - p.window : 0);
+        ref[c] = -INFINITY;
+        sum[c] = 0.f;
+      }
+      const uint32_t p_at = smem_u32(smem + C::P_OFFSET) + warp * 2048 + (lane & 3) * 4;
+      // whether a tile's 16-token blocks have a page: lane l block l of four tiles, as the copies take them
+      auto page_of = [&](int i) {
+        const int t = t_base + i * kFp4Tile + lane * 16;
+        return t < thi ? __ldg(table + t / p.page_size) : -1;
+      };
+      int page = page_of(0);
+      uint32_t blocks = 0;
+      // The four warps leave together: one whose wait ran out says so at the next
+      // tile's barrier.
+      auto give_up = [&]() {
+        good = false;
+        if (lane == 0) *failed_at = 1u;
+        __syncwarp();
+      };
+#pragma unroll 1
+      for (int i = 0; i < tiles; ++i) {
+        const int sbuf = i % SB, buf = i & 1;
+        if ((i & 3) == 0) {
+          blocks = __ballot_sync(kFullMask, (unsigned)page < (unsigned)p.num_pages);
+          page = page_of(i + 4);
+        }
+        if (good) {
+          const bool scored = mbar_wait(&s_full[sbuf], (i / SB) & 1);
+          if (__any_sync(kFullMask, !scored)) give_up();
+        }
+        tmem_fence_after();
+        float s[C::CC];
+        {
+          uint32_t w[kFp4Terms * C::CC / 8][8];
+#pragma unroll
+          for (int k = 0; k < kFp4Terms * C::CC / 8; ++k) tmem_ld(w[k], tmem + kTmemS + sbuf * C::N + quarter + k * 8);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < C::CC; ++c) {
+            float x = 0.f;
+#pragma unroll
+            for (int t = kFp4Terms - 1; t >= 0; --t) x += __uint_as_float(w[(t * C::CC + c) / 8][(t * C::CC + c) % 8]);
+            s[c] = x * col_mul[c];
+          }
+        }
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_empty[sbuf]);
+        const int row = warp * 32 + lane, t = t_base + i * kFp4Tile + row;
+        const bool ok = (blocks >> ((i & 3) * 8 + (row >> 4))) & 1u;
+        bool above = !good;
+#pragma unroll
+        for (int c = 0; c < C::CC; ++c) {
+          if (!(ok && t >= col_lo[c] && t < col_hi[c])) s[c] = -INFINITY;
+          above = above || s[c] > ref[c] + kRefRange;
+        }
+        if (named_bar_or(2, 128, above)) {
+          if (*failed_at) {
+            good = false;
+            break;
+          }
+          // new references: the tile's maximum, where that is out of reach
+#pragma unroll
+          for (int c = 0; c < C::CC; ++c) {
+            const int top = __reduce_max_sync(kFullMask, ordered(isnan(s[c]) ? -INFINITY : s[c]));
+            if (lane == 0) red[warp * C::CC + c] = unordered(top);
+          }
+          named_bar_sync(2, 128);
+          float f[C::CC];
+          bool held = false;
+#pragma unroll
+          for (int c = 0; c < C::CC; ++c) {
+            const float top = fmaxf(fmaxf(red[c], red[C::CC + c]), fmaxf(red[2 * C::CC + c], red[3 * C::CC + c]));
+            const bool up = top > ref[c] + kRefRange;
+            f[c] = up && ref[c] != -INFINITY ? ex2(ref[c] - top) : 1.f;
+            held = held || f[c] != 1.f;
+            sum[c] *= f[c];
+            if (up) ref[c] = top;
+          }
+          named_bar_sync(2, 128);  // red may be written again
+          if (held) {
+            // sums that hold something: rescaled once the tiles before are in them
+            const bool summed = mbar_wait(&p_empty[(i - 1) & 1], ((i - 1) >> 1) & 1);
+            if (__any_sync(kFullMask, !summed)) give_up();
+            tmem_fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < CH; ++c0) {
+              uint32_t o[8];
+              tmem_ld(o, tmem + kTmemO + c0 * 16 + quarter);
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < C::CC; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f[c]);
+              tmem_st(tmem + kTmemO + c0 * 16 + quarter, o);
+            }
+            tmem_wait_st();
+            tmem_fence_before();
+          }
+        }
+        if (i >= 2) {
+          const bool freed = mbar_wait(&p_empty[buf], ((i >> 1) - 1) & 1);
+          if (__any_sync(kFullMask, !freed)) give_up();
+        }
+#pragma unroll
+        for (int c = 0; c < C::CC; ++c) {
+          // rounded to tf32 here, to nearest (the product would cut it off); the sum takes what the product takes
+          uint32_t w;
+          const float e = ex2(s[c] - (ref[c] == -INFINITY ? 0.f : ref[c]));
+          asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(w) : "f"(e));
+          sum[c] += __uint_as_float(w);
+          const uint32_t at = p_at + buf * C::P_BYTES + (c >> 3) * 1024 + (c & 7) * 128 + (((lane >> 2) ^ (c & 7)) << 4);
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(w) : "memory");
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[buf]);
+      }
+      if (!good && lane == 0) atomicOr(p.err, kErrTimeout);
+#pragma unroll
+      for (int c = 0; c < C::CC; ++c) {
+        float l = sum[c];
+#pragma unroll
+        for (int m = 16; m; m >>= 1) l += __shfl_xor_sync(kFullMask, l, m);
+        if (lane == 0) red[warp * C::CC + c] = l;
+        if (tid == 0) my_lse[c] = ref[c];
+      }
+    } else if (warp < kCodeWarp) {
+      // ---- scales into tensor memory: lane l, column 4 k + j holds the 4 scales of row l + 32 j, dims 64 k ..;
+      // every quarter of the lanes all rows'
       {
-        // the query terms' scales: lane l, column 4 k + j: the 4 bytes of row l + 32 j, dims 64 k .. 64 k + 63
+        uint32_t one[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) one[k] = 0x38383838u;  // e4m3 1.0
+        tmem_st(tmem + kTmemSfi + quarter, one);
 #pragma unroll
         for (int k0 = 0; k0 < C::KSTEPS; k0 += 2) {
           uint32_t r8[8];
@@ -484,131 +586,104 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
                                                                     (k0 + (i >> 2)) * 4)
                                : 0u;
           }
-          tmem_st(t_sfb + quarter + k0 * 4, r8);
+          tmem_st(tmem + kTmemSfq + quarter + k0 * 4, r8);
         }
       }
-      // K scales of tile i into tensor memory; every quarter of its lanes holds all 128 rows'
-      bool good = true;
-      uint32_t here_next = 0;  // the 16-token blocks that the tile holds
-      auto put_scales = [&](int i) {
-        const int st = i % C::NK;
-        const bool landed = mbar_wait(&full[st], (i / C::NK) & 1);
-        if (__any_sync(kFullMask, !landed)) {
-          good = false;
-          return;
+      auto put = [&](const uint8_t* sf, uint32_t at, bool v, uint32_t here, int t0) {
+        uint32_t x[C::KSTEPS * 4];  // [64 dims][row group]
+#pragma unroll
+        for (int k0 = 0; k0 < C::KSTEPS; k0 += 4) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint4 w = *reinterpret_cast<const uint4*>(sf + (lane + 32 * j) * C::ROW_SF + k0 * 4);
+            x[k0 * 4 + j] = w.x;
+            x[k0 * 4 + 4 + j] = w.y;
+            x[k0 * 4 + 8 + j] = w.z;
+            x[k0 * 4 + 12 + j] = w.w;
+          }
         }
-        const uint8_t* sf = smem + st * C::ITEM_BYTES + C::CODE_BYTES;
+        if (v) {
+          // V's rows that do not count have scale 0: their probabilities are 0, but 0 * NaN is NaN
+          if (!(here == 0xffu && t0 >= tlo && t0 + kFp4Tile <= thi)) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int row = lane + 32 * j, t = t0 + row;
+              if (((here >> (row >> 4)) & 1u) && t >= tlo && t < thi) continue;
+#pragma unroll
+              for (int k = 0; k < C::KSTEPS; ++k) x[k * 4 + j] = 0u;
+            }
+          }
+          // A NaN block would spread over the unit matrix's zeros to other dims
+          // (and, of a token that only some of several query tokens attend, to the
+          // others): it is taken out and marked for the results it belongs to.
+          uint32_t bad = 0;
+#pragma unroll
+          for (int k = 0; k < C::KSTEPS * 4; ++k) bad |= nan_scales(x[k]);
+          if (__any_sync(kFullMask, bad != 0u)) {
+#pragma unroll
+            for (int k = 0; k < C::KSTEPS * 4; ++k) {
+              const uint32_t nan = nan_scales(x[k]);
+              if (!nan) continue;
+              x[k] &= ~((nan >> 7) * 0xffu);
+              if (warp != kSfWarp) continue;
+              const int t = t0 + lane + 32 * (k & 3);
+              for (int c = 0; c < C::CC && cm.valid(c); ++c) {
+                const int end = L - cm.T + cm.token(c) + 1;
+                if (t >= end || (p.window > 0 && t < end - p.window)) continue;
+                for (int y = 0; y < 4; ++y)
+                  if ((nan >> (8 * y + 7)) & 1u) atomicOr(&poison[c], 1u << ((k >> 2) * 4 + y));
+              }
+            }
+          }
+        }
 #pragma unroll
         for (int k0 = 0; k0 < C::KSTEPS; k0 += 4) {
           uint32_t r16[16];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint4 w = *reinterpret_cast<const uint4*>(sf + (lane + 32 * j) * C::ROW_SF + k0 * 4);
-            r16[j] = w.x;
-            r16[4 + j] = w.y;
-            r16[8 + j] = w.z;
-            r16[12 + j] = w.w;
-          }
-          tmem_st(t_sfa + (i & 1) * 32 + quarter + k0 * 4, r16);
+          for (int q = 0; q < 16; ++q) r16[q] = x[k0 * 4 + q];
+          tmem_st(at + k0 * 4, r16);
         }
-        here_next = valid[st];
         tmem_wait_st();
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sf_ready[i & 1]);
       };
-      put_scales(0);
-      float col_mul[C::CC];
-      int col_hi[C::CC], col_lo[C::CC];
-      float m_run[C::CC], l_run[C::CC];
-#pragma unroll
-      for (int c = 0; c < C::CC; ++c) {
-        col_mul[c] = reinterpret_cast<const float*>(smem + C::COL_OFFSET)[c];
-        col_hi[c] = cm.valid(c) ? min(thi, L - cm.T + cm.token(c) + 1) : 0;
-        col_lo[c] = max(tlo, (p.window > 0 && cm.valid(c)) ? L - cm.T + cm.token(c) + 1 - p.window : 0);
-        m_run[c] = -INFINITY;
-        l_run[c] = 0.f;
-      }
 #pragma unroll 1
-      for (int i = 0; i < tiles && good; ++i) {
-        const int buf = i & 1;
-        const uint32_t here = here_next;
-        // the next tile's scales first, if they are there already
-        bool ahead = i + 1 < tiles && mbar_test(&full[(i + 1) % C::NK], ((i + 1) / C::NK) & 1);
-        ahead = __all_sync(kFullMask, ahead);
-        if (ahead) put_scales(i + 1);
-        const bool scored = mbar_wait(&s_full[buf], (i >> 1) & 1);
-        if (__any_sync(kFullMask, !scored)) {
+      for (int i = 0; i < tiles; ++i) {
+        // K's, once the product before has read the last tile's
+        const int st = i % C::NK;
+        bool ready = mbar_wait(&full[st], (i / C::NK) & 1);
+        if (ready && i > 0) ready = mbar_wait(&s_full[(i - 1) % SB], ((i - 1) / SB) & 1);
+        if (__any_sync(kFullMask, !ready)) {
           good = false;
           break;
         }
         tmem_fence_after();
-        float s[C::CC];
-        {
-          uint32_t w[kFp4Terms * C::CC / 8][8];
-#pragma unroll
-          for (int k = 0; k < kFp4Terms * C::CC / 8; ++k) tmem_ld(w[k], t_s + buf * 64 + quarter + k * 8);
-          tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < C::CC; ++c) {
-            float sum = 0.f;
-#pragma unroll
-            for (int t = kFp4Terms - 1; t >= 0; --t)
-              sum += __uint_as_float(w[(t * C::CC + c) / 8][(t * C::CC + c) % 8]);
-            s[c] = sum * col_mul[c];
-          }
+        put(smem + st * C::ITEM_BYTES + C::CODE_BYTES, tmem + kTmemSfk + quarter, false, 0u, 0);
+        if (lane == 0) mbar_arrive(sfk_ready);
+        // V's likewise
+        const int n = C::KVS ? C::NK : C::NV, sv = (C::KVS ? 0 : C::NK) + i % n;
+        ready = C::KVS || mbar_wait(&full[sv], (i / n) & 1);
+        if (ready && i > 0) ready = mbar_wait(dq_done, (i - 1) & 1);
+        if (__any_sync(kFullMask, !ready)) {
+          good = false;
+          break;
         }
-        tmem_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_empty[buf]);
-        const int row = warp * 32 + lane, t = t_base + i * kFp4Tile + row;
-        const bool ok = (here >> (row >> 4)) & 1u;
-        float pr[C::CC], alpha[C::CC];
-#pragma unroll
-        for (int c = 0; c < C::CC; ++c) {
-          if (!(ok && t >= col_lo[c] && t < col_hi[c])) s[c] = -INFINITY;
-          const float mn = fmaxf(m_run[c], unordered(__reduce_max_sync(kFullMask, ordered(s[c]))));
-          alpha[c] = mn == -INFINITY ? 1.f : ex2(m_run[c] - mn);
-          pr[c] = ex2(s[c] - (mn == -INFINITY ? 0.f : mn) + kPShift);
-          l_run[c] = fmaf(l_run[c], alpha[c], pr[c]);
-          m_run[c] = mn;
-        }
-        if (i >= 2) {
-          const bool freed = mbar_wait(&p_empty[warp * 2 + buf], ((i >> 1) - 1) & 1);
-          if (__any_sync(kFullMask, !freed)) {
-            good = false;
-            break;
-          }
-        }
-        uint8_t* pb = smem + C::P_OFFSET + (warp * 2 + buf) * C::CC * C::P_ROW + lane * 2;
-        float* al = reinterpret_cast<float*>(smem + C::ALPHA_OFFSET) + (warp * 2 + buf) * 8;
-#pragma unroll
-        for (int c = 0; c < C::CC; ++c) {
-          *reinterpret_cast<__half*>(pb + c * C::P_ROW) = __float2half_rn(pr[c]);
-          if (lane == c) al[c] = alpha[c];
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[warp * 2 + buf]);
-        if (!ahead && i + 1 < tiles) put_scales(i + 1);
+        tmem_fence_after();
+        const uint32_t here = valid[sv];
+        const int t0 = t_base + i * kFp4Tile;
+        put(smem + sv * C::ITEM_BYTES + C::CODE_BYTES, tmem + kTmemSfv + quarter, true, here, t0);
+        if (lane == 0) mbar_arrive(sfv_ready);
       }
       if (!good && lane == 0) atomicOr(p.err, kErrTimeout);
-#pragma unroll
-      for (int c = 0; c < C::CC; ++c) {
-        float l = l_run[c];
-#pragma unroll
-        for (int m = 16; m; m >>= 1) l += __shfl_xor_sync(kFullMask, l, m);
-        if (lane == 0) reinterpret_cast<float2*>(smem + C::ML_OFFSET)[warp * C::CC + c] = make_float2(m_run[c], l);
-      }
-    } else if (warp == kMmaWarp) {
-      // ---- score products
-      constexpr uint32_t kIdesc = (1u << 7) | (1u << 10) | ((uint32_t)(C::N / 8) << 17) | (8u << 24);  // e2m1 x e2m1, e4m3 scales
+    } else if (warp == kQkWarp) {
+      // ---- S = K q^T
+      constexpr uint32_t kIdesc = (1u << 7) | (1u << 10) | ((uint32_t)(C::N / 8) << 17) | (8u << 24);  // e2m1, e4m3 scales
       int issued = 0;
-      bool good = true;
 #pragma unroll 1
       for (int i = 0; i < tiles; ++i) {
-        const int st = i % C::NK, buf = i & 1;
-        bool ready = mbar_wait(&full[st], (i / C::NK) & 1) && mbar_wait(&sf_ready[buf], (i >> 1) & 1);
-        if (ready && i >= 2) ready = mbar_wait(&s_empty[buf], ((i >> 1) - 1) & 1);
+        const int st = i % C::NK, sbuf = i % SB;
+        bool ready = mbar_wait(&full[st], (i / C::NK) & 1) && mbar_wait(sfk_ready, i & 1);
+        if (ready && i >= SB) ready = mbar_wait(&s_empty[sbuf], (i / SB - 1) & 1);
         if (__any_sync(kFullMask, !ready)) {
           good = false;
           break;
@@ -619,10 +694,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
 #pragma unroll
           for (int k = 0; k < C::KSTEPS; ++k) {
             const uint32_t off = (k >> 2) * 1024 + (k & 3) * 32;
-            mma_fp4(t_s + buf * 64, smem_desc(a + off, 0, C::SL * 1024), smem_desc(q + off, 0, C::SL * 1024), kIdesc,
-                    t_sfa + buf * 32 + k * 4, t_sfb + k * 4, k > 0);
+            mma_fp4(tmem + kTmemS + sbuf * C::N, smem_desc(a + off, 0, C::SL * 1024), smem_desc(q + off, 0, C::SL * 1024),
+                    kIdesc, tmem + kTmemSfk + k * 4, tmem + kTmemSfq + k * 4, k > 0);
           }
-          mma_commit<1>(&s_full[buf]);
+          mma_commit<1>(&s_full[sbuf]);
           mma_commit<1>(&empty[st]);
         }
         __syncwarp();
@@ -630,176 +705,137 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
       }
       if (!good) {
         // what was issued ends before its operands and its result are used for something else
-        if (issued > 0) mbar_wait(&s_full[(issued - 1) & 1], ((issued - 1) >> 1) & 1);
+        if (issued > 0) mbar_wait(&s_full[(issued - 1) % SB], ((issued - 1) / SB) & 1);
         if (lane == 0) atomicOr(p.err, kErrTimeout);
       }
-    } else {
-      // ---- PV warps
-      const int qd = (warp - 4) >> 1, part = (warp - 4) & 1;
-      const int qh = lane >> 2, r = lane & 3;
-      // positions [all_lo, all_hi) are attended by every column
-      const int all_hi = cm.T > 1 ? first_hi : hi;
-      const int all_lo = p.window > 0 ? L - cm.T + j_last + 1 - p.window : 0;
-      float acc[16][4];
-#pragma unroll
-      for (int m = 0; m < 16; ++m)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) acc[m][k] = 0.f;
-      bool good = true;
+    } else if (warp == kDqWarp) {
+      // ---- V^T = I V^T, a chunk of 128 dims after another
+      constexpr uint32_t kIdesc = (1u << 7) | (1u << 10) | ((uint32_t)(kFp4Tile / 8) << 17) | (8u << 24);
+      const uint32_t eye = smem_u32(smem + C::EYE_OFFSET);
+      int issued = 0;
 #pragma unroll 1
-      for (int i = 0; i < tiles; ++i) {
-        const int n = C::KVS ? C::NK : C::NV, st = (C::KVS ? 0 : C::NK) + i % n, buf = i & 1;
-        const bool ready = mbar_wait(&full[st], (i / n) & 1) && mbar_wait(&p_full[qd * 2 + buf], (i >> 1) & 1);
+      for (int i = 0; i < tiles && good; ++i) {
+        const int n = C::KVS ? C::NK : C::NV, st = (C::KVS ? 0 : C::NK) + i % n;
+        const bool ready = mbar_wait(&full[st], (i / n) & 1) && mbar_wait(sfv_ready, i & 1);
         if (__any_sync(kFullMask, !ready)) {
           good = false;
           break;
         }
-        const uint8_t* tile = smem + st * C::ITEM_BYTES;
-        const uint32_t here = valid[st];
-        const int t0 = t_base + i * kFp4Tile + qd * 32;
-        const uint8_t* pb = smem + C::P_OFFSET + (qd * 2 + buf) * C::CC * C::P_ROW + qh * C::P_ROW + r * 4;
-        const float* al = reinterpret_cast<const float*>(smem + C::ALPHA_OFFSET) + (qd * 2 + buf) * 8;
-        const float a0 = 2 * r < C::CC ? al[2 * r] : 1.f, a1 = 2 * r < C::CC ? al[2 * r + 1] : 1.f;
-        if (__any_sync(kFullMask, a0 != 1.f || a1 != 1.f)) {
+        tmem_fence_after();
+        const uint32_t v = smem_u32(smem + st * C::ITEM_BYTES);
 #pragma unroll
-          for (int m = 0; m < 16; ++m) {
-            acc[m][0] *= a0;
-            acc[m][1] *= a1;
-            acc[m][2] *= a0;
-            acc[m][3] *= a1;
-          }
-        }
-        constexpr int BLOCKS = C::SL == 2 ? 2 : 1;  // 16-token blocks of this warp
-        const int first = C::SL == 2 ? 0 : part, slab = C::SL == 2 ? part : 0;
-        const int ta = t0 + first * 16;
-        const uint32_t want = BLOCKS == 2 ? 3u : 1u;
-        if (((here >> (qd * 2 + first)) & want) == want && ta >= tlo && ta + BLOCKS * 16 <= thi && ta >= all_lo &&
-            ta + BLOCKS * 16 <= all_hi) {
-          // every token is attended by every column
-#pragma unroll
-          for (int k = first; k < first + BLOCKS; ++k) {
-            uint32_t b0 = 0, b1 = 0;
-            if (C::CC == 8 || qh < C::CC) {
-              b0 = *reinterpret_cast<const uint32_t*>(pb + k * 32);
-              b1 = *reinterpret_cast<const uint32_t*>(pb + k * 32 + 16);
+        for (int c = 0; c < CH; ++c) {
+          const int at = i * CH + c, buf = c & 1;  // (CH is even)
+          if (at >= 2) {
+            const bool freed = mbar_wait(&vt_empty[buf], ((at >> 1) - 1) & 1);
+            if (__any_sync(kFullMask, !freed)) {
+              good = false;
+              break;
             }
-            pv_block<C>(acc, tile, qd * 32 + k * 16, slab, b0, b1, 15u, false, lane);
+            tmem_fence_after();
           }
-        } else {
-#pragma unroll 1
-        for (int k = first; k < first + BLOCKS; ++k) {
-          const int tk = t0 + k * 16, row0 = qd * 32 + k * 16;
-          if (!((here >> (row0 >> 4)) & 1u) || tk >= thi || tk + 16 <= tlo) continue;
-          uint32_t b0 = 0, b1 = 0;
-          if (C::CC == 8 || qh < C::CC) {
-            b0 = *reinterpret_cast<const uint32_t*>(pb + k * 32);
-            b1 = *reinterpret_cast<const uint32_t*>(pb + k * 32 + 16);
-          }
-          uint32_t ok = 15u;
-          if (tk < tlo || tk + 16 > thi) {
-            const int tr = tk + 2 * r;
-            ok = (uint32_t)(tr >= tlo && tr < thi) | (uint32_t)(tr + 1 >= tlo && tr + 1 < thi) << 1 |
-                 (uint32_t)(tr + 8 >= tlo && tr + 8 < thi) << 2 | (uint32_t)(tr + 9 >= tlo && tr + 9 < thi) << 3;
-          }
-          // Tokens that some columns attend and others do not (several query
-          // tokens): a NaN there belongs to the former alone, but 0 * NaN is NaN,
-          // so it is taken out of the product and put into their sums.
-          const bool mixed = p.query_tokens > 1 && (tk + 16 > all_hi || tk < all_lo);
-          if (mixed) {
-            const uint8_t* sf = tile + C::CODE_BYTES + row0 * C::ROW_SF + slab * 16 + 2 * qh;
-#pragma unroll 1
-            for (int j = 0; j < 16; ++j) {
-              const uint32_t two = *reinterpret_cast<const uint16_t*>(sf + j * C::ROW_SF);
-              if (two == without_nan(two)) continue;
+          if (elect_one()) {
 #pragma unroll
-              for (int hh = 0; hh < 2; ++hh) {
-                const int c = 2 * r + hh, t = tk + j;
-                if (c >= C::CC || !cm.valid(c) || t < tlo || t >= thi) continue;
-                const int end = L - cm.T + cm.token(c) + 1;
-                if (t >= end || (p.window > 0 && t < end - p.window)) continue;
-#pragma unroll
-                for (int m = 0; m < 16; ++m) {
-                  if ((two >> (m < 8 ? 0 : 8) & 0x7fu) != 0x7fu) continue;
-                  acc[m][hh] = NAN;
-                  acc[m][2 + hh] = NAN;
-                }
-              }
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t off = (c >> 1) * 1024 + (c & 1) * 64 + j * 32;
+              mma_fp4(tmem + kTmemVt + buf * 128, smem_desc(eye + j * 32, 0, 512, 64), smem_desc(v + off, 0, C::SL * 1024),
+                      kIdesc, tmem + kTmemSfi, tmem + kTmemSfv + (c * 2 + j) * 4, j > 0);
+            }
+            mma_commit<1>(&vt_full[buf]);
+            if (c == CH - 1) {
+              mma_commit<1>(&empty[st]);
+              mma_commit<1>(dq_done);
             }
           }
-          pv_block<C>(acc, tile, row0, slab, b0, b1, ok, mixed, lane);
+          __syncwarp();
+          issued = at + 1;
         }
+      }
+      if (!good) {
+        if (issued > 0) mbar_wait(&vt_full[(issued - 1) & 1], ((issued - 1) >> 1) & 1);
+        if (lane == 0) atomicOr(p.err, kErrTimeout);
+      }
+    } else {
+      // ---- O^T += V^T P^T
+      constexpr uint32_t kIdesc = (1u << 4) | (2u << 7) | (2u << 10) | (2u << 17) | (8u << 24);  // tf32 -> fp32, 128 x 16
+      const uint32_t p0 = smem_u32(smem + C::P_OFFSET);
+      int issued = 0;
+#pragma unroll 1
+      for (int i = 0; i < tiles && good; ++i) {
+        const bool ready = mbar_wait(&p_full[i & 1], (i >> 1) & 1);
+        if (__any_sync(kFullMask, !ready)) {
+          good = false;
+          break;
         }
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&p_empty[qd * 2 + buf]);
-          mbar_arrive(&empty[st]);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          const int at = i * CH + c, buf = c & 1;
+          const bool there = mbar_wait(&vt_full[buf], (at >> 1) & 1);
+          if (__any_sync(kFullMask, !there)) {
+            good = false;
+            break;
+          }
+          tmem_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int q = 0; q < kFp4Tile / 8; ++q)
+              mma_tf32(tmem + kTmemO + c * 16, tmem + kTmemVt + buf * 128 + q * 8,
+                       smem_desc(p0 + (i & 1) * C::P_BYTES + (q >> 2) * 2048 + (q & 3) * 32, 0, 1024), kIdesc,
+                       i > 0 || q > 0);
+            mma_commit<1>(&vt_empty[buf]);
+            if (c == CH - 1) mma_commit<1>(&p_empty[i & 1]);
+          }
+          __syncwarp();
+          issued = at + 1;
         }
       }
       if (!good && lane == 0) atomicOr(p.err, kErrTimeout);
-      // every warp is done with the ring
-      named_bar_sync(3, 8 * 32);
-      float* comb = reinterpret_cast<float*>(smem) + (warp - 4) * C::CC * C::COMB_ROW + qh * 36;
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        if (2 * r + hh >= C::CC) continue;
-#pragma unroll
-        for (int m = 0; m < 16; ++m)
-          *reinterpret_cast<float2*>(comb + (2 * r + hh) * C::COMB_ROW + 2 * m) = make_float2(acc[m][hh], acc[m][2 + hh]);
-      }
+      if (issued > 0) mbar_wait(&vt_empty[(issued - 1) & 1], ((issued - 1) >> 1) & 1);  // all of it is in the sums
     }
   }
   __syncthreads();
 
-  // ---- the quarters' sums joined
-  float* coef = reinterpret_cast<float*>(smem + C::COEF_OFFSET);  // [4][CC]
+  // ---- the piece's result
   if (tid < C::CC) {
-    float M = -INFINITY, sum = 0.f, f[4];
-    const float2* ml = reinterpret_cast<const float2*>(smem + C::ML_OFFSET);
-    if (tiles > 0) {
-#pragma unroll
-      for (int w = 0; w < 4; ++w) M = fmaxf(M, ml[w * C::CC + tid].x);
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        f[w] = M == -INFINITY ? 0.f : ex2(ml[w * C::CC + tid].x - M);
-        sum += f[w] * ml[w * C::CC + tid].y;
-      }
-#pragma unroll
-      for (int w = 0; w < 4; ++w) coef[w * C::CC + tid] = sum != 0.f ? f[w] / sum * p.v_mul : 0.f;
-    }
-    my_lse[tid] = sum != 0.f ? (M + __log2f(sum) - kPShift) * 0.69314718055994530942f : -INFINITY;
+    const float s = tiles > 0 ? (red[tid] + red[C::CC + tid]) + (red[2 * C::CC + tid] + red[3 * C::CC + tid]) : 0.f;
+    coef[tid] = s != 0.f ? p.v_mul / s : 0.f;
+    my_lse[tid] = s != 0.f ? (my_lse[tid] + __log2f(s)) * 0.69314718055994530942f : -INFINITY;
   }
   __syncthreads();
-  constexpr int D4 = C::D / 4;
-  for (int e = tid; e < C::CC * D4; e += C::THREADS) {
-    const int c = e / D4, dim = (e % D4) * 4;
-    if (!cm.valid(c)) continue;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (tiles > 0) {
-      const int in = dim % 256 + 4 * ((dim % 256) / 32);
+  // warps 0-7: lane l of quarter w has dim 32 w + l of a chunk; warps 0-3 the even chunks, 4-7 the odd ones
+  if (warp < 8) {
+    tmem_fence_after();
+#pragma unroll 1
+    for (int c0 = warp >> 2; c0 < CH; c0 += 2) {
+      uint32_t o[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+      if (tiles > 0) {
+        tmem_ld(o, tmem + kTmemO + c0 * 16 + quarter);
+        tmem_wait_ld();
+      }
+      const int dim = c0 * 128 + (warp & 3) * 32 + lane;
 #pragma unroll
-      for (int k = 0; k < (C::SL == 2 ? 4 : 8); ++k) {
-        const int w = C::SL == 2 ? 2 * k + dim / 256 : k;
-        const float f = coef[(w >> 1) * C::CC + c];
-        const float4 a = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem) +
-                                                          (w * C::CC + c) * C::COMB_ROW + in);
-        o.x = fmaf(f, a.x, o.x);
-        o.y = fmaf(f, a.y, o.y);
-        o.z = fmaf(f, a.z, o.z);
-        o.w = fmaf(f, a.w, o.w);
+      for (int c = 0; c < C::CC; ++c) {
+        if (!cm.valid(c)) break;
+        // (no attended token: coefficient 0, and sums that nothing has written)
+        float x = coef[c] != 0.f ? __uint_as_float(o[c]) * coef[c] : 0.f;
+        if (tiles > 0 && ((poison[c] >> (dim >> 4)) & 1u)) x = NAN;
+        if (p.direct_out)
+          reinterpret_cast<__nv_bfloat16*>(p.out)[cm.row(c) * C::D + dim] = __float2bfloat16_rn(x);
+        else if (p.cluster_merge)
+          my_out[c * C::D + dim] = x;
+        else
+          p.o_part[(cm.row(c) * p.num_splits + split) * C::D + dim] = x;
       }
     }
-    if (p.direct_out) {
-      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + cm.row(c) * C::D + dim) =
-          make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
-    } else if (p.cluster_merge) {
-      *reinterpret_cast<float4*>(my_out + c * C::D + dim) = o;
-    } else {
-      const size_t row = cm.row(c) * p.num_splits + split;
-      *reinterpret_cast<float4*>(p.o_part + row * C::D + dim) = o;
-      if (dim == 0) p.lse_part[row] = my_lse[c];
-    }
+    tmem_fence_before();
   }
-  if (warp == kMmaWarp) tmem_dealloc<1>(tmem, 256);
+  if (!p.direct_out && !p.cluster_merge && tid < C::CC && cm.valid(tid))
+    p.lse_part[cm.row(tid) * p.num_splits + split] = my_lse[tid];
+  __syncthreads();
+  if (warp == kPvWarp) {
+    tmem_fence_after();
+    tmem_dealloc<1>(*tmem_at, kTmemCols);
+  }
   if (!p.cluster_merge) return;
 
   // ---- the pieces' results joined over distributed shared memory: each CTA of
@@ -807,6 +843,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
   //   out = sum_s w_s o_s,  w_s = exp(lse_s - M) / sum_s' exp(lse_s' - M)
   cluster_sync_all();
   const int S = p.num_splits, rank = (int)cluster_ctarank();
+  constexpr int D4 = C::D / 4;
   const uint32_t out_at = smem_u32(my_out), lse_at = smem_u32(my_lse);
   for (int e = rank * C::THREADS + tid; e < C::CC * D4; e += S * C::THREADS) {
     const int c = e / D4, dim = (e % D4) * 4;
