@@ -51,7 +51,7 @@ struct Fp4Cfg {
   static constexpr int BAR_OFFSET = (VALID_OFFSET + (NK + NV) * 4 + 7) / 8 * 8;
   static constexpr int NUM_BARS = 2 * (NK + NV) + 15;
   static constexpr int SMEM_BYTES = BAR_OFFSET + NUM_BARS * 8 + 16 + 1024;  // (+ 1 KiB to start on a 1024-byte boundary)
-  static constexpr int WARPS = 14;
+  static constexpr int WARPS = 12;
   static constexpr int THREADS = 32 * WARPS;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
   static_assert(Q_OFFSET % 1024 == 0 && P_OFFSET % 1024 == 0 && EYE_OFFSET % 1024 == 0 && QSF_OFFSET % 16 == 0,

@@ -29,7 +29,7 @@
 //
 // Roles (one CTA an SM): warps 0-3 softmax (a lane a token); 4-7 write the
 // tiles' scales to tensor memory; 8, 9 copy codes (TMA), 10 scales (cp.async);
-// 11, 12, 13 issue the three products. Warps 0-7 read the sums at the end.
+// 11 issues the products. Warps 0-7 read the sums at the end.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
   uint32_t* valid = reinterpret_cast<uint32_t*>(smem + C::VALID_OFFSET);
   volatile uint32_t* failed_at = reinterpret_cast<uint32_t*>(smem + C::FAILED_OFFSET);
   uint32_t* poison = reinterpret_cast<uint32_t*>(smem + C::POISON_OFFSET);
-  constexpr int kSfWarp = 4, kCodeWarp = 8, kScaleWarp = 10, kQkWarp = 11, kDqWarp = 12, kPvWarp = 13;
+  constexpr int kSfWarp = 4, kCodeWarp = 8, kScaleWarp = 10, kMmaWarp = 11;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool copies = warp >= kCodeWarp && warp <= kScaleWarp;
   const bool early = p.early_kv != 0 && copies;
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
     }
     fence_barrier_init();
   }
-  if (warp == kPvWarp) tmem_alloc<1>(tmem_at, kTmemCols);
+  if (warp == kMmaWarp) tmem_alloc<1>(tmem_at, kTmemCols);
   if (copies) {
     named_bar_sync(5, 3 * 32);
     named_bar_arrive(4, C::THREADS);
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
       if (tid == 0) *failed_at = 0u;
       fence_proxy_async_smem();
     }
-    named_bar_sync(1, 11 * 32);  // warps 0-7 and the products'
+    named_bar_sync(1, 9 * 32);  // warps 0-7 and the products'
 
     if (warp < kSfWarp) {
       // ---- softmax: rows 32 warp .. + 31 of every tile
@@ -675,122 +675,99 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
         if (lane == 0) mbar_arrive(sfv_ready);
       }
       if (!good && lane == 0) atomicOr(p.err, kErrTimeout);
-    } else if (warp == kQkWarp) {
-      // ---- S = K q^T
-      constexpr uint32_t kIdesc = (1u << 7) | (1u << 10) | ((uint32_t)(C::N / 8) << 17) | (8u << 24);  // e2m1, e4m3 scales
-      int issued = 0;
-#pragma unroll 1
-      for (int i = 0; i < tiles; ++i) {
-        const int st = i % C::NK, sbuf = i % SB;
-        bool ready = mbar_wait(&full[st], (i / C::NK) & 1) && mbar_wait(sfk_ready, i & 1);
-        if (ready && i >= SB) ready = mbar_wait(&s_empty[sbuf], (i / SB - 1) & 1);
-        if (__any_sync(kFullMask, !ready)) {
-          good = false;
-          break;
-        }
-        tmem_fence_after();
-        if (elect_one()) {
-          const uint32_t a = smem_u32(smem + st * C::ITEM_BYTES), q = smem_u32(smem + C::Q_OFFSET);
+    } else {
+      // ---- the products, by one warp in an order that keeps the tensor core busy
+      // (issued by three warps, a product each, they got in one another's way:
+      // a tf32 instruction took 62 cycles instead of 14). Chunks of 128 dims go
+      // in pairs, V^T of both and then both sums, so that one waits for its
+      // operand while the other runs; the next tile's scores go out between
+      // them, as soon as they can.
+      constexpr uint32_t kQk = (1u << 7) | (1u << 10) | ((uint32_t)(C::N / 8) << 17) | (8u << 24);  // e2m1, e4m3 scales
+      constexpr uint32_t kDq = (1u << 7) | (1u << 10) | ((uint32_t)(kFp4Tile / 8) << 17) | (8u << 24);
+      constexpr uint32_t kPv = (1u << 4) | (2u << 7) | (2u << 10) | (2u << 17) | (8u << 24);  // tf32 -> fp32, 128 x 16
+      if (elect_one()) {
+        // descriptors' bases; a step further is a constant added to the address field
+        const uint64_t ring_desc = smem_desc(smem_u32(smem), 0, C::SL * 1024);
+        const uint64_t q_desc = smem_desc(smem_u32(smem + C::Q_OFFSET), 0, C::SL * 1024);
+        const uint64_t eye_desc = smem_desc(smem_u32(smem + C::EYE_OFFSET), 0, 512, 64);
+        const uint64_t p_desc = smem_desc(smem_u32(smem + C::P_OFFSET), 0, 1024);
+        constexpr int kItem = C::ITEM_BYTES >> 4;
+        int scores = 0, widened = 0, summed = 0;  // tiles, chunks, chunks issued so far
+        auto qk = [&](int i) {
+          tmem_fence_after();
+          const int st = i % C::NK, sbuf = i % SB;
+          const uint64_t a = ring_desc + st * kItem;
 #pragma unroll
-          for (int k = 0; k < C::KSTEPS; ++k) {
-            const uint32_t off = (k >> 2) * 1024 + (k & 3) * 32;
-            mma_fp4(tmem + kTmemS + sbuf * C::N, smem_desc(a + off, 0, C::SL * 1024), smem_desc(q + off, 0, C::SL * 1024),
-                    kIdesc, tmem + kTmemSfk + k * 4, tmem + kTmemSfq + k * 4, k > 0);
-          }
+          for (int k = 0; k < C::KSTEPS; ++k)
+            mma_fp4(tmem + kTmemS + sbuf * C::N, a + (k >> 2) * 64 + (k & 3) * 2, q_desc + (k >> 2) * 64 + (k & 3) * 2, kQk,
+                    tmem + kTmemSfk + k * 4, tmem + kTmemSfq + k * 4, k > 0);
           mma_commit<1>(&s_full[sbuf]);
           mma_commit<1>(&empty[st]);
-        }
-        __syncwarp();
-        issued = i + 1;
-      }
-      if (!good) {
-        // what was issued ends before its operands and its result are used for something else
-        if (issued > 0) mbar_wait(&s_full[(issued - 1) % SB], ((issued - 1) / SB) & 1);
-        if (lane == 0) atomicOr(p.err, kErrTimeout);
-      }
-    } else if (warp == kDqWarp) {
-      // ---- V^T = I V^T, a chunk of 128 dims after another
-      constexpr uint32_t kIdesc = (1u << 7) | (1u << 10) | ((uint32_t)(kFp4Tile / 8) << 17) | (8u << 24);
-      const uint32_t eye = smem_u32(smem + C::EYE_OFFSET);
-      int issued = 0;
+          scores = i + 1;
+        };
+        auto may_qk = [&](int i) {  // without waiting
+          return mbar_test(&full[i % C::NK], (i / C::NK) & 1) && mbar_test(sfk_ready, i & 1) &&
+                 (i < SB || mbar_test(&s_empty[i % SB], (i / SB - 1) & 1));
+        };
 #pragma unroll 1
-      for (int i = 0; i < tiles && good; ++i) {
-        const int n = C::KVS ? C::NK : C::NV, st = (C::KVS ? 0 : C::NK) + i % n;
-        const bool ready = mbar_wait(&full[st], (i / n) & 1) && mbar_wait(sfv_ready, i & 1);
-        if (__any_sync(kFullMask, !ready)) {
-          good = false;
-          break;
-        }
-        tmem_fence_after();
-        const uint32_t v = smem_u32(smem + st * C::ITEM_BYTES);
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          const int at = i * CH + c, buf = c & 1;  // (CH is even)
-          if (at >= 2) {
-            const bool freed = mbar_wait(&vt_empty[buf], ((at >> 1) - 1) & 1);
-            if (__any_sync(kFullMask, !freed)) {
-              good = false;
-              break;
-            }
-            tmem_fence_after();
+        for (int i = 0; i < tiles && good; ++i) {
+          if (scores == i) {
+            good = mbar_wait(&full[i % C::NK], (i / C::NK) & 1) && mbar_wait(sfk_ready, i & 1) &&
+                   (i < SB || mbar_wait(&s_empty[i % SB], (i / SB - 1) & 1));
+            if (!good) break;
+            qk(i);
           }
-          if (elect_one()) {
+          const int n = C::KVS ? C::NK : C::NV, st = (C::KVS ? 0 : C::NK) + i % n;
+          good = mbar_wait(&full[st], (i / n) & 1) && mbar_wait(sfv_ready, i & 1);
+          const uint64_t v = ring_desc + st * kItem;
+          const uint64_t pd = p_desc + (i & 1) * (C::P_BYTES >> 4);
+#pragma unroll 1
+          for (int c0 = 0; c0 < CH && good; c0 += 2) {
+            const int at = i * CH + c0;  // (even)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint32_t off = (c >> 1) * 1024 + (c & 1) * 64 + j * 32;
-              mma_fp4(tmem + kTmemVt + buf * 128, smem_desc(eye + j * 32, 0, 512, 64), smem_desc(v + off, 0, C::SL * 1024),
-                      kIdesc, tmem + kTmemSfi, tmem + kTmemSfv + (c * 2 + j) * 4, j > 0);
+            for (int c = 0; c < 2; ++c) {
+              if (good && at > 0) good = mbar_wait(&vt_empty[c], ((at >> 1) - 1) & 1);
+              if (!good) break;
+              tmem_fence_after();
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                mma_fp4(tmem + kTmemVt + c * 128, eye_desc + j * 2, v + (c0 >> 1) * 64 + c * 4 + j * 2, kDq, tmem + kTmemSfi,
+                        tmem + kTmemSfv + c0 * 8 + (c * 2 + j) * 4, j > 0);
+              mma_commit<1>(&vt_full[c]);
+              widened = at + c + 1;
             }
-            mma_commit<1>(&vt_full[buf]);
-            if (c == CH - 1) {
+            if (!good) break;
+            if (c0 + 2 == CH) {
               mma_commit<1>(&empty[st]);
               mma_commit<1>(dq_done);
             }
-          }
-          __syncwarp();
-          issued = at + 1;
-        }
-      }
-      if (!good) {
-        if (issued > 0) mbar_wait(&vt_full[(issued - 1) & 1], ((issued - 1) >> 1) & 1);
-        if (lane == 0) atomicOr(p.err, kErrTimeout);
-      }
-    } else {
-      // ---- O^T += V^T P^T
-      constexpr uint32_t kIdesc = (1u << 4) | (2u << 7) | (2u << 10) | (2u << 17) | (8u << 24);  // tf32 -> fp32, 128 x 16
-      const uint32_t p0 = smem_u32(smem + C::P_OFFSET);
-      int issued = 0;
-#pragma unroll 1
-      for (int i = 0; i < tiles && good; ++i) {
-        const bool ready = mbar_wait(&p_full[i & 1], (i >> 1) & 1);
-        if (__any_sync(kFullMask, !ready)) {
-          good = false;
-          break;
-        }
+            if (i + 1 < tiles && scores == i + 1 && may_qk(i + 1)) qk(i + 1);
+            if (c0 == 0) good = mbar_wait(&p_full[i & 1], (i >> 1) & 1);
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          const int at = i * CH + c, buf = c & 1;
-          const bool there = mbar_wait(&vt_full[buf], (at >> 1) & 1);
-          if (__any_sync(kFullMask, !there)) {
-            good = false;
-            break;
-          }
-          tmem_fence_after();
-          if (elect_one()) {
+            for (int c = 0; c < 2; ++c) {
+              if (good) good = mbar_wait(&vt_full[c], (at >> 1) & 1);
+              if (!good) break;
+              tmem_fence_after();
 #pragma unroll
-            for (int q = 0; q < kFp4Tile / 8; ++q)
-              mma_tf32(tmem + kTmemO + c * 16, tmem + kTmemVt + buf * 128 + q * 8,
-                       smem_desc(p0 + (i & 1) * C::P_BYTES + (q >> 2) * 2048 + (q & 3) * 32, 0, 1024), kIdesc,
-                       i > 0 || q > 0);
-            mma_commit<1>(&vt_empty[buf]);
-            if (c == CH - 1) mma_commit<1>(&p_empty[i & 1]);
+              for (int q = 0; q < kFp4Tile / 8; ++q)
+                mma_tf32(tmem + kTmemO + c0 * 16 + c * 16, tmem + kTmemVt + c * 128 + q * 8, pd + (q >> 2) * 128 + (q & 3) * 2,
+                         kPv, i > 0 || q > 0);
+              mma_commit<1>(&vt_empty[c]);
+              summed = at + c + 1;
+            }
+            if (good && c0 + 2 == CH) mma_commit<1>(&p_empty[i & 1]);
+            if (good && i + 1 < tiles && scores == i + 1 && may_qk(i + 1)) qk(i + 1);
           }
-          __syncwarp();
-          issued = at + 1;
         }
+        // what was issued ends before its operands and results are used for something else
+        if (!good) {
+          if (scores > 0) mbar_wait(&s_full[(scores - 1) % SB], ((scores - 1) / SB) & 1);
+          if (widened > 0) mbar_wait(&vt_full[(widened - 1) & 1], ((widened - 1) >> 1) & 1);
+          atomicOr(p.err, kErrTimeout);
+        }
+        if (summed > 0) mbar_wait(&vt_empty[(summed - 1) & 1], ((summed - 1) >> 1) & 1);
       }
-      if (!good && lane == 0) atomicOr(p.err, kErrTimeout);
-      if (issued > 0) mbar_wait(&vt_empty[(issued - 1) & 1], ((issued - 1) >> 1) & 1);  // all of it is in the sums
+      __syncwarp();
     }
   }
   __syncthreads();
@@ -832,7 +809,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
   if (!p.direct_out && !p.cluster_merge && tid < C::CC && cm.valid(tid))
     p.lse_part[cm.row(tid) * p.num_splits + split] = my_lse[tid];
   __syncthreads();
-  if (warp == kPvWarp) {
+  if (warp == kMmaWarp) {
     tmem_fence_after();
     tmem_dealloc<1>(*tmem_at, kTmemCols);
   }
