@@ -12,7 +12,10 @@ constexpr int kFp4Block = 16;    // dims under one scale
 constexpr int kFp4Tile = 128;    // tokens of a tile: the matrix instruction's rows
 constexpr int kFp4Terms = 6;     // e2m1 terms a query element is written as
 constexpr int kFp4FirstId = 60;  // variant ids follow stage 1's
-constexpr int kFp4MaxCluster = 8;
+constexpr int kFp4MaxShares = 4096;  // CTAs of a launch
+// Workspace: [error word, padded to 256 B][u32 per share: pieces of its last unit that
+// are there][fp32 log-sum-exps [shares][2][CC]][fp32 pieces [shares][2][CC][D]]
+constexpr uint64_t fp4_counters_bytes(int shares) { return ((uint64_t)shares * 4 + 255) / 256 * 256; }
 
 // D   head_dim; KVS K=V shared pool; CC columns (query rows) of a CTA
 template <int D_, bool KVS_, int CC_>
@@ -34,27 +37,29 @@ struct Fp4Cfg {
   static constexpr int RING_BYTES = (NK + NV) * ITEM_BYTES;
   static constexpr int CHUNKS = D / 128;   // of 128 dims: V is widened and summed a chunk at a time
   static constexpr int S_BUFS = N <= 32 ? 2 : 1;  // score buffers in tensor memory
-  static_assert(CC * D * 4 <= RING_BYTES, "the CTA's result, float [CC][D], lies over the ring at the end");
-  static constexpr int Q_OFFSET = RING_BYTES;                     // query terms' codes, like a tile's
-  static constexpr int P_OFFSET = Q_OFFSET + N * D / 2;           // 2 x P, tf32: [32 tokens][16 columns][128 B, swizzled]
-  static constexpr int P_BYTES = 16 * kFp4Tile * 4;
+  static constexpr int Q_BYTES = N * D / 2;                       // a query's terms: codes like a tile's
+  static constexpr int Q_OFFSET = RING_BYTES;                     // [2]: of this segment and the next
+  static constexpr int P_BYTES = 8 * kFp4Tile * 4;                // P, tf32: [32 tokens][8 columns][128 B, swizzled]
+  static constexpr int P_OFFSET = Q_OFFSET + 2 * Q_BYTES;         // [2]
   static constexpr int EYE_OFFSET = P_OFFSET + 2 * P_BYTES;       // the unit matrix in e2m1: 128 rows of 64 B, swizzled
   static constexpr int EYE_BYTES = 128 * 64;
   static constexpr int QSF_OFFSET = EYE_OFFSET + EYE_BYTES;       // query terms' scales [N][D / 16]
-  static constexpr int COL_OFFSET = QSF_OFFSET + N * ROW_SF;      // float [CC]: score scale of a column
-  static constexpr int POISON_OFFSET = COL_OFFSET + CC * 4;       // u32 [CC]: 16-dim blocks that are NaN
-  static constexpr int RED_OFFSET = POISON_OFFSET + CC * 4;       // float [4][CC]: the softmax warps' maxima, then sums
-  static constexpr int LSE_OFFSET = RED_OFFSET + 4 * CC * 4;      // float [CC]
-  static constexpr int COEF_OFFSET = LSE_OFFSET + CC * 4;         // float [CC]
-  static constexpr int FAILED_OFFSET = COEF_OFFSET + CC * 4;      // u32: a softmax warp's wait ran out
-  static constexpr int VALID_OFFSET = FAILED_OFFSET + 4;          // u32 [NK + NV]: the 16-token blocks that a slot's tile holds
+  static constexpr int COL_OFFSET = QSF_OFFSET + N * ROW_SF;      // float [2][CC]: score scale of a column
+  static constexpr int POISON_OFFSET = COL_OFFSET + 2 * CC * 4;   // u32 [4][CC]: 16-dim blocks that are NaN
+  static constexpr int TOP_OFFSET = POISON_OFFSET + 4 * CC * 4;   // float [4][CC]: the softmax warps' maxima
+  static constexpr int SUM_OFFSET = TOP_OFFSET + 4 * CC * 4;      // float [2][5][CC]: their sums, and the references
+  static constexpr int MISC_OFFSET = SUM_OFFSET + 2 * 5 * CC * 4; // u32: a softmax warp's wait ran out; the join's ticket
+  static constexpr int VALID_OFFSET = MISC_OFFSET + 8;            // u32 [NK + NV]: what a slot's tile is (kTile...)
   static constexpr int BAR_OFFSET = (VALID_OFFSET + (NK + NV) * 4 + 7) / 8 * 8;
-  static constexpr int NUM_BARS = 2 * (NK + NV) + 15;
+  static constexpr int NUM_BARS = 2 * (NK + NV) + 15 + 9;
   static constexpr int SMEM_BYTES = BAR_OFFSET + NUM_BARS * 8 + 16 + 1024;  // (+ 1 KiB to start on a 1024-byte boundary)
-  static constexpr int WARPS = 12;
+  static constexpr int WARPS = 16;
   static constexpr int THREADS = 32 * WARPS;
+  // what a share leaves to be joined: its first and its last unit's piece
+  static constexpr int PIECE_FLOATS = CC * D;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
-  static_assert(Q_OFFSET % 1024 == 0 && P_OFFSET % 1024 == 0 && EYE_OFFSET % 1024 == 0 && QSF_OFFSET % 16 == 0,
+  static_assert(Q_OFFSET % 1024 == 0 && Q_BYTES % 1024 == 0 && P_OFFSET % 1024 == 0 && EYE_OFFSET % 1024 == 0 &&
+                    QSF_OFFSET % 16 == 0,
                 "alignment");
 };
 
@@ -69,19 +74,19 @@ struct Fp4Cfg {
   X(66, 256, true, 4)       \
   X(67, 256, true, 8)
 
-// What a launch needs beyond Stage1Params' common part.
 struct Fp4Params {
   CUtensorMap kmap, vmap;  // codes as {128 B, 8 rows, slabs, 8-row groups}
   const uint16_t* q;       // bf16 [B, T, Hq, D]
   const uint8_t *k_sf, *v_sf;  // e4m3 [num_pages, Hkv, P, D / 16]
   const int32_t *block_tables, *seq_lens;
   void* out;
+  uint32_t* counters;  // [shares], zero between launches
   float *lse_part, *o_part;
   uint32_t* err;
   float scale_log2;  // softmax scale * log2(e) * 2^k_exp
   float v_mul;       // 2^v_exp
-  int32_t direct_out, cluster_merge, stall_bytes, early_kv;
-  int32_t window, num_pages, max_pages, page_size, num_q_heads, num_kv_heads, num_splits, chunk_tokens;
+  int32_t stall_bytes, early_kv;
+  int32_t batch, window, num_pages, max_pages, page_size, num_q_heads, num_kv_heads;
   int32_t query_tokens, group, col_tiles;
 };
 

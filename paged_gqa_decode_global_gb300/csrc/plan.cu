@@ -38,7 +38,7 @@ namespace pd {
 // The 4-bit instances (kv_fp8 2, `group` their columns) follow by id.
 #define PD_FP4_ROW(ID, D, KVS, CC)                                                                   \
   VariantInfo{ID, D, CC, KVS ? 1 : 0, 2, 8, 0, 16, Fp4Cfg<D, KVS, CC>::THREADS,                      \
-              Fp4Cfg<D, KVS, CC>::SMEM_BYTES, kFp4MaxCluster, 1, 0, kFp4Tile / 16, 1},
+              Fp4Cfg<D, KVS, CC>::SMEM_BYTES, 1, 1, 0, kFp4Tile / 16, 1},
 const VariantInfo kVariants[] = {PD_FOR_EACH_VARIANT(PD_VARIANT_ROW) PD_FOR_EACH_FP4(PD_FP4_ROW)};
 #undef PD_VARIANT_ROW
 #undef PD_FP4_ROW
@@ -149,7 +149,6 @@ int cluster_slots(int splits, int sm_count) {
 // in one tile), and for bf16 CTAs of two tiles.
 double cta_tokens_per_us(const pd::VariantInfo& v) {
   const bool kvs = v.kv_shared != 0;
-  if (v.kv_fp8 == PD_KV_FP4_E2M1) return v.head_dim == 512 ? (kvs ? 120.0 : 90.0) : (kvs ? 220.0 : 170.0);
   if (v.tiles == 2) {
     if (v.head_dim == 512) return kvs ? 48.5 : 47.2;
     return 67.0;  // d256 (K=V not measured: the K != V figure)
@@ -381,6 +380,35 @@ pd_status plan_impl(const pd_layer_desc* layer, int32_t batch, int32_t query_tok
   if ((long long)ly.num_kv_heads * groups > 65535) return PD_ERR_UNSUPPORTED;
   const int hkv_ctas = ly.num_kv_heads * groups;
 
+  if (fp4) {
+    // One persistent CTA an SM, each an equal share of all tiles, worked out on the
+    // GPU from the lengths it finds: nothing here depends on the planned ones.
+    const long long units = (long long)batch * hkv_ctas;
+    if (units * ((cap + pd::kFp4Tile - 1) / pd::kFp4Tile) >= (1 << 30)) return PD_ERR_UNSUPPORTED;
+    std::memset(plan, 0, sizeof(*plan));
+    plan->layer = ly;
+    plan->batch = batch;
+    plan->num_splits = 1;  // joined in the launch: there is nothing to merge
+    plan->chunk_tokens = pd::kFp4Tile;
+    plan->block_tokens = TB;
+    plan->variant = v->id;
+    plan->grid_x = std::min(sm_count, pd::kFp4MaxShares);
+    plan->grid_y = 1;
+    plan->grid_z = 1;
+    plan->query_tokens = T;
+    plan->threads_per_cta = v->threads;
+    plan->smem_bytes = v->smem_bytes;
+    plan->sm_count = sm_count;
+    plan->max_seq_len = max_len;
+    plan->merge_mode = 0;
+    plan->lse_offset = pd::kWorkspaceHeader + pd::fp4_counters_bytes(plan->grid_x);
+    plan->opart_offset = align_up(plan->lse_offset + (uint64_t)plan->grid_x * 2 * v->group * 4, 256);
+    plan->workspace_bytes = plan->opart_offset + (uint64_t)plan->grid_x * 2 * v->group * ly.head_dim * 4;
+    plan->magic = kPlanMagic;
+    plan->version = kAbiVersion;
+    return PD_OK;
+  }
+
   // block-aligned attended span of each request (several query tokens: the
   // union of their ranges, from the first token's window start)
   std::vector<int> n_tok(batch);
@@ -397,7 +425,7 @@ pd_status plan_impl(const pd_layer_desc* layer, int32_t batch, int32_t query_tok
 
   CostModel cm;
   const double kv_bytes_per_token =
-      (double)ly.head_dim * (fp4 ? 0.5 + 1.0 / 16 : fp8 ? 1.0 : 2.0) * (ly.kv_shared ? 1.0 : 2.0);
+      (double)ly.head_dim * (fp8 ? 1.0 : 2.0) * (ly.kv_shared ? 1.0 : 2.0);
   // ~7.3 TB/s of HBM on a 152-SM GB300, in proportion for other SM counts
   cm.hbm_tok_per_us = 7.3e12 / 1e6 / kv_bytes_per_token * sm_count / 152.0;
   cm.cap_tok_per_us = cta_tokens_per_us(*v);
@@ -569,7 +597,6 @@ bool plan_is_valid(const pd_plan* plan) {
   const int group = ly.num_q_heads / ly.num_kv_heads;
   if (v.kv_fp8 == PD_KV_FP4_E2M1) {
     if (group > kMaxGroup || plan->query_tokens < 1 || plan->query_tokens > kMaxQueryTokens) return false;
-    if (plan->partial || plan->grid_y != ly.num_kv_heads * col_groups(v, plan->query_tokens, group)) return false;
   } else if (v.multi) {
     if (group > kMaxGroup || plan->query_tokens < 1 || plan->query_tokens > kMaxQueryTokens) return false;
     if (!tiled(plan->query_tokens, group)) return false;
@@ -579,6 +606,21 @@ bool plan_is_valid(const pd_plan* plan) {
   }
   if (ly.head_dim != v.head_dim || ly.kv_shared != v.kv_shared) return false;
   if (ly.kv_dtype != v.kv_fp8) return false;
+  if (v.kv_fp8 == PD_KV_FP4_E2M1) {
+    const int cc = v.group;
+    const long long tiles = ((long long)ly.max_pages_per_seq * ly.page_size + kFp4Tile - 1) / kFp4Tile;
+    const long long units = (long long)plan->batch * ly.num_kv_heads * col_groups(v, plan->query_tokens, group);
+    const uint64_t shares = plan->grid_x;
+    return plan->batch >= 0 && plan->batch <= 65535 && plan->grid_x >= 1 && plan->grid_x <= kFp4MaxShares &&
+           plan->grid_y == 1 && plan->grid_z == 1 && plan->num_splits == 1 && plan->merge_mode == 0 && plan->partial == 0 &&
+           plan->block_tokens == v.block_tokens && plan->threads_per_cta == v.threads && plan->smem_bytes == v.smem_bytes &&
+           plan->test_stall_bytes >= 0 && plan->test_stall_bytes <= (1 << 16) && plan->test_stall_bytes % 16 == 0 &&
+           (plan->early_kv == 0 || plan->early_kv == 1) && ly.max_pages_per_seq > 0 && ly.page_size > 0 &&
+           units * tiles < (1 << 30) && plan->lse_offset >= kWorkspaceHeader + fp4_counters_bytes(plan->grid_x) &&
+           plan->lse_offset % 256 == 0 && plan->opart_offset % 256 == 0 && plan->lse_offset < (1ull << 40) &&
+           plan->opart_offset < (1ull << 40) && plan->opart_offset >= plan->lse_offset + shares * 2 * cc * 4 &&
+           plan->workspace_bytes >= plan->opart_offset + shares * 2 * cc * (uint64_t)ly.head_dim * 4;
+  }
   if (plan->num_splits < 1 || plan->num_splits > kMaxSplits || plan->chunk_tokens < 16 || plan->chunk_tokens % 16 != 0)
     return false;
   if (plan->batch < 0 || plan->grid_x != plan->num_splits || plan->grid_z != plan->batch) return false;

@@ -1,6 +1,11 @@
-// Stage 1 of paged decode attention over a 4-bit cache (sm_103a): one CTA per
-// (KV piece, KV head and column tile, request) streams the piece's codes and
-// block scales once and serves up to CC query rows ("columns") of that KV head.
+// Decode attention over a paged 4-bit cache (sm_103a), pieces joined in the same
+// launch. A unit of work is a (request, KV head, tile of up to CC query rows,
+// "columns"); its tokens come in tiles of 128. One CTA an SM takes an equal share
+// of all units' tiles, in order, so that a share may end in the middle of a unit:
+// what it holds of one then is a piece, and the last CTA to leave its piece of a
+// unit joins them, in the pieces' order. Within a share every role runs on from
+// unit to unit without a gap (a CTA's start takes ~4 us; with a CTA a piece, 61
+// windows of 1024 tokens took 3.2 waves of them, 49 us instead of 27).
 //
 // Mathematics: a cached element is e2m1(code) * e4m3(scale of its 16 dims) *
 // 2^exp. All three products of a tile of 128 tokens run on tcgen05, and no
@@ -27,9 +32,9 @@
 // first tile that holds a token it attends, and stays until a score exceeds it
 // by 2^60 (tf32 has fp32's exponents), which rescales the sums.
 //
-// Roles (one CTA an SM): warps 0-3 softmax (a lane a token); 4-7 write the
-// tiles' scales to tensor memory; 8, 9 copy codes (TMA), 10 scales (cp.async);
-// 11 issues the products. Warps 0-7 read the sums at the end.
+// Roles: warps 0-3 softmax (a lane a token); 4-7 write the tiles' scales to tensor
+// memory; 8, 9 copy codes (TMA), 10 scales (cp.async); 11 issues the products;
+// 12-15 write the next unit's query terms, read a unit's sums and join pieces.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -89,24 +94,140 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// The query rows behind a CTA's columns: column c is pair tile * CC + c of the
+// What a ring slot's word says of its tile, beside the 16-token blocks that have a page (bits 0-7).
+constexpr uint32_t kTileFirst = 0x100u, kTileLast = 0x200u, kTileEnd = 0x400u;  // of its segment; of the share
+
+// The query rows behind a unit's columns: column c is pair tile * CC + c of the
 // request's T x group (token, head) pairs, token-major.
 template <class C>
 struct Columns {
   int b, g, first, T, group, Hq;
-  __device__ __forceinline__ explicit Columns(const Fp4Params& p) {
-    b = blockIdx.z;
-    g = blockIdx.y / p.col_tiles;
-    first = (blockIdx.y % p.col_tiles) * C::CC;
+  __device__ __forceinline__ Columns(const Fp4Params& p, int b_, int y) {
+    b = b_;
+    g = y / p.col_tiles;
+    first = (y % p.col_tiles) * C::CC;
     T = p.query_tokens;
     group = p.group;
     Hq = p.num_q_heads;
   }
   __device__ __forceinline__ bool valid(int c) const { return first + c < T * group; }
-  __device__ __forceinline__ int token(int c) const { return (first + c) / group; }
+  __device__ __forceinline__ int token(int c) const { return min((first + c) / group, T - 1); }
   __device__ __forceinline__ size_t row(int c) const {
     const int pr = first + c;
     return ((size_t)b * T + pr / group) * Hq + (size_t)g * group + pr % group;
+  }
+};
+
+// A request's attended range, cut to what its block table holds.
+struct Span {
+  int L, lo, base, tiles;  // cached tokens; the first one attended, rounded down to 16; tiles from there (at least one)
+  bool bad;
+  __device__ __forceinline__ Span(const Fp4Params& p, int raw) {
+    const int cap = p.max_pages * p.page_size;
+    bad = raw < 0 || raw > cap || (p.query_tokens > 1 && raw < p.query_tokens);
+    L = max(0, min(raw, cap));
+    const int first_hi = L - p.query_tokens + 1;
+    lo = p.window > 0 && first_hi > p.window ? first_hi - p.window : 0;
+    base = lo / 16 * 16;
+    tiles = max(1, (L - base + kFp4Tile - 1) / kFp4Tile);
+  }
+};
+
+// The tiles of a share that belong to one unit.
+template <class C>
+struct Segment {
+  int b, y, L, tiles;
+  int t_base;    // first token of the first tile
+  int tlo, thi;  // tokens of it that some column attends
+  int pieces, piece, first_share;  // of the unit
+  bool bad;
+  // column c's attended positions
+  __device__ __forceinline__ int col_hi(const Fp4Params& p, const Columns<C>& cm, int c) const {
+    return L - p.query_tokens + cm.token(c) + 1;
+  }
+};
+
+// One warp's walk over the CTA's share; all lanes take part.
+template <class C>
+struct Walk {
+  const Fp4Params& p;
+  const int lane, Y;
+  int lens = 0, chunk = -1;  // this lane's request's length, of 32
+  int b = 0, y = 0, k = 0;   // where the next segment begins
+  int unit = 0;              // tiles before unit (b, y) (all of them are fewer than 2^30)
+  int left = 0;              // tiles of the share not yet handed out
+  int each = 1;              // tiles of a share
+  __device__ __forceinline__ Walk(const Fp4Params& p_, int lane_)
+      : p(p_), lane(lane_), Y(p_.num_kv_heads * p_.col_tiles) {
+    const int chunks = (p.batch + 31) / 32;
+    int total = 0;
+    for (int c = 0; c < chunks; ++c) {
+      load(c);
+      total += (int)__reduce_add_sync(kFullMask, count()) * Y;
+    }
+    each = (total + gridDim.x - 1) / gridDim.x;
+    if (blockIdx.x * (long long)each >= total) return;
+    const int start = blockIdx.x * each;
+    left = min(each, total - start);
+    for (int c = 0; c < chunks; ++c) {
+      load(c);
+      const int n = count();
+      int upto = n;  // tiles of the requests up to this lane's
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const int o = __shfl_up_sync(kFullMask, upto, m);
+        if (lane >= m) upto += o;
+      }
+      const uint32_t past = __ballot_sync(kFullMask, unit + upto * Y > start);
+      if (past == 0) {
+        unit += __shfl_sync(kFullMask, upto, 31) * Y;
+        continue;
+      }
+      const int at = __ffs(past) - 1;
+      const int tiles = __shfl_sync(kFullMask, n, at);
+      unit += (__shfl_sync(kFullMask, upto, at) - tiles) * Y;
+      b = c * 32 + at;
+      y = (start - unit) / tiles;
+      unit += y * tiles;
+      k = start - unit;
+      break;
+    }
+  }
+  __device__ __forceinline__ void load(int c) {
+    if (c == chunk) return;
+    chunk = c;
+    const int at = c * 32 + lane;
+    lens = at < p.batch ? p.seq_lens[at] : 0;
+  }
+  __device__ __forceinline__ int count() const { return chunk * 32 + lane < p.batch ? Span(p, lens).tiles : 0; }
+  __device__ __forceinline__ bool next(Segment<C>& s) {
+    if (left == 0) return false;
+    load(b >> 5);
+    const Span sp(p, __shfl_sync(kFullMask, lens, b & 31));
+    s.b = b;
+    s.y = y;
+    s.L = sp.L;
+    s.bad = sp.bad;
+    s.tiles = min(sp.tiles - k, left);
+    s.t_base = sp.base + k * kFp4Tile;
+    const Columns<C> cm(p, b, y);
+    const int hi = max(0, s.col_hi(p, cm, C::CC - 1)), first = s.col_hi(p, cm, 0);
+    s.tlo = max(s.t_base, p.window > 0 ? first - p.window : 0);
+    s.thi = min(hi, s.t_base + s.tiles * kFp4Tile);
+    s.first_share = unit / each;
+    s.piece = (int)blockIdx.x - s.first_share;
+    s.pieces = (unit + sp.tiles - 1) / each - s.first_share + 1;
+    left -= s.tiles;
+    k += s.tiles;
+    if (k == sp.tiles) {
+      k = 0;
+      unit += sp.tiles;
+      if (++y == Y) {
+        y = 0;
+        ++b;
+      }
+    }
+    return true;
   }
 };
 
@@ -117,50 +238,57 @@ __device__ __forceinline__ uint32_t code_offset(int row, int byte) {
   return (row >> 3) * (C::SL * 1024) + sl * 1024 + (row & 7) * 128 + ((c ^ (row & 7)) << 4) + (byte & 15);
 }
 
-// The query rows of the CTA's columns as terms in shared memory, by 8 warps:
-// one takes 256 dims of a row, a lane 8 of them, two lanes a block of 16.
+// The query rows of a unit's columns as terms in shared memory (`q`) and their
+// scales (`sf`, `mul`), by 4 warps: one takes 256 dims of a row, a lane 8 of them,
+// two lanes a block of 16.
 template <class C>
-__device__ __forceinline__ void write_query_terms(const Fp4Params& p, const Columns<C>& cm, uint8_t* smem, int warp,
-                                                  int lane) {
-  constexpr int ITEMS = C::CC * C::SL, EACH = (ITEMS + 7) / 8;
-  uint4 w[EACH];
-  uint32_t big[EACH];
+__device__ __forceinline__ void write_query_terms(const Fp4Params& p, const Columns<C>& cm, uint8_t* q, uint8_t* sf,
+                                                  float* mul, int warp, int lane) {
+  constexpr int ITEMS = C::CC * C::SL, EACH = ITEMS / 4;
+  float x[EACH][8];
+  bool odd[EACH];
+  {
+    uint4 w[EACH], o[EACH];
 #pragma unroll
-  for (int k = 0; k < EACH; ++k) {
-    const int item = warp + 8 * k, col = item / C::SL, part = item % C::SL;
-    uint4 o = make_uint4(0u, 0u, 0u, 0u);
-    w[k] = o;
-    if (item < ITEMS && cm.valid(col)) {
-      const uint4* row = reinterpret_cast<const uint4*>(p.q + cm.row(col) * C::D) + lane;
-      w[k] = __ldg(row + part * 32);
-      if (C::SL == 2) o = __ldg(row + (part ^ 1) * 32);  // (for the row's largest)
+    for (int k = 0; k < EACH; ++k) {
+      const int item = warp + 4 * k, col = item / C::SL, part = item % C::SL;
+      w[k] = o[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (cm.valid(col)) {
+        const uint4* row = reinterpret_cast<const uint4*>(p.q + cm.row(col) * C::D) + lane;
+        w[k] = __ldg(row + part * 32);
+        if (C::SL == 2) o[k] = __ldg(row + (part ^ 1) * 32);  // (for the row's largest)
+      }
     }
-    uint32_t m = 0;
 #pragma unroll
-    for (uint32_t v : {w[k].x, w[k].y, w[k].z, w[k].w, o.x, o.y, o.z, o.w}) m = __vmaxu2(m, v & 0x7fff7fffu);
-    big[k] = max(m << 16, m & 0xffff0000u);
+    for (int k = 0; k < EACH; ++k) {
+      const int item = warp + 4 * k, col = item / C::SL, part = item % C::SL;
+      // the row's largest magnitude, as whole numbers (infinity and NaN are the largest)
+      uint32_t m = 0;
+#pragma unroll
+      for (uint32_t v : {w[k].x, w[k].y, w[k].z, w[k].w, o[k].x, o[k].y, o[k].z, o[k].w})
+        m = __vmaxu2(m, v & 0x7fff7fffu);
+      const uint32_t top = __reduce_max_sync(kFullMask, max(m << 16, m & 0xffff0000u));
+      odd[k] = top >= 0x7f800000u;  // a NaN or an infinity: the row's scores are NaN
+      // brings the largest to [2^10, 2^11) (a row that is below 2^-116 altogether: as near as a factor of 2^126 does)
+      const int shift = min(126, 137 - (int)(top >> 23));
+      const float up = __int_as_float((127 + shift) << 23);
+      const uint32_t v[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[k][2 * i] = odd[k] ? 0.f : __uint_as_float(v[i] << 16) * up;
+        x[k][2 * i + 1] = odd[k] ? 0.f : __uint_as_float(v[i] & 0xffff0000u) * up;
+      }
+      if (part == 0 && lane == 0) mul[col] = p.scale_log2 * __int_as_float((127 - shift) << 23);
+    }
   }
 #pragma unroll
-  for (int k = 0; k < EACH; ++k) {
-    const int item = warp + 8 * k, col = item / C::SL, part = item % C::SL;
-    if (item >= ITEMS) break;
-    // the row's largest magnitude, as whole numbers (infinity and NaN are the largest)
-    const uint32_t top = __reduce_max_sync(kFullMask, big[k]);
-    const bool odd = top >= 0x7f800000u;  // a NaN or an infinity: the row's scores are NaN
-    // brings the largest to [2^10, 2^11) (a row that is below 2^-116 altogether: as near as a factor of 2^126 does)
-    const int shift = min(126, 137 - (int)(top >> 23));
-    const float up = __int_as_float((127 + shift) << 23);
-    const uint32_t v[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-    float x[8];
+  for (int t = 0; t < kFp4Terms; ++t) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = odd ? 0.f : __uint_as_float(v[i] << 16) * up;
-      x[2 * i + 1] = odd ? 0.f : __uint_as_float(v[i] & 0xffff0000u) * up;
-    }
-#pragma unroll
-    for (int t = 0; t < kFp4Terms; ++t) {
-      float a = fmaxf(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))),
-                      fmaxf(fmaxf(fabsf(x[4]), fabsf(x[5])), fmaxf(fabsf(x[6]), fabsf(x[7]))));
+    for (int k = 0; k < EACH; ++k) {
+      const int item = warp + 4 * k, col = item / C::SL, part = item % C::SL;
+      float(&y)[8] = x[k];
+      float a = fmaxf(fmaxf(fmaxf(fabsf(y[0]), fabsf(y[1])), fmaxf(fabsf(y[2]), fabsf(y[3]))),
+                      fmaxf(fmaxf(fabsf(y[4]), fabsf(y[5])), fmaxf(fabsf(y[6]), fabsf(y[7]))));
       a = fmaxf(a, __shfl_xor_sync(kFullMask, a, 1));
       uint16_t s8;
       asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s8) : "f"(0.f), "f"(a * (1.f / 6.f)));
@@ -176,32 +304,23 @@ __device__ __forceinline__ void write_query_terms(const Fp4Params& p, const Colu
           "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
           "mov.b32 %0, {a, b, c, d};\n\t}"
           : "=r"(codes)
-          : "f"(x[0] * r), "f"(x[1] * r), "f"(x[2] * r), "f"(x[3] * r), "f"(x[4] * r), "f"(x[5] * r), "f"(x[6] * r),
-            "f"(x[7] * r));
+          : "f"(y[0] * r), "f"(y[1] * r), "f"(y[2] * r), "f"(y[3] * r), "f"(y[4] * r), "f"(y[5] * r), "f"(y[6] * r),
+            "f"(y[7] * r));
       if (t + 1 < kFp4Terms) {
         uint32_t f[4];
         e2m1x8_to_f16x8(codes, f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 two = __half22float2(*reinterpret_cast<const __half2*>(&f[i]));
-          x[2 * i] = fmaf(-two.x, s, x[2 * i]);
-          x[2 * i + 1] = fmaf(-two.y, s, x[2 * i + 1]);
+          y[2 * i] = fmaf(-two.x, s, y[2 * i]);
+          y[2 * i + 1] = fmaf(-two.y, s, y[2 * i + 1]);
         }
       }
       const int n = t * C::CC + col;
-      *reinterpret_cast<uint32_t*>(smem + C::Q_OFFSET + code_offset<C>(n, part * 128 + lane * 4)) = codes;
-      if ((lane & 1) == 0)
-        smem[C::QSF_OFFSET + n * C::ROW_SF + part * 16 + lane / 2] = odd ? (uint8_t)0x7f : (uint8_t)s8;
+      *reinterpret_cast<uint32_t*>(q + code_offset<C>(n, part * 128 + lane * 4)) = codes;
+      if ((lane & 1) == 0) sf[n * C::ROW_SF + part * 16 + lane / 2] = odd[k] ? (uint8_t)0x7f : (uint8_t)s8;
     }
-    if (part == 0 && lane == 0)
-      reinterpret_cast<float*>(smem + C::COL_OFFSET)[col] = p.scale_log2 * __int_as_float((127 - shift) << 23);
   }
-  // rows beyond the terms: zeros
-  constexpr int USED = C::CC * kFp4Terms;
-  for (int i = warp * 32 + lane; i < (C::N - USED) * C::ROW_SF; i += 256) smem[C::QSF_OFFSET + USED * C::ROW_SF + i] = 0;
-  for (int i = warp * 32 + lane; i < (C::N - USED) * (C::D / 32); i += 256)
-    *reinterpret_cast<uint4*>(smem + C::Q_OFFSET + code_offset<C>(USED + i / (C::D / 32), (i % (C::D / 32)) * 16)) =
-        make_uint4(0u, 0u, 0u, 0u);
 }
 
 // 16 bytes global -> shared, counted by cp_async_arrive.
@@ -216,22 +335,8 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 // Four e4m3 scales: 0x80 in the bytes that are NaN.
 __device__ __forceinline__ uint32_t nan_scales(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
-__device__ __forceinline__ float ld_dsmem_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ float4 ld_dsmem_f32x4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-
 template <class C>
-__global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_constant__ Fp4Params p) {
+__global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_constant__ Fp4Params p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   constexpr int SB = C::S_BUFS, CH = C::CHUNKS, RINGS = C::NK + C::NV;
@@ -246,11 +351,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
   uint64_t* dq_done = vt_empty + 2;                                    // a tile's V^T all there
   uint64_t* p_full = dq_done + 1;                                      // [2]
   uint64_t* p_empty = p_full + 2;                                      // [2]: the tile is in the sums
+  uint64_t* q_full = p_empty + 2;                                      // [2] a segment's query terms there
+  uint64_t* qk_done = q_full + 2;                                      // a segment's scores all computed
+  uint64_t* o_full = qk_done + 1;                                      // a segment's sums complete
+  uint64_t* o_empty = o_full + 1;                                      // and read
+  uint64_t* l_full = o_empty + 1;                                      // [2] a segment's probabilities' sums there
+  uint64_t* l_empty = l_full + 2;                                      // [2] and read
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(full + C::NUM_BARS);
-  uint32_t* valid = reinterpret_cast<uint32_t*>(smem + C::VALID_OFFSET);
-  volatile uint32_t* failed_at = reinterpret_cast<uint32_t*>(smem + C::FAILED_OFFSET);
-  uint32_t* poison = reinterpret_cast<uint32_t*>(smem + C::POISON_OFFSET);
-  constexpr int kSfWarp = 4, kCodeWarp = 8, kScaleWarp = 10, kMmaWarp = 11;
+  volatile uint32_t* valid = reinterpret_cast<uint32_t*>(smem + C::VALID_OFFSET);
+  constexpr int kSfWarp = 4, kCodeWarp = 8, kScaleWarp = 10, kMmaWarp = 11, kEndWarp = 12;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool copies = warp >= kCodeWarp && warp <= kScaleWarp;
   const bool early = p.early_kv != 0 && copies;
@@ -267,6 +376,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
     mbar_init(sfk_ready, 4);
     mbar_init(sfv_ready, 4);
     mbar_init(dq_done, 1);
+    mbar_init(qk_done, 1);
+    mbar_init(o_full, 2);
+    mbar_init(o_empty, 4);
 #pragma unroll 1
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
@@ -275,6 +387,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
       mbar_init(&vt_empty[s], 1);
       mbar_init(&p_full[s], 4);
       mbar_init(&p_empty[s], 1);
+      mbar_init(&q_full[s], 4);
+      mbar_init(&l_full[s], 4);
+      mbar_init(&l_empty[s], 4);
     }
     fence_barrier_init();
   }
@@ -283,36 +398,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
     named_bar_sync(5, 3 * 32);
     named_bar_arrive(4, C::THREADS);
   }
-  if (!early) grid_dependency_wait();
-
-  const Columns<C> cm(p);
-  const int split = blockIdx.x, b = cm.b, g = cm.g;
-  const int cap = p.max_pages * p.page_size;
-  const int32_t* table = p.block_tables + (size_t)b * p.max_pages;
-  int L = p.seq_lens[b];
-  if (L < 0 || L > cap || (cm.T > 1 && L < cm.T)) {
-    if (tid == 0) atomicOr(p.err, kErrBadSeqLen);
-    L = L < 0 ? 0 : (L > cap ? cap : L);
+  if (!early) {
+    grid_dependency_wait();
+    grid_launch_dependents();
   }
-  // attended range [lo, hi) of the CTA's query rows: the union of their tokens' causal ranges
-  int j_last = cm.token(C::CC - 1);
-  if (j_last > cm.T - 1) j_last = cm.T - 1;
-  const int hi = max(0, L - cm.T + j_last + 1);
-  const int first_hi = L - cm.T + cm.token(0) + 1;
-  const int lo = (p.window > 0 && first_hi > p.window) ? first_hi - p.window : 0;
-  const int base = (lo / 16) * 16;
-  const long long piece_lo = (long long)base + (long long)split * p.chunk_tokens;
-  const int tlo = (int)min((long long)hi, piece_lo > lo ? piece_lo : lo);
-  const long long piece_hi = (split == p.num_splits - 1) ? (long long)hi : piece_lo + p.chunk_tokens;
-  const int thi = (int)(piece_hi < hi ? piece_hi : hi);
-  const int t_base = (tlo / 16) * 16;
-  const int tiles = thi > tlo ? (thi - t_base + kFp4Tile - 1) / kFp4Tile : 0;
-  if (!early) grid_launch_dependents();
-
-  float* red = reinterpret_cast<float*>(smem + C::RED_OFFSET);     // [4][CC]
-  float* my_lse = reinterpret_cast<float*>(smem + C::LSE_OFFSET);  // [CC]
-  float* coef = reinterpret_cast<float*>(smem + C::COEF_OFFSET);   // [CC]
-  float* my_out = reinterpret_cast<float*>(smem);                  // [CC][D], over the ring
   uint32_t tmem = 0;
   if (!copies) {
     // the barriers and tensor memory are there (the copies do not wait for the other warps)
@@ -322,35 +411,53 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
   }
   const uint32_t quarter = (uint32_t)(warp & 3) << 21;  // this warp's lanes of tensor memory
 
+  // A wait that runs out is reported; its role then goes through what is left of
+  // its loops without waiting (the copies and the products stop), so that all
+  // threads meet again.
+  bool good = true;
+  auto await = [&](uint64_t* bar, uint32_t phase) {
+    if (good && __any_sync(kFullMask, !mbar_wait(bar, phase & 1))) {
+      good = false;
+      if (lane == 0) atomicOr(p.err, kErrTimeout);
+    }
+  };
+  Walk<C> walk(p, lane);
+  Segment<C> seg, next;
+  bool any = walk.next(seg);
+  // page ids of tiles i .. i + 3 of a segment: lane l its 16 tokens 16 l ..
+  auto pages_of = [&](const Segment<C>& s, int i) {
+    const int t = s.t_base + i * kFp4Tile + lane * 16;
+    return t < s.thi ? __ldg(p.block_tables + (size_t)s.b * p.max_pages + t / p.page_size) : -1;
+  };
+
   if (copies) {
-    bool waited = !early;
+    // ---- copies, four tiles' page ids ahead (one tile ahead, their latency bound
+    // the kernel: 4 x 32768 tokens 77 -> 62 us)
+    bool waited = !early, stop = false;
     uint32_t err_bits = 0;
-    if (tiles > 0) {
-      // ---- copies. Rows four tiles at a time: lane l the 16 tokens 16 l .. of
-      // them, its page id fetched four tiles ahead (one tile ahead, its latency
-      // bound the kernel: 4 x 32768 tokens 77 -> 62 us).
-      const uint64_t policy = l2_evict_first_policy();
-      const int mine = warp - kCodeWarp;  // 0: K's codes, 1: V's (K = V: the lower and the upper half), 2: scales
-      const int fresh_from = L - p.query_tokens;  // rows from here on may still be written by the kernel in front
-      auto page_of = [&](int i) {
-        const int t = t_base + i * kFp4Tile + lane * 16;
-        return t < thi ? __ldg(table + t / p.page_size) : -1;
-      };
-      int page = page_of(0), rows = -1;
-      bool stop = false;
-      int done = 0;  // tiles whose copies went out
+    const uint64_t policy = l2_evict_first_policy();
+    const int mine = warp - kCodeWarp;  // 0: K's codes, 1: V's (K = V: the lower and the upper half), 2: scales
+    int page = any ? pages_of(seg, 0) : -1, rows = -1;
+    int it = 0;  // tiles whose copies went out
+    while (any && !stop) {
+      const bool more = walk.next(next);
+      const int g = seg.y / p.col_tiles;
 #pragma unroll 1
-      for (int i = 0; i < tiles && !stop; ++i) {
+      for (int i = 0; i < seg.tiles; ++i) {
         if ((i & 3) == 0) {
-          const int t = t_base + i * kFp4Tile + lane * 16;
+          const int t = seg.t_base + i * kFp4Tile + lane * 16;
           const bool here = (unsigned)page < (unsigned)p.num_pages;
-          if (t < thi && !here) err_bits |= kErrBadPage;
-          rows = t < thi && here ? (page * p.num_kv_heads + g) * p.page_size + t % p.page_size : -1;
-          page = page_of(i + 4);
+          if (t < seg.thi && !here) err_bits |= kErrBadPage;
+          rows = t < seg.thi && here ? (page * p.num_kv_heads + g) * p.page_size + t % p.page_size : -1;
+          page = i + 4 < seg.tiles ? pages_of(seg, i + 4) : more ? pages_of(next, 0) : -1;
         }
         const int row0 = __shfl_sync(kFullMask, rows, (i & 3) * 8 + (lane & 7));
         const uint32_t bits = __ballot_sync(kFullMask, row0 >= 0) & 0xffu;
-        if (!waited && (i >= C::NK || (!C::KVS && i >= C::NV) || t_base + (i + 1) * kFp4Tile > fresh_from)) {
+        const bool last = i + 1 == seg.tiles;
+        const uint32_t word = bits | (i == 0 ? kTileFirst : 0u) | (last ? kTileLast : 0u) | (last && !more ? kTileEnd : 0u);
+        // rows of the newest tokens may still be written by the kernel in front
+        if (!waited && (it >= C::NK || (!C::KVS && it >= C::NV) ||
+                        seg.t_base + (i + 1) * kFp4Tile > seg.L - p.query_tokens)) {
           grid_dependency_wait();
           grid_launch_dependents();
           waited = true;
@@ -358,7 +465,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
 #pragma unroll
         for (int v = 0; v < (C::KVS ? 1 : 2); ++v) {
           if (!C::KVS && mine != 2 && mine != v) continue;
-          const int n = v ? C::NV : C::NK, st = (v ? C::NK : 0) + i % n, round = i / n;
+          const int n = v ? C::NV : C::NK, st = (v ? C::NK : 0) + it % n, round = it / n;
           if (round > 0) {
             const bool freed = mbar_wait(&empty[st], (round - 1) & 1);
             if (__any_sync(kFullMask, !freed)) {
@@ -371,7 +478,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
           if (mine < 2) {
             const uint32_t part = C::KVS ? (mine ? bits & 0xf0u : bits & 0x0fu) : bits;
             if (lane == 0) {
-              if (!C::KVS || mine == 0) valid[st] = bits;
+              if (!C::KVS || mine == 0) valid[st] = word;
               if (part)
                 mbar_arrive_expect_tx(&full[st], __popc(part) * (16 * C::D / 2) + (mine == 0 ? p.stall_bytes : 0));
               else
@@ -395,16 +502,19 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
             cp_async_arrive(&full[st]);
           }
         }
-        if (!stop) done = i + 1;
+        if (stop) break;
+        ++it;
       }
-      // no copy may still be landing when the shared memory is used for something else
-      const unsigned long long deadline = global_timer_ns() + kWaitTimeoutNs;
-      for (int s = lane; s < RINGS; s += 32) {
-        const int n = s < C::NK ? C::NK : C::NV, at = s < C::NK ? s : s - C::NK;
-        if (at >= done || (!C::KVS && mine != 2 && (s >= C::NK) != (mine == 1))) continue;
-        const int last = at + n * ((done - 1 - at) / n);
-        if (!mbar_wait_until(&full[s], (last / n) & 1, deadline)) err_bits |= kErrTimeout;
-      }
+      seg = next;
+      any = more;
+    }
+    // no copy may still be landing when the CTA ends
+    const unsigned long long deadline = global_timer_ns() + kWaitTimeoutNs;
+    for (int s = lane; s < RINGS; s += 32) {
+      const int n = s < C::NK ? C::NK : C::NV, at = s < C::NK ? s : s - C::NK;
+      if (at >= it || (!C::KVS && mine != 2 && (s >= C::NK) != (mine == 1))) continue;
+      const int last = at + n * ((it - 1 - at) / n);
+      if (!mbar_wait_until(&full[s], (last / n) & 1, deadline)) err_bits |= kErrTimeout;
     }
     if (!waited) {
       grid_dependency_wait();
@@ -412,67 +522,45 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
     }
     err_bits = __reduce_or_sync(kFullMask, err_bits);
     if (lane == 0 && err_bits) atomicOr(p.err, err_bits);
-  } else if (tiles > 0) {
-    bool good = true;
-    if (warp < 8) {
-      // the query's terms, the unit matrix and P's unused rows
-      write_query_terms<C>(p, cm, smem, warp, lane);
-      for (int i = tid; i < C::EYE_BYTES / 16; i += 256) {
-        // 16 bytes of row m: dims 32 c ..; its one lies at dim m (e2m1 1.0 is 2)
-        const int m = i >> 2, c = (i & 3) ^ ((m >> 1) & 3);
-        const uint32_t one = (m >> 5) == c ? 2u << (4 * (m & 7)) : 0u;
-        const int word = (m >> 3) & 3;
-        *reinterpret_cast<uint4*>(smem + C::EYE_OFFSET + (m >> 3) * 512 + (m & 7) * 64 + (i & 3) * 16) =
-            make_uint4(word == 0 ? one : 0u, word == 1 ? one : 0u, word == 2 ? one : 0u, word == 3 ? one : 0u);
-      }
-      for (int i = tid; i < 2 * C::P_BYTES / 16; i += 256) {
-        const int row = ((i >> 6) & 1) * 8 + ((i >> 3) & 7);  // [slab][2 groups][8 rows][128 B]
-        if (row >= C::CC) *reinterpret_cast<uint4*>(smem + C::P_OFFSET + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-      }
-      if (tid < C::CC) poison[tid] = 0u;
-      if (tid == 0) *failed_at = 0u;
-      fence_proxy_async_smem();
+  } else if (warp < kSfWarp) {
+    // ---- softmax: rows 32 warp .. + 31 of every tile
+    const uint32_t p_at = smem_u32(smem + C::P_OFFSET) + warp * 1024 + (lane & 3) * 4;
+    if (C::CC < 8) {  // P's unused columns
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        for (int i = lane; i < (8 - C::CC) * 8; i += 32)
+          *reinterpret_cast<uint4*>(smem + C::P_OFFSET + k * C::P_BYTES + warp * 1024 + C::CC * 128 + i * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
     }
-    named_bar_sync(1, 9 * 32);  // warps 0-7 and the products'
-
-    if (warp < kSfWarp) {
-      // ---- softmax: rows 32 warp .. + 31 of every tile
+    float* top_of = reinterpret_cast<float*>(smem + C::TOP_OFFSET);  // [4][CC]
+    int page = any ? pages_of(seg, 0) : -1;
+    uint32_t blocks = 0;
+    int it = 0;
+#pragma unroll 1
+    for (int sg = 0; any; ++sg) {
+      const bool more = walk.next(next);
+      const Columns<C> cm(p, seg.b, seg.y);
+      if (seg.bad && tid == 0) atomicOr(p.err, kErrBadSeqLen);
+      await(&q_full[sg & 1], sg >> 1);
       float col_mul[C::CC], ref[C::CC], sum[C::CC];
       int col_hi[C::CC], col_lo[C::CC];
 #pragma unroll
       for (int c = 0; c < C::CC; ++c) {
-        col_mul[c] = reinterpret_cast<const float*>(smem + C::COL_OFFSET)[c];
-        col_hi[c] = cm.valid(c) ? min(thi, L - cm.T + cm.token(c) + 1) : 0;
-        col_lo[c] = max(tlo, (p.window > 0 && cm.valid(c)) ? L - cm.T + cm.token(c) + 1 - p.window : 0);
+        col_mul[c] = reinterpret_cast<const float*>(smem + C::COL_OFFSET)[(sg & 1) * C::CC + c];
+        const int end = seg.col_hi(p, cm, c);
+        col_hi[c] = cm.valid(c) ? min(seg.thi, end) : 0;
+        col_lo[c] = max(seg.tlo, p.window > 0 ? end - p.window : 0);
         ref[c] = -INFINITY;
         sum[c] = 0.f;
       }
-      const uint32_t p_at = smem_u32(smem + C::P_OFFSET) + warp * 2048 + (lane & 3) * 4;
-      // whether a tile's 16-token blocks have a page: lane l block l of four tiles, as the copies take them
-      auto page_of = [&](int i) {
-        const int t = t_base + i * kFp4Tile + lane * 16;
-        return t < thi ? __ldg(table + t / p.page_size) : -1;
-      };
-      int page = page_of(0);
-      uint32_t blocks = 0;
-      // The four warps leave together: one whose wait ran out says so at the next
-      // tile's barrier.
-      auto give_up = [&]() {
-        good = false;
-        if (lane == 0) *failed_at = 1u;
-        __syncwarp();
-      };
 #pragma unroll 1
-      for (int i = 0; i < tiles; ++i) {
-        const int sbuf = i % SB, buf = i & 1;
+      for (int i = 0; i < seg.tiles; ++i, ++it) {
+        const int sbuf = it % SB, buf = it & 1;
         if ((i & 3) == 0) {
           blocks = __ballot_sync(kFullMask, (unsigned)page < (unsigned)p.num_pages);
-          page = page_of(i + 4);
+          page = i + 4 < seg.tiles ? pages_of(seg, i + 4) : more ? pages_of(next, 0) : -1;
         }
-        if (good) {
-          const bool scored = mbar_wait(&s_full[sbuf], (i / SB) & 1);
-          if (__any_sync(kFullMask, !scored)) give_up();
-        }
+        await(&s_full[sbuf], it / SB);
         tmem_fence_after();
         float s[C::CC];
         {
@@ -491,42 +579,37 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
         tmem_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_empty[sbuf]);
-        const int row = warp * 32 + lane, t = t_base + i * kFp4Tile + row;
+        const int row = warp * 32 + lane, t = seg.t_base + i * kFp4Tile + row;
         const bool ok = (blocks >> ((i & 3) * 8 + (row >> 4))) & 1u;
-        bool above = !good;
+        bool above = false;
 #pragma unroll
         for (int c = 0; c < C::CC; ++c) {
           if (!(ok && t >= col_lo[c] && t < col_hi[c])) s[c] = -INFINITY;
           above = above || s[c] > ref[c] + kRefRange;
         }
         if (named_bar_or(2, 128, above)) {
-          if (*failed_at) {
-            good = false;
-            break;
-          }
           // new references: the tile's maximum, where that is out of reach
 #pragma unroll
           for (int c = 0; c < C::CC; ++c) {
             const int top = __reduce_max_sync(kFullMask, ordered(isnan(s[c]) ? -INFINITY : s[c]));
-            if (lane == 0) red[warp * C::CC + c] = unordered(top);
+            if (lane == 0) top_of[warp * C::CC + c] = unordered(top);
           }
           named_bar_sync(2, 128);
           float f[C::CC];
           bool held = false;
 #pragma unroll
           for (int c = 0; c < C::CC; ++c) {
-            const float top = fmaxf(fmaxf(red[c], red[C::CC + c]), fmaxf(red[2 * C::CC + c], red[3 * C::CC + c]));
+            const float top = fmaxf(fmaxf(top_of[c], top_of[C::CC + c]), fmaxf(top_of[2 * C::CC + c], top_of[3 * C::CC + c]));
             const bool up = top > ref[c] + kRefRange;
             f[c] = up && ref[c] != -INFINITY ? ex2(ref[c] - top) : 1.f;
             held = held || f[c] != 1.f;
             sum[c] *= f[c];
             if (up) ref[c] = top;
           }
-          named_bar_sync(2, 128);  // red may be written again
+          named_bar_sync(2, 128);  // the maxima may be written again
           if (held) {
             // sums that hold something: rescaled once the tiles before are in them
-            const bool summed = mbar_wait(&p_empty[(i - 1) & 1], ((i - 1) >> 1) & 1);
-            if (__any_sync(kFullMask, !summed)) give_up();
+            await(&p_empty[(it - 1) & 1], (it - 1) >> 1);
             tmem_fence_after();
 #pragma unroll 1
             for (int c0 = 0; c0 < CH; ++c0) {
@@ -541,10 +624,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
             tmem_fence_before();
           }
         }
-        if (i >= 2) {
-          const bool freed = mbar_wait(&p_empty[buf], ((i >> 1) - 1) & 1);
-          if (__any_sync(kFullMask, !freed)) give_up();
-        }
+        if (it >= 2) await(&p_empty[buf], (it >> 1) - 1);
 #pragma unroll
         for (int c = 0; c < C::CC; ++c) {
           // rounded to tf32 here, to nearest (the product would cut it off); the sum takes what the product takes
@@ -552,43 +632,37 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
           const float e = ex2(s[c] - (ref[c] == -INFINITY ? 0.f : ref[c]));
           asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(w) : "f"(e));
           sum[c] += __uint_as_float(w);
-          const uint32_t at = p_at + buf * C::P_BYTES + (c >> 3) * 1024 + (c & 7) * 128 + (((lane >> 2) ^ (c & 7)) << 4);
+          const uint32_t at = p_at + buf * C::P_BYTES + c * 128 + (((lane >> 2) ^ c) << 4);
           asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(w) : "memory");
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[buf]);
       }
-      if (!good && lane == 0) atomicOr(p.err, kErrTimeout);
+      float* sum_of = reinterpret_cast<float*>(smem + C::SUM_OFFSET) + (sg & 1) * 5 * C::CC;  // [4][CC], references
+      if (sg >= 2) await(&l_empty[sg & 1], (sg >> 1) - 1);
 #pragma unroll
       for (int c = 0; c < C::CC; ++c) {
         float l = sum[c];
 #pragma unroll
         for (int m = 16; m; m >>= 1) l += __shfl_xor_sync(kFullMask, l, m);
-        if (lane == 0) red[warp * C::CC + c] = l;
-        if (tid == 0) my_lse[c] = ref[c];
+        if (lane == 0) sum_of[warp * C::CC + c] = l;
+        if (tid == 0) sum_of[4 * C::CC + c] = ref[c];
       }
-    } else if (warp < kCodeWarp) {
-      // ---- scales into tensor memory: lane l, column 4 k + j holds the 4 scales of row l + 32 j, dims 64 k ..;
-      // every quarter of the lanes all rows'
-      {
-        uint32_t one[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) one[k] = 0x38383838u;  // e4m3 1.0
-        tmem_st(tmem + kTmemSfi + quarter, one);
-#pragma unroll
-        for (int k0 = 0; k0 < C::KSTEPS; k0 += 2) {
-          uint32_t r8[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int row = lane + 32 * (i & 3);
-            r8[i] = row < C::N ? *reinterpret_cast<const uint32_t*>(smem + C::QSF_OFFSET + row * C::ROW_SF +
-                                                                    (k0 + (i >> 2)) * 4)
-                               : 0u;
-          }
-          tmem_st(tmem + kTmemSfq + quarter + k0 * 4, r8);
-        }
-      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&l_full[sg & 1]);
+      seg = next;
+      any = more;
+    }
+  } else if (warp < kCodeWarp) {
+    // ---- scales into tensor memory: lane l, column 4 k + j holds the 4 scales of row l + 32 j, dims 64 k ..;
+    // every quarter of the lanes all rows'
+    uint32_t* poison_of = reinterpret_cast<uint32_t*>(smem + C::POISON_OFFSET);
+    int it = 0;
+#pragma unroll 1
+    for (int sg = 0; any; ++sg) {
+      const Columns<C> cm(p, seg.b, seg.y);
+      uint32_t* poison = poison_of + (sg & 3) * C::CC;
       auto put = [&](const uint8_t* sf, uint32_t at, bool v, uint32_t here, int t0) {
         uint32_t x[C::KSTEPS * 4];  // [64 dims][row group]
 #pragma unroll
@@ -604,11 +678,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
         }
         if (v) {
           // V's rows that do not count have scale 0: their probabilities are 0, but 0 * NaN is NaN
-          if (!(here == 0xffu && t0 >= tlo && t0 + kFp4Tile <= thi)) {
+          if (!(here == 0xffu && t0 >= seg.tlo && t0 + kFp4Tile <= seg.thi)) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int row = lane + 32 * j, t = t0 + row;
-              if (((here >> (row >> 4)) & 1u) && t >= tlo && t < thi) continue;
+              if (((here >> (row >> 4)) & 1u) && t >= seg.tlo && t < seg.thi) continue;
 #pragma unroll
               for (int k = 0; k < C::KSTEPS; ++k) x[k * 4 + j] = 0u;
             }
@@ -628,7 +702,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
               if (warp != kSfWarp) continue;
               const int t = t0 + lane + 32 * (k & 3);
               for (int c = 0; c < C::CC && cm.valid(c); ++c) {
-                const int end = L - cm.T + cm.token(c) + 1;
+                const int end = seg.col_hi(p, cm, c);
                 if (t >= end || (p.window > 0 && t < end - p.window)) continue;
                 for (int y = 0; y < 4; ++y)
                   if ((nan >> (8 * y + 7)) & 1u) atomicOr(&poison[c], 1u << ((k >> 2) * 4 + y));
@@ -648,208 +722,292 @@ __global__ void __launch_bounds__(C::THREADS, 1) stage1_fp4_kernel(const __grid_
         __syncwarp();
       };
 #pragma unroll 1
-      for (int i = 0; i < tiles; ++i) {
+      for (int i = 0; i < seg.tiles; ++i, ++it) {
         // K's, once the product before has read the last tile's
-        const int st = i % C::NK;
-        bool ready = mbar_wait(&full[st], (i / C::NK) & 1);
-        if (ready && i > 0) ready = mbar_wait(&s_full[(i - 1) % SB], ((i - 1) / SB) & 1);
-        if (__any_sync(kFullMask, !ready)) {
-          good = false;
-          break;
-        }
+        const int st = it % C::NK;
+        await(&full[st], it / C::NK);
+        if (it > 0) await(&s_full[(it - 1) % SB], (it - 1) / SB);
         tmem_fence_after();
         put(smem + st * C::ITEM_BYTES + C::CODE_BYTES, tmem + kTmemSfk + quarter, false, 0u, 0);
         if (lane == 0) mbar_arrive(sfk_ready);
         // V's likewise
-        const int n = C::KVS ? C::NK : C::NV, sv = (C::KVS ? 0 : C::NK) + i % n;
-        ready = C::KVS || mbar_wait(&full[sv], (i / n) & 1);
-        if (ready && i > 0) ready = mbar_wait(dq_done, (i - 1) & 1);
-        if (__any_sync(kFullMask, !ready)) {
-          good = false;
-          break;
-        }
+        const int n = C::KVS ? C::NK : C::NV, sv = (C::KVS ? 0 : C::NK) + it % n;
+        if (!C::KVS) await(&full[sv], it / n);
+        if (it > 0) await(dq_done, it - 1);
         tmem_fence_after();
-        const uint32_t here = valid[sv];
-        const int t0 = t_base + i * kFp4Tile;
-        put(smem + sv * C::ITEM_BYTES + C::CODE_BYTES, tmem + kTmemSfv + quarter, true, here, t0);
+        put(smem + sv * C::ITEM_BYTES + C::CODE_BYTES, tmem + kTmemSfv + quarter, true, valid[sv] & 0xffu,
+            seg.t_base + i * kFp4Tile);
         if (lane == 0) mbar_arrive(sfv_ready);
       }
-      if (!good && lane == 0) atomicOr(p.err, kErrTimeout);
-    } else {
-      // ---- the products, by one warp in an order that keeps the tensor core busy
-      // (issued by three warps, a product each, they got in one another's way:
-      // a tf32 instruction took 62 cycles instead of 14). Chunks of 128 dims go
-      // in pairs, V^T of both and then both sums, so that one waits for its
-      // operand while the other runs; the next tile's scores go out between
-      // them, as soon as they can.
-      constexpr uint32_t kQk = (1u << 7) | (1u << 10) | ((uint32_t)(C::N / 8) << 17) | (8u << 24);  // e2m1, e4m3 scales
-      constexpr uint32_t kDq = (1u << 7) | (1u << 10) | ((uint32_t)(kFp4Tile / 8) << 17) | (8u << 24);
-      constexpr uint32_t kPv = (1u << 4) | (2u << 7) | (2u << 10) | (2u << 17) | (8u << 24);  // tf32 -> fp32, 128 x 16
-      if (elect_one()) {
-        // descriptors' bases; a step further is a constant added to the address field
-        const uint64_t ring_desc = smem_desc(smem_u32(smem), 0, C::SL * 1024);
-        const uint64_t q_desc = smem_desc(smem_u32(smem + C::Q_OFFSET), 0, C::SL * 1024);
-        const uint64_t eye_desc = smem_desc(smem_u32(smem + C::EYE_OFFSET), 0, 512, 64);
-        const uint64_t p_desc = smem_desc(smem_u32(smem + C::P_OFFSET), 0, 1024);
-        constexpr int kItem = C::ITEM_BYTES >> 4;
-        int scores = 0, widened = 0, summed = 0;  // tiles, chunks, chunks issued so far
-        auto qk = [&](int i) {
-          tmem_fence_after();
-          const int st = i % C::NK, sbuf = i % SB;
-          const uint64_t a = ring_desc + st * kItem;
+      any = walk.next(seg);
+    }
+  } else if (warp == kMmaWarp) {
+    // ---- the products, by one lane in an order that keeps the tensor core busy
+    // (issued by three warps, a product each, they got in one another's way: a
+    // tf32 instruction took 62 cycles instead of 14). Chunks of 128 dims go in
+    // pairs, V^T of both and then both sums, so that one waits for its operand
+    // while the other runs; the next tile's scores go out between them, as soon
+    // as they can.
+    constexpr uint32_t kQk = (1u << 7) | (1u << 10) | ((uint32_t)(C::N / 8) << 17) | (8u << 24);  // e2m1, e4m3 scales
+    constexpr uint32_t kDq = (1u << 7) | (1u << 10) | ((uint32_t)(kFp4Tile / 8) << 17) | (8u << 24);
+    constexpr uint32_t kPv = (1u << 4) | (2u << 7) | (2u << 10) | (2u << 17) | (8u << 24);  // tf32 -> fp32, 128 x 16
+    if (any && elect_one()) {
+      // descriptors' bases; a step further is a constant added to the address field
+      const uint64_t ring_desc = smem_desc(smem_u32(smem), 0, C::SL * 1024);
+      const uint64_t q_desc = smem_desc(smem_u32(smem + C::Q_OFFSET), 0, C::SL * 1024);
+      const uint64_t eye_desc = smem_desc(smem_u32(smem + C::EYE_OFFSET), 0, 512, 64);
+      // (both 8-column groups of P are the same one: the upper columns are not read)
+      const uint64_t p_desc = smem_desc(smem_u32(smem + C::P_OFFSET), 0, 0);
+      constexpr int kItem = C::ITEM_BYTES >> 4;
+      int scores = 0, widened = 0, summed = 0;  // tiles, chunks, chunks issued so far
+      int q_seg = -1, o_seg = -1;               // segments of the newest scores and sums
+      auto qk = [&](int i) {
+        tmem_fence_after();
+        const int st = i % C::NK, sbuf = i % SB;
+        const uint32_t word = valid[st];
+        if (word & kTileFirst) ++q_seg;
+        const uint64_t a = ring_desc + st * kItem, q = q_desc + (q_seg & 1) * (C::Q_BYTES >> 4);
 #pragma unroll
-          for (int k = 0; k < C::KSTEPS; ++k)
-            mma_fp4(tmem + kTmemS + sbuf * C::N, a + (k >> 2) * 64 + (k & 3) * 2, q_desc + (k >> 2) * 64 + (k & 3) * 2, kQk,
-                    tmem + kTmemSfk + k * 4, tmem + kTmemSfq + k * 4, k > 0);
-          mma_commit<1>(&s_full[sbuf]);
-          mma_commit<1>(&empty[st]);
-          scores = i + 1;
-        };
-        auto may_qk = [&](int i) {  // without waiting
-          return mbar_test(&full[i % C::NK], (i / C::NK) & 1) && mbar_test(sfk_ready, i & 1) &&
-                 (i < SB || mbar_test(&s_empty[i % SB], (i / SB - 1) & 1));
-        };
+        for (int k = 0; k < C::KSTEPS; ++k)
+          mma_fp4(tmem + kTmemS + sbuf * C::N, a + (k >> 2) * 64 + (k & 3) * 2, q + (k >> 2) * 64 + (k & 3) * 2, kQk,
+                  tmem + kTmemSfk + k * 4, tmem + kTmemSfq + k * 4, k > 0);
+        mma_commit<1>(&s_full[sbuf]);
+        mma_commit<1>(&empty[st]);
+        if (word & kTileLast) mma_commit<1>(qk_done);
+        scores = i + 1;
+      };
+      auto may_qk = [&](int i) {  // without waiting
+        const int st = i % C::NK, sn = q_seg + 1;
+        return mbar_test(&full[st], (i / C::NK) & 1) && mbar_test(sfk_ready, i & 1) &&
+               (i < SB || mbar_test(&s_empty[i % SB], (i / SB - 1) & 1)) &&
+               (!(valid[st] & kTileFirst) || mbar_test(&q_full[sn & 1], (sn >> 1) & 1));
+      };
+      bool end = false;
 #pragma unroll 1
-        for (int i = 0; i < tiles && good; ++i) {
-          if (scores == i) {
-            good = mbar_wait(&full[i % C::NK], (i / C::NK) & 1) && mbar_wait(sfk_ready, i & 1) &&
-                   (i < SB || mbar_wait(&s_empty[i % SB], (i / SB - 1) & 1));
-            if (!good) break;
-            qk(i);
-          }
-          const int n = C::KVS ? C::NK : C::NV, st = (C::KVS ? 0 : C::NK) + i % n;
-          good = mbar_wait(&full[st], (i / n) & 1) && mbar_wait(sfv_ready, i & 1);
-          const uint64_t v = ring_desc + st * kItem;
-          const uint64_t pd = p_desc + (i & 1) * (C::P_BYTES >> 4);
+      for (int i = 0; good && !end; ++i) {
+        if (scores == i) {
+          const int sk = i % C::NK, sn = q_seg + 1;
+          good = mbar_wait(&full[sk], (i / C::NK) & 1) && mbar_wait(sfk_ready, i & 1) &&
+                 (i < SB || mbar_wait(&s_empty[i % SB], (i / SB - 1) & 1)) &&
+                 (!(valid[sk] & kTileFirst) || mbar_wait(&q_full[sn & 1], (sn >> 1) & 1));
+          if (!good) break;
+          qk(i);
+        }
+        const int n = C::KVS ? C::NK : C::NV, st = (C::KVS ? 0 : C::NK) + i % n;
+        good = mbar_wait(&full[st], (i / n) & 1) && mbar_wait(sfv_ready, i & 1);
+        if (!good) break;
+        const uint32_t word = valid[st];
+        const bool first = (word & kTileFirst) != 0;
+        end = (word & kTileEnd) != 0;
+        if (first) ++o_seg;
+        const uint64_t v = ring_desc + st * kItem;
+        const uint64_t pd = p_desc + (i & 1) * (C::P_BYTES >> 4);
 #pragma unroll 1
-          for (int c0 = 0; c0 < CH && good; c0 += 2) {
-            const int at = i * CH + c0;  // (even)
+        for (int c0 = 0; c0 < CH && good; c0 += 2) {
+          const int at = i * CH + c0;  // (even)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              if (good && at > 0) good = mbar_wait(&vt_empty[c], ((at >> 1) - 1) & 1);
-              if (!good) break;
-              tmem_fence_after();
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
-                mma_fp4(tmem + kTmemVt + c * 128, eye_desc + j * 2, v + (c0 >> 1) * 64 + c * 4 + j * 2, kDq, tmem + kTmemSfi,
-                        tmem + kTmemSfv + c0 * 8 + (c * 2 + j) * 4, j > 0);
-              mma_commit<1>(&vt_full[c]);
-              widened = at + c + 1;
-            }
+          for (int c = 0; c < 2; ++c) {
+            if (good && at > 0) good = mbar_wait(&vt_empty[c], ((at >> 1) - 1) & 1);
             if (!good) break;
-            if (c0 + 2 == CH) {
-              mma_commit<1>(&empty[st]);
-              mma_commit<1>(dq_done);
-            }
-            if (i + 1 < tiles && scores == i + 1 && may_qk(i + 1)) qk(i + 1);
-            if (c0 == 0) good = mbar_wait(&p_full[i & 1], (i >> 1) & 1);
+            tmem_fence_after();
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              if (good) good = mbar_wait(&vt_full[c], (at >> 1) & 1);
-              if (!good) break;
-              tmem_fence_after();
-#pragma unroll
-              for (int q = 0; q < kFp4Tile / 8; ++q)
-                mma_tf32(tmem + kTmemO + c0 * 16 + c * 16, tmem + kTmemVt + c * 128 + q * 8, pd + (q >> 2) * 128 + (q & 3) * 2,
-                         kPv, i > 0 || q > 0);
-              mma_commit<1>(&vt_empty[c]);
-              summed = at + c + 1;
-            }
-            if (good && c0 + 2 == CH) mma_commit<1>(&p_empty[i & 1]);
-            if (good && i + 1 < tiles && scores == i + 1 && may_qk(i + 1)) qk(i + 1);
+            for (int j = 0; j < 2; ++j)
+              mma_fp4(tmem + kTmemVt + c * 128, eye_desc + j * 2, v + (c0 >> 1) * 64 + c * 4 + j * 2, kDq, tmem + kTmemSfi,
+                      tmem + kTmemSfv + c0 * 8 + (c * 2 + j) * 4, j > 0);
+            mma_commit<1>(&vt_full[c]);
+            widened = at + c + 1;
           }
+          if (!good) break;
+          if (c0 + 2 == CH) {
+            mma_commit<1>(&empty[st]);
+            mma_commit<1>(dq_done);
+          }
+          if (!end && scores == i + 1 && may_qk(i + 1)) qk(i + 1);
+          if (c0 == 0) good = mbar_wait(&p_full[i & 1], (i >> 1) & 1) &&
+                              (!first || o_seg == 0 || mbar_wait(o_empty, (o_seg - 1) & 1));
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            if (good) good = mbar_wait(&vt_full[c], (at >> 1) & 1);
+            if (!good) break;
+            tmem_fence_after();
+#pragma unroll
+            for (int q = 0; q < kFp4Tile / 8; ++q)
+              mma_tf32(tmem + kTmemO + c0 * 16 + c * 16, tmem + kTmemVt + c * 128 + q * 8, pd + (q >> 2) * 64 + (q & 3) * 2,
+                       kPv, !first || q > 0);
+            mma_commit<1>(&vt_empty[c]);
+            summed = at + c + 1;
+          }
+          if (!good) break;
+          if (c0 + 2 == CH) {
+            mma_commit<1>(&p_empty[i & 1]);
+            if (word & kTileLast) {
+              mma_commit<1>(o_full);
+              mbar_arrive(o_full);  // (orders what this lane has seen of the scale warps' marks)
+            }
+          }
+          if (!end && scores == i + 1 && may_qk(i + 1)) qk(i + 1);
         }
-        // what was issued ends before its operands and results are used for something else
-        if (!good) {
-          if (scores > 0) mbar_wait(&s_full[(scores - 1) % SB], ((scores - 1) / SB) & 1);
-          if (widened > 0) mbar_wait(&vt_full[(widened - 1) & 1], ((widened - 1) >> 1) & 1);
-          atomicOr(p.err, kErrTimeout);
+      }
+      // what was issued ends before its operands and results are used for something else
+      if (!good) {
+        if (scores > 0) mbar_wait(&s_full[(scores - 1) % SB], ((scores - 1) / SB) & 1);
+        if (widened > 0) mbar_wait(&vt_full[(widened - 1) & 1], ((widened - 1) >> 1) & 1);
+        atomicOr(p.err, kErrTimeout);
+      }
+      if (summed > 0) mbar_wait(&vt_empty[(summed - 1) & 1], ((summed - 1) >> 1) & 1);
+    }
+    __syncwarp();
+  } else {
+    // ---- the next segment's query terms, and a segment's results
+    const int we = warp - kEndWarp, wt = tid - kEndWarp * 32;
+    uint32_t* poison_of = reinterpret_cast<uint32_t*>(smem + C::POISON_OFFSET);
+    volatile uint32_t* ticket = reinterpret_cast<uint32_t*>(smem + C::MISC_OFFSET);
+    // the unit matrix in e2m1 (1.0 is 2): 16 bytes of row m hold dims 32 c .., the one lies at dim m
+    for (int i = wt; i < C::EYE_BYTES / 16; i += 128) {
+      const int m = i >> 2, c = (i & 3) ^ ((m >> 1) & 3), word = (m >> 3) & 3;
+      const uint32_t one = (m >> 5) == c ? 2u << (4 * (m & 7)) : 0u;
+      *reinterpret_cast<uint4*>(smem + C::EYE_OFFSET + (m >> 3) * 512 + (m & 7) * 64 + (i & 3) * 16) =
+          make_uint4(word == 0 ? one : 0u, word == 1 ? one : 0u, word == 2 ? one : 0u, word == 3 ? one : 0u);
+    }
+    // the query rows beyond the terms, and the marks
+    constexpr int USED = C::CC * kFp4Terms, REST = (C::N - USED) * (C::D / 32);  // 16-byte pieces of a buffer
+    for (int i = wt; i < (C::N - USED) * C::ROW_SF; i += 128) smem[C::QSF_OFFSET + USED * C::ROW_SF + i] = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      for (int i = wt; i < REST; i += 128)
+        *reinterpret_cast<uint4*>(smem + C::Q_OFFSET + k * C::Q_BYTES +
+                                  code_offset<C>(USED + i / (C::D / 32), (i % (C::D / 32)) * 16)) =
+            make_uint4(0u, 0u, 0u, 0u);
+    for (int i = wt; i < 4 * C::CC; i += 128) poison_of[i] = 0u;
+    {
+      uint32_t one[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) one[k] = 0x38383838u;  // e4m3 1.0
+      tmem_st(tmem + kTmemSfi + quarter, one);
+    }
+    auto prepare = [&](int sg, const Segment<C>& s) {
+      named_bar_sync(3, 128);  // the scales of the segment before are in tensor memory
+      // (its terms' buffer: the scores of the last segment but one are computed, as this warp has seen)
+      write_query_terms<C>(p, Columns<C>(p, s.b, s.y), smem + C::Q_OFFSET + (sg & 1) * C::Q_BYTES, smem + C::QSF_OFFSET,
+                           reinterpret_cast<float*>(smem + C::COL_OFFSET) + (sg & 1) * C::CC, we, lane);
+      fence_proxy_async_smem();
+      named_bar_sync(3, 128);
+      if (sg > 0) await(qk_done, sg - 1);
+      tmem_fence_after();
+#pragma unroll
+      for (int k0 = 0; k0 < C::KSTEPS; k0 += 2) {
+        uint32_t r8[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = lane + 32 * (i & 3);
+          r8[i] = row < C::N
+                      ? *reinterpret_cast<const uint32_t*>(smem + C::QSF_OFFSET + row * C::ROW_SF + (k0 + (i >> 2)) * 4)
+                      : 0u;
         }
-        if (summed > 0) mbar_wait(&vt_empty[(summed - 1) & 1], ((summed - 1) >> 1) & 1);
+        tmem_st(tmem + kTmemSfq + quarter + k0 * 4, r8);
+      }
+      tmem_wait_st();
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[sg & 1]);
+    };
+    if (any) prepare(0, seg);
+#pragma unroll 1
+    for (int sg = 0; any; ++sg) {
+      const bool more = walk.next(next);
+      if (more) prepare(sg + 1, next);
+      const Columns<C> cm(p, seg.b, seg.y);
+      await(&l_full[sg & 1], sg >> 1);
+      await(o_full, sg);
+      tmem_fence_after();
+      // lane l of quarter w has dim 32 w + l of each chunk
+      uint32_t o[CH][8];
+#pragma unroll
+      for (int k = 0; k < CH; ++k) tmem_ld(o[k], tmem + kTmemO + k * 16 + quarter);
+      tmem_wait_ld();
+      tmem_fence_before();
+      const float* sum_of = reinterpret_cast<const float*>(smem + C::SUM_OFFSET) + (sg & 1) * 5 * C::CC;
+      uint32_t* poison = poison_of + (sg & 3) * C::CC;
+      float coef[C::CC], lse[C::CC];
+      uint32_t nan[C::CC];
+#pragma unroll
+      for (int c = 0; c < C::CC; ++c) {
+        const float s = (sum_of[c] + sum_of[C::CC + c]) + (sum_of[2 * C::CC + c] + sum_of[3 * C::CC + c]);
+        coef[c] = s != 0.f ? p.v_mul / s : 0.f;
+        lse[c] = s != 0.f ? (sum_of[4 * C::CC + c] + __log2f(s)) * 0.69314718055994530942f : -INFINITY;
+        nan[c] = poison[c];
       }
       __syncwarp();
-    }
-  }
-  __syncthreads();
-
-  // ---- the piece's result
-  if (tid < C::CC) {
-    const float s = tiles > 0 ? (red[tid] + red[C::CC + tid]) + (red[2 * C::CC + tid] + red[3 * C::CC + tid]) : 0.f;
-    coef[tid] = s != 0.f ? p.v_mul / s : 0.f;
-    my_lse[tid] = s != 0.f ? (my_lse[tid] + __log2f(s)) * 0.69314718055994530942f : -INFINITY;
-  }
-  __syncthreads();
-  // warps 0-7: lane l of quarter w has dim 32 w + l of a chunk; warps 0-3 the even chunks, 4-7 the odd ones
-  if (warp < 8) {
-    tmem_fence_after();
-#pragma unroll 1
-    for (int c0 = warp >> 2; c0 < CH; c0 += 2) {
-      uint32_t o[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-      if (tiles > 0) {
-        tmem_ld(o, tmem + kTmemO + c0 * 16 + quarter);
-        tmem_wait_ld();
+      if (lane == 0) {
+        mbar_arrive(o_empty);
+        mbar_arrive(&l_empty[sg & 1]);
       }
-      const int dim = c0 * 128 + (warp & 3) * 32 + lane;
+      named_bar_sync(3, 128);
+      if (wt < C::CC) poison[wt] = 0u;
+      const int slot = blockIdx.x * 2 + (seg.piece == 0 ? 1 : 0);
 #pragma unroll
       for (int c = 0; c < C::CC; ++c) {
         if (!cm.valid(c)) break;
-        // (no attended token: coefficient 0, and sums that nothing has written)
-        float x = coef[c] != 0.f ? __uint_as_float(o[c]) * coef[c] : 0.f;
-        if (tiles > 0 && ((poison[c] >> (dim >> 4)) & 1u)) x = NAN;
-        if (p.direct_out)
-          reinterpret_cast<__nv_bfloat16*>(p.out)[cm.row(c) * C::D + dim] = __float2bfloat16_rn(x);
-        else if (p.cluster_merge)
-          my_out[c * C::D + dim] = x;
-        else
-          p.o_part[(cm.row(c) * p.num_splits + split) * C::D + dim] = x;
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+          const int dim = k * 128 + we * 32 + lane;
+          // (no attended token: coefficient 0)
+          float x = coef[c] != 0.f ? __uint_as_float(o[k][c]) * coef[c] : 0.f;
+          if ((nan[c] >> (dim >> 4)) & 1u) x = NAN;
+          if (seg.pieces == 1)
+            reinterpret_cast<__nv_bfloat16*>(p.out)[cm.row(c) * C::D + dim] = __float2bfloat16_rn(x);
+          else
+            p.o_part[((size_t)slot * C::CC + c) * C::D + dim] = x;
+        }
+        if (seg.pieces > 1 && wt == c) p.lse_part[slot * C::CC + c] = lse[c];
       }
+      if (seg.pieces > 1) {
+        // whoever leaves the last piece joins them all, in their order:
+        // out = sum_s w_s o_s,  w_s = exp(lse_s - M) / sum_s' exp(lse_s' - M)
+        __threadfence();
+        named_bar_sync(3, 128);
+        if (wt == 0) *ticket = atomicAdd(&p.counters[seg.first_share], 1u);
+        named_bar_sync(3, 128);
+        if (*ticket == (uint32_t)seg.pieces - 1) {
+          __threadfence();
+          if (wt == 0) p.counters[seg.first_share] = 0u;
+          auto slot_of = [&](int q) { return (seg.first_share + q) * 2 + (q == 0 ? 1 : 0); };
+#pragma unroll 1
+          for (int e = wt; e < C::CC * (C::D / 4); e += 128) {
+            const int c = e / (C::D / 4), dim = (e % (C::D / 4)) * 4;
+            if (!cm.valid(c)) break;
+            float M = -INFINITY;
+#pragma unroll 4
+            for (int q = 0; q < seg.pieces; ++q) M = fmaxf(M, __ldcg(p.lse_part + slot_of(q) * C::CC + c));
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            float w_sum = 0.f;
+#pragma unroll 4
+            for (int q = 0; q < seg.pieces; ++q) {
+              const float l = __ldcg(p.lse_part + slot_of(q) * C::CC + c);
+              const float4 x =
+                  __ldcg(reinterpret_cast<const float4*>(p.o_part + ((size_t)slot_of(q) * C::CC + c) * C::D + dim));
+              const float w = l == -INFINITY ? 0.f : ex2((l - M) * 1.4426950408889634f);
+              w_sum += w;
+              acc.x = fmaf(w, x.x, acc.x);
+              acc.y = fmaf(w, x.y, acc.y);
+              acc.z = fmaf(w, x.z, acc.z);
+              acc.w = fmaf(w, x.w, acc.w);
+            }
+            const float inv = w_sum != 0.f ? 1.f / w_sum : 0.f;
+            *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + cm.row(c) * C::D + dim) =
+                make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+          }
+        }
+      }
+      seg = next;
+      any = more;
     }
-    tmem_fence_before();
   }
-  if (!p.direct_out && !p.cluster_merge && tid < C::CC && cm.valid(tid))
-    p.lse_part[cm.row(tid) * p.num_splits + split] = my_lse[tid];
   __syncthreads();
   if (warp == kMmaWarp) {
     tmem_fence_after();
     tmem_dealloc<1>(*tmem_at, kTmemCols);
   }
-  if (!p.cluster_merge) return;
-
-  // ---- the pieces' results joined over distributed shared memory: each CTA of
-  // the cluster a share of the elements, in piece order
-  //   out = sum_s w_s o_s,  w_s = exp(lse_s - M) / sum_s' exp(lse_s' - M)
-  cluster_sync_all();
-  const int S = p.num_splits, rank = (int)cluster_ctarank();
-  constexpr int D4 = C::D / 4;
-  const uint32_t out_at = smem_u32(my_out), lse_at = smem_u32(my_lse);
-  for (int e = rank * C::THREADS + tid; e < C::CC * D4; e += S * C::THREADS) {
-    const int c = e / D4, dim = (e % D4) * 4;
-    if (!cm.valid(c)) continue;
-    float l[kFp4MaxCluster], M = -INFINITY, sum = 0.f;
-    float4 v[kFp4MaxCluster];
-#pragma unroll
-    for (int s = 0; s < kFp4MaxCluster; ++s) {
-      l[s] = s < S ? ld_dsmem_f32(map_smem_rank(lse_at + c * 4, s)) : -INFINITY;
-      if (s < S) v[s] = ld_dsmem_f32x4(map_smem_rank(out_at + (c * C::D + dim) * 4, s));
-    }
-#pragma unroll
-    for (int s = 0; s < kFp4MaxCluster; ++s) M = fmaxf(M, l[s]);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int s = 0; s < kFp4MaxCluster; ++s) {
-      if (s >= S || l[s] == -INFINITY) continue;
-      const float w = ex2((l[s] - M) * 1.4426950408889634f);
-      sum += w;
-      o.x = fmaf(w, v[s].x, o.x);
-      o.y = fmaf(w, v[s].y, o.y);
-      o.z = fmaf(w, v[s].z, o.z);
-      o.w = fmaf(w, v[s].w, o.w);
-    }
-    const float inv = sum != 0.f ? 1.f / sum : 0.f;
-    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + cm.row(c) * C::D + dim) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-  }
-  cluster_sync_all();  // nobody's shared memory goes while another reads it
 }
 
 }  // namespace
@@ -858,7 +1016,7 @@ const void* fp4_kernel_ptr(int variant) {
   switch (variant) {
 #define PD_FP4_CASE(ID, D, KVS, CC) \
   case ID:                          \
-    return reinterpret_cast<const void*>(&stage1_fp4_kernel<Fp4Cfg<D, KVS, CC>>);
+    return reinterpret_cast<const void*>(&decode_fp4_kernel<Fp4Cfg<D, KVS, CC>>);
     PD_FOR_EACH_FP4(PD_FP4_CASE)
 #undef PD_FP4_CASE
     default:
@@ -918,48 +1076,36 @@ pd_status decode_fp4(const pd_plan* plan, const void* q, const void* k_pool, con
   p.block_tables = block_tables;
   p.seq_lens = seq_lens;
   p.out = out;
+  p.counters = reinterpret_cast<uint32_t*>(ws + kWorkspaceHeader);
   p.lse_part = reinterpret_cast<float*>(ws + plan->lse_offset);
   p.o_part = reinterpret_cast<float*>(ws + plan->opart_offset);
   p.err = reinterpret_cast<uint32_t*>(ws);
   p.scale_log2 = scale_log2;
   p.v_mul = std::ldexp(1.f, v_exp);
-  p.direct_out = plan->num_splits == 1 ? 1 : 0;
-  p.cluster_merge = plan->merge_mode == 2 ? 1 : 0;
   p.stall_bytes = plan->test_stall_bytes;
   p.early_kv = plan->early_kv;
+  p.batch = plan->batch;
   p.window = ly.window;
   p.num_pages = ly.num_pages;
   p.max_pages = ly.max_pages_per_seq;
   p.page_size = ly.page_size;
   p.num_q_heads = ly.num_q_heads;
   p.num_kv_heads = ly.num_kv_heads;
-  p.num_splits = plan->num_splits;
-  p.chunk_tokens = plan->chunk_tokens;
   p.query_tokens = plan->query_tokens;
   p.group = ly.num_q_heads / ly.num_kv_heads;
-  p.col_tiles = plan->grid_y / ly.num_kv_heads;
+  p.col_tiles = (p.query_tokens * p.group + kVariants[plan->variant].group - 1) / kVariants[plan->variant].group;
 
   void* args[] = {&p};
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(plan->grid_x, plan->grid_y, plan->grid_z);
+  cfg.gridDim = dim3(plan->grid_x);
   cfg.blockDim = dim3(plan->threads_per_cta);
   cfg.dynamicSmemBytes = plan->smem_bytes;
   cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[2];
-  int na = 0;
-  attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[na].val.programmaticStreamSerializationAllowed = 1;
-  ++na;
-  if (p.cluster_merge) {
-    // the pieces of one (request, KV head, column tile) are consecutive in x: one cluster
-    attr[na].id = cudaLaunchAttributeClusterDimension;
-    attr[na].val.clusterDim.x = plan->num_splits;
-    attr[na].val.clusterDim.y = 1;
-    attr[na].val.clusterDim.z = 1;
-    ++na;
-  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = na;
+  cfg.numAttrs = 1;
   if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) {
     (void)cudaGetLastError();
     return PD_ERR_CUDA;
