@@ -48,8 +48,9 @@ struct Fp4Cfg {
   static constexpr int POISON_OFFSET = COL_OFFSET + 2 * CC * 4;   // u32 [4][CC]: 16-dim blocks that are NaN
   static constexpr int TOP_OFFSET = POISON_OFFSET + 4 * CC * 4;   // float [4][CC]: the softmax warps' maxima
   static constexpr int SUM_OFFSET = TOP_OFFSET + 4 * CC * 4;      // float [2][5][CC]: their sums, and the references
-  static constexpr int MISC_OFFSET = SUM_OFFSET + 2 * 5 * CC * 4; // u32: a softmax warp's wait ran out; the join's ticket
-  static constexpr int VALID_OFFSET = MISC_OFFSET + 8;            // u32 [NK + NV]: what a slot's tile is (kTile...)
+  static constexpr int MISC_OFFSET = SUM_OFFSET + 2 * 5 * CC * 4; // u32: the join's ticket
+  static constexpr int BLOCKS_OFFSET = MISC_OFFSET + 8;           // u32 [4]: the 16-token blocks that tiles i .. i + 3 hold
+  static constexpr int VALID_OFFSET = BLOCKS_OFFSET + 16;         // u32 [NK + NV]: what a slot's tile is (kTile...)
   static constexpr int BAR_OFFSET = (VALID_OFFSET + (NK + NV) * 4 + 7) / 8 * 8;
   static constexpr int NUM_BARS = 2 * (NK + NV) + 15 + 9;
   static constexpr int SMEM_BYTES = BAR_OFFSET + NUM_BARS * 8 + 16 + 1024;  // (+ 1 KiB to start on a 1024-byte boundary)
@@ -88,6 +89,8 @@ struct Fp4Params {
   int32_t stall_bytes, early_kv;
   int32_t batch, window, num_pages, max_pages, page_size, num_q_heads, num_kv_heads;
   int32_t query_tokens, group, col_tiles;
+  int32_t units;  // of a request: KV heads x column tiles
+  int32_t cap;    // tokens a block table's row holds
 };
 
 const void* fp4_kernel_ptr(int variant);

@@ -49,27 +49,34 @@ namespace pd {
 namespace {
 
 constexpr float kRefRange = 60.f;  // log2 of how far a score may exceed its column's reference
-// tensor memory columns: scores [S_BUFS][N], scales of V, of the unit matrix, V^T [2][128], sums [CHUNKS][16],
-// scales of K, of the query
+// Tensor memory columns: scores [S_BUFS][N], scales of V, of the unit matrix, V^T [2][128], sums [CHUNKS][16],
+// scales of K, of the query. All of it is allocated, so it begins at column 0.
 constexpr uint32_t kTmemS = 0, kTmemSfv = 64, kTmemSfi = 96, kTmemVt = 128, kTmemO = 384, kTmemSfk = 448,
                    kTmemSfq = 480, kTmemCols = 512;
 
+// Descriptors of shared-memory operands as two words, of which only the lower,
+// with the address, varies.
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo, int row_bytes = 128) {
+  return (sbo >> 4) | 1u << 14 | (uint32_t)swizzle_code(row_bytes) << 29;
+}
+
 // D[tmem] (+)= A . B over 64 dims, both e2m1 with an e4m3 scale per 16 dims.
-__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                        bool accumulate) {
+template <uint32_t A_HI, uint32_t B_HI, uint32_t IDESC>
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint32_t a, uint32_t b, uint32_t sfa, uint32_t sfb, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"((uint32_t)accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %6};\n\tmov.b64 b, {%2, %7};\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], a, b, %8, [%3], [%4], p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(sfa), "r"(sfb), "r"((uint32_t)accumulate), "n"(A_HI), "n"(B_HI), "n"(IDESC)
       : "memory");
 }
 
 // D[tmem] (+)= A[tmem] . B over 8 tokens, tf32.
-__device__ __forceinline__ void mma_tf32(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+template <uint32_t B_HI, uint32_t IDESC>
+__device__ __forceinline__ void mma_tf32(uint32_t d, uint32_t a, uint32_t b, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %3, 0;\n\tmov.b64 b, {%2, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], b, %5, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"((uint32_t)accumulate), "n"(B_HI), "n"(IDESC)
       : "memory");
 }
 
@@ -94,142 +101,171 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// What a ring slot's word says of its tile, beside the 16-token blocks that have a page (bits 0-7).
-constexpr uint32_t kTileFirst = 0x100u, kTileLast = 0x200u, kTileEnd = 0x400u;  // of its segment; of the share
+// Four e4m3 scales: 0x80 in the bytes that are NaN.
+__device__ __forceinline__ uint32_t nan_scales(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
-// The query rows behind a unit's columns: column c is pair tile * CC + c of the
-// request's T x group (token, head) pairs, token-major.
-template <class C>
-struct Columns {
-  int b, g, first, T, group, Hq;
-  __device__ __forceinline__ Columns(const Fp4Params& p, int b_, int y) {
-    b = b_;
-    g = y / p.col_tiles;
-    first = (y % p.col_tiles) * C::CC;
-    T = p.query_tokens;
-    group = p.group;
-    Hq = p.num_q_heads;
-  }
-  __device__ __forceinline__ bool valid(int c) const { return first + c < T * group; }
-  __device__ __forceinline__ int token(int c) const { return min((first + c) / group, T - 1); }
-  __device__ __forceinline__ size_t row(int c) const {
-    const int pr = first + c;
-    return ((size_t)b * T + pr / group) * Hq + (size_t)g * group + pr % group;
-  }
-};
+// A wait of up to kWaitTimeoutNs. The hardware suspends the thread for up to the
+// time asked for, so that a long wait takes no issue slots. One copy for all.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity) {
+  const unsigned long long start = global_timer_ns();
+  do {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"(1000000u)
+        : "memory");
+    if (done) return true;
+  } while (global_timer_ns() - start < kWaitTimeoutNs);
+  return false;
+}
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t phase) {
+  return mbar_test(bar, phase & 1) || wait_long(smem_u32(bar), phase & 1);
+}
+
+// What a ring slot's word says of its tile, beside the 16-token blocks that have a page (bits 0-7).
+constexpr uint32_t kTileFirst = 0x100u, kTileLast = 0x200u, kTileOdd = 0x400u;  // of its segment; an odd one
 
 // A request's attended range, cut to what its block table holds.
 struct Span {
-  int L, lo, base, tiles;  // cached tokens; the first one attended, rounded down to 16; tiles from there (at least one)
+  int L, base, tiles;  // cached tokens; the first one attended, rounded down to 16; tiles from there (at least one)
   bool bad;
   __device__ __forceinline__ Span(const Fp4Params& p, int raw) {
-    const int cap = p.max_pages * p.page_size;
-    bad = raw < 0 || raw > cap || (p.query_tokens > 1 && raw < p.query_tokens);
-    L = max(0, min(raw, cap));
+    bad = raw < (p.query_tokens > 1 ? p.query_tokens : 0) || raw > p.cap;
+    L = max(0, min(raw, p.cap));
     const int first_hi = L - p.query_tokens + 1;
-    lo = p.window > 0 && first_hi > p.window ? first_hi - p.window : 0;
-    base = lo / 16 * 16;
+    base = p.window > 0 && first_hi > p.window ? (first_hi - p.window) & ~15 : 0;
     tiles = max(1, (L - base + kFp4Tile - 1) / kFp4Tile);
   }
 };
 
-// The tiles of a share that belong to one unit.
-template <class C>
+// The tiles of a share that belong to one unit. Its column c is the c-th
+// (token, head) pair from (token, head) on, token-major.
 struct Segment {
-  int b, y, L, tiles;
+  int b, g, L, tiles;
   int t_base;    // first token of the first tile
   int tlo, thi;  // tokens of it that some column attends
+  int token, head;
   int pieces, piece, first_share;  // of the unit
-  bool bad;
-  // column c's attended positions
-  __device__ __forceinline__ int col_hi(const Fp4Params& p, const Columns<C>& cm, int c) const {
-    return L - p.query_tokens + cm.token(c) + 1;
+  int bad;
+};
+// The (token, head) pair of a column, from one to the next.
+struct Pair {
+  int j, r;
+  __device__ __forceinline__ explicit Pair(const Segment& s) : j(s.token), r(s.head) {}
+  __device__ __forceinline__ void next(const Fp4Params& p) {
+    if (++r == p.group) {
+      r = 0;
+      ++j;
+    }
+  }
+  __device__ __forceinline__ bool valid(const Fp4Params& p) const { return j < p.query_tokens; }
+  // one past the last position it attends
+  __device__ __forceinline__ int end(const Fp4Params& p, const Segment& s) const { return s.L - p.query_tokens + j + 1; }
+  __device__ __forceinline__ size_t row(const Fp4Params& p, const Segment& s) const {
+    return ((size_t)s.b * p.query_tokens + j) * p.num_q_heads + (size_t)s.g * p.group + r;
   }
 };
 
 // One warp's walk over the CTA's share; all lanes take part.
-template <class C>
 struct Walk {
-  const Fp4Params& p;
-  const int lane, Y;
-  int lens = 0, chunk = -1;  // this lane's request's length, of 32
-  int b = 0, y = 0, k = 0;   // where the next segment begins
-  int unit = 0;              // tiles before unit (b, y) (all of them are fewer than 2^30)
-  int left = 0;              // tiles of the share not yet handed out
-  int each = 1;              // tiles of a share
-  __device__ __forceinline__ Walk(const Fp4Params& p_, int lane_)
-      : p(p_), lane(lane_), Y(p_.num_kv_heads * p_.col_tiles) {
-    const int chunks = (p.batch + 31) / 32;
-    int total = 0;
-    for (int c = 0; c < chunks; ++c) {
-      load(c);
-      total += (int)__reduce_add_sync(kFullMask, count()) * Y;
-    }
-    each = (total + gridDim.x - 1) / gridDim.x;
-    if (blockIdx.x * (long long)each >= total) return;
-    const int start = blockIdx.x * each;
-    left = min(each, total - start);
-    for (int c = 0; c < chunks; ++c) {
-      load(c);
-      const int n = count();
-      int upto = n;  // tiles of the requests up to this lane's
-#pragma unroll
-      for (int m = 1; m < 32; m <<= 1) {
-        const int o = __shfl_up_sync(kFullMask, upto, m);
-        if (lane >= m) upto += o;
-      }
-      const uint32_t past = __ballot_sync(kFullMask, unit + upto * Y > start);
-      if (past == 0) {
-        unit += __shfl_sync(kFullMask, upto, 31) * Y;
-        continue;
-      }
-      const int at = __ffs(past) - 1;
-      const int tiles = __shfl_sync(kFullMask, n, at);
-      unit += (__shfl_sync(kFullMask, upto, at) - tiles) * Y;
-      b = c * 32 + at;
-      y = (start - unit) / tiles;
-      unit += y * tiles;
-      k = start - unit;
-      break;
-    }
-  }
-  __device__ __forceinline__ void load(int c) {
-    if (c == chunk) return;
-    chunk = c;
-    const int at = c * 32 + lane;
-    lens = at < p.batch ? p.seq_lens[at] : 0;
-  }
-  __device__ __forceinline__ int count() const { return chunk * 32 + lane < p.batch ? Span(p, lens).tiles : 0; }
-  __device__ __forceinline__ bool next(Segment<C>& s) {
-    if (left == 0) return false;
-    load(b >> 5);
-    const Span sp(p, __shfl_sync(kFullMask, lens, b & 31));
-    s.b = b;
-    s.y = y;
-    s.L = sp.L;
-    s.bad = sp.bad;
-    s.tiles = min(sp.tiles - k, left);
-    s.t_base = sp.base + k * kFp4Tile;
-    const Columns<C> cm(p, b, y);
-    const int hi = max(0, s.col_hi(p, cm, C::CC - 1)), first = s.col_hi(p, cm, 0);
-    s.tlo = max(s.t_base, p.window > 0 ? first - p.window : 0);
-    s.thi = min(hi, s.t_base + s.tiles * kFp4Tile);
-    s.first_share = unit / each;
-    s.piece = (int)blockIdx.x - s.first_share;
-    s.pieces = (unit + sp.tiles - 1) / each - s.first_share + 1;
-    left -= s.tiles;
-    k += s.tiles;
-    if (k == sp.tiles) {
-      k = 0;
-      unit += sp.tiles;
-      if (++y == Y) {
-        y = 0;
-        ++b;
-      }
-    }
-    return true;
-  }
+  int lens, chunk;      // this lane's request's length, of 32
+  int b, y, k;          // where the next segment begins
+  int unit;             // tiles before unit (b, y) (all of them are fewer than 2^30)
+  int left;             // tiles of the share not yet handed out
+  int each;             // tiles of a share
+  int first_share;      // the share that unit (b, y) begins in
 };
+__device__ __forceinline__ void walk_load(const Fp4Params& p, Walk& w, int c) {
+  if (c == w.chunk) return;
+  w.chunk = c;
+  const int at = c * 32 + (threadIdx.x & 31);
+  w.lens = at < p.batch ? p.seq_lens[at] : 0;
+}
+__device__ __forceinline__ int walk_count(const Fp4Params& p, const Walk& w) {
+  return w.chunk * 32 + (int)(threadIdx.x & 31) < p.batch ? Span(p, w.lens).tiles : 0;
+}
+__device__ __forceinline__ void walk_start(const Fp4Params& p, Walk& w) {
+  const int lane = threadIdx.x & 31, chunks = (p.batch + 31) / 32;
+  w.chunk = -1;
+  w.b = w.y = w.k = w.unit = w.left = w.first_share = 0;
+  int total = 0;
+#pragma unroll 1
+  for (int c = 0; c < chunks; ++c) {
+    walk_load(p, w, c);
+    total += (int)__reduce_add_sync(kFullMask, walk_count(p, w)) * p.units;
+  }
+  w.each = (total + gridDim.x - 1) / gridDim.x;
+  const int start = blockIdx.x * w.each;  // (below 2^30 + 2^30)
+  if (start >= total) return;
+  w.left = min(w.each, total - start);
+#pragma unroll 1
+  for (int c = 0; c < chunks; ++c) {
+    walk_load(p, w, c);
+    const int n = walk_count(p, w);
+    int upto = n;  // tiles of the requests up to this lane's
+#pragma unroll 1
+    for (int m = 1; m < 32; m <<= 1) {
+      const int o = __shfl_up_sync(kFullMask, upto, m);
+      if (lane >= m) upto += o;
+    }
+    const uint32_t past = __ballot_sync(kFullMask, w.unit + upto * p.units > start);
+    if (past == 0) {
+      w.unit += __shfl_sync(kFullMask, upto, 31) * p.units;
+      continue;
+    }
+    const int at = __ffs(past) - 1, tiles = __shfl_sync(kFullMask, n, at);
+    w.unit += (__shfl_sync(kFullMask, upto, at) - tiles) * p.units;
+    w.b = c * 32 + at;
+    w.y = (start - w.unit) / tiles;
+    w.unit += w.y * tiles;
+    w.k = start - w.unit;
+    break;
+  }
+  w.first_share = w.k ? w.unit / w.each : blockIdx.x;
+}
+template <int CC>
+__device__ __forceinline__ bool walk_next(const Fp4Params& p, Walk& w, Segment& s) {
+  if (w.left == 0) return false;
+  walk_load(p, w, w.b >> 5);
+  const Span sp(p, __shfl_sync(kFullMask, w.lens, w.b & 31));
+  s.b = w.b;
+  s.g = w.y;
+  s.token = s.head = 0;
+  int last = p.query_tokens - 1;  // token of the last column
+  if (p.col_tiles > 1) {
+    s.g = w.y / p.col_tiles;
+    const int c0 = (w.y - s.g * p.col_tiles) * CC;
+    s.token = c0 / p.group;
+    s.head = c0 - s.token * p.group;
+    last = min(last, s.token + (s.head + CC - 1) / p.group);
+  }
+  s.L = sp.L;
+  s.bad = sp.bad;
+  s.tiles = min(sp.tiles - w.k, w.left);
+  s.t_base = sp.base + w.k * kFp4Tile;
+  // the union of the columns' tokens' causal ranges
+  const int end0 = sp.L - p.query_tokens + 1;
+  s.tlo = max(s.t_base, p.window > 0 ? end0 + s.token - p.window : 0);
+  s.thi = min(end0 + last, s.t_base + s.tiles * kFp4Tile);
+  const bool whole = w.k + s.tiles == sp.tiles;  // the unit ends in this share
+  s.first_share = w.first_share;
+  s.piece = (int)blockIdx.x - w.first_share;
+  s.pieces = s.piece + 1;
+  if (!whole) s.pieces = (w.unit + sp.tiles - 1) / w.each - w.first_share + 1;
+  w.left -= s.tiles;
+  w.k += s.tiles;
+  if (whole) {
+    w.k = 0;
+    w.unit += sp.tiles;
+    w.first_share = blockIdx.x;
+    if (++w.y == p.units) {
+      w.y = 0;
+      ++w.b;
+    }
+  }
+  return true;
+}
 
 // Byte of (row, byte of the row) in a swizzled tile of codes.
 template <class C>
@@ -238,92 +274,84 @@ __device__ __forceinline__ uint32_t code_offset(int row, int byte) {
   return (row >> 3) * (C::SL * 1024) + sl * 1024 + (row & 7) * 128 + ((c ^ (row & 7)) << 4) + (byte & 15);
 }
 
-// The query rows of a unit's columns as terms in shared memory (`q`) and their
+// The query rows of a segment's columns as terms in shared memory (`q`) and their
 // scales (`sf`, `mul`), by 4 warps: one takes 256 dims of a row, a lane 8 of them,
 // two lanes a block of 16.
 template <class C>
-__device__ __forceinline__ void write_query_terms(const Fp4Params& p, const Columns<C>& cm, uint8_t* q, uint8_t* sf,
-                                                  float* mul, int warp, int lane) {
-  constexpr int ITEMS = C::CC * C::SL, EACH = ITEMS / 4;
-  float x[EACH][8];
-  bool odd[EACH];
-  {
-    uint4 w[EACH], o[EACH];
-#pragma unroll
-    for (int k = 0; k < EACH; ++k) {
-      const int item = warp + 4 * k, col = item / C::SL, part = item % C::SL;
-      w[k] = o[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (cm.valid(col)) {
-        const uint4* row = reinterpret_cast<const uint4*>(p.q + cm.row(col) * C::D) + lane;
-        w[k] = __ldg(row + part * 32);
-        if (C::SL == 2) o[k] = __ldg(row + (part ^ 1) * 32);  // (for the row's largest)
-      }
+__device__ __forceinline__ void write_query_terms(const Fp4Params& p, const Segment& s, uint8_t* q, uint8_t* sf, float* mul,
+                                                  int warp, int lane) {
+#pragma unroll 1
+  for (int item = warp; item < C::CC * C::SL; item += 4) {
+    const int col = item / C::SL, part = item % C::SL;
+    const int pair = s.head + col;
+    int j = 0, r = pair;
+    if (pair >= p.group) {
+      j = pair / p.group;
+      r = pair - j * p.group;
     }
-#pragma unroll
-    for (int k = 0; k < EACH; ++k) {
-      const int item = warp + 4 * k, col = item / C::SL, part = item % C::SL;
-      // the row's largest magnitude, as whole numbers (infinity and NaN are the largest)
-      uint32_t m = 0;
-#pragma unroll
-      for (uint32_t v : {w[k].x, w[k].y, w[k].z, w[k].w, o[k].x, o[k].y, o[k].z, o[k].w})
-        m = __vmaxu2(m, v & 0x7fff7fffu);
-      const uint32_t top = __reduce_max_sync(kFullMask, max(m << 16, m & 0xffff0000u));
-      odd[k] = top >= 0x7f800000u;  // a NaN or an infinity: the row's scores are NaN
-      // brings the largest to [2^10, 2^11) (a row that is below 2^-116 altogether: as near as a factor of 2^126 does)
-      const int shift = min(126, 137 - (int)(top >> 23));
-      const float up = __int_as_float((127 + shift) << 23);
-      const uint32_t v[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[k][2 * i] = odd[k] ? 0.f : __uint_as_float(v[i] << 16) * up;
-        x[k][2 * i + 1] = odd[k] ? 0.f : __uint_as_float(v[i] & 0xffff0000u) * up;
-      }
-      if (part == 0 && lane == 0) mul[col] = p.scale_log2 * __int_as_float((127 - shift) << 23);
+    j += s.token;
+    uint4 w = make_uint4(0u, 0u, 0u, 0u), o = w;
+    if (j < p.query_tokens) {
+      const uint4* row = reinterpret_cast<const uint4*>(
+          p.q + (((size_t)s.b * p.query_tokens + j) * p.num_q_heads + (size_t)s.g * p.group + r) * C::D) + lane;
+      w = __ldg(row + part * 32);
+      if (C::SL == 2) o = __ldg(row + (part ^ 1) * 32);  // (for the row's largest)
     }
-  }
+    // the row's largest magnitude, as whole numbers (infinity and NaN are the largest)
+    uint32_t m = 0;
 #pragma unroll
-  for (int t = 0; t < kFp4Terms; ++t) {
+    for (uint32_t v : {w.x, w.y, w.z, w.w, o.x, o.y, o.z, o.w}) m = __vmaxu2(m, v & 0x7fff7fffu);
+    const uint32_t top = __reduce_max_sync(kFullMask, max(m << 16, m & 0xffff0000u));
+    const bool odd = top >= 0x7f800000u;  // a NaN or an infinity: the row's scores are NaN
+    // brings the largest to [2^10, 2^11) (a row that is below 2^-116 altogether: as near as a factor of 2^126 does)
+    const int shift = min(126, 137 - (int)(top >> 23));
+    const float up = __int_as_float((127 + shift) << 23);
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+    float x[8];
 #pragma unroll
-    for (int k = 0; k < EACH; ++k) {
-      const int item = warp + 4 * k, col = item / C::SL, part = item % C::SL;
-      float(&y)[8] = x[k];
-      float a = fmaxf(fmaxf(fmaxf(fabsf(y[0]), fabsf(y[1])), fmaxf(fabsf(y[2]), fabsf(y[3]))),
-                      fmaxf(fmaxf(fabsf(y[4]), fabsf(y[5])), fmaxf(fabsf(y[6]), fabsf(y[7]))));
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = odd ? 0.f : __uint_as_float(v[i] << 16) * up;
+      x[2 * i + 1] = odd ? 0.f : __uint_as_float(v[i] & 0xffff0000u) * up;
+    }
+    if (part == 0 && lane == 0) mul[col] = p.scale_log2 * __int_as_float((127 - shift) << 23);
+#pragma unroll 1
+    for (int t = 0; t < kFp4Terms; ++t) {
+      float a = fmaxf(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))),
+                      fmaxf(fmaxf(fabsf(x[4]), fabsf(x[5])), fmaxf(fabsf(x[6]), fabsf(x[7]))));
       a = fmaxf(a, __shfl_xor_sync(kFullMask, a, 1));
       uint16_t s8;
       asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s8) : "f"(0.f), "f"(a * (1.f / 6.f)));
       uint32_t s16;
       asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s16) : "h"(s8));
-      const float s = __half2float(__ushort_as_half((unsigned short)(s16 & 0xffffu)));
-      float r;  // (what a term leaves over, the next one takes: its rounding need not be exact)
-      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-      r = s > 0.f ? r : 0.f;
+      const float sc = __half2float(__ushort_as_half((unsigned short)(s16 & 0xffffu)));
+      float rc;  // (what a term leaves over, the next one takes: its rounding need not be exact)
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rc) : "f"(sc));
+      rc = sc > 0.f ? rc : 0.f;
       uint32_t codes;
       asm("{\n\t.reg .b8 a, b, c, d;\n\t"
           "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
           "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
           "mov.b32 %0, {a, b, c, d};\n\t}"
           : "=r"(codes)
-          : "f"(y[0] * r), "f"(y[1] * r), "f"(y[2] * r), "f"(y[3] * r), "f"(y[4] * r), "f"(y[5] * r), "f"(y[6] * r),
-            "f"(y[7] * r));
-      if (t + 1 < kFp4Terms) {
-        uint32_t f[4];
-        e2m1x8_to_f16x8(codes, f);
+          : "f"(x[0] * rc), "f"(x[1] * rc), "f"(x[2] * rc), "f"(x[3] * rc), "f"(x[4] * rc), "f"(x[5] * rc),
+            "f"(x[6] * rc), "f"(x[7] * rc));
+      uint32_t f[4];
+      e2m1x8_to_f16x8(codes, f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 two = __half22float2(*reinterpret_cast<const __half2*>(&f[i]));
-          y[2 * i] = fmaf(-two.x, s, y[2 * i]);
-          y[2 * i + 1] = fmaf(-two.y, s, y[2 * i + 1]);
-        }
+      for (int i = 0; i < 4; ++i) {
+        const float2 two = __half22float2(*reinterpret_cast<const __half2*>(&f[i]));
+        x[2 * i] = fmaf(-two.x, sc, x[2 * i]);
+        x[2 * i + 1] = fmaf(-two.y, sc, x[2 * i + 1]);
       }
       const int n = t * C::CC + col;
       *reinterpret_cast<uint32_t*>(q + code_offset<C>(n, part * 128 + lane * 4)) = codes;
-      if ((lane & 1) == 0) sf[n * C::ROW_SF + part * 16 + lane / 2] = odd[k] ? (uint8_t)0x7f : (uint8_t)s8;
+      if ((lane & 1) == 0) sf[n * C::ROW_SF + part * 16 + lane / 2] = odd ? (uint8_t)0x7f : (uint8_t)s8;
     }
   }
 }
 
-// 16 bytes global -> shared, counted by cp_async_arrive.
+// 16 bytes global -> shared, counted by cp_async_arrive. (With an L2 cache policy the
+// instruction is illegal here.)
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
@@ -332,9 +360,9 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Four e4m3 scales: 0x80 in the bytes that are NaN.
-__device__ __forceinline__ uint32_t nan_scales(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
-
+// The kernel's loops are kept short: its roles run different code side by side, and
+// what does not fit the instruction caches is fetched again every tile (unrolled,
+// 350 KB of code, it took three times as long).
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_constant__ Fp4Params p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -342,56 +370,45 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
   constexpr int SB = C::S_BUFS, CH = C::CHUNKS, RINGS = C::NK + C::NV;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFFSET);  // [RINGS]: K's ring, then V's
   uint64_t* empty = full + RINGS;                                      // [RINGS]
-  uint64_t* sfk_ready = empty + RINGS;                                 // K's scales in tensor memory
-  uint64_t* sfv_ready = sfk_ready + 1;                                 // V's
-  uint64_t* s_full = sfv_ready + 1;                                    // [2] scores computed
-  uint64_t* s_empty = s_full + 2;                                      // [2] scores read
-  uint64_t* vt_full = s_empty + 2;                                     // [2] a chunk of V^T there
-  uint64_t* vt_empty = vt_full + 2;                                    // [2] and used
-  uint64_t* dq_done = vt_empty + 2;                                    // a tile's V^T all there
-  uint64_t* p_full = dq_done + 1;                                      // [2]
-  uint64_t* p_empty = p_full + 2;                                      // [2]: the tile is in the sums
-  uint64_t* q_full = p_empty + 2;                                      // [2] a segment's query terms there
-  uint64_t* qk_done = q_full + 2;                                      // a segment's scores all computed
-  uint64_t* o_full = qk_done + 1;                                      // a segment's sums complete
-  uint64_t* o_empty = o_full + 1;                                      // and read
-  uint64_t* l_full = o_empty + 1;                                      // [2] a segment's probabilities' sums there
-  uint64_t* l_empty = l_full + 2;                                      // [2] and read
+  // one arrival: the products' commits
+  uint64_t* vt_full = empty + RINGS;    // [2] a chunk of V^T there
+  uint64_t* vt_empty = vt_full + 2;     // [2] and used
+  uint64_t* p_empty = vt_empty + 2;     // [2] P used: the tile is in the sums
+  uint64_t* dq_done = p_empty + 2;      // a tile's V^T all there
+  uint64_t* qk_done = dq_done + 1;      // a segment's scores all computed
+  // two: a commit, and an arrival of the same lane (which orders what it has seen of others)
+  uint64_t* s_full = qk_done + 1;       // [2] scores computed
+  uint64_t* o_full = s_full + 2;        // a segment's sums complete
+  // four warps
+  uint64_t* sfk_ready = o_full + 1;     // K's scales in tensor memory
+  uint64_t* sfv_ready = sfk_ready + 1;  // V's
+  uint64_t* s_empty = sfv_ready + 1;    // [2] scores read
+  uint64_t* p_full = s_empty + 2;       // [2]
+  uint64_t* q_full = p_full + 2;        // [2] a segment's query terms there
+  uint64_t* o_empty = q_full + 2;       // a segment's sums read
+  uint64_t* l_full = o_empty + 1;       // [2] a segment's probabilities' sums there
+  uint64_t* l_empty = l_full + 2;       // [2] and read
+  static_assert(C::NUM_BARS == 2 * RINGS + 8 + 3 + 13, "as listed");
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(full + C::NUM_BARS);
-  volatile uint32_t* valid = reinterpret_cast<uint32_t*>(smem + C::VALID_OFFSET);
+  volatile uint32_t* valid = reinterpret_cast<uint32_t*>(smem + C::VALID_OFFSET);  // [RINGS]
+  volatile uint32_t* blocks_of = reinterpret_cast<uint32_t*>(smem + C::BLOCKS_OFFSET);  // [4] by tile
   constexpr int kSfWarp = 4, kCodeWarp = 8, kScaleWarp = 10, kMmaWarp = 11, kEndWarp = 12;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool copies = warp >= kCodeWarp && warp <= kScaleWarp;
   const bool early = p.early_kv != 0 && copies;
 
-  if (tid == kCodeWarp * 32) {
-    prefetch_tensormap(&p.kmap);
-    if (!C::KVS) prefetch_tensormap(&p.vmap);
-#pragma unroll 1
-    for (int s = 0; s < RINGS; ++s) {
-      // the codes' byte count (K = V: two warps') and every lane's scales
-      mbar_init(&full[s], (C::KVS ? 2 : 1) + 32);
-      mbar_init(&empty[s], C::KVS ? 2 : 1);  // the products that read the slot
+  if (warp == kCodeWarp) {
+    if (lane == 0) {
+      prefetch_tensormap(&p.kmap);
+      if (!C::KVS) prefetch_tensormap(&p.vmap);
     }
-    mbar_init(sfk_ready, 4);
-    mbar_init(sfv_ready, 4);
-    mbar_init(dq_done, 1);
-    mbar_init(qk_done, 1);
-    mbar_init(o_full, 2);
-    mbar_init(o_empty, 4);
-#pragma unroll 1
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&s_full[s], 1);
-      mbar_init(&s_empty[s], 4);
-      mbar_init(&vt_full[s], 1);
-      mbar_init(&vt_empty[s], 1);
-      mbar_init(&p_full[s], 4);
-      mbar_init(&p_empty[s], 1);
-      mbar_init(&q_full[s], 4);
-      mbar_init(&l_full[s], 4);
-      mbar_init(&l_empty[s], 4);
+    for (int i = lane; i < C::NUM_BARS; i += 32) {
+      const int r = i - 2 * RINGS;
+      // full: the codes' byte count (K = V: two warps') and every lane's scales; empty: the products that read the slot
+      mbar_init(&full[i], i < RINGS ? (C::KVS ? 34 : 33) : r < 0 ? (C::KVS ? 2 : 1) : r < 8 ? 1 : r < 11 ? 2 : 4);
     }
     fence_barrier_init();
+    __syncwarp();
   }
   if (warp == kMmaWarp) tmem_alloc<1>(tmem_at, kTmemCols);
   if (copies) {
@@ -402,12 +419,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     grid_dependency_wait();
     grid_launch_dependents();
   }
-  uint32_t tmem = 0;
+  Walk walk;
+  walk_start(p, walk);
+  const int share_tiles = walk.left;
+  Segment seg;
   if (!copies) {
     // the barriers and tensor memory are there (the copies do not wait for the other warps)
     named_bar_sync(4, C::THREADS);
     tmem_fence_after();
-    tmem = *tmem_at;
   }
   const uint32_t quarter = (uint32_t)(warp & 3) << 21;  // this warp's lanes of tensor memory
 
@@ -416,45 +435,46 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
   // threads meet again.
   bool good = true;
   auto await = [&](uint64_t* bar, uint32_t phase) {
-    if (good && __any_sync(kFullMask, !mbar_wait(bar, phase & 1))) {
+    if (good && __any_sync(kFullMask, !wait_for(bar, phase))) {
       good = false;
       if (lane == 0) atomicOr(p.err, kErrTimeout);
     }
   };
-  Walk<C> walk(p, lane);
-  Segment<C> seg, next;
-  bool any = walk.next(seg);
-  // page ids of tiles i .. i + 3 of a segment: lane l its 16 tokens 16 l ..
-  auto pages_of = [&](const Segment<C>& s, int i) {
-    const int t = s.t_base + i * kFp4Tile + lane * 16;
-    return t < s.thi ? __ldg(p.block_tables + (size_t)s.b * p.max_pages + t / p.page_size) : -1;
-  };
 
   if (copies) {
     // ---- copies, four tiles' page ids ahead (one tile ahead, their latency bound
-    // the kernel: 4 x 32768 tokens 77 -> 62 us)
+    // the kernel: 4 x 32768 tokens 77 -> 62 us): lane l has the 16 tokens 16 l .. of
+    // four tiles
     bool waited = !early, stop = false;
     uint32_t err_bits = 0;
     const uint64_t policy = l2_evict_first_policy();
     const int mine = warp - kCodeWarp;  // 0: K's codes, 1: V's (K = V: the lower and the upper half), 2: scales
-    int page = any ? pages_of(seg, 0) : -1, rows = -1;
+    Segment next;
+    bool any = walk_next<C::CC>(p, walk, next);
+    auto page_of = [&](const Segment& s, int i) {
+      const int t = s.t_base + i * kFp4Tile + lane * 16;
+      return t < s.thi ? __ldg(p.block_tables + (size_t)s.b * p.max_pages + t / p.page_size) : -1;
+    };
+    int page = any ? page_of(next, 0) : -1, rows = -1;
     int it = 0;  // tiles whose copies went out
-    while (any && !stop) {
-      const bool more = walk.next(next);
-      const int g = seg.y / p.col_tiles;
+#pragma unroll 1
+    for (uint32_t odd = 0; any && !stop; odd ^= kTileOdd) {
+      seg = next;
+      any = walk_next<C::CC>(p, walk, next);
 #pragma unroll 1
       for (int i = 0; i < seg.tiles; ++i) {
         if ((i & 3) == 0) {
           const int t = seg.t_base + i * kFp4Tile + lane * 16;
           const bool here = (unsigned)page < (unsigned)p.num_pages;
           if (t < seg.thi && !here) err_bits |= kErrBadPage;
-          rows = t < seg.thi && here ? (page * p.num_kv_heads + g) * p.page_size + t % p.page_size : -1;
-          page = i + 4 < seg.tiles ? pages_of(seg, i + 4) : more ? pages_of(next, 0) : -1;
+          rows = t < seg.thi && here ? (page * p.num_kv_heads + seg.g) * p.page_size + t % p.page_size : -1;
+          page = -1;
+          const bool on = i + 4 < seg.tiles;
+          if (on || any) page = page_of(on ? seg : next, on ? i + 4 : 0);
         }
         const int row0 = __shfl_sync(kFullMask, rows, (i & 3) * 8 + (lane & 7));
         const uint32_t bits = __ballot_sync(kFullMask, row0 >= 0) & 0xffu;
-        const bool last = i + 1 == seg.tiles;
-        const uint32_t word = bits | (i == 0 ? kTileFirst : 0u) | (last ? kTileLast : 0u) | (last && !more ? kTileEnd : 0u);
+        const uint32_t word = bits | odd | (i == 0 ? kTileFirst : 0u) | (i + 1 == seg.tiles ? kTileLast : 0u);
         // rows of the newest tokens may still be written by the kernel in front
         if (!waited && (it >= C::NK || (!C::KVS && it >= C::NV) ||
                         seg.t_base + (i + 1) * kFp4Tile > seg.L - p.query_tokens)) {
@@ -462,21 +482,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
           grid_launch_dependents();
           waited = true;
         }
-#pragma unroll
+#pragma unroll 1
         for (int v = 0; v < (C::KVS ? 1 : 2); ++v) {
-          if (!C::KVS && mine != 2 && mine != v) continue;
-          const int n = v ? C::NV : C::NK, st = (v ? C::NK : 0) + it % n, round = it / n;
-          if (round > 0) {
-            const bool freed = mbar_wait(&empty[st], (round - 1) & 1);
-            if (__any_sync(kFullMask, !freed)) {
-              err_bits |= kErrTimeout;
-              stop = true;
-              break;
-            }
+          if (!C::KVS && mine == 1 - v) continue;
+          const int n = v ? C::NV : C::NK, round = it / n, st = (v ? C::NK : 0) + it - round * n;
+          if (round > 0 && __any_sync(kFullMask, !wait_for(&empty[st], round - 1))) {
+            err_bits |= kErrTimeout;
+            stop = true;
+            break;
           }
           uint8_t* item = smem + st * C::ITEM_BYTES;
           if (mine < 2) {
-            const uint32_t part = C::KVS ? (mine ? bits & 0xf0u : bits & 0x0fu) : bits;
+            const uint32_t part = C::KVS ? bits & (mine ? 0xf0u : 0x0fu) : bits;
             if (lane == 0) {
               if (!C::KVS || mine == 0) valid[st] = word;
               if (part)
@@ -490,14 +507,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
           } else {
             // 16 bytes a lane (as bulk copies these would be half of all copies)
             constexpr int LANES = C::ROW_SF;  // 16-byte pieces of 16 tokens' scales
-            const uint8_t* sf = v ? p.v_sf : p.k_sf;
+            const uint8_t* sf = (v ? p.v_sf : p.k_sf) + (lane % LANES) * 16;
+            uint8_t* to = item + C::CODE_BYTES + lane * 16;
 #pragma unroll
             for (int k = 0; k < 8; k += 32 / LANES) {
               const int at = k + lane / LANES;  // the 16 tokens this lane copies a piece of
               const int row = __shfl_sync(kFullMask, row0, at);
-              if ((bits >> at) & 1u)
-                cp_async16(item + C::CODE_BYTES + at * 16 * C::ROW_SF + (lane % LANES) * 16,
-                           sf + (size_t)row * C::ROW_SF + (lane % LANES) * 16);
+              if (row >= 0) cp_async16(to + k * 16 * C::ROW_SF, sf + (size_t)row * C::ROW_SF);
             }
             cp_async_arrive(&full[st]);
           }
@@ -505,8 +521,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
         if (stop) break;
         ++it;
       }
-      seg = next;
-      any = more;
     }
     // no copy may still be landing when the CTA ends
     const unsigned long long deadline = global_timer_ns() + kWaitTimeoutNs;
@@ -526,47 +540,41 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     // ---- softmax: rows 32 warp .. + 31 of every tile
     const uint32_t p_at = smem_u32(smem + C::P_OFFSET) + warp * 1024 + (lane & 3) * 4;
     if (C::CC < 8) {  // P's unused columns
-#pragma unroll
       for (int k = 0; k < 2; ++k)
         for (int i = lane; i < (8 - C::CC) * 8; i += 32)
           *reinterpret_cast<uint4*>(smem + C::P_OFFSET + k * C::P_BYTES + warp * 1024 + C::CC * 128 + i * 16) =
               make_uint4(0u, 0u, 0u, 0u);
     }
     float* top_of = reinterpret_cast<float*>(smem + C::TOP_OFFSET);  // [4][CC]
-    int page = any ? pages_of(seg, 0) : -1;
-    uint32_t blocks = 0;
     int it = 0;
 #pragma unroll 1
-    for (int sg = 0; any; ++sg) {
-      const bool more = walk.next(next);
-      const Columns<C> cm(p, seg.b, seg.y);
+    for (int sg = 0; walk_next<C::CC>(p, walk, seg); ++sg) {
       if (seg.bad && tid == 0) atomicOr(p.err, kErrBadSeqLen);
       await(&q_full[sg & 1], sg >> 1);
       float col_mul[C::CC], ref[C::CC], sum[C::CC];
       int col_hi[C::CC], col_lo[C::CC];
+      {
+        Pair col(seg);
 #pragma unroll
-      for (int c = 0; c < C::CC; ++c) {
-        col_mul[c] = reinterpret_cast<const float*>(smem + C::COL_OFFSET)[(sg & 1) * C::CC + c];
-        const int end = seg.col_hi(p, cm, c);
-        col_hi[c] = cm.valid(c) ? min(seg.thi, end) : 0;
-        col_lo[c] = max(seg.tlo, p.window > 0 ? end - p.window : 0);
-        ref[c] = -INFINITY;
-        sum[c] = 0.f;
+        for (int c = 0; c < C::CC; ++c, col.next(p)) {
+          col_mul[c] = reinterpret_cast<const float*>(smem + C::COL_OFFSET)[(sg & 1) * C::CC + c];
+          const int end = col.end(p, seg);
+          col_hi[c] = col.valid(p) ? min(seg.thi, end) : 0;
+          col_lo[c] = max(seg.tlo, p.window > 0 ? end - p.window : 0);
+          ref[c] = -INFINITY;
+          sum[c] = 0.f;
+        }
       }
 #pragma unroll 1
       for (int i = 0; i < seg.tiles; ++i, ++it) {
         const int sbuf = it % SB, buf = it & 1;
-        if ((i & 3) == 0) {
-          blocks = __ballot_sync(kFullMask, (unsigned)page < (unsigned)p.num_pages);
-          page = i + 4 < seg.tiles ? pages_of(seg, i + 4) : more ? pages_of(next, 0) : -1;
-        }
         await(&s_full[sbuf], it / SB);
         tmem_fence_after();
         float s[C::CC];
         {
           uint32_t w[kFp4Terms * C::CC / 8][8];
 #pragma unroll
-          for (int k = 0; k < kFp4Terms * C::CC / 8; ++k) tmem_ld(w[k], tmem + kTmemS + sbuf * C::N + quarter + k * 8);
+          for (int k = 0; k < kFp4Terms * C::CC / 8; ++k) tmem_ld(w[k], kTmemS + sbuf * C::N + quarter + k * 8);
           tmem_wait_ld();
 #pragma unroll
           for (int c = 0; c < C::CC; ++c) {
@@ -576,11 +584,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
             s[c] = x * col_mul[c];
           }
         }
+        const int row = warp * 32 + lane, t = seg.t_base + i * kFp4Tile + row;
+        const bool ok = (blocks_of[it & 3] >> (row >> 4)) & 1u;
         tmem_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_empty[sbuf]);
-        const int row = warp * 32 + lane, t = seg.t_base + i * kFp4Tile + row;
-        const bool ok = (blocks >> ((i & 3) * 8 + (row >> 4))) & 1u;
         bool above = false;
 #pragma unroll
         for (int c = 0; c < C::CC; ++c) {
@@ -614,17 +622,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
 #pragma unroll 1
             for (int c0 = 0; c0 < CH; ++c0) {
               uint32_t o[8];
-              tmem_ld(o, tmem + kTmemO + c0 * 16 + quarter);
+              tmem_ld(o, kTmemO + c0 * 16 + quarter);
               tmem_wait_ld();
 #pragma unroll
               for (int c = 0; c < C::CC; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f[c]);
-              tmem_st(tmem + kTmemO + c0 * 16 + quarter, o);
+              tmem_st(kTmemO + c0 * 16 + quarter, o);
             }
             tmem_wait_st();
             tmem_fence_before();
           }
         }
         if (it >= 2) await(&p_empty[buf], (it >> 1) - 1);
+        if (i == 0 && sg > 0) await(o_empty, sg - 1);  // (on behalf of the sums' product)
 #pragma unroll
         for (int c = 0; c < C::CC; ++c) {
           // rounded to tf32 here, to nearest (the product would cut it off); the sum takes what the product takes
@@ -651,210 +660,176 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&l_full[sg & 1]);
-      seg = next;
-      any = more;
     }
   } else if (warp < kCodeWarp) {
     // ---- scales into tensor memory: lane l, column 4 k + j holds the 4 scales of row l + 32 j, dims 64 k ..;
-    // every quarter of the lanes all rows'
+    // every quarter of the lanes all rows'. K's, once the product before has read
+    // the last tile's, then V's likewise.
     uint32_t* poison_of = reinterpret_cast<uint32_t*>(smem + C::POISON_OFFSET);
     int it = 0;
 #pragma unroll 1
-    for (int sg = 0; any; ++sg) {
-      const Columns<C> cm(p, seg.b, seg.y);
-      uint32_t* poison = poison_of + (sg & 3) * C::CC;
-      auto put = [&](const uint8_t* sf, uint32_t at, bool v, uint32_t here, int t0) {
-        uint32_t x[C::KSTEPS * 4];  // [64 dims][row group]
-#pragma unroll
-        for (int k0 = 0; k0 < C::KSTEPS; k0 += 4) {
+    for (int sg = 0; walk_next<C::CC>(p, walk, seg); ++sg) {
+#pragma unroll 1
+      for (int u = 0; u < 2 * seg.tiles; ++u) {
+        const bool v = (u & 1) != 0;
+        const int n = v && !C::KVS ? C::NV : C::NK, round = it / n, st = (v && !C::KVS ? C::NK : 0) + it - round * n;
+        await(&full[st], round);
+        if (it > 0) await(v ? dq_done : &s_full[(it - 1) % SB], v ? it - 1 : (it - 1) / SB);
+        if (!v) {
+          // what the scores' product needs besides: a free buffer, and the segment's query terms
+          if (it >= SB) await(&s_empty[it % SB], it / SB - 1);
+          if (u == 0) await(&q_full[sg & 1], sg >> 1);
+        }
+        tmem_fence_after();
+        const uint32_t here = valid[st] & 0xffu;
+        const int t0 = seg.t_base + (u >> 1) * kFp4Tile;
+        if (!v && warp == kSfWarp && lane == 0) blocks_of[it & 3] = here;
+        // V's rows that do not count have scale 0: their probabilities are 0, but 0 * NaN is NaN
+        uint32_t count = 15u;
+        if (v && !(here == 0xffu && t0 >= seg.tlo && t0 + kFp4Tile <= seg.thi)) {
+          count = 0u;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint4 w = *reinterpret_cast<const uint4*>(sf + (lane + 32 * j) * C::ROW_SF + k0 * 4);
-            x[k0 * 4 + j] = w.x;
-            x[k0 * 4 + 4 + j] = w.y;
-            x[k0 * 4 + 8 + j] = w.z;
-            x[k0 * 4 + 12 + j] = w.w;
+            const int row = lane + 32 * j, t = t0 + row;
+            if (((here >> (row >> 4)) & 1u) && t >= seg.tlo && t < seg.thi) count |= 1u << j;
           }
         }
-        if (v) {
-          // V's rows that do not count have scale 0: their probabilities are 0, but 0 * NaN is NaN
-          if (!(here == 0xffu && t0 >= seg.tlo && t0 + kFp4Tile <= seg.thi)) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int row = lane + 32 * j, t = t0 + row;
-              if (((here >> (row >> 4)) & 1u) && t >= seg.tlo && t < seg.thi) continue;
-#pragma unroll
-              for (int k = 0; k < C::KSTEPS; ++k) x[k * 4 + j] = 0u;
-            }
-          }
-          // A NaN block would spread over the unit matrix's zeros to other dims
-          // (and, of a token that only some of several query tokens attend, to the
-          // others): it is taken out and marked for the results it belongs to.
-          uint32_t bad = 0;
-#pragma unroll
-          for (int k = 0; k < C::KSTEPS * 4; ++k) bad |= nan_scales(x[k]);
-          if (__any_sync(kFullMask, bad != 0u)) {
-#pragma unroll
-            for (int k = 0; k < C::KSTEPS * 4; ++k) {
-              const uint32_t nan = nan_scales(x[k]);
-              if (!nan) continue;
-              x[k] &= ~((nan >> 7) * 0xffu);
-              if (warp != kSfWarp) continue;
-              const int t = t0 + lane + 32 * (k & 3);
-              for (int c = 0; c < C::CC && cm.valid(c); ++c) {
-                const int end = seg.col_hi(p, cm, c);
-                if (t >= end || (p.window > 0 && t < end - p.window)) continue;
-                for (int y = 0; y < 4; ++y)
-                  if ((nan >> (8 * y + 7)) & 1u) atomicOr(&poison[c], 1u << ((k >> 2) * 4 + y));
-              }
-            }
-          }
-        }
-#pragma unroll
+        const uint8_t* sf = smem + st * C::ITEM_BYTES + C::CODE_BYTES + lane * C::ROW_SF;
+#pragma unroll 1
         for (int k0 = 0; k0 < C::KSTEPS; k0 += 4) {
-          uint32_t r16[16];
+          uint32_t x[16], bad = 0;  // [64 dims][row group]
 #pragma unroll
-          for (int q = 0; q < 16; ++q) r16[q] = x[k0 * 4 + q];
-          tmem_st(at + k0 * 4, r16);
+          for (int j = 0; j < 4; ++j) {
+            uint4 w = *reinterpret_cast<const uint4*>(sf + 32 * j * C::ROW_SF + k0 * 4);
+            if (!((count >> j) & 1u)) w = make_uint4(0u, 0u, 0u, 0u);
+            x[j] = w.x;
+            x[4 + j] = w.y;
+            x[8 + j] = w.z;
+            x[12 + j] = w.w;
+            bad |= nan_scales(w.x) | nan_scales(w.y) | nan_scales(w.z) | nan_scales(w.w);
+          }
+          if (v && __any_sync(kFullMask, bad != 0u)) {
+            // A NaN block would spread over the unit matrix's zeros to other dims
+            // (and, of a token that only some of several query tokens attend, to the
+            // others): it is taken out and marked for the results it belongs to.
+#pragma unroll
+            for (int k = 0; k < 16; ++k) x[k] &= ~((nan_scales(x[k]) >> 7) * 0xffu);
+            if (warp == kSfWarp) {
+#pragma unroll 1
+              for (int e = 0; e < 64; ++e) {  // [row group][64 dims][16 dims]
+                const int j = e >> 4, y = e & 15, t = t0 + lane + 32 * j;
+                if (!((count >> j) & 1u) || (sf[32 * j * C::ROW_SF + k0 * 4 + y] & 0x7f) != 0x7f) continue;
+                Pair col(seg);
+#pragma unroll 1
+                for (int c = 0; c < C::CC && col.valid(p); ++c, col.next(p)) {
+                  const int end = col.end(p, seg);
+                  if (t < end && (p.window == 0 || t >= end - p.window))
+                    atomicOr(&poison_of[(sg & 3) * C::CC + c], 1u << (k0 * 4 + y));
+                }
+              }
+              __syncwarp();
+            }
+          }
+          tmem_st((v ? kTmemSfv : kTmemSfk) + quarter + k0 * 4, x);
         }
         tmem_wait_st();
         tmem_fence_before();
         __syncwarp();
-      };
-#pragma unroll 1
-      for (int i = 0; i < seg.tiles; ++i, ++it) {
-        // K's, once the product before has read the last tile's
-        const int st = it % C::NK;
-        await(&full[st], it / C::NK);
-        if (it > 0) await(&s_full[(it - 1) % SB], (it - 1) / SB);
-        tmem_fence_after();
-        put(smem + st * C::ITEM_BYTES + C::CODE_BYTES, tmem + kTmemSfk + quarter, false, 0u, 0);
-        if (lane == 0) mbar_arrive(sfk_ready);
-        // V's likewise
-        const int n = C::KVS ? C::NK : C::NV, sv = (C::KVS ? 0 : C::NK) + it % n;
-        if (!C::KVS) await(&full[sv], it / n);
-        if (it > 0) await(dq_done, it - 1);
-        tmem_fence_after();
-        put(smem + sv * C::ITEM_BYTES + C::CODE_BYTES, tmem + kTmemSfv + quarter, true, valid[sv] & 0xffu,
-            seg.t_base + i * kFp4Tile);
-        if (lane == 0) mbar_arrive(sfv_ready);
+        if (lane == 0) mbar_arrive(v ? sfv_ready : sfk_ready);
+        it += v;
       }
-      any = walk.next(seg);
     }
   } else if (warp == kMmaWarp) {
-    // ---- the products, by one lane in an order that keeps the tensor core busy
-    // (issued by three warps, a product each, they got in one another's way: a
-    // tf32 instruction took 62 cycles instead of 14). Chunks of 128 dims go in
-    // pairs, V^T of both and then both sums, so that one waits for its operand
-    // while the other runs; the next tile's scores go out between them, as soon
-    // as they can.
-    constexpr uint32_t kQk = (1u << 7) | (1u << 10) | ((uint32_t)(C::N / 8) << 17) | (8u << 24);  // e2m1, e4m3 scales
-    constexpr uint32_t kDq = (1u << 7) | (1u << 10) | ((uint32_t)(kFp4Tile / 8) << 17) | (8u << 24);
-    constexpr uint32_t kPv = (1u << 4) | (2u << 7) | (2u << 10) | (2u << 17) | (8u << 24);  // tf32 -> fp32, 128 x 16
-    if (any && elect_one()) {
-      // descriptors' bases; a step further is a constant added to the address field
-      const uint64_t ring_desc = smem_desc(smem_u32(smem), 0, C::SL * 1024);
-      const uint64_t q_desc = smem_desc(smem_u32(smem + C::Q_OFFSET), 0, C::SL * 1024);
-      const uint64_t eye_desc = smem_desc(smem_u32(smem + C::EYE_OFFSET), 0, 512, 64);
-      // (both 8-column groups of P are the same one: the upper columns are not read)
-      const uint64_t p_desc = smem_desc(smem_u32(smem + C::P_OFFSET), 0, 0);
+    // ---- the products, by one lane in an order that keeps the tensor core busy.
+    // Chunks of 128 dims go in pairs, V^T of both and then both sums, so that one
+    // waits for its operand while the other runs; the next tile's scores go out
+    // between them, as soon as they can. The lane's looks at barriers (~50 cycles
+    // each) are what the tensor core, which holds little of what is issued ahead,
+    // waits for: whoever can has waited for it on this lane's behalf, so that a
+    // tile takes one for its scores, one for V^T, one for P, and four a pair.
+    if (share_tiles > 0 && elect_one()) {
+      constexpr uint32_t kQk = (1u << 7) | (1u << 10) | ((uint32_t)(C::N / 8) << 17) | (8u << 24);  // e2m1, e4m3 scales
+      constexpr uint32_t kDq = (1u << 7) | (1u << 10) | ((uint32_t)(kFp4Tile / 8) << 17) | (8u << 24);
+      constexpr uint32_t kPv = (1u << 4) | (2u << 7) | (2u << 10) | (2u << 17) | (8u << 24);  // tf32 -> fp32, 128 x 16
+      constexpr uint32_t kRows = desc_hi(C::SL * 1024), kEye = desc_hi(512, 64);
+      constexpr uint32_t kP = desc_hi(0);  // (both 8-column groups of P are the same: the upper columns are not read)
       constexpr int kItem = C::ITEM_BYTES >> 4;
-      int scores = 0, widened = 0, summed = 0;  // tiles, chunks, chunks issued so far
-      int q_seg = -1, o_seg = -1;               // segments of the newest scores and sums
-      auto qk = [&](int i) {
+      // descriptors' lower words: 16-byte units, a step further is a constant added
+      const uint32_t ring = smem_u32(smem) >> 4, q0 = ring + (C::Q_OFFSET >> 4), eye = ring + (C::EYE_OFFSET >> 4);
+      int scores = 0, sk = 0, sv = C::KVS ? 0 : C::NK;  // tiles whose scores are out; ring slots
+      auto qk = [&]() {
         tmem_fence_after();
-        const int st = i % C::NK, sbuf = i % SB;
-        const uint32_t word = valid[st];
-        if (word & kTileFirst) ++q_seg;
-        const uint64_t a = ring_desc + st * kItem, q = q_desc + (q_seg & 1) * (C::Q_BYTES >> 4);
+        const uint32_t word = valid[sk], buf = scores % SB;
+        const uint32_t a = ring + sk * kItem, q = q0 + ((word & kTileOdd) ? C::Q_BYTES >> 4 : 0);
 #pragma unroll
         for (int k = 0; k < C::KSTEPS; ++k)
-          mma_fp4(tmem + kTmemS + sbuf * C::N, a + (k >> 2) * 64 + (k & 3) * 2, q + (k >> 2) * 64 + (k & 3) * 2, kQk,
-                  tmem + kTmemSfk + k * 4, tmem + kTmemSfq + k * 4, k > 0);
-        mma_commit<1>(&s_full[sbuf]);
-        mma_commit<1>(&empty[st]);
+          mma_fp4<kRows, kRows, kQk>(kTmemS + buf * C::N, a + (k >> 2) * 64 + (k & 3) * 2, q + (k >> 2) * 64 + (k & 3) * 2,
+                                     kTmemSfk + k * 4, kTmemSfq + k * 4, k > 0);
+        mma_commit<1>(&s_full[buf]);
+        mma_commit<1>(&empty[sk]);
         if (word & kTileLast) mma_commit<1>(qk_done);
-        scores = i + 1;
+        mbar_arrive(&s_full[buf]);
+        ++scores;
+        if (++sk == C::NK) sk = 0;
       };
-      auto may_qk = [&](int i) {  // without waiting
-        const int st = i % C::NK, sn = q_seg + 1;
-        return mbar_test(&full[st], (i / C::NK) & 1) && mbar_test(sfk_ready, i & 1) &&
-               (i < SB || mbar_test(&s_empty[i % SB], (i / SB - 1) & 1)) &&
-               (!(valid[st] & kTileFirst) || mbar_test(&q_full[sn & 1], (sn >> 1) & 1));
-      };
-      bool end = false;
+      good = *tmem_at == 0;
+      int i = 0;
 #pragma unroll 1
-      for (int i = 0; good && !end; ++i) {
+      for (; i < share_tiles && good; ++i) {
         if (scores == i) {
-          const int sk = i % C::NK, sn = q_seg + 1;
-          good = mbar_wait(&full[sk], (i / C::NK) & 1) && mbar_wait(sfk_ready, i & 1) &&
-                 (i < SB || mbar_wait(&s_empty[i % SB], (i / SB - 1) & 1)) &&
-                 (!(valid[sk] & kTileFirst) || mbar_wait(&q_full[sn & 1], (sn >> 1) & 1));
-          if (!good) break;
-          qk(i);
+          if (!(good = wait_for(sfk_ready, i))) break;
+          qk();
         }
-        const int n = C::KVS ? C::NK : C::NV, st = (C::KVS ? 0 : C::NK) + i % n;
-        good = mbar_wait(&full[st], (i / n) & 1) && mbar_wait(sfv_ready, i & 1);
-        if (!good) break;
-        const uint32_t word = valid[st];
+        if (!(good = wait_for(sfv_ready, i))) break;
+        const uint32_t word = valid[sv], v = ring + sv * kItem, pa = ring + ((C::P_OFFSET + (i & 1) * C::P_BYTES) >> 4);
         const bool first = (word & kTileFirst) != 0;
-        end = (word & kTileEnd) != 0;
-        if (first) ++o_seg;
-        const uint64_t v = ring_desc + st * kItem;
-        const uint64_t pd = p_desc + (i & 1) * (C::P_BYTES >> 4);
-#pragma unroll 1
-        for (int c0 = 0; c0 < CH && good; c0 += 2) {
-          const int at = i * CH + c0;  // (even)
+#pragma unroll
+        for (int c0 = 0; c0 < CH; c0 += 2) {
+          const int use = i * (CH / 2) + c0 / 2;  // of either V^T buffer
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            if (good && at > 0) good = mbar_wait(&vt_empty[c], ((at >> 1) - 1) & 1);
-            if (!good) break;
+            // ---- V^T = I V^T of chunk c0 + c
+            good = good && (use == 0 || wait_for(&vt_empty[c], use - 1));
             tmem_fence_after();
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              mma_fp4(tmem + kTmemVt + c * 128, eye_desc + j * 2, v + (c0 >> 1) * 64 + c * 4 + j * 2, kDq, tmem + kTmemSfi,
-                      tmem + kTmemSfv + c0 * 8 + (c * 2 + j) * 4, j > 0);
+            const uint32_t b = v + (c0 >> 1) * 64 + c * 4, sfv = kTmemSfv + (c0 + c) * 8;
+            mma_fp4<kEye, kRows, kDq>(kTmemVt + c * 128, eye, b, kTmemSfi, sfv, false);
+            mma_fp4<kEye, kRows, kDq>(kTmemVt + c * 128, eye + 2, b + 2, kTmemSfi, sfv + 4, true);
             mma_commit<1>(&vt_full[c]);
-            widened = at + c + 1;
           }
-          if (!good) break;
           if (c0 + 2 == CH) {
-            mma_commit<1>(&empty[st]);
+            mma_commit<1>(&empty[sv]);
             mma_commit<1>(dq_done);
           }
-          if (!end && scores == i + 1 && may_qk(i + 1)) qk(i + 1);
-          if (c0 == 0) good = mbar_wait(&p_full[i & 1], (i >> 1) & 1) &&
-                              (!first || o_seg == 0 || mbar_wait(o_empty, (o_seg - 1) & 1));
+          if (scores == i + 1 && scores < share_tiles && mbar_test(sfk_ready, (i + 1) & 1)) qk();
+          if (c0 == 0) good = good && wait_for(&p_full[i & 1], i >> 1);
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            if (good) good = mbar_wait(&vt_full[c], (at >> 1) & 1);
-            if (!good) break;
+            // ---- O^T += V^T P^T of chunk c0 + c
+            good = good && wait_for(&vt_full[c], use);
             tmem_fence_after();
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
 #pragma unroll
-            for (int q = 0; q < kFp4Tile / 8; ++q)
-              mma_tf32(tmem + kTmemO + c0 * 16 + c * 16, tmem + kTmemVt + c * 128 + q * 8, pd + (q >> 2) * 64 + (q & 3) * 2,
-                       kPv, !first || q > 0);
-            mma_commit<1>(&vt_empty[c]);
-            summed = at + c + 1;
-          }
-          if (!good) break;
-          if (c0 + 2 == CH) {
-            mma_commit<1>(&p_empty[i & 1]);
-            if (word & kTileLast) {
-              mma_commit<1>(o_full);
-              mbar_arrive(o_full);  // (orders what this lane has seen of the scale warps' marks)
+              for (int k = 0; k < 4; ++k)
+                mma_tf32<kP, kPv>(kTmemO + (c0 + c) * 16, kTmemVt + c * 128 + q * 32 + k * 8, pa + q * 64 + k * 2,
+                                  !first || q > 0 || k > 0);
             }
+            mma_commit<1>(&vt_empty[c]);
           }
-          if (!end && scores == i + 1 && may_qk(i + 1)) qk(i + 1);
         }
+        mma_commit<1>(&p_empty[i & 1]);
+        if (word & kTileLast) {
+          mma_commit<1>(o_full);
+          mbar_arrive(o_full);
+        }
+        if (++sv == RINGS) sv = C::KVS ? 0 : C::NK;
       }
       // what was issued ends before its operands and results are used for something else
       if (!good) {
-        if (scores > 0) mbar_wait(&s_full[(scores - 1) % SB], ((scores - 1) / SB) & 1);
-        if (widened > 0) mbar_wait(&vt_full[(widened - 1) & 1], ((widened - 1) >> 1) & 1);
+        if (scores > 0) wait_for(&s_full[(scores - 1) % SB], (scores - 1) / SB);
         atomicOr(p.err, kErrTimeout);
       }
-      if (summed > 0) mbar_wait(&vt_empty[(summed - 1) & 1], ((summed - 1) >> 1) & 1);
+      if (i > 0) wait_for(&vt_empty[1], i * (CH / 2) - 1);
     }
     __syncwarp();
   } else {
@@ -863,6 +838,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     uint32_t* poison_of = reinterpret_cast<uint32_t*>(smem + C::POISON_OFFSET);
     volatile uint32_t* ticket = reinterpret_cast<uint32_t*>(smem + C::MISC_OFFSET);
     // the unit matrix in e2m1 (1.0 is 2): 16 bytes of row m hold dims 32 c .., the one lies at dim m
+#pragma unroll 1
     for (int i = wt; i < C::EYE_BYTES / 16; i += 128) {
       const int m = i >> 2, c = (i & 3) ^ ((m >> 1) & 3), word = (m >> 3) & 3;
       const uint32_t one = (m >> 5) == c ? 2u << (4 * (m & 7)) : 0u;
@@ -871,136 +847,135 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     }
     // the query rows beyond the terms, and the marks
     constexpr int USED = C::CC * kFp4Terms, REST = (C::N - USED) * (C::D / 32);  // 16-byte pieces of a buffer
-    for (int i = wt; i < (C::N - USED) * C::ROW_SF; i += 128) smem[C::QSF_OFFSET + USED * C::ROW_SF + i] = 0;
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      for (int i = wt; i < REST; i += 128)
-        *reinterpret_cast<uint4*>(smem + C::Q_OFFSET + k * C::Q_BYTES +
-                                  code_offset<C>(USED + i / (C::D / 32), (i % (C::D / 32)) * 16)) =
-            make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+    for (int i = wt; i < 2 * REST; i += 128) {
+      const int r = i < REST ? i : i - REST;
+      *reinterpret_cast<uint4*>(smem + C::Q_OFFSET + (i < REST ? 0 : C::Q_BYTES) +
+                                code_offset<C>(USED + r / (C::D / 32), (r % (C::D / 32)) * 16)) = make_uint4(0u, 0u, 0u, 0u);
+      if (i < (C::N - USED) * C::ROW_SF / 16)
+        *reinterpret_cast<uint4*>(smem + C::QSF_OFFSET + USED * C::ROW_SF + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
     for (int i = wt; i < 4 * C::CC; i += 128) poison_of[i] = 0u;
     {
       uint32_t one[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) one[k] = 0x38383838u;  // e4m3 1.0
-      tmem_st(tmem + kTmemSfi + quarter, one);
+      tmem_st(kTmemSfi + quarter, one);
     }
-    auto prepare = [&](int sg, const Segment<C>& s) {
-      named_bar_sync(3, 128);  // the scales of the segment before are in tensor memory
-      // (its terms' buffer: the scores of the last segment but one are computed, as this warp has seen)
-      write_query_terms<C>(p, Columns<C>(p, s.b, s.y), smem + C::Q_OFFSET + (sg & 1) * C::Q_BYTES, smem + C::QSF_OFFSET,
-                           reinterpret_cast<float*>(smem + C::COL_OFFSET) + (sg & 1) * C::CC, we, lane);
-      fence_proxy_async_smem();
-      named_bar_sync(3, 128);
-      if (sg > 0) await(qk_done, sg - 1);
-      tmem_fence_after();
-#pragma unroll
-      for (int k0 = 0; k0 < C::KSTEPS; k0 += 2) {
-        uint32_t r8[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int row = lane + 32 * (i & 3);
-          r8[i] = row < C::N
-                      ? *reinterpret_cast<const uint32_t*>(smem + C::QSF_OFFSET + row * C::ROW_SF + (k0 + (i >> 2)) * 4)
-                      : 0u;
-        }
-        tmem_st(tmem + kTmemSfq + quarter + k0 * 4, r8);
-      }
-      tmem_wait_st();
-      tmem_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[sg & 1]);
-    };
-    if (any) prepare(0, seg);
+    Segment next;
+    bool any = walk_next<C::CC>(p, walk, next);
 #pragma unroll 1
-    for (int sg = 0; any; ++sg) {
-      const bool more = walk.next(next);
-      if (more) prepare(sg + 1, next);
-      const Columns<C> cm(p, seg.b, seg.y);
-      await(&l_full[sg & 1], sg >> 1);
-      await(o_full, sg);
-      tmem_fence_after();
-      // lane l of quarter w has dim 32 w + l of each chunk
-      uint32_t o[CH][8];
+    for (int sg = -1; sg < 0 ? any : true; ++sg) {
+      if (any) {
+        // ---- segment sg + 1's terms (their buffer is free: the scores of segment sg - 1 are computed, as these warps
+        // have seen), and their scales once segment sg's scores are computed
+        named_bar_sync(3, 128);  // the scales before are in tensor memory
+        write_query_terms<C>(p, next, smem + C::Q_OFFSET + ((sg + 1) & 1) * C::Q_BYTES, smem + C::QSF_OFFSET,
+                             reinterpret_cast<float*>(smem + C::COL_OFFSET) + ((sg + 1) & 1) * C::CC, we, lane);
+        fence_proxy_async_smem();
+        named_bar_sync(3, 128);
+        if (sg >= 0) await(qk_done, sg);
+        tmem_fence_after();
+#pragma unroll 1
+        for (int k0 = 0; k0 < C::KSTEPS; k0 += 2) {
+          uint32_t r8[8];
 #pragma unroll
-      for (int k = 0; k < CH; ++k) tmem_ld(o[k], tmem + kTmemO + k * 16 + quarter);
-      tmem_wait_ld();
-      tmem_fence_before();
-      const float* sum_of = reinterpret_cast<const float*>(smem + C::SUM_OFFSET) + (sg & 1) * 5 * C::CC;
-      uint32_t* poison = poison_of + (sg & 3) * C::CC;
-      float coef[C::CC], lse[C::CC];
-      uint32_t nan[C::CC];
-#pragma unroll
-      for (int c = 0; c < C::CC; ++c) {
-        const float s = (sum_of[c] + sum_of[C::CC + c]) + (sum_of[2 * C::CC + c] + sum_of[3 * C::CC + c]);
-        coef[c] = s != 0.f ? p.v_mul / s : 0.f;
-        lse[c] = s != 0.f ? (sum_of[4 * C::CC + c] + __log2f(s)) * 0.69314718055994530942f : -INFINITY;
-        nan[c] = poison[c];
+          for (int i = 0; i < 8; ++i) {
+            const int row = lane + 32 * (i & 3);
+            r8[i] = row < C::N
+                        ? *reinterpret_cast<const uint32_t*>(smem + C::QSF_OFFSET + row * C::ROW_SF + (k0 + (i >> 2)) * 4)
+                        : 0u;
+          }
+          tmem_st(kTmemSfq + quarter + k0 * 4, r8);
+        }
+        tmem_wait_st();
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[(sg + 1) & 1]);
       }
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(o_empty);
-        mbar_arrive(&l_empty[sg & 1]);
-      }
-      named_bar_sync(3, 128);
-      if (wt < C::CC) poison[wt] = 0u;
-      const int slot = blockIdx.x * 2 + (seg.piece == 0 ? 1 : 0);
-#pragma unroll
-      for (int c = 0; c < C::CC; ++c) {
-        if (!cm.valid(c)) break;
-#pragma unroll
+      if (sg >= 0) {
+        // ---- segment sg's results
+        await(&l_full[sg & 1], sg >> 1);
+        await(o_full, sg);
+        tmem_fence_after();
+        const float* sum_of = reinterpret_cast<const float*>(smem + C::SUM_OFFSET) + (sg & 1) * 5 * C::CC;
+        uint32_t* poison = poison_of + (sg & 3) * C::CC;
+        const int slot = blockIdx.x * 2 + (seg.piece == 0 ? 1 : 0);
+        // lane l of quarter w has dim 32 w + l of each chunk
+#pragma unroll 1
         for (int k = 0; k < CH; ++k) {
+          uint32_t o[8];
+          tmem_ld(o, kTmemO + k * 16 + quarter);
+          tmem_wait_ld();
           const int dim = k * 128 + we * 32 + lane;
-          // (no attended token: coefficient 0)
-          float x = coef[c] != 0.f ? __uint_as_float(o[k][c]) * coef[c] : 0.f;
-          if ((nan[c] >> (dim >> 4)) & 1u) x = NAN;
-          if (seg.pieces == 1)
-            reinterpret_cast<__nv_bfloat16*>(p.out)[cm.row(c) * C::D + dim] = __float2bfloat16_rn(x);
-          else
-            p.o_part[((size_t)slot * C::CC + c) * C::D + dim] = x;
-        }
-        if (seg.pieces > 1 && wt == c) p.lse_part[slot * C::CC + c] = lse[c];
-      }
-      if (seg.pieces > 1) {
-        // whoever leaves the last piece joins them all, in their order:
-        // out = sum_s w_s o_s,  w_s = exp(lse_s - M) / sum_s' exp(lse_s' - M)
-        __threadfence();
-        named_bar_sync(3, 128);
-        if (wt == 0) *ticket = atomicAdd(&p.counters[seg.first_share], 1u);
-        named_bar_sync(3, 128);
-        if (*ticket == (uint32_t)seg.pieces - 1) {
-          __threadfence();
-          if (wt == 0) p.counters[seg.first_share] = 0u;
-          auto slot_of = [&](int q) { return (seg.first_share + q) * 2 + (q == 0 ? 1 : 0); };
-#pragma unroll 1
-          for (int e = wt; e < C::CC * (C::D / 4); e += 128) {
-            const int c = e / (C::D / 4), dim = (e % (C::D / 4)) * 4;
-            if (!cm.valid(c)) break;
-            float M = -INFINITY;
-#pragma unroll 4
-            for (int q = 0; q < seg.pieces; ++q) M = fmaxf(M, __ldcg(p.lse_part + slot_of(q) * C::CC + c));
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            float w_sum = 0.f;
-#pragma unroll 4
-            for (int q = 0; q < seg.pieces; ++q) {
-              const float l = __ldcg(p.lse_part + slot_of(q) * C::CC + c);
-              const float4 x =
-                  __ldcg(reinterpret_cast<const float4*>(p.o_part + ((size_t)slot_of(q) * C::CC + c) * C::D + dim));
-              const float w = l == -INFINITY ? 0.f : ex2((l - M) * 1.4426950408889634f);
-              w_sum += w;
-              acc.x = fmaf(w, x.x, acc.x);
-              acc.y = fmaf(w, x.y, acc.y);
-              acc.z = fmaf(w, x.z, acc.z);
-              acc.w = fmaf(w, x.w, acc.w);
+          Pair col(seg);
+#pragma unroll
+          for (int c = 0; c < C::CC; ++c, col.next(p)) {
+            const float l = (sum_of[c] + sum_of[C::CC + c]) + (sum_of[2 * C::CC + c] + sum_of[3 * C::CC + c]);
+            // (no attended token: zeros, whatever the sums hold)
+            float x = l != 0.f ? __uint_as_float(o[c]) * (p.v_mul / l) : 0.f;
+            if ((poison[c] >> (dim >> 4)) & 1u) x = NAN;
+            if (!col.valid(p)) continue;
+            if (seg.pieces == 1) {
+              reinterpret_cast<__nv_bfloat16*>(p.out)[col.row(p, seg) * C::D + dim] = __float2bfloat16_rn(x);
+            } else {
+              p.o_part[((size_t)slot * C::CC + c) * C::D + dim] = x;
+              if (k == 0 && wt == c)
+                p.lse_part[slot * C::CC + c] =
+                    l != 0.f ? (sum_of[4 * C::CC + c] + __log2f(l)) * 0.69314718055994530942f : -INFINITY;
             }
-            const float inv = w_sum != 0.f ? 1.f / w_sum : 0.f;
-            *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + cm.row(c) * C::D + dim) =
-                make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+          }
+        }
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_empty);
+        if (seg.pieces > 1) __threadfence();
+        named_bar_sync(3, 128);
+        if (lane == 0) mbar_arrive(&l_empty[sg & 1]);
+        if (wt < C::CC) poison[wt] = 0u;
+        if (seg.pieces > 1) {
+          // whoever leaves the last piece joins them all, in their order:
+          // out = sum_s w_s o_s,  w_s = exp(lse_s - M) / sum_s' exp(lse_s' - M)
+          if (wt == 0) *ticket = atomicAdd(&p.counters[seg.first_share], 1u);
+          named_bar_sync(3, 128);
+          if (*ticket == (uint32_t)seg.pieces - 1) {
+            __threadfence();
+            if (wt == 0) p.counters[seg.first_share] = 0u;
+            Pair col(seg);
+#pragma unroll 1
+            for (int c = 0; c < C::CC && col.valid(p); ++c, col.next(p)) {
+              const float* lse = p.lse_part + c;
+              // piece q lies in slot 2 (first_share + q), the first one in the next
+              float M = -INFINITY;
+#pragma unroll 4
+              for (int q = 0; q < seg.pieces; ++q)
+                M = fmaxf(M, __ldcg(lse + ((seg.first_share + q) * 2 + (q == 0)) * C::CC));
+              float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+              float w_sum = 0.f;
+              if (wt < C::D / 4) {
+#pragma unroll 4
+                for (int q = 0; q < seg.pieces; ++q) {
+                  const size_t at = ((size_t)(seg.first_share + q) * 2 + (q == 0)) * C::CC;
+                  const float l = __ldcg(lse + at);
+                  const float4 x = __ldcg(reinterpret_cast<const float4*>(p.o_part + (at + c) * C::D) + wt);
+                  const float w = l == -INFINITY ? 0.f : ex2((l - M) * 1.4426950408889634f);
+                  w_sum += w;
+                  acc.x = fmaf(w, x.x, acc.x);
+                  acc.y = fmaf(w, x.y, acc.y);
+                  acc.z = fmaf(w, x.z, acc.z);
+                  acc.w = fmaf(w, x.w, acc.w);
+                }
+                const float inv = w_sum != 0.f ? 1.f / w_sum : 0.f;
+                reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + col.row(p, seg) * C::D)[wt] =
+                    make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+              }
+            }
           }
         }
       }
+      if (!any) break;
       seg = next;
-      any = more;
+      any = walk_next<C::CC>(p, walk, next);
     }
   }
   __syncthreads();
@@ -1094,6 +1069,8 @@ pd_status decode_fp4(const pd_plan* plan, const void* q, const void* k_pool, con
   p.query_tokens = plan->query_tokens;
   p.group = ly.num_q_heads / ly.num_kv_heads;
   p.col_tiles = (p.query_tokens * p.group + kVariants[plan->variant].group - 1) / kVariants[plan->variant].group;
+  p.units = ly.num_kv_heads * p.col_tiles;
+  p.cap = ly.max_pages_per_seq * ly.page_size;
 
   void* args[] = {&p};
   cudaLaunchConfig_t cfg = {};
