@@ -33,7 +33,8 @@
 // by 2^60 (tf32 has fp32's exponents), which rescales the sums.
 //
 // Roles: warps 0-3 softmax (a lane a token); 4-7 write the tiles' scales to tensor
-// memory; 8, 9 copy codes (TMA), 10 scales (cp.async); 11 issues the products;
+// memory; 8 copies codes (TMA), 9 scales (cp.async); 10 issues the scores and V^T,
+// 11 the sums;
 // 12-15 write the next unit's query terms, read a unit's sums and join pieces.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -125,6 +126,8 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t phase) {
 
 // What a ring slot's word says of its tile, beside the 16-token blocks that have a page (bits 0-7).
 constexpr uint32_t kTileFirst = 0x100u, kTileLast = 0x200u, kTileOdd = 0x400u;  // of its segment; an odd one
+
+constexpr uint32_t kNoRow = 0xffffffffu;
 
 // A request's attended range, cut to what its block table holds.
 struct Span {
@@ -371,13 +374,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFFSET);  // [RINGS]: K's ring, then V's
   uint64_t* empty = full + RINGS;                                      // [RINGS]
   // one arrival: the products' commits
-  uint64_t* vt_full = empty + RINGS;    // [2] a chunk of V^T there
-  uint64_t* vt_empty = vt_full + 2;     // [2] and used
+  uint64_t* vt_empty = empty + RINGS;   // [2] a chunk of V^T used
   uint64_t* p_empty = vt_empty + 2;     // [2] P used: the tile is in the sums
   uint64_t* dq_done = p_empty + 2;      // a tile's V^T all there
   uint64_t* qk_done = dq_done + 1;      // a segment's scores all computed
   // two: a commit, and an arrival of the same lane (which orders what it has seen of others)
-  uint64_t* s_full = qk_done + 1;       // [2] scores computed
+  uint64_t* vt_full = qk_done + 1;      // [2] a chunk of V^T there
+  uint64_t* s_full = vt_full + 2;       // [2] scores computed
   uint64_t* o_full = s_full + 2;        // a segment's sums complete
   // four warps
   uint64_t* sfk_ready = o_full + 1;     // K's scales in tensor memory
@@ -388,13 +391,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
   uint64_t* o_empty = q_full + 2;       // a segment's sums read
   uint64_t* l_full = o_empty + 1;       // [2] a segment's probabilities' sums there
   uint64_t* l_empty = l_full + 2;       // [2] and read
-  static_assert(C::NUM_BARS == 2 * RINGS + 8 + 3 + 13, "as listed");
+  static_assert(C::NUM_BARS == 2 * RINGS + 6 + 5 + 13, "as listed");
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(full + C::NUM_BARS);
   volatile uint32_t* valid = reinterpret_cast<uint32_t*>(smem + C::VALID_OFFSET);  // [RINGS]
+  volatile uint32_t* tile_of = reinterpret_cast<uint32_t*>(smem + C::TILE_OFFSET);      // [2] first, last: by P buffer
   volatile uint32_t* blocks_of = reinterpret_cast<uint32_t*>(smem + C::BLOCKS_OFFSET);  // [4] by tile
-  constexpr int kSfWarp = 4, kCodeWarp = 8, kScaleWarp = 10, kMmaWarp = 11, kEndWarp = 12;
+  constexpr int kSfWarp = 4, kCodeWarp = 8, kScaleWarp = 9, kMmaWarp = 10, kSumWarp = 11, kEndWarp = 12;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const bool copies = warp >= kCodeWarp && warp <= kScaleWarp;
+  const bool copies = warp == kCodeWarp || warp == kScaleWarp;
   const bool early = p.early_kv != 0 && copies;
 
   if (warp == kCodeWarp) {
@@ -404,15 +408,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     }
     for (int i = lane; i < C::NUM_BARS; i += 32) {
       const int r = i - 2 * RINGS;
-      // full: the codes' byte count (K = V: two warps') and every lane's scales; empty: the products that read the slot
-      mbar_init(&full[i], i < RINGS ? (C::KVS ? 34 : 33) : r < 0 ? (C::KVS ? 2 : 1) : r < 8 ? 1 : r < 11 ? 2 : 4);
+      // full: the codes' byte count and every lane's scales; empty: the products that read the slot
+      mbar_init(&full[i], i < RINGS ? 33 : r < 0 ? (C::KVS ? 2 : 1) : r < 6 ? 1 : r < 11 ? 2 : 4);
     }
     fence_barrier_init();
     __syncwarp();
   }
   if (warp == kMmaWarp) tmem_alloc<1>(tmem_at, kTmemCols);
   if (copies) {
-    named_bar_sync(5, 3 * 32);
+    named_bar_sync(5, 2 * 32);
     named_bar_arrive(4, C::THREADS);
   }
   if (!early) {
@@ -448,7 +452,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     bool waited = !early, stop = false;
     uint32_t err_bits = 0;
     const uint64_t policy = l2_evict_first_policy();
-    const int mine = warp - kCodeWarp;  // 0: K's codes, 1: V's (K = V: the lower and the upper half), 2: scales
+    const bool codes = warp == kCodeWarp;  // (the other warp: the scales)
     Segment next;
     bool any = walk_next<C::CC>(p, walk, next);
     auto page_of = [&](const Segment& s, int i) {
@@ -474,7 +478,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
         }
         const int row0 = __shfl_sync(kFullMask, rows, (i & 3) * 8 + (lane & 7));
         const uint32_t bits = __ballot_sync(kFullMask, row0 >= 0) & 0xffu;
-        const uint32_t word = bits | odd | (i == 0 ? kTileFirst : 0u) | (i + 1 == seg.tiles ? kTileLast : 0u);
+        const uint32_t word = bits | odd | (i + 1 == seg.tiles ? kTileLast : 0u);
         // rows of the newest tokens may still be written by the kernel in front
         if (!waited && (it >= C::NK || (!C::KVS && it >= C::NV) ||
                         seg.t_base + (i + 1) * kFp4Tile > seg.L - p.query_tokens)) {
@@ -484,7 +488,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
         }
 #pragma unroll 1
         for (int v = 0; v < (C::KVS ? 1 : 2); ++v) {
-          if (!C::KVS && mine == 1 - v) continue;
           const int n = v ? C::NV : C::NK, round = it / n, st = (v ? C::NK : 0) + it - round * n;
           if (round > 0 && __any_sync(kFullMask, !wait_for(&empty[st], round - 1))) {
             err_bits |= kErrTimeout;
@@ -492,17 +495,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
             break;
           }
           uint8_t* item = smem + st * C::ITEM_BYTES;
-          if (mine < 2) {
-            const uint32_t part = C::KVS ? bits & (mine ? 0xf0u : 0x0fu) : bits;
+          if (codes) {
             if (lane == 0) {
-              if (!C::KVS || mine == 0) valid[st] = word;
-              if (part)
-                mbar_arrive_expect_tx(&full[st], __popc(part) * (16 * C::D / 2) + (mine == 0 ? p.stall_bytes : 0));
+              valid[st] = word;
+              if (bits)
+                mbar_arrive_expect_tx(&full[st], __popc(bits) * (16 * C::D / 2) + (v ? 0 : p.stall_bytes));
               else
                 mbar_arrive(&full[st]);
             }
             __syncwarp();
-            if (lane < 8 && ((part >> lane) & 1u))
+            if (lane < 8 && row0 >= 0)
               tma_load_4d(item + lane * 16 * (C::D / 2), v ? &p.vmap : &p.kmap, 0, 0, 0, row0 / 8, &full[st], policy);
           } else {
             // 16 bytes a lane (as bulk copies these would be half of all copies)
@@ -526,7 +528,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     const unsigned long long deadline = global_timer_ns() + kWaitTimeoutNs;
     for (int s = lane; s < RINGS; s += 32) {
       const int n = s < C::NK ? C::NK : C::NV, at = s < C::NK ? s : s - C::NK;
-      if (at >= it || (!C::KVS && mine != 2 && (s >= C::NK) != (mine == 1))) continue;
+      if (at >= it) continue;
       const int last = at + n * ((it - 1 - at) / n);
       if (!mbar_wait_until(&full[s], (last / n) & 1, deadline)) err_bits |= kErrTimeout;
     }
@@ -644,6 +646,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
           const uint32_t at = p_at + buf * C::P_BYTES + c * 128 + (((lane >> 2) ^ c) << 4);
           asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(w) : "memory");
         }
+        if (tid == 0) tile_of[buf] = (i == 0 ? kTileFirst : 0u) | (i + 1 == seg.tiles ? kTileLast : 0u);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[buf]);
@@ -674,13 +677,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
         const bool v = (u & 1) != 0;
         const int n = v && !C::KVS ? C::NV : C::NK, round = it / n, st = (v && !C::KVS ? C::NK : 0) + it - round * n;
         await(&full[st], round);
-        if (it > 0) await(v ? dq_done : &s_full[(it - 1) % SB], v ? it - 1 : (it - 1) / SB);
-        if (!v) {
-          // what the scores' product needs besides: a free buffer, and the segment's query terms
-          if (it >= SB) await(&s_empty[it % SB], it / SB - 1);
-          if (u == 0) await(&q_full[sg & 1], sg >> 1);
-        }
-        tmem_fence_after();
         const uint32_t here = valid[st] & 0xffu;
         const int t0 = seg.t_base + (u >> 1) * kFp4Tile;
         if (!v && warp == kSfWarp && lane == 0) blocks_of[it & 3] = here;
@@ -695,43 +691,50 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
           }
         }
         const uint8_t* sf = smem + st * C::ITEM_BYTES + C::CODE_BYTES + lane * C::ROW_SF;
-#pragma unroll 1
-        for (int k0 = 0; k0 < C::KSTEPS; k0 += 4) {
-          uint32_t x[16], bad = 0;  // [64 dims][row group]
+        uint32_t x[C::KSTEPS / 4][16], bad = 0;  // [256 dims][64 dims][row group]
+#pragma unroll
+        for (int k = 0; k < C::KSTEPS / 4; ++k)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            uint4 w = *reinterpret_cast<const uint4*>(sf + 32 * j * C::ROW_SF + k0 * 4);
+            uint4 w = *reinterpret_cast<const uint4*>(sf + 32 * j * C::ROW_SF + k * 16);
             if (!((count >> j) & 1u)) w = make_uint4(0u, 0u, 0u, 0u);
-            x[j] = w.x;
-            x[4 + j] = w.y;
-            x[8 + j] = w.z;
-            x[12 + j] = w.w;
+            x[k][j] = w.x;
+            x[k][4 + j] = w.y;
+            x[k][8 + j] = w.z;
+            x[k][12 + j] = w.w;
             bad |= nan_scales(w.x) | nan_scales(w.y) | nan_scales(w.z) | nan_scales(w.w);
           }
-          if (v && __any_sync(kFullMask, bad != 0u)) {
-            // A NaN block would spread over the unit matrix's zeros to other dims
-            // (and, of a token that only some of several query tokens attend, to the
-            // others): it is taken out and marked for the results it belongs to.
+        if (v && __any_sync(kFullMask, bad != 0u)) {
+          // A NaN block would spread over the unit matrix's zeros to other dims
+          // (and, of a token that only some of several query tokens attend, to the
+          // others): it is taken out and marked for the results it belongs to.
 #pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] &= ~((nan_scales(x[k]) >> 7) * 0xffu);
-            if (warp == kSfWarp) {
+          for (int k = 0; k < C::KSTEPS * 4; ++k) x[k >> 4][k & 15] &= ~((nan_scales(x[k >> 4][k & 15]) >> 7) * 0xffu);
+          if (warp == kSfWarp) {
 #pragma unroll 1
-              for (int e = 0; e < 64; ++e) {  // [row group][64 dims][16 dims]
-                const int j = e >> 4, y = e & 15, t = t0 + lane + 32 * j;
-                if (!((count >> j) & 1u) || (sf[32 * j * C::ROW_SF + k0 * 4 + y] & 0x7f) != 0x7f) continue;
-                Pair col(seg);
+            for (int e = 0; e < 4 * C::ROW_SF; ++e) {  // [row group][16 dims]
+              const int j = e / C::ROW_SF, y = e % C::ROW_SF, t = t0 + lane + 32 * j;
+              if (!((count >> j) & 1u) || (sf[32 * j * C::ROW_SF + y] & 0x7f) != 0x7f) continue;
+              Pair col(seg);
 #pragma unroll 1
-                for (int c = 0; c < C::CC && col.valid(p); ++c, col.next(p)) {
-                  const int end = col.end(p, seg);
-                  if (t < end && (p.window == 0 || t >= end - p.window))
-                    atomicOr(&poison_of[(sg & 3) * C::CC + c], 1u << (k0 * 4 + y));
-                }
+              for (int c = 0; c < C::CC && col.valid(p); ++c, col.next(p)) {
+                const int end = col.end(p, seg);
+                if (t < end && (p.window == 0 || t >= end - p.window)) atomicOr(&poison_of[(sg & 3) * C::CC + c], 1u << y);
               }
-              __syncwarp();
             }
+            __syncwarp();
           }
-          tmem_st((v ? kTmemSfv : kTmemSfk) + quarter + k0 * 4, x);
         }
+        // the product that reads the tile before's is done; what the scores' product
+        // needs besides: a free buffer, and the segment's query terms
+        if (it > 0) await(v ? dq_done : &s_full[(it - 1) % SB], v ? it - 1 : (it - 1) / SB);
+        if (!v) {
+          if (it >= SB) await(&s_empty[it % SB], it / SB - 1);
+          if (u == 0) await(&q_full[sg & 1], sg >> 1);
+        }
+        tmem_fence_after();
+#pragma unroll
+        for (int k = 0; k < C::KSTEPS / 4; ++k) tmem_st((v ? kTmemSfv : kTmemSfk) + quarter + k * 16, x[k]);
         tmem_wait_st();
         tmem_fence_before();
         __syncwarp();
@@ -740,80 +743,91 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
       }
     }
   } else if (warp == kMmaWarp) {
-    // ---- the products, by one lane in an order that keeps the tensor core busy.
-    // Chunks of 128 dims go in pairs, V^T of both and then both sums, so that one
-    // waits for its operand while the other runs; the next tile's scores go out
-    // between them, as soon as they can. The lane's looks at barriers (~50 cycles
-    // each) are what the tensor core, which holds little of what is issued ahead,
-    // waits for: whoever can has waited for it on this lane's behalf, so that a
-    // tile takes one for its scores, one for V^T, one for P, and four a pair.
+    // ---- the scores and V^T, by one lane, which looks at barriers (~50 cycles a
+    // look) as seldom as can be: whoever else can has waited on its behalf. The
+    // tensor core holds little of what is issued ahead, so the sums are another
+    // warp's, whose looks fall elsewhere.
     if (share_tiles > 0 && elect_one()) {
       constexpr uint32_t kQk = (1u << 7) | (1u << 10) | ((uint32_t)(C::N / 8) << 17) | (8u << 24);  // e2m1, e4m3 scales
       constexpr uint32_t kDq = (1u << 7) | (1u << 10) | ((uint32_t)(kFp4Tile / 8) << 17) | (8u << 24);
-      constexpr uint32_t kPv = (1u << 4) | (2u << 7) | (2u << 10) | (2u << 17) | (8u << 24);  // tf32 -> fp32, 128 x 16
       constexpr uint32_t kRows = desc_hi(C::SL * 1024), kEye = desc_hi(512, 64);
-      constexpr uint32_t kP = desc_hi(0);  // (both 8-column groups of P are the same: the upper columns are not read)
       constexpr int kItem = C::ITEM_BYTES >> 4;
       // descriptors' lower words: 16-byte units, a step further is a constant added
       const uint32_t ring = smem_u32(smem) >> 4, q0 = ring + (C::Q_OFFSET >> 4), eye = ring + (C::EYE_OFFSET >> 4);
-      int scores = 0, sk = 0, sv = C::KVS ? 0 : C::NK;  // tiles whose scores are out; ring slots
-      auto qk = [&]() {
-        tmem_fence_after();
-        const uint32_t word = valid[sk], buf = scores % SB;
-        const uint32_t a = ring + sk * kItem, q = q0 + ((word & kTileOdd) ? C::Q_BYTES >> 4 : 0);
-#pragma unroll
-        for (int k = 0; k < C::KSTEPS; ++k)
-          mma_fp4<kRows, kRows, kQk>(kTmemS + buf * C::N, a + (k >> 2) * 64 + (k & 3) * 2, q + (k >> 2) * 64 + (k & 3) * 2,
-                                     kTmemSfk + k * 4, kTmemSfq + k * 4, k > 0);
-        mma_commit<1>(&s_full[buf]);
-        mma_commit<1>(&empty[sk]);
-        if (word & kTileLast) mma_commit<1>(qk_done);
-        mbar_arrive(&s_full[buf]);
-        ++scores;
-        if (++sk == C::NK) sk = 0;
-      };
+      int scores = 0, sk = 0, sv = C::KVS ? 0 : C::NK, i = 0;  // tiles whose scores are out; ring slots
       good = *tmem_at == 0;
-      int i = 0;
 #pragma unroll 1
-      for (; i < share_tiles && good; ++i) {
-        if (scores == i) {
-          if (!(good = wait_for(sfk_ready, i))) break;
-          qk();
+      for (int u = 0; good; u ^= 1) {
+        // u 0: a tile begins; 1: half of its chunks are out
+        if (scores == i ? u == 0 : scores < share_tiles && mbar_test(sfk_ready, scores & 1)) {
+          // ---- S = K q^T, of this tile at the latest and of the next as soon as it can be
+          if (!(good = wait_for(sfk_ready, scores))) break;
+          tmem_fence_after();
+          const uint32_t word = valid[sk], buf = scores % SB;
+          const uint32_t a = ring + sk * kItem, q = q0 + ((word & kTileOdd) ? C::Q_BYTES >> 4 : 0);
+#pragma unroll
+          for (int k = 0; k < C::KSTEPS; ++k)
+            mma_fp4<kRows, kRows, kQk>(kTmemS + buf * C::N, a + (k >> 2) * 64 + (k & 3) * 2,
+                                       q + (k >> 2) * 64 + (k & 3) * 2, kTmemSfk + k * 4, kTmemSfq + k * 4, k > 0);
+          mma_commit<1>(&s_full[buf]);
+          mma_commit<1>(&empty[sk]);
+          if (word & kTileLast) mma_commit<1>(qk_done);
+          mbar_arrive(&s_full[buf]);
+          ++scores;
+          if (++sk == C::NK) sk = 0;
         }
-        if (!(good = wait_for(sfv_ready, i))) break;
-        const uint32_t word = valid[sv], v = ring + sv * kItem, pa = ring + ((C::P_OFFSET + (i & 1) * C::P_BYTES) >> 4);
-        const bool first = (word & kTileFirst) != 0;
+        if (u == 0 && !(good = wait_for(sfv_ready, i))) break;
+        // ---- V^T = I V^T, two chunks of 128 dims (d 256: one)
+        const uint32_t v = ring + sv * kItem + (CH == 4 ? u * 64 : u * 4), sfv = kTmemSfv + u * (CH * 4);
+        const int use = i * (CH / 2) + (CH == 4 ? u : 0);  // of a V^T buffer
 #pragma unroll
-        for (int c0 = 0; c0 < CH; c0 += 2) {
-          const int use = i * (CH / 2) + c0 / 2;  // of either V^T buffer
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            // ---- V^T = I V^T of chunk c0 + c
-            good = good && (use == 0 || wait_for(&vt_empty[c], use - 1));
-            tmem_fence_after();
-            const uint32_t b = v + (c0 >> 1) * 64 + c * 4, sfv = kTmemSfv + (c0 + c) * 8;
-            mma_fp4<kEye, kRows, kDq>(kTmemVt + c * 128, eye, b, kTmemSfi, sfv, false);
-            mma_fp4<kEye, kRows, kDq>(kTmemVt + c * 128, eye + 2, b + 2, kTmemSfi, sfv + 4, true);
-            mma_commit<1>(&vt_full[c]);
-          }
-          if (c0 + 2 == CH) {
+        for (int k = 0; k < CH / 2; ++k) {
+          const int c = CH == 4 ? k : u;
+          good = good && (use == 0 || wait_for(&vt_empty[c], use - 1));
+          tmem_fence_after();
+          mma_fp4<kEye, kRows, kDq>(kTmemVt + c * 128, eye, v + k * 4, kTmemSfi, sfv + k * 8, false);
+          mma_fp4<kEye, kRows, kDq>(kTmemVt + c * 128, eye + 2, v + k * 4 + 2, kTmemSfi, sfv + k * 8 + 4, true);
+          mma_commit<1>(&vt_full[c]);
+          if (u == 1 && k == CH / 2 - 1) {
             mma_commit<1>(&empty[sv]);
             mma_commit<1>(dq_done);
           }
-          if (scores == i + 1 && scores < share_tiles && mbar_test(sfk_ready, (i + 1) & 1)) qk();
-          if (c0 == 0) good = good && wait_for(&p_full[i & 1], i >> 1);
+          mbar_arrive(&vt_full[c]);
+        }
+        if (u == 1) {
+          if (++sv == RINGS) sv = C::KVS ? 0 : C::NK;
+          if (++i == share_tiles) break;
+        }
+      }
+      // what was issued ends before its operands and results are used for something else
+      if (scores > 0) wait_for(&s_full[(scores - 1) % SB], (scores - 1) / SB);
+      if (i > 0) wait_for(&vt_full[1], i * (CH / 2) - 1);
+      if (!good) atomicOr(p.err, kErrTimeout);
+    }
+    __syncwarp();
+  } else if (warp == kSumWarp) {
+    // ---- the sums O^T += V^T P^T, a chunk of 128 dims after another
+    if (share_tiles > 0 && elect_one()) {
+      constexpr uint32_t kPv = (1u << 4) | (2u << 7) | (2u << 10) | (2u << 17) | (8u << 24);  // tf32 -> fp32, 128 x 16
+      constexpr uint32_t kP = desc_hi(0);  // (both 8-column groups of P are the same: the upper columns are not read)
+      const uint32_t p0 = (smem_u32(smem) + C::P_OFFSET) >> 4;
+      int i = 0;
+#pragma unroll 1
+      for (; i < share_tiles && good; ++i) {
+        if (!(good = wait_for(&p_full[i & 1], i >> 1))) break;
+        const uint32_t word = tile_of[i & 1], pa = p0 + (i & 1) * (C::P_BYTES >> 4);
+        const bool first = (word & kTileFirst) != 0;
+#pragma unroll 1
+        for (int c0 = 0; c0 < CH; c0 += 2) {
+          const int use = i * (CH / 2) + (c0 >> 1);  // of a V^T buffer
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            // ---- O^T += V^T P^T of chunk c0 + c
             good = good && wait_for(&vt_full[c], use);
             tmem_fence_after();
-#pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_tf32<kP, kPv>(kTmemO + (c0 + c) * 16, kTmemVt + c * 128 + q * 32 + k * 8, pa + q * 64 + k * 2,
-                                  !first || q > 0 || k > 0);
-            }
+            for (int q = 0; q < 16; ++q)
+              mma_tf32<kP, kPv>(kTmemO + (c0 + c) * 16, kTmemVt + c * 128 + q * 8, pa + (q >> 2) * 64 + (q & 3) * 2,
+                                !first || q > 0);
             mma_commit<1>(&vt_empty[c]);
           }
         }
@@ -822,14 +836,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
           mma_commit<1>(o_full);
           mbar_arrive(o_full);
         }
-        if (++sv == RINGS) sv = C::KVS ? 0 : C::NK;
-      }
-      // what was issued ends before its operands and results are used for something else
-      if (!good) {
-        if (scores > 0) wait_for(&s_full[(scores - 1) % SB], (scores - 1) / SB);
-        atomicOr(p.err, kErrTimeout);
       }
       if (i > 0) wait_for(&vt_empty[1], i * (CH / 2) - 1);
+      if (!good) atomicOr(p.err, kErrTimeout);
     }
     __syncwarp();
   } else {
@@ -901,6 +910,21 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
         const float* sum_of = reinterpret_cast<const float*>(smem + C::SUM_OFFSET) + (sg & 1) * 5 * C::CC;
         uint32_t* poison = poison_of + (sg & 3) * C::CC;
         const int slot = blockIdx.x * 2 + (seg.piece == 0 ? 1 : 0);
+        // 0: no attended token, so zeros, whatever the sums hold. (Times 2^v_exp last: over a sum of 2^80 it would be subnormal.)
+        float mul[C::CC];
+        uint32_t row[C::CC];  // of the output; invalid columns: none
+        {
+          Pair col(seg);
+#pragma unroll
+          for (int c = 0; c < C::CC; ++c, col.next(p)) {
+            const float l = (sum_of[c] + sum_of[C::CC + c]) + (sum_of[2 * C::CC + c] + sum_of[3 * C::CC + c]);
+            mul[c] = l != 0.f ? 1.f / l : 0.f;
+            row[c] = col.valid(p) ? (uint32_t)col.row(p, seg) : kNoRow;
+            if (seg.pieces > 1 && wt == c && col.valid(p))
+              p.lse_part[slot * C::CC + c] =
+                  l != 0.f ? (sum_of[4 * C::CC + c] + __log2f(l)) * 0.69314718055994530942f : -INFINITY;
+          }
+        }
         // lane l of quarter w has dim 32 w + l of each chunk
 #pragma unroll 1
         for (int k = 0; k < CH; ++k) {
@@ -908,22 +932,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
           tmem_ld(o, kTmemO + k * 16 + quarter);
           tmem_wait_ld();
           const int dim = k * 128 + we * 32 + lane;
-          Pair col(seg);
 #pragma unroll
-          for (int c = 0; c < C::CC; ++c, col.next(p)) {
-            const float l = (sum_of[c] + sum_of[C::CC + c]) + (sum_of[2 * C::CC + c] + sum_of[3 * C::CC + c]);
-            // (no attended token: zeros, whatever the sums hold)
-            float x = l != 0.f ? __uint_as_float(o[c]) * (p.v_mul / l) : 0.f;
+          for (int c = 0; c < C::CC; ++c) {
+            float x = mul[c] != 0.f ? __uint_as_float(o[c]) * mul[c] * p.v_mul : 0.f;
             if ((poison[c] >> (dim >> 4)) & 1u) x = NAN;
-            if (!col.valid(p)) continue;
-            if (seg.pieces == 1) {
-              reinterpret_cast<__nv_bfloat16*>(p.out)[col.row(p, seg) * C::D + dim] = __float2bfloat16_rn(x);
-            } else {
+            if (row[c] == kNoRow) continue;
+            if (seg.pieces == 1)
+              reinterpret_cast<__nv_bfloat16*>(p.out)[(size_t)row[c] * C::D + dim] = __float2bfloat16_rn(x);
+            else
               p.o_part[((size_t)slot * C::CC + c) * C::D + dim] = x;
-              if (k == 0 && wt == c)
-                p.lse_part[slot * C::CC + c] =
-                    l != 0.f ? (sum_of[4 * C::CC + c] + __log2f(l)) * 0.69314718055994530942f : -INFINITY;
-            }
           }
         }
         tmem_fence_before();
