@@ -36,7 +36,6 @@ struct Fp4Cfg {
   static constexpr int NV = KVS ? 0 : (D == 512 ? 3 : 6);
   static constexpr int RING_BYTES = (NK + NV) * ITEM_BYTES;
   static constexpr int CHUNKS = D / 128;   // of 128 dims: V is widened and summed a chunk at a time
-  static constexpr int S_BUFS = N <= 32 ? 2 : 1;  // score buffers in tensor memory
   static constexpr int Q_BYTES = N * D / 2;                       // a query's terms: codes like a tile's
   static constexpr int Q_OFFSET = RING_BYTES;                     // [2]: of this segment and the next
   static constexpr int P_BYTES = 8 * kFp4Tile * 4;                // P, tf32: [32 tokens][8 columns][128 B, swizzled]
@@ -45,15 +44,15 @@ struct Fp4Cfg {
   static constexpr int EYE_BYTES = 128 * 64;
   static constexpr int QSF_OFFSET = EYE_OFFSET + EYE_BYTES;       // query terms' scales [N][D / 16]
   static constexpr int COL_OFFSET = QSF_OFFSET + N * ROW_SF;      // float [2][CC]: score scale of a column
-  static constexpr int POISON_OFFSET = COL_OFFSET + 2 * CC * 4;   // u32 [4][CC]: 16-dim blocks that are NaN
-  static constexpr int TOP_OFFSET = POISON_OFFSET + 4 * CC * 4;   // float [4][CC]: the softmax warps' maxima
+  static constexpr int POISON_OFFSET = COL_OFFSET + 2 * CC * 4;   // u32 [16][CC]: 16-dim blocks that are NaN
+  static constexpr int TOP_OFFSET = POISON_OFFSET + 16 * CC * 4;  // float [4][CC]: the softmax warps' maxima
   static constexpr int SUM_OFFSET = TOP_OFFSET + 4 * CC * 4;      // float [2][5][CC]: their sums, and the references
   static constexpr int MISC_OFFSET = SUM_OFFSET + 2 * 5 * CC * 4; // u32: the join's ticket
-  static constexpr int BLOCKS_OFFSET = MISC_OFFSET + 8;           // u32 [4]: the 16-token blocks that tiles i .. i + 3 hold
-  static constexpr int TILE_OFFSET = BLOCKS_OFFSET + 16;          // u32 [2]: of P's tiles
+  static constexpr int BLOCKS_OFFSET = MISC_OFFSET + 4;           // u32: the 16-token blocks that the scores' tile holds
+  static constexpr int TILE_OFFSET = BLOCKS_OFFSET + 4;           // u32 [2]: of P's tiles
   static constexpr int VALID_OFFSET = TILE_OFFSET + 8;           // u32 [NK + NV]: what a slot's tile is (kTile...)
   static constexpr int BAR_OFFSET = (VALID_OFFSET + (NK + NV) * 4 + 7) / 8 * 8;
-  static constexpr int NUM_BARS = 2 * (NK + NV) + 15 + 9;
+  static constexpr int NUM_BARS = 3 * (NK + NV) + 19;
   static constexpr int SMEM_BYTES = BAR_OFFSET + NUM_BARS * 8 + 16 + 1024;  // (+ 1 KiB to start on a 1024-byte boundary)
   static constexpr int WARPS = 16;
   static constexpr int THREADS = 32 * WARPS;

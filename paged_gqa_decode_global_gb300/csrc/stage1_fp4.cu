@@ -50,15 +50,15 @@ namespace pd {
 namespace {
 
 constexpr float kRefRange = 60.f;  // log2 of how far a score may exceed its column's reference
-// Tensor memory columns: scores [S_BUFS][N], scales of V, of the unit matrix, V^T [2][128], sums [CHUNKS][16],
+// Tensor memory columns: scores [N], scales of V, of the unit matrix, V^T [2][128], sums [CHUNKS][16],
 // scales of K, of the query. All of it is allocated, so it begins at column 0.
 constexpr uint32_t kTmemS = 0, kTmemSfv = 64, kTmemSfi = 96, kTmemVt = 128, kTmemO = 384, kTmemSfk = 448,
                    kTmemSfq = 480, kTmemCols = 512;
 
 // Descriptors of shared-memory operands as two words, of which only the lower,
-// with the address, varies.
+// with the address, varies. (row_bytes 0: not swizzled, rows of 16 bytes.)
 __host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo, int row_bytes = 128) {
-  return (sbo >> 4) | 1u << 14 | (uint32_t)swizzle_code(row_bytes) << 29;
+  return (sbo >> 4) | 1u << 14 | (row_bytes ? (uint32_t)swizzle_code(row_bytes) << 29 : 0u);
 }
 
 // D[tmem] (+)= A . B over 64 dims, both e2m1 with an e4m3 scale per 16 dims.
@@ -69,6 +69,15 @@ __device__ __forceinline__ void mma_fp4(uint32_t d, uint32_t a, uint32_t b, uint
       "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], a, b, %8, [%3], [%4], p;\n\t}" ::"r"(d),
       "r"(a), "r"(b), "r"(sfa), "r"(sfb), "r"((uint32_t)accumulate), "n"(A_HI), "n"(B_HI), "n"(IDESC)
       : "memory");
+}
+
+// Scales of 128 rows and 64 dims (512 bytes: row l + 32 j's four at 16 l + 4 j) to
+// 4 columns of tensor memory, in every quarter of its lanes. Products issued by the
+// same thread afterwards see them.
+__device__ __forceinline__ void copy_scales(uint32_t to, uint32_t from) {
+  asm volatile("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\ttcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}" ::"r"(to),
+               "r"(from), "n"(desc_hi(128, 0))
+               : "memory");
 }
 
 // D[tmem] (+)= A[tmem] . B over 8 tokens, tf32.
@@ -128,6 +137,9 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t phase) {
 constexpr uint32_t kTileFirst = 0x100u, kTileLast = 0x200u, kTileOdd = 0x400u;  // of its segment; an odd one
 
 constexpr uint32_t kNoRow = 0xffffffffu;
+// Segments whose NaN marks are kept: a ring's tiles (up to 10) may be of as many,
+// and the marks are cleared up to 3 segments late.
+constexpr int kPoison = 16;
 
 // A request's attended range, cut to what its block table holds.
 struct Span {
@@ -278,13 +290,13 @@ __device__ __forceinline__ uint32_t code_offset(int row, int byte) {
 }
 
 // The query rows of a segment's columns as terms in shared memory (`q`) and their
-// scales (`sf`, `mul`), by 4 warps: one takes 256 dims of a row, a lane 8 of them,
+// scales (`sf`, `mul`), by `warps` warps: one takes 256 dims of a row, a lane 8 of them,
 // two lanes a block of 16.
 template <class C>
 __device__ __forceinline__ void write_query_terms(const Fp4Params& p, const Segment& s, uint8_t* q, uint8_t* sf, float* mul,
-                                                  int warp, int lane) {
+                                                  int warp, int warps, int lane) {
 #pragma unroll 1
-  for (int item = warp; item < C::CC * C::SL; item += 4) {
+  for (int item = warp; item < C::CC * C::SL; item += warps) {
     const int col = item / C::SL, part = item % C::SL;
     const int pair = s.head + col;
     int j = 0, r = pair;
@@ -370,36 +382,36 @@ template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_constant__ Fp4Params p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  constexpr int SB = C::S_BUFS, CH = C::CHUNKS, RINGS = C::NK + C::NV;
+  constexpr int CH = C::CHUNKS, RINGS = C::NK + C::NV;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFFSET);  // [RINGS]: K's ring, then V's
   uint64_t* empty = full + RINGS;                                      // [RINGS]
+  // four arrivals, one a warp: the slot's scales are where tcgen05.cp takes them from
+  uint64_t* ready = empty + RINGS;      // [RINGS]
   // one arrival: the products' commits
-  uint64_t* vt_empty = empty + RINGS;   // [2] a chunk of V^T used
+  uint64_t* vt_empty = ready + RINGS;   // [2] a chunk of V^T used
   uint64_t* p_empty = vt_empty + 2;     // [2] P used: the tile is in the sums
-  uint64_t* dq_done = p_empty + 2;      // a tile's V^T all there
-  uint64_t* qk_done = dq_done + 1;      // a segment's scores all computed
+  uint64_t* qk_done = p_empty + 2;      // a segment's scores all computed
   // two: a commit, and an arrival of the same lane (which orders what it has seen of others)
   uint64_t* vt_full = qk_done + 1;      // [2] a chunk of V^T there
-  uint64_t* s_full = vt_full + 2;       // [2] scores computed
-  uint64_t* o_full = s_full + 2;        // a segment's sums complete
+  uint64_t* s_full = vt_full + 2;       // scores computed
+  uint64_t* o_full = s_full + 1;        // a segment's sums complete
   // four warps
-  uint64_t* sfk_ready = o_full + 1;     // K's scales in tensor memory
-  uint64_t* sfv_ready = sfk_ready + 1;  // V's
-  uint64_t* s_empty = sfv_ready + 1;    // [2] scores read
-  uint64_t* p_full = s_empty + 2;       // [2]
+  uint64_t* s_empty = o_full + 1;       // scores read
+  uint64_t* p_full = s_empty + 1;       // [2]
   uint64_t* q_full = p_full + 2;        // [2] a segment's query terms there
   uint64_t* o_empty = q_full + 2;       // a segment's sums read
   uint64_t* l_full = o_empty + 1;       // [2] a segment's probabilities' sums there
   uint64_t* l_empty = l_full + 2;       // [2] and read
-  static_assert(C::NUM_BARS == 2 * RINGS + 6 + 5 + 13, "as listed");
+  static_assert(C::NUM_BARS == 3 * RINGS + 5 + 4 + 10, "as listed");
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(full + C::NUM_BARS);
   volatile uint32_t* valid = reinterpret_cast<uint32_t*>(smem + C::VALID_OFFSET);  // [RINGS]
   volatile uint32_t* tile_of = reinterpret_cast<uint32_t*>(smem + C::TILE_OFFSET);      // [2] first, last: by P buffer
-  volatile uint32_t* blocks_of = reinterpret_cast<uint32_t*>(smem + C::BLOCKS_OFFSET);  // [4] by tile
+  volatile uint32_t* blocks_of = reinterpret_cast<uint32_t*>(smem + C::BLOCKS_OFFSET);  // of the scores' tile
   constexpr int kSfWarp = 4, kCodeWarp = 8, kScaleWarp = 9, kMmaWarp = 10, kSumWarp = 11, kEndWarp = 12;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool copies = warp == kCodeWarp || warp == kScaleWarp;
   const bool early = p.early_kv != 0 && copies;
+  uint32_t* poison_of = reinterpret_cast<uint32_t*>(smem + C::POISON_OFFSET);  // [kPoison][CC], by segment
 
   if (warp == kCodeWarp) {
     if (lane == 0) {
@@ -407,9 +419,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
       if (!C::KVS) prefetch_tensormap(&p.vmap);
     }
     for (int i = lane; i < C::NUM_BARS; i += 32) {
-      const int r = i - 2 * RINGS;
+      const int r = i - 3 * RINGS;
       // full: the codes' byte count and every lane's scales; empty: the products that read the slot
-      mbar_init(&full[i], i < RINGS ? 33 : r < 0 ? (C::KVS ? 2 : 1) : r < 6 ? 1 : r < 11 ? 2 : 4);
+      mbar_init(&full[i], i < RINGS ? 33 : i < 2 * RINGS ? (C::KVS ? 2 : 1) : r < 0 ? 4 : r < 5 ? 1 : r < 9 ? 2 : 4);
     }
     fence_barrier_init();
     __syncwarp();
@@ -418,6 +430,34 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
   if (copies) {
     named_bar_sync(5, 2 * 32);
     named_bar_arrive(4, C::THREADS);
+  }
+  // what depends on nothing
+  if (warp >= kEndWarp) {
+    const int wt = tid - kEndWarp * 32;
+    // the unit matrix in e2m1 (1.0 is 2): 16 bytes of row m hold dims 32 c .., the one lies at dim m
+#pragma unroll 1
+    for (int i = wt; i < C::EYE_BYTES / 16; i += 128) {
+      const int m = i >> 2, c = (i & 3) ^ ((m >> 1) & 3), word = (m >> 3) & 3;
+      const uint32_t one = (m >> 5) == c ? 2u << (4 * (m & 7)) : 0u;
+      *reinterpret_cast<uint4*>(smem + C::EYE_OFFSET + (m >> 3) * 512 + (m & 7) * 64 + (i & 3) * 16) =
+          make_uint4(word == 0 ? one : 0u, word == 1 ? one : 0u, word == 2 ? one : 0u, word == 3 ? one : 0u);
+    }
+    // the query rows beyond the terms, and the marks
+    constexpr int USED = C::CC * kFp4Terms, REST = (C::N - USED) * (C::D / 32);  // 16-byte pieces of a buffer
+#pragma unroll 1
+    for (int i = wt; i < 2 * REST; i += 128) {
+      const int r = i < REST ? i : i - REST;
+      *reinterpret_cast<uint4*>(smem + C::Q_OFFSET + (i < REST ? 0 : C::Q_BYTES) +
+                                code_offset<C>(USED + r / (C::D / 32), (r % (C::D / 32)) * 16)) = make_uint4(0u, 0u, 0u, 0u);
+      if (i < (C::N - USED) * C::ROW_SF / 16)
+        *reinterpret_cast<uint4*>(smem + C::QSF_OFFSET + USED * C::ROW_SF + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    for (int i = wt; i < kPoison * C::CC; i += 128) poison_of[i] = 0u;
+  } else if (warp < kSfWarp && C::CC < 8) {  // P's unused columns
+    for (int k = 0; k < 2; ++k)
+      for (int i = lane; i < (8 - C::CC) * 8; i += 32)
+        *reinterpret_cast<uint4*>(smem + C::P_OFFSET + k * C::P_BYTES + warp * 1024 + C::CC * 128 + i * 16) =
+            make_uint4(0u, 0u, 0u, 0u);
   }
   if (!early) {
     grid_dependency_wait();
@@ -431,6 +471,24 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     // the barriers and tensor memory are there (the copies do not wait for the other warps)
     named_bar_sync(4, C::THREADS);
     tmem_fence_after();
+  }
+  // the first segment's query terms, by all who have nothing to do yet
+  Segment next;
+  bool any = false;
+  if (!copies && warp != kMmaWarp && warp != kSumWarp) {
+    Walk begin = walk;
+    if (walk_next<C::CC>(p, begin, next)) {
+      any = true;
+      write_query_terms<C>(p, next, smem + C::Q_OFFSET, smem + C::QSF_OFFSET, reinterpret_cast<float*>(smem + C::COL_OFFSET),
+                           warp < kCodeWarp ? warp : warp - 4, 12, lane);
+      fence_proxy_async_smem();
+    }
+    if (warp >= kEndWarp) {
+      walk = begin;
+      named_bar_sync(7, 12 * 32);
+    } else {
+      named_bar_arrive(7, 12 * 32);
+    }
   }
   const uint32_t quarter = (uint32_t)(warp & 3) << 21;  // this warp's lanes of tensor memory
 
@@ -453,8 +511,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     uint32_t err_bits = 0;
     const uint64_t policy = l2_evict_first_policy();
     const bool codes = warp == kCodeWarp;  // (the other warp: the scales)
-    Segment next;
-    bool any = walk_next<C::CC>(p, walk, next);
+    any = walk_next<C::CC>(p, walk, next);
     auto page_of = [&](const Segment& s, int i) {
       const int t = s.t_base + i * kFp4Tile + lane * 16;
       return t < s.thi ? __ldg(p.block_tables + (size_t)s.b * p.max_pages + t / p.page_size) : -1;
@@ -478,7 +535,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
         }
         const int row0 = __shfl_sync(kFullMask, rows, (i & 3) * 8 + (lane & 7));
         const uint32_t bits = __ballot_sync(kFullMask, row0 >= 0) & 0xffu;
-        const uint32_t word = bits | odd | (i + 1 == seg.tiles ? kTileLast : 0u);
+        const uint32_t word = bits | odd | (i == 0 ? kTileFirst : 0u) | (i + 1 == seg.tiles ? kTileLast : 0u);
         // rows of the newest tokens may still be written by the kernel in front
         if (!waited && (it >= C::NK || (!C::KVS && it >= C::NV) ||
                         seg.t_base + (i + 1) * kFp4Tile > seg.L - p.query_tokens)) {
@@ -541,12 +598,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
   } else if (warp < kSfWarp) {
     // ---- softmax: rows 32 warp .. + 31 of every tile
     const uint32_t p_at = smem_u32(smem + C::P_OFFSET) + warp * 1024 + (lane & 3) * 4;
-    if (C::CC < 8) {  // P's unused columns
-      for (int k = 0; k < 2; ++k)
-        for (int i = lane; i < (8 - C::CC) * 8; i += 32)
-          *reinterpret_cast<uint4*>(smem + C::P_OFFSET + k * C::P_BYTES + warp * 1024 + C::CC * 128 + i * 16) =
-              make_uint4(0u, 0u, 0u, 0u);
-    }
     float* top_of = reinterpret_cast<float*>(smem + C::TOP_OFFSET);  // [4][CC]
     int it = 0;
 #pragma unroll 1
@@ -569,14 +620,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
       }
 #pragma unroll 1
       for (int i = 0; i < seg.tiles; ++i, ++it) {
-        const int sbuf = it % SB, buf = it & 1;
-        await(&s_full[sbuf], it / SB);
+        const int buf = it & 1;
+        await(s_full, it);
         tmem_fence_after();
         float s[C::CC];
         {
           uint32_t w[kFp4Terms * C::CC / 8][8];
 #pragma unroll
-          for (int k = 0; k < kFp4Terms * C::CC / 8; ++k) tmem_ld(w[k], kTmemS + sbuf * C::N + quarter + k * 8);
+          for (int k = 0; k < kFp4Terms * C::CC / 8; ++k) tmem_ld(w[k], kTmemS + quarter + k * 8);
           tmem_wait_ld();
 #pragma unroll
           for (int c = 0; c < C::CC; ++c) {
@@ -587,10 +638,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
           }
         }
         const int row = warp * 32 + lane, t = seg.t_base + i * kFp4Tile + row;
-        const bool ok = (blocks_of[it & 3] >> (row >> 4)) & 1u;
+        const bool ok = (*blocks_of >> (row >> 4)) & 1u;
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s_empty[sbuf]);
+        if (lane == 0) mbar_arrive(s_empty);
         bool above = false;
 #pragma unroll
         for (int c = 0; c < C::CC; ++c) {
@@ -665,143 +716,151 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
       if (lane == 0) mbar_arrive(&l_full[sg & 1]);
     }
   } else if (warp < kCodeWarp) {
-    // ---- scales into tensor memory: lane l, column 4 k + j holds the 4 scales of row l + 32 j, dims 64 k ..;
-    // every quarter of the lanes all rows'. K's, once the product before has read
-    // the last tile's, then V's likewise.
-    uint32_t* poison_of = reinterpret_cast<uint32_t*>(smem + C::POISON_OFFSET);
+    // ---- a tile's scales put where tcgen05.cp takes them from, in place: from a row's
+    // behind each other to 64 dims' of all rows behind each other. A lane has a row.
+    const int j = warp - kSfWarp, row = j * 32 + lane;
     int it = 0;
 #pragma unroll 1
     for (int sg = 0; walk_next<C::CC>(p, walk, seg); ++sg) {
 #pragma unroll 1
-      for (int u = 0; u < 2 * seg.tiles; ++u) {
-        const bool v = (u & 1) != 0;
+      for (int u = 0; u < (C::KVS ? 1 : 2) * seg.tiles; ++u) {
+        const bool v = C::KVS || (u & 1) != 0;
         const int n = v && !C::KVS ? C::NV : C::NK, round = it / n, st = (v && !C::KVS ? C::NK : 0) + it - round * n;
         await(&full[st], round);
-        const uint32_t here = valid[st] & 0xffu;
-        const int t0 = seg.t_base + (u >> 1) * kFp4Tile;
-        if (!v && warp == kSfWarp && lane == 0) blocks_of[it & 3] = here;
-        // V's rows that do not count have scale 0: their probabilities are 0, but 0 * NaN is NaN
-        uint32_t count = 15u;
-        if (v && !(here == 0xffu && t0 >= seg.tlo && t0 + kFp4Tile <= seg.thi)) {
-          count = 0u;
+        uint8_t* sf = smem + st * C::ITEM_BYTES + C::CODE_BYTES;
+        uint32_t x[C::KSTEPS];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int row = lane + 32 * j, t = t0 + row;
-            if (((here >> (row >> 4)) & 1u) && t >= seg.tlo && t < seg.thi) count |= 1u << j;
-          }
+        for (int k = 0; k < C::KSTEPS; k += 4) {
+          const uint4 w = *reinterpret_cast<const uint4*>(sf + row * C::ROW_SF + k * 4);
+          x[k] = w.x;
+          x[k + 1] = w.y;
+          x[k + 2] = w.z;
+          x[k + 3] = w.w;
         }
-        const uint8_t* sf = smem + st * C::ITEM_BYTES + C::CODE_BYTES + lane * C::ROW_SF;
-        uint32_t x[C::KSTEPS / 4][16], bad = 0;  // [256 dims][64 dims][row group]
+        if (v) {
+          // rows that do not count have scale 0: their probabilities are 0, but 0 * NaN is NaN
+          const int t = seg.t_base + (C::KVS ? u : u >> 1) * kFp4Tile + row;
+          const bool counts = ((valid[st] >> (row >> 4)) & 1u) && t >= seg.tlo && t < seg.thi;
+          uint32_t bad = 0u;
 #pragma unroll
-        for (int k = 0; k < C::KSTEPS / 4; ++k)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint4 w = *reinterpret_cast<const uint4*>(sf + 32 * j * C::ROW_SF + k * 16);
-            if (!((count >> j) & 1u)) w = make_uint4(0u, 0u, 0u, 0u);
-            x[k][j] = w.x;
-            x[k][4 + j] = w.y;
-            x[k][8 + j] = w.z;
-            x[k][12 + j] = w.w;
-            bad |= nan_scales(w.x) | nan_scales(w.y) | nan_scales(w.z) | nan_scales(w.w);
+          for (int k = 0; k < C::KSTEPS; ++k) {
+            if (!counts) x[k] = 0u;
+            bad |= nan_scales(x[k]);
           }
-        if (v && __any_sync(kFullMask, bad != 0u)) {
-          // A NaN block would spread over the unit matrix's zeros to other dims
-          // (and, of a token that only some of several query tokens attend, to the
-          // others): it is taken out and marked for the results it belongs to.
+          if (bad != 0u) {
+            // A NaN block would spread over the unit matrix's zeros to other dims (and, of
+            // a token that only some of several query tokens attend, to the others): it is
+            // taken out and marked for the results it belongs to: its dims' or, as K's
+            // too, all.
+            uint32_t blocks = 0u;
 #pragma unroll
-          for (int k = 0; k < C::KSTEPS * 4; ++k) x[k >> 4][k & 15] &= ~((nan_scales(x[k >> 4][k & 15]) >> 7) * 0xffu);
-          if (warp == kSfWarp) {
-#pragma unroll 1
-            for (int e = 0; e < 4 * C::ROW_SF; ++e) {  // [row group][16 dims]
-              const int j = e / C::ROW_SF, y = e % C::ROW_SF, t = t0 + lane + 32 * j;
-              if (!((count >> j) & 1u) || (sf[32 * j * C::ROW_SF + y] & 0x7f) != 0x7f) continue;
-              Pair col(seg);
-#pragma unroll 1
-              for (int c = 0; c < C::CC && col.valid(p); ++c, col.next(p)) {
-                const int end = col.end(p, seg);
-                if (t < end && (p.window == 0 || t >= end - p.window)) atomicOr(&poison_of[(sg & 3) * C::CC + c], 1u << y);
-              }
+            for (int k = 0; k < C::KSTEPS; ++k) {
+              const uint32_t nan = nan_scales(x[k]) >> 7;
+              blocks |= ((nan * 0x10204080u) >> 28) << (4 * k);
+              x[k] &= ~(nan * 0xffu);
             }
-            __syncwarp();
+            Pair col(seg);
+#pragma unroll 1
+            for (int c = 0; c < C::CC && col.valid(p); ++c, col.next(p)) {
+              const int end = col.end(p, seg);
+              if (t < end && (p.window == 0 || t >= end - p.window))
+                atomicOr(&poison_of[(sg % kPoison) * C::CC + c], C::KVS ? 0xffffffffu : blocks);
+            }
           }
         }
-        // the product that reads the tile before's is done; what the scores' product
-        // needs besides: a free buffer, and the segment's query terms
-        if (it > 0) await(v ? dq_done : &s_full[(it - 1) % SB], v ? it - 1 : (it - 1) / SB);
-        if (!v) {
-          if (it >= SB) await(&s_empty[it % SB], it / SB - 1);
-          if (u == 0) await(&q_full[sg & 1], sg >> 1);
-        }
-        tmem_fence_after();
+        named_bar_sync(6, 128);  // all are read
 #pragma unroll
-        for (int k = 0; k < C::KSTEPS / 4; ++k) tmem_st((v ? kTmemSfv : kTmemSfk) + quarter + k * 16, x[k]);
-        tmem_wait_st();
-        tmem_fence_before();
+        for (int k = 0; k < C::KSTEPS; ++k) *reinterpret_cast<uint32_t*>(sf + k * 512 + lane * 16 + j * 4) = x[k];
+        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(v ? sfv_ready : sfk_ready);
+        if (lane == 0) mbar_arrive(&ready[st]);
         it += v;
       }
     }
   } else if (warp == kMmaWarp) {
-    // ---- the scores and V^T, by one lane, which looks at barriers (~50 cycles a
-    // look) as seldom as can be: whoever else can has waited on its behalf. The
-    // tensor core holds little of what is issued ahead, so the sums are another
-    // warp's, whose looks fall elsewhere.
+    // ---- the scores and V^T, by one lane, whichever can go on. The tensor core holds
+    // little of what is issued ahead, so the sums are another warp's.
     if (share_tiles > 0 && elect_one()) {
       constexpr uint32_t kQk = (1u << 7) | (1u << 10) | ((uint32_t)(C::N / 8) << 17) | (8u << 24);  // e2m1, e4m3 scales
       constexpr uint32_t kDq = (1u << 7) | (1u << 10) | ((uint32_t)(kFp4Tile / 8) << 17) | (8u << 24);
       constexpr uint32_t kRows = desc_hi(C::SL * 1024), kEye = desc_hi(512, 64);
-      constexpr int kItem = C::ITEM_BYTES >> 4;
+      constexpr int kItem = C::ITEM_BYTES >> 4, kScales = C::CODE_BYTES >> 4;
       // descriptors' lower words: 16-byte units, a step further is a constant added
       const uint32_t ring = smem_u32(smem) >> 4, q0 = ring + (C::Q_OFFSET >> 4), eye = ring + (C::EYE_OFFSET >> 4);
-      int scores = 0, sk = 0, sv = C::KVS ? 0 : C::NK, i = 0;  // tiles whose scores are out; ring slots
+      int scores = 0, sk = 0, k_round = 0, sg = 0;                // tiles whose scores are out; its slot
+      int chunk = 0, i = 0, sv = C::KVS ? 0 : C::NK, v_round = 0;  // the next chunk of V^T, of tile i
+      bool k_ok = false, v_ok = false;
+      uint32_t word = 0;  // of the scores' tile
+      int idle = 0;
+      unsigned long long start = 0;
       good = *tmem_at == 0;
 #pragma unroll 1
-      for (int u = 0; good; u ^= 1) {
-        // u 0: a tile begins; 1: half of its chunks are out
-        if (scores == i ? u == 0 : scores < share_tiles && mbar_test(sfk_ready, scores & 1)) {
-          // ---- S = K q^T, of this tile at the latest and of the next as soon as it can be
-          if (!(good = wait_for(sfk_ready, scores))) break;
-          tmem_fence_after();
-          const uint32_t word = valid[sk], buf = scores % SB;
-          const uint32_t a = ring + sk * kItem, q = q0 + ((word & kTileOdd) ? C::Q_BYTES >> 4 : 0);
-#pragma unroll
-          for (int k = 0; k < C::KSTEPS; ++k)
-            mma_fp4<kRows, kRows, kQk>(kTmemS + buf * C::N, a + (k >> 2) * 64 + (k & 3) * 2,
-                                       q + (k >> 2) * 64 + (k & 3) * 2, kTmemSfk + k * 4, kTmemSfq + k * 4, k > 0);
-          mma_commit<1>(&s_full[buf]);
-          mma_commit<1>(&empty[sk]);
-          if (word & kTileLast) mma_commit<1>(qk_done);
-          mbar_arrive(&s_full[buf]);
-          ++scores;
-          if (++sk == C::NK) sk = 0;
-        }
-        if (u == 0 && !(good = wait_for(sfv_ready, i))) break;
-        // ---- V^T = I V^T, two chunks of 128 dims (d 256: one)
-        const uint32_t v = ring + sv * kItem + (CH == 4 ? u * 64 : u * 4), sfv = kTmemSfv + u * (CH * 4);
-        const int use = i * (CH / 2) + (CH == 4 ? u : 0);  // of a V^T buffer
-#pragma unroll
-        for (int k = 0; k < CH / 2; ++k) {
-          const int c = CH == 4 ? k : u;
-          good = good && (use == 0 || wait_for(&vt_empty[c], use - 1));
-          tmem_fence_after();
-          mma_fp4<kEye, kRows, kDq>(kTmemVt + c * 128, eye, v + k * 4, kTmemSfi, sfv + k * 8, false);
-          mma_fp4<kEye, kRows, kDq>(kTmemVt + c * 128, eye + 2, v + k * 4 + 2, kTmemSfi, sfv + k * 8 + 4, true);
-          mma_commit<1>(&vt_full[c]);
-          if (u == 1 && k == CH / 2 - 1) {
-            mma_commit<1>(&empty[sv]);
-            mma_commit<1>(dq_done);
+      while (good && (i < share_tiles || scores < share_tiles)) {
+        bool on = false;
+        if (scores < share_tiles) {
+          // ---- S = K q^T, over the scores before once they are read (so their product has read K's scales)
+          // (the first of a segment: once its query terms are there, which may wait for V^T of a segment before)
+          if (!k_ok && mbar_test(&ready[sk], k_round & 1)) {
+            word = valid[sk];
+            k_ok = !(word & kTileFirst) || mbar_test(&q_full[sg & 1], (sg >> 1) & 1);
           }
-          mbar_arrive(&vt_full[c]);
+          if (k_ok && (scores == 0 || mbar_test(s_empty, (scores - 1) & 1))) {
+            if (word & kTileFirst) ++sg;
+            tmem_fence_after();
+            const uint32_t a = ring + sk * kItem, q = q0 + ((word & kTileOdd) ? C::Q_BYTES >> 4 : 0);
+#pragma unroll
+            for (int k = 0; k < C::KSTEPS; ++k) copy_scales(kTmemSfk + k * 4, a + kScales + k * 32);
+#pragma unroll
+            for (int k = 0; k < C::KSTEPS; ++k)
+              mma_fp4<kRows, kRows, kQk>(kTmemS, a + (k >> 2) * 64 + (k & 3) * 2, q + (k >> 2) * 64 + (k & 3) * 2,
+                                         kTmemSfk + k * 4, kTmemSfq + k * 4, k > 0);
+            *blocks_of = word & 0xffu;
+            mma_commit<1>(s_full);
+            mma_commit<1>(&empty[sk]);
+            if (word & kTileLast) mma_commit<1>(qk_done);
+            mbar_arrive(s_full);
+            ++scores;
+            if (++sk == C::NK) sk = 0, ++k_round;
+            k_ok = false;
+            on = true;
+          }
         }
-        if (u == 1) {
-          if (++sv == RINGS) sv = C::KVS ? 0 : C::NK;
-          if (++i == share_tiles) break;
+        if (!v_ok && i < share_tiles) v_ok = C::KVS ? scores > i : mbar_test(&ready[sv], v_round & 1);
+        if (v_ok) {
+          // ---- a chunk V^T = I V^T, 128 dims. (What its scales lie over was read: the chunk before in its buffer is used.)
+          const int at = i * CH + chunk, c = at & 1;
+          if (at < 2 || mbar_test(&vt_empty[c], ((at >> 1) - 1) & 1)) {
+            tmem_fence_after();
+            const uint32_t item = ring + sv * kItem, v = item + (chunk >> 1) * 64 + (chunk & 1) * 4;
+            const uint32_t sfv = kTmemSfv + chunk * 8;
+            copy_scales(sfv, item + kScales + chunk * 64);
+            copy_scales(sfv + 4, item + kScales + chunk * 64 + 32);
+            mma_fp4<kEye, kRows, kDq>(kTmemVt + c * 128, eye, v, kTmemSfi, sfv, false);
+            mma_fp4<kEye, kRows, kDq>(kTmemVt + c * 128, eye + 2, v + 2, kTmemSfi, sfv + 4, true);
+            mma_commit<1>(&vt_full[c]);
+            if (++chunk == CH) mma_commit<1>(&empty[sv]);
+            mbar_arrive(&vt_full[c]);
+            if (chunk == CH) {
+              chunk = 0;
+              ++i;
+              if (++sv == RINGS) sv = C::KVS ? 0 : C::NK, ++v_round;
+              v_ok = false;
+            }
+            on = true;
+          }
+        }
+        if (on) {
+          idle = 0;
+        } else if ((++idle & 255) == 0) {
+          const unsigned long long now = global_timer_ns();
+          if (idle == 256) start = now;
+          else if (now - start > kWaitTimeoutNs) good = false;
         }
       }
       // what was issued ends before its operands and results are used for something else
-      if (scores > 0) wait_for(&s_full[(scores - 1) % SB], (scores - 1) / SB);
-      if (i > 0) wait_for(&vt_full[1], i * (CH / 2) - 1);
+      if (scores > 0) wait_for(s_full, scores - 1);
+      const int last = i * CH + chunk - 1;
+      if (last >= 0) wait_for(&vt_full[last & 1], last >> 1);
       if (!good) atomicOr(p.err, kErrTimeout);
     }
     __syncwarp();
@@ -844,46 +903,26 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
   } else {
     // ---- the next segment's query terms, and a segment's results
     const int we = warp - kEndWarp, wt = tid - kEndWarp * 32;
-    uint32_t* poison_of = reinterpret_cast<uint32_t*>(smem + C::POISON_OFFSET);
     volatile uint32_t* ticket = reinterpret_cast<uint32_t*>(smem + C::MISC_OFFSET);
-    // the unit matrix in e2m1 (1.0 is 2): 16 bytes of row m hold dims 32 c .., the one lies at dim m
-#pragma unroll 1
-    for (int i = wt; i < C::EYE_BYTES / 16; i += 128) {
-      const int m = i >> 2, c = (i & 3) ^ ((m >> 1) & 3), word = (m >> 3) & 3;
-      const uint32_t one = (m >> 5) == c ? 2u << (4 * (m & 7)) : 0u;
-      *reinterpret_cast<uint4*>(smem + C::EYE_OFFSET + (m >> 3) * 512 + (m & 7) * 64 + (i & 3) * 16) =
-          make_uint4(word == 0 ? one : 0u, word == 1 ? one : 0u, word == 2 ? one : 0u, word == 3 ? one : 0u);
-    }
-    // the query rows beyond the terms, and the marks
-    constexpr int USED = C::CC * kFp4Terms, REST = (C::N - USED) * (C::D / 32);  // 16-byte pieces of a buffer
-#pragma unroll 1
-    for (int i = wt; i < 2 * REST; i += 128) {
-      const int r = i < REST ? i : i - REST;
-      *reinterpret_cast<uint4*>(smem + C::Q_OFFSET + (i < REST ? 0 : C::Q_BYTES) +
-                                code_offset<C>(USED + r / (C::D / 32), (r % (C::D / 32)) * 16)) = make_uint4(0u, 0u, 0u, 0u);
-      if (i < (C::N - USED) * C::ROW_SF / 16)
-        *reinterpret_cast<uint4*>(smem + C::QSF_OFFSET + USED * C::ROW_SF + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-    }
-    for (int i = wt; i < 4 * C::CC; i += 128) poison_of[i] = 0u;
     {
       uint32_t one[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) one[k] = 0x38383838u;  // e4m3 1.0
       tmem_st(kTmemSfi + quarter, one);
     }
-    Segment next;
-    bool any = walk_next<C::CC>(p, walk, next);
 #pragma unroll 1
     for (int sg = -1; sg < 0 ? any : true; ++sg) {
       if (any) {
         // ---- segment sg + 1's terms (their buffer is free: the scores of segment sg - 1 are computed, as these warps
         // have seen), and their scales once segment sg's scores are computed
-        named_bar_sync(3, 128);  // the scales before are in tensor memory
-        write_query_terms<C>(p, next, smem + C::Q_OFFSET + ((sg + 1) & 1) * C::Q_BYTES, smem + C::QSF_OFFSET,
-                             reinterpret_cast<float*>(smem + C::COL_OFFSET) + ((sg + 1) & 1) * C::CC, we, lane);
-        fence_proxy_async_smem();
-        named_bar_sync(3, 128);
-        if (sg >= 0) await(qk_done, sg);
+        if (sg >= 0) {
+          named_bar_sync(3, 128);  // the scales before are in tensor memory
+          write_query_terms<C>(p, next, smem + C::Q_OFFSET + ((sg + 1) & 1) * C::Q_BYTES, smem + C::QSF_OFFSET,
+                               reinterpret_cast<float*>(smem + C::COL_OFFSET) + ((sg + 1) & 1) * C::CC, we, 4, lane);
+          fence_proxy_async_smem();
+          named_bar_sync(3, 128);
+          await(qk_done, sg);
+        }
         tmem_fence_after();
 #pragma unroll 1
         for (int k0 = 0; k0 < C::KSTEPS; k0 += 2) {
@@ -908,7 +947,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
         await(o_full, sg);
         tmem_fence_after();
         const float* sum_of = reinterpret_cast<const float*>(smem + C::SUM_OFFSET) + (sg & 1) * 5 * C::CC;
-        uint32_t* poison = poison_of + (sg & 3) * C::CC;
+        uint32_t* poison = poison_of + (sg % kPoison) * C::CC;
         const int slot = blockIdx.x * 2 + (seg.piece == 0 ? 1 : 0);
         // 0: no attended token, so zeros, whatever the sums hold. (Times 2^v_exp last: over a sum of 2^80 it would be subnormal.)
         float mul[C::CC];
