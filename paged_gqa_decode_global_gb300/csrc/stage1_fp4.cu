@@ -32,10 +32,11 @@
 // first tile that holds a token it attends, and stays until a score exceeds it
 // by 2^60 (tf32 has fp32's exponents), which rescales the sums.
 //
-// Roles: warps 0-3 softmax (a lane a token); 4-7 write the tiles' scales to tensor
-// memory; 8 copies codes (TMA), 9 scales (cp.async); 10 issues the scores and V^T,
-// 11 the sums;
-// 12-15 write the next unit's query terms, read a unit's sums and join pieces.
+// Roles: warps 0-3 softmax (a lane a token); 4-7 put a tile's scales in tcgen05.cp's
+// order; 8 copies; one lane each of 9 issues the scores, of 10 V^T, of 11 the sums
+// (a look at a barrier takes ~150 cycles, and one lane that does all three spends
+// most of them looking); 12-15 write the next unit's query terms, read a unit's sums
+// and join pieces.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -117,8 +118,9 @@ __device__ __forceinline__ uint32_t nan_scales(uint32_t w) { return ((w & 0x7f7f
 // A wait of up to kWaitTimeoutNs. The hardware suspends the thread for up to the
 // time asked for, so that a long wait takes no issue slots. One copy for all.
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity) {
-  const unsigned long long start = global_timer_ns();
-  do {
+  unsigned long long start = 0;
+#pragma unroll 1
+  for (int n = 0;; ++n) {
     uint32_t done;
     asm volatile(
         "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
@@ -126,8 +128,10 @@ __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity) {
         : "r"(bar), "r"(parity), "r"(1000000u)
         : "memory");
     if (done) return true;
-  } while (global_timer_ns() - start < kWaitTimeoutNs);
-  return false;
+    const unsigned long long now = global_timer_ns();
+    if (n == 0) start = now;
+    if (now - start > kWaitTimeoutNs) return false;
+  }
 }
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t phase) {
   return mbar_test(bar, phase & 1) || wait_long(smem_u32(bar), phase & 1);
@@ -407,13 +411,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
   volatile uint32_t* valid = reinterpret_cast<uint32_t*>(smem + C::VALID_OFFSET);  // [RINGS]
   volatile uint32_t* tile_of = reinterpret_cast<uint32_t*>(smem + C::TILE_OFFSET);      // [2] first, last: by P buffer
   volatile uint32_t* blocks_of = reinterpret_cast<uint32_t*>(smem + C::BLOCKS_OFFSET);  // of the scores' tile
-  constexpr int kSfWarp = 4, kCodeWarp = 8, kScaleWarp = 9, kMmaWarp = 10, kSumWarp = 11, kEndWarp = 12;
+  constexpr int kSfWarp = 4, kCopyWarp = 8, kScoreWarp = 9, kWideWarp = 10, kSumWarp = 11, kEndWarp = 12;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const bool copies = warp == kCodeWarp || warp == kScaleWarp;
+  const bool copies = warp == kCopyWarp;
   const bool early = p.early_kv != 0 && copies;
   uint32_t* poison_of = reinterpret_cast<uint32_t*>(smem + C::POISON_OFFSET);  // [kPoison][CC], by segment
 
-  if (warp == kCodeWarp) {
+  if (copies) {
     if (lane == 0) {
       prefetch_tensormap(&p.kmap);
       if (!C::KVS) prefetch_tensormap(&p.vmap);
@@ -426,11 +430,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     fence_barrier_init();
     __syncwarp();
   }
-  if (warp == kMmaWarp) tmem_alloc<1>(tmem_at, kTmemCols);
-  if (copies) {
-    named_bar_sync(5, 2 * 32);
-    named_bar_arrive(4, C::THREADS);
-  }
+  if (warp == kScoreWarp) tmem_alloc<1>(tmem_at, kTmemCols);
+  if (copies) named_bar_arrive(4, C::THREADS);
   // what depends on nothing
   if (warp >= kEndWarp) {
     const int wt = tid - kEndWarp * 32;
@@ -475,12 +476,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
   // the first segment's query terms, by all who have nothing to do yet
   Segment next;
   bool any = false;
-  if (!copies && warp != kMmaWarp && warp != kSumWarp) {
+  if (warp < kCopyWarp || warp >= kEndWarp) {
     Walk begin = walk;
     if (walk_next<C::CC>(p, begin, next)) {
       any = true;
       write_query_terms<C>(p, next, smem + C::Q_OFFSET, smem + C::QSF_OFFSET, reinterpret_cast<float*>(smem + C::COL_OFFSET),
-                           warp < kCodeWarp ? warp : warp - 4, 12, lane);
+                           warp < kCopyWarp ? warp : warp - 4, 12, lane);
       fence_proxy_async_smem();
     }
     if (warp >= kEndWarp) {
@@ -510,7 +511,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     bool waited = !early, stop = false;
     uint32_t err_bits = 0;
     const uint64_t policy = l2_evict_first_policy();
-    const bool codes = warp == kCodeWarp;  // (the other warp: the scales)
     any = walk_next<C::CC>(p, walk, next);
     auto page_of = [&](const Segment& s, int i) {
       const int t = s.t_base + i * kFp4Tile + lane * 16;
@@ -552,30 +552,27 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
             break;
           }
           uint8_t* item = smem + st * C::ITEM_BYTES;
-          if (codes) {
-            if (lane == 0) {
-              valid[st] = word;
-              if (bits)
-                mbar_arrive_expect_tx(&full[st], __popc(bits) * (16 * C::D / 2) + (v ? 0 : p.stall_bytes));
-              else
-                mbar_arrive(&full[st]);
-            }
-            __syncwarp();
-            if (lane < 8 && row0 >= 0)
-              tma_load_4d(item + lane * 16 * (C::D / 2), v ? &p.vmap : &p.kmap, 0, 0, 0, row0 / 8, &full[st], policy);
-          } else {
-            // 16 bytes a lane (as bulk copies these would be half of all copies)
-            constexpr int LANES = C::ROW_SF;  // 16-byte pieces of 16 tokens' scales
-            const uint8_t* sf = (v ? p.v_sf : p.k_sf) + (lane % LANES) * 16;
-            uint8_t* to = item + C::CODE_BYTES + lane * 16;
-#pragma unroll
-            for (int k = 0; k < 8; k += 32 / LANES) {
-              const int at = k + lane / LANES;  // the 16 tokens this lane copies a piece of
-              const int row = __shfl_sync(kFullMask, row0, at);
-              if (row >= 0) cp_async16(to + k * 16 * C::ROW_SF, sf + (size_t)row * C::ROW_SF);
-            }
-            cp_async_arrive(&full[st]);
+          if (lane == 0) {
+            valid[st] = word;
+            if (bits)
+              mbar_arrive_expect_tx(&full[st], __popc(bits) * (16 * C::D / 2) + (v ? 0 : p.stall_bytes));
+            else
+              mbar_arrive(&full[st]);
           }
+          __syncwarp();
+          if (lane < 8 && row0 >= 0)
+            tma_load_4d(item + lane * 16 * (C::D / 2), v ? &p.vmap : &p.kmap, 0, 0, 0, row0 / 8, &full[st], policy);
+          // scales: 16 bytes a lane (as bulk copies these would be half of all copies)
+          constexpr int LANES = C::ROW_SF;  // 16-byte pieces of 16 tokens' scales
+          const uint8_t* sf = (v ? p.v_sf : p.k_sf) + (lane % LANES) * 16;
+          uint8_t* to = item + C::CODE_BYTES + lane * 16;
+#pragma unroll
+          for (int k = 0; k < 8; k += 32 / LANES) {
+            const int at = k + lane / LANES;  // the 16 tokens this lane copies a piece of
+            const int row = __shfl_sync(kFullMask, row0, at);
+            if (row >= 0) cp_async16(to + k * 16 * C::ROW_SF, sf + (size_t)row * C::ROW_SF);
+          }
+          cp_async_arrive(&full[st]);
         }
         if (stop) break;
         ++it;
@@ -715,7 +712,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
       __syncwarp();
       if (lane == 0) mbar_arrive(&l_full[sg & 1]);
     }
-  } else if (warp < kCodeWarp) {
+  } else if (warp < kCopyWarp) {
     // ---- a tile's scales put where tcgen05.cp takes them from, in place: from a row's
     // behind each other to 64 dims' of all rows behind each other. A lane has a row.
     const int j = warp - kSfWarp, row = j * 32 + lane;
@@ -777,90 +774,82 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
         it += v;
       }
     }
-  } else if (warp == kMmaWarp) {
-    // ---- the scores and V^T, by one lane, whichever can go on. The tensor core holds
-    // little of what is issued ahead, so the sums are another warp's.
+  } else if (warp == kScoreWarp) {
+    // ---- S = K q^T, by one lane, a tile after another
     if (share_tiles > 0 && elect_one()) {
       constexpr uint32_t kQk = (1u << 7) | (1u << 10) | ((uint32_t)(C::N / 8) << 17) | (8u << 24);  // e2m1, e4m3 scales
-      constexpr uint32_t kDq = (1u << 7) | (1u << 10) | ((uint32_t)(kFp4Tile / 8) << 17) | (8u << 24);
-      constexpr uint32_t kRows = desc_hi(C::SL * 1024), kEye = desc_hi(512, 64);
-      constexpr int kItem = C::ITEM_BYTES >> 4, kScales = C::CODE_BYTES >> 4;
+      constexpr uint32_t kRows = desc_hi(C::SL * 1024);
       // descriptors' lower words: 16-byte units, a step further is a constant added
-      const uint32_t ring = smem_u32(smem) >> 4, q0 = ring + (C::Q_OFFSET >> 4), eye = ring + (C::EYE_OFFSET >> 4);
-      int scores = 0, sk = 0, k_round = 0, sg = 0;                // tiles whose scores are out; its slot
-      int chunk = 0, i = 0, sv = C::KVS ? 0 : C::NK, v_round = 0;  // the next chunk of V^T, of tile i
-      bool k_ok = false, v_ok = false;
-      uint32_t word = 0;  // of the scores' tile
-      int idle = 0;
-      unsigned long long start = 0;
+      const uint32_t ring = smem_u32(smem) >> 4, q0 = ring + (C::Q_OFFSET >> 4);
+      int i = 0, sk = 0, round = 0, sg = 0;  // the tile, its slot, its segment
       good = *tmem_at == 0;
 #pragma unroll 1
-      while (good && (i < share_tiles || scores < share_tiles)) {
-        bool on = false;
-        if (scores < share_tiles) {
-          // ---- S = K q^T, over the scores before once they are read (so their product has read K's scales)
-          // (the first of a segment: once its query terms are there, which may wait for V^T of a segment before)
-          if (!k_ok && mbar_test(&ready[sk], k_round & 1)) {
-            word = valid[sk];
-            k_ok = !(word & kTileFirst) || mbar_test(&q_full[sg & 1], (sg >> 1) & 1);
-          }
-          if (k_ok && (scores == 0 || mbar_test(s_empty, (scores - 1) & 1))) {
-            if (word & kTileFirst) ++sg;
-            tmem_fence_after();
-            const uint32_t a = ring + sk * kItem, q = q0 + ((word & kTileOdd) ? C::Q_BYTES >> 4 : 0);
-#pragma unroll
-            for (int k = 0; k < C::KSTEPS; ++k) copy_scales(kTmemSfk + k * 4, a + kScales + k * 32);
-#pragma unroll
-            for (int k = 0; k < C::KSTEPS; ++k)
-              mma_fp4<kRows, kRows, kQk>(kTmemS, a + (k >> 2) * 64 + (k & 3) * 2, q + (k >> 2) * 64 + (k & 3) * 2,
-                                         kTmemSfk + k * 4, kTmemSfq + k * 4, k > 0);
-            *blocks_of = word & 0xffu;
-            mma_commit<1>(s_full);
-            mma_commit<1>(&empty[sk]);
-            if (word & kTileLast) mma_commit<1>(qk_done);
-            mbar_arrive(s_full);
-            ++scores;
-            if (++sk == C::NK) sk = 0, ++k_round;
-            k_ok = false;
-            on = true;
-          }
+      for (; i < share_tiles && good; ++i) {
+        if (!(good = wait_for(&ready[sk], round))) break;
+        const uint32_t word = valid[sk];
+        if (word & kTileFirst) {
+          if (!(good = wait_for(&q_full[sg & 1], sg >> 1))) break;
+          ++sg;
         }
-        if (!v_ok && i < share_tiles) v_ok = C::KVS ? scores > i : mbar_test(&ready[sv], v_round & 1);
-        if (v_ok) {
-          // ---- a chunk V^T = I V^T, 128 dims. (What its scales lie over was read: the chunk before in its buffer is used.)
-          const int at = i * CH + chunk, c = at & 1;
-          if (at < 2 || mbar_test(&vt_empty[c], ((at >> 1) - 1) & 1)) {
-            tmem_fence_after();
-            const uint32_t item = ring + sv * kItem, v = item + (chunk >> 1) * 64 + (chunk & 1) * 4;
-            const uint32_t sfv = kTmemSfv + chunk * 8;
-            copy_scales(sfv, item + kScales + chunk * 64);
-            copy_scales(sfv + 4, item + kScales + chunk * 64 + 32);
-            mma_fp4<kEye, kRows, kDq>(kTmemVt + c * 128, eye, v, kTmemSfi, sfv, false);
-            mma_fp4<kEye, kRows, kDq>(kTmemVt + c * 128, eye + 2, v + 2, kTmemSfi, sfv + 4, true);
-            mma_commit<1>(&vt_full[c]);
-            if (++chunk == CH) mma_commit<1>(&empty[sv]);
-            mbar_arrive(&vt_full[c]);
-            if (chunk == CH) {
-              chunk = 0;
-              ++i;
-              if (++sv == RINGS) sv = C::KVS ? 0 : C::NK, ++v_round;
-              v_ok = false;
-            }
-            on = true;
-          }
-        }
-        if (on) {
-          idle = 0;
-        } else if ((++idle & 255) == 0) {
-          const unsigned long long now = global_timer_ns();
-          if (idle == 256) start = now;
-          else if (now - start > kWaitTimeoutNs) good = false;
+        // over the scores before once they are read (so their product has read K's scales too)
+        if (i > 0 && !(good = wait_for(s_empty, i - 1))) break;
+        tmem_fence_after();
+        const uint32_t a = ring + sk * (C::ITEM_BYTES >> 4), q = q0 + ((word & kTileOdd) ? C::Q_BYTES >> 4 : 0);
+#pragma unroll
+        for (int k = 0; k < C::KSTEPS; ++k) copy_scales(kTmemSfk + k * 4, a + (C::CODE_BYTES >> 4) + k * 32);
+#pragma unroll
+        for (int k = 0; k < C::KSTEPS; ++k)
+          mma_fp4<kRows, kRows, kQk>(kTmemS, a + (k >> 2) * 64 + (k & 3) * 2, q + (k >> 2) * 64 + (k & 3) * 2,
+                                     kTmemSfk + k * 4, kTmemSfq + k * 4, k > 0);
+        *blocks_of = word & 0xffu;
+        mma_commit<1>(s_full);
+        mma_commit<1>(&empty[sk]);
+        if (word & kTileLast) mma_commit<1>(qk_done);
+        mbar_arrive(s_full);
+        if (++sk == C::NK) {
+          sk = 0;
+          ++round;
         }
       }
       // what was issued ends before its operands and results are used for something else
-      if (scores > 0) wait_for(s_full, scores - 1);
-      const int last = i * CH + chunk - 1;
-      if (last >= 0) wait_for(&vt_full[last & 1], last >> 1);
+      if (i > 0) wait_for(s_full, i - 1);
+      if (!good) atomicOr(p.err, kErrTimeout);
+    }
+    __syncwarp();
+  } else if (warp == kWideWarp) {
+    // ---- V^T = I V^T, a chunk of 128 dims after another
+    if (share_tiles > 0 && elect_one()) {
+      constexpr uint32_t kDq = (1u << 7) | (1u << 10) | ((uint32_t)(kFp4Tile / 8) << 17) | (8u << 24);
+      constexpr uint32_t kRows = desc_hi(C::SL * 1024), kEye = desc_hi(512, 64);
+      const uint32_t ring = smem_u32(smem) >> 4, eye = ring + (C::EYE_OFFSET >> 4);
+      int i = 0, sv = C::KVS ? 0 : C::NK, round = 0, at = 0;  // the tile, its slot; chunks so far
+      good = *tmem_at == 0;
+#pragma unroll 1
+      for (; i < share_tiles && good; ++i) {
+        if (!(good = wait_for(&ready[sv], round))) break;
+        const uint32_t item = ring + sv * (C::ITEM_BYTES >> 4);
+#pragma unroll 1
+        for (int chunk = 0; chunk < CH; ++chunk, ++at) {
+          const int c = at & 1;
+          if (at >= 2 && !(good = wait_for(&vt_empty[c], (at >> 1) - 1))) break;
+          tmem_fence_after();
+          const uint32_t v = item + (chunk >> 1) * 64 + (chunk & 1) * 4, sf = item + (C::CODE_BYTES >> 4) + chunk * 64;
+          // (the product that these scales' columns were for before is done: its chunk is used, or its buffer would not be free)
+          const uint32_t sfv = kTmemSfv + chunk * 8;
+          copy_scales(sfv, sf);
+          copy_scales(sfv + 4, sf + 32);
+          mma_fp4<kEye, kRows, kDq>(kTmemVt + c * 128, eye, v, kTmemSfi, sfv, false);
+          mma_fp4<kEye, kRows, kDq>(kTmemVt + c * 128, eye + 2, v + 2, kTmemSfi, sfv + 4, true);
+          mma_commit<1>(&vt_full[c]);
+          mbar_arrive(&vt_full[c]);
+        }
+        mma_commit<1>(&empty[sv]);
+        if (++sv == RINGS) {
+          sv = C::KVS ? 0 : C::NK;
+          ++round;
+        }
+      }
+      if (at > 0) wait_for(&vt_full[(at - 1) & 1], (at - 1) >> 1);
       if (!good) atomicOr(p.err, kErrTimeout);
     }
     __syncwarp();
@@ -1035,7 +1024,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     }
   }
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     tmem_fence_after();
     tmem_dealloc<1>(*tmem_at, kTmemCols);
   }
