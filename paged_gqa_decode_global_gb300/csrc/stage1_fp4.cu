@@ -33,10 +33,10 @@
 // by 2^60 (tf32 has fp32's exponents), which rescales the sums.
 //
 // Roles: warps 0-3 softmax (a lane a token); 4-7 put a tile's scales in tcgen05.cp's
-// order; 8 copies; one lane each of 9 issues the scores, of 10 V^T, of 11 the sums
-// (a look at a barrier takes ~150 cycles, and one lane that does all three spends
-// most of them looking); 12-15 write the next unit's query terms, read a unit's sums
-// and join pieces.
+// order; 8-11 write the next unit's query terms, read a unit's sums and join pieces;
+// 12, 13 copy codes (TMA), 14 scales (cp.async); one lane each of 15 issues the
+// scores, of 16 V^T, of 17 the sums (a look at a barrier takes 60 to 150 cycles, and
+// one lane that does all three spends most of them looking).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -411,29 +411,32 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
   volatile uint32_t* valid = reinterpret_cast<uint32_t*>(smem + C::VALID_OFFSET);  // [RINGS]
   volatile uint32_t* tile_of = reinterpret_cast<uint32_t*>(smem + C::TILE_OFFSET);      // [2] first, last: by P buffer
   volatile uint32_t* blocks_of = reinterpret_cast<uint32_t*>(smem + C::BLOCKS_OFFSET);  // of the scores' tile
-  constexpr int kSfWarp = 4, kCopyWarp = 8, kScoreWarp = 9, kWideWarp = 10, kSumWarp = 11, kEndWarp = 12;
+  constexpr int kSfWarp = 4, kEndWarp = 8, kCodeWarp = 12, kScaleWarp = 14, kScoreWarp = 15, kWideWarp = 16, kSumWarp = 17;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const bool copies = warp == kCopyWarp;
+  const bool copies = warp >= kCodeWarp && warp <= kScaleWarp;
   const bool early = p.early_kv != 0 && copies;
   uint32_t* poison_of = reinterpret_cast<uint32_t*>(smem + C::POISON_OFFSET);  // [kPoison][CC], by segment
 
-  if (copies) {
+  if (warp == kCodeWarp) {
     if (lane == 0) {
       prefetch_tensormap(&p.kmap);
       if (!C::KVS) prefetch_tensormap(&p.vmap);
     }
     for (int i = lane; i < C::NUM_BARS; i += 32) {
       const int r = i - 3 * RINGS;
-      // full: the codes' byte count and every lane's scales; empty: the products that read the slot
-      mbar_init(&full[i], i < RINGS ? 33 : i < 2 * RINGS ? (C::KVS ? 2 : 1) : r < 0 ? 4 : r < 5 ? 1 : r < 9 ? 2 : 4);
+      // full: the codes' byte count (K = V: two warps') and every lane's scales; empty: the products that read the slot
+      mbar_init(&full[i], i < RINGS ? (C::KVS ? 34 : 33) : i < 2 * RINGS ? (C::KVS ? 2 : 1) : r < 0 ? 4 : r < 5 ? 1 : r < 9 ? 2 : 4);
     }
     fence_barrier_init();
     __syncwarp();
   }
   if (warp == kScoreWarp) tmem_alloc<1>(tmem_at, kTmemCols);
-  if (copies) named_bar_arrive(4, C::THREADS);
+  if (copies) {
+    named_bar_sync(5, 3 * 32);
+    named_bar_arrive(4, C::THREADS);
+  }
   // what depends on nothing
-  if (warp >= kEndWarp) {
+  if (warp >= kEndWarp && warp < kCodeWarp) {
     const int wt = tid - kEndWarp * 32;
     // the unit matrix in e2m1 (1.0 is 2): 16 bytes of row m hold dims 32 c .., the one lies at dim m
 #pragma unroll 1
@@ -476,12 +479,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
   // the first segment's query terms, by all who have nothing to do yet
   Segment next;
   bool any = false;
-  if (warp < kCopyWarp || warp >= kEndWarp) {
+  if (warp < kCodeWarp) {
     Walk begin = walk;
     if (walk_next<C::CC>(p, begin, next)) {
       any = true;
       write_query_terms<C>(p, next, smem + C::Q_OFFSET, smem + C::QSF_OFFSET, reinterpret_cast<float*>(smem + C::COL_OFFSET),
-                           warp < kCopyWarp ? warp : warp - 4, 12, lane);
+                           warp, 12, lane);
       fence_proxy_async_smem();
     }
     if (warp >= kEndWarp) {
@@ -508,6 +511,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     // ---- copies, four tiles' page ids ahead (one tile ahead, their latency bound
     // the kernel: 4 x 32768 tokens 77 -> 62 us): lane l has the 16 tokens 16 l .. of
     // four tiles
+    const int mine = warp - kCodeWarp;  // 0: K's codes, 1: V's (K = V: the lower and the upper half), 2: scales
     bool waited = !early, stop = false;
     uint32_t err_bits = 0;
     const uint64_t policy = l2_evict_first_policy();
@@ -545,6 +549,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
         }
 #pragma unroll 1
         for (int v = 0; v < (C::KVS ? 1 : 2); ++v) {
+          if (!C::KVS && mine == 1 - v) continue;
           const int n = v ? C::NV : C::NK, round = it / n, st = (v ? C::NK : 0) + it - round * n;
           if (round > 0 && __any_sync(kFullMask, !wait_for(&empty[st], round - 1))) {
             err_bits |= kErrTimeout;
@@ -552,27 +557,31 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
             break;
           }
           uint8_t* item = smem + st * C::ITEM_BYTES;
-          if (lane == 0) {
-            valid[st] = word;
-            if (bits)
-              mbar_arrive_expect_tx(&full[st], __popc(bits) * (16 * C::D / 2) + (v ? 0 : p.stall_bytes));
-            else
-              mbar_arrive(&full[st]);
-          }
-          __syncwarp();
-          if (lane < 8 && row0 >= 0)
-            tma_load_4d(item + lane * 16 * (C::D / 2), v ? &p.vmap : &p.kmap, 0, 0, 0, row0 / 8, &full[st], policy);
-          // scales: 16 bytes a lane (as bulk copies these would be half of all copies)
-          constexpr int LANES = C::ROW_SF;  // 16-byte pieces of 16 tokens' scales
-          const uint8_t* sf = (v ? p.v_sf : p.k_sf) + (lane % LANES) * 16;
-          uint8_t* to = item + C::CODE_BYTES + lane * 16;
+          if (mine < 2) {
+            const uint32_t part = C::KVS ? bits & (mine ? 0xf0u : 0x0fu) : bits;
+            if (lane == 0) {
+              if (!C::KVS || mine == 0) valid[st] = word;
+              if (part)
+                mbar_arrive_expect_tx(&full[st], __popc(part) * (16 * C::D / 2) + (mine == 0 ? p.stall_bytes : 0));
+              else
+                mbar_arrive(&full[st]);
+            }
+            __syncwarp();
+            if (lane < 8 && ((part >> lane) & 1u))
+              tma_load_4d(item + lane * 16 * (C::D / 2), v ? &p.vmap : &p.kmap, 0, 0, 0, row0 / 8, &full[st], policy);
+          } else {
+            // 16 bytes a lane (as bulk copies these would be half of all copies)
+            constexpr int LANES = C::ROW_SF;  // 16-byte pieces of 16 tokens' scales
+            const uint8_t* sf = (v ? p.v_sf : p.k_sf) + (lane % LANES) * 16;
+            uint8_t* to = item + C::CODE_BYTES + lane * 16;
 #pragma unroll
-          for (int k = 0; k < 8; k += 32 / LANES) {
-            const int at = k + lane / LANES;  // the 16 tokens this lane copies a piece of
-            const int row = __shfl_sync(kFullMask, row0, at);
-            if (row >= 0) cp_async16(to + k * 16 * C::ROW_SF, sf + (size_t)row * C::ROW_SF);
+            for (int k = 0; k < 8; k += 32 / LANES) {
+              const int at = k + lane / LANES;  // the 16 tokens this lane copies a piece of
+              const int row = __shfl_sync(kFullMask, row0, at);
+              if (row >= 0) cp_async16(to + k * 16 * C::ROW_SF, sf + (size_t)row * C::ROW_SF);
+            }
+            cp_async_arrive(&full[st]);
           }
-          cp_async_arrive(&full[st]);
         }
         if (stop) break;
         ++it;
@@ -582,7 +591,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     const unsigned long long deadline = global_timer_ns() + kWaitTimeoutNs;
     for (int s = lane; s < RINGS; s += 32) {
       const int n = s < C::NK ? C::NK : C::NV, at = s < C::NK ? s : s - C::NK;
-      if (at >= it) continue;
+      if (at >= it || (!C::KVS && mine != 2 && (s >= C::NK) != (mine == 1))) continue;
       const int last = at + n * ((it - 1 - at) / n);
       if (!mbar_wait_until(&full[s], (last / n) & 1, deadline)) err_bits |= kErrTimeout;
     }
@@ -601,16 +610,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     for (int sg = 0; walk_next<C::CC>(p, walk, seg); ++sg) {
       if (seg.bad && tid == 0) atomicOr(p.err, kErrBadSeqLen);
       await(&q_full[sg & 1], sg >> 1);
-      float col_mul[C::CC], ref[C::CC], sum[C::CC];
-      int col_hi[C::CC], col_lo[C::CC];
+      const float* col_mul = reinterpret_cast<const float*>(smem + C::COL_OFFSET) + (sg & 1) * C::CC;
+      const uint32_t reach = p.window > 0 ? p.window : 0x7fffffff;
+      float ref[C::CC], sum[C::CC];
+      int newest[C::CC];  // position a column attends: it and the reach - 1 before it
       {
         Pair col(seg);
 #pragma unroll
         for (int c = 0; c < C::CC; ++c, col.next(p)) {
-          col_mul[c] = reinterpret_cast<const float*>(smem + C::COL_OFFSET)[(sg & 1) * C::CC + c];
-          const int end = col.end(p, seg);
-          col_hi[c] = col.valid(p) ? min(seg.thi, end) : 0;
-          col_lo[c] = max(seg.tlo, p.window > 0 ? end - p.window : 0);
+          newest[c] = col.valid(p) ? col.end(p, seg) - 1 : -1;
           ref[c] = -INFINITY;
           sum[c] = 0.f;
         }
@@ -622,17 +630,21 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
         tmem_fence_after();
         float s[C::CC];
         {
-          uint32_t w[kFp4Terms * C::CC / 8][8];
+          // the terms' columns, smallest terms first, three loads at a time (for the registers)
+          float x[C::CC];
 #pragma unroll
-          for (int k = 0; k < kFp4Terms * C::CC / 8; ++k) tmem_ld(w[k], kTmemS + quarter + k * 8);
-          tmem_wait_ld();
+          for (int c = 0; c < C::CC; ++c) x[c] = 0.f;
 #pragma unroll
-          for (int c = 0; c < C::CC; ++c) {
-            float x = 0.f;
+          for (int k0 = kFp4Terms * C::CC / 8 - 3; k0 >= 0; k0 -= 3) {
+            uint32_t w[3][8];
 #pragma unroll
-            for (int t = kFp4Terms - 1; t >= 0; --t) x += __uint_as_float(w[(t * C::CC + c) / 8][(t * C::CC + c) % 8]);
-            s[c] = x * col_mul[c];
+            for (int k = 0; k < 3; ++k) tmem_ld(w[k], kTmemS + quarter + (k0 + k) * 8);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 23; i >= 0; --i) x[i % C::CC] += __uint_as_float(w[i >> 3][i & 7]);
           }
+#pragma unroll
+          for (int c = 0; c < C::CC; ++c) s[c] = x[c] * col_mul[c];
         }
         const int row = warp * 32 + lane, t = seg.t_base + i * kFp4Tile + row;
         const bool ok = (*blocks_of >> (row >> 4)) & 1u;
@@ -642,7 +654,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
         bool above = false;
 #pragma unroll
         for (int c = 0; c < C::CC; ++c) {
-          if (!(ok && t >= col_lo[c] && t < col_hi[c])) s[c] = -INFINITY;
+          if (!ok || (uint32_t)(newest[c] - t) >= reach) s[c] = -INFINITY;
           above = above || s[c] > ref[c] + kRefRange;
         }
         if (named_bar_or(2, 128, above)) {
@@ -712,7 +724,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
       __syncwarp();
       if (lane == 0) mbar_arrive(&l_full[sg & 1]);
     }
-  } else if (warp < kCopyWarp) {
+  } else if (warp < kEndWarp) {
     // ---- a tile's scales put where tcgen05.cp takes them from, in place: from a row's
     // behind each other to 64 dims' of all rows behind each other. A lane has a row.
     const int j = warp - kSfWarp, row = j * 32 + lane;
@@ -866,11 +878,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
         const uint32_t word = tile_of[i & 1], pa = p0 + (i & 1) * (C::P_BYTES >> 4);
         const bool first = (word & kTileFirst) != 0;
 #pragma unroll 1
-        for (int c0 = 0; c0 < CH; c0 += 2) {
+        for (int c0 = 0; c0 < CH && good; c0 += 2) {
           const int use = i * (CH / 2) + (c0 >> 1);  // of a V^T buffer
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            good = good && wait_for(&vt_full[c], use);
+            if (!(good = good && wait_for(&vt_full[c], use))) break;
             tmem_fence_after();
 #pragma unroll
             for (int q = 0; q < 16; ++q)
