@@ -35,8 +35,8 @@
 // Roles: warps 0-3 softmax (a lane a token); 4-7 put a tile's scales in tcgen05.cp's
 // order; 8-11 write the next unit's query terms, read a unit's sums and join pieces;
 // 12, 13 copy codes (TMA), 14 scales (cp.async); one lane each of 15 issues the
-// scores, of 16 V^T, of 17 the sums (a look at a barrier takes 60 to 150 cycles, and
-// one lane that does all three spends most of them looking).
+// scores, of 16 and 17 V^T, of 18 and 19 the sums (a look at a barrier takes 60 to 150 cycles, and
+// one lane that does all this spends most of them looking).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -393,11 +393,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
   uint64_t* ready = empty + RINGS;      // [RINGS]
   // one arrival: the products' commits
   uint64_t* vt_empty = ready + RINGS;   // [2] a chunk of V^T used
-  uint64_t* p_empty = vt_empty + 2;     // [2] P used: the tile is in the sums
-  uint64_t* qk_done = p_empty + 2;      // a segment's scores all computed
-  // two: a commit, and an arrival of the same lane (which orders what it has seen of others)
-  uint64_t* vt_full = qk_done + 1;      // [2] a chunk of V^T there
+  uint64_t* qk_done = vt_empty + 2;     // a segment's scores all computed
+  // two: both of V^T's buffers' products' commits
+  uint64_t* p_empty = qk_done + 1;      // [2] P used: the tile is in the sums
+  // or a commit, and an arrival of the same lane (which orders what it has seen of others)
+  uint64_t* vt_full = p_empty + 2;      // [2] a chunk of V^T there
   uint64_t* s_full = vt_full + 2;       // scores computed
+  // four: both of both buffers'
   uint64_t* o_full = s_full + 1;        // a segment's sums complete
   // four warps
   uint64_t* s_empty = o_full + 1;       // scores read
@@ -411,7 +413,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
   volatile uint32_t* valid = reinterpret_cast<uint32_t*>(smem + C::VALID_OFFSET);  // [RINGS]
   volatile uint32_t* tile_of = reinterpret_cast<uint32_t*>(smem + C::TILE_OFFSET);      // [2] first, last: by P buffer
   volatile uint32_t* blocks_of = reinterpret_cast<uint32_t*>(smem + C::BLOCKS_OFFSET);  // of the scores' tile
-  constexpr int kSfWarp = 4, kEndWarp = 8, kCodeWarp = 12, kScaleWarp = 14, kScoreWarp = 15, kWideWarp = 16, kSumWarp = 17;
+  constexpr int kSfWarp = 4, kEndWarp = 8, kCodeWarp = 12, kScaleWarp = 14, kScoreWarp = 15, kWideWarp = 16, kSumWarp = 18;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool copies = warp >= kCodeWarp && warp <= kScaleWarp;
   const bool early = p.early_kv != 0 && copies;
@@ -425,7 +427,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     for (int i = lane; i < C::NUM_BARS; i += 32) {
       const int r = i - 3 * RINGS;
       // full: the codes' byte count (K = V: two warps') and every lane's scales; empty: the products that read the slot
-      mbar_init(&full[i], i < RINGS ? (C::KVS ? 34 : 33) : i < 2 * RINGS ? (C::KVS ? 2 : 1) : r < 0 ? 4 : r < 5 ? 1 : r < 9 ? 2 : 4);
+      mbar_init(&full[i], i < RINGS ? (C::KVS ? 34 : 33) : i < 2 * RINGS ? (C::KVS ? 3 : i - RINGS < C::NK ? 1 : 2) : r < 0 ? 4 : r < 3 ? 1 : r < 8 ? 2 : 4);
     }
     fence_barrier_init();
     __syncwarp();
@@ -828,32 +830,33 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
       if (!good) atomicOr(p.err, kErrTimeout);
     }
     __syncwarp();
-  } else if (warp == kWideWarp) {
-    // ---- V^T = I V^T, a chunk of 128 dims after another
+  } else if (warp >= kWideWarp && warp < kSumWarp) {
+    // ---- V^T = I V^T, 128 dims at a time: this lane's chunks are those of buffer c
     if (share_tiles > 0 && elect_one()) {
       constexpr uint32_t kDq = (1u << 7) | (1u << 10) | ((uint32_t)(kFp4Tile / 8) << 17) | (8u << 24);
       constexpr uint32_t kRows = desc_hi(C::SL * 1024), kEye = desc_hi(512, 64);
-      const uint32_t ring = smem_u32(smem) >> 4, eye = ring + (C::EYE_OFFSET >> 4);
-      int i = 0, sv = C::KVS ? 0 : C::NK, round = 0, at = 0;  // the tile, its slot; chunks so far
+      const uint32_t c = warp - kWideWarp, ring = smem_u32(smem) >> 4, eye = ring + (C::EYE_OFFSET >> 4);
+      const uint32_t to = kTmemVt + c * 128;
+      uint64_t *my_full = vt_full + c, *my_empty = vt_empty + c;
+      int i = 0, sv = C::KVS ? 0 : C::NK, round = 0, use = 0;  // the tile, its slot; chunks so far
       good = *tmem_at == 0;
 #pragma unroll 1
       for (; i < share_tiles && good; ++i) {
         if (!(good = wait_for(&ready[sv], round))) break;
-        const uint32_t item = ring + sv * (C::ITEM_BYTES >> 4);
-#pragma unroll 1
-        for (int chunk = 0; chunk < CH; ++chunk, ++at) {
-          const int c = at & 1;
-          if (at >= 2 && !(good = wait_for(&vt_empty[c], (at >> 1) - 1))) break;
+        const uint32_t item = ring + sv * (C::ITEM_BYTES >> 4) + c * 4, sf = item - c * 4 + (C::CODE_BYTES >> 4) + c * 64;
+#pragma unroll
+        for (int k = 0; k < CH / 2; ++k) {
+          if (use > 0 && !(good = good && wait_for(my_empty, use - 1))) break;
           tmem_fence_after();
-          const uint32_t v = item + (chunk >> 1) * 64 + (chunk & 1) * 4, sf = item + (C::CODE_BYTES >> 4) + chunk * 64;
           // (the product that these scales' columns were for before is done: its chunk is used, or its buffer would not be free)
-          const uint32_t sfv = kTmemSfv + chunk * 8;
-          copy_scales(sfv, sf);
-          copy_scales(sfv + 4, sf + 32);
-          mma_fp4<kEye, kRows, kDq>(kTmemVt + c * 128, eye, v, kTmemSfi, sfv, false);
-          mma_fp4<kEye, kRows, kDq>(kTmemVt + c * 128, eye + 2, v + 2, kTmemSfi, sfv + 4, true);
-          mma_commit<1>(&vt_full[c]);
-          mbar_arrive(&vt_full[c]);
+          const uint32_t sfv = kTmemSfv + c * 8 + k * 16;
+          copy_scales(sfv, sf + k * 128);
+          copy_scales(sfv + 4, sf + k * 128 + 32);
+          mma_fp4<kEye, kRows, kDq>(to, eye, item + k * 64, kTmemSfi, sfv, false);
+          mma_fp4<kEye, kRows, kDq>(to, eye + 2, item + k * 64 + 2, kTmemSfi, sfv + 4, true);
+          mma_commit<1>(my_full);
+          mbar_arrive(my_full);
+          ++use;
         }
         mma_commit<1>(&empty[sv]);
         if (++sv == RINGS) {
@@ -861,35 +864,33 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
           ++round;
         }
       }
-      if (at > 0) wait_for(&vt_full[(at - 1) & 1], (at - 1) >> 1);
+      if (use > 0) wait_for(my_full, use - 1);
       if (!good) atomicOr(p.err, kErrTimeout);
     }
     __syncwarp();
-  } else if (warp == kSumWarp) {
-    // ---- the sums O^T += V^T P^T, a chunk of 128 dims after another
+  } else if (warp >= kSumWarp) {
+    // ---- the sums O^T += V^T P^T, likewise
     if (share_tiles > 0 && elect_one()) {
       constexpr uint32_t kPv = (1u << 4) | (2u << 7) | (2u << 10) | (2u << 17) | (8u << 24);  // tf32 -> fp32, 128 x 16
       constexpr uint32_t kP = desc_hi(0);  // (both 8-column groups of P are the same: the upper columns are not read)
+      const uint32_t c = warp - kSumWarp, from = kTmemVt + c * 128, to = kTmemO + c * 16;
       const uint32_t p0 = (smem_u32(smem) + C::P_OFFSET) >> 4;
-      int i = 0;
+      uint64_t *my_full = vt_full + c, *my_empty = vt_empty + c;
+      int i = 0, use = 0;
 #pragma unroll 1
       for (; i < share_tiles && good; ++i) {
         if (!(good = wait_for(&p_full[i & 1], i >> 1))) break;
         const uint32_t word = tile_of[i & 1], pa = p0 + (i & 1) * (C::P_BYTES >> 4);
-        const bool first = (word & kTileFirst) != 0;
+        const bool more = (word & kTileFirst) == 0;
 #pragma unroll 1
-        for (int c0 = 0; c0 < CH && good; c0 += 2) {
-          const int use = i * (CH / 2) + (c0 >> 1);  // of a V^T buffer
+        for (int k = 0; k < CH / 2; ++k) {
+          if (!(good = wait_for(my_full, use))) break;
+          tmem_fence_after();
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            if (!(good = good && wait_for(&vt_full[c], use))) break;
-            tmem_fence_after();
-#pragma unroll
-            for (int q = 0; q < 16; ++q)
-              mma_tf32<kP, kPv>(kTmemO + (c0 + c) * 16, kTmemVt + c * 128 + q * 8, pa + (q >> 2) * 64 + (q & 3) * 2,
-                                !first || q > 0);
-            mma_commit<1>(&vt_empty[c]);
-          }
+          for (int q = 0; q < 16; ++q)
+            mma_tf32<kP, kPv>(to + k * 32, from + q * 8, pa + (q >> 2) * 64 + (q & 3) * 2, more || q > 0);
+          mma_commit<1>(my_empty);
+          ++use;
         }
         mma_commit<1>(&p_empty[i & 1]);
         if (word & kTileLast) {
@@ -897,7 +898,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
           mbar_arrive(o_full);
         }
       }
-      if (i > 0) wait_for(&vt_empty[1], i * (CH / 2) - 1);
+      if (use > 0) wait_for(my_empty, use - 1);
       if (!good) atomicOr(p.err, kErrTimeout);
     }
     __syncwarp();
