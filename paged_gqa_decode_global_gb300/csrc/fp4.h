@@ -50,7 +50,8 @@ struct Fp4Cfg {
   static constexpr int MISC_OFFSET = SUM_OFFSET + 2 * 5 * CC * 4; // u32: the join's ticket
   static constexpr int BLOCKS_OFFSET = MISC_OFFSET + 4;           // u32: the 16-token blocks that the scores' tile holds
   static constexpr int TILE_OFFSET = BLOCKS_OFFSET + 4;           // u32 [2]: of P's tiles
-  static constexpr int VALID_OFFSET = TILE_OFFSET + 8;           // u32 [NK + NV]: what a slot's tile is (kTile...)
+  static constexpr int BEGIN_OFFSET = TILE_OFFSET + 8;            // int [64]: where the share begins
+  static constexpr int VALID_OFFSET = BEGIN_OFFSET + 256;          // u32 [NK + NV]: what a slot's tile is (kTile...)
   static constexpr int BAR_OFFSET = (VALID_OFFSET + (NK + NV) * 4 + 7) / 8 * 8;
   static constexpr int NUM_BARS = 3 * (NK + NV) + 19;
   static constexpr int SMEM_BYTES = BAR_OFFSET + NUM_BARS * 8 + 16 + 1024;  // (+ 1 KiB to start on a 1024-byte boundary)

@@ -433,10 +433,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     __syncwarp();
   }
   if (warp == kScoreWarp) tmem_alloc<1>(tmem_at, kTmemCols);
-  if (copies) {
-    named_bar_sync(5, 3 * 32);
-    named_bar_arrive(4, C::THREADS);
-  }
   // what depends on nothing
   if (warp >= kEndWarp && warp < kCodeWarp) {
     const int wt = tid - kEndWarp * 32;
@@ -469,32 +465,55 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     grid_dependency_wait();
     grid_launch_dependents();
   }
+  // One warp finds the share and its first segment (20 that did it side by side took
+  // 1.5 us instead of 1); what all lanes have of them goes round through shared memory.
   Walk walk;
-  walk_start(p, walk);
-  const int share_tiles = walk.left;
-  Segment seg;
-  if (!copies) {
-    // the barriers and tensor memory are there (the copies do not wait for the other warps)
+  Segment next;
+  constexpr int WALK = sizeof(Walk) / 4, BEGIN = WALK + sizeof(Segment) / 4 + 2;
+  static_assert(BEGIN * 4 <= 128, "as laid out");
+  int* begin = reinterpret_cast<int*>(smem + C::BEGIN_OFFSET);  // Walk, Segment, tiles, any; lengths [32]
+  if (warp == kCodeWarp) {
+    walk_start(p, walk);
+    const int tiles = walk.left;
+    const bool first = walk_next<C::CC>(p, walk, next);
+    if (lane == 0) {
+#pragma unroll
+      for (int i = 0; i < WALK; ++i) begin[i] = reinterpret_cast<const int*>(&walk)[i];
+#pragma unroll
+      for (int i = WALK; i < BEGIN - 2; ++i) begin[i] = reinterpret_cast<const int*>(&next)[i - WALK];
+      begin[BEGIN - 2] = tiles;
+      begin[BEGIN - 1] = first;
+    }
+    begin[32 + lane] = walk.lens;
+    __syncwarp();
+  }
+  // the barriers and tensor memory are there (the copies do not wait for the other warps)
+  if (copies) {
+    named_bar_sync(5, 3 * 32);
+    named_bar_arrive(4, C::THREADS);
+  } else {
     named_bar_sync(4, C::THREADS);
     tmem_fence_after();
   }
+#pragma unroll
+  for (int i = 0; i < WALK; ++i) reinterpret_cast<int*>(&walk)[i] = begin[i];
+#pragma unroll
+  for (int i = WALK; i < BEGIN - 2; ++i) reinterpret_cast<int*>(&next)[i - WALK] = begin[i];
+  walk.lens = begin[32 + lane];
+  const int share_tiles = begin[BEGIN - 2];
+  bool any = begin[BEGIN - 1] != 0;  // next is a segment
+  Segment seg = next;
   // the first segment's query terms, by all who have nothing to do yet
-  Segment next;
-  bool any = false;
   if (warp < kCodeWarp) {
-    Walk begin = walk;
-    if (walk_next<C::CC>(p, begin, next)) {
-      any = true;
+    if (any) {
       write_query_terms<C>(p, next, smem + C::Q_OFFSET, smem + C::QSF_OFFSET, reinterpret_cast<float*>(smem + C::COL_OFFSET),
                            warp, 12, lane);
       fence_proxy_async_smem();
     }
-    if (warp >= kEndWarp) {
-      walk = begin;
+    if (warp >= kEndWarp)
       named_bar_sync(7, 12 * 32);
-    } else {
+    else
       named_bar_arrive(7, 12 * 32);
-    }
   }
   const uint32_t quarter = (uint32_t)(warp & 3) << 21;  // this warp's lanes of tensor memory
 
@@ -517,7 +536,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     bool waited = !early, stop = false;
     uint32_t err_bits = 0;
     const uint64_t policy = l2_evict_first_policy();
-    any = walk_next<C::CC>(p, walk, next);
     auto page_of = [&](const Segment& s, int i) {
       const int t = s.t_base + i * kFp4Tile + lane * 16;
       return t < s.thi ? __ldg(p.block_tables + (size_t)s.b * p.max_pages + t / p.page_size) : -1;
@@ -609,7 +627,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     float* top_of = reinterpret_cast<float*>(smem + C::TOP_OFFSET);  // [4][CC]
     int it = 0;
 #pragma unroll 1
-    for (int sg = 0; walk_next<C::CC>(p, walk, seg); ++sg) {
+    for (int sg = 0; any; ++sg, any = walk_next<C::CC>(p, walk, seg)) {
       if (seg.bad && tid == 0) atomicOr(p.err, kErrBadSeqLen);
       await(&q_full[sg & 1], sg >> 1);
       const float* col_mul = reinterpret_cast<const float*>(smem + C::COL_OFFSET) + (sg & 1) * C::CC;
@@ -732,7 +750,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     const int j = warp - kSfWarp, row = j * 32 + lane;
     int it = 0;
 #pragma unroll 1
-    for (int sg = 0; walk_next<C::CC>(p, walk, seg); ++sg) {
+    for (int sg = 0; any; ++sg, any = walk_next<C::CC>(p, walk, seg)) {
 #pragma unroll 1
       for (int u = 0; u < (C::KVS ? 1 : 2) * seg.tiles; ++u) {
         const bool v = C::KVS || (u & 1) != 0;
@@ -946,8 +964,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
       if (sg >= 0) {
         // ---- segment sg's results
         await(&l_full[sg & 1], sg >> 1);
-        await(o_full, sg);
-        tmem_fence_after();
         const float* sum_of = reinterpret_cast<const float*>(smem + C::SUM_OFFSET) + (sg & 1) * 5 * C::CC;
         uint32_t* poison = poison_of + (sg % kPoison) * C::CC;
         const int slot = blockIdx.x * 2 + (seg.piece == 0 ? 1 : 0);
@@ -966,6 +982,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
                   l != 0.f ? (sum_of[4 * C::CC + c] + __log2f(l)) * 0.69314718055994530942f : -INFINITY;
           }
         }
+        await(o_full, sg);
+        tmem_fence_after();
         // lane l of quarter w has dim 32 w + l of each chunk
 #pragma unroll 1
         for (int k = 0; k < CH; ++k) {
