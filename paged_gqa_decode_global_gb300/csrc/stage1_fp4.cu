@@ -140,7 +140,6 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t phase) {
 // What a ring slot's word says of its tile, beside the 16-token blocks that have a page (bits 0-7).
 constexpr uint32_t kTileFirst = 0x100u, kTileLast = 0x200u, kTileOdd = 0x400u;  // of its segment; an odd one
 
-constexpr uint32_t kNoRow = 0xffffffffu;
 // Segments whose NaN marks are kept: a ring's tiles (up to 10) may be of as many,
 // and the marks are cleared up to 3 segments late.
 constexpr int kPoison = 16;
@@ -223,7 +222,7 @@ __device__ __forceinline__ void walk_start(const Fp4Params& p, Walk& w) {
     walk_load(p, w, c);
     const int n = walk_count(p, w);
     int upto = n;  // tiles of the requests up to this lane's
-#pragma unroll 1
+#pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
       const int o = __shfl_up_sync(kFullMask, upto, m);
       if (lane >= m) upto += o;
@@ -536,11 +535,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     bool waited = !early, stop = false;
     uint32_t err_bits = 0;
     const uint64_t policy = l2_evict_first_policy();
+    int page = -1, in_page = 0, rows = -1;
     auto page_of = [&](const Segment& s, int i) {
-      const int t = s.t_base + i * kFp4Tile + lane * 16;
-      return t < s.thi ? __ldg(p.block_tables + (size_t)s.b * p.max_pages + t / p.page_size) : -1;
+      const int t = s.t_base + i * kFp4Tile + lane * 16, at = t / p.page_size;
+      in_page = t - at * p.page_size + s.g * p.page_size;
+      page = t < s.thi ? __ldg(p.block_tables + (size_t)s.b * p.max_pages + at) : -1;
     };
-    int page = any ? page_of(next, 0) : -1, rows = -1;
+    if (any) page_of(next, 0);
     int it = 0;  // tiles whose copies went out
 #pragma unroll 1
     for (uint32_t odd = 0; any && !stop; odd ^= kTileOdd) {
@@ -552,10 +553,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
           const int t = seg.t_base + i * kFp4Tile + lane * 16;
           const bool here = (unsigned)page < (unsigned)p.num_pages;
           if (t < seg.thi && !here) err_bits |= kErrBadPage;
-          rows = t < seg.thi && here ? (page * p.num_kv_heads + seg.g) * p.page_size + t % p.page_size : -1;
-          page = -1;
+          rows = t < seg.thi && here ? page * p.num_kv_heads * p.page_size + in_page : -1;
           const bool on = i + 4 < seg.tiles;
-          if (on || any) page = page_of(on ? seg : next, on ? i + 4 : 0);
+          if (on || any) page_of(on ? seg : next, on ? i + 4 : 0);
         }
         const int row0 = __shfl_sync(kFullMask, rows, (i & 3) * 8 + (lane & 7));
         const uint32_t bits = __ballot_sync(kFullMask, row0 >= 0) & 0xffu;
@@ -587,8 +587,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
                 mbar_arrive(&full[st]);
             }
             __syncwarp();
-            if (lane < 8 && ((part >> lane) & 1u))
-              tma_load_4d(item + lane * 16 * (C::D / 2), v ? &p.vmap : &p.kmap, 0, 0, 0, row0 / 8, &full[st], policy);
+            // (one lane for all: eight lanes' take turns at ~130 cycles each)
+            int at[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) at[k] = __shfl_sync(kFullMask, row0, k);
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                if ((part >> k) & 1u)
+                  tma_load_4d(item + k * 16 * (C::D / 2), v ? &p.vmap : &p.kmap, 0, 0, 0, at[k] / 8, &full[st], policy);
+            }
+            __syncwarp();
           } else {
             // 16 bytes a lane (as bulk copies these would be half of all copies)
             constexpr int LANES = C::ROW_SF;  // 16-byte pieces of 16 tokens' scales
@@ -944,17 +953,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
           await(qk_done, sg);
         }
         tmem_fence_after();
-#pragma unroll 1
-        for (int k0 = 0; k0 < C::KSTEPS; k0 += 2) {
-          uint32_t r8[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int row = lane + 32 * (i & 3);
-            r8[i] = row < C::N
-                        ? *reinterpret_cast<const uint32_t*>(smem + C::QSF_OFFSET + row * C::ROW_SF + (k0 + (i >> 2)) * 4)
-                        : 0u;
+        for (int k0 = 0; k0 < C::KSTEPS; k0 += 4) {
+          uint32_t x[16] = {};  // [64 dims][row group]
+#pragma unroll
+          for (int r = 0; r < C::N; r += 32) {
+            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+            if (r + 32 <= C::N || r + lane < C::N)
+              w = *reinterpret_cast<const uint4*>(smem + C::QSF_OFFSET + (r + lane) * C::ROW_SF + k0 * 4);
+            x[r / 32] = w.x;
+            x[4 + r / 32] = w.y;
+            x[8 + r / 32] = w.z;
+            x[12 + r / 32] = w.w;
           }
-          tmem_st(kTmemSfq + quarter + k0 * 4, r8);
+          tmem_st(kTmemSfq + quarter + k0 * 4, x);
         }
         tmem_wait_st();
         tmem_fence_before();
@@ -969,42 +981,58 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
         const int slot = blockIdx.x * 2 + (seg.piece == 0 ? 1 : 0);
         // 0: no attended token, so zeros, whatever the sums hold. (Times 2^v_exp last: over a sum of 2^80 it would be subnormal.)
         float mul[C::CC];
-        uint32_t row[C::CC];  // of the output; invalid columns: none
-        {
-          Pair col(seg);
 #pragma unroll
-          for (int c = 0; c < C::CC; ++c, col.next(p)) {
-            const float l = (sum_of[c] + sum_of[C::CC + c]) + (sum_of[2 * C::CC + c] + sum_of[3 * C::CC + c]);
-            mul[c] = l != 0.f ? 1.f / l : 0.f;
-            row[c] = col.valid(p) ? (uint32_t)col.row(p, seg) : kNoRow;
-            if (seg.pieces > 1 && wt == c && col.valid(p))
-              p.lse_part[slot * C::CC + c] =
-                  l != 0.f ? (sum_of[4 * C::CC + c] + __log2f(l)) * 0.69314718055994530942f : -INFINITY;
-          }
+        for (int c = 0; c < C::CC; ++c) {
+          const float l = (sum_of[c] + sum_of[C::CC + c]) + (sum_of[2 * C::CC + c] + sum_of[3 * C::CC + c]);
+          mul[c] = l != 0.f ? 1.f / l : 0.f;
+          if (seg.pieces > 1 && wt == c)
+            p.lse_part[slot * C::CC + c] =
+                l != 0.f ? (sum_of[4 * C::CC + c] + __log2f(l)) * 0.69314718055994530942f : -INFINITY;
         }
         await(o_full, sg);
         tmem_fence_after();
         // lane l of quarter w has dim 32 w + l of each chunk
-#pragma unroll 1
-        for (int k = 0; k < CH; ++k) {
-          uint32_t o[8];
-          tmem_ld(o, kTmemO + k * 16 + quarter);
+        float x[CH][C::CC];
+        uint32_t marks = 0u;
+        {
+          uint32_t o[CH][8];
+#pragma unroll
+          for (int k = 0; k < CH; ++k) tmem_ld(o[k], kTmemO + k * 16 + quarter);
           tmem_wait_ld();
-          const int dim = k * 128 + we * 32 + lane;
+          tmem_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(o_empty);
 #pragma unroll
           for (int c = 0; c < C::CC; ++c) {
-            float x = mul[c] != 0.f ? __uint_as_float(o[c]) * mul[c] * p.v_mul : 0.f;
-            if ((poison[c] >> (dim >> 4)) & 1u) x = NAN;
-            if (row[c] == kNoRow) continue;
-            if (seg.pieces == 1)
-              reinterpret_cast<__nv_bfloat16*>(p.out)[(size_t)row[c] * C::D + dim] = __float2bfloat16_rn(x);
-            else
-              p.o_part[((size_t)slot * C::CC + c) * C::D + dim] = x;
+            marks |= poison[c];
+#pragma unroll
+            for (int k = 0; k < CH; ++k) x[k][c] = mul[c] != 0.f ? __uint_as_float(o[k][c]) * mul[c] * p.v_mul : 0.f;
           }
         }
-        tmem_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(o_empty);
+        const int dim = we * 32 + lane;
+        if (marks) {
+#pragma unroll
+          for (int c = 0; c < C::CC; ++c)
+#pragma unroll
+            for (int k = 0; k < CH; ++k)
+              if ((poison[c] >> ((k * 128 + dim) >> 4)) & 1u) x[k][c] = NAN;
+        }
+        if (seg.pieces > 1) {
+          float* to = p.o_part + (size_t)slot * (C::CC * C::D) + dim;
+#pragma unroll
+          for (int c = 0; c < C::CC; ++c)
+#pragma unroll
+            for (int k = 0; k < CH; ++k) to[c * C::D + k * 128] = x[k][c];
+        } else {
+          Pair col(seg);
+#pragma unroll
+          for (int c = 0; c < C::CC; ++c, col.next(p)) {
+            if (!col.valid(p)) break;
+            __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(p.out) + col.row(p, seg) * C::D + dim;
+#pragma unroll
+            for (int k = 0; k < CH; ++k) to[k * 128] = __float2bfloat16_rn(x[k][c]);
+          }
+        }
         if (seg.pieces > 1) __threadfence();
         named_bar_sync(3, 128);
         if (lane == 0) mbar_arrive(&l_empty[sg & 1]);
@@ -1017,34 +1045,43 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
           if (*ticket == (uint32_t)seg.pieces - 1) {
             __threadfence();
             if (wt == 0) p.counters[seg.first_share] = 0u;
-            Pair col(seg);
+            // a warp a column; piece q lies in slot 2 (first_share + q), the first one in the next
+            constexpr int V4 = C::D / 128;  // float4s of a lane
+            auto slot_of = [&](int q) { return (size_t)((seg.first_share + q) * 2 + (q == 0)) * C::CC; };
 #pragma unroll 1
-            for (int c = 0; c < C::CC && col.valid(p); ++c, col.next(p)) {
-              const float* lse = p.lse_part + c;
-              // piece q lies in slot 2 (first_share + q), the first one in the next
+            for (int c = we; c < C::CC; c += 4) {
+              const int at = seg.head + c, j = at / p.group + seg.token;
+              if (j >= p.query_tokens) break;
+              const size_t row = ((size_t)seg.b * p.query_tokens + j) * p.num_q_heads + (size_t)seg.g * p.group + at % p.group;
               float M = -INFINITY;
-#pragma unroll 4
-              for (int q = 0; q < seg.pieces; ++q)
-                M = fmaxf(M, __ldcg(lse + ((seg.first_share + q) * 2 + (q == 0)) * C::CC));
-              float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+              for (int q = lane; q < seg.pieces; q += 32) M = fmaxf(M, __ldcg(p.lse_part + slot_of(q) + c));
+#pragma unroll
+              for (int m = 16; m; m >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, m));
+              float4 acc[V4];
+#pragma unroll
+              for (int k = 0; k < V4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
               float w_sum = 0.f;
-              if (wt < C::D / 4) {
-#pragma unroll 4
-                for (int q = 0; q < seg.pieces; ++q) {
-                  const size_t at = ((size_t)(seg.first_share + q) * 2 + (q == 0)) * C::CC;
-                  const float l = __ldcg(lse + at);
-                  const float4 x = __ldcg(reinterpret_cast<const float4*>(p.o_part + (at + c) * C::D) + wt);
-                  const float w = l == -INFINITY ? 0.f : ex2((l - M) * 1.4426950408889634f);
-                  w_sum += w;
-                  acc.x = fmaf(w, x.x, acc.x);
-                  acc.y = fmaf(w, x.y, acc.y);
-                  acc.z = fmaf(w, x.z, acc.z);
-                  acc.w = fmaf(w, x.w, acc.w);
+#pragma unroll 2
+              for (int q = 0; q < seg.pieces; ++q) {
+                const float l = __ldcg(p.lse_part + slot_of(q) + c);
+                const float4* o = reinterpret_cast<const float4*>(p.o_part + (slot_of(q) + c) * C::D) + lane;
+                const float w = l == -INFINITY ? 0.f : ex2((l - M) * 1.4426950408889634f);
+                w_sum += w;
+#pragma unroll
+                for (int k = 0; k < V4; ++k) {
+                  const float4 y = __ldcg(o + k * 32);
+                  acc[k].x = fmaf(w, y.x, acc[k].x);
+                  acc[k].y = fmaf(w, y.y, acc[k].y);
+                  acc[k].z = fmaf(w, y.z, acc[k].z);
+                  acc[k].w = fmaf(w, y.w, acc[k].w);
                 }
-                const float inv = w_sum != 0.f ? 1.f / w_sum : 0.f;
-                reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + col.row(p, seg) * C::D)[wt] =
-                    make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
               }
+              const float inv = w_sum != 0.f ? 1.f / w_sum : 0.f;
+              uint2* to = reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + row * C::D) + lane;
+#pragma unroll
+              for (int k = 0; k < V4; ++k)
+                to[k * 32] = make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv), pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
             }
           }
         }
