@@ -55,7 +55,9 @@ struct Fp4Cfg {
   static constexpr int BAR_OFFSET = (VALID_OFFSET + (NK + NV) * 4 + 7) / 8 * 8;
   static constexpr int NUM_BARS = 3 * (NK + NV) + 19;
   static constexpr int SMEM_BYTES = BAR_OFFSET + NUM_BARS * 8 + 16 + 1024;  // (+ 1 KiB to start on a 1024-byte boundary)
-  static constexpr int WARPS = 20;
+  // d 512 has the longer products, d 256 more copies for them
+  static constexpr int SCALE_WARPS = D == 256 ? 2 : 1, LANES = D == 256 ? 1 : 2;
+  static constexpr int WARPS = 15 + SCALE_WARPS + 2 * LANES;
   static constexpr int THREADS = 32 * WARPS;
   // what a share leaves to be joined: its first and its last unit's piece
   static constexpr int PIECE_FLOATS = CC * D;

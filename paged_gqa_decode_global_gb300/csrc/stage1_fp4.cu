@@ -34,9 +34,10 @@
 //
 // Roles: warps 0-3 softmax (a lane a token); 4-7 put a tile's scales in tcgen05.cp's
 // order; 8-11 write the next unit's query terms, read a unit's sums and join pieces;
-// 12, 13 copy codes (TMA), 14 scales (cp.async); one lane each of 15 issues the
-// scores, of 16 and 17 V^T, of 18 and 19 the sums (a look at a barrier takes 60 to 150 cycles, and
-// one lane that does all this spends most of them looking).
+// then two that copy codes (TMA), one or two that copy scales (cp.async), and warps of
+// which one lane issues the scores, V^T (one or two) and the sums (as many): a look at
+// a barrier takes 60 to 150 cycles, and one lane that does all this spends most of
+// them looking. (Warps 5 to a quarter of the SM at most, for 96 registers a thread.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -393,12 +394,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
   // one arrival: the products' commits
   uint64_t* vt_empty = ready + RINGS;   // [2] a chunk of V^T used
   uint64_t* qk_done = vt_empty + 2;     // a segment's scores all computed
-  // two: both of V^T's buffers' products' commits
+  // those of every lane that issues the sums
   uint64_t* p_empty = qk_done + 1;      // [2] P used: the tile is in the sums
-  // or a commit, and an arrival of the same lane (which orders what it has seen of others)
+  // two: a commit, and an arrival of the same lane (which orders what it has seen of others)
   uint64_t* vt_full = p_empty + 2;      // [2] a chunk of V^T there
   uint64_t* s_full = vt_full + 2;       // scores computed
-  // four: both of both buffers'
+  // both of every such lane
   uint64_t* o_full = s_full + 1;        // a segment's sums complete
   // four warps
   uint64_t* s_empty = o_full + 1;       // scores read
@@ -412,9 +413,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
   volatile uint32_t* valid = reinterpret_cast<uint32_t*>(smem + C::VALID_OFFSET);  // [RINGS]
   volatile uint32_t* tile_of = reinterpret_cast<uint32_t*>(smem + C::TILE_OFFSET);      // [2] first, last: by P buffer
   volatile uint32_t* blocks_of = reinterpret_cast<uint32_t*>(smem + C::BLOCKS_OFFSET);  // of the scores' tile
-  constexpr int kSfWarp = 4, kEndWarp = 8, kCodeWarp = 12, kScaleWarp = 14, kScoreWarp = 15, kWideWarp = 16, kSumWarp = 18;
+  constexpr int SW = C::SCALE_WARPS;
+  constexpr int kSfWarp = 4, kEndWarp = 8, kCodeWarp = 12, kScaleWarp = 14, kScoreWarp = kScaleWarp + C::SCALE_WARPS,
+                kWideWarp = kScoreWarp + 1, kSumWarp = kWideWarp + C::LANES;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const bool copies = warp >= kCodeWarp && warp <= kScaleWarp;
+  const bool copies = warp >= kCodeWarp && warp < kScoreWarp;
   const bool early = p.early_kv != 0 && copies;
   uint32_t* poison_of = reinterpret_cast<uint32_t*>(smem + C::POISON_OFFSET);  // [kPoison][CC], by segment
 
@@ -426,7 +429,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     for (int i = lane; i < C::NUM_BARS; i += 32) {
       const int r = i - 3 * RINGS;
       // full: the codes' byte count (K = V: two warps') and every lane's scales; empty: the products that read the slot
-      mbar_init(&full[i], i < RINGS ? (C::KVS ? 34 : 33) : i < 2 * RINGS ? (C::KVS ? 3 : i - RINGS < C::NK ? 1 : 2) : r < 0 ? 4 : r < 3 ? 1 : r < 8 ? 2 : 4);
+      mbar_init(&full[i], i < RINGS       ? (C::KVS ? 2 + 32 * SW : 33)
+                          : i < 2 * RINGS ? (C::KVS ? 1 + C::LANES : i - RINGS < C::NK ? 1 : C::LANES)
+                          : r < 0         ? 4
+                          : r < 3         ? 1
+                          : r < 5         ? C::LANES
+                          : r < 8         ? 2
+                          : r < 9         ? 2 * C::LANES
+                                          : 4);
     }
     fence_barrier_init();
     __syncwarp();
@@ -488,7 +498,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
   }
   // the barriers and tensor memory are there (the copies do not wait for the other warps)
   if (copies) {
-    named_bar_sync(5, 3 * 32);
+    named_bar_sync(5, (2 + SW) * 32);
     named_bar_arrive(4, C::THREADS);
   } else {
     named_bar_sync(4, C::THREADS);
@@ -531,7 +541,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     // ---- copies, four tiles' page ids ahead (one tile ahead, their latency bound
     // the kernel: 4 x 32768 tokens 77 -> 62 us): lane l has the 16 tokens 16 l .. of
     // four tiles
-    const int mine = warp - kCodeWarp;  // 0: K's codes, 1: V's (K = V: the lower and the upper half), 2: scales
+    const int mine = warp - kCodeWarp;  // 0: K's codes, 1: V's (K = V: the lower and the upper half), 2: scales (or 2: K's, 3: V's)
+    const int v0 = C::KVS ? 0 : mine < 2 ? mine : SW == 2 ? mine - 2 : 0, v1 = !C::KVS && SW == 1 && mine == 2 ? 2 : v0 + 1;
     bool waited = !early, stop = false;
     uint32_t err_bits = 0;
     const uint64_t policy = l2_evict_first_policy();
@@ -568,8 +579,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
           waited = true;
         }
 #pragma unroll 1
-        for (int v = 0; v < (C::KVS ? 1 : 2); ++v) {
-          if (!C::KVS && mine == 1 - v) continue;
+        for (int v = v0; v < v1; ++v) {
           const int n = v ? C::NV : C::NK, round = it / n, st = (v ? C::NK : 0) + it - round * n;
           if (round > 0 && __any_sync(kFullMask, !wait_for(&empty[st], round - 1))) {
             err_bits |= kErrTimeout;
@@ -600,12 +610,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
             __syncwarp();
           } else {
             // 16 bytes a lane (as bulk copies these would be half of all copies)
-            constexpr int LANES = C::ROW_SF;  // 16-byte pieces of 16 tokens' scales
+            constexpr int LANES = C::ROW_SF, EACH = C::KVS ? 8 / SW : 8;  // 16-byte pieces of 16 tokens' scales; a warp's 16s
+            const int k0 = C::KVS && SW == 2 ? (mine - 2) * EACH : 0;
             const uint8_t* sf = (v ? p.v_sf : p.k_sf) + (lane % LANES) * 16;
-            uint8_t* to = item + C::CODE_BYTES + lane * 16;
+            uint8_t* to = item + C::CODE_BYTES + lane * 16 + k0 * 16 * C::ROW_SF;
 #pragma unroll
-            for (int k = 0; k < 8; k += 32 / LANES) {
-              const int at = k + lane / LANES;  // the 16 tokens this lane copies a piece of
+            for (int k = 0; k < EACH; k += 32 / LANES) {
+              const int at = k0 + k + lane / LANES;  // the 16 tokens this lane copies a piece of
               const int row = __shfl_sync(kFullMask, row0, at);
               if (row >= 0) cp_async16(to + k * 16 * C::ROW_SF, sf + (size_t)row * C::ROW_SF);
             }
@@ -620,7 +631,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     const unsigned long long deadline = global_timer_ns() + kWaitTimeoutNs;
     for (int s = lane; s < RINGS; s += 32) {
       const int n = s < C::NK ? C::NK : C::NV, at = s < C::NK ? s : s - C::NK;
-      if (at >= it || (!C::KVS && mine != 2 && (s >= C::NK) != (mine == 1))) continue;
+      if (at >= it || (!C::KVS && ((s >= C::NK) < v0 || (s >= C::NK) >= v1))) continue;
       const int last = at + n * ((it - 1 - at) / n);
       if (!mbar_wait_until(&full[s], (last / n) & 1, deadline)) err_bits |= kErrTimeout;
     }
@@ -858,32 +869,33 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     }
     __syncwarp();
   } else if (warp >= kWideWarp && warp < kSumWarp) {
-    // ---- V^T = I V^T, 128 dims at a time: this lane's chunks are those of buffer c
+    // ---- V^T = I V^T, 128 dims at a time. Two lanes: one has the first buffer's chunks, one the second's.
     if (share_tiles > 0 && elect_one()) {
       constexpr uint32_t kDq = (1u << 7) | (1u << 10) | ((uint32_t)(kFp4Tile / 8) << 17) | (8u << 24);
       constexpr uint32_t kRows = desc_hi(C::SL * 1024), kEye = desc_hi(512, 64);
-      const uint32_t c = warp - kWideWarp, ring = smem_u32(smem) >> 4, eye = ring + (C::EYE_OFFSET >> 4);
-      const uint32_t to = kTmemVt + c * 128;
-      uint64_t *my_full = vt_full + c, *my_empty = vt_empty + c;
-      int i = 0, sv = C::KVS ? 0 : C::NK, round = 0, use = 0;  // the tile, its slot; chunks so far
+      const uint32_t me = warp - kWideWarp, ring = smem_u32(smem) >> 4, eye = ring + (C::EYE_OFFSET >> 4);
+      int i = 0, sv = C::KVS ? 0 : C::NK, round = 0, use = 0;  // the tile, its slot; uses of a buffer so far
       good = *tmem_at == 0;
 #pragma unroll 1
       for (; i < share_tiles && good; ++i) {
         if (!(good = wait_for(&ready[sv], round))) break;
-        const uint32_t item = ring + sv * (C::ITEM_BYTES >> 4) + c * 4, sf = item - c * 4 + (C::CODE_BYTES >> 4) + c * 64;
+        const uint32_t item = ring + sv * (C::ITEM_BYTES >> 4) + me * 4;
+        const uint32_t sf = ring + sv * (C::ITEM_BYTES >> 4) + (C::CODE_BYTES >> 4) + me * 64;
 #pragma unroll
-        for (int k = 0; k < CH / 2; ++k) {
-          if (use > 0 && !(good = good && wait_for(my_empty, use - 1))) break;
+        for (int k = 0; k < CH / C::LANES; ++k) {
+          // chunk me + k LANES, in buffer c
+          const uint32_t c = C::LANES == 2 ? me : k & 1, sfv = kTmemSfv + me * 8 + k * 8 * C::LANES, to = kTmemVt + c * 128;
+          const uint32_t v = item + (C::LANES == 2 ? k * 64 : (k >> 1) * 64 + (k & 1) * 4);
+          if (use > 0 && !(good = good && wait_for(&vt_empty[c], use - 1))) break;
           tmem_fence_after();
           // (the product that these scales' columns were for before is done: its chunk is used, or its buffer would not be free)
-          const uint32_t sfv = kTmemSfv + c * 8 + k * 16;
-          copy_scales(sfv, sf + k * 128);
-          copy_scales(sfv + 4, sf + k * 128 + 32);
-          mma_fp4<kEye, kRows, kDq>(to, eye, item + k * 64, kTmemSfi, sfv, false);
-          mma_fp4<kEye, kRows, kDq>(to, eye + 2, item + k * 64 + 2, kTmemSfi, sfv + 4, true);
-          mma_commit<1>(my_full);
-          mbar_arrive(my_full);
-          ++use;
+          copy_scales(sfv, sf + k * 64 * C::LANES);
+          copy_scales(sfv + 4, sf + k * 64 * C::LANES + 32);
+          mma_fp4<kEye, kRows, kDq>(to, eye, v, kTmemSfi, sfv, false);
+          mma_fp4<kEye, kRows, kDq>(to, eye + 2, v + 2, kTmemSfi, sfv + 4, true);
+          mma_commit<1>(&vt_full[c]);
+          mbar_arrive(&vt_full[c]);
+          if (C::LANES == 2 || (k & 1)) ++use;
         }
         mma_commit<1>(&empty[sv]);
         if (++sv == RINGS) {
@@ -891,7 +903,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
           ++round;
         }
       }
-      if (use > 0) wait_for(my_full, use - 1);
+      if (use > 0) wait_for(&vt_full[C::LANES == 2 ? me : 1], use - 1);
       if (!good) atomicOr(p.err, kErrTimeout);
     }
     __syncwarp();
@@ -900,9 +912,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     if (share_tiles > 0 && elect_one()) {
       constexpr uint32_t kPv = (1u << 4) | (2u << 7) | (2u << 10) | (2u << 17) | (8u << 24);  // tf32 -> fp32, 128 x 16
       constexpr uint32_t kP = desc_hi(0);  // (both 8-column groups of P are the same: the upper columns are not read)
-      const uint32_t c = warp - kSumWarp, from = kTmemVt + c * 128, to = kTmemO + c * 16;
+      const uint32_t me = warp - kSumWarp;
       const uint32_t p0 = (smem_u32(smem) + C::P_OFFSET) >> 4;
-      uint64_t *my_full = vt_full + c, *my_empty = vt_empty + c;
       int i = 0, use = 0;
 #pragma unroll 1
       for (; i < share_tiles && good; ++i) {
@@ -910,14 +921,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
         const uint32_t word = tile_of[i & 1], pa = p0 + (i & 1) * (C::P_BYTES >> 4);
         const bool more = (word & kTileFirst) == 0;
 #pragma unroll 1
-        for (int k = 0; k < CH / 2; ++k) {
-          if (!(good = wait_for(my_full, use))) break;
+        for (int k = 0; k < CH / C::LANES; ++k) {
+          const uint32_t c = C::LANES == 2 ? me : k & 1;
+          if (!(good = wait_for(&vt_full[c], use))) break;
           tmem_fence_after();
+          const uint32_t to = kTmemO + me * 16 + k * 16 * C::LANES, from = kTmemVt + c * 128;
 #pragma unroll
           for (int q = 0; q < 16; ++q)
-            mma_tf32<kP, kPv>(to + k * 32, from + q * 8, pa + (q >> 2) * 64 + (q & 3) * 2, more || q > 0);
-          mma_commit<1>(my_empty);
-          ++use;
+            mma_tf32<kP, kPv>(to, from + q * 8, pa + (q >> 2) * 64 + (q & 3) * 2, more || q > 0);
+          mma_commit<1>(&vt_empty[c]);
+          if (C::LANES == 2 || (k & 1)) ++use;
         }
         mma_commit<1>(&p_empty[i & 1]);
         if (word & kTileLast) {
@@ -925,7 +938,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
           mbar_arrive(o_full);
         }
       }
-      if (use > 0) wait_for(my_empty, use - 1);
+      if (use > 0) wait_for(&vt_empty[C::LANES == 2 ? me : 1], use - 1);
       if (!good) atomicOr(p.err, kErrTimeout);
     }
     __syncwarp();
