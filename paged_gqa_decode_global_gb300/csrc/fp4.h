@@ -35,6 +35,9 @@ struct Fp4Cfg {
   static constexpr int NK = KVS ? (D == 512 ? 5 : 10) : (D == 512 ? 2 : 4);
   static constexpr int NV = KVS ? 0 : (D == 512 ? 3 : 6);
   static constexpr int RING_BYTES = (NK + NV) * ITEM_BYTES;
+  // Segments told of at a time. Copies run ahead by a ring's tiles, which may be of as
+  // many segments, of one more to come, and of up to 3 whose results are not out yet.
+  static constexpr int SEGS = NK > 5 || NV > 5 ? 32 : 16;
   static constexpr int CHUNKS = D / 128;   // of 128 dims: V is widened and summed a chunk at a time
   static constexpr int Q_BYTES = N * D / 2;                       // a query's terms: codes like a tile's
   static constexpr int Q_OFFSET = RING_BYTES;                     // [2]: of this segment and the next
@@ -44,16 +47,17 @@ struct Fp4Cfg {
   static constexpr int EYE_BYTES = 128 * 64;
   static constexpr int QSF_OFFSET = EYE_OFFSET + EYE_BYTES;       // query terms' scales [N][D / 16]
   static constexpr int COL_OFFSET = QSF_OFFSET + N * ROW_SF;      // float [2][CC]: score scale of a column
-  static constexpr int POISON_OFFSET = COL_OFFSET + 2 * CC * 4;   // u32 [16][CC]: 16-dim blocks that are NaN
-  static constexpr int TOP_OFFSET = POISON_OFFSET + 16 * CC * 4;  // float [4][CC]: the softmax warps' maxima
+  static constexpr int POISON_OFFSET = COL_OFFSET + 2 * CC * 4;   // u32 [SEGS][CC]: 16-dim blocks that are NaN
+  static constexpr int TOP_OFFSET = POISON_OFFSET + SEGS * CC * 4; // float [4][CC]: the softmax warps' maxima
   static constexpr int SUM_OFFSET = TOP_OFFSET + 4 * CC * 4;      // float [2][5][CC]: their sums, and the references
   static constexpr int MISC_OFFSET = SUM_OFFSET + 2 * 5 * CC * 4; // u32: the join's ticket
   static constexpr int BLOCKS_OFFSET = MISC_OFFSET + 4;           // u32: the 16-token blocks that the scores' tile holds
   static constexpr int TILE_OFFSET = BLOCKS_OFFSET + 4;           // u32 [2]: of P's tiles
   static constexpr int BEGIN_OFFSET = TILE_OFFSET + 8;            // int [64]: where the share begins
-  static constexpr int VALID_OFFSET = BEGIN_OFFSET + 256;          // u32 [NK + NV]: what a slot's tile is (kTile...)
+  static constexpr int SEG_OFFSET = (BEGIN_OFFSET + 256 + 15) / 16 * 16;  // [SEGS] of 64 bytes
+  static constexpr int VALID_OFFSET = SEG_OFFSET + SEGS * 64;          // u32 [NK + NV]: what a slot's tile is (kTile...)
   static constexpr int BAR_OFFSET = (VALID_OFFSET + (NK + NV) * 4 + 7) / 8 * 8;
-  static constexpr int NUM_BARS = 3 * (NK + NV) + 19;
+  static constexpr int NUM_BARS = 3 * (NK + NV) + 19 + SEGS;
   static constexpr int SMEM_BYTES = BAR_OFFSET + NUM_BARS * 8 + 16 + 1024;  // (+ 1 KiB to start on a 1024-byte boundary)
   // d 512 has the longer products, d 256 more copies for them
   static constexpr int SCALE_WARPS = D == 256 ? 2 : 1, LANES = D == 256 ? 1 : 2;

@@ -141,10 +141,6 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t phase) {
 // What a ring slot's word says of its tile, beside the 16-token blocks that have a page (bits 0-7).
 constexpr uint32_t kTileFirst = 0x100u, kTileLast = 0x200u, kTileOdd = 0x400u;  // of its segment; an odd one
 
-// Segments whose NaN marks are kept: a ring's tiles (up to 10) may be of as many,
-// and the marks are cleared up to 3 segments late.
-constexpr int kPoison = 16;
-
 // A request's attended range, cut to what its block table holds.
 struct Span {
   int L, base, tiles;  // cached tokens; the first one attended, rounded down to 16; tiles from there (at least one)
@@ -160,7 +156,7 @@ struct Span {
 
 // The tiles of a share that belong to one unit. Its column c is the c-th
 // (token, head) pair from (token, head) on, token-major.
-struct Segment {
+struct alignas(16) Segment {
   int b, g, L, tiles;
   int t_base;    // first token of the first tile
   int tlo, thi;  // tokens of it that some column attends
@@ -408,7 +404,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
   uint64_t* o_empty = q_full + 2;       // a segment's sums read
   uint64_t* l_full = o_empty + 1;       // [2] a segment's probabilities' sums there
   uint64_t* l_empty = l_full + 2;       // [2] and read
-  static_assert(C::NUM_BARS == 3 * RINGS + 5 + 4 + 10, "as listed");
+  // one
+  uint64_t* seg_full = l_empty + 2;     // [SEGS] a segment told
+  static_assert(C::NUM_BARS == 3 * RINGS + 5 + 4 + 10 + C::SEGS, "as listed");
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(full + C::NUM_BARS);
   volatile uint32_t* valid = reinterpret_cast<uint32_t*>(smem + C::VALID_OFFSET);  // [RINGS]
   volatile uint32_t* tile_of = reinterpret_cast<uint32_t*>(smem + C::TILE_OFFSET);      // [2] first, last: by P buffer
@@ -419,7 +417,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool copies = warp >= kCodeWarp && warp < kScoreWarp;
   const bool early = p.early_kv != 0 && copies;
-  uint32_t* poison_of = reinterpret_cast<uint32_t*>(smem + C::POISON_OFFSET);  // [kPoison][CC], by segment
+  uint32_t* poison_of = reinterpret_cast<uint32_t*>(smem + C::POISON_OFFSET);  // [SEGS][CC], by segment
 
   if (warp == kCodeWarp) {
     if (lane == 0) {
@@ -436,7 +434,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
                           : r < 5         ? C::LANES
                           : r < 8         ? 2
                           : r < 9         ? 2 * C::LANES
-                                          : 4);
+                          : r < 19        ? 4
+                                          : 1);
     }
     fence_barrier_init();
     __syncwarp();
@@ -463,7 +462,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
       if (i < (C::N - USED) * C::ROW_SF / 16)
         *reinterpret_cast<uint4*>(smem + C::QSF_OFFSET + USED * C::ROW_SF + i * 16) = make_uint4(0u, 0u, 0u, 0u);
     }
-    for (int i = wt; i < kPoison * C::CC; i += 128) poison_of[i] = 0u;
+    for (int i = wt; i < C::SEGS * C::CC; i += 128) poison_of[i] = 0u;
   } else if (warp < kSfWarp && C::CC < 8) {  // P's unused columns
     for (int k = 0; k < 2; ++k)
       for (int i = lane; i < (8 - C::CC) * 8; i += 32)
@@ -474,24 +473,28 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     grid_dependency_wait();
     grid_launch_dependents();
   }
-  // One warp finds the share and its first segment (20 that did it side by side took
-  // 1.5 us instead of 1); what all lanes have of them goes round through shared memory.
+  // One warp finds the share and its segments, and tells all others through shared
+  // memory (20 that did it side by side took longer to begin, and the code of it was
+  // fetched anew by every role at every segment: ~2000 cycles each).
   Walk walk;
-  Segment next;
-  constexpr int WALK = sizeof(Walk) / 4, BEGIN = WALK + sizeof(Segment) / 4 + 2;
-  static_assert(BEGIN * 4 <= 128, "as laid out");
-  int* begin = reinterpret_cast<int*>(smem + C::BEGIN_OFFSET);  // Walk, Segment, tiles, any; lengths [32]
+  constexpr int WALK = sizeof(Walk) / 4;
+  static_assert(WALK + 1 <= 32, "as laid out");
+  int* begin = reinterpret_cast<int*>(smem + C::BEGIN_OFFSET);  // Walk; lengths [32]; tiles at 31
+  Segment* seg_of = reinterpret_cast<Segment*>(smem + C::SEG_OFFSET);  // [SEGS]
+  auto tell = [&](int sg, const Segment& s) {
+    if (lane == 0) {
+      seg_of[sg % C::SEGS] = s;
+      mbar_arrive(&seg_full[sg % C::SEGS]);
+    }
+  };
+  Segment seg;
   if (warp == kCodeWarp) {
     walk_start(p, walk);
-    const int tiles = walk.left;
-    const bool first = walk_next<C::CC>(p, walk, next);
+    if (lane == 0) begin[31] = walk.left;
+    if (walk_next<C::CC>(p, walk, seg)) tell(0, seg);
     if (lane == 0) {
 #pragma unroll
       for (int i = 0; i < WALK; ++i) begin[i] = reinterpret_cast<const int*>(&walk)[i];
-#pragma unroll
-      for (int i = WALK; i < BEGIN - 2; ++i) begin[i] = reinterpret_cast<const int*>(&next)[i - WALK];
-      begin[BEGIN - 2] = tiles;
-      begin[BEGIN - 1] = first;
     }
     begin[32 + lane] = walk.lens;
     __syncwarp();
@@ -504,18 +507,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     named_bar_sync(4, C::THREADS);
     tmem_fence_after();
   }
-#pragma unroll
-  for (int i = 0; i < WALK; ++i) reinterpret_cast<int*>(&walk)[i] = begin[i];
-#pragma unroll
-  for (int i = WALK; i < BEGIN - 2; ++i) reinterpret_cast<int*>(&next)[i - WALK] = begin[i];
-  walk.lens = begin[32 + lane];
-  const int share_tiles = begin[BEGIN - 2];
-  bool any = begin[BEGIN - 1] != 0;  // next is a segment
-  Segment seg = next;
+  const int share_tiles = begin[31];
+  bool any = share_tiles > 0;
+  if (any) seg = seg_of[0];
   // the first segment's query terms, by all who have nothing to do yet
   if (warp < kCodeWarp) {
     if (any) {
-      write_query_terms<C>(p, next, smem + C::Q_OFFSET, smem + C::QSF_OFFSET, reinterpret_cast<float*>(smem + C::COL_OFFSET),
+      write_query_terms<C>(p, seg, smem + C::Q_OFFSET, smem + C::QSF_OFFSET, reinterpret_cast<float*>(smem + C::COL_OFFSET),
                            warp, 12, lane);
       fence_proxy_async_smem();
     }
@@ -546,6 +544,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     bool waited = !early, stop = false;
     uint32_t err_bits = 0;
     const uint64_t policy = l2_evict_first_policy();
+    Segment next = seg;
+    if (warp != kCodeWarp) {
+#pragma unroll
+      for (int i = 0; i < WALK; ++i) reinterpret_cast<int*>(&walk)[i] = begin[i];
+      walk.lens = begin[32 + lane];
+    }
     int page = -1, in_page = 0, rows = -1;
     auto page_of = [&](const Segment& s, int i) {
       const int t = s.t_base + i * kFp4Tile + lane * 16, at = t / p.page_size;
@@ -555,9 +559,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     if (any) page_of(next, 0);
     int it = 0;  // tiles whose copies went out
 #pragma unroll 1
-    for (uint32_t odd = 0; any && !stop; odd ^= kTileOdd) {
+    for (int sg = 0; any && !stop; ++sg) {
+      const uint32_t odd = sg & 1 ? kTileOdd : 0u;
       seg = next;
       any = walk_next<C::CC>(p, walk, next);
+      if (any && warp == kCodeWarp) tell(sg + 1, next);
 #pragma unroll 1
       for (int i = 0; i < seg.tiles; ++i) {
         if ((i & 3) == 0) {
@@ -647,9 +653,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     float* top_of = reinterpret_cast<float*>(smem + C::TOP_OFFSET);  // [4][CC]
     int it = 0;
 #pragma unroll 1
-    for (int sg = 0; any; ++sg, any = walk_next<C::CC>(p, walk, seg)) {
-      if (seg.bad && tid == 0) atomicOr(p.err, kErrBadSeqLen);
+    for (int sg = 0; it < share_tiles; ++sg) {
       await(&q_full[sg & 1], sg >> 1);
+      seg = seg_of[sg % C::SEGS];
+      if (!good) seg.tiles = share_tiles - it;  // (as many turns as the other warps)
+      if (seg.bad && good && tid == 0) atomicOr(p.err, kErrBadSeqLen);
       const float* col_mul = reinterpret_cast<const float*>(smem + C::COL_OFFSET) + (sg & 1) * C::CC;
       const uint32_t reach = p.window > 0 ? p.window : 0x7fffffff;
       float ref[C::CC], sum[C::CC];
@@ -770,7 +778,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
     const int j = warp - kSfWarp, row = j * 32 + lane;
     int it = 0;
 #pragma unroll 1
-    for (int sg = 0; any; ++sg, any = walk_next<C::CC>(p, walk, seg)) {
+    for (int sg = 0; it < share_tiles; ++sg) {
+      await(&seg_full[sg % C::SEGS], sg / C::SEGS);
+      seg = seg_of[sg % C::SEGS];
+      if (!good) seg.tiles = share_tiles - it;
 #pragma unroll 1
       for (int u = 0; u < (C::KVS ? 1 : 2) * seg.tiles; ++u) {
         const bool v = C::KVS || (u & 1) != 0;
@@ -813,7 +824,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
             for (int c = 0; c < C::CC && col.valid(p); ++c, col.next(p)) {
               const int end = col.end(p, seg);
               if (t < end && (p.window == 0 || t >= end - p.window))
-                atomicOr(&poison_of[(sg % kPoison) * C::CC + c], C::KVS ? 0xffffffffu : blocks);
+                atomicOr(&poison_of[(sg % C::SEGS) * C::CC + c], C::KVS ? 0xffffffffu : blocks);
             }
           }
         }
@@ -952,9 +963,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
       for (int k = 0; k < 8; ++k) one[k] = 0x38383838u;  // e4m3 1.0
       tmem_st(kTmemSfi + quarter, one);
     }
+    int left = share_tiles;  // tiles of the segments to come
+    Segment next = seg;
 #pragma unroll 1
     for (int sg = -1; sg < 0 ? any : true; ++sg) {
+      any = left > 0;
       if (any) {
+        await(&seg_full[(sg + 1) % C::SEGS], (sg + 1) / C::SEGS);
+        if (named_bar_or(3, 128, !good)) break;  // (all of them or none)
+        next = seg_of[(sg + 1) % C::SEGS];
+        left -= next.tiles;
         // ---- segment sg + 1's terms (their buffer is free: the scores of segment sg - 1 are computed, as these warps
         // have seen), and their scales once segment sg's scores are computed
         if (sg >= 0) {
@@ -990,7 +1008,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
         // ---- segment sg's results
         await(&l_full[sg & 1], sg >> 1);
         const float* sum_of = reinterpret_cast<const float*>(smem + C::SUM_OFFSET) + (sg & 1) * 5 * C::CC;
-        uint32_t* poison = poison_of + (sg % kPoison) * C::CC;
+        uint32_t* poison = poison_of + (sg % C::SEGS) * C::CC;
         const int slot = blockIdx.x * 2 + (seg.piece == 0 ? 1 : 0);
         // 0: no attended token, so zeros, whatever the sums hold. (Times 2^v_exp last: over a sum of 2^80 it would be subnormal.)
         float mul[C::CC];
@@ -1101,7 +1119,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
       }
       if (!any) break;
       seg = next;
-      any = walk_next<C::CC>(p, walk, next);
     }
   }
   __syncthreads();
