@@ -135,7 +135,7 @@ __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity) {
   }
 }
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t phase) {
-  return mbar_test(bar, phase & 1) || wait_long(smem_u32(bar), phase & 1);
+  return __builtin_expect(mbar_test(bar, phase & 1), 1) || wait_long(smem_u32(bar), phase & 1);
 }
 
 // What a ring slot's word says of its tile, beside the 16-token blocks that have a page (bits 0-7).
@@ -660,16 +660,24 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
       if (seg.bad && good && tid == 0) atomicOr(p.err, kErrBadSeqLen);
       const float* col_mul = reinterpret_cast<const float*>(smem + C::COL_OFFSET) + (sg & 1) * C::CC;
       const uint32_t reach = p.window > 0 ? p.window : 0x7fffffff;
-      float ref[C::CC], sum[C::CC];
+      float ref[C::CC], top[C::CC], sum[C::CC];  // top: what a score may not exceed, 2^60 above the reference
       int newest[C::CC];  // position a column attends: it and the reach - 1 before it
       {
         Pair col(seg);
 #pragma unroll
         for (int c = 0; c < C::CC; ++c, col.next(p)) {
           newest[c] = col.valid(p) ? col.end(p, seg) - 1 : -1;
-          ref[c] = -INFINITY;
+          ref[c] = top[c] = -INFINITY;
           sum[c] = 0.f;
         }
+      }
+      // tokens that all columns attend (of columns without a query row nothing is used: what they hold is finite)
+      int whole_lo = 0, whole_hi = 0x7fffffff;
+#pragma unroll
+      for (int c = 0; c < C::CC; ++c) {
+        if (newest[c] < 0) continue;
+        whole_hi = min(whole_hi, newest[c] + 1);
+        if (p.window > 0) whole_lo = max(whole_lo, newest[c] + 1 - p.window);
       }
 #pragma unroll 1
       for (int i = 0; i < seg.tiles; ++i, ++it) {
@@ -699,30 +707,35 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
         tmem_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(s_empty);
+        if (!__all_sync(kFullMask, ok && t >= whole_lo && t < whole_hi)) {
+#pragma unroll
+          for (int c = 0; c < C::CC; ++c)
+            if (!ok || (uint32_t)(newest[c] - t) >= reach) s[c] = -INFINITY;
+        }
         bool above = false;
 #pragma unroll
-        for (int c = 0; c < C::CC; ++c) {
-          if (!ok || (uint32_t)(newest[c] - t) >= reach) s[c] = -INFINITY;
-          above = above || s[c] > ref[c] + kRefRange;
-        }
-        if (named_bar_or(2, 128, above)) {
+        for (int c = 0; c < C::CC; ++c) above = above || s[c] > top[c];
+        if (__builtin_expect(named_bar_or(2, 128, above), 0)) {
           // new references: the tile's maximum, where that is out of reach
 #pragma unroll
           for (int c = 0; c < C::CC; ++c) {
-            const int top = __reduce_max_sync(kFullMask, ordered(isnan(s[c]) ? -INFINITY : s[c]));
-            if (lane == 0) top_of[warp * C::CC + c] = unordered(top);
+            const int m = __reduce_max_sync(kFullMask, ordered(isnan(s[c]) ? -INFINITY : s[c]));
+            if (lane == 0) top_of[warp * C::CC + c] = unordered(m);
           }
           named_bar_sync(2, 128);
           float f[C::CC];
           bool held = false;
 #pragma unroll
           for (int c = 0; c < C::CC; ++c) {
-            const float top = fmaxf(fmaxf(top_of[c], top_of[C::CC + c]), fmaxf(top_of[2 * C::CC + c], top_of[3 * C::CC + c]));
-            const bool up = top > ref[c] + kRefRange;
-            f[c] = up && ref[c] != -INFINITY ? ex2(ref[c] - top) : 1.f;
+            const float m = fmaxf(fmaxf(top_of[c], top_of[C::CC + c]), fmaxf(top_of[2 * C::CC + c], top_of[3 * C::CC + c]));
+            const bool up = m > top[c];
+            f[c] = up && ref[c] != -INFINITY ? ex2(ref[c] - m) : 1.f;
             held = held || f[c] != 1.f;
             sum[c] *= f[c];
-            if (up) ref[c] = top;
+            if (up) {
+              ref[c] = m;
+              top[c] = m + kRefRange;
+            }
           }
           named_bar_sync(2, 128);  // the maxima may be written again
           if (held) {
@@ -807,7 +820,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
             if (!counts) x[k] = 0u;
             bad |= nan_scales(x[k]);
           }
-          if (bad != 0u) {
+          if (__builtin_expect(bad != 0u, 0)) {
             // A NaN block would spread over the unit matrix's zeros to other dims (and, of
             // a token that only some of several query tokens attend, to the others): it is
             // taken out and marked for the results it belongs to: its dims' or, as K's
@@ -1041,7 +1054,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
           }
         }
         const int dim = we * 32 + lane;
-        if (marks) {
+        if (__builtin_expect(marks != 0u, 0)) {
 #pragma unroll
           for (int c = 0; c < C::CC; ++c)
 #pragma unroll
