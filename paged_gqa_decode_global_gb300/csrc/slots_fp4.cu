@@ -4,9 +4,9 @@
 //
 // Bound: HBM, every row read and written once. A CTA takes a run of tokens of
 // K or of V: their rows' places in the pool are worked out once per token, then
-// every thread takes the same 8 elements of each token, so that a warp's loads
-// and stores of bf16 rows are 512 contiguous bytes; several tokens are in
-// flight a thread.
+// every thread takes the same elements of each token, 16 of a write and 8 of a
+// read, so that a warp's loads and stores of bf16 rows are 1024 and 512 contiguous
+// bytes; several tokens are in flight a thread.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -76,15 +76,36 @@ __device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
   return r;
 }
 
-// Eight bf16 of a block, the other eight held by the neighbouring lane: their codes, and the block's scale.
+// A block of 16 bf16: 32 bytes of one lane.
+struct Block {
+  uint32_t w[8];
+};
+template <bool WIDE>
+__device__ __forceinline__ Block load_block(const void* p) {
+  Block b;
+  if constexpr (WIDE) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(b.w[0]), "=r"(b.w[1]), "=r"(b.w[2]), "=r"(b.w[3]), "=r"(b.w[4]), "=r"(b.w[5]), "=r"(b.w[6]),
+                   "=r"(b.w[7])
+                 : "l"(p));
+  } else {
+    const uint4 x = load_once(p), y = load_once(static_cast<const uint8_t*>(p) + 16);
+    b.w[0] = x.x, b.w[1] = x.y, b.w[2] = x.z, b.w[3] = x.w;
+    b.w[4] = y.x, b.w[5] = y.y, b.w[6] = y.z, b.w[7] = y.w;
+  }
+  return b;
+}
+
+// Its codes, and its scale.
 // The quotients have to be right to the last bit only where a value is halfway
 // between two codes (a bf16 is 8 bits and a scale 4 wide: any other quotient is
 // 2^-9 away from there). x (1 / s) with the reciprocal rounded misses that for
 // scales of significand 15/8, so the reciprocal is taken in two parts; over all
 // e4m3 scales and all bf16 up to 7 scales the codes are those of the exact quotients.
-__device__ __forceinline__ uint32_t quantise8(const uint4& v, float down, uint8_t& scale) {
-  uint32_t m = larger2(larger2(larger2(v.x & 0x7fff7fffu, v.y), v.z), v.w);  // (as whole numbers: NaN is the largest)
-  m = __vmaxu2(m, __shfl_xor_sync(kFullMask, m, 1));
+__device__ __forceinline__ uint2 quantise16(Block v, float down, uint8_t& scale) {
+  uint32_t m = 0;  // (as whole numbers: NaN is the largest)
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = larger2(m, v.w[i]);
   m = max(m << 16, m & 0xffff0000u);
   const float want = __uint_as_float(m) * ((1.f / 6.f) * down);
   uint16_t s8;
@@ -93,41 +114,52 @@ __device__ __forceinline__ uint32_t quantise8(const uint4& v, float down, uint8_
   uint32_t s16;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s16) : "h"(s8));
   const float s = __half2float(__ushort_as_half((unsigned short)(s16 & 0xffffu)));
-  if (scale == 0 || scale == 0x7f) return 0u;  // zeros, or NaN whatever the codes
-  const float r = __frcp_rz(s), rest = fmaf(-r, s, 1.f) * r;  // (rest >= 0: a zero keeps its sign)
-  const uint64_t r_hi = f32x2(r * down, r * down), r_lo = f32x2(rest * down, rest * down);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  float y[8];
-  // a clamped scale: quotients may pass the range of fp32, and all past 6 give the largest code
-  const bool over = want > 448.f;
-  const float top = over ? 8.f * 448.f / down : 0.f;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  r = __uint_as_float(__float_as_uint(r) - 16u);  // below 1 / s by some last bits, so that
+  const float rest = fmaf(-r, s, 1.f) * r;        // rest > 0 and a zero keeps its sign
+  uint64_t r_hi = f32x2(r * down, r * down), r_lo = f32x2(rest * down, rest * down);
+  if (__builtin_expect(want > 448.f, 0)) {
+    // a clamped scale: quotients may pass the range of fp32, and all past 6 give the largest code
+    const float top = 8.f * 448.f / down;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float a = __uint_as_float(w[i] << 16), b = __uint_as_float(w[i] & 0xffff0000u);
-    if (over) {
-      a = fminf(fmaxf(a, -top), top);
-      b = fminf(fmaxf(b, -top), top);
+    for (int i = 0; i < 8; ++i) {
+      const float a = fminf(fmaxf(__uint_as_float(v.w[i] << 16), -top), top);
+      const float b = fminf(fmaxf(__uint_as_float(v.w[i] & 0xffff0000u), -top), top);
+      v.w[i] = (__float_as_uint(a) >> 16) | (__float_as_uint(b) & 0xffff0000u);  // (cut to a bf16: still above 6)
     }
-    uint64_t x = f32x2(a, b), t;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(x), "l"(r_lo));
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(t) : "l"(x), "l"(r_hi));
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(y[2 * i]), "=f"(y[2 * i + 1]) : "l"(t));
   }
-  uint32_t codes;
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
-      "mov.b32 %0, {a, b, c, d};\n\t}"
-      : "=r"(codes)
-      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
-  return codes;
+  if (scale == 0 || scale == 0x7f) r_hi = r_lo = 0;  // zeros, or NaN whatever the codes
+  uint32_t codes[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = v.w[h * 4 + i];
+      uint64_t x = f32x2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)), t;
+      asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(x), "l"(r_lo));
+      asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(t) : "l"(x), "l"(r_hi));
+      asm("mov.b64 {%0, %1}, %2;" : "=f"(y[2 * i]), "=f"(y[2 * i + 1]) : "l"(t));
+    }
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(codes[h])
+        : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+  }
+  const bool none = scale == 0 || scale == 0x7f;
+  return make_uint2(none ? 0u : codes[0], none ? 0u : codes[1]);
 }
 
-// Every thread of a warp takes part in quantise8's exchange: `lanes` (a token's
-// threads) and the tokens' conditions are the same for a whole warp.
+// WIDE: rows that begin on 32 bytes, a load a block. (16384 tokens of 4 x 512, K
+// and V, with their read-back: 63 us; with 8 elements a lane, two lanes finding the
+// scale that one does here, 142 instructions for 8 elements bound it: 74 us.)
+template <bool WIDE>
 __global__ void __launch_bounds__(kRowsThreads) write_fp4_kernel(const __grid_constant__ RowsParams p) {
   __shared__ Places places;
-  constexpr int kAhead = 8;  // tokens a thread has in flight: 128 bytes of loads
+  constexpr int kAhead = 4;  // tokens a thread has in flight: 128 bytes of loads
   grid_dependency_wait();
   grid_launch_dependents();
   const int tid = threadIdx.x, v = blockIdx.y;
@@ -138,33 +170,31 @@ __global__ void __launch_bounds__(kRowsThreads) write_fp4_kernel(const __grid_co
   uint8_t* pool = v ? p.pool[1] : p.pool[0];
   uint8_t* scale = static_cast<uint8_t*>(v ? p.scale[1] : p.scale[0]);
   const float down = v ? p.up[1] : p.up[0];
-  const int per_row = p.dim / 8, per_token = p.heads * per_row;
+  const int per_row = p.dim / kFp4Block, per_token = p.heads * per_row;
   const int lanes = min(per_token, kRowsThreads), together = kRowsThreads / lanes;
   const int sub = tid / lanes;
   if (sub >= together) return;
-  // (the lanes of a token past its last 8 elements go with the others)
-  for (int c0 = 0; c0 < per_token; c0 += lanes) {
-    const int c = c0 + tid - sub * lanes;
-    if (c >= per_token) continue;
+  for (int c = tid - sub * lanes; c < per_token; c += lanes) {
     const int h = c / per_row;
-    const uint16_t* src = in + (int64_t)first * stride + c * 8;
-    const long long to = (long long)h * (p.page_size - 1) * p.dim + (long long)c * 8;  // h P d + (c mod row) 8
+    const uint16_t* src = in + (int64_t)first * stride + c * kFp4Block;
+    const long long to = (long long)h * (p.page_size - 1) * per_row + c;  // blocks: h P + (c mod row)
     for (int t0 = sub; t0 < run; t0 += together * kAhead) {
-      uint4 a[kAhead];
+      Block a[kAhead];
+      long long at[kAhead];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         const int t = t0 + k * together;
-        if (t < run && places.at[t] >= 0) a[k] = load_once(src + t * stride);
+        at[k] = t < run ? places.at[t] : -1;
+        if (at[k] >= 0) a[k] = load_block<WIDE>(src + t * stride);
       }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        const int t = t0 + k * together;
-        if (t >= run || places.at[t] < 0) continue;
-        const long long at = places.at[t] + to;
+        if (at[k] < 0) continue;
+        const long long block = at[k] / kFp4Block + to;
         uint8_t s;
-        const uint32_t codes = quantise8(a[k], down, s);
-        *reinterpret_cast<uint32_t*>(pool + at / 2) = codes;
-        if ((tid & 1) == 0) scale[at / kFp4Block] = s;
+        const uint2 codes = quantise16(a[k], down, s);
+        reinterpret_cast<uint2*>(pool)[block] = codes;
+        scale[block] = s;
       }
     }
   }
@@ -347,7 +377,10 @@ pd_status write_fp4(const pd_layer_desc* layer, int32_t num_tokens, const void* 
   RowsParams p = {};
   const pd_status st = rows_params(layer, PD_KV_FP4_E2M1, num_tokens, k_in, v_in, k_stride, v_stride, slot_map, k_pool,
                                    v_pool, k_scale, v_scale, k_exp, v_exp, device_flags, true, &p);
-  return st != PD_OK ? st : launch_rows(p, layer->kv_shared != 0, write_fp4_kernel, stream);
+  if (st != PD_OK) return st;
+  const bool kvs = layer->kv_shared != 0;
+  const bool wide = aligned(k_in, 32) && k_stride % 16 == 0 && (kvs || (aligned(v_in, 32) && v_stride % 16 == 0));
+  return launch_rows(p, kvs, wide ? write_fp4_kernel<true> : write_fp4_kernel<false>, stream);
 }
 
 pd_status read_rows(const pd_layer_desc* layer, int kv_dtype, int32_t num_tokens, const int32_t* slot_map,
