@@ -214,7 +214,8 @@ pd_status paged_decode_qkv_norm_rope_write(const pd_layer_desc* layer, int32_t b
     return PD_ERR_INVALID_ARG;
   if (ly.page_size <= 0 || ly.num_pages <= 0 || ly.max_pages_per_seq <= 0) return PD_ERR_INVALID_ARG;
   if (ly.kv_shared != 0 && ly.kv_shared != 1) return PD_ERR_INVALID_ARG;
-  if (ly.kv_dtype != PD_KV_BF16) return ly.kv_dtype == PD_KV_FP8_E4M3 ? PD_ERR_UNSUPPORTED : PD_ERR_INVALID_ARG;
+  if (ly.kv_dtype != PD_KV_BF16)
+    return ly.kv_dtype == PD_KV_FP8_E4M3 || ly.kv_dtype == PD_KV_FP4_E2M1 ? PD_ERR_UNSUPPORTED : PD_ERR_INVALID_ARG;
   if (ly.head_dim != 256 && ly.head_dim != 512) return PD_ERR_UNSUPPORTED;
   if (batch < 0 || rotary_dim < 0 || rotary_dim % 2 || rotary_dim > ly.head_dim) return PD_ERR_INVALID_ARG;
   if (!(eps >= 0.f) || !std::isfinite(eps)) return PD_ERR_INVALID_ARG;
