@@ -692,14 +692,25 @@ pd_status paged_decode_read_slots_fp4(const pd_layer_desc* layer, int32_t num_to
                                       int64_t k_stride, int64_t v_stride, uint32_t* device_flags, void* stream);
 
 /*
- * Stage 1 over a 4-bit cache: as paged_decode_global / paged_decode_window
- * (plans from paged_decode_plan or paged_decode_plan_multi on a layer with
- * kv_dtype PD_KV_FP4_E2M1; paged_decode_merge follows). v_pool and v_scale of a
- * K=V layer are NULL or k_pool and k_scale. A query element enters the score
- * product as a sum of 4-bit terms that leaves out at most 2^-14 of the largest
- * of its 16; a query row with a NaN or an infinity gives a NaN row.
- * Probabilities are rounded to f16 relative to the largest so far of the tokens
- * one quarter of the kernel serves (below 2^-39 of it they vanish).
+ * Decode over a 4-bit cache: as paged_decode_global / paged_decode_window (plans
+ * from paged_decode_plan or paged_decode_plan_multi on a layer with kv_dtype
+ * PD_KV_FP4_E2M1, groups of 1..16, T of 1..256). One CTA an SM takes an equal
+ * share of all tokens and the last one to finish a row's pieces joins them, in an
+ * order that does not vary: out is complete after the call, and
+ * paged_decode_merge has nothing to do (num_splits is 1). The workspace, zeroed
+ * once after allocating it, holds counts that every launch leaves at zero; after
+ * PD_DEVFLAG_WAIT_TIMEOUT paged_decode_check_device_error sets them back.
+ * v_pool and v_scale of a K=V layer are NULL or k_pool and k_scale.
+ *
+ * A query element enters the score product as a sum of 4-bit terms that leaves
+ * out at most 2^-14 of the largest of its 16; a query row with a NaN or an
+ * infinity gives a NaN row. Probabilities are rounded to tf32 (2^-11 of
+ * themselves) relative to a reference that a score may pass by 2^60, sums are
+ * fp32. A NaN block of an attended V row makes its dims NaN, of a K row the whole
+ * output row.
+ * The plan is PD_ERR_UNSUPPORTED for head_dim 128, for batch * Hkv * column tiles
+ * * 128-token tiles of a block table's row of 2^30 and more, and for partial and
+ * shared-prefix plans.
  */
 pd_status paged_decode_global_fp4(const pd_plan* plan, const void* q, const void* k_pool, const void* v_pool,
                                   const void* k_scale, const void* v_scale, int32_t k_exp, int32_t v_exp,

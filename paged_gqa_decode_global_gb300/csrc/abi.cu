@@ -413,7 +413,6 @@ pd_status paged_decode_combine(int32_t num_parts, int32_t rows, int32_t head_dim
 
 pd_status paged_decode_check_device_error(const pd_plan* plan, void* workspace, size_t workspace_bytes,
                                           void* stream, uint32_t* flags) {
-  (void)plan;
   if (!workspace || workspace_bytes < sizeof(uint32_t)) return PD_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cudaStreamSynchronize(s) != cudaSuccess) return PD_ERR_CUDA;
@@ -421,7 +420,10 @@ pd_status paged_decode_check_device_error(const pd_plan* plan, void* workspace, 
   if (cudaMemcpy(&word, workspace, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return PD_ERR_CUDA;
   if (flags) *flags = word;
   if (word != 0) {
-    if (cudaMemset(workspace, 0, sizeof(word)) != cudaSuccess) return PD_ERR_CUDA;
+    // (a 4-bit decode that gave up may have left counts of its pieces behind the word)
+    const bool counts = plan && pd::plan_is_valid(plan) && plan->layer.kv_dtype == PD_KV_FP4_E2M1 &&
+                        workspace_bytes >= plan->workspace_bytes;
+    if (cudaMemset(workspace, 0, counts ? plan->lse_offset : sizeof(word)) != cudaSuccess) return PD_ERR_CUDA;
     return PD_ERR_DEVICE_FAULT;
   }
   return PD_OK;

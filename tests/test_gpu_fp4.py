@@ -5,9 +5,9 @@ Tolerance, per output element, from the kernel's roundings:
     2^-18 of the row's largest, where the last scales are e4m3's smallest), so a score is off by at most
     scale * sum_blocks (3.1e-5 max|q| + 2^-18 max|q_row|) sum|k|, and by fp32 sums of 512 products (2^-14 of sum|q k|
     at most, far less in fact: 512 roundings of 2^-24);
-  - probabilities, 2^15 times themselves relative to the largest so far, are rounded to f16: by 2^-11, and where f16 has
-    only its smallest step of 2^-24 left, by half of that, 2^-40 of the largest weight (at most 1) per token;
-    exponentials are within 2^-21;
+  - probabilities are rounded to tf32: by 2^-11 of themselves; below 2^-126 of their reference, which is at most 2^60
+    below the largest, they may vanish, which 2^-40 of the largest weight (at most 1) per token covers; exponentials are
+    within 2^-21;
   - the output is rounded to bf16 (2^-8).
 With e = the largest score error of a row and w the exact weights, weights are off by a factor of at most
 exp(2 e) (1 + 2^-10) and by 2^-40, so |out - exact| <= 2^-8 |exact| + (exp(2 e) (1 + 2^-10) - 1) * 2 * sum w |v| +
@@ -101,7 +101,7 @@ class Case:
             ka = k.abs().unflatten(-1, (-1, 16)).sum(-1)
             err = torch.einsum("thgb,nhb->thgn", lost, ka) + 512 * 2.0 ** -24 * torch.einsum(
                 "thgd,nhd->thgn", q.abs(), k.abs())
-            e = (err * self.scale).masked_fill(~seen, 0).amax(-1, keepdim=True)
+            e = (err * abs(self.scale)).masked_fill(~seen, 0).amax(-1, keepdim=True)  # |scale x| errs by |scale| |error of x|
             w = torch.softmax(s.masked_fill(~seen, -math.inf), -1)
             w = torch.nan_to_num(w, nan=0.0)  # a token that attends nothing
             o = torch.einsum("thgn,nhd->thgd", w, v)
