@@ -30,14 +30,14 @@ struct Fp4Cfg {
   static constexpr int CODE_BYTES = kFp4Tile * D / 2;
   static constexpr int SF_BYTES = kFp4Tile * ROW_SF;
   static constexpr int ITEM_BYTES = CODE_BYTES + SF_BYTES;
-  // K != V: a ring for K (a tile is done with once its scores are computed)
-  // and a longer one for V
-  static constexpr int NK = KVS ? (D == 512 ? 5 : 10) : (D == 512 ? 2 : 4);
-  static constexpr int NV = KVS ? 0 : (D == 512 ? 3 : 6);
+  // K != V: a ring for K (a tile is done with once its scores are computed) and
+  // one for V, at d 512 a longer one (windows of 1024 at d 256: 4 and 6 43.1 us, 5 and 5 39.3)
+  static constexpr int NK = KVS ? (D == 512 ? 5 : 10) : (D == 512 ? 2 : 5);
+  static constexpr int NV = KVS ? 0 : (D == 512 ? 3 : 5);
   static constexpr int RING_BYTES = (NK + NV) * ITEM_BYTES;
   // Segments told of at a time. Copies run ahead by a ring's tiles, which may be of as
   // many segments, of one more to come, and of up to 3 whose results are not out yet.
-  static constexpr int SEGS = NK > 5 || NV > 5 ? 32 : 16;
+  static constexpr int SEGS = D == 256 ? 32 : 16;
   static constexpr int CHUNKS = D / 128;   // of 128 dims: V is widened and summed a chunk at a time
   static constexpr int Q_BYTES = N * D / 2;                       // a query's terms: codes like a tile's
   static constexpr int Q_OFFSET = RING_BYTES;                     // [2]: of this segment and the next
