@@ -905,7 +905,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
         if (!(good = wait_for(&ready[sv], round))) break;
         const uint32_t item = ring + sv * (C::ITEM_BYTES >> 4) + me * 4;
         const uint32_t sf = ring + sv * (C::ITEM_BYTES >> 4) + (C::CODE_BYTES >> 4) + me * 64;
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < CH / C::LANES; ++k) {
           // chunk me + k LANES, in buffer c
           const uint32_t c = C::LANES == 2 ? me : k & 1, sfv = kTmemSfv + me * 8 + k * 8 * C::LANES, to = kTmemVt + c * 128;
