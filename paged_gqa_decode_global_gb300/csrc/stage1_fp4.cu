@@ -5,7 +5,14 @@
 // what it holds of one then is a piece, and the last CTA to leave its piece of a
 // unit joins them, in the pieces' order. Within a share every role runs on from
 // unit to unit without a gap (a CTA's start takes ~4 us; with a CTA a piece, 61
-// windows of 1024 tokens took 3.2 waves of them, 49 us instead of 27).
+// windows of 1024 tokens took 3.2 waves of them).
+//
+// Bound and measured (time of a launch in a CUDA graph; floor at the measured copy
+// rate): HBM where K and V differ at d 512 (4 x 32768 tokens 54 us, floor 45: a tile
+// takes its copies' 3170 cycles, start and end ~8 us); at K = V the chain of V^T's two
+// buffers (8 requests of 1K to 128K 66 us, floor 36: ~2600 cycles a tile, its copies
+// 1590); at d 256 the softmax warps (61 windows of 1024 38 us, floor 21); latency for
+// short lengths (8 x 1024 13.6 us).
 //
 // Mathematics: a cached element is e2m1(code) * e4m3(scale of its 16 dims) *
 // 2^exp. All three products of a tile of 128 tokens run on tcgen05, and no
@@ -537,7 +544,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
 
   if (copies) {
     // ---- copies, four tiles' page ids ahead (one tile ahead, their latency bound
-    // the kernel: 4 x 32768 tokens 77 -> 62 us): lane l has the 16 tokens 16 l .. of
+    // the kernel, then 77 instead of 62 us): lane l has the 16 tokens 16 l .. of
     // four tiles
     const int mine = warp - kCodeWarp;  // 0: K's codes, 1: V's (K = V: the lower and the upper half), 2: scales (or 2: K's, 3: V's)
     const int v0 = C::KVS ? 0 : mine < 2 ? mine : SW == 2 ? mine - 2 : 0, v1 = !C::KVS && SW == 1 && mine == 2 ? 2 : v0 + 1;

@@ -131,3 +131,20 @@ def test_extreme_exponents_of_v(v_exp):
     over = (got.double() - want).abs() - tol
     assert float(over.max()) <= 0
     assert float(values(c.vc, c.vs, v_exp).abs().max()) > 0
+
+
+@pytest.mark.parametrize("T,window", [(1, 0), (3, 0), (3, 20)])
+@pytest.mark.parametrize("sms", [1, 152])
+def test_nan_block_of_a_shared_pool(T, window, sms):
+    # as K it makes the whole output row NaN, of the query tokens that attend it and of no other
+    c = Case(16, 4, 512, [500, 300], T=T, window=window, kvs=True, seed=T)
+    step = c.step(sm_count=sms)
+    clean = c.run(step).clone()
+    at = 499 if T == 1 else 498  # attended by the tokens from position 498 on: not by the first of three
+    page = int(c.table[0, at // c.P])
+    c.ks[page, 2, at % c.P, 5] = 0x7f
+    got = c.run(step)
+    hit = torch.zeros(c.q.shape, dtype=torch.bool, device="cuda")
+    hit[0, (0 if T == 1 else 1):, 8:12] = True
+    assert torch.isnan(got[hit]).all()
+    assert torch.equal(got[~hit], clean[~hit])
