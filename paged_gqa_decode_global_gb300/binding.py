@@ -777,32 +777,39 @@ def _slot_rows(what: str, kv: int, desc, k_rows, v_rows, slot_map, k_pool, v_poo
     (n,), dev, heads, d = slot_map.shape, slot_map.get_device(), desc.num_kv_heads, desc.head_dim
     if desc.kv_dtype != kv:
         raise ValueError(f"{what}: the layer's kv_dtype is {desc.kv_dtype}, not {kv}")
-    bf16, u8, shared = torch.bfloat16, torch.uint8, desc.kv_shared
     _want(slot_map, "slot_map", torch.int32, (n,), dev)
-    pool, rows = (desc.num_pages, heads, desc.page_size, d), (n, heads, d)
+    pages, rows, scale_type = (desc.num_pages, heads, desc.page_size), (n, heads, d), None
     if kv == PD_KV_FP4_E2M1:
-        pool, scales = _fp4_shapes(desc)
-        kinds = (u8, u8)
+        pool_type = scale_type = torch.uint8
+        pool, scales = pages + (d // 2,), pages + (d // 16,)
+    elif kv == PD_KV_FP8_E4M3:
+        pool_type, scale_type = torch.uint8, torch.float32
+        pool, scales = pages + (d,), pages[:2]
     else:
-        scales, kinds = pool[:2], (u8, torch.float32) if kv == PD_KV_FP8_E4M3 else (bf16, None)
-    stride = [0, 0]
-    sides = (("k", k_rows, k_pool, k_scale),) if shared else (
-        ("k", k_rows, k_pool, k_scale), ("v", v_rows, v_pool, v_scale))
-    for i, (x, r, p, s) in enumerate(sides):
-        if r is None or p is None or (s is None and kinds[1] is not None):
-            raise ValueError(f"{what}: {x}'s rows, pool and (a quantised cache's) scales are wanted")
-        _want(p, x + "_pool", kinds[0], pool, dev)
-        if kinds[1] is not None:
-            _want(s, x + "_scale", kinds[1], scales, dev)
-        stride[i] = _token_rows(r, x + " rows", bf16, rows, dev)
-    if shared:
-        v_rows, v_pool, v_scale = None, None, None
+        pool_type, pool = torch.bfloat16, pages + (d,)
+    if k_rows is None or k_pool is None or (scale_type and k_scale is None):
+        raise ValueError(f"{what}: k's rows, pool and (a quantised cache's) scales are wanted")
+    _want(k_pool, "k_pool", pool_type, pool, dev)
+    k_stride, v_stride = _token_rows(k_rows, "k rows", torch.bfloat16, rows, dev), 0
+    k_at, v_at, v_pool_at, k_scale_at, v_scale_at = k_rows.data_ptr(), 0, 0, 0, 0
+    if scale_type:
+        _want(k_scale, "k_scale", scale_type, scales, dev)
+        k_scale_at = k_scale.data_ptr()
+    if not desc.kv_shared:
+        if v_rows is None or v_pool is None or (scale_type and v_scale is None):
+            raise ValueError(f"{what}: v's rows, pool and (a quantised cache's) scales are wanted")
+        _want(v_pool, "v_pool", pool_type, pool, dev)
+        v_stride = _token_rows(v_rows, "v rows", torch.bfloat16, rows, dev)
+        v_at, v_pool_at = v_rows.data_ptr(), v_pool.data_ptr()
+        if scale_type:
+            _want(v_scale, "v_scale", scale_type, scales, dev)
+            v_scale_at = v_scale.data_ptr()
     if not _is_word(device_flags, dev):
         _refuse_bytes("device_flags", device_flags, 4)
     raw = _launch_stream(stream, dev)
     args = _ROWS_ARGS(
-        ctypes.addressof(desc), n, k_exp, v_exp, 0, k_rows.data_ptr(), _ptr(v_rows) or 0, *stride, slot_map.data_ptr(),
-        k_pool.data_ptr(), _ptr(v_pool) or 0, _ptr(k_scale) or 0, _ptr(v_scale) or 0, device_flags.data_ptr(), raw)
+        ctypes.addressof(desc), n, k_exp, v_exp, 0, k_at, v_at, k_stride, v_stride, slot_map.data_ptr(),
+        k_pool.data_ptr(), v_pool_at, k_scale_at, v_scale_at, device_flags.data_ptr(), raw)
     lib = load_library()
     write = what == "paged_decode_write_slots_fp4"
     st = lib.paged_decode_write_slots_fp4_args(args) if write else lib.paged_decode_read_slots_args(args)
