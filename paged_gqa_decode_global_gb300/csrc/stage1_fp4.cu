@@ -667,14 +667,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
       if (seg.bad && good && tid == 0) atomicOr(p.err, kErrBadSeqLen);
       const float* col_mul = reinterpret_cast<const float*>(smem + C::COL_OFFSET) + (sg & 1) * C::CC;
       const uint32_t reach = p.window > 0 ? p.window : 0x7fffffff;
-      float ref[C::CC], top[C::CC], sum[C::CC];  // top: what a score may not exceed, 2^60 above the reference
+      float base[C::CC], top[C::CC], sum[C::CC];  // the reference (0 while there is none); what a score may not exceed
       int newest[C::CC];  // position a column attends: it and the reach - 1 before it
       {
         Pair col(seg);
 #pragma unroll
         for (int c = 0; c < C::CC; ++c, col.next(p)) {
           newest[c] = col.valid(p) ? col.end(p, seg) - 1 : -1;
-          ref[c] = top[c] = -INFINITY;
+          base[c] = 0.f;
+          top[c] = -INFINITY;
           sum[c] = 0.f;
         }
       }
@@ -736,11 +737,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
           for (int c = 0; c < C::CC; ++c) {
             const float m = fmaxf(fmaxf(top_of[c], top_of[C::CC + c]), fmaxf(top_of[2 * C::CC + c], top_of[3 * C::CC + c]));
             const bool up = m > top[c];
-            f[c] = up && ref[c] != -INFINITY ? ex2(ref[c] - m) : 1.f;
+            f[c] = up && top[c] != -INFINITY ? ex2(base[c] - m) : 1.f;
             held = held || f[c] != 1.f;
             sum[c] *= f[c];
             if (up) {
-              ref[c] = m;
+              base[c] = m;
               top[c] = m + kRefRange;
             }
           }
@@ -768,7 +769,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
         for (int c = 0; c < C::CC; ++c) {
           // rounded to tf32 here, to nearest (the product would cut it off); the sum takes what the product takes
           uint32_t w;
-          const float e = ex2(s[c] - (ref[c] == -INFINITY ? 0.f : ref[c]));
+          const float e = ex2(s[c] - base[c]);
           asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(w) : "f"(e));
           sum[c] += __uint_as_float(w);
           const uint32_t at = p_at + buf * C::P_BYTES + c * 128 + (((lane >> 2) ^ c) << 4);
@@ -787,7 +788,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
 #pragma unroll
         for (int m = 16; m; m >>= 1) l += __shfl_xor_sync(kFullMask, l, m);
         if (lane == 0) sum_of[warp * C::CC + c] = l;
-        if (tid == 0) sum_of[4 * C::CC + c] = ref[c];
+        if (tid == 0) sum_of[4 * C::CC + c] = base[c];
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&l_full[sg & 1]);
