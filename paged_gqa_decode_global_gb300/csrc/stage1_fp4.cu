@@ -918,11 +918,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
           // chunk me + k LANES, in buffer c
           const uint32_t c = C::LANES == 2 ? me : k & 1, sfv = kTmemSfv + me * 8 + k * 8 * C::LANES, to = kTmemVt + c * 128;
           const uint32_t v = item + (C::LANES == 2 ? k * 64 : (k >> 1) * 64 + (k & 1) * 4);
+          // Its scales' columns were the chunk's of the tile before, whose product has to be
+          // done: with a buffer a lane, the last wait said so of the chunk before last, which
+          // that is (K = V at d 512: 66.2 -> 65.2 us); with two, this one will.
+          auto scales = [&]() {
+            copy_scales(sfv, sf + k * 64 * C::LANES);
+            copy_scales(sfv + 4, sf + k * 64 * C::LANES + 32);
+          };
+          static_assert(C::LANES == 1 ? CH == 2 : CH == 4, "or the columns are another chunk's");
+          if (C::LANES == 2) scales();
           if (use > 0 && !(good = good && wait_for(&vt_empty[c], use - 1))) break;
           tmem_fence_after();
-          // (the product that these scales' columns were for before is done: its chunk is used, or its buffer would not be free)
-          copy_scales(sfv, sf + k * 64 * C::LANES);
-          copy_scales(sfv + 4, sf + k * 64 * C::LANES + 32);
+          if (C::LANES == 1) scales();
           mma_fp4<kEye, kRows, kDq>(to, eye, v, kTmemSfi, sfv, false);
           mma_fp4<kEye, kRows, kDq>(to, eye + 2, v + 2, kTmemSfi, sfv + 4, true);
           mma_commit<1>(&vt_full[c]);
