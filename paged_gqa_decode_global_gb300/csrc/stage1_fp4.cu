@@ -10,7 +10,7 @@
 // Bound and measured (time of a launch in a CUDA graph; floor at the measured copy
 // rate): HBM where K and V differ at d 512 (4 x 32768 tokens 54 us, floor 45: a tile
 // takes its copies' 3170 cycles, start and end ~8 us); at K = V the chain of V^T's two
-// buffers (8 requests of 1K to 128K 66 us, floor 36: ~2600 cycles a tile, its copies
+// buffers (8 requests of 1K to 128K 65 us, floor 36: ~2600 cycles a tile, its copies
 // 1590); at d 256 the softmax warps (61 windows of 1024 38 us, floor 21); latency for
 // short lengths (8 x 1024 13.6 us).
 //
@@ -694,18 +694,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
         tmem_fence_after();
         float s[C::CC];
         {
-          // the terms' columns, smallest terms first, three loads at a time (for the registers)
+          // the terms' columns, smallest terms first, 24 at a time (for the registers)
           float x[C::CC];
 #pragma unroll
           for (int c = 0; c < C::CC; ++c) x[c] = 0.f;
 #pragma unroll
-          for (int k0 = kFp4Terms * C::CC / 8 - 3; k0 >= 0; k0 -= 3) {
-            uint32_t w[3][8];
-#pragma unroll
-            for (int k = 0; k < 3; ++k) tmem_ld(w[k], kTmemS + quarter + (k0 + k) * 8);
+          for (int k = kFp4Terms * C::CC - 24; k >= 0; k -= 24) {
+            uint32_t lo[16], hi[8];
+            tmem_ld(lo, kTmemS + quarter + k);
+            tmem_ld(hi, kTmemS + quarter + k + 16);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 23; i >= 0; --i) x[i % C::CC] += __uint_as_float(w[i >> 3][i & 7]);
+            for (int i = 23; i >= 0; --i) x[i % C::CC] += __uint_as_float(i < 16 ? lo[i & 15] : hi[i & 7]);
           }
 #pragma unroll
           for (int c = 0; c < C::CC; ++c) s[c] = x[c] * col_mul[c];
