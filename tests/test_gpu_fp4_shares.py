@@ -148,3 +148,20 @@ def test_nan_block_of_a_shared_pool(T, window, sms):
     hit[0, (0 if T == 1 else 1):, 8:12] = True
     assert torch.isnan(got[hit]).all()
     assert torch.equal(got[~hit], clean[~hit])
+
+
+def test_two_streams_at_once():
+    cases = [Case(16, 4, 512, [3000, 700], seed=21), Case(16, 8, 256, [900, 40, 2000], window=300, kvs=True, seed=22)]
+    steps = [c.step() for c in cases]
+    want = [c.run(s).clone() for c, s in zip(cases, steps)]
+    outs = [[torch.full_like(c.q[:, 0], 7.0) for _ in range(20)] for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for c, s, o, st in zip(cases, steps, outs, streams):
+            with torch.cuda.stream(st):
+                c.run(s, out=o[i], check=False)
+    torch.cuda.synchronize()
+    for s, o, w in zip(steps, outs, want):
+        s.check()
+        assert all(torch.equal(x.view(w.shape), w) for x in o)
