@@ -907,7 +907,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
       constexpr uint32_t kRows = desc_hi(C::SL * 1024), kEye = desc_hi(512, 64);
       const uint32_t me = warp - kWideWarp, ring = smem_u32(smem) >> 4, eye = ring + (C::EYE_OFFSET >> 4);
       int i = 0, sv = C::KVS ? 0 : C::NK, round = 0, use = 0;  // the tile, its slot; uses of a buffer so far
-      good = *tmem_at == 0;
+      // The unit matrix and its scales in tensor memory come from the warps that write the query terms, which say so
+      // with the first segment's: a tile may be ready before. (That barrier's next phase waits for results of these
+      // products, so the first one cannot be missed.)
+      good = *tmem_at == 0 && wait_for(&q_full[0], 0);
 #pragma unroll 1
       for (; i < share_tiles && good; ++i) {
         if (!(good = wait_for(&ready[sv], round))) break;
