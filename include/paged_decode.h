@@ -65,8 +65,10 @@
  * an error word at the start of the workspace: the offending page is skipped
  * (its tokens are masked out), the length clamped; paged_decode_check_device_error
  * reports PD_ERR_DEVICE_FAULT. The error word must be zero before the first
- * call: zero the workspace once after allocating it. Calls that share a
- * workspace must not overlap on the GPU: order them on one stream.
+ * call: zero the workspace once after allocating it. Plans of any kind (cache
+ * types, shared prefixes, partial results, other numbers of SMs) may take one
+ * workspace in turn; calls that share it must not overlap on the GPU: order them
+ * on one stream.
  */
 #ifndef PAGED_DECODE_H
 #define PAGED_DECODE_H
@@ -698,8 +700,10 @@ pd_status paged_decode_read_slots_fp4(const pd_layer_desc* layer, int32_t num_to
  * share of all tokens and the last one to finish a row's pieces joins them, in an
  * order that does not vary: out is complete after the call, and
  * paged_decode_merge has nothing to do (num_splits is 1). The workspace, zeroed
- * once after allocating it, holds counts that every launch leaves at zero; after
- * PD_DEVFLAG_WAIT_TIMEOUT paged_decode_check_device_error sets them back.
+ * once after allocating it, holds counts behind the error word that every launch
+ * leaves at zero and no other plan's launches touch; after
+ * PD_DEVFLAG_WAIT_TIMEOUT paged_decode_check_device_error, with any plan that the
+ * workspace is large enough for, sets them back.
  * v_pool and v_scale of a K=V layer are NULL or k_pool and k_scale.
  *
  * A query element enters the score product as a sum of 4-bit terms that leaves

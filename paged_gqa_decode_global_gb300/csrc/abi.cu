@@ -420,10 +420,10 @@ pd_status paged_decode_check_device_error(const pd_plan* plan, void* workspace, 
   if (cudaMemcpy(&word, workspace, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return PD_ERR_CUDA;
   if (flags) *flags = word;
   if (word != 0) {
-    // (a 4-bit decode that gave up may have left counts of its pieces behind the word)
-    const bool counts = plan && pd::plan_is_valid(plan) && plan->layer.kv_dtype == PD_KV_FP4_E2M1 &&
-                        workspace_bytes >= plan->workspace_bytes;
-    if (cudaMemset(workspace, 0, counts ? plan->lse_offset : sizeof(word)) != cudaSuccess) return PD_ERR_CUDA;
+    // (a 4-bit decode that gave up may have left counts of its pieces in the header behind the word, whichever plan
+    // of those that share the workspace is asked about)
+    const bool header = pd::plan_is_valid(plan) && workspace_bytes >= plan->workspace_bytes;
+    if (cudaMemset(workspace, 0, header ? pd::kWorkspaceHeader : sizeof(word)) != cudaSuccess) return PD_ERR_CUDA;
     return PD_ERR_DEVICE_FAULT;
   }
   return PD_OK;

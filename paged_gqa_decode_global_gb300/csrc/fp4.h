@@ -12,10 +12,14 @@ constexpr int kFp4Block = 16;    // dims under one scale
 constexpr int kFp4Tile = 128;    // tokens of a tile: the matrix instruction's rows
 constexpr int kFp4Terms = 6;     // e2m1 terms a query element is written as
 constexpr int kFp4FirstId = 60;  // variant ids follow stage 1's
-constexpr int kFp4MaxShares = 4096;  // CTAs of a launch
-// Workspace: [error word, padded to 256 B][u32 per share: pieces of its last unit that
-// are there][fp32 log-sum-exps [shares][2][CC]][fp32 pieces [shares][2][CC][D]]
-constexpr uint64_t fp4_counters_bytes(int shares) { return ((uint64_t)shares * 4 + 255) / 256 * 256; }
+// Workspace: [error word][a byte per share: pieces of its last unit that are there][free]
+// [fp32 log-sum-exps [shares][2][CC]][fp32 pieces [shares][2][CC][D]]
+// The counts have to be zero between launches, whatever plans take the workspace in
+// turn: they lie in the 256-byte header, of which other plans write the error word
+// alone, and no plan's pieces.
+constexpr int kFp4MaxShares = (kWorkspaceHeader - 4) / 4 * 4;  // CTAs of a launch, so the most pieces of a unit
+static_assert(kFp4MaxShares <= 255, "a count is a byte");
+constexpr uint64_t fp4_parts_offset(int shares) { return kWorkspaceHeader + ((uint64_t)shares * 4 + 255) / 256 * 256; }
 
 // D   head_dim; KVS K=V shared pool; CC columns (query rows) of a CTA
 template <int D_, bool KVS_, int CC_>
@@ -88,7 +92,7 @@ struct Fp4Params {
   const uint8_t *k_sf, *v_sf;  // e4m3 [num_pages, Hkv, P, D / 16]
   const int32_t *block_tables, *seq_lens;
   void* out;
-  uint32_t* counters;  // [shares], zero between launches
+  uint32_t* counters;  // a byte a share, zero between launches
   float *lse_part, *o_part;
   uint32_t* err;
   float scale_log2;  // softmax scale * log2(e) * 2^k_exp

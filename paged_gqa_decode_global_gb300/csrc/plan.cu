@@ -401,7 +401,7 @@ pd_status plan_impl(const pd_layer_desc* layer, int32_t batch, int32_t query_tok
     plan->sm_count = sm_count;
     plan->max_seq_len = max_len;
     plan->merge_mode = 0;
-    plan->lse_offset = pd::kWorkspaceHeader + pd::fp4_counters_bytes(plan->grid_x);
+    plan->lse_offset = pd::fp4_parts_offset(plan->grid_x);
     plan->opart_offset = align_up(plan->lse_offset + (uint64_t)plan->grid_x * 2 * v->group * 4, 256);
     plan->workspace_bytes = plan->opart_offset + (uint64_t)plan->grid_x * 2 * v->group * ly.head_dim * 4;
     plan->magic = kPlanMagic;
@@ -616,7 +616,7 @@ bool plan_is_valid(const pd_plan* plan) {
            plan->block_tokens == v.block_tokens && plan->threads_per_cta == v.threads && plan->smem_bytes == v.smem_bytes &&
            plan->test_stall_bytes >= 0 && plan->test_stall_bytes <= (1 << 16) && plan->test_stall_bytes % 16 == 0 &&
            (plan->early_kv == 0 || plan->early_kv == 1) && ly.max_pages_per_seq > 0 && ly.page_size > 0 &&
-           units * tiles < (1 << 30) && plan->lse_offset >= kWorkspaceHeader + fp4_counters_bytes(plan->grid_x) &&
+           units * tiles < (1 << 30) && plan->lse_offset >= fp4_parts_offset(plan->grid_x) &&
            plan->lse_offset % 256 == 0 && plan->opart_offset % 256 == 0 && plan->lse_offset < (1ull << 40) &&
            plan->opart_offset < (1ull << 40) && plan->opart_offset >= plan->lse_offset + shares * 2 * cc * 4 &&
            plan->workspace_bytes >= plan->opart_offset + shares * 2 * cc * (uint64_t)ly.head_dim * 4;

@@ -1102,11 +1102,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
         if (seg.pieces > 1) {
           // whoever leaves the last piece joins them all, in their order:
           // out = sum_s w_s o_s,  w_s = exp(lse_s - M) / sum_s' exp(lse_s' - M)
-          if (wt == 0) *ticket = atomicAdd(&p.counters[seg.first_share], 1u);
+          uint32_t* count = p.counters + seg.first_share / 4;
+          const uint32_t byte = seg.first_share % 4 * 8;  // (a unit has at most as many pieces as there are CTAs: no carry)
+          if (wt == 0) *ticket = (atomicAdd(count, 1u << byte) >> byte) & 0xffu;
           named_bar_sync(3, 128);
           if (*ticket == (uint32_t)seg.pieces - 1) {
             __threadfence();
-            if (wt == 0) p.counters[seg.first_share] = 0u;
+            if (wt == 0) atomicAnd(count, ~(0xffu << byte));
             // a warp a column; piece q lies in slot 2 (first_share + q), the first one in the next
             constexpr int V4 = C::D / 128;  // float4s of a lane
             auto slot_of = [&](int q) { return (size_t)((seg.first_share + q) * 2 + (q == 0)) * C::CC; };
@@ -1225,7 +1227,7 @@ pd_status decode_fp4(const pd_plan* plan, const void* q, const void* k_pool, con
   p.block_tables = block_tables;
   p.seq_lens = seq_lens;
   p.out = out;
-  p.counters = reinterpret_cast<uint32_t*>(ws + kWorkspaceHeader);
+  p.counters = reinterpret_cast<uint32_t*>(ws + sizeof(uint32_t));
   p.lse_part = reinterpret_cast<float*>(ws + plan->lse_offset);
   p.o_part = reinterpret_cast<float*>(ws + plan->opart_offset);
   p.err = reinterpret_cast<uint32_t*>(ws);
