@@ -707,8 +707,9 @@ pd_status paged_decode_read_slots_fp4(const pd_layer_desc* layer, int32_t num_to
  * v_pool and v_scale of a K=V layer are NULL or k_pool and k_scale.
  *
  * A query element enters the score product as a sum of 4-bit terms that leaves
- * out at most 2^-14 of the largest of its 16; a query row with a NaN or an
- * infinity gives a NaN row. Probabilities are rounded to tf32 (2^-11 of
+ * out at most 2^-14 of the largest of its 16 plus 2^-27 of the largest of its row
+ * (of 2^-116 in a row below that); a query row with a NaN or an infinity gives a
+ * NaN row. Probabilities are rounded to tf32 (2^-11 of
  * themselves) relative to a reference that a score may pass by 2^60, sums are
  * fp32. A NaN block of an attended V row makes its dims NaN, of a K row the whole
  * output row.

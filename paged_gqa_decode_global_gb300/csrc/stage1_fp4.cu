@@ -20,10 +20,14 @@
 //   S = K q^T    kind::mxf4nvf4 on codes and scales as they lie in the cache. The
 //                query row is written as kFp4Terms e2m1 terms, each with its own
 //                scale per 16 dims, the next taking what the one before left
-//                over. A term leaves at most 0.177 of its block's largest, so six
-//                leave 2^-14.9 of it (the row is first brought to [2^10, 2^11) by
-//                a power of two, so that the last terms' scales still are e4m3
-//                numbers); the terms' scores are summed afterwards;
+//                over 4 times up; the terms' scores are summed afterwards, each
+//                brought down again. A term leaves at most max(0.177 m + 2^-10,
+//                6 * 2^-10) of a block whose largest is m (the second parts are
+//                half of e4m3's smallest step). With the row's largest in
+//                [2^10, 2^11) (by a power of two) and the last term 4^5 up, six
+//                leave 2^-14.9 of the block's largest and 2^-27.4 of the row's (all
+//                terms at one size left 2^-17.4 of it, for the same time: 61 windows
+//                of 1024 37.6 us and 37.5; 4 and 8 times up in turn 38.3);
 //   V^T = I V^T  the same kind with a unit matrix: V widened, scaled and turned,
 //                128 dims at a time, exactly (one term a sum) and as fp32 in
 //                tensor memory, where it is a tf32 operand as it is (two and four
@@ -119,6 +123,10 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
 }
+
+// How far up what a term leaves over is taken for the next one: it never passes what
+// the row's largest was (0.177 * 4 of it), so no scale is clamped.
+constexpr float kTermStep = 4.f;
 
 // Four e4m3 scales: 0x80 in the bytes that are NaN.
 __device__ __forceinline__ uint32_t nan_scales(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
@@ -362,8 +370,8 @@ __device__ __forceinline__ void write_query_terms(const Fp4Params& p, const Segm
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 two = __half22float2(*reinterpret_cast<const __half2*>(&f[i]));
-        x[2 * i] = fmaf(-two.x, sc, x[2 * i]);
-        x[2 * i + 1] = fmaf(-two.y, sc, x[2 * i + 1]);
+        x[2 * i] = fmaf(-two.x, sc * kTermStep, x[2 * i] * kTermStep);
+        x[2 * i + 1] = fmaf(-two.y, sc * kTermStep, x[2 * i + 1] * kTermStep);
       }
       const int n = t * C::CC + col;
       *reinterpret_cast<uint32_t*>(q + code_offset<C>(n, part * 128 + lane * 4)) = codes;
@@ -694,10 +702,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
         tmem_fence_after();
         float s[C::CC];
         {
-          // the terms' columns, smallest terms first, 24 at a time (for the registers)
-          float x[C::CC];
+          // the terms' columns, smallest terms first, the sum brought down to the next term's size each time; 24 at a
+          // time (for the registers), two columns an instruction
+          uint64_t x[C::CC / 2];
 #pragma unroll
-          for (int c = 0; c < C::CC; ++c) x[c] = 0.f;
+          for (int c = 0; c < C::CC / 2; ++c) x[c] = 0;
 #pragma unroll
           for (int k = kFp4Terms * C::CC - 24; k >= 0; k -= 24) {
             uint32_t lo[16], hi[8];
@@ -705,10 +714,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
             tmem_ld(hi, kTmemS + quarter + k + 16);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 23; i >= 0; --i) x[i % C::CC] += __uint_as_float(i < 16 ? lo[i & 15] : hi[i & 7]);
+            for (int i = 22; i >= 0; i -= 2) {
+              const uint32_t a = i < 16 ? lo[i & 15] : hi[i & 7], b = i < 16 ? lo[(i & 15) + 1] : hi[(i & 7) + 1];
+              asm("{\n\t.reg .b64 f, y;\n\tmov.b64 f, {%3, %3};\n\tmov.b64 y, {%1, %2};\n\tfma.rn.f32x2 %0, %0, f, y;\n\t}"
+                  : "+l"(x[i % C::CC / 2])
+                  : "r"(a), "r"(b), "f"(1.f / kTermStep));
+            }
           }
 #pragma unroll
-          for (int c = 0; c < C::CC; ++c) s[c] = x[c] * col_mul[c];
+          for (int c = 0; c < C::CC / 2; ++c) {
+            float lo, hi;
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x[c]));
+            s[2 * c] = lo * col_mul[2 * c];
+            s[2 * c + 1] = hi * col_mul[2 * c + 1];
+          }
         }
         const int row = warp * 32 + lane, t = seg.t_base + i * kFp4Tile + row;
         const bool ok = (*blocks_of >> (row >> 4)) & 1u;
