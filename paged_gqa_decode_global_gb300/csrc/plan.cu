@@ -593,7 +593,14 @@ bool plan_is_valid(const pd_plan* plan) {
   if (plan->variant < 0 || plan->variant >= kNumVariants) return false;
   const VariantInfo& v = kVariants[plan->variant];
   const pd_layer_desc& ly = plan->layer;
-  if (ly.num_kv_heads <= 0 || ly.num_q_heads % ly.num_kv_heads != 0) return false;
+  // (as plan_impl has them: kernels divide by these, and count pool rows and a request's tokens in 32 bits)
+  if (ly.num_q_heads <= 0 || ly.num_kv_heads <= 0 || ly.num_kv_heads > 65535 || ly.num_q_heads % ly.num_kv_heads != 0)
+    return false;
+  if (ly.page_size <= 0 || ly.page_size % 16 != 0 || ly.num_pages <= 0 || ly.max_pages_per_seq <= 0 || ly.window < 0)
+    return false;
+  if ((long long)ly.max_pages_per_seq * ly.page_size > 0x7fffffffLL) return false;
+  const long long pool_pages = (long long)ly.num_pages * ly.num_kv_heads;
+  if (pool_pages > 0x7fffffffLL || pool_pages * ly.page_size > 0x7fffffffLL) return false;
   const int group = ly.num_q_heads / ly.num_kv_heads;
   if (v.kv_fp8 == PD_KV_FP4_E2M1) {
     if (group > kMaxGroup || plan->query_tokens < 1 || plan->query_tokens > kMaxQueryTokens) return false;
@@ -615,8 +622,8 @@ bool plan_is_valid(const pd_plan* plan) {
            plan->grid_y == 1 && plan->grid_z == 1 && plan->num_splits == 1 && plan->merge_mode == 0 && plan->partial == 0 &&
            plan->block_tokens == v.block_tokens && plan->threads_per_cta == v.threads && plan->smem_bytes == v.smem_bytes &&
            plan->test_stall_bytes >= 0 && plan->test_stall_bytes <= (1 << 16) && plan->test_stall_bytes % 16 == 0 &&
-           (plan->early_kv == 0 || plan->early_kv == 1) && ly.max_pages_per_seq > 0 && ly.page_size > 0 &&
-           units * tiles < (1 << 30) && plan->lse_offset >= fp4_parts_offset(plan->grid_x) &&
+           (plan->early_kv == 0 || plan->early_kv == 1) && units * tiles < (1 << 30) &&
+           plan->lse_offset >= fp4_parts_offset(plan->grid_x) &&
            plan->lse_offset % 256 == 0 && plan->opart_offset % 256 == 0 && plan->lse_offset < (1ull << 40) &&
            plan->opart_offset < (1ull << 40) && plan->opart_offset >= plan->lse_offset + shares * 2 * cc * 4 &&
            plan->workspace_bytes >= plan->opart_offset + shares * 2 * cc * (uint64_t)ly.head_dim * 4;
