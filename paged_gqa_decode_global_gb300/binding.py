@@ -417,9 +417,11 @@ def _fp4_shapes(ly) -> tuple:
 
 def fp4_exponent(largest: float) -> int:
     """The layer exponent for values of magnitudes up to `largest`: the smallest e in [-64, 64] with
-    largest <= 6 * 448 * 2^e."""
+    largest <= 6 * 448 * 2^e; 64 past them all (infinity too), 0 without a positive magnitude (NaN too)."""
     if not largest > 0.0:
         return 0
+    if math.isinf(largest):
+        return 64
     m, e = math.frexp(largest / (6.0 * 448.0))
     return max(-64, min(64, e - 1 if m == 0.5 else e))
 
