@@ -422,8 +422,8 @@ def fp4_exponent(largest: float) -> int:
         return 0
     if math.isinf(largest):
         return 64
-    m, e = math.frexp(largest / (6.0 * 448.0))
-    return max(-64, min(64, e - 1 if m == 0.5 else e))
+    m, e = math.frexp(largest)  # (a quotient by 6 * 448 = 0.65625 * 2^12 would be 0 for the smallest numbers)
+    return max(-64, min(64, e - 12 if m <= 0.65625 else e - 11))
 
 
 def paged_decode_merge(plan: Plan, workspace, out, stream=None, workspace_bytes: Optional[int] = None) -> None:
