@@ -145,7 +145,8 @@ typedef struct {
                                2: the own part of a pd_shared_plan (likewise) */
   int32_t early_kv;         /* 0 (as planned). A caller may set 1 when no kernel that can still be
                                running as stage 1 starts writes block_tables, seq_lens, the FP8 scales
-                               or a cached row other than each request's newest query_tokens positions.
+                               or a cached row (over a 4-bit cache its codes and scales) other than each
+                               request's newest query_tokens positions.
                                Those kernels are the one launched just before stage 1 on its stream and,
                                if that one lets its dependents start before it waits for its own
                                predecessor (paged_decode_qkv_norm_rope_write does), the one before it,
@@ -202,8 +203,9 @@ pd_status paged_decode_plan(const pd_layer_desc* layer, int32_t batch, const int
  * [batch, T, Hq, d]; a device length below T sets PD_DEVFLAG_BAD_SEQLEN and the
  * tokens before position 0 attend nothing (zero output). The (token, head)
  * pairs of one KV head are served 8 per CTA, so for T * group <= 8 every KV
- * byte is still read once. bf16 or FP8 caches (an FP8 plan goes with
- * paged_decode_global_fp8 / paged_decode_window_fp8), head_dim 256 or 512,
+ * byte is still read once. Any cache (an FP8 plan goes with
+ * paged_decode_global_fp8 / paged_decode_window_fp8, a 4-bit one with
+ * paged_decode_global_fp4 / paged_decode_window_fp4), head_dim 256 or 512,
  * group Hq / Hkv up to 16.
  */
 pd_status paged_decode_plan_multi(const pd_layer_desc* layer, int32_t batch, int32_t query_tokens,
@@ -297,8 +299,8 @@ pd_status paged_decode_check_device_error(const pd_plan* plan, void* workspace,
  *                 (PD_DEVFLAG_*) of this call; NULL to ignore it
  *   stream        cudaStream_t as void*
  * Every argument is checked before anything is queued: PD_ERR_INVALID_ARG for
- * what paged_decode_global / paged_decode_window refuse, and for an FP8 plan
- * (its scales have no argument here) or a plan from paged_decode_plan_partial;
+ * what paged_decode_global / paged_decode_window refuse, and for an FP8 or 4-bit
+ * plan (its scales have no argument here) or a plan from paged_decode_plan_partial;
  * PD_ERR_WORKSPACE_TOO_SMALL when the plan needs more than 8 MiB of scratch
  * (plan->workspace_bytes > 8 MiB). With batch 0 nothing is launched and
  * device_flags is not written. Otherwise it returns the statuses of the calls

@@ -495,8 +495,8 @@ class LayerStep:
 
     @classmethod
     def for_inputs(cls, li, sm_count=None, query_tokens=1, early_kv=False):
-        """A step for a LayerInputs (bf16 cache) or Fp8LayerInputs (e4m3 cache);
-        query_tokens > 1: q and out are [B, T, Hq, d]."""
+        """A step for a LayerInputs (bf16 cache) or Fp8LayerInputs (e4m3 cache), which run() takes (a step over a 4-bit
+        cache is called with its tensors); query_tokens > 1: q and out are [B, T, Hq, d]."""
         fp8 = hasattr(li, "k8")
         return cls(li.num_q_heads, li.num_kv_heads, li.head_dim, li.page_size, li.num_pages, li.max_pages,
                    li.seq_lens_list(), window=li.window, kv_shared=li.kv_shared,
@@ -508,9 +508,8 @@ class LayerStep:
         if self.fp4:
             _decode_fp4(self.plan, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens, self.window or None,
                         scale, self.workspace, out, stream, None, k_exp, v_exp)
-            if self.plan.merge_mode != 1:  # merged already
-                return out
-        elif self.fp8:
+            return out  # joined in the launch
+        if self.fp8:
             if self.window > 0:
                 paged_decode_window_fp8(self.plan, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens,
                                         self.window, scale, self.workspace, out, stream)

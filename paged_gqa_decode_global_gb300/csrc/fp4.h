@@ -67,8 +67,6 @@ struct Fp4Cfg {
   static constexpr int SCALE_WARPS = D == 256 ? 2 : 1, LANES = D == 256 ? 1 : 2;
   static constexpr int WARPS = 15 + SCALE_WARPS + 2 * LANES;
   static constexpr int THREADS = 32 * WARPS;
-  // what a share leaves to be joined: its first and its last unit's piece
-  static constexpr int PIECE_FLOATS = CC * D;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
   static_assert(Q_OFFSET % 1024 == 0 && Q_BYTES % 1024 == 0 && P_OFFSET % 1024 == 0 && EYE_OFFSET % 1024 == 0 &&
                     QSF_OFFSET % 16 == 0,

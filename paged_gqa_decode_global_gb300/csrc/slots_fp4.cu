@@ -154,8 +154,9 @@ __device__ __forceinline__ uint2 quantise16(Block v, float down, uint8_t& scale)
 }
 
 // WIDE: rows that begin on 32 bytes, a load a block. (16384 tokens of 4 x 512, K
-// and V, with their read-back: 60 us; with 8 elements a lane, two lanes finding the
-// scale that one does here, 142 instructions for 8 elements bound it: 74 us.)
+// and V: 30 us, floor 25, waiting for its loads with issue slots at 62%; with their
+// read-back 60 us, where 8 elements a lane, two lanes finding the scale that one
+// does here, took 74 by their 142 instructions for 8 elements.)
 template <bool WIDE>
 __global__ void __launch_bounds__(kRowsThreads) write_fp4_kernel(const __grid_constant__ RowsParams p) {
   __shared__ Places places;
@@ -362,7 +363,7 @@ pd_status rows_params(const pd_layer_desc* layer, int kv_dtype, int32_t num_toke
   p.dim = ly.head_dim;
   p.page_size = ly.page_size;
   p.num_slots = slots;
-  // runs of up to 16 tokens, shorter while that leaves SMs without a CTA
+  // runs of up to 16 tokens, shorter while that leaves a GB300's 152 SMs less than two CTAs each (304)
   p.run = kRowsMaxRun;
   while (p.run > 1 && (long long)num_tokens < 304ll * p.run) p.run /= 2;
   *out = p;

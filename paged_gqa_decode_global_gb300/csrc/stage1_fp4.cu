@@ -12,7 +12,8 @@
 // takes its copies' 3170 cycles, start and end ~8 us); at K = V the chain of V^T's two
 // buffers (8 requests of 1K to 128K 65 us, floor 36: ~2600 cycles a tile, its copies
 // 1590); at d 256 the softmax warps (61 windows of 1024 38 us, floor 21); latency for
-// short lengths (8 x 1024 13.6 us).
+// short lengths (8 x 1024 13.5 us; 10.6 with a CTA a piece, which took 158 us for the
+// 8 requests of 1K to 128K when this one took 99).
 //
 // Mathematics: a cached element is e2m1(code) * e4m3(scale of its 16 dims) *
 // 2^exp. All three products of a tile of 128 tokens run on tcgen05, and no
