@@ -717,7 +717,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_fp4_kernel(const __grid_
 #pragma unroll
             for (int i = 22; i >= 0; i -= 2) {
               const uint32_t a = i < 16 ? lo[i & 15] : hi[i & 7], b = i < 16 ? lo[(i & 15) + 1] : hi[(i & 7) + 1];
-              asm("{\n\t.reg .b64 f, y;\n\tmov.b64 f, {%3, %3};\n\tmov.b64 y, {%1, %2};\n\tfma.rn.f32x2 %0, %0, f, y;\n\t}"
+              // (volatile: it stays behind the wait for what it takes)
+              asm volatile(
+                  "{\n\t.reg .b64 f, y;\n\tmov.b64 f, {%3, %3};\n\tmov.b64 y, {%1, %2};\n\tfma.rn.f32x2 %0, %0, f, y;\n\t}"
                   : "+l"(x[i % C::CC / 2])
                   : "r"(a), "r"(b), "f"(1.f / kTermStep));
             }
